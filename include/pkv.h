@@ -492,6 +492,152 @@ PKV_API int pkv_paged_decode_attention_static_ws(
     float scale, pkv_bf16* out, int num_splits, int32_t* dev_err,
     pkv_stream_t stream);
 
+/*
+ * Long contexts
+ * -------------
+ * Attention of more than one new token, attention that does not see the whole
+ * cache, and a cache that does not keep every token.  (The source pages have
+ * prefill attention and the decode step only; these calls are this library's
+ * own.)  Shapes, pool, tables, scale, dev_err, streams and errors are as
+ * above; every call also returns PKV_EINVAL when an output overlaps an input
+ * that it must not.  A query at position p sees the cached token t when
+ *   t <= p  and  (t > p - window  or  t < sinks).
+ * Tokens that a query does not see never reach its result, whatever their K
+ * and V hold (NaN and infinities included), and a row that sees none is zero.
+ */
+
+/*
+ * pkv_paged_chunk_attention -- attention of a ragged batch of new tokens over
+ * the paged cache that already holds their K and V (pkv_kv_write_prefill):
+ * prefill in chunks, verification of drafted tokens, or chunks and single
+ * tokens side by side.
+ *
+ * Sequence b owns rows [token_offsets[b], token_offsets[b+1]) of q and out
+ * (none is allowed); its i-th of n tokens stands at position seq_lens[b] - n
+ * + i and sees the tokens above.  Scores, softmax and sums are FP32; the
+ * weights enter the product with V as bf16 (the row sums take them unrounded)
+ * and the output is rounded to bf16 once.
+ *
+ *   q, out         [num_tokens][num_q_heads][head_dim] bf16 (q rotated)
+ *   token_offsets  int32 [batch + 1], non-decreasing, in [0, num_tokens];
+ *                  rows outside [token_offsets[0], token_offsets[batch]) are
+ *                  left as they were
+ *   seq_lens       int32 [batch], cached tokens, the chunk's included
+ *   window         0: no window; else the tokens a query sees, itself included
+ *   sinks          first tokens seen from any position
+ *   workspace      at least pkv_chunk_workspace_bytes() bytes, 16-byte aligned
+ *   num_splits     0: automatic; S > 0: at most S ranges of the cached tokens
+ *                  per row tile, combined afterwards (repeated runs give the
+ *                  same bits)
+ *   dev_err        PKV_DEVERR_PAGE / _SEQLEN / _OFFSETS (offsets that are not
+ *                  as above: the rows they misplace may be left unwritten) /
+ *                  _POSITION (a chunk longer than its sequence: the rows before
+ *                  position 0 are zero) / _TIMEOUT
+ * Table entries of pages that no query of the chunk sees are not read, so
+ * pages that have left every window may be freed.
+ */
+PKV_API int pkv_paged_chunk_attention(
+    const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const pkv_bf16* pool,
+    int64_t num_pages, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+    int batch, int num_q_heads, int num_kv_heads, int head_dim, int page_size, int window,
+    int sinks, float scale, pkv_bf16* out, void* workspace, size_t workspace_bytes,
+    int num_splits, int32_t* dev_err, pkv_stream_t stream);
+
+/* Bytes of workspace that call needs; (size_t)-1 for invalid sizes. */
+PKV_API size_t pkv_chunk_workspace_bytes(int num_tokens, int batch, int num_q_heads,
+                                         int num_kv_heads, int head_dim, int max_blocks,
+                                         int window, int sinks, int num_splits);
+
+/*
+ * pkv_paged_window_attention -- pkv_paged_decode_attention under a sliding
+ * window (>= 1 tokens, the newest included) with sink tokens: the query of
+ * sequence b stands at position seq_lens[b] - 1.  Table entries of pages that
+ * it does not see are not read.  Workspace, num_splits and dev_err as for
+ * pkv_paged_decode_attention, sized by pkv_window_workspace_bytes().
+ */
+PKV_API int pkv_paged_window_attention(
+    const pkv_bf16* q, const pkv_bf16* pool, int64_t num_pages, const int32_t* block_table,
+    int max_blocks, const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, int window, int sinks, float scale, pkv_bf16* out,
+    void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
+    pkv_stream_t stream);
+
+/* Bytes of workspace that call needs; (size_t)-1 for invalid sizes. */
+PKV_API size_t pkv_window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int max_blocks, int window, int sinks,
+                                          int num_splits);
+
+/*
+ * pkv_paged_scored_attention -- pkv_paged_decode_attention that also adds
+ * each cached token's attention weight to a running mass:
+ *   mass[(b * num_kv_heads + g) * mass_stride + t] += sum over the query heads
+ *   j of kv head g of softmax_t(scale * q[b][j] . K_t),   t < seq_lens[b],
+ * in FP32, in an order that does not change from run to run.
+ *   mass  float, rows of mass_stride >= max_blocks * page_size; entries at or
+ *         past seq_lens[b] and those of skipped pages are left as they were
+ * Workspace, num_splits and dev_err as for pkv_paged_decode_attention, sized
+ * by pkv_scored_workspace_bytes().
+ */
+PKV_API int pkv_paged_scored_attention(
+    const pkv_bf16* q, const pkv_bf16* pool, int64_t num_pages, const int32_t* block_table,
+    int max_blocks, const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, float scale, pkv_bf16* out, float* mass, int64_t mass_stride,
+    void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
+    pkv_stream_t stream);
+
+/* Bytes of workspace that call needs; (size_t)-1 for invalid sizes. */
+PKV_API size_t pkv_scored_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int max_blocks, int num_splits);
+
+/*
+ * pkv_kv_evict -- keep part of each sequence's cache, chosen per kv head by
+ * the accumulated weights.  With L = seq_lens[b] and n = min(L, budget), kv
+ * head g of sequence b keeps all L tokens when L <= budget, and otherwise its
+ * first `sinks`, its last `recent` and the budget - sinks - recent heaviest of
+ * the others (of equal weights the lower token; NaN counts as heavier than
+ * every number).  The kept tokens' K and V rows go, in token order, to slots
+ * 0..n-1 of dst_block_table's pages; new_lens[b] = n.  Each head keeps tokens
+ * of its own, so a slot holds different tokens for different heads: attention
+ * over the new cache needs no positions (keys are stored rotated), and
+ * further tokens are added with pkv_kv_append_at.
+ *
+ *   mass             as pkv_paged_scored_attention fills it
+ *   dst_block_table  int32 [batch][dst_max_blocks], dst_max_blocks * page_size
+ *                    >= budget: pages for the new cache.  No page of its live
+ *                    part may be named by a live entry of block_table, nor
+ *                    twice: the rows are copied while others are still read
+ *   new_lens         int32 [batch], written
+ *   new_mass         float, rows of new_mass_stride >= budget, written whole:
+ *                    the kept tokens' masses, then zeros
+ *   kept             int32 [batch][num_kv_heads][budget], written: the kept
+ *                    tokens' old places in order, then -1
+ *   dev_err          PKV_DEVERR_PAGE (a row whose old or new page is bad is
+ *                    not copied) / _SEQLEN
+ * 0 <= sinks, 0 <= recent, sinks + recent <= budget, budget >= 1.  The old
+ * pages are read only (a shared prefix stays intact); dst slots at or past
+ * new_lens[b] are left as they were.
+ */
+PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
+                         int64_t num_pages, const int32_t* block_table, int max_blocks,
+                         const int32_t* seq_lens, int batch, int num_kv_heads, int head_dim,
+                         int page_size, int budget, int sinks, int recent,
+                         const int32_t* dst_block_table, int dst_max_blocks, int32_t* new_lens,
+                         float* new_mass, int64_t new_mass_stride, int32_t* kept,
+                         int32_t* dev_err, pkv_stream_t stream);
+
+/*
+ * pkv_kv_append_at -- pkv_kv_append with the RoPE position and the cache slot
+ * given apart: sequence b's token is rotated for positions[b] (any value >= 0)
+ * and stored as cached token slots[b] of its table.  pkv_kv_append is the
+ * case slots == positions, bit for bit.  q_in and q_out must not overlap.
+ */
+PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_bf16* pool,
+                             int64_t num_pages, const int32_t* block_table, int max_blocks,
+                             const int32_t* positions, const int32_t* slots, int batch,
+                             int num_kv_heads, int head_dim, int page_size, double rope_theta,
+                             const pkv_bf16* q_in, pkv_bf16* q_out, int num_q_heads,
+                             int32_t* dev_err, pkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

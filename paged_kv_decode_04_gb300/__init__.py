@@ -9,7 +9,9 @@ __version__ = "0.1.0"
 
 _BINDING_NAMES = {
     "kv_append", "paged_decode_attention", "decode_step", "kv_write_prefill", "workspace_bytes", "plan_splits", "strerror",
-    "abi_version", "PkvError",
+    "abi_version", "PkvError", "paged_chunk_attention", "chunk_workspace_bytes",
+    "paged_window_attention", "window_workspace_bytes", "paged_scored_attention",
+    "scored_workspace_bytes", "kv_evict", "kv_append_at",
 }
 
 

@@ -97,6 +97,27 @@ def _load():
     L.pkv_decode_steps_planned.restype = i32
     L.pkv_kv_write_prefill_layers.argtypes = [i32] + L.pkv_kv_write_prefill.argtypes
     L.pkv_kv_write_prefill_layers.restype = i32
+    L.pkv_kv_append_at.argtypes = [vp, vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, f64, vp,
+                                   vp, i32, vp, vp]
+    L.pkv_kv_append_at.restype = i32
+    L.pkv_chunk_workspace_bytes.argtypes = [i32] * 9
+    L.pkv_chunk_workspace_bytes.restype = sz
+    L.pkv_paged_chunk_attention.argtypes = [vp, i32, vp, vp, i64, vp, i32, vp, i32, i32, i32, i32,
+                                            i32, i32, i32, f32, vp, vp, sz, i32, vp, vp]
+    L.pkv_paged_chunk_attention.restype = i32
+    L.pkv_window_workspace_bytes.argtypes = [i32] * 8
+    L.pkv_window_workspace_bytes.restype = sz
+    L.pkv_paged_window_attention.argtypes = [vp, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32,
+                                             i32, i32, f32, vp, vp, sz, i32, vp, vp]
+    L.pkv_paged_window_attention.restype = i32
+    L.pkv_scored_workspace_bytes.argtypes = [i32] * 6
+    L.pkv_scored_workspace_bytes.restype = sz
+    L.pkv_paged_scored_attention.argtypes = [vp, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32,
+                                             f32, vp, vp, i64, vp, sz, i32, vp, vp]
+    L.pkv_paged_scored_attention.restype = i32
+    L.pkv_kv_evict.argtypes = [vp, i64, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                               vp, i32, vp, vp, i64, vp, vp, vp]
+    L.pkv_kv_evict.restype = i32
     return L
 
 
@@ -593,3 +614,282 @@ def decode_steps_planned(qs, k_news, v_news, pool, block_tables, seq_lens, plan,
     if rc != PKV_OK:
         raise PkvError(rc, "pkv_decode_steps_planned")
     return out
+
+
+# ----------------------------------------------------------- long contexts --
+
+INT32_MAX = 2 ** 31 - 1
+
+
+def _cuda(t, name="pool"):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
+    return t.device
+
+
+def _count(v, name, least=0):
+    v = int(v)
+    if not least <= v <= INT32_MAX:
+        raise ValueError(f"{name} must be in [{least}, {INT32_MAX}], got {v}")
+    return v
+
+
+def _bytes(n, what):
+    if n == ctypes.c_size_t(-1).value:
+        raise PkvError(PKV_EINVAL, what)
+    return n
+
+
+class _On:
+    """Launch on the tensors' device, whichever is current: `stream` (or that
+    device's current one), and the tensors a call made for itself kept alive
+    for the stream it used them on."""
+
+    def __init__(self, dev, stream):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.dev = dev
+        self.other = stream is not None
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+
+    def new(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.dev)
+        if self.other:
+            t.record_stream(self.stream)
+        return t
+
+    def workspace(self, ws, need):
+        """(workspace, its bytes): the caller's, or one of `need` bytes."""
+        if ws is None:
+            if not need:
+                return None, 0
+            ws = self.new(need, torch.uint8)
+        elif ws.device != self.dev or not ws.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the pool's device")
+        return ws, ws.numel() * ws.element_size()
+
+    def call(self, what, *args):
+        f = getattr(_lib, what)
+        if torch.cuda.current_device() == self.dev.index:
+            rc = f(*args, self.ptr)
+        else:
+            with torch.cuda.device(self.dev):
+                rc = f(*args, self.ptr)
+        if rc != PKV_OK:
+            raise PkvError(rc, what)
+
+
+def _heads(t, name, dev, rows=None, heads=NUM_Q_HEADS):
+    """A bf16 tensor [rows][heads][64]; its number of rows."""
+    _check(t, name, torch.bfloat16, 3, dev)
+    if t.shape[1] != heads or t.shape[2] != HEAD_DIM or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}][{heads}]"
+                         f"[{HEAD_DIM}], got {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def _tables(block_table, seq_lens, dev, name="block_table"):
+    """The batch and table width of int32 tables and lengths on `dev`."""
+    _check(block_table, name, torch.int32, 2, dev)
+    _check(seq_lens, "seq_lens", torch.int32, 1, dev)
+    if block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"{name} and seq_lens disagree on the batch")
+    return block_table.shape
+
+
+def _err(dev_err, dev):
+    if dev_err is not None:
+        _check(dev_err, "dev_err", torch.int32, None, dev)
+        if dev_err.numel() < 1:
+            raise ValueError("dev_err must hold one int32")
+    return _ptr(dev_err)
+
+
+def chunk_workspace_bytes(num_tokens: int, batch: int, max_blocks: int, num_splits: int = 0, *,
+                          window: int = 0, sinks: int = 0) -> int:
+    """Workspace bytes of paged_chunk_attention for these sizes."""
+    return _bytes(_lib.pkv_chunk_workspace_bytes(
+        _count(num_tokens, "num_tokens"), _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS,
+        HEAD_DIM, _count(max_blocks, "max_blocks"), _count(window, "window"),
+        _count(sinks, "sinks"), _count(num_splits, "num_splits")), "pkv_chunk_workspace_bytes")
+
+
+def paged_chunk_attention(q, token_offsets, pool, block_table, seq_lens, out=None, *,
+                          window: int = 0, sinks: int = 0, scale: float = None, workspace=None,
+                          num_splits: int = 0, dev_err=None, stream=None) -> torch.Tensor:
+    """Attention of a ragged batch of new tokens whose K and V are cached
+    already: rows token_offsets[b] .. token_offsets[b + 1] of q ([num_tokens]
+    [32][64]) are the last tokens of sequence b's seq_lens[b] cached ones, each
+    seeing the tokens up to itself -- with window > 0 the newest `window` of
+    them and the first `sinks`.  Without `out` rows of no sequence are zero."""
+    num_pages = _pool_pages(pool)
+    dev = _cuda(pool)
+    rows = _heads(q, "q", dev)
+    _check(token_offsets, "token_offsets", torch.int32, 1, dev)
+    B, max_blocks = _tables(block_table, seq_lens, dev)
+    if token_offsets.shape[0] != B + 1:
+        raise ValueError("token_offsets must have batch + 1 entries")
+    window, sinks = _count(window, "window"), _count(sinks, "sinks")
+    num_splits = _count(num_splits, "num_splits")
+    on = _On(dev, stream)
+    if out is None:
+        with torch.cuda.stream(on.stream):
+            out = torch.zeros_like(q)
+    _heads(out, "out", dev, rows)
+    if rows == 0 or B == 0:
+        return out
+    need = 0
+    if workspace is None:
+        need = chunk_workspace_bytes(rows, B, max_blocks, num_splits, window=window, sinks=sinks)
+    ws, ws_bytes = on.workspace(workspace, need)
+    on.call("pkv_paged_chunk_attention", _ptr(q), rows, _ptr(token_offsets), _ptr(pool), num_pages,
+            _ptr(block_table), max_blocks, _ptr(seq_lens), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
+            PAGE_SIZE, window, sinks, float(HEAD_DIM ** -0.5 if scale is None else scale),
+            _ptr(out), _ptr(ws), ws_bytes, num_splits, _err(dev_err, dev))
+    return out
+
+
+def window_workspace_bytes(batch: int, max_blocks: int, window: int, num_splits: int = 0, *,
+                           sinks: int = 0) -> int:
+    """Workspace bytes of paged_window_attention for these sizes."""
+    return _bytes(_lib.pkv_window_workspace_bytes(
+        _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
+        _count(max_blocks, "max_blocks"), _count(window, "window", 1), _count(sinks, "sinks"),
+        _count(num_splits, "num_splits")), "pkv_window_workspace_bytes")
+
+
+def paged_window_attention(q, pool, block_table, seq_lens, window: int, out=None, *,
+                           sinks: int = 0, scale: float = None, workspace=None,
+                           num_splits: int = 0, dev_err=None, stream=None) -> torch.Tensor:
+    """paged_decode_attention over each sequence's newest `window` tokens and
+    its first `sinks`; pages that it does not see need not exist."""
+    num_pages = _pool_pages(pool)
+    dev = _cuda(pool)
+    B, max_blocks = _tables(block_table, seq_lens, dev)
+    _heads(q, "q", dev, B)
+    window, sinks = _count(window, "window", 1), _count(sinks, "sinks")
+    num_splits = _count(num_splits, "num_splits")
+    on = _On(dev, stream)
+    if out is None:
+        out = on.new(q.shape, q.dtype)
+    _heads(out, "out", dev, B)
+    if B == 0:
+        return out
+    need = 0
+    if workspace is None:
+        need = window_workspace_bytes(B, max_blocks, window, num_splits, sinks=sinks)
+    ws, ws_bytes = on.workspace(workspace, need)
+    on.call("pkv_paged_window_attention", _ptr(q), _ptr(pool), num_pages, _ptr(block_table),
+            max_blocks, _ptr(seq_lens), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, window,
+            sinks, float(HEAD_DIM ** -0.5 if scale is None else scale), _ptr(out), _ptr(ws),
+            ws_bytes, num_splits, _err(dev_err, dev))
+    return out
+
+
+def scored_workspace_bytes(batch: int, max_blocks: int, num_splits: int = 0) -> int:
+    """Workspace bytes of paged_scored_attention for these sizes."""
+    return _bytes(_lib.pkv_scored_workspace_bytes(
+        _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
+        _count(max_blocks, "max_blocks"), _count(num_splits, "num_splits")),
+        "pkv_scored_workspace_bytes")
+
+
+def _mass(t, name, dev, batch, least):
+    """A float32 tensor [batch][8][tokens] with at least `least` tokens; tokens."""
+    _check(t, name, torch.float32, 3, dev)
+    if t.shape[0] != batch or t.shape[1] != NUM_KV_HEADS or t.shape[2] < least:
+        raise ValueError(f"{name} must be [{batch}][{NUM_KV_HEADS}][{least} or more], got "
+                         f"{tuple(t.shape)}")
+    return t.shape[2]
+
+
+def paged_scored_attention(q, pool, block_table, seq_lens, mass, out=None, *,
+                           scale: float = None, workspace=None, num_splits: int = 0,
+                           dev_err=None, stream=None) -> torch.Tensor:
+    """paged_decode_attention that adds each cached token's attention weight,
+    summed over the query heads of its kv head, to mass ([B][8][max_blocks * 16
+    or more] float32)."""
+    num_pages = _pool_pages(pool)
+    dev = _cuda(pool)
+    B, max_blocks = _tables(block_table, seq_lens, dev)
+    _heads(q, "q", dev, B)
+    stride = _mass(mass, "mass", dev, B, max_blocks * PAGE_SIZE)
+    num_splits = _count(num_splits, "num_splits")
+    on = _On(dev, stream)
+    if out is None:
+        out = on.new(q.shape, q.dtype)
+    _heads(out, "out", dev, B)
+    if B == 0:
+        return out
+    need = 0 if workspace is not None else scored_workspace_bytes(B, max_blocks, num_splits)
+    ws, ws_bytes = on.workspace(workspace, need)
+    on.call("pkv_paged_scored_attention", _ptr(q), _ptr(pool), num_pages, _ptr(block_table),
+            max_blocks, _ptr(seq_lens), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE,
+            float(HEAD_DIM ** -0.5 if scale is None else scale), _ptr(out), _ptr(mass), stride,
+            _ptr(ws), ws_bytes, num_splits, _err(dev_err, dev))
+    return out
+
+
+def kv_evict(mass, pool, block_table, seq_lens, dst_block_table, new_lens=None, new_mass=None,
+             kept=None, *, budget: int, sinks: int = 0, recent: int = 0, dev_err=None,
+             stream=None):
+    """Keep at most `budget` cached tokens of each sequence, chosen per kv head:
+    the first `sinks`, the last `recent` and the heaviest others by `mass`.
+    Their rows are packed into dst_block_table's pages (which no live entry of
+    block_table names).  Returns (new_lens [B], new_mass [B][8][dst slots],
+    kept [B][8][budget]: old places, -1 past the end)."""
+    num_pages = _pool_pages(pool)
+    dev = _cuda(pool)
+    B, max_blocks = _tables(block_table, seq_lens, dev)
+    _, dst_blocks = _tables(dst_block_table, seq_lens, dev, "dst_block_table")
+    stride = _mass(mass, "mass", dev, B, max_blocks * PAGE_SIZE)
+    budget, sinks = _count(budget, "budget", 1), _count(sinks, "sinks")
+    recent = _count(recent, "recent")
+    on = _On(dev, stream)
+    if new_lens is None:
+        new_lens = on.new((B,), torch.int32)
+    if new_mass is None:
+        new_mass = on.new((B, NUM_KV_HEADS, dst_blocks * PAGE_SIZE), torch.float32)
+    if kept is None:
+        kept = on.new((B, NUM_KV_HEADS, budget), torch.int32)
+    _check(new_lens, "new_lens", torch.int32, 1, dev)
+    _check(kept, "kept", torch.int32, 3, dev)
+    if new_lens.shape[0] != B or tuple(kept.shape) != (B, NUM_KV_HEADS, budget):
+        raise ValueError("new_lens must be [batch] and kept [batch][8][budget]")
+    new_stride = _mass(new_mass, "new_mass", dev, B, budget)
+    if B == 0:
+        return new_lens, new_mass, kept
+    on.call("pkv_kv_evict", _ptr(mass), stride, _ptr(pool), num_pages, _ptr(block_table),
+            max_blocks, _ptr(seq_lens), B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, budget, sinks,
+            recent, _ptr(dst_block_table), dst_blocks, _ptr(new_lens), _ptr(new_mass), new_stride,
+            _ptr(kept), _err(dev_err, dev))
+    return new_lens, new_mass, kept
+
+
+def kv_append_at(k_new, v_new, pool, block_table, positions, slots, *,
+                 rope_theta: float = 500000.0, q_in=None, q_out=None, dev_err=None,
+                 stream=None) -> None:
+    """kv_append with the cache slot apart from the RoPE position: sequence b's
+    token is rotated for positions[b] and stored as cached token slots[b]."""
+    num_pages = _pool_pages(pool)
+    dev = _cuda(pool)
+    _check(block_table, "block_table", torch.int32, 2, dev)
+    _check(positions, "positions", torch.int32, 1, dev)
+    _check(slots, "slots", torch.int32, 1, dev)
+    B, max_blocks = block_table.shape
+    _heads(k_new, "k_new", dev, B, NUM_KV_HEADS)
+    _heads(v_new, "v_new", dev, B, NUM_KV_HEADS)
+    if positions.shape[0] != B or slots.shape[0] != B:
+        raise ValueError("positions, slots and block_table disagree on the batch")
+    Hq = 0
+    if q_in is not None or q_out is not None:
+        _heads(q_in, "q_in", dev, B)
+        _heads(q_out, "q_out", dev, B)
+        Hq = NUM_Q_HEADS
+    if B == 0:
+        return
+    _On(dev, stream).call(
+        "pkv_kv_append_at", _ptr(k_new), _ptr(v_new), _ptr(pool), num_pages, _ptr(block_table),
+        max_blocks, _ptr(positions), _ptr(slots), B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE,
+        float(rope_theta), _ptr(q_in), _ptr(q_out), Hq, _err(dev_err, dev))

@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kAppendThreads)
                      const uint16_t* __restrict__ v_new,
                      uint16_t* __restrict__ pool, int64_t num_pages,
                      const int32_t* __restrict__ block_table, int max_blocks,
-                     const int32_t* __restrict__ positions, RopeFreqs freqs,
+                     const int32_t* __restrict__ positions,
+                     const int32_t* __restrict__ slots, RopeFreqs freqs,
                      const uint16_t* __restrict__ q_in,
                      uint16_t* __restrict__ q_out, int32_t* dev_err) {
   const int b = blockIdx.x;
@@ -79,9 +80,11 @@ __global__ void __launch_bounds__(kAppendThreads)
   const uint32_t vw = reinterpret_cast<const uint32_t*>(v_new + src)[tid];
   const bool table_ok = rope_table_ready(freqs);
   const int32_t pos = positions[b];
-  const bool pos_ok = pos >= 0 && pos < max_blocks * kPageSize;
+  // where the token goes in the cache: at its position, unless told otherwise
+  const int32_t at = slots != nullptr ? slots[b] : pos;
+  const bool pos_ok = pos >= 0 && at >= 0 && at < max_blocks * kPageSize;
   const int32_t page =
-      pos_ok ? block_table[static_cast<int64_t>(b) * max_blocks + pos / kPageSize] : -1;
+      pos_ok ? block_table[static_cast<int64_t>(b) * max_blocks + at / kPageSize] : -1;
   RopeCS cs = rope_cs(freqs, table_ok, pos, i);
 
   // Optional out-of-place query rotation: 32 heads x 32 pairs, 4 per thread.
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     if (tid == 0) record_error(dev_err, kErrPage);
     return;
   }
-  const int slot = pos % kPageSize;
+  const int slot = at % kPageSize;
   uint16_t* k_dst = pool + ((static_cast<int64_t>(page) * 2 + 0) * kPageSize + slot) * row;
   uint16_t* v_dst = pool + ((static_cast<int64_t>(page) * 2 + 1) * kPageSize + slot) * row;
   uint16_t y1, y2;
@@ -511,12 +514,12 @@ cudaError_t launch_kv_write_prefill(const uint16_t* k, const uint16_t* v, int nu
 cudaError_t launch_kv_append(const uint16_t* k_new, const uint16_t* v_new,
                              uint16_t* pool, int64_t num_pages,
                              const int32_t* block_table, int max_blocks,
-                             const int32_t* positions, int batch,
+                             const int32_t* positions, const int32_t* slots, int batch,
                              const RopeFreqs& freqs, const uint16_t* q_in,
                              uint16_t* q_out, int32_t* dev_err,
                              cudaStream_t stream) {
   return launch_pdl(kv_append_kernel, dim3(batch), dim3(kAppendThreads), 0, stream, k_new,
-                    v_new, pool, num_pages, block_table, max_blocks, positions, freqs, q_in,
+                    v_new, pool, num_pages, block_table, max_blocks, positions, slots, freqs, q_in,
                     q_out, dev_err);
 }
 

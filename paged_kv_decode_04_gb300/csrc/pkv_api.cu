@@ -320,8 +320,8 @@ PKV_API int pkv_kv_append(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_bf16
       cudaSuccess)
     return PKV_ECUDA;
   const cudaError_t err = pkv::launch_kv_append(
-      k_new, v_new, pool, num_pages, block_table, max_blocks, positions, batch, freqs, q_in,
-      q_out, dev_err, reinterpret_cast<cudaStream_t>(stream));
+      k_new, v_new, pool, num_pages, block_table, max_blocks, positions, nullptr, batch, freqs,
+      q_in, q_out, dev_err, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -854,6 +854,261 @@ PKV_API int pkv_kv_write_prefill_layers(int layers, const pkv_bf16* k, const pkv
     if (err != cudaSuccess) return PKV_ECUDA;
   }
   return PKV_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Long contexts: chunks of new tokens, sliding windows with sinks, attention
+// weights and eviction by them, and the append at a slot of its own.
+
+namespace {
+
+// True when [p, p + n) and [q, q + m) share a byte.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p != nullptr && q != nullptr && n > 0 && m > 0 && a < b + m && b < a + n;
+}
+
+bool bad_cache(int batch, int64_t num_pages, int max_blocks) {
+  return batch < 0 || batch > 65535 || num_pages < 1 || num_pages > INT32_MAX || max_blocks < 1 ||
+         max_blocks > (INT32_MAX / kPageSize);
+}
+
+size_t q_row_bytes(int rows) {
+  return static_cast<size_t>(rows) * kNumQHeads * kHeadDim * sizeof(pkv_bf16);
+}
+
+}  // namespace
+
+extern "C" {
+
+PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_bf16* pool,
+                             int64_t num_pages, const int32_t* block_table, int max_blocks,
+                             const int32_t* positions, const int32_t* slots, int batch,
+                             int num_kv_heads, int head_dim, int page_size, double rope_theta,
+                             const pkv_bf16* q_in, pkv_bf16* q_out, int num_q_heads,
+                             int32_t* dev_err, pkv_stream_t stream) {
+  if (!k_new || !v_new || !pool || !block_table || !positions || !slots) return PKV_EINVAL;
+  if (bad_cache(batch, num_pages, max_blocks)) return PKV_EINVAL;
+  if ((q_in == nullptr) != (q_out == nullptr)) return PKV_EINVAL;
+  if (!(rope_theta > 0.0) || !isfinite(rope_theta)) return PKV_EINVAL;
+  if (num_kv_heads != kNumKvHeads || head_dim != kHeadDim || page_size != kPageSize)
+    return PKV_EUNSUPPORTED;
+  if (q_in != nullptr && num_q_heads != kNumQHeads) return PKV_EUNSUPPORTED;
+  if (!aligned(pool, 16) || !aligned(v_new, 4) || !aligned(k_new, 2) || !aligned(q_in, 2) ||
+      !aligned(q_out, 2) || !aligned(positions, 4) || !aligned(slots, 4) ||
+      !aligned(block_table, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  if (overlap(q_in, q_row_bytes(batch), q_out, q_row_bytes(batch))) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  pkv::RopeFreqs freqs;
+  if (pkv::prepare_rope(rope_theta, &freqs, st) != cudaSuccess) return PKV_ECUDA;
+  const cudaError_t err =
+      pkv::launch_kv_append(k_new, v_new, pool, num_pages, block_table, max_blocks, positions,
+                            slots, batch, freqs, q_in, q_out, dev_err, st);
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API size_t pkv_chunk_workspace_bytes(int num_tokens, int batch, int num_q_heads,
+                                         int num_kv_heads, int head_dim, int max_blocks,
+                                         int window, int sinks, int num_splits) {
+  if (num_tokens < 0 || bad_cache(batch, 1, max_blocks) || window < 0 || sinks < 0 ||
+      num_splits < 0 || !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
+    return static_cast<size_t>(-1);
+  return 0;
+}
+
+PKV_API int pkv_paged_chunk_attention(
+    const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const pkv_bf16* pool,
+    int64_t num_pages, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+    int batch, int num_q_heads, int num_kv_heads, int head_dim, int page_size, int window,
+    int sinks, float scale, pkv_bf16* out, void* workspace, size_t workspace_bytes,
+    int num_splits, int32_t* dev_err, pkv_stream_t stream) {
+  if (!q || !token_offsets || !pool || !block_table || !seq_lens || !out) return PKV_EINVAL;
+  if (num_tokens < 0 || bad_cache(batch, num_pages, max_blocks) || window < 0 || sinks < 0 ||
+      num_splits < 0)
+    return PKV_EINVAL;
+  if (!(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+  if (!supported_dims(num_q_heads, num_kv_heads, head_dim, page_size)) return PKV_EUNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+      !aligned(token_offsets, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  if (overlap(q, q_row_bytes(num_tokens), out, q_row_bytes(num_tokens))) return PKV_EINVAL;
+  if (batch == 0 || num_tokens == 0) return PKV_OK;
+  pkv::MaskedArgs a = {};
+  a.q = q;
+  a.pool = pool;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.token_offsets = token_offsets;
+  a.out = out;
+  a.dev_err = dev_err;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.num_tokens = num_tokens;
+  a.window = window > 0 ? window : INT32_MAX;
+  a.sinks = sinks;
+  a.num_splits = 1;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = pkv::wait_limit_ns();
+  const cudaError_t err = pkv::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API size_t pkv_window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int max_blocks, int window, int sinks,
+                                          int num_splits) {
+  if (bad_cache(batch, 1, max_blocks) || window < 1 || sinks < 0 || num_splits < 0 ||
+      !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
+    return static_cast<size_t>(-1);
+  return 0;
+}
+
+PKV_API int pkv_paged_window_attention(
+    const pkv_bf16* q, const pkv_bf16* pool, int64_t num_pages, const int32_t* block_table,
+    int max_blocks, const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, int window, int sinks, float scale, pkv_bf16* out,
+    void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
+    pkv_stream_t stream) {
+  if (!q || !pool || !block_table || !seq_lens || !out) return PKV_EINVAL;
+  if (bad_cache(batch, num_pages, max_blocks) || window < 1 || sinks < 0 || num_splits < 0)
+    return PKV_EINVAL;
+  if (!(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+  if (!supported_dims(num_q_heads, num_kv_heads, head_dim, page_size)) return PKV_EUNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 4) || !aligned(workspace, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  pkv::MaskedArgs a = {};
+  a.q = q;
+  a.pool = pool;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.dev_err = dev_err;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.num_tokens = batch;
+  a.window = window;
+  a.sinks = sinks;
+  a.num_splits = 1;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = pkv::wait_limit_ns();
+  const cudaError_t err = pkv::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API size_t pkv_scored_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int max_blocks, int num_splits) {
+  if (bad_cache(batch, 1, max_blocks) || num_splits < 0 ||
+      !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
+    return static_cast<size_t>(-1);
+  return 0;
+}
+
+PKV_API int pkv_paged_scored_attention(
+    const pkv_bf16* q, const pkv_bf16* pool, int64_t num_pages, const int32_t* block_table,
+    int max_blocks, const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, float scale, pkv_bf16* out, float* mass, int64_t mass_stride,
+    void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
+    pkv_stream_t stream) {
+  if (!q || !pool || !block_table || !seq_lens || !out || !mass) return PKV_EINVAL;
+  if (bad_cache(batch, num_pages, max_blocks) || num_splits < 0 ||
+      mass_stride < static_cast<int64_t>(max_blocks) * kPageSize)
+    return PKV_EINVAL;
+  if (!(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+  if (!supported_dims(num_q_heads, num_kv_heads, head_dim, page_size)) return PKV_EUNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 4) || !aligned(workspace, 16) ||
+      !aligned(mass, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  pkv::MaskedArgs a = {};
+  a.q = q;
+  a.pool = pool;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.mass = mass;
+  a.mass_stride = mass_stride;
+  a.dev_err = dev_err;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.num_tokens = batch;
+  a.window = INT32_MAX;
+  a.num_splits = 1;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = pkv::wait_limit_ns();
+  const cudaError_t err = pkv::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
+                         int64_t num_pages, const int32_t* block_table, int max_blocks,
+                         const int32_t* seq_lens, int batch, int num_kv_heads, int head_dim,
+                         int page_size, int budget, int sinks, int recent,
+                         const int32_t* dst_block_table, int dst_max_blocks, int32_t* new_lens,
+                         float* new_mass, int64_t new_mass_stride, int32_t* kept,
+                         int32_t* dev_err, pkv_stream_t stream) {
+  if (!mass || !pool || !block_table || !seq_lens || !dst_block_table || !new_lens ||
+      !new_mass || !kept)
+    return PKV_EINVAL;
+  if (bad_cache(batch, num_pages, max_blocks) || bad_cache(batch, num_pages, dst_max_blocks) ||
+      budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks ||
+      budget > static_cast<int64_t>(dst_max_blocks) * kPageSize ||
+      mass_stride < static_cast<int64_t>(max_blocks) * kPageSize || new_mass_stride < budget)
+    return PKV_EINVAL;
+  if (num_kv_heads != kNumKvHeads || head_dim != kHeadDim || page_size != kPageSize)
+    return PKV_EUNSUPPORTED;
+  if (!aligned(pool, 16) || !aligned(mass, 4) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(dst_block_table, 4) || !aligned(new_lens, 4) ||
+      !aligned(new_mass, 4) || !aligned(kept, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  // the outputs are written while the inputs are still read
+  const size_t rows = static_cast<size_t>(batch) * kNumKvHeads;
+  const struct { const void* p; size_t n; } in[] = {
+      {mass, rows * mass_stride * 4}, {seq_lens, static_cast<size_t>(batch) * 4},
+      {block_table, static_cast<size_t>(batch) * max_blocks * 4},
+      {dst_block_table, static_cast<size_t>(batch) * dst_max_blocks * 4}};
+  const struct { const void* p; size_t n; } outs[] = {
+      {new_lens, static_cast<size_t>(batch) * 4}, {new_mass, rows * new_mass_stride * 4},
+      {kept, rows * budget * 4}};
+  for (int o = 0; o < 3; ++o) {
+    for (const auto& i : in)
+      if (overlap(outs[o].p, outs[o].n, i.p, i.n)) return PKV_EINVAL;
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o].p, outs[o].n, outs[p].p, outs[p].n)) return PKV_EINVAL;
+  }
+  if (batch == 0) return PKV_OK;
+  pkv::EvictArgs a = {};
+  a.mass = mass;
+  a.pool = pool;
+  a.block_table = block_table;
+  a.dst_block_table = dst_block_table;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.new_mass = new_mass;
+  a.kept = kept;
+  a.dev_err = dev_err;
+  a.num_pages = num_pages;
+  a.mass_stride = mass_stride;
+  a.new_mass_stride = new_mass_stride;
+  a.max_blocks = max_blocks;
+  a.dst_max_blocks = dst_max_blocks;
+  a.batch = batch;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  const cudaError_t err = pkv::launch_kv_evict(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 }  // extern "C"

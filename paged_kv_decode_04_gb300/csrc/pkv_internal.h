@@ -153,10 +153,11 @@ struct SplitPlan {
   int pages_per_split;  // logical pages per range
 };
 
+// slots: the cache slot of each sequence's token, or nullptr for its position.
 cudaError_t launch_kv_append(const uint16_t* k_new, const uint16_t* v_new,
                              uint16_t* pool, int64_t num_pages,
                              const int32_t* block_table, int max_blocks,
-                             const int32_t* positions, int batch,
+                             const int32_t* positions, const int32_t* slots, int batch,
                              const RopeFreqs& freqs, const uint16_t* q_in,
                              uint16_t* q_out, int32_t* dev_err,
                              cudaStream_t stream);
@@ -246,6 +247,55 @@ cudaError_t launch_split_merge(const AttnArgs& args, int num_merges, cudaStream_
 cudaError_t launch_shared_prefix_attention(const CUtensorMap& pool_map, const AttnArgs& args,
                                            int num_shared, int range_pages, cudaStream_t stream,
                                            bool beside = false);
+
+// Attention of rows of new tokens over the paged cache under a causal mask, a
+// sliding window and sink tokens (chunk_attention.cu, window_attention.cu).
+// A query at position p sees cached token t when t <= p and (t > p - window
+// or t < sinks); window is at least 1 (INT32_MAX: no window).
+struct MaskedArgs {
+  const uint16_t* q;
+  const uint16_t* pool;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* token_offsets;  // chunks only: [batch + 1]
+  uint16_t* out;
+  float* mass;                   // weights per (sequence, kv head, token), or nullptr
+  float* part_acc;               // split partials: unnormalised accumulators
+  float* part_ml;                // and (max in log2 units, sum) pairs
+  float* scores;                 // scores of split sequences (weights wanted only)
+  int32_t* dev_err;
+  int64_t num_pages;
+  int64_t mass_stride;
+  int max_blocks;
+  int batch;
+  int num_tokens;
+  int window;
+  int sinks;
+  int num_splits;
+  float scale_log2;              // softmax scale * log2(e)
+  unsigned long long wait_ns;
+};
+
+cudaError_t launch_chunk_attention(const MaskedArgs& args, cudaStream_t stream);
+
+struct EvictArgs {
+  const float* mass;
+  uint16_t* pool;
+  const int32_t* block_table;
+  const int32_t* dst_block_table;
+  const int32_t* seq_lens;
+  int32_t* new_lens;
+  float* new_mass;
+  int32_t* kept;
+  int32_t* dev_err;
+  int64_t num_pages;
+  int64_t mass_stride, new_mass_stride;
+  int max_blocks, dst_max_blocks;
+  int batch;
+  int budget, sinks, recent;
+};
+
+cudaError_t launch_kv_evict(const EvictArgs& args, cudaStream_t stream);
 
 // Largest logical page range one attention CTA handles.
 int max_pages_per_split();
