@@ -1,14 +1,50 @@
-// chunk_attention.cu -- attention of new tokens over the paged cache under a
-// causal mask, a sliding window and sink tokens, and the accumulation of the
-// attention weights.
+// chunk_attention.cu -- attention of a ragged batch of new tokens over the
+// paged cache under a causal mask, a sliding window and sink tokens, on the
+// fifth-generation tensor cores (tcgen05, accumulators in TMEM).
 //
-// One CTA per (query token, kv head), one warp per query head of the group:
-// lane i of a warp scores key t0 + i (64 dims in registers of the query), the
-// warp takes one FP32 online-softmax step per 32 keys, and lane i then adds
-// the weighted values of dims 2i and 2i + 1.
+// A query at position p sees token t when t <= p and (t > p - window or
+// t < sinks).  A tile is up to 64 consecutive new tokens of one sequence; for
+// one kv head their 4 query heads each make 256 rows (row = 4 token + head),
+// two MMA row tiles of 128, which share every K/V row that is loaded.  The
+// cached tokens come in tiles of 128 (8 pages).  Per row tile and kv tile
+//
+//   S = Q K^T   (128 x 128, 4 MMAs of K = 16; Q and K rows in shared memory)
+//   P = 2^(c S - m), the FP32 online softmax, one thread per row
+//   O += P V    (128 x 64, 8 MMAs of K = 16; P in TMEM, V rows in shared)
+//
+// A tile of at most 32 tokens has one row tile only; the two softmax warp
+// groups then take the even and the odd kv tiles of the same rows, and their
+// states are joined at the end like two ranges.
+//
+// TMEM (512 columns): S of row tile / group w at 128 w, P at 256 + 64 w, O at
+// 384 + 64 w.  P does not lie over S, so S of the next kv tile is computed
+// while this one's exponentials are taken.
+//
+// Warps, one persistent CTA per SM, each role walking the CTA's items (tile,
+// kv head, range of the kv tiles) and handing over through mbarriers, so the
+// next item's loads and first products run under the last one's epilogue:
+//   0-3, 4-7  softmax of S_0 and S_1, rescaling of O, epilogue
+//   8         issues the MMAs: QK(u + 2) before PV(u) where it can, u counting
+//             the (row tile, kv tile) units, which alternate between S_0, S_1
+//   9         loads: Q by one box per row tile, K and V by 2 KiB boxes of one
+//             page and head; pages outside every row's sight (or with a bad
+//             id) are read at a page index past the pool, i.e. as zeros
+//   10        finds the CTA's next item from the offsets and lengths; items
+//             without any kv tile it answers itself
+//   11        relays "V has landed", and in the tiles that some row sees in
+//             part only it first replaces non-finite V values by zero (a
+//             masked weight is zero, but 0 x NaN is not); rows that do see
+//             such a value get it added in the epilogue
+// P enters the product with V as bf16 (8 significant bits, an error of at
+// most 2^-8 of sum p |v|, averaged over the tokens, below the output's own
+// bf16 rounding); the row sums take the unrounded FP32 values.  The reference
+// maximum moves only when a score exceeds it by 2^8, so O is rarely rescaled.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -18,128 +54,878 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kQTokens = kChunkTileTokens;    // 64 tokens a tile
+constexpr int kHalfTokens = kQTokens / 2;     // 32 tokens: one MMA row tile
+constexpr int kKvTokens = kChunkKvTokens;     // 128 cached tokens a kv tile
+constexpr int kKvPages = kKvTokens / kPageSize;
+constexpr int kRow = kHeadDim * 2;            // 128 B
+constexpr int kRowTileBytes = 128 * kRow;     // 16 KiB: a row tile of Q, a kv tile of K or V
+constexpr int kPageBytes = kPageSize * kRow;  // 2 KiB: one head's K (or V) rows of a page
+constexpr int kStages = 4;                    // kv tiles in flight
+constexpr int kItems = 4;                     // items published ahead
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10, kFixWarp = 11;
+constexpr int kThreads = 32 * 12;
+// Registers: 168 x 384 threads at launch = 64512 = 256 x 216 + 128 x 72.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads,
+              "the split stays within the registers the block starts with");
+constexpr float kRescale = 8.0f;
 
-// Dot product of a query row (floats in shared memory) and a key row.
-__device__ __forceinline__ float dot_row(const float* q, const uint16_t* k) {
-  const uint4* kw = reinterpret_cast<const uint4*>(k);
-  float s = 0.f;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint4 w = kw[c];
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = bf16x2_to_float2(ws[e]);
-      s = fmaf(f.x, q[8 * c + 2 * e], s);
-      s = fmaf(f.y, q[8 * c + 2 * e + 1], s);
-    }
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemP = 256, kTmemO = 384;
+constexpr uint32_t kIdescQK = tc_idesc_bf16(128, kKvTokens, false);
+constexpr uint32_t kIdescPV = tc_idesc_bf16(128, kHeadDim, true);
+
+// Shared memory, from a 1024-byte aligned base.
+constexpr int kOffQ = 0;                               // [2 items][2 row tiles]
+constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
+constexpr int kOffV = kOffK + kStages * kRowTileBytes;
+constexpr int kOffMl = kOffV + kStages * kRowTileBytes;  // [2][128] (m, l) handed between groups
+constexpr int kOffItems = kOffMl + 2 * 128 * 8;
+constexpr int kItemWords = 16;
+constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
+enum {
+  kBarKFull = 0,
+  kBarKEmpty = kBarKFull + kStages,
+  kBarVFull = kBarKEmpty + kStages,
+  kBarVReady = kBarVFull + kStages,
+  kBarVEmpty = kBarVReady + kStages,
+  kBarQFull = kBarVEmpty + kStages,
+  kBarQEmpty = kBarQFull + 2,
+  kBarSFull = kBarQEmpty + 2,
+  kBarSFree = kBarSFull + 2,
+  kBarPFull = kBarSFree + 2,
+  kBarPvDone = kBarPFull + 2,
+  kBarItemFull = kBarPvDone + 2,
+  kBarItemEmpty = kBarItemFull + kItems,
+  kBarXch = kBarItemEmpty + kItems,
+  kBarFin = kBarXch + 2,
+  kNumBars
+};
+// Bad-page bits of the last kv tiles, then the TMEM address.  Twice the stages:
+// while a softmax group reads kv tile j's, QK(j + 2) has not been issued, so
+// the loads are at tile j + 1 + kStages at most.
+constexpr int kMeta = 2 * kStages;
+constexpr int kOffMeta = kOffBars + 8 * kNumBars;
+constexpr int kSmem = 1024 + kOffMeta + 4 * (kMeta + 4);
+static_assert(kSmem <= 227 * 1024, "fits one CTA");
+
+// One item as the roles see it (also its words in shared memory).
+struct Item {
+  int b;        // sequence, -1: no more items
+  int row0;     // row of q of the tile's first token
+  int nt;       // its tokens
+  int pos0;     // position of the first (negative: before the sequence)
+  int g;        // kv head
+  int split;    // range
+  int ns;       // kv tiles of sinks in front of the window's
+  int w0;       // first kv tile of the window
+  int t0, t1;   // range [t0, t1) of the tile's list: sinks, then window
+  int lo;       // first token of any row's window
+  int first_w;  // softmax group of the first unit
+  int bad;      // a live non-finite V value was replaced (the relay's answer)
+  int pad[3];
+
+  __device__ __forceinline__ bool halves() const { return nt <= kHalfTokens; }
+  __device__ __forceinline__ int tiles() const { return t1 - t0; }
+  __device__ __forceinline__ int units() const { return halves() ? tiles() : 2 * tiles(); }
+  __device__ __forceinline__ int units_of(int w) const {
+    return halves() ? (tiles() + (w == first_w ? 1 : 0)) >> 1 : tiles();
   }
-  return s;
+  __device__ __forceinline__ int tile(int k) const { return k < ns ? k : w0 + (k - ns); }
+  __device__ __forceinline__ int end() const { return pos0 + nt; }  // tokens seen by the last row
+  // Some row of the tile does not see some token of this kv tile.
+  __device__ __forceinline__ bool partial(int tile, const MaskedArgs& a) const {
+    const int base = tile * kKvTokens, last = base + kKvTokens - 1;
+    if (last > pos0) return true;
+    const int64_t gone = static_cast<int64_t>(end()) - 1 - a.window;  // last token out of the window
+    const int64_t from = base > a.sinks ? base : a.sinks;
+    return from <= (gone < last ? gone : last);
+  }
+};
+static_assert(sizeof(Item) == kItemWords * 4, "item words");
+
+__device__ __forceinline__ Item read_item(const int* w) {
+  Item it;
+  const int4* p = reinterpret_cast<const int4*>(w);
+  const int4 a = p[0], b = p[1], c = p[2];
+  it.b = a.x; it.row0 = a.y; it.nt = a.z; it.pos0 = a.w;
+  it.g = b.x; it.split = b.y; it.ns = b.z; it.w0 = b.w;
+  it.t0 = c.x; it.t1 = c.y; it.lo = c.z; it.first_w = c.w;
+  it.bad = it.pad[0] = it.pad[1] = it.pad[2] = 0;
+  return it;
 }
 
-__global__ void __launch_bounds__(128) masked_attention_kernel(const MaskedArgs a) {
-  __shared__ float s_q[kGroup][kHeadDim];
-  __shared__ float s_m[kGroup], s_l[kGroup];
-  const int g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;  // query token
+// 3-D box of a tensor map, with the default L2 policy: K/V rows are read again
+// by the other row tiles.
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                             int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long ra, rb, rd;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
+}
+
+// Bits [lo, hi) of 32 (bounds outside are clamped).
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  lo = lo < 0 ? 0 : lo;
+  hi = hi > 32 ? 32 : hi;
+  if (lo >= hi) return 0u;
+  return (0xFFFFFFFFu >> (32 - hi)) & (0xFFFFFFFFu << lo);
+}
+
+__device__ __forceinline__ int clamp_cols(int64_t v) {
+  return v < -1 ? -1 : (v > kKvTokens ? kKvTokens : static_cast<int>(v));
+}
+
+// bf16 pair: mask of the halves that are not finite.
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
+  return ((w & 0x00007F80u) == 0x00007F80u ? 0x0000FFFFu : 0u) |
+         ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
+    const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap page_map,
+    const MaskedArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_addr(smem);
+  auto bar = [&](int i) { return sb + kOffBars + 8u * i; };
+  int* s_items = reinterpret_cast<int*>(smem + kOffItems);
+  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta], then the TMEM address
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // Barriers and TMEM before a dependent grid may start: its CTAs then never
+  // take columns that this one still needs.
+  if (tid == 0) {
+    tma_prefetch_desc(&q_map);
+    tma_prefetch_desc(&page_map);
+    for (int i = 0; i < kNumBars; ++i) {
+      int n = 1;
+      if (i >= kBarQEmpty && i < kBarSFull) n = kSoftmaxWarps;
+      if (i >= kBarSFree && i < kBarPvDone) n = 4;               // s_free, p_full
+      if (i >= kBarItemEmpty && i < kBarXch) n = kSoftmaxWarps + 3;
+      if (i >= kBarXch && i < kBarFin) n = 4;
+      mbar_init(bar(i), n);
+    }
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_alloc(sb + kOffMeta + 4 * kMeta, kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = s_meta[kMeta];
   wait_for_prior_grids();
   allow_dependent_grids();
-  int b = static_cast<int>(row), ahead = 0;  // tokens of the sequence after this one
-  if (a.token_offsets != nullptr) {
-    if (row == 0 && g == 0)
-      for (int i = threadIdx.x; i <= a.batch; i += 128) {
-        const int32_t o = a.token_offsets[i];
-        if (o < 0 || o > a.num_tokens || (i > 0 && o < a.token_offsets[i - 1]))
-          record_error(a.dev_err, kErrOffsets);
+
+  bool ok = true;
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSchedWarp) {
+      // ------------------------------------------------------ scheduler
+      // Items in order (tile, range, head); the tiles of a sequence from its
+      // last (under a causal mask the longest) to its first.  Every second
+      // round runs through the CTAs backwards, so that long items pair with
+      // short ones.
+      const int per_tile = a.num_splits * kNumKvHeads;
+      int b0 = -32, before = 0, sum = 0;      // 32 sequences from b0: tiles before them, theirs
+      int cnt = 0, incl = 0, o0 = 0, o1 = 0;  // this lane's sequence
+      int parity = 0, out_i = 0;              // units so far mod 2, items published
+      bool more = true;
+      for (int round = 0; more; ++round) {
+        const int64_t idx = static_cast<int64_t>(round) * gridDim.x +
+                            ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const int64_t tile64 = idx / per_tile;
+        const int rest = static_cast<int>(idx % per_tile);
+        while (b0 < a.batch && tile64 >= static_cast<int64_t>(before) + sum) {
+          before += sum;
+          b0 += 32;
+          const int b = b0 + lane;
+          cnt = 0;
+          if (b < a.batch) {
+            o0 = a.token_offsets[b];
+            o1 = a.token_offsets[b + 1];
+            if (o0 < 0 || o1 < o0 || o1 > a.num_tokens) {
+              if (blockIdx.x == 0) record_error(a.dev_err, kErrOffsets);
+            } else {
+              cnt = (o1 - o0 + kQTokens - 1) / kQTokens;
+            }
+          }
+          incl = cnt;
+#pragma unroll
+          for (int x = 1; x < 32; x <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, x);
+            if (lane >= x) incl += y;
+          }
+          sum = __shfl_sync(kFull, incl, 31);
+        }
+        Item it = {};
+        it.b = -1;
+        more = b0 < a.batch;
+        if (more) {
+          const int at = static_cast<int>(tile64 - before);
+          const int src = __ffs(__ballot_sync(kFull, at < incl)) - 1;
+          const int s_incl = __shfl_sync(kFull, incl, src);
+          const int s_o0 = __shfl_sync(kFull, o0, src), s_o1 = __shfl_sync(kFull, o1, src);
+          const int n = s_o1 - s_o0;
+          const int qt = s_incl - 1 - at;  // the last tile of the sequence first
+          it.b = b0 + src;
+          it.row0 = s_o0 + qt * kQTokens;
+          it.nt = min(kQTokens, n - qt * kQTokens);
+          it.g = rest % kNumKvHeads;
+          it.split = rest / kNumKvHeads;
+          const int Lmax = a.max_blocks * kPageSize;
+          int L = a.seq_lens[it.b];
+          if (L < 0 || L > Lmax) {
+            if (lane == 0) record_error(a.dev_err, kErrSeqLen);
+            L = L < 0 ? 0 : Lmax;
+          }
+          it.pos0 = L - n + qt * kQTokens;
+          if (it.pos0 < 0 && lane == 0) record_error(a.dev_err, kErrPosition);
+          const int p0 = max(it.pos0, 0);
+          it.lo = p0 >= a.window ? p0 - a.window + 1 : 0;
+          it.w0 = it.lo / kKvTokens;
+          it.ns = min((min(a.sinks, it.lo) + kKvTokens - 1) / kKvTokens, it.w0);
+          const int tiles =
+              it.end() > 0 ? it.ns + (it.end() + kKvTokens - 1) / kKvTokens - it.w0 : 0;
+          it.t0 = static_cast<int>(static_cast<int64_t>(tiles) * it.split / a.num_splits);
+          it.t1 = static_cast<int>(static_cast<int64_t>(tiles) * (it.split + 1) / a.num_splits);
+          if (it.tiles() == 0) {
+            // nothing to see in this range: zero rows, or empty partials
+            for (int r = lane; r < it.nt * kGroup; r += 32) {
+              const int64_t row = static_cast<int64_t>(it.row0 + r / kGroup) * kNumQHeads +
+                                  it.g * kGroup + r % kGroup;
+              if (a.num_splits == 1) {
+                uint4* dst = reinterpret_cast<uint4*>(a.out + row * kHeadDim);
+                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                *reinterpret_cast<float2*>(a.part_ml + 2 * (row * a.num_splits + it.split)) =
+                    make_float2(-INFINITY, 0.f);
+              }
+            }
+            continue;
+          }
+          it.first_w = parity;
+          parity = (parity + it.units()) & 1;
+        }
+        const int slot = out_i % kItems;
+        if (out_i >= kItems &&
+            !mbar_wait_bounded(bar(kBarItemEmpty + slot), (out_i / kItems - 1) & 1, a.wait_ns))
+          ok = false;
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          int4* w = reinterpret_cast<int4*>(s_items + slot * kItemWords);
+          w[0] = make_int4(it.b, it.row0, it.nt, it.pos0);
+          w[1] = make_int4(it.g, it.split, it.ns, it.w0);
+          w[2] = make_int4(it.t0, it.t1, it.lo, it.first_w);
+          w[3] = make_int4(0, 0, 0, 0);
+          mbar_arrive(bar(kBarItemFull + slot));
+        }
+        __syncwarp();
+        ++out_i;
       }
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.token_offsets[mid] <= row) lo = mid; else hi = mid;
-    }
-    b = lo;
-    if (row < a.token_offsets[b] || row >= a.token_offsets[b + 1]) return;  // no sequence's token
-    ahead = static_cast<int>(a.token_offsets[b + 1] - 1 - row);
-  }
-  const int Lmax = a.max_blocks * kPageSize;
-  int L = a.seq_lens[b];
-  if (L < 0 || L > Lmax) {
-    if (threadIdx.x == 0) record_error(a.dev_err, kErrSeqLen);
-    L = L < 0 ? 0 : Lmax;
-  }
-  const int pos = L - 1 - ahead;
-  if (pos < 0 && a.token_offsets != nullptr && threadIdx.x == 0) record_error(a.dev_err, kErrPosition);
-  const int64_t qrow = row * kNumQHeads + g * kGroup + warp;
-  s_q[warp][2 * lane] = bf16_to_float(a.q[qrow * kHeadDim + 2 * lane]);
-  s_q[warp][2 * lane + 1] = bf16_to_float(a.q[qrow * kHeadDim + 2 * lane + 1]);
-  __syncwarp();
-  const int first = pos >= a.window ? pos - a.window + 1 : 0;  // of the window
-  const int sink = min(a.sinks, first);
-  // visible index i: sinks, then the window
-  const int n = pos < 0 ? 0 : sink + (pos + 1 - first);
-  auto token = [&](int i) { return i < sink ? i : first + (i - sink); };
-  auto key_row = [&](int t) -> const uint16_t* {
-    const int32_t pid = a.block_table[static_cast<int64_t>(b) * a.max_blocks + t / kPageSize];
-    if (pid < 0 || pid >= a.num_pages) {
-      record_error(a.dev_err, kErrPage);
-      return nullptr;
-    }
-    return a.pool + ((static_cast<int64_t>(pid) * 2 * kPageSize + t % kPageSize) * kNumKvHeads + g) *
-                        kHeadDim;
-  };
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const uint16_t* kr = i0 + lane < n ? key_row(token(i0 + lane)) : nullptr;
-    const float s = kr != nullptr ? dot_row(s_q[warp], kr) * a.scale_log2 : -INFINITY;
-    float mx = s;
+    } else if (warp == kLoadWarp) {
+      // ----------------------------------------------------------- loads
+      int kt = 0, qn = 0;  // kv tiles and items loaded so far
+      int k_issued = 0, v_issued = 0;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kItems;
+        if (!mbar_wait_bounded(bar(kBarItemFull + slot), (i / kItems) & 1, a.wait_ns)) ok = false;
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        const Item it = read_item(s_items + slot * kItemWords);
+        __syncwarp();
+        if (it.b < 0) break;
+        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+        const int qb = qn & 1;
+        if (qn >= 2 && !mbar_wait_bounded(bar(kBarQEmpty + qb), (qn / 2 - 1) & 1, a.wait_ns))
+          ok = false;
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t qbar = bar(kBarQFull + qb);
+          const uint32_t dst = sb + kOffQ + qb * 2 * kRowTileBytes;
+          mbar_arrive_expect_tx(qbar, (it.halves() ? 1 : 2) * kRowTileBytes);
+          tma_load_box(dst, &q_map, qbar, 0, it.g * kGroup, it.row0);
+          if (!it.halves())
+            tma_load_box(dst + kRowTileBytes, &q_map, qbar, 0, it.g * kGroup,
+                         it.row0 + kHalfTokens);
+        }
+        __syncwarp();
+        ++qn;
+        const int64_t bt = static_cast<int64_t>(it.b) * a.max_blocks;
+        const int end = it.end();
+        // lane p < 8: page id of page p of the kv tile, one tile ahead
+        auto page_of = [&](int k) {
+          int pid = -2;  // no row sees it
+          if (lane < kKvPages && k < it.t1) {
+            const int page = it.tile(k) * kKvPages + lane, t = page * kPageSize;
+            if (t < end && (t + kPageSize > it.lo || t < a.sinks)) {
+              pid = a.block_table[bt + page];
+              if (pid < 0 || pid >= a.num_pages) {
+                record_error(a.dev_err, kErrPage);
+                pid = -1;
+              }
+            }
+          }
+          return pid;
+        };
+        int next = page_of(it.t0);
+        for (int k = it.t0; k < it.t1; ++k, ++kt) {
+          const int pid = next;
+          next = page_of(k + 1);
+          const int st = kt % kStages;
+          const uint32_t par = (kt / kStages - 1) & 1;
+          const unsigned bad = __ballot_sync(kFull, pid == -1) & 0xFFu;
+          if (kt >= kStages && !mbar_wait_bounded(bar(kBarKEmpty + st), par, a.wait_ns)) ok = false;
+          if (!__all_sync(kFull, ok)) {
+            ok = false;
+            break;
+          }
+          const int z = pid < 0 ? static_cast<int>(a.num_pages) : pid;  // past the pool: zeros
+          if (lane == 0) {
+            s_meta[kt % kMeta] = bad;
+            mbar_arrive_expect_tx(bar(kBarKFull + st), kRowTileBytes);
+          }
+          __syncwarp();
+          if (lane < kKvPages)
+            tma_load_box(sb + kOffK + st * kRowTileBytes + lane * kPageBytes, &page_map,
+                         bar(kBarKFull + st), it.g * kHeadDim, 0, z);
+          k_issued = kt + 1;
+          if (kt >= kStages && !mbar_wait_bounded(bar(kBarVEmpty + st), par, a.wait_ns)) ok = false;
+          if (!__all_sync(kFull, ok)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + st), kRowTileBytes);
+          __syncwarp();
+          if (lane < kKvPages)
+            tma_load_box(sb + kOffV + st * kRowTileBytes + lane * kPageBytes, &page_map,
+                         bar(kBarVFull + st), it.g * kHeadDim, kPageSize, z);
+          v_issued = kt + 1;
+        }
+      }
+      // every copy issued has landed before the CTA ends (full limit)
+      for (int j = max(0, k_issued - kStages); j < k_issued; ++j)
+        if (!mbar_wait_bounded(bar(kBarKFull + j % kStages), (j / kStages) & 1) && lane == 0)
+          record_error(a.dev_err, kErrTimeout);
+      for (int j = max(0, v_issued - kStages); j < v_issued; ++j)
+        if (!mbar_wait_bounded(bar(kBarVFull + j % kStages), (j / kStages) & 1) && lane == 0)
+          record_error(a.dev_err, kErrTimeout);
+      for (int j = max(0, qn - 2); j < qn; ++j)
+        if (!mbar_wait_bounded(bar(kBarQFull + (j & 1)), (j >> 1) & 1) && lane == 0)
+          record_error(a.dev_err, kErrTimeout);
+    } else if (warp == kFixWarp) {
+      // ---------------------------------------------------- V's relay
+      int kt = 0;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kItems;
+        if (!mbar_wait_bounded(bar(kBarItemFull + slot), (i / kItems) & 1, a.wait_ns)) ok = false;
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        const Item it = read_item(s_items + slot * kItemWords);
+        if (it.b < 0) break;
+        bool live_bad = false;
+        for (int k = it.t0; k < it.t1; ++k, ++kt) {
+          const int st = kt % kStages, tile = it.tile(k);
+          if (!mbar_wait_bounded(bar(kBarVFull + st), (kt / kStages) & 1, a.wait_ns)) ok = false;
+          if (!__all_sync(kFull, ok)) {
+            ok = false;
+            break;
+          }
+          if (it.partial(tile, a)) {
+            // 4 rows of 8 16-byte chunks at a time (the swizzle permutes
+            // chunks within a row only)
+            const uint32_t v0 = sb + kOffV + st * kRowTileBytes + lane * 16;
+            const int row_end = it.end() - tile * kKvTokens;  // rows that some query sees
+            for (int r = 0; r < kKvTokens; r += 16) {
+              uint4 x[4];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;  // no live key so far
-    const float r = fast_exp2(m - mn);
-    const float p = kr != nullptr ? fast_exp2(s - mn) : 0.f;
-    m = mn;
-    l = l * r + p;
-    o0 *= r;
-    o1 *= r;
-    for (int k = 0; k < 32; ++k) {
-      const float pk = __shfl_sync(kFull, p, k);
-      const unsigned long long vp = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(kr), k);
-      if (vp == 0) continue;
-      const uint32_t w = reinterpret_cast<const uint32_t*>(
-          reinterpret_cast<const uint16_t*>(vp) + kPageSize * kNumKvHeads * kHeadDim)[lane];
-      const float2 v = bf16x2_to_float2(w);
-      o0 = fmaf(pk, v.x, o0);
-      o1 = fmaf(pk, v.y, o1);
+              for (int e = 0; e < 4; ++e) x[e] = lds128(v0 + (r + 4 * e) * kRow);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t m0 = nonfinite_halves(x[e].x), m1 = nonfinite_halves(x[e].y),
+                               m2 = nonfinite_halves(x[e].z), m3 = nonfinite_halves(x[e].w);
+                if ((m0 | m1 | m2 | m3) != 0u) {
+                  if (r + 4 * e + (lane >> 3) < row_end) live_bad = true;
+                  sts128(v0 + (r + 4 * e) * kRow, x[e].x & ~m0, x[e].y & ~m1, x[e].z & ~m2,
+                         x[e].w & ~m3);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          const bool any = __any_sync(kFull, live_bad);
+          if (lane == 0) {
+            if (k == it.t1 - 1) s_items[slot * kItemWords + 12] = any ? 1 : 0;
+            mbar_arrive(bar(kBarVReady + st));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+      }
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ MMAs
+      struct Cursor {
+        int i = -1;   // item
+        int u = 0, U = 0;
+        int kt = 0;   // kv tiles before the item
+        bool end = false;
+        Item it;
+      } cq, cp;       // QK(u) and PV(u)
+      int n_s = 0, n_p = 0;  // units whose QK / PV was issued; unit n is group (n & 1)'s n / 2th
+      // to the next unit; false: a wait ran out
+      auto next = [&](Cursor& c, bool release) {
+        if (c.end || c.u < c.U) return true;
+        if (c.i >= 0) {
+          if (release) mbar_arrive(bar(kBarItemEmpty + c.i % kItems));
+          c.kt += c.it.tiles();
+        }
+        ++c.i;
+        const int slot = c.i % kItems;
+        if (!mbar_wait_bounded(bar(kBarItemFull + slot), (c.i / kItems) & 1, a.wait_ns))
+          return false;
+        c.it = read_item(s_items + slot * kItemWords);
+        c.u = 0;
+        c.end = c.it.b < 0;
+        c.U = c.end ? 0 : c.it.units();
+        return true;
+      };
+      auto issue_qk = [&]() {
+        const bool one = cq.it.halves();
+        const int w = n_s & 1;
+        const int kt = cq.kt + (one ? cq.u : cq.u >> 1), st = kt % kStages, qb = cq.i & 1;
+        if (cq.u == 0 && !mbar_wait_bounded(bar(kBarQFull + qb), (cq.i >> 1) & 1, a.wait_ns))
+          return false;
+        if (!mbar_wait_bounded(bar(kBarKFull + st), (kt / kStages) & 1, a.wait_ns)) return false;
+        if (n_s >= 2 &&
+            !mbar_wait_bounded(bar(kBarSFree + w), ((n_s >> 1) - 1) & 1, a.wait_ns))
+          return false;
+        tc_fence_after_sync();
+        const uint32_t q = sb + kOffQ + (2 * qb + (one ? 0 : w)) * kRowTileBytes;
+        const uint32_t kr = sb + kOffK + st * kRowTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < kHeadDim / 16; ++kk)
+          tc_mma_bf16(tmem + 128 * w, sw128_desc(q + 32 * kk), sw128_desc(kr + 32 * kk), kIdescQK,
+                      kk > 0 ? 1u : 0u);
+        tc_commit(bar(kBarSFull + w));
+        if (one || (cq.u & 1)) tc_commit(bar(kBarKEmpty + st));
+        ++n_s;
+        ++cq.u;
+        return true;
+      };
+      while (ok) {
+        if (!next(cp, true)) {
+          ok = false;
+          break;
+        }
+        if (cp.end) break;
+        // QK up to two units ahead, but no further than the next item: the
+        // one after it takes the Q buffer that this item still holds
+        while (ok && n_s < n_p + 3) {
+          ok = next(cq, false);
+          if (!ok || cq.end || cq.i > cp.i + 1) break;
+          ok = issue_qk();
+        }
+        if (!ok) break;
+        const bool one = cp.it.halves();
+        const int w = n_p & 1;
+        const int kt = cp.kt + (one ? cp.u : cp.u >> 1), st = kt % kStages;
+        if (!mbar_wait_bounded(bar(kBarVReady + st), (kt / kStages) & 1, a.wait_ns) ||
+            !mbar_wait_bounded(bar(kBarPFull + w), (n_p >> 1) & 1, a.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t vr = sb + kOffV + st * kRowTileBytes;
+        const bool first = cp.u < 2;  // the group's first unit of this item
+#pragma unroll
+        for (int p = 0; p < kKvPages; ++p)
+          tc_mma_bf16_ta(tmem + kTmemO + kHeadDim * w, tmem + kTmemP + 64 * w + 8 * p,
+                         sw128_desc(vr + p * kPageBytes), kIdescPV, (p > 0 || !first) ? 1u : 0u);
+        tc_commit(bar(kBarPvDone + w));
+        if (one || (cp.u & 1)) tc_commit(bar(kBarVEmpty + st));
+        ++n_p;
+        ++cp.u;
+      }
+      // no MMA in flight past here
+      tc_commit(bar(kBarFin));
+      if (!mbar_wait_bounded(bar(kBarFin), 0)) record_error(a.dev_err, kErrTimeout);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // --------------------------------------------------- softmax, epilogue
+    const int w = warp >> 2;
+    const int row = tid & 127;                 // MMA row = TMEM lane
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tS = t_lane + 128 * w, tP = t_lane + kTmemP + 64 * w,
+                   tO = t_lane + kTmemO + kHeadDim * w;
+    const float c = a.scale_log2;
+    // this group's units, kv tiles of the items before, rows handed over
+    int units = 0, kt0 = 0, xch0 = 0, xch1 = 0;
+    for (int i = 0; ok; ++i) {
+      const int slot = i % kItems;
+      if (!mbar_wait_bounded(bar(kBarItemFull + slot), (i / kItems) & 1, a.wait_ns)) ok = false;
+      if (!__all_sync(kFull, ok)) {
+        ok = false;
+        break;
+      }
+      const Item it = read_item(s_items + slot * kItemWords);
+      if (it.b < 0) break;
+      const int qb = i & 1;
+      // Q has landed, so both groups are done with its buffer's last item, and
+      // this one's arrivals count for this item also when it has no unit of it
+      if (!mbar_wait_bounded(bar(kBarQFull + qb), (i >> 1) & 1, a.wait_ns)) ok = false;
+      if (!__all_sync(kFull, ok)) {
+        ok = false;
+        break;
+      }
+      const bool one = it.halves();
+      const int tok = (row >> 2) + (one ? 0 : kHalfTokens * w);
+      const int pos = it.pos0 + tok;
+      const bool idle = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w) >= it.nt;  // whole warp
+      float m_ref = -INFINITY, l_run = 0.f;
+      const int nu = it.units_of(w);
+      for (int v = 0; v < nu; ++v, ++units) {
+        // place in the item's list of kv tiles
+        const int kk = one ? 2 * v + (w == it.first_w ? 0 : 1) : v;
+        const int tile = it.tile(it.t0 + kk);
+        if (!mbar_wait_bounded(bar(kBarSFull + w), units & 1, a.wait_ns)) ok = false;
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t s[8][16];
+        float alpha = 1.f;
+        bool grow = false;
+        if (!idle) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) tmem_ld16(tS + 16 * q, s[q]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) reg_after_wait(s[q]);
+        }
+        tc_fence_before_sync();
+        // (written before the loads that QK waited for)
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(s_meta + (kt0 + kk) % kMeta);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBarSFree + w));
+          if (v == nu - 1 && !one) mbar_arrive(bar(kBarQEmpty + qb));
+        }
+        if (!idle) {
+          if (bad != 0u || it.partial(tile, a)) {
+            const int64_t base = static_cast<int64_t>(tile) * kKvTokens;
+            const int ch = clamp_cols(pos - base) + 1;  // columns [0, ch): t <= pos
+            // [cl, ..): t > pos - window; [0, cs): t < sinks
+            const int cl = clamp_cols(static_cast<int64_t>(pos) - a.window - base) + 1;
+            const int cs = clamp_cols(a.sinks - base);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t vis = bits_between(0, ch - 32 * q) &
+                             (bits_between(cl - 32 * q, 32) | bits_between(0, cs - 32 * q));
+              if ((bad >> (2 * q)) & 1u) vis &= 0xFFFF0000u;
+              if ((bad >> (2 * q + 1)) & 1u) vis &= 0x0000FFFFu;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((vis >> e) & 1u)) s[2 * q + (e >> 4)][e & 15] = 0xFF800000u;  // -inf
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[q][e]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          grow = top > m_ref + kRescale;
+          if (grow) {
+            alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
+            m_ref = top;
+          }
+          // (a row that has seen no token yet: every weight 2^(-inf) = 0)
+          const float m = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float2 x = ffma2(make_float2(__uint_as_float(s[q][2 * e]),
+                                           __uint_as_float(s[q][2 * e + 1])), c2, m2);
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              ls[e & 1] = fadd2(ls[e & 1], x);
+              s[q >> 1][(q & 1) * 8 + e] = pack_bf16x2(x.x, x.y);
+            }
+          const float2 l2 = fadd2(ls[0], ls[1]);
+          l_run = l_run * alpha + (l2.x + l2.y);
+        }
+        // PV of the group's last tile has read P and added to O
+        if (v > 0 && !mbar_wait_bounded(bar(kBarPvDone + w), (units - 1) & 1, a.wait_ns))
+          ok = false;
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (!idle) {
+          if (v > 0 && __any_sync(kFull, grow)) {
+#pragma unroll
+            for (int q = 0; q < kHeadDim / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * q, o);
+              tmem_wait_ld();
+              reg_after_wait(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tO + 16 * q, o);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_st16(tP + 16 * q, s[q]);
+          tmem_wait_st();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + w));
+      }
+      if (!ok) break;
+      kt0 += it.tiles();
+
+      // ---- epilogue
+      if (nu > 0 && !mbar_wait_bounded(bar(kBarPvDone + w), (units - 1) & 1, a.wait_ns)) ok = false;
+      if (!__all_sync(kFull, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      float o[kHeadDim];
+#pragma unroll
+      for (int q = 0; q < kHeadDim / 16; ++q) {
+        uint32_t x[16];
+        if (nu > 0 && !idle) {
+          tmem_ld16(tO + 16 * q, x);
+          tmem_wait_ld();
+          reg_after_wait(x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[16 * q + e] = __uint_as_float(x[e]);
+      }
+      tc_fence_before_sync();
+      bool writes = tok < it.nt;
+      if (one) {
+        // the second group hands its rows to the first through the item's Q
+        // buffer (every QK of the item has completed)
+        float4* xrow = reinterpret_cast<float4*>(smem + kOffQ + qb * 2 * kRowTileBytes) + row * 16;
+        float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + qb * 128 + row;
+        const uint32_t xbar = bar(kBarXch + qb);
+        const bool other = it.units_of(1) > 0;
+        if (w == 1) {
+          if (other && !idle) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              xrow[q ^ (row & 15)] =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            *xml = make_float2(m_ref, l_run);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && other) mbar_arrive(xbar);
+          writes = false;
+        } else {
+          if (other && !mbar_wait_bounded(xbar, (qb ? xch1 : xch0) & 1, a.wait_ns)) ok = false;
+          if (!__all_sync(kFull, ok)) {
+            ok = false;
+            break;
+          }
+          if (other && !idle) {
+            const float2 ml = *xml;
+            const float M = fmaxf(m_ref, ml.x);
+            const float w0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
+            const float w1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+            l_run = l_run * w0 + ml.y * w1;  // (a group that saw no token: zeros)
+            m_ref = M;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float4 x = xrow[q ^ (row & 15)];
+              o[4 * q] = o[4 * q] * w0 + x.x * w1;
+              o[4 * q + 1] = o[4 * q + 1] * w0 + x.y * w1;
+              o[4 * q + 2] = o[4 * q + 2] * w0 + x.z * w1;
+              o[4 * q + 3] = o[4 * q + 3] * w0 + x.w * w1;
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        if (other) {
+          if (qb) ++xch1; else ++xch0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQEmpty + qb));
+      }
+      const int bad_v = *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+      if (writes && bad_v != 0) {
+        // values that the relay replaced: rows that see them get them whole
+        for (int k = it.t0; k < it.t1; ++k) {
+          const int tile = it.tile(k);
+          if (!it.partial(tile, a)) continue;
+          for (int x = 0; x < kKvTokens; ++x) {
+            const int t = tile * kKvTokens + x;
+            if (t > pos || (static_cast<int64_t>(t) <= static_cast<int64_t>(pos) - a.window &&
+                            t >= a.sinks))
+              continue;
+            const int pid = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + t / kPageSize];
+            if (pid < 0 || pid >= a.num_pages) continue;
+            const uint16_t* vr =
+                a.pool + (((static_cast<int64_t>(pid) * 2 + 1) * kPageSize + t % kPageSize) *
+                              kNumKvHeads + it.g) * kHeadDim;
+#pragma unroll
+            for (int d = 0; d < kHeadDim; ++d) {
+              const float f = bf16_to_float(vr[d]);
+              if (!(fabsf(f) < INFINITY)) o[d] += f;
+            }
+          }
+        }
+      }
+      if (writes) {
+        const int64_t r =
+            static_cast<int64_t>(it.row0 + tok) * kNumQHeads + it.g * kGroup + (row & 3);
+        if (a.num_splits == 1) {
+          const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+          uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv),
+                                pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                                pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        } else {
+          const int64_t part = r * a.num_splits + it.split;
+          *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_run);
+          if (l_run != 0.f) {
+            float4* dst = reinterpret_cast<float4*>(a.part_acc + part * kHeadDim);
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+      }
     }
   }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  reinterpret_cast<uint32_t*>(a.out + qrow * kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
-  if (a.mass == nullptr) return;
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = inv;
-  }
+  if (!ok && lane == 0) record_error(a.dev_err, kErrTimeout);
+
+  // ---- every copy and MMA of this CTA has completed; the columns go back
+  tc_fence_before_sync();
   __syncthreads();
-  float* mass = a.mass + (static_cast<int64_t>(b) * kNumKvHeads + g) * a.mass_stride;
-  for (int i = threadIdx.x; i < n; i += 128) {
-    const int t = token(i);
-    const uint16_t* kr = key_row(t);
-    if (kr == nullptr) continue;
-    float w = 0.f;
-    for (int r = 0; r < kGroup; ++r)
-      if (s_l[r] != 0.f) w += fast_exp2(dot_row(s_q[r], kr) * a.scale_log2 - s_m[r]) * s_l[r];
-    mass[t] += w;
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Combine the ranges of each query row: one warp per row, lane l holding dims
+// 2l and 2l + 1; the ranges are added in order.
+constexpr int kMergeRows = 4;
+__global__ void __launch_bounds__(32 * kMergeRows) merge_chunk_kernel(const MaskedArgs a) {
+  allow_dependent_grids();
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  const int tok = static_cast<int>(row / kNumQHeads);
+  // rows of no sequence keep what they hold
+  int lo = 0, hi = a.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.token_offsets[mid] <= tok) lo = mid; else hi = mid;
+  }
+  const int o0 = a.token_offsets[lo], o1 = a.token_offsets[lo + 1];
+  if (o0 < 0 || o1 > a.num_tokens || tok < o0 || tok >= o1) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.num_splits;
+  const float2* acc = reinterpret_cast<const float2*>(a.part_acc) +
+                      row * a.num_splits * (kHeadDim / 2) + lane;
+  float M = -INFINITY;
+  for (int s = lane; s < a.num_splits; s += 32) {
+    const float2 x = __ldcg(ml + s);
+    if (x.y != 0.f) M = fmaxf(M, x.x);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+  float L = 0.f;
+  float2 O = make_float2(0.f, 0.f);
+  for (int s = 0; s < a.num_splits; ++s) {
+    const float2 x = __ldcg(ml + s);
+    if (x.y == 0.f) continue;  // saw no token; its accumulator was not written
+    const float wt = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M);  // (-inf: a NaN row)
+    const float2 v = __ldcg(acc + static_cast<int64_t>(s) * (kHeadDim / 2));
+    L = fmaf(x.y, wt, L);
+    O.x = fmaf(v.x, wt, O.x);
+    O.y = fmaf(v.y, wt, O.y);
+  }
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
+}
+
+cudaError_t configure(int device) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = 1ull << (device & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes fa;
+  cudaError_t err = cudaFuncGetAttributes(&fa, paged_chunk_kernel);
+  if (err != cudaSuccess) return err;
+  // the register split must stay within what the block starts with
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  err = cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return err;
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_attention(const MaskedArgs& args, cudaStream_t stream) {
-  return launch_pdl(masked_attention_kernel, dim3(args.num_tokens, kNumKvHeads), dim3(128), 0,
-                    stream, args);
+cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& page_map,
+                                   const MaskedArgs& args, int grid, cudaStream_t stream) {
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  if ((err = configure(device)) != cudaSuccess) return err;
+  err = launch_pdl(paged_chunk_kernel, dim3(grid), dim3(kThreads), kSmem, stream, q_map, page_map,
+                   args);
+  if (err != cudaSuccess || args.num_splits == 1) return err;
+  static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
+  return launch_pdl(merge_chunk_kernel, dim3(args.num_tokens * (kNumQHeads / kMergeRows)),
+                    dim3(32 * kMergeRows), 0, stream, args);
 }
 
 }  // namespace pkv

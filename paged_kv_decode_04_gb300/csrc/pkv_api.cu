@@ -8,6 +8,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "pkv.h"
@@ -875,6 +876,59 @@ bool bad_cache(int batch, int64_t num_pages, int max_blocks) {
          max_blocks > (INT32_MAX / kPageSize);
 }
 
+// TMA descriptor of the query rows of a chunk, [num_tokens][32 heads][64] bf16:
+// a box of 4 heads of 32 tokens, 128-byte swizzled.
+bool chunk_q_map(const void* q, int num_tokens, CUtensorMap* out) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim),
+                              static_cast<cuuint64_t>(kNumQHeads),
+                              static_cast<cuuint64_t>(num_tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim * 2),
+                                 static_cast<cuuint64_t>(kNumQHeads * kHeadDim * 2)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim),
+                             static_cast<cuuint32_t>(pkv::kGroup),
+                             static_cast<cuuint32_t>(pkv::kChunkTileTokens / 2)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Ranges and CTAs of a chunk call.  A tile holds up to 64 tokens of one
+// sequence, so there are at most min(tokens, batch + tokens / 64) of them.
+struct ChunkPlan {
+  int num_splits, grid;
+  size_t workspace;
+};
+
+bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks, int num_splits,
+                ChunkPlan* plan) {
+  const long long tiles =
+      std::min<long long>(num_tokens, batch + num_tokens / pkv::kChunkTileTokens);
+  const long long items = tiles * kNumKvHeads;
+  constexpr int kKvPages = pkv::kChunkKvTokens / kPageSize;
+  long long kv = (max_blocks + kKvPages - 1) / kKvPages;  // most kv tiles of an item
+  if (window > 0)
+    kv = std::min(kv, (static_cast<long long>(window) + pkv::kChunkTileTokens - 2) /
+                              pkv::kChunkKvTokens + 2 +
+                          (static_cast<long long>(sinks) + pkv::kChunkKvTokens - 1) /
+                              pkv::kChunkKvTokens);
+  long long s = num_splits;
+  const int sms = current_sm_count();
+  if (s == 0) {
+    if (sms <= 0) return false;
+    s = std::max(1LL, std::min(sms / std::max(items, 1LL), kv / 2));
+  }
+  s = std::min(s, std::max(kv, 1LL));
+  plan->num_splits = static_cast<int>(s);
+  plan->grid = static_cast<int>(std::min<long long>(sms > 0 ? sms : 1, items * s));
+  const size_t parts = static_cast<size_t>(num_tokens) * kNumQHeads * plan->num_splits;
+  plan->workspace = s > 1 ? parts * (kHeadDim + 2) * sizeof(float) : 0;
+  return true;
+}
+
 size_t q_row_bytes(int rows) {
   return static_cast<size_t>(rows) * kNumQHeads * kHeadDim * sizeof(pkv_bf16);
 }
@@ -917,7 +971,11 @@ PKV_API size_t pkv_chunk_workspace_bytes(int num_tokens, int batch, int num_q_he
   if (num_tokens < 0 || bad_cache(batch, 1, max_blocks) || window < 0 || sinks < 0 ||
       num_splits < 0 || !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
-  return 0;
+  if (num_tokens == 0 || batch == 0) return 0;
+  ChunkPlan plan;
+  if (!chunk_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
+    return static_cast<size_t>(-1);
+  return plan.workspace;
 }
 
 PKV_API int pkv_paged_chunk_attention(
@@ -938,6 +996,11 @@ PKV_API int pkv_paged_chunk_attention(
     return PKV_EALIGN;
   if (overlap(q, q_row_bytes(num_tokens), out, q_row_bytes(num_tokens))) return PKV_EINVAL;
   if (batch == 0 || num_tokens == 0) return PKV_OK;
+  ChunkPlan plan;
+  if (!chunk_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
+    return PKV_ECUDA;
+  if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
+    return PKV_EWORKSPACE;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.pool = pool;
@@ -952,10 +1015,19 @@ PKV_API int pkv_paged_chunk_attention(
   a.num_tokens = num_tokens;
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
-  a.num_splits = 1;
+  a.num_splits = plan.num_splits;
+  if (plan.workspace > 0) {
+    a.part_acc = static_cast<float*>(workspace);
+    a.part_ml = a.part_acc + static_cast<size_t>(num_tokens) * kNumQHeads * plan.num_splits * kHeadDim;
+  }
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  const cudaError_t err = pkv::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap q_map, page_map;
+  if (!chunk_q_map(q, num_tokens, &q_map) ||
+      !pool_tensor_map(pool, num_pages, &page_map, kPageSize))
+    return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_chunk_attention(q_map, page_map, a, plan.grid,
+                                                      reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -1000,7 +1072,7 @@ PKV_API int pkv_paged_window_attention(
   a.num_splits = 1;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  const cudaError_t err = pkv::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t err = pkv::launch_masked_attention(a, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -1047,7 +1119,7 @@ PKV_API int pkv_paged_scored_attention(
   a.num_splits = 1;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  const cudaError_t err = pkv::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t err = pkv::launch_masked_attention(a, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -276,7 +276,18 @@ struct MaskedArgs {
   unsigned long long wait_ns;
 };
 
-cudaError_t launch_chunk_attention(const MaskedArgs& args, cudaStream_t stream);
+// Tiles of the chunk kernel: new tokens (all 4 query heads of a kv head) and
+// cached tokens.
+constexpr int kChunkTileTokens = 64;
+constexpr int kChunkKvTokens = 128;
+
+// grid persistent CTAs (at most one per SM), then the merge of the ranges.
+// q_map: q as [num_tokens][32][64], boxes of 32 tokens and 4 heads, 128-byte
+// swizzled; page_map: boxes of one page's K (or V) rows of one head.
+cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& page_map,
+                                   const MaskedArgs& args, int grid, cudaStream_t stream);
+
+cudaError_t launch_masked_attention(const MaskedArgs& args, cudaStream_t stream);
 
 struct EvictArgs {
   const float* mass;

@@ -61,6 +61,17 @@ def test_chunk_window(window, sinks, splits):
     assert run_chunk([700, 90, 33], [140, 90, 2], window, sinks, splits=splits) == 0
 
 
+@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("lens,counts,window", [
+    # several items for each CTA: of one kv tile, of none, of both row tiles
+    ([100] * 70, [2] * 70, 0), ([1 + i for i in range(64)], [1] * 64, 0),
+    ([90 + 20 * i for i in range(40)], [1 + (i * 29) % 80 for i in range(40)], 0),
+    ([200 + 7 * (i % 5) for i in range(45)], [(0, 1, 33, 64, 70)[i % 5] for i in range(45)], 60),
+])
+def test_chunk_many_items(lens, counts, window, splits):
+    assert run_chunk(lens, counts, window, 3 if window else 0, splits=splits) == 0
+
+
 def test_chunk_scales():
     # flat weights, and weights that all fall on a few tokens
     run_chunk([400], [70], scale=2.0 ** -20)
