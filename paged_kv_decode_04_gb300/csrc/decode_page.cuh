@@ -86,27 +86,22 @@ __device__ __forceinline__ void load_q_frags(const uint16_t* qrow0, const LaneGe
   }
 }
 
-// Fold one page (tile at shared address kt, `valid` live tokens) into S.
-// c = softmax scale * log2(e).  Tokens at or past `valid` get no weight and
-// their V rows are zeroed in the tile first (they may hold any bytes).
-__device__ __forceinline__ void attend_page(uint32_t kt, int valid, const uint32_t (&qb)[4][2],
-                                            float c, const LaneGeom& G, int lane,
-                                            AttnState& S) {
-  const uint32_t vt = kt + kPageSize * kRowBytes;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};  // tokens fg | fg+8 x rows 2ft, 2ft+1
+// Scores of one page (tile at shared address kt): tokens fg | fg+8 x rows 2ft, 2ft+1.
+__device__ __forceinline__ void page_scores(uint32_t kt, const uint32_t (&qb)[4][2],
+                                            const LaneGeom& G, float (&s)[4]) {
+  s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     uint32_t ka[4];
     ldsm_x4(kt + G.k_row + (static_cast<uint32_t>((2 * kk + G.k_chunk) ^ G.lr) << 4), ka);
     mma_16816_bf16(s, ka, qb[kk][0], qb[kk][1]);
   }
-  if (valid < kPageSize) {
-    if (G.fg >= valid) s[0] = s[1] = -INFINITY;
-    if (G.fg + 8 >= valid) s[2] = s[3] = -INFINITY;
-    for (int idx = lane; idx < (kPageSize - valid) * 8; idx += 32)
-      sts128_zero(vt + (valid + (idx >> 3)) * kRowBytes + ((idx & 7) << 4));
-    __syncwarp();
-  }
+}
+
+// Fold a page's (masked) scores into S.  c = softmax scale * log2(e).
+__device__ __forceinline__ void fold_page(uint32_t kt, const float (&s)[4], float c,
+                                          const LaneGeom& G, AttnState& S) {
+  const uint32_t vt = kt + kPageSize * kRowBytes;
   float mx0 = fmaxf(s[0], s[2]) * c;
   float mx1 = fmaxf(s[1], s[3]) * c;
   const bool grow = mx0 > S.m_ref[0] + kRescaleLog2 || mx1 > S.m_ref[1] + kRescaleLog2;
@@ -167,6 +162,25 @@ __device__ __forceinline__ void attend_page(uint32_t kt, int valid, const uint32
     mma_16816_bf16(S.oacc[mt], va, pb[0][0], pb[0][1]);
     mma_16816_bf16(S.oacc[mt], va, pb[1][0], pb[1][1]);
   }
+}
+
+// Fold one page (tile at shared address kt, `valid` live tokens) into S.
+// Tokens at or past `valid` get no weight and their V rows are zeroed in the
+// tile first (they may hold any bytes).
+__device__ __forceinline__ void attend_page(uint32_t kt, int valid, const uint32_t (&qb)[4][2],
+                                            float c, const LaneGeom& G, int lane,
+                                            AttnState& S) {
+  const uint32_t vt = kt + kPageSize * kRowBytes;
+  float s[4];
+  page_scores(kt, qb, G, s);
+  if (valid < kPageSize) {
+    if (G.fg >= valid) s[0] = s[1] = -INFINITY;
+    if (G.fg + 8 >= valid) s[2] = s[3] = -INFINITY;
+    for (int idx = lane; idx < (kPageSize - valid) * 8; idx += 32)
+      sts128_zero(vt + (valid + (idx >> 3)) * kRowBytes + ((idx & 7) << 4));
+    __syncwarp();
+  }
+  fold_page(kt, s, c, G, S);
 }
 
 // Sum the lanes' shares of the row sums (lanes with the same ft).

@@ -929,6 +929,37 @@ bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks
   return true;
 }
 
+// Ranges of a one-token call whose sequences see at most `pages` pages, as
+// make_plan chooses them: about four CTAs per SM, eight pages a range or more.
+int one_token_splits(int batch, long long pages, int num_splits) {
+  if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, pages));
+  const int sms = current_sm_count();
+  if (sms <= 0) return -1;
+  const long long units = static_cast<long long>(batch) * kNumKvHeads;
+  return static_cast<int>(std::max(
+      1LL, std::min((4LL * sms + units - 1) / units, (pages + 7) / 8)));
+}
+
+long long window_pages(int max_blocks, int window, int sinks) {
+  return std::min<long long>(max_blocks, (static_cast<long long>(window) + kPageSize - 2) / kPageSize +
+                                             1 + (static_cast<long long>(sinks) + kPageSize - 1) /
+                                                     kPageSize);
+}
+
+size_t part_bytes(int batch, int splits) {
+  return splits > 1 ? static_cast<size_t>(batch) * kNumQHeads * splits * (kHeadDim + 2) *
+                          sizeof(float)
+                    : 0;
+}
+
+// Scores of a call that wants the weights, when shared memory does not hold
+// them: four floats for every token of the tables and kv head.
+size_t score_bytes(int batch, int max_blocks, int splits) {
+  if (splits == 1 && max_blocks <= pkv::kScoredSmemPages) return 0;
+  return static_cast<size_t>(batch) * kNumKvHeads * max_blocks * kPageSize * pkv::kGroup *
+         sizeof(float);
+}
+
 size_t q_row_bytes(int rows) {
   return static_cast<size_t>(rows) * kNumQHeads * kHeadDim * sizeof(pkv_bf16);
 }
@@ -1037,7 +1068,9 @@ PKV_API size_t pkv_window_workspace_bytes(int batch, int num_q_heads, int num_kv
   if (bad_cache(batch, 1, max_blocks) || window < 1 || sinks < 0 || num_splits < 0 ||
       !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
-  return 0;
+  if (batch == 0) return 0;
+  const int splits = one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits);
+  return splits < 1 ? static_cast<size_t>(-1) : part_bytes(batch, splits);
 }
 
 PKV_API int pkv_paged_window_attention(
@@ -1056,6 +1089,10 @@ PKV_API int pkv_paged_window_attention(
     return PKV_EALIGN;
   if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
+  const int splits = one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits);
+  if (splits < 1) return PKV_ECUDA;
+  const size_t need = part_bytes(batch, splits);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.pool = pool;
@@ -1069,10 +1106,17 @@ PKV_API int pkv_paged_window_attention(
   a.num_tokens = batch;
   a.window = window;
   a.sinks = sinks;
-  a.num_splits = 1;
+  a.num_splits = splits;
+  if (need > 0) {
+    a.part_acc = static_cast<float*>(workspace);
+    a.part_ml = a.part_acc + static_cast<size_t>(batch) * kNumQHeads * splits * kHeadDim;
+  }
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  const cudaError_t err = pkv::launch_masked_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap map;
+  if (!pool_tensor_map(pool, num_pages, &map)) return PKV_ECUDA;
+  const cudaError_t err =
+      pkv::launch_window_attention(map, a, 0, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -1081,7 +1125,10 @@ PKV_API size_t pkv_scored_workspace_bytes(int batch, int num_q_heads, int num_kv
   if (bad_cache(batch, 1, max_blocks) || num_splits < 0 ||
       !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
-  return 0;
+  if (batch == 0) return 0;
+  const int splits = one_token_splits(batch, max_blocks, num_splits);
+  return splits < 1 ? static_cast<size_t>(-1)
+                    : part_bytes(batch, splits) + score_bytes(batch, max_blocks, splits);
 }
 
 PKV_API int pkv_paged_scored_attention(
@@ -1102,6 +1149,11 @@ PKV_API int pkv_paged_scored_attention(
     return PKV_EALIGN;
   if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
+  const int splits = one_token_splits(batch, max_blocks, num_splits);
+  if (splits < 1) return PKV_ECUDA;
+  const size_t parts = part_bytes(batch, splits), keep = score_bytes(batch, max_blocks, splits);
+  if (parts + keep > 0 && (workspace == nullptr || workspace_bytes < parts + keep))
+    return PKV_EWORKSPACE;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.pool = pool;
@@ -1116,10 +1168,19 @@ PKV_API int pkv_paged_scored_attention(
   a.batch = batch;
   a.num_tokens = batch;
   a.window = INT32_MAX;
-  a.num_splits = 1;
+  a.num_splits = splits;
+  // the scores (16-byte aligned) first, then the partials
+  if (keep > 0) a.scores = static_cast<float*>(workspace);
+  if (parts > 0) {
+    a.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + keep);
+    a.part_ml = a.part_acc + static_cast<size_t>(batch) * kNumQHeads * splits * kHeadDim;
+  }
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  const cudaError_t err = pkv::launch_masked_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap map;
+  if (!pool_tensor_map(pool, num_pages, &map)) return PKV_ECUDA;
+  const cudaError_t err =
+      pkv::launch_window_attention(map, a, keep > 0 ? 0 : max_blocks, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

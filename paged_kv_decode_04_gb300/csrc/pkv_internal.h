@@ -287,7 +287,13 @@ constexpr int kChunkKvTokens = 128;
 cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& page_map,
                                    const MaskedArgs& args, int grid, cudaStream_t stream);
 
-cudaError_t launch_masked_attention(const MaskedArgs& args, cudaStream_t stream);
+// One-token attention under a window, or with the weights added to args.mass
+// (no window then), and the merge of the ranges when args.num_splits > 1.
+// Scores (weights wanted only) are kept in shared memory for score_pages
+// pages, at most kScoredSmemPages, when args.scores is null (one range then).
+constexpr int kScoredSmemPages = 256;
+cudaError_t launch_window_attention(const CUtensorMap& pool_map, const MaskedArgs& args,
+                                    int score_pages, cudaStream_t stream);
 
 struct EvictArgs {
   const float* mass;

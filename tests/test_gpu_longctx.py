@@ -269,7 +269,8 @@ def mass_reference(q, pool, bt, lens, mass):
 
 
 @pytest.mark.parametrize("splits", [0, 1, 2, 6])
-@pytest.mark.parametrize("lens", [[1], [16, 17, 0, 300], [700], [1, 1500, 64, 65, 31]])
+@pytest.mark.parametrize("lens", [[1], [16, 17, 0, 300], [700], [1, 1500, 64, 65, 31],
+                                  [4200, 40]])
 def test_scored(lens, splits):
     dev, b = cuda_or_skip(), binding()
     pool, bt = make_cache(lens, seed=31)
