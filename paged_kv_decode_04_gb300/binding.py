@@ -617,14 +617,31 @@ def decode_steps_planned(qs, k_news, v_news, pool, block_tables, seq_lens, plan,
 
 
 # ----------------------------------------------------------- long contexts --
+# One-token calls take a few microseconds on the device, so these checks stay
+# cheap: a tensor that is as it should be passes one expression, and _check
+# words the error of one that is not.
 
 INT32_MAX = 2 ** 31 - 1
+_SCALE = HEAD_DIM ** -0.5
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_POOL_ROW = (2, PAGE_SIZE, NUM_KV_HEADS, HEAD_DIM)
 
 
-def _cuda(t, name="pool"):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
-    return t.device
+def _is(t, name, dtype, ndim, index):
+    """t is a contiguous `dtype` tensor of `ndim` dims on CUDA device `index`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
+            and t.get_device() == index and t.is_contiguous()):
+        _check(t, name, dtype, ndim, torch.device("cuda", index))
+
+
+def _pool(pool):
+    """(device index, pages) of the pool."""
+    if not (isinstance(pool, torch.Tensor) and pool.dtype is _BF16 and pool.dim() == 5
+            and pool.shape[1:] == _POOL_ROW and pool.is_contiguous()):
+        _pool_pages(pool)
+    if not pool.is_cuda:
+        raise ValueError(f"pool must be on a CUDA device, not {pool.device}")
+    return pool.get_device(), pool.shape[0]
 
 
 def _count(v, name, least=0):
@@ -640,70 +657,74 @@ def _bytes(n, what):
     return n
 
 
-class _On:
-    """Launch on the tensors' device, whichever is current: `stream` (or that
-    device's current one), and the tensors a call made for itself kept alive
-    for the stream it used them on."""
-
-    def __init__(self, dev, stream):
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.dev = dev
-        self.other = stream is not None
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
-
-    def new(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if self.other:
-            t.record_stream(self.stream)
-        return t
-
-    def workspace(self, ws, need):
-        """(workspace, its bytes): the caller's, or one of `need` bytes."""
-        if ws is None:
-            if not need:
-                return None, 0
-            ws = self.new(need, torch.uint8)
-        elif ws.device != self.dev or not ws.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the pool's device")
-        return ws, ws.numel() * ws.element_size()
-
-    def call(self, what, *args):
-        f = getattr(_lib, what)
-        if torch.cuda.current_device() == self.dev.index:
-            rc = f(*args, self.ptr)
-        else:
-            with torch.cuda.device(self.dev):
-                rc = f(*args, self.ptr)
-        if rc != PKV_OK:
-            raise PkvError(rc, what)
-
-
-def _heads(t, name, dev, rows=None, heads=NUM_Q_HEADS):
-    """A bf16 tensor [rows][heads][64]; its number of rows."""
-    _check(t, name, torch.bfloat16, 3, dev)
-    if t.shape[1] != heads or t.shape[2] != HEAD_DIM or (rows is not None and t.shape[0] != rows):
+def _heads(t, name, index, rows, heads=NUM_Q_HEADS):
+    """t is a bf16 tensor [rows][heads][64] (rows None: any number of rows)."""
+    _is(t, name, _BF16, 3, index)
+    n, h, d = t.shape
+    if h != heads or d != HEAD_DIM or (rows is not None and n != rows):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}][{heads}]"
                          f"[{HEAD_DIM}], got {tuple(t.shape)}")
-    return t.shape[0]
+    return n
 
 
-def _tables(block_table, seq_lens, dev, name="block_table"):
-    """The batch and table width of int32 tables and lengths on `dev`."""
-    _check(block_table, name, torch.int32, 2, dev)
-    _check(seq_lens, "seq_lens", torch.int32, 1, dev)
-    if block_table.shape[0] != seq_lens.shape[0]:
+def _tables(block_table, seq_lens, index, name="block_table"):
+    """The batch and table width of int32 tables and lengths."""
+    _is(block_table, name, _I32, 2, index)
+    _is(seq_lens, "seq_lens", _I32, 1, index)
+    B, width = block_table.shape
+    if seq_lens.shape[0] != B:
         raise ValueError(f"{name} and seq_lens disagree on the batch")
-    return block_table.shape
+    return B, width
 
 
-def _err(dev_err, dev):
-    if dev_err is not None:
-        _check(dev_err, "dev_err", torch.int32, None, dev)
-        if dev_err.numel() < 1:
-            raise ValueError("dev_err must hold one int32")
-    return _ptr(dev_err)
+def _err(dev_err, index):
+    if dev_err is None:
+        return None
+    _check(dev_err, "dev_err", _I32, None, torch.device("cuda", index))
+    if dev_err.numel() < 1:
+        raise ValueError("dev_err must hold one int32")
+    return dev_err.data_ptr()
+
+
+def _new(shape, dtype, index, stream):
+    """A tensor the call makes for itself, kept for the stream it is used on."""
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _scratch(ws, need, index, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one of
+    need() bytes."""
+    if ws is None:
+        n = need()
+        if not n:
+            return None, None, 0
+        ws = _new(n, torch.uint8, index, stream)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the pool's device")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _on(index, stream):
+    """The raw stream to launch on: `stream`, or the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _launch(f, index, *args):
+    """Call entry point `f` with the tensors' device current."""
+    if torch._C._cuda_getDevice() == index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args)
+    if rc != PKV_OK:
+        raise PkvError(rc, f.__name__)
 
 
 def chunk_workspace_bytes(num_tokens: int, batch: int, max_blocks: int, num_splits: int = 0, *,
@@ -723,30 +744,32 @@ def paged_chunk_attention(q, token_offsets, pool, block_table, seq_lens, out=Non
     [32][64]) are the last tokens of sequence b's seq_lens[b] cached ones, each
     seeing the tokens up to itself -- with window > 0 the newest `window` of
     them and the first `sinks`.  Without `out` rows of no sequence are zero."""
-    num_pages = _pool_pages(pool)
-    dev = _cuda(pool)
-    rows = _heads(q, "q", dev)
-    _check(token_offsets, "token_offsets", torch.int32, 1, dev)
-    B, max_blocks = _tables(block_table, seq_lens, dev)
+    index, num_pages = _pool(pool)
+    rows = _heads(q, "q", index, None)
+    _is(token_offsets, "token_offsets", _I32, 1, index)
+    B, max_blocks = _tables(block_table, seq_lens, index)
     if token_offsets.shape[0] != B + 1:
         raise ValueError("token_offsets must have batch + 1 entries")
     window, sinks = _count(window, "window"), _count(sinks, "sinks")
     num_splits = _count(num_splits, "num_splits")
-    on = _On(dev, stream)
+    raw = _on(index, stream)
     if out is None:
-        with torch.cuda.stream(on.stream):
+        if stream is None:
             out = torch.zeros_like(q)
-    _heads(out, "out", dev, rows)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.zeros_like(q)
+    _heads(out, "out", index, rows)
     if rows == 0 or B == 0:
         return out
-    need = 0
-    if workspace is None:
-        need = chunk_workspace_bytes(rows, B, max_blocks, num_splits, window=window, sinks=sinks)
-    ws, ws_bytes = on.workspace(workspace, need)
-    on.call("pkv_paged_chunk_attention", _ptr(q), rows, _ptr(token_offsets), _ptr(pool), num_pages,
-            _ptr(block_table), max_blocks, _ptr(seq_lens), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
-            PAGE_SIZE, window, sinks, float(HEAD_DIM ** -0.5 if scale is None else scale),
-            _ptr(out), _ptr(ws), ws_bytes, num_splits, _err(dev_err, dev))
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: chunk_workspace_bytes(rows, B, max_blocks, num_splits, window=window,
+                                                 sinks=sinks), index, stream)
+    _launch(_lib.pkv_paged_chunk_attention, index, q.data_ptr(), rows, token_offsets.data_ptr(),
+            pool.data_ptr(), num_pages, block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B,
+            NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, window, sinks,
+            _SCALE if scale is None else float(scale), out.data_ptr(), ws_ptr, ws_bytes,
+            num_splits, _err(dev_err, index), raw)
     return out
 
 
@@ -764,26 +787,25 @@ def paged_window_attention(q, pool, block_table, seq_lens, window: int, out=None
                            num_splits: int = 0, dev_err=None, stream=None) -> torch.Tensor:
     """paged_decode_attention over each sequence's newest `window` tokens and
     its first `sinks`; pages that it does not see need not exist."""
-    num_pages = _pool_pages(pool)
-    dev = _cuda(pool)
-    B, max_blocks = _tables(block_table, seq_lens, dev)
-    _heads(q, "q", dev, B)
+    index, num_pages = _pool(pool)
+    B, max_blocks = _tables(block_table, seq_lens, index)
+    _heads(q, "q", index, B)
     window, sinks = _count(window, "window", 1), _count(sinks, "sinks")
     num_splits = _count(num_splits, "num_splits")
-    on = _On(dev, stream)
+    raw = _on(index, stream)
     if out is None:
-        out = on.new(q.shape, q.dtype)
-    _heads(out, "out", dev, B)
+        out = _new(q.shape, _BF16, index, stream)
+    else:
+        _heads(out, "out", index, B)
     if B == 0:
         return out
-    need = 0
-    if workspace is None:
-        need = window_workspace_bytes(B, max_blocks, window, num_splits, sinks=sinks)
-    ws, ws_bytes = on.workspace(workspace, need)
-    on.call("pkv_paged_window_attention", _ptr(q), _ptr(pool), num_pages, _ptr(block_table),
-            max_blocks, _ptr(seq_lens), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, window,
-            sinks, float(HEAD_DIM ** -0.5 if scale is None else scale), _ptr(out), _ptr(ws),
-            ws_bytes, num_splits, _err(dev_err, dev))
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: window_workspace_bytes(B, max_blocks, window, num_splits, sinks=sinks),
+        index, stream)
+    _launch(_lib.pkv_paged_window_attention, index, q.data_ptr(), pool.data_ptr(), num_pages,
+            block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B, NUM_Q_HEADS, NUM_KV_HEADS,
+            HEAD_DIM, PAGE_SIZE, window, sinks, _SCALE if scale is None else float(scale),
+            out.data_ptr(), ws_ptr, ws_bytes, num_splits, _err(dev_err, index), raw)
     return out
 
 
@@ -795,13 +817,14 @@ def scored_workspace_bytes(batch: int, max_blocks: int, num_splits: int = 0) -> 
         "pkv_scored_workspace_bytes")
 
 
-def _mass(t, name, dev, batch, least):
-    """A float32 tensor [batch][8][tokens] with at least `least` tokens; tokens."""
-    _check(t, name, torch.float32, 3, dev)
-    if t.shape[0] != batch or t.shape[1] != NUM_KV_HEADS or t.shape[2] < least:
+def _mass(t, name, index, batch, least):
+    """The tokens of a float32 tensor [batch][8][at least `least` tokens]."""
+    _is(t, name, _F32, 3, index)
+    n, h, tokens = t.shape
+    if n != batch or h != NUM_KV_HEADS or tokens < least:
         raise ValueError(f"{name} must be [{batch}][{NUM_KV_HEADS}][{least} or more], got "
                          f"{tuple(t.shape)}")
-    return t.shape[2]
+    return tokens
 
 
 def paged_scored_attention(q, pool, block_table, seq_lens, mass, out=None, *,
@@ -810,24 +833,24 @@ def paged_scored_attention(q, pool, block_table, seq_lens, mass, out=None, *,
     """paged_decode_attention that adds each cached token's attention weight,
     summed over the query heads of its kv head, to mass ([B][8][max_blocks * 16
     or more] float32)."""
-    num_pages = _pool_pages(pool)
-    dev = _cuda(pool)
-    B, max_blocks = _tables(block_table, seq_lens, dev)
-    _heads(q, "q", dev, B)
-    stride = _mass(mass, "mass", dev, B, max_blocks * PAGE_SIZE)
+    index, num_pages = _pool(pool)
+    B, max_blocks = _tables(block_table, seq_lens, index)
+    _heads(q, "q", index, B)
+    stride = _mass(mass, "mass", index, B, max_blocks * PAGE_SIZE)
     num_splits = _count(num_splits, "num_splits")
-    on = _On(dev, stream)
+    raw = _on(index, stream)
     if out is None:
-        out = on.new(q.shape, q.dtype)
-    _heads(out, "out", dev, B)
+        out = _new(q.shape, _BF16, index, stream)
+    else:
+        _heads(out, "out", index, B)
     if B == 0:
         return out
-    need = 0 if workspace is not None else scored_workspace_bytes(B, max_blocks, num_splits)
-    ws, ws_bytes = on.workspace(workspace, need)
-    on.call("pkv_paged_scored_attention", _ptr(q), _ptr(pool), num_pages, _ptr(block_table),
-            max_blocks, _ptr(seq_lens), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE,
-            float(HEAD_DIM ** -0.5 if scale is None else scale), _ptr(out), _ptr(mass), stride,
-            _ptr(ws), ws_bytes, num_splits, _err(dev_err, dev))
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: scored_workspace_bytes(B, max_blocks, num_splits), index, stream)
+    _launch(_lib.pkv_paged_scored_attention, index, q.data_ptr(), pool.data_ptr(), num_pages,
+            block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B, NUM_Q_HEADS, NUM_KV_HEADS,
+            HEAD_DIM, PAGE_SIZE, _SCALE if scale is None else float(scale), out.data_ptr(),
+            mass.data_ptr(), stride, ws_ptr, ws_bytes, num_splits, _err(dev_err, index), raw)
     return out
 
 
@@ -839,31 +862,35 @@ def kv_evict(mass, pool, block_table, seq_lens, dst_block_table, new_lens=None, 
     Their rows are packed into dst_block_table's pages (which no live entry of
     block_table names).  Returns (new_lens [B], new_mass [B][8][dst slots],
     kept [B][8][budget]: old places, -1 past the end)."""
-    num_pages = _pool_pages(pool)
-    dev = _cuda(pool)
-    B, max_blocks = _tables(block_table, seq_lens, dev)
-    _, dst_blocks = _tables(dst_block_table, seq_lens, dev, "dst_block_table")
-    stride = _mass(mass, "mass", dev, B, max_blocks * PAGE_SIZE)
+    index, num_pages = _pool(pool)
+    B, max_blocks = _tables(block_table, seq_lens, index)
+    _is(dst_block_table, "dst_block_table", _I32, 2, index)
+    dst_batch, dst_blocks = dst_block_table.shape
+    if dst_batch != B:
+        raise ValueError("dst_block_table and seq_lens disagree on the batch")
+    stride = _mass(mass, "mass", index, B, max_blocks * PAGE_SIZE)
     budget, sinks = _count(budget, "budget", 1), _count(sinks, "sinks")
     recent = _count(recent, "recent")
-    on = _On(dev, stream)
+    raw = _on(index, stream)
     if new_lens is None:
-        new_lens = on.new((B,), torch.int32)
+        new_lens = _new((B,), _I32, index, stream)
+    else:
+        _is(new_lens, "new_lens", _I32, 1, index)
     if new_mass is None:
-        new_mass = on.new((B, NUM_KV_HEADS, dst_blocks * PAGE_SIZE), torch.float32)
+        new_mass = _new((B, NUM_KV_HEADS, dst_blocks * PAGE_SIZE), _F32, index, stream)
     if kept is None:
-        kept = on.new((B, NUM_KV_HEADS, budget), torch.int32)
-    _check(new_lens, "new_lens", torch.int32, 1, dev)
-    _check(kept, "kept", torch.int32, 3, dev)
+        kept = _new((B, NUM_KV_HEADS, budget), _I32, index, stream)
+    else:
+        _is(kept, "kept", _I32, 3, index)
     if new_lens.shape[0] != B or tuple(kept.shape) != (B, NUM_KV_HEADS, budget):
         raise ValueError("new_lens must be [batch] and kept [batch][8][budget]")
-    new_stride = _mass(new_mass, "new_mass", dev, B, budget)
-    if B == 0:
-        return new_lens, new_mass, kept
-    on.call("pkv_kv_evict", _ptr(mass), stride, _ptr(pool), num_pages, _ptr(block_table),
-            max_blocks, _ptr(seq_lens), B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, budget, sinks,
-            recent, _ptr(dst_block_table), dst_blocks, _ptr(new_lens), _ptr(new_mass), new_stride,
-            _ptr(kept), _err(dev_err, dev))
+    new_stride = _mass(new_mass, "new_mass", index, B, budget)
+    if B > 0:
+        _launch(_lib.pkv_kv_evict, index, mass.data_ptr(), stride, pool.data_ptr(), num_pages,
+                block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B, NUM_KV_HEADS, HEAD_DIM,
+                PAGE_SIZE, budget, sinks, recent, dst_block_table.data_ptr(), dst_blocks,
+                new_lens.data_ptr(), new_mass.data_ptr(), new_stride, kept.data_ptr(),
+                _err(dev_err, index), raw)
     return new_lens, new_mass, kept
 
 
@@ -872,24 +899,23 @@ def kv_append_at(k_new, v_new, pool, block_table, positions, slots, *,
                  stream=None) -> None:
     """kv_append with the cache slot apart from the RoPE position: sequence b's
     token is rotated for positions[b] and stored as cached token slots[b]."""
-    num_pages = _pool_pages(pool)
-    dev = _cuda(pool)
-    _check(block_table, "block_table", torch.int32, 2, dev)
-    _check(positions, "positions", torch.int32, 1, dev)
-    _check(slots, "slots", torch.int32, 1, dev)
+    index, num_pages = _pool(pool)
+    _is(block_table, "block_table", _I32, 2, index)
+    _is(positions, "positions", _I32, 1, index)
+    _is(slots, "slots", _I32, 1, index)
     B, max_blocks = block_table.shape
-    _heads(k_new, "k_new", dev, B, NUM_KV_HEADS)
-    _heads(v_new, "v_new", dev, B, NUM_KV_HEADS)
+    _heads(k_new, "k_new", index, B, NUM_KV_HEADS)
+    _heads(v_new, "v_new", index, B, NUM_KV_HEADS)
     if positions.shape[0] != B or slots.shape[0] != B:
         raise ValueError("positions, slots and block_table disagree on the batch")
-    Hq = 0
+    q_ptr = out_ptr = None
     if q_in is not None or q_out is not None:
-        _heads(q_in, "q_in", dev, B)
-        _heads(q_out, "q_out", dev, B)
-        Hq = NUM_Q_HEADS
-    if B == 0:
-        return
-    _On(dev, stream).call(
-        "pkv_kv_append_at", _ptr(k_new), _ptr(v_new), _ptr(pool), num_pages, _ptr(block_table),
-        max_blocks, _ptr(positions), _ptr(slots), B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE,
-        float(rope_theta), _ptr(q_in), _ptr(q_out), Hq, _err(dev_err, dev))
+        _heads(q_in, "q_in", index, B)
+        _heads(q_out, "q_out", index, B)
+        q_ptr, out_ptr = q_in.data_ptr(), q_out.data_ptr()
+    raw = _on(index, stream)
+    if B > 0:
+        _launch(_lib.pkv_kv_append_at, index, k_new.data_ptr(), v_new.data_ptr(), pool.data_ptr(),
+                num_pages, block_table.data_ptr(), max_blocks, positions.data_ptr(),
+                slots.data_ptr(), B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, float(rope_theta), q_ptr,
+                out_ptr, 0 if q_ptr is None else NUM_Q_HEADS, _err(dev_err, index), raw)

@@ -85,7 +85,24 @@ __global__ void __launch_bounds__(kAppendThreads)
   const bool pos_ok = pos >= 0 && at >= 0 && at < max_blocks * kPageSize;
   const int32_t page =
       pos_ok ? block_table[static_cast<int64_t>(b) * max_blocks + at / kPageSize] : -1;
-  RopeCS cs = rope_cs(freqs, table_ok, pos, i);
+  // Past the table the FP64 sincos of a pair is taken once and shared by the
+  // 8 heads' threads (FP64 runs at a small fraction of FP32's rate here).
+  __shared__ double2 s_cs[kHalf];
+  RopeCS cs;
+  if (__syncthreads_or(!table_ok || pos < 0 || pos >= kRopeTablePositions)) {
+    if (h == 0) {
+      const RopeCS f = rope_cs(freqs, false, pos, i);
+      s_cs[i] = make_double2(f.c64, f.s64);
+    }
+    __syncthreads();
+    cs.c64 = s_cs[i].x;
+    cs.s64 = s_cs[i].y;
+    cs.c32 = static_cast<float>(cs.c64);
+    cs.s32 = static_cast<float>(cs.s64);
+    cs.have64 = true;
+  } else {
+    cs = rope_cs(freqs, true, pos, i);
+  }
 
   // Optional out-of-place query rotation: 32 heads x 32 pairs, 4 per thread.
   if (q_in != nullptr) {

@@ -1240,7 +1240,9 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
   a.budget = budget;
   a.sinks = sinks;
   a.recent = recent;
-  const cudaError_t err = pkv::launch_kv_evict(a, reinterpret_cast<cudaStream_t>(stream));
+  const int sms = current_sm_count();
+  if (sms <= 0) return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_kv_evict(a, sms, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -312,7 +312,7 @@ struct EvictArgs {
   int budget, sinks, recent;
 };
 
-cudaError_t launch_kv_evict(const EvictArgs& args, cudaStream_t stream);
+cudaError_t launch_kv_evict(const EvictArgs& args, int num_sms, cudaStream_t stream);
 
 // Largest logical page range one attention CTA handles.
 int max_pages_per_split();
