@@ -4,12 +4,14 @@
 // in token order into the pages of another block table.
 //
 // Selection: the weights map to 32-bit keys whose unsigned order is the
-// weights' order (NaN above +inf, -0 as +0); a radix descent of four 8-bit
-// digits over a shared-memory histogram finds the key of the last token kept
-// and how many tokens of that key are kept, lowest index first.  Counts only:
-// the result does not depend on the order of the atomics.  Then every warp
-// takes a contiguous part of the tokens, counts its kept ones with ballots,
-// and writes them at the sum of the counts before it.
+// weights' order (NaN above +inf, -0 as +0); a radix descent of three digits
+// (11, 11 and 10 bits: the first one holds the exponent and two bits more, so
+// that weights of like size spread over many counters) over a shared-memory
+// histogram finds the key of the last token kept and how many tokens of that
+// key are kept, lowest index first.  Counts only: the result does not depend
+// on the order of the atomics.  Then every warp takes a contiguous part of the
+// tokens, counts its kept ones with ballots, and writes them at the sum of the
+// counts before it.
 //
 // The copy is bound by memory (512 bytes a kept token and head, as 128-byte
 // rows) and wants many CTAs, the selection reads 4 bytes a token and is short:
@@ -30,12 +32,14 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 // Tables up to this many tokens keep the keys in shared memory; longer ones
 // read the weights again (from L2) in every pass.
-constexpr int kSmemTokens = 12288;
+constexpr int kSmemTokens = 8192;
 constexpr int kCopyRows = 4;  // tokens whose rows a group of 8 lanes has in flight
 
 // Order-preserving key of a weight.
@@ -46,10 +50,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 template <bool kSmemKeys>
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_evict_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ int s_hist[256];
-  __shared__ int s_eq[kWarps], s_keep[kWarps];
+  __shared__ __align__(16) int s_hist[kBins];
+  __shared__ int s_above[kWarps], s_eq[kWarps], s_gt[kWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -90,44 +94,53 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
     auto key = [&](int t) { return kSmemKeys ? s_keys[t] : weight_key(mass[t]); };
     uint32_t prefix = 0;
     int need = a.budget - a.sinks - a.recent;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) s_hist[tid] = 0;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      const uint32_t high = pass == 0 ? 0u : (pass == 1 ? ~0u << 21 : ~0u << 10);
+      constexpr int kMine = kBins / kThreads;  // consecutive counters of one thread
+      int4* mine = reinterpret_cast<int4*>(s_hist + tid * kMine);
+#pragma unroll
+      for (int e = 0; e < kMine / 4; ++e) mine[e] = make_int4(0, 0, 0, 0);
       __syncthreads();
-      const uint32_t high = shift == 24 ? 0u : ~0u << (shift + 8);
       for (int t = lo + tid; t < hi; t += kThreads) {
         const uint32_t k = key(t);
-        if ((k & high) != prefix) continue;
-        // one atomic per digit and warp: the first digit of weights of like
-        // size is the same for nearly all
-        const int d = (k >> shift) & 255;
-        const unsigned same = __match_any_sync(__activemask(), d);
-        if (lane == __ffs(same) - 1) atomicAdd(&s_hist[d], __popc(same));
+        if ((k & high) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
       }
       __syncthreads();
-      if (warp == 0) {
-        // lane l holds digits 8 l .. 8 l + 7; from the highest digit down, the
-        // first one whose running count reaches need
-        int h[8], sum = 0;
+      // from the highest digit down, the first whose running count reaches need
+      int h[kMine], sum = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += h[e] = s_hist[8 * lane + e];
-        int above = sum;  // tokens of this lane's digits and higher ones
+      for (int e = 0; e < kMine / 4; ++e) {
+        const int4 v = mine[e];
+        h[4 * e] = v.x;
+        h[4 * e + 1] = v.y;
+        h[4 * e + 2] = v.z;
+        h[4 * e + 3] = v.w;
+      }
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-          const int y = __shfl_down_sync(kFull, above, x);
-          if (lane + x < 32) above += y;
-        }
-        const unsigned reach = __ballot_sync(kFull, above >= need);
-        if (lane == 31 - __clz(reach)) {
-          int left = need - (above - sum), d = 7;
+      for (int e = 0; e < kMine; ++e) sum += h[e];
+      int above = sum;  // tokens of this thread's digits and the warp's higher ones
 #pragma unroll
-          for (int e = 7; e > 0; --e)
-            if (d == e && h[e] < left) {
-              left -= h[e];
-              d = e - 1;
-            }
-          s_prefix = prefix | (static_cast<uint32_t>(8 * lane + d) << shift);
-          s_need = left;
-        }
+      for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_down_sync(kFull, above, x);
+        if (lane + x < 32) above += y;
+      }
+      if (lane == 0) s_above[warp] = above;
+      __syncthreads();
+      for (int x = warp + 1; x < kWarps; ++x) above += s_above[x];
+      // one thread's digits hold the need-th token (need 0: the highest digit)
+      if ((above >= need && above - sum < need) || (need == 0 && tid == kThreads - 1)) {
+        int left = need - (above - sum), d = kMine - 1;
+#pragma unroll
+        for (int e = kMine - 1; e > 0; --e)
+          if (d == e && h[e] < left) {
+            left -= h[e];
+            d = e - 1;
+          }
+        s_prefix = prefix | (static_cast<uint32_t>(tid * kMine + d) << shift);
+        s_need = left;
       }
       __syncthreads();
       prefix = s_prefix;
@@ -136,41 +149,41 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
     // kept: keys above prefix, and the first `need` tokens of that key
     const int span = ((L + kWarps - 1) / kWarps + 31) & ~31;
     const int t0 = min(warp * span, L), t1 = min(t0 + span, L);
-    int eq = 0;
-    for (int t = t0 + lane; t < t1; t += 32) eq += t >= lo && t < hi && key(t) == prefix;
+    int eq = 0, gt = 0;
+    for (int t = t0 + lane; t < t1; t += 32) {
+      const bool contest = t >= lo && t < hi;
+      const uint32_t k = contest ? key(t) : 0xFFFFFFFFu;
+      eq += contest && k == prefix;
+      gt += !contest || k > prefix;
+    }
     eq = __reduce_add_sync(kFull, eq);
-    if (lane == 0) s_eq[warp] = eq;
+    gt = __reduce_add_sync(kFull, gt);
+    if (lane == 0) {
+      s_eq[warp] = eq;
+      s_gt[warp] = gt;
+    }
     __syncthreads();
-    int eq_base = 0;
-    for (int x = 0; x < warp; ++x) eq_base += s_eq[x];
-    // at(t): how many are kept in [t & ~31, t) of the warp's 32 tokens
-    auto step = [&](int tt, int& eqs, bool& keep) {
-      const int t = tt + lane;
-      const bool in = t < t1, contest = in && t >= lo && t < hi;
-      const uint32_t k = contest ? key(t) : 0u;
-      const bool e = contest && k == prefix;
-      const unsigned eb = __ballot_sync(kFull, e);
-      keep = in && (!contest || k > prefix ||
-                    (e && eqs + __popc(eb & ((1u << lane) - 1u)) < need));
-      eqs += __popc(eb);
-      return __ballot_sync(kFull, keep);
-    };
-    int cnt = 0, eqs = eq_base;
-    bool keep;
-    for (int tt = t0; tt < t1; tt += 32) cnt += __popc(step(tt, eqs, keep));
-    if (lane == 0) s_keep[warp] = cnt;
-    __syncthreads();
-    int at = 0;
-    for (int x = 0; x < warp; ++x) at += s_keep[x];
-    eqs = eq_base;
-    if (at < c1 && at + cnt > c0) {
-      for (int tt = t0; tt < t1; tt += 32) {
-        const unsigned kb = step(tt, eqs, keep);
+    int at = 0, eqs = 0;  // kept, and of key prefix, before this warp's tokens
+    for (int x = 0; x < warp; ++x) {
+      at += s_gt[x] + min(max(need - eqs, 0), s_eq[x]);
+      eqs += s_eq[x];
+    }
+    if (at < c1) {
+      for (int tt = t0; tt < t1 && at < c1; tt += 32) {
+        const int t = tt + lane;
+        const bool in = t < t1, contest = in && t >= lo && t < hi;
+        const uint32_t k = contest ? key(t) : 0u;
+        const unsigned eb = __ballot_sync(kFull, contest && k == prefix);
+        const int rank = eqs + __popc(eb & ((1u << lane) - 1u));
+        const bool keep =
+            in && (!contest || k > prefix || (k == prefix && rank < need));
+        const unsigned kb = __ballot_sync(kFull, keep);
         const int i = at + __popc(kb & ((1u << lane) - 1u));
         if (keep && i >= c0 && i < c1) {
-          kept[i] = tt + lane;
-          new_mass[i] = mass[tt + lane];
+          kept[i] = t;
+          new_mass[i] = mass[t];
         }
+        eqs += __popc(eb);
         at += __popc(kb);
       }
     }
@@ -181,35 +194,55 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
   const int group = tid >> 3, chunk = tid & 7;
   constexpr int kGroups = kThreads / 8;
   const int64_t slot_row = kNumKvHeads * kHeadDim;  // elements between slots
-  uint4 x[kCopyRows][2];
+  const int32_t* src_table = a.block_table + static_cast<int64_t>(b) * a.max_blocks;
+  const int32_t* dst_table = a.dst_block_table + static_cast<int64_t>(b) * a.dst_max_blocks;
+  // addresses of the next kCopyRows tokens of this group, fetched while the
+  // rows of the last ones are on their way
+  const uint16_t* src[kCopyRows];
   uint16_t* dst[kCopyRows];
-  for (int i0 = c0 + group; i0 < c1; i0 += kGroups * kCopyRows) {
+  auto addresses = [&](int i0) {
+    int t[kCopyRows], sp[kCopyRows], dp[kCopyRows];
+#pragma unroll
+    for (int e = 0; e < kCopyRows; ++e) {
+      const int i = i0 + e * kGroups;
+      t[e] = i < c1 ? __ldcg(kept + i) : -1;
+      dp[e] = i < c1 ? dst_table[i / kPageSize] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < kCopyRows; ++e) sp[e] = t[e] >= 0 ? src_table[t[e] / kPageSize] : 0;
 #pragma unroll
     for (int e = 0; e < kCopyRows; ++e) {
       const int i = i0 + e * kGroups;
       dst[e] = nullptr;
-      if (i >= c1) continue;
-      const int t = __ldcg(kept + i);
-      const int32_t sp = a.block_table[static_cast<int64_t>(b) * a.max_blocks + t / kPageSize];
-      const int32_t dp =
-          a.dst_block_table[static_cast<int64_t>(b) * a.dst_max_blocks + i / kPageSize];
-      if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages) {
+      if (t[e] < 0) continue;
+      if (sp[e] < 0 || sp[e] >= a.num_pages || dp[e] < 0 || dp[e] >= a.num_pages) {
         if (chunk == 0) record_error(a.dev_err, kErrPage);
         continue;
       }
-      const uint16_t* src = a.pool +
-                            (static_cast<int64_t>(sp) * 2 * kPageSize + t % kPageSize) * slot_row +
-                            g * kHeadDim + chunk * 8;
-      dst[e] = a.pool + (static_cast<int64_t>(dp) * 2 * kPageSize + i % kPageSize) * slot_row +
+      src[e] = a.pool +
+               (static_cast<int64_t>(sp[e]) * 2 * kPageSize + t[e] % kPageSize) * slot_row +
                g * kHeadDim + chunk * 8;
-      x[e][0] = *reinterpret_cast<const uint4*>(src);
-      x[e][1] = *reinterpret_cast<const uint4*>(src + kPageSize * slot_row);
+      dst[e] = a.pool + (static_cast<int64_t>(dp[e]) * 2 * kPageSize + i % kPageSize) * slot_row +
+               g * kHeadDim + chunk * 8;
     }
+  };
+  addresses(c0 + group);
+  for (int i0 = c0 + group; i0 < c1; i0 += kGroups * kCopyRows) {
+    uint4 x[kCopyRows][2];
+    uint16_t* to[kCopyRows];
 #pragma unroll
     for (int e = 0; e < kCopyRows; ++e) {
-      if (dst[e] == nullptr) continue;
-      *reinterpret_cast<uint4*>(dst[e]) = x[e][0];
-      *reinterpret_cast<uint4*>(dst[e] + kPageSize * slot_row) = x[e][1];
+      to[e] = dst[e];
+      if (to[e] == nullptr) continue;
+      x[e][0] = __ldcs(reinterpret_cast<const uint4*>(src[e]));
+      x[e][1] = __ldcs(reinterpret_cast<const uint4*>(src[e] + kPageSize * slot_row));
+    }
+    addresses(i0 + kGroups * kCopyRows);
+#pragma unroll
+    for (int e = 0; e < kCopyRows; ++e) {
+      if (to[e] == nullptr) continue;
+      *reinterpret_cast<uint4*>(to[e]) = x[e][0];
+      *reinterpret_cast<uint4*>(to[e] + kPageSize * slot_row) = x[e][1];
     }
   }
 }
@@ -217,10 +250,10 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& args, int num_sms, cudaStream_t stream) {
-  // CTAs for about two waves of two per SM, at least 64 kept rows each
+  // one wave of CTAs, at least 64 kept rows each
   const long long units = static_cast<long long>(args.batch) * kNumKvHeads;
   const long long parts = std::max(
-      1LL, std::min((4LL * num_sms + units - 1) / units, (args.budget + 63LL) / 64));
+      1LL, std::min(static_cast<long long>(kCtasPerSm) * num_sms / units, (args.budget + 63LL) / 64));
   const dim3 grid(static_cast<unsigned>(kNumKvHeads * parts), args.batch);
   const int64_t tokens = static_cast<int64_t>(args.max_blocks) * kPageSize;
   return tokens <= kSmemTokens
