@@ -124,8 +124,8 @@ struct Item {
   int t0, t1;   // range [t0, t1) of the tile's list: sinks, then window
   int lo;       // first token of any row's window
   int first_w;  // softmax group of the first unit
-  int bad;      // a live non-finite V value was replaced (the relay's answer)
-  int pad[3];
+  // in shared memory also: whether a live non-finite V value was replaced (the
+  // relay's answer), units(), tiles() and halves() (what the MMA warp reads)
 
   __device__ __forceinline__ bool halves() const { return nt <= kHalfTokens; }
   __device__ __forceinline__ int tiles() const { return t1 - t0; }
@@ -144,7 +144,7 @@ struct Item {
     return from <= (gone < last ? gone : last);
   }
 };
-static_assert(sizeof(Item) == kItemWords * 4, "item words");
+static_assert(sizeof(Item) + 16 == kItemWords * 4, "item words");
 
 __device__ __forceinline__ Item read_item(const int* w) {
   Item it;
@@ -153,7 +153,6 @@ __device__ __forceinline__ Item read_item(const int* w) {
   it.b = a.x; it.row0 = a.y; it.nt = a.z; it.pos0 = a.w;
   it.g = b.x; it.split = b.y; it.ns = b.z; it.w0 = b.w;
   it.t0 = c.x; it.t1 = c.y; it.lo = c.z; it.first_w = c.w;
-  it.bad = it.pad[0] = it.pad[1] = it.pad[2] = 0;
   return it;
 }
 
@@ -165,6 +164,41 @@ __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* ma
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
       "{%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// The MMAs with sw128_desc's descriptors given by their low words: the high
+// word is the same for every tile, and a step inside a tile adds its offset
+// in units of 16 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((1024u >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
@@ -338,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           w[0] = make_int4(it.b, it.row0, it.nt, it.pos0);
           w[1] = make_int4(it.g, it.split, it.ns, it.w0);
           w[2] = make_int4(it.t0, it.t1, it.lo, it.first_w);
-          w[3] = make_int4(0, 0, 0, 0);
+          w[3] = make_int4(0, it.b < 0 ? 0 : it.units(), it.tiles(), it.halves() ? 1 : 0);
           mbar_arrive(bar(kBarItemFull + slot));
         }
         __syncwarp();
@@ -490,62 +524,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         }
         if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
       }
-    } else if (lane == 0) {
+    } else {
       // ------------------------------------------------------------ MMAs
+      // The whole warp walks the units, so that what the instructions take is
+      // uniform over the warp; one elected lane issues them.
       struct Cursor {
-        int i = -1;   // item
-        int u = 0, U = 0;
-        int kt = 0;   // kv tiles before the item
+        int i = -1;          // item
+        int u = 0, U = 0;    // unit of it, its units
+        int kt = 0, n = 0;   // kv tiles before the item, its own
+        bool one = false;    // one row tile
         bool end = false;
-        Item it;
-      } cq, cp;       // QK(u) and PV(u)
+      } cq, cp;              // QK(u) and PV(u)
       int n_s = 0, n_p = 0;  // units whose QK / PV was issued; unit n is group (n & 1)'s n / 2th
+      const bool issuer = elect_one();
+      auto wait = [&](int which, int parity) {
+        return __all_sync(kFull, mbar_wait_bounded(bar(which), parity & 1, a.wait_ns)) != 0;
+      };
       // to the next unit; false: a wait ran out
       auto next = [&](Cursor& c, bool release) {
         if (c.end || c.u < c.U) return true;
-        if (c.i >= 0) {
-          if (release) mbar_arrive(bar(kBarItemEmpty + c.i % kItems));
-          c.kt += c.it.tiles();
-        }
+        if (c.i >= 0 && release && issuer) mbar_arrive(bar(kBarItemEmpty + c.i % kItems));
+        c.kt += c.n;
         ++c.i;
         const int slot = c.i % kItems;
-        if (!mbar_wait_bounded(bar(kBarItemFull + slot), (c.i / kItems) & 1, a.wait_ns))
-          return false;
-        c.it = read_item(s_items + slot * kItemWords);
+        if (!wait(kBarItemFull + slot, c.i / kItems)) return false;
+        const int4 x = *reinterpret_cast<const int4*>(s_items + slot * kItemWords + 12);
         c.u = 0;
-        c.end = c.it.b < 0;
-        c.U = c.end ? 0 : c.it.units();
+        c.end = x.y == 0;
+        c.U = x.y;
+        c.n = x.z;
+        c.one = x.w != 0;
         return true;
       };
       auto issue_qk = [&]() {
-        const bool one = cq.it.halves();
         const int w = n_s & 1;
-        const int kt = cq.kt + (one ? cq.u : cq.u >> 1), st = kt % kStages, qb = cq.i & 1;
-        if (cq.u == 0 && !mbar_wait_bounded(bar(kBarQFull + qb), (cq.i >> 1) & 1, a.wait_ns))
-          return false;
-        if (!mbar_wait_bounded(bar(kBarKFull + st), (kt / kStages) & 1, a.wait_ns)) return false;
-        if (n_s >= 2 &&
-            !mbar_wait_bounded(bar(kBarSFree + w), ((n_s >> 1) - 1) & 1, a.wait_ns))
-          return false;
+        const int kt = cq.kt + (cq.one ? cq.u : cq.u >> 1), st = kt % kStages, qb = cq.i & 1;
+        if (cq.u == 0 && !wait(kBarQFull + qb, cq.i >> 1)) return false;
+        if ((cq.one || !(cq.u & 1)) && !wait(kBarKFull + st, kt / kStages)) return false;
+        if (n_s >= 2 && !wait(kBarSFree + w, (n_s >> 1) - 1)) return false;
         tc_fence_after_sync();
-        const uint32_t q = sb + kOffQ + (2 * qb + (one ? 0 : w)) * kRowTileBytes;
-        const uint32_t kr = sb + kOffK + st * kRowTileBytes;
+        const uint32_t q = desc_lo(sb + kOffQ + (2 * qb + (cq.one ? 0 : w)) * kRowTileBytes);
+        const uint32_t kr = desc_lo(sb + kOffK + st * kRowTileBytes);
+        if (issuer) {
 #pragma unroll
-        for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          tc_mma_bf16(tmem + 128 * w, sw128_desc(q + 32 * kk), sw128_desc(kr + 32 * kk), kIdescQK,
-                      kk > 0 ? 1u : 0u);
-        tc_commit(bar(kBarSFull + w));
-        if (one || (cq.u & 1)) tc_commit(bar(kBarKEmpty + st));
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
+          tc_commit(bar(kBarSFull + w));
+          if (cq.one || (cq.u & 1)) tc_commit(bar(kBarKEmpty + st));
+        }
         ++n_s;
         ++cq.u;
         return true;
       };
       while (ok) {
-        if (!next(cp, true)) {
-          ok = false;
-          break;
-        }
-        if (cp.end) break;
+        ok = next(cp, true);
+        if (!ok || cp.end) break;
         // QK up to two units ahead, but no further than the next item: the
         // one after it takes the Q buffer that this item still holds
         while (ok && n_s < n_p + 3) {
@@ -554,29 +587,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           ok = issue_qk();
         }
         if (!ok) break;
-        const bool one = cp.it.halves();
         const int w = n_p & 1;
-        const int kt = cp.kt + (one ? cp.u : cp.u >> 1), st = kt % kStages;
-        if (!mbar_wait_bounded(bar(kBarVReady + st), (kt / kStages) & 1, a.wait_ns) ||
-            !mbar_wait_bounded(bar(kBarPFull + w), (n_p >> 1) & 1, a.wait_ns)) {
+        const int kt = cp.kt + (cp.one ? cp.u : cp.u >> 1), st = kt % kStages;
+        if ((cp.one || !(cp.u & 1)) && !wait(kBarVReady + st, kt / kStages)) ok = false;
+        if (!ok || !wait(kBarPFull + w, n_p >> 1)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t vr = sb + kOffV + st * kRowTileBytes;
+        const uint32_t vr = desc_lo(sb + kOffV + st * kRowTileBytes);
         const bool first = cp.u < 2;  // the group's first unit of this item
+        if (issuer) {
 #pragma unroll
-        for (int p = 0; p < kKvPages; ++p)
-          tc_mma_bf16_ta(tmem + kTmemO + kHeadDim * w, tmem + kTmemP + 64 * w + 8 * p,
-                         sw128_desc(vr + p * kPageBytes), kIdescPV, (p > 0 || !first) ? 1u : 0u);
-        tc_commit(bar(kBarPvDone + w));
-        if (one || (cp.u & 1)) tc_commit(bar(kBarVEmpty + st));
+          for (int p = 0; p < kKvPages; ++p)
+            mma_ts(tmem + kTmemO + kHeadDim * w, tmem + kTmemP + 64 * w + 8 * p,
+                   vr + p * (kPageBytes >> 4), kIdescPV, p > 0 || !first);
+          tc_commit(bar(kBarPvDone + w));
+          if (cp.one || (cp.u & 1)) tc_commit(bar(kBarVEmpty + st));
+        }
         ++n_p;
         ++cp.u;
       }
       // no MMA in flight past here
-      tc_commit(bar(kBarFin));
-      if (!mbar_wait_bounded(bar(kBarFin), 0)) record_error(a.dev_err, kErrTimeout);
+      if (issuer) {
+        tc_commit(bar(kBarFin));
+        if (!mbar_wait_bounded(bar(kBarFin), 0)) record_error(a.dev_err, kErrTimeout);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
