@@ -24,17 +24,21 @@
 // kv head, range of the kv tiles) and handing over through mbarriers, so the
 // next item's loads and first products run under the last one's epilogue:
 //   0-3, 4-7  softmax of S_0 and S_1, rescaling of O, epilogue
-//   8         issues the MMAs: QK(u + 2) before PV(u) where it can, u counting
-//             the (row tile, kv tile) units, which alternate between S_0, S_1
+//   8, 11     issue QK and PV.  A unit is a (row tile, kv tile) pair; units
+//             alternate between S_0 and S_1, across items too
 //   9         loads: Q by one box per row tile, K and V by 2 KiB boxes of one
 //             page and head; pages outside every row's sight (or with a bad
 //             id) are read at a page index past the pool, i.e. as zeros
-//   10        finds the CTA's next item from the offsets and lengths; items
-//             without any kv tile it answers itself
-//   11        relays "V has landed", and in the tiles that some row sees in
-//             part only it first replaces non-finite V values by zero (a
-//             masked weight is zero, but 0 x NaN is not); rows that do see
-//             such a value get it added in the epilogue
+//   10        finds the CTA's next items from the offsets and lengths (items
+//             without any kv tile it answers itself), and relays "V has
+//             landed": in the tiles that some row sees in part only it first
+//             replaces non-finite V values by zero (a masked weight is zero,
+//             but 0 x NaN is not); rows that do see such a value get it added
+//             in the epilogue
+// What a warp executes per unit besides its math is kept short: one thread's
+// instruction stream issues the MMAs, and with the look-ahead of both products
+// in one warp that stream, not the tensor cores, set the pace (2 x 4096 tokens
+// over 8192: 680 us; with two short streams TIME us).
 // P enters the product with V as bf16 (8 significant bits, an error of at
 // most 2^-8 of sum p |v|, averaged over the tokens, below the output's own
 // bf16 rounding); the row sums take the unrounded FP32 values.  The reference
@@ -62,9 +66,10 @@ constexpr int kRow = kHeadDim * 2;            // 128 B
 constexpr int kRowTileBytes = 128 * kRow;     // 16 KiB: a row tile of Q, a kv tile of K or V
 constexpr int kPageBytes = kPageSize * kRow;  // 2 KiB: one head's K (or V) rows of a page
 constexpr int kStages = 4;                    // kv tiles in flight
-constexpr int kItems = 4;                     // items published ahead
+constexpr int kItems = 8;                     // slots for published items
+constexpr int kAhead = 3;                     // items published before the relay starts one
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10, kFixWarp = 11;
+constexpr int kQkWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11 issues PV
 constexpr int kThreads = 32 * 12;
 // Registers: 168 x 384 threads at launch = 64512 = 256 x 216 + 128 x 72.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -81,8 +86,8 @@ constexpr uint32_t kIdescPV = tc_idesc_bf16(128, kHeadDim, true);
 constexpr int kOffQ = 0;                               // [2 items][2 row tiles]
 constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
 constexpr int kOffV = kOffK + kStages * kRowTileBytes;
-constexpr int kOffMl = kOffV + kStages * kRowTileBytes;  // [2][128] (m, l) handed between groups
-constexpr int kOffItems = kOffMl + 2 * 128 * 8;
+constexpr int kOffMl = kOffV + kStages * kRowTileBytes;  // [128] (m, l) handed between groups
+constexpr int kOffItems = kOffMl + 128 * 8;
 constexpr int kItemWords = 16;
 constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
 enum {
@@ -99,8 +104,10 @@ enum {
   kBarPvDone = kBarPFull + 2,
   kBarItemFull = kBarPvDone + 2,
   kBarItemEmpty = kBarItemFull + kItems,
-  kBarXch = kBarItemEmpty + kItems,
-  kBarFin = kBarXch + 2,
+  kBarXFull = kBarItemEmpty + kItems,
+  kBarXFree,
+  kBarQkFin,
+  kBarPvFin,
   kNumBars
 };
 // Bad-page bits of the last kv tiles, then the TMEM address.  Twice the stages:
@@ -202,6 +209,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       : "memory");
 }
 
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   unsigned long long ra, rb, rd;
   asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
@@ -210,6 +223,14 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   float2 d;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
   return d;
+}
+
+// Wait of a whole warp for phase `phase` (mod 2) of a barrier; false for all
+// lanes when the limit ran out.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, int phase, unsigned long long limit_ns) {
+  const uint32_t parity = static_cast<uint32_t>(phase) & 1u;
+  if (__builtin_expect(__all_sync(kFull, mbar_test_wait(bar, parity)), 1)) return true;
+  return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit_ns)) != 0;
 }
 
 // Bits [lo, hi) of 32 (bounds outside are clamped).
@@ -230,6 +251,33 @@ __device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
          ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
+// Add to dims [d0, d0 + 16) of a row at position pos the non-finite V values
+// that the relay replaced by zero and the row sees (rare: plain loads).
+__device__ __forceinline__ void add_nonfinite(const MaskedArgs& a, const Item& it, int pos, int d0,
+                                              float (&o)[16]) {
+#pragma unroll 1
+  for (int k = it.t0; k < it.t1; ++k) {
+    const int tile = it.tile(k);
+    if (!it.partial(tile, a)) continue;
+#pragma unroll 1
+    for (int x = 0; x < kKvTokens; ++x) {
+      const int t = tile * kKvTokens + x;
+      if (t > pos || (static_cast<int64_t>(t) <= static_cast<int64_t>(pos) - a.window &&
+                      t >= a.sinks))
+        continue;
+      const int pid = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + t / kPageSize];
+      if (pid < 0 || pid >= a.num_pages) continue;
+      const uint16_t* vr = a.pool + (((static_cast<int64_t>(pid) * 2 + 1) * kPageSize +
+                                      t % kPageSize) * kNumKvHeads + it.g) * kHeadDim + d0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float f = bf16_to_float(vr[e]);
+        if (!(fabsf(f) < INFINITY)) o[e] += f;
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap page_map,
     const MaskedArgs a) {
@@ -238,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
   auto bar = [&](int i) { return sb + kOffBars + 8u * i; };
+  auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
   int* s_items = reinterpret_cast<int*>(smem + kOffItems);
   uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta], then the TMEM address
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -249,15 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     tma_prefetch_desc(&page_map);
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
-      if (i >= kBarQEmpty && i < kBarSFull) n = kSoftmaxWarps;
       if (i >= kBarSFree && i < kBarPvDone) n = 4;               // s_free, p_full
-      if (i >= kBarItemEmpty && i < kBarXch) n = kSoftmaxWarps + 3;
-      if (i >= kBarXch && i < kBarFin) n = 4;
+      if (i >= kBarItemEmpty && i < kBarXFull) n = kSoftmaxWarps + 4;
+      if (i == kBarXFull || i == kBarXFree) n = 4;
       mbar_init(bar(i), n);
     }
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     __syncwarp();
     tmem_alloc(sb + kOffMeta + 4 * kMeta, kTmemCols);
     tmem_relinquish_alloc_permit();
@@ -270,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   allow_dependent_grids();
 
   bool ok = true;
-  if (warp >= kMmaWarp) {
+  if (warp >= kQkWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSchedWarp) {
-      // ------------------------------------------------------ scheduler
+      // --------------------------------------------- scheduler, V's relay
       // Items in order (tile, range, head); the tiles of a sequence from its
       // last (under a causal mask the longest) to its first.  Every second
       // round runs through the CTAs backwards, so that long items pair with
@@ -282,8 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       int b0 = -32, before = 0, sum = 0;      // 32 sequences from b0: tiles before them, theirs
       int cnt = 0, incl = 0, o0 = 0, o1 = 0;  // this lane's sequence
       int parity = 0, out_i = 0;              // units so far mod 2, items published
+      int round = 0, kt = 0;
       bool more = true;
-      for (int round = 0; more; ++round) {
+      // publish the next item (or the end); false: a wait ran out
+      auto publish = [&]() {
+       for (;; ++round) {
         const int64_t idx = static_cast<int64_t>(round) * gridDim.x +
                             ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         const int64_t tile64 = idx / per_tile;
@@ -360,13 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           parity = (parity + it.units()) & 1;
         }
         const int slot = out_i % kItems;
-        if (out_i >= kItems &&
-            !mbar_wait_bounded(bar(kBarItemEmpty + slot), (out_i / kItems - 1) & 1, a.wait_ns))
-          ok = false;
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
+        if (out_i >= kItems && !wait(kBarItemEmpty + slot, out_i / kItems - 1)) return false;
         if (lane == 0) {
           int4* w = reinterpret_cast<int4*>(s_items + slot * kItemWords);
           w[0] = make_int4(it.b, it.row0, it.nt, it.pos0);
@@ -377,6 +422,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         }
         __syncwarp();
         ++out_i;
+        ++round;
+        return true;
+       }
+      };
+      for (int i = 0; ok; ++i) {
+        while (ok && more && out_i <= i + kAhead) ok = publish();
+        const int slot = i % kItems;
+        if (!ok || !wait(kBarItemFull + slot, i / kItems)) {
+          ok = false;
+          break;
+        }
+        const Item it = read_item(s_items + slot * kItemWords);
+        if (it.b < 0) break;
+        bool live_bad = false;
+        for (int k = it.t0; k < it.t1; ++k, ++kt) {
+          const int st = kt % kStages, tile = it.tile(k);
+          if (!wait(kBarVFull + st, kt / kStages)) {
+            ok = false;
+            break;
+          }
+          if (it.partial(tile, a)) {
+            // 4 rows of 8 16-byte chunks at a time (the swizzle permutes
+            // chunks within a row only)
+            const uint32_t v0 = sb + kOffV + st * kRowTileBytes + lane * 16;
+            const int row_end = it.end() - tile * kKvTokens;  // rows that some query sees
+#pragma unroll 1
+            for (int r = 0; r < kKvTokens; r += 16) {
+              uint4 x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = lds128(v0 + (r + 4 * e) * kRow);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t m0 = nonfinite_halves(x[e].x), m1 = nonfinite_halves(x[e].y),
+                               m2 = nonfinite_halves(x[e].z), m3 = nonfinite_halves(x[e].w);
+                if ((m0 | m1 | m2 | m3) != 0u) {
+                  if (r + 4 * e + (lane >> 3) < row_end) live_bad = true;
+                  sts128(v0 + (r + 4 * e) * kRow, x[e].x & ~m0, x[e].y & ~m1, x[e].z & ~m2,
+                         x[e].w & ~m3);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          const bool any = __any_sync(kFull, live_bad);
+          if (lane == 0) {
+            if (k == it.t1 - 1) s_items[slot * kItemWords + 12] = any ? 1 : 0;
+            mbar_arrive(bar(kBarVReady + st));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
       }
     } else if (warp == kLoadWarp) {
       // ----------------------------------------------------------- loads
@@ -384,8 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       int k_issued = 0, v_issued = 0;
       for (int i = 0; ok; ++i) {
         const int slot = i % kItems;
-        if (!mbar_wait_bounded(bar(kBarItemFull + slot), (i / kItems) & 1, a.wait_ns)) ok = false;
-        if (!__all_sync(kFull, ok)) {
+        if (!wait(kBarItemFull + slot, i / kItems)) {
           ok = false;
           break;
         }
@@ -394,9 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         if (it.b < 0) break;
         if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
         const int qb = qn & 1;
-        if (qn >= 2 && !mbar_wait_bounded(bar(kBarQEmpty + qb), (qn / 2 - 1) & 1, a.wait_ns))
-          ok = false;
-        if (!__all_sync(kFull, ok)) {
+        if (qn >= 2 && !wait(kBarQEmpty + qb, qn / 2 - 1)) {
           ok = false;
           break;
         }
@@ -433,10 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           const int pid = next;
           next = page_of(k + 1);
           const int st = kt % kStages;
-          const uint32_t par = (kt / kStages - 1) & 1;
           const unsigned bad = __ballot_sync(kFull, pid == -1) & 0xFFu;
-          if (kt >= kStages && !mbar_wait_bounded(bar(kBarKEmpty + st), par, a.wait_ns)) ok = false;
-          if (!__all_sync(kFull, ok)) {
+          if (kt >= kStages && !wait(kBarKEmpty + st, kt / kStages - 1)) {
             ok = false;
             break;
           }
@@ -450,8 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             tma_load_box(sb + kOffK + st * kRowTileBytes + lane * kPageBytes, &page_map,
                          bar(kBarKFull + st), it.g * kHeadDim, 0, z);
           k_issued = kt + 1;
-          if (kt >= kStages && !mbar_wait_bounded(bar(kBarVEmpty + st), par, a.wait_ns)) ok = false;
-          if (!__all_sync(kFull, ok)) {
+          if (kt >= kStages && !wait(kBarVEmpty + st, kt / kStages - 1)) {
             ok = false;
             break;
           }
@@ -473,145 +563,81 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       for (int j = max(0, qn - 2); j < qn; ++j)
         if (!mbar_wait_bounded(bar(kBarQFull + (j & 1)), (j >> 1) & 1) && lane == 0)
           record_error(a.dev_err, kErrTimeout);
-    } else if (warp == kFixWarp) {
-      // ---------------------------------------------------- V's relay
-      int kt = 0;
-      for (int i = 0; ok; ++i) {
-        const int slot = i % kItems;
-        if (!mbar_wait_bounded(bar(kBarItemFull + slot), (i / kItems) & 1, a.wait_ns)) ok = false;
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
-        const Item it = read_item(s_items + slot * kItemWords);
-        if (it.b < 0) break;
-        bool live_bad = false;
-        for (int k = it.t0; k < it.t1; ++k, ++kt) {
-          const int st = kt % kStages, tile = it.tile(k);
-          if (!mbar_wait_bounded(bar(kBarVFull + st), (kt / kStages) & 1, a.wait_ns)) ok = false;
-          if (!__all_sync(kFull, ok)) {
-            ok = false;
-            break;
-          }
-          if (it.partial(tile, a)) {
-            // 4 rows of 8 16-byte chunks at a time (the swizzle permutes
-            // chunks within a row only)
-            const uint32_t v0 = sb + kOffV + st * kRowTileBytes + lane * 16;
-            const int row_end = it.end() - tile * kKvTokens;  // rows that some query sees
-            for (int r = 0; r < kKvTokens; r += 16) {
-              uint4 x[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = lds128(v0 + (r + 4 * e) * kRow);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t m0 = nonfinite_halves(x[e].x), m1 = nonfinite_halves(x[e].y),
-                               m2 = nonfinite_halves(x[e].z), m3 = nonfinite_halves(x[e].w);
-                if ((m0 | m1 | m2 | m3) != 0u) {
-                  if (r + 4 * e + (lane >> 3) < row_end) live_bad = true;
-                  sts128(v0 + (r + 4 * e) * kRow, x[e].x & ~m0, x[e].y & ~m1, x[e].z & ~m2,
-                         x[e].w & ~m3);
-                }
-              }
-            }
-            fence_proxy_async_smem();
-          }
-          const bool any = __any_sync(kFull, live_bad);
-          if (lane == 0) {
-            if (k == it.t1 - 1) s_items[slot * kItemWords + 12] = any ? 1 : 0;
-            mbar_arrive(bar(kBarVReady + st));
-          }
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
-      }
-    } else {
-      // ------------------------------------------------------------ MMAs
-      // The whole warp walks the units, so that what the instructions take is
-      // uniform over the warp; one elected lane issues them.
-      struct Cursor {
-        int i = -1;          // item
-        int u = 0, U = 0;    // unit of it, its units
-        int kt = 0, n = 0;   // kv tiles before the item, its own
-        bool one = false;    // one row tile
-        bool end = false;
-      } cq, cp;              // QK(u) and PV(u)
-      int n_s = 0, n_p = 0;  // units whose QK / PV was issued; unit n is group (n & 1)'s n / 2th
+    } else if (warp == kQkWarp) {
+      // -------------------------------------------------------- S = Q K^T
+      // (the whole warp walks the units, so that what the instructions take
+      // is uniform over it; one elected lane issues them)
       const bool issuer = elect_one();
-      auto wait = [&](int which, int parity) {
-        return __all_sync(kFull, mbar_wait_bounded(bar(which), parity & 1, a.wait_ns)) != 0;
-      };
-      // to the next unit; false: a wait ran out
-      auto next = [&](Cursor& c, bool release) {
-        if (c.end || c.u < c.U) return true;
-        if (c.i >= 0 && release && issuer) mbar_arrive(bar(kBarItemEmpty + c.i % kItems));
-        c.kt += c.n;
-        ++c.i;
-        const int slot = c.i % kItems;
-        if (!wait(kBarItemFull + slot, c.i / kItems)) return false;
+      int n = 0, kt = 0;  // units and kv tiles before; unit n is group (n & 1)'s n / 2th
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kItems, qb = i & 1;
+        if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
         const int4 x = *reinterpret_cast<const int4*>(s_items + slot * kItemWords + 12);
-        c.u = 0;
-        c.end = x.y == 0;
-        c.U = x.y;
-        c.n = x.z;
-        c.one = x.w != 0;
-        return true;
-      };
-      auto issue_qk = [&]() {
-        const int w = n_s & 1;
-        const int kt = cq.kt + (cq.one ? cq.u : cq.u >> 1), st = kt % kStages, qb = cq.i & 1;
-        if (cq.u == 0 && !wait(kBarQFull + qb, cq.i >> 1)) return false;
-        if ((cq.one || !(cq.u & 1)) && !wait(kBarKFull + st, kt / kStages)) return false;
-        if (n_s >= 2 && !wait(kBarSFree + w, (n_s >> 1) - 1)) return false;
-        tc_fence_after_sync();
-        const uint32_t q = desc_lo(sb + kOffQ + (2 * qb + (cq.one ? 0 : w)) * kRowTileBytes);
-        const uint32_t kr = desc_lo(sb + kOffK + st * kRowTileBytes);
-        if (issuer) {
+        const int U = x.y;
+        const bool one = x.w != 0;
+        if (U == 0) break;
+        if (!(ok = wait(kBarQFull + qb, i >> 1))) break;
+        const uint32_t q0 = desc_lo(sb + kOffQ + 2 * qb * kRowTileBytes);
+        for (int u = 0; u < U; ++u, ++n) {
+          const int w = n & 1, st = kt % kStages;
+          const bool last = one || (u & 1);  // use of this kv tile
+          if (!(ok = wait(kBarKFull + st, kt / kStages))) break;
+          if (n >= 2 && !(ok = wait(kBarSFree + w, (n >> 1) - 1))) break;
+          tc_fence_after_sync();
+          const uint32_t q = q0 + (one ? 0 : w) * (kRowTileBytes >> 4);
+          const uint32_t kr = desc_lo(sb + kOffK) + st * (kRowTileBytes >> 4);
+          if (issuer) {
 #pragma unroll
-          for (int kk = 0; kk < kHeadDim / 16; ++kk)
-            mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
-          tc_commit(bar(kBarSFull + w));
-          if (cq.one || (cq.u & 1)) tc_commit(bar(kBarKEmpty + st));
+            for (int kk = 0; kk < kHeadDim / 16; ++kk)
+              mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
+            tc_commit(bar(kBarSFull + w));
+            if (last) tc_commit(bar(kBarKEmpty + st));
+            if (u == U - 1) tc_commit(bar(kBarQEmpty + qb));
+          }
+          if (last) ++kt;
         }
-        ++n_s;
-        ++cq.u;
-        return true;
-      };
-      while (ok) {
-        ok = next(cp, true);
-        if (!ok || cp.end) break;
-        // QK up to two units ahead, but no further than the next item: the
-        // one after it takes the Q buffer that this item still holds
-        while (ok && n_s < n_p + 3) {
-          ok = next(cq, false);
-          if (!ok || cq.end || cq.i > cp.i + 1) break;
-          ok = issue_qk();
-        }
-        if (!ok) break;
-        const int w = n_p & 1;
-        const int kt = cp.kt + (cp.one ? cp.u : cp.u >> 1), st = kt % kStages;
-        if ((cp.one || !(cp.u & 1)) && !wait(kBarVReady + st, kt / kStages)) ok = false;
-        if (!ok || !wait(kBarPFull + w, n_p >> 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t vr = desc_lo(sb + kOffV + st * kRowTileBytes);
-        const bool first = cp.u < 2;  // the group's first unit of this item
-        if (issuer) {
-#pragma unroll
-          for (int p = 0; p < kKvPages; ++p)
-            mma_ts(tmem + kTmemO + kHeadDim * w, tmem + kTmemP + 64 * w + 8 * p,
-                   vr + p * (kPageBytes >> 4), kIdescPV, p > 0 || !first);
-          tc_commit(bar(kBarPvDone + w));
-          if (cp.one || (cp.u & 1)) tc_commit(bar(kBarVEmpty + st));
-        }
-        ++n_p;
-        ++cp.u;
+        if (issuer) mbar_arrive(bar(kBarItemEmpty + slot));
       }
       // no MMA in flight past here
       if (issuer) {
-        tc_commit(bar(kBarFin));
-        if (!mbar_wait_bounded(bar(kBarFin), 0)) record_error(a.dev_err, kErrTimeout);
+        tc_commit(bar(kBarQkFin));
+        if (!mbar_wait_bounded(bar(kBarQkFin), 0)) record_error(a.dev_err, kErrTimeout);
+      }
+      __syncwarp();
+    } else {
+      // --------------------------------------------------------- O += P V
+      const bool issuer = elect_one();
+      int n = 0, kt = 0;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kItems;
+        if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
+        const int4 x = *reinterpret_cast<const int4*>(s_items + slot * kItemWords + 12);
+        const int U = x.y;
+        const bool one = x.w != 0;
+        if (U == 0) break;
+        for (int u = 0; u < U; ++u, ++n) {
+          const int w = n & 1, st = kt % kStages;
+          const bool last = one || (u & 1);
+          if (!(ok = wait(kBarVReady + st, kt / kStages))) break;
+          if (!(ok = wait(kBarPFull + w, n >> 1))) break;
+          tc_fence_after_sync();
+          const uint32_t vr = desc_lo(sb + kOffV) + st * (kRowTileBytes >> 4);
+          if (issuer) {
+            const uint32_t d = tmem + kTmemO + kHeadDim * w, pa = tmem + kTmemP + 64 * w;
+            mma_ts(d, pa, vr, kIdescPV, u >= 2);  // a group's first unit of the item starts O
+#pragma unroll
+            for (int p = 1; p < kKvPages; ++p)
+              mma_ts(d, pa + 8 * p, vr + p * (kPageBytes >> 4), kIdescPV, true);
+            tc_commit(bar(kBarPvDone + w));
+            if (last) tc_commit(bar(kBarVEmpty + st));
+          }
+          if (last) ++kt;
+        }
+        if (issuer) mbar_arrive(bar(kBarItemEmpty + slot));
+      }
+      if (issuer) {
+        tc_commit(bar(kBarPvFin));
+        if (!mbar_wait_bounded(bar(kBarPvFin), 0)) record_error(a.dev_err, kErrTimeout);
       }
       __syncwarp();
     }
@@ -625,24 +651,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
                    tO = t_lane + kTmemO + kHeadDim * w;
     const float c = a.scale_log2;
     // this group's units, kv tiles of the items before, rows handed over
-    int units = 0, kt0 = 0, xch0 = 0, xch1 = 0;
+    int units = 0, kt0 = 0, xn = 0;
+    bool held = false;  // the second group's O has not been read by the first yet
     for (int i = 0; ok; ++i) {
       const int slot = i % kItems;
-      if (!mbar_wait_bounded(bar(kBarItemFull + slot), (i / kItems) & 1, a.wait_ns)) ok = false;
-      if (!__all_sync(kFull, ok)) {
-        ok = false;
-        break;
-      }
+      if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
       const Item it = read_item(s_items + slot * kItemWords);
       if (it.b < 0) break;
-      const int qb = i & 1;
-      // Q has landed, so both groups are done with its buffer's last item, and
-      // this one's arrivals count for this item also when it has no unit of it
-      if (!mbar_wait_bounded(bar(kBarQFull + qb), (i >> 1) & 1, a.wait_ns)) ok = false;
-      if (!__all_sync(kFull, ok)) {
-        ok = false;
-        break;
-      }
       const bool one = it.halves();
       const int tok = (row >> 2) + (one ? 0 : kHalfTokens * w);
       const int pos = it.pos0 + tok;
@@ -653,11 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         // place in the item's list of kv tiles
         const int kk = one ? 2 * v + (w == it.first_w ? 0 : 1) : v;
         const int tile = it.tile(it.t0 + kk);
-        if (!mbar_wait_bounded(bar(kBarSFull + w), units & 1, a.wait_ns)) ok = false;
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
+        if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
         uint32_t s[8][16];
         float alpha = 1.f;
@@ -673,10 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         // (written before the loads that QK waited for)
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(s_meta + (kt0 + kk) % kMeta);
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kBarSFree + w));
-          if (v == nu - 1 && !one) mbar_arrive(bar(kBarQEmpty + qb));
-        }
+        if (lane == 0) mbar_arrive(bar(kBarSFree + w));
         if (!idle) {
           if (bad != 0u || it.partial(tile, a)) {
             const int64_t base = static_cast<int64_t>(tile) * kKvTokens;
@@ -699,37 +707,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
 #pragma unroll
           for (int q = 0; q < 8; ++q)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[q][e]));
+            for (int e = 0; e < 16; e += 2)
+              mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(s[q][e]),
+                                       __uint_as_float(s[q][e + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           grow = top > m_ref + kRescale;
           if (grow) {
             alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
             m_ref = top;
           }
-          // (a row that has seen no token yet: every weight 2^(-inf) = 0)
-          const float m = m_ref == -INFINITY ? 0.f : m_ref;
-          const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
-          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float2 x = ffma2(make_float2(__uint_as_float(s[q][2 * e]),
-                                           __uint_as_float(s[q][2 * e + 1])), c2, m2);
-              x.x = fast_exp2(x.x);
-              x.y = fast_exp2(x.y);
-              ls[e & 1] = fadd2(ls[e & 1], x);
-              s[q >> 1][(q & 1) * 8 + e] = pack_bf16x2(x.x, x.y);
-            }
-          const float2 l2 = fadd2(ls[0], ls[1]);
-          l_run = l_run * alpha + (l2.x + l2.y);
         }
-        // PV of the group's last tile has read P and added to O
-        if (v > 0 && !mbar_wait_bounded(bar(kBarPvDone + w), (units - 1) & 1, a.wait_ns))
-          ok = false;
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
+        // PV of the group's last tile has read P and added to O; the item's
+        // first may start O once the first group has read what it holds
+        if (v > 0) {
+          if (!(ok = wait(kBarPvDone + w, units - 1))) break;
+        } else if (held) {
+          if (!(ok = wait(kBarXFree, xn - 1))) break;
+          held = false;
         }
         tc_fence_after_sync();
         if (!idle) {
@@ -745,8 +739,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
               tmem_st16(tO + 16 * q, o);
             }
           }
+          // (a row that has seen no token yet: every weight 2^(-inf) = 0)
+          const float m = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // 32 columns at a time: the scores of a step enter it at its start,
+          // so that the steps before do not hold its results in registers
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_st16(tP + 16 * q, s[q]);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pw[16];
+            reg_after_wait(s[2 * q]);
+            reg_after_wait(s[2 * q + 1]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t* sp = &s[2 * q + (e >> 3)][2 * (e & 7)];
+              float2 x = ffma2(make_float2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), c2, m2);
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              ls[e & 1] = fadd2(ls[e & 1], x);
+              pw[e] = pack_bf16x2(x.x, x.y);
+            }
+            tmem_st16(tP + 16 * q, pw);
+          }
+          const float2 l2 = fadd2(ls[0], ls[1]);
+          l_run = l_run * alpha + (l2.x + l2.y);
           tmem_wait_st();
         }
         tc_fence_before_sync();
@@ -757,127 +773,90 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       kt0 += it.tiles();
 
       // ---- epilogue
-      if (nu > 0 && !mbar_wait_bounded(bar(kBarPvDone + w), (units - 1) & 1, a.wait_ns)) ok = false;
-      if (!__all_sync(kFull, ok)) {
-        ok = false;
-        break;
-      }
+      if (nu > 0 && !(ok = wait(kBarPvDone + w, units - 1))) break;
       tc_fence_after_sync();
-      float o[kHeadDim];
-#pragma unroll
-      for (int q = 0; q < kHeadDim / 16; ++q) {
-        uint32_t x[16];
-        if (nu > 0 && !idle) {
-          tmem_ld16(tO + 16 * q, x);
-          tmem_wait_ld();
-          reg_after_wait(x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[16 * q + e] = __uint_as_float(x[e]);
-      }
-      tc_fence_before_sync();
       bool writes = tok < it.nt;
-      if (one) {
-        // the second group hands its rows to the first through the item's Q
-        // buffer (every QK of the item has completed)
-        float4* xrow = reinterpret_cast<float4*>(smem + kOffQ + qb * 2 * kRowTileBytes) + row * 16;
-        float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + qb * 128 + row;
-        const uint32_t xbar = bar(kBarXch + qb);
-        const bool other = it.units_of(1) > 0;
-        if (w == 1) {
-          if (other && !idle) {
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              xrow[q ^ (row & 15)] =
-                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-            *xml = make_float2(m_ref, l_run);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && other) mbar_arrive(xbar);
-          writes = false;
-        } else {
-          if (other && !mbar_wait_bounded(xbar, (qb ? xch1 : xch0) & 1, a.wait_ns)) ok = false;
-          if (!__all_sync(kFull, ok)) {
-            ok = false;
-            break;
-          }
-          if (other && !idle) {
-            const float2 ml = *xml;
-            const float M = fmaxf(m_ref, ml.x);
-            const float w0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
-            const float w1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
-            l_run = l_run * w0 + ml.y * w1;  // (a group that saw no token: zeros)
-            m_ref = M;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const float4 x = xrow[q ^ (row & 15)];
-              o[4 * q] = o[4 * q] * w0 + x.x * w1;
-              o[4 * q + 1] = o[4 * q + 1] * w0 + x.y * w1;
-              o[4 * q + 2] = o[4 * q + 2] * w0 + x.z * w1;
-              o[4 * q + 3] = o[4 * q + 3] * w0 + x.w * w1;
-            }
-          }
-          fence_proxy_async_smem();
-        }
+      const bool other = one && it.units_of(1) > 0;  // both groups saw these rows
+      float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + row;
+      if (one && w == 1) {
+        // the first group takes this one's rows from TMEM (the same lanes)
+        writes = false;
         if (other) {
-          if (qb) ++xch1; else ++xch0;
+          *xml = make_float2(m_ref, l_run);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarXFull));
+          held = true;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQEmpty + qb));
       }
+      float w0 = 1.f, w1 = 0.f;
+      if (other && w == 0) {
+        if (!(ok = wait(kBarXFull, xn))) break;
+        tc_fence_after_sync();
+        const float2 ml = *xml;
+        const float M = fmaxf(m_ref, ml.x);
+        // (a group whose tiles the row did not see: zeros)
+        w0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
+        w1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+        l_run = l_run * w0 + ml.y * w1;
+        m_ref = M;
+      }
+      // (written before the last kv tile's V was handed to its PV, which this
+      // row's group, or the other one, has waited for)
       const int bad_v = *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
-      if (writes && bad_v != 0) {
-        // values that the relay replaced: rows that see them get them whole
-        for (int k = it.t0; k < it.t1; ++k) {
-          const int tile = it.tile(k);
-          if (!it.partial(tile, a)) continue;
-          for (int x = 0; x < kKvTokens; ++x) {
-            const int t = tile * kKvTokens + x;
-            if (t > pos || (static_cast<int64_t>(t) <= static_cast<int64_t>(pos) - a.window &&
-                            t >= a.sinks))
-              continue;
-            const int pid = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + t / kPageSize];
-            if (pid < 0 || pid >= a.num_pages) continue;
-            const uint16_t* vr =
-                a.pool + (((static_cast<int64_t>(pid) * 2 + 1) * kPageSize + t % kPageSize) *
-                              kNumKvHeads + it.g) * kHeadDim;
-#pragma unroll
-            for (int d = 0; d < kHeadDim; ++d) {
-              const float f = bf16_to_float(vr[d]);
-              if (!(fabsf(f) < INFINITY)) o[d] += f;
-            }
-          }
-        }
-      }
-      if (writes) {
+      if (!(one && w == 1) && !idle) {
         const int64_t r =
             static_cast<int64_t>(it.row0 + tok) * kNumQHeads + it.g * kGroup + (row & 3);
-        if (a.num_splits == 1) {
-          const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
-          uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv),
-                                pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
-        } else {
-          const int64_t part = r * a.num_splits + it.split;
+        const int64_t part = r * a.num_splits + it.split;
+        const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+        if (a.num_splits > 1 && writes)
           *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_run);
-          if (l_run != 0.f) {
-            float4* dst = reinterpret_cast<float4*>(a.part_acc + part * kHeadDim);
+#pragma unroll 1
+        for (int q = 0; q < kHeadDim / 16; ++q) {
+          uint32_t x[16];
+          float o[16];
+          if (nu > 0) {
+            tmem_ld16(tO + 16 * q, x);
+            tmem_wait_ld();
+            reg_after_wait(x);
+          } else {
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-              dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int e = 0; e < 16; ++e) x[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]) * w0;
+          if (other) {
+            tmem_ld16(tO + kHeadDim + 16 * q, x);
+            tmem_wait_ld();
+            reg_after_wait(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), w1, o[e]);
+          }
+          if (!writes) continue;
+          if (bad_v != 0) add_nonfinite(a, it, pos, 16 * q, o);
+          if (a.num_splits == 1) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                  pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                  pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          } else if (l_run != 0.f) {
+            float4* dst = reinterpret_cast<float4*>(a.part_acc + part * kHeadDim + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
       }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (other && w == 0) mbar_arrive(bar(kBarXFree));
+        mbar_arrive(bar(kBarItemEmpty + slot));
+      }
+      if (other) ++xn;
     }
   }
   if (!ok && lane == 0) record_error(a.dev_err, kErrTimeout);
@@ -885,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   // ---- every copy and MMA of this CTA has completed; the columns go back
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
