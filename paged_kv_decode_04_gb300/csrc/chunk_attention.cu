@@ -110,12 +110,14 @@ enum {
   kBarPvFin,
   kNumBars
 };
-// Bad-page bits of the last kv tiles, then the TMEM address.  Twice the stages:
-// while a softmax group reads kv tile j's, QK(j + 2) has not been issued, so
-// the loads are at tile j + 1 + kStages at most.
+// The loader's notes on the last kv tiles (place in the sequence; bits of bad
+// pages, and kPartial), then the TMEM address.  Twice the stages: while a
+// softmax group reads kv tile j's, QK(j + 2) has not been issued, so the loads
+// are at tile j + 1 + kStages at most.
 constexpr int kMeta = 2 * kStages;
+constexpr uint32_t kPartial = 0x100;  // some row does not see some token
 constexpr int kOffMeta = kOffBars + 8 * kNumBars;
-constexpr int kSmem = 1024 + kOffMeta + 4 * (kMeta + 4);
+constexpr int kSmem = 1024 + kOffMeta + 4 * (2 * kMeta + 4);
 static_assert(kSmem <= 227 * 1024, "fits one CTA");
 
 // One item as the roles see it (also its words in shared memory).
@@ -153,10 +155,11 @@ struct Item {
 };
 static_assert(sizeof(Item) + 16 == kItemWords * 4, "item words");
 
-__device__ __forceinline__ Item read_item(const int* w) {
+// (volatile loads: the softmax reads the item where it needs it, rather than
+// hold its words in registers next to a row of scores)
+__device__ __forceinline__ Item read_item(uint32_t addr) {
   Item it;
-  const int4* p = reinterpret_cast<const int4*>(w);
-  const int4 a = p[0], b = p[1], c = p[2];
+  const uint4 a = lds128(addr), b = lds128(addr + 16), c = lds128(addr + 32);
   it.b = a.x; it.row0 = a.y; it.nt = a.z; it.pos0 = a.w;
   it.g = b.x; it.split = b.y; it.ns = b.z; it.w0 = b.w;
   it.t0 = c.x; it.t1 = c.y; it.lo = c.z; it.first_w = c.w;
@@ -172,6 +175,17 @@ __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* ma
       "{%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ int lds_int(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
 }
 
 // True in one lane of the (converged) warp, the same one every time.
@@ -288,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   auto bar = [&](int i) { return sb + kOffBars + 8u * i; };
   auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
   int* s_items = reinterpret_cast<int*>(smem + kOffItems);
-  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta], then the TMEM address
+  auto item_addr = [&](int slot) { return sb + kOffItems + 4u * kItemWords * slot; };
+  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta][2], then the TMEM address
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // Barriers and TMEM before a dependent grid may start: its CTAs then never
@@ -307,13 +322,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   }
   if (warp == kQkWarp) {
     __syncwarp();
-    tmem_alloc(sb + kOffMeta + 4 * kMeta, kTmemCols);
+    tmem_alloc(sb + kOffMeta + 8 * kMeta, kTmemCols);
     tmem_relinquish_alloc_permit();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = s_meta[kMeta];
+  const uint32_t tmem = s_meta[2 * kMeta];
   wait_for_prior_grids();
   allow_dependent_grids();
 
@@ -433,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           ok = false;
           break;
         }
-        const Item it = read_item(s_items + slot * kItemWords);
+        const Item it = read_item(item_addr(slot));
         if (it.b < 0) break;
         bool live_bad = false;
         for (int k = it.t0; k < it.t1; ++k, ++kt) {
@@ -484,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           ok = false;
           break;
         }
-        const Item it = read_item(s_items + slot * kItemWords);
+        const Item it = read_item(item_addr(slot));
         __syncwarp();
         if (it.b < 0) break;
         if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
@@ -533,7 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           }
           const int z = pid < 0 ? static_cast<int>(a.num_pages) : pid;  // past the pool: zeros
           if (lane == 0) {
-            s_meta[kt % kMeta] = bad;
+            *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
+                make_uint2(it.tile(k), bad | (it.partial(it.tile(k), a) ? kPartial : 0u));
             mbar_arrive_expect_tx(bar(kBarKFull + st), kRowTileBytes);
           }
           __syncwarp();
@@ -656,18 +672,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     for (int i = 0; ok; ++i) {
       const int slot = i % kItems;
       if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
-      const Item it = read_item(s_items + slot * kItemWords);
-      if (it.b < 0) break;
-      const bool one = it.halves();
-      const int tok = (row >> 2) + (one ? 0 : kHalfTokens * w);
-      const int pos = it.pos0 + tok;
-      const bool idle = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w) >= it.nt;  // whole warp
+      bool one, idle;  // one row tile; no row of this warp is a token's
+      int nu, first;   // this group's units, its first place in the list of kv tiles
+      {
+        const Item it = read_item(item_addr(slot));
+        if (it.b < 0) break;
+        one = it.halves();
+        idle = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w) >= it.nt;
+        nu = it.units_of(w);
+        first = one && w != it.first_w ? 1 : 0;
+      }
       float m_ref = -INFINITY, l_run = 0.f;
-      const int nu = it.units_of(w);
       for (int v = 0; v < nu; ++v, ++units) {
-        // place in the item's list of kv tiles
-        const int kk = one ? 2 * v + (w == it.first_w ? 0 : 1) : v;
-        const int tile = it.tile(it.t0 + kk);
         if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
         uint32_t s[8][16];
@@ -682,12 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         }
         tc_fence_before_sync();
         // (written before the loads that QK waited for)
-        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(s_meta + (kt0 + kk) % kMeta);
+        const uint2 note =
+            lds64(sb + kOffMeta + 8u * ((kt0 + first + (one ? 2 * v : v)) % kMeta));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarSFree + w));
         if (!idle) {
-          if (bad != 0u || it.partial(tile, a)) {
-            const int64_t base = static_cast<int64_t>(tile) * kKvTokens;
+          if (note.y != 0u) {
+            const uint32_t bad = note.y;
+            const int pos = lds_int(item_addr(slot) + 12) + (row >> 2) + (one ? 0 : kHalfTokens * w);
+            const int64_t base = static_cast<int64_t>(note.x) * kKvTokens;
             const int ch = clamp_cols(pos - base) + 1;  // columns [0, ch): t <= pos
             // [cl, ..): t > pos - window; [0, cs): t < sinks
             const int cl = clamp_cols(static_cast<int64_t>(pos) - a.window - base) + 1;
@@ -770,7 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         if (lane == 0) mbar_arrive(bar(kBarPFull + w));
       }
       if (!ok) break;
+      const Item it = read_item(item_addr(slot));
       kt0 += it.tiles();
+      const int tok = (row >> 2) + (one ? 0 : kHalfTokens * w);
+      const int pos = it.pos0 + tok;
 
       // ---- epilogue
       if (nu > 0 && !(ok = wait(kBarPvDone + w, units - 1))) break;
