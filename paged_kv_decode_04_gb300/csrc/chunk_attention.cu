@@ -491,24 +491,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       }
     } else if (warp == kLoadWarp) {
       // ----------------------------------------------------------- loads
+      // One elected lane issues the copies (a lane apiece took 76 cycles a
+      // copy, one lane for all 48).  Lane 8 j + p holds the id of page p of
+      // the j-th of the next four kv tiles, fetched four tiles ahead, across
+      // items too.
+      const bool issuer = elect_one();
       int kt = 0, qn = 0;  // kv tiles and items loaded so far
       int k_issued = 0, v_issued = 0;
-      for (int i = 0; ok; ++i) {
-        const int slot = i % kItems;
-        if (!wait(kBarItemFull + slot, i / kItems)) {
-          ok = false;
-          break;
+      auto fetch = [&](int i, Item& it) {
+        if (!wait(kBarItemFull + i % kItems, i / kItems)) return false;
+        it = read_item(item_addr(i % kItems));
+        return true;
+      };
+      auto load_ids = [&](const Item& it, int k0) {
+        int pid = -2;  // no row sees it
+        const int k = k0 + (lane >> 3);
+        if (k < it.t1) {
+          const int page = it.tile(k) * kKvPages + (lane & 7), t = page * kPageSize;
+          if (t < it.end() && (t + kPageSize > it.lo || t < a.sinks)) {
+            pid = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + page];
+            if (pid < 0 || pid >= a.num_pages) {
+              record_error(a.dev_err, kErrPage);
+              pid = -1;
+            }
+          }
         }
-        const Item it = read_item(item_addr(slot));
-        __syncwarp();
-        if (it.b < 0) break;
-        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+        return pid;
+      };
+      Item it, nx;
+      ok = fetch(0, it);
+      int ids = ok && it.b >= 0 ? load_ids(it, it.t0) : 0;
+      for (int i = 0; ok && it.b >= 0; ++i) {
         const int qb = qn & 1;
-        if (qn >= 2 && !wait(kBarQEmpty + qb, qn / 2 - 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
+        if (qn >= 2 && !(ok = wait(kBarQEmpty + qb, qn / 2 - 1))) break;
+        if (issuer) {
           const uint32_t qbar = bar(kBarQFull + qb);
           const uint32_t dst = sb + kOffQ + qb * 2 * kRowTileBytes;
           mbar_arrive_expect_tx(qbar, (it.halves() ? 1 : 2) * kRowTileBytes);
@@ -519,55 +535,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         }
         __syncwarp();
         ++qn;
-        const int64_t bt = static_cast<int64_t>(it.b) * a.max_blocks;
-        const int end = it.end();
-        // lane p < 8: page id of page p of the kv tile, one tile ahead
-        auto page_of = [&](int k) {
-          int pid = -2;  // no row sees it
-          if (lane < kKvPages && k < it.t1) {
-            const int page = it.tile(k) * kKvPages + lane, t = page * kPageSize;
-            if (t < end && (t + kPageSize > it.lo || t < a.sinks)) {
-              pid = a.block_table[bt + page];
-              if (pid < 0 || pid >= a.num_pages) {
-                record_error(a.dev_err, kErrPage);
-                pid = -1;
-              }
+        for (int k0 = it.t0; ok && k0 < it.t1; k0 += 4) {
+          int ids_next = 0;
+          if (k0 + 4 < it.t1) {
+            ids_next = load_ids(it, k0 + 4);
+          } else {
+            if (!(ok = fetch(i + 1, nx))) break;
+            if (nx.b >= 0) ids_next = load_ids(nx, nx.t0);
+          }
+          const unsigned bad = __ballot_sync(kFull, ids == -1);
+          const int z = ids < 0 ? static_cast<int>(a.num_pages) : ids;  // past the pool: zeros
+          for (int j = 0; j < 4 && k0 + j < it.t1; ++j, ++kt) {
+            const int st = kt % kStages;
+            if (kt >= kStages && !(ok = wait(kBarKEmpty + st, kt / kStages - 1))) break;
+            const int tile = it.tile(k0 + j);
+            const bool part = it.partial(tile, a);
+            if (issuer) {
+              *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
+                  make_uint2(tile, ((bad >> (8 * j)) & 0xFFu) | (part ? kPartial : 0u));
+              mbar_arrive_expect_tx(bar(kBarKFull + st), kRowTileBytes);
             }
+#pragma unroll
+            for (int p = 0; p < kKvPages; ++p) {
+              const int zp = __shfl_sync(kFull, z, 8 * j + p);
+              if (issuer)
+                tma_load_box(sb + kOffK + st * kRowTileBytes + p * kPageBytes, &page_map,
+                             bar(kBarKFull + st), it.g * kHeadDim, 0, zp);
+            }
+            k_issued = kt + 1;
+            if (kt >= kStages && !(ok = wait(kBarVEmpty + st, kt / kStages - 1))) break;
+            if (issuer) mbar_arrive_expect_tx(bar(kBarVFull + st), kRowTileBytes);
+#pragma unroll
+            for (int p = 0; p < kKvPages; ++p) {
+              const int zp = __shfl_sync(kFull, z, 8 * j + p);
+              if (issuer)
+                tma_load_box(sb + kOffV + st * kRowTileBytes + p * kPageBytes, &page_map,
+                             bar(kBarVFull + st), it.g * kHeadDim, kPageSize, zp);
+            }
+            v_issued = kt + 1;
           }
-          return pid;
-        };
-        int next = page_of(it.t0);
-        for (int k = it.t0; k < it.t1; ++k, ++kt) {
-          const int pid = next;
-          next = page_of(k + 1);
-          const int st = kt % kStages;
-          const unsigned bad = __ballot_sync(kFull, pid == -1) & 0xFFu;
-          if (kt >= kStages && !wait(kBarKEmpty + st, kt / kStages - 1)) {
-            ok = false;
-            break;
-          }
-          const int z = pid < 0 ? static_cast<int>(a.num_pages) : pid;  // past the pool: zeros
-          if (lane == 0) {
-            *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
-                make_uint2(it.tile(k), bad | (it.partial(it.tile(k), a) ? kPartial : 0u));
-            mbar_arrive_expect_tx(bar(kBarKFull + st), kRowTileBytes);
-          }
-          __syncwarp();
-          if (lane < kKvPages)
-            tma_load_box(sb + kOffK + st * kRowTileBytes + lane * kPageBytes, &page_map,
-                         bar(kBarKFull + st), it.g * kHeadDim, 0, z);
-          k_issued = kt + 1;
-          if (kt >= kStages && !wait(kBarVEmpty + st, kt / kStages - 1)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + st), kRowTileBytes);
-          __syncwarp();
-          if (lane < kKvPages)
-            tma_load_box(sb + kOffV + st * kRowTileBytes + lane * kPageBytes, &page_map,
-                         bar(kBarVFull + st), it.g * kHeadDim, kPageSize, z);
-          v_issued = kt + 1;
+          ids = ids_next;
         }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + i % kItems));
+        it = nx;
       }
       // every copy issued has landed before the CTA ends (full limit)
       for (int j = max(0, k_issued - kStages); j < k_issued; ++j)
