@@ -550,28 +550,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             if (kt >= kStages && !(ok = wait(kBarKEmpty + st, kt / kStages - 1))) break;
             const int tile = it.tile(k0 + j);
             const bool part = it.partial(tile, a);
+            int zp[kKvPages];
+#pragma unroll
+            for (int p = 0; p < kKvPages; ++p) zp[p] = __shfl_sync(kFull, z, 8 * j + p);
+            const int x = it.g * kHeadDim;
             if (issuer) {
               *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
                   make_uint2(tile, ((bad >> (8 * j)) & 0xFFu) | (part ? kPartial : 0u));
-              mbar_arrive_expect_tx(bar(kBarKFull + st), kRowTileBytes);
-            }
+              const uint32_t full = bar(kBarKFull + st), dst = sb + kOffK + st * kRowTileBytes;
+              mbar_arrive_expect_tx(full, kRowTileBytes);
 #pragma unroll
-            for (int p = 0; p < kKvPages; ++p) {
-              const int zp = __shfl_sync(kFull, z, 8 * j + p);
-              if (issuer)
-                tma_load_box(sb + kOffK + st * kRowTileBytes + p * kPageBytes, &page_map,
-                             bar(kBarKFull + st), it.g * kHeadDim, 0, zp);
+              for (int p = 0; p < kKvPages; ++p)
+                tma_load_box(dst + p * kPageBytes, &page_map, full, x, 0, zp[p]);
             }
             k_issued = kt + 1;
             if (kt >= kStages && !(ok = wait(kBarVEmpty + st, kt / kStages - 1))) break;
-            if (issuer) mbar_arrive_expect_tx(bar(kBarVFull + st), kRowTileBytes);
+            if (issuer) {
+              const uint32_t full = bar(kBarVFull + st), dst = sb + kOffV + st * kRowTileBytes;
+              mbar_arrive_expect_tx(full, kRowTileBytes);
 #pragma unroll
-            for (int p = 0; p < kKvPages; ++p) {
-              const int zp = __shfl_sync(kFull, z, 8 * j + p);
-              if (issuer)
-                tma_load_box(sb + kOffV + st * kRowTileBytes + p * kPageBytes, &page_map,
-                             bar(kBarVFull + st), it.g * kHeadDim, kPageSize, zp);
+              for (int p = 0; p < kKvPages; ++p)
+                tma_load_box(dst + p * kPageBytes, &page_map, full, x, kPageSize, zp[p]);
             }
+            __syncwarp();
             v_issued = kt + 1;
           }
           ids = ids_next;
