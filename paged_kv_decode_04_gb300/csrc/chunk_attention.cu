@@ -42,7 +42,8 @@
 // P enters the product with V as bf16 (8 significant bits, an error of at
 // most 2^-8 of sum p |v|, averaged over the tokens, below the output's own
 // bf16 rounding); the row sums take the unrounded FP32 values.  The reference
-// maximum moves only when a score exceeds it by 2^8, so O is rarely rescaled.
+// maximum m is the first tile's and moves only when a tile's weights sum to
+// 2^16, so the other tiles take one pass over their scores and no maximum.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -75,7 +76,7 @@ constexpr int kThreads = 32 * 12;
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads,
               "the split stays within the registers the block starts with");
-constexpr float kRescale = 8.0f;
+constexpr float kRescale = 65536.f;  // 2^16
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemP = 256, kTmemO = 384;
@@ -175,6 +176,27 @@ __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* ma
       "{%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// 32 consecutive 32-bit columns of this thread's TMEM lane; the registers hold
+// them after tmem_wait_ld and reg_after_wait32.
+#define PKV_R16(r, i)                                                                       \
+  "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+      "=r"(r[i + 6]), "=r"(r[i + 7]), "=r"(r[i + 8]), "=r"(r[i + 9]), "=r"(r[i + 10]),      \
+      "=r"(r[i + 11]), "=r"(r[i + 12]), "=r"(r[i + 13]), "=r"(r[i + 14]), "=r"(r[i + 15])
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : PKV_R16(r, 0), PKV_R16(r, 16)
+      : "r"(taddr)
+      : "memory");
+}
+#undef PKV_R16
+__device__ __forceinline__ void reg_after_wait32(uint32_t (&r)[32]) {
+  reg_after_wait(*reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+  reg_after_wait(*reinterpret_cast<uint32_t(*)[16]>(&r[16]));
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -698,24 +720,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       for (int v = 0; v < nu; ++v, ++units) {
         if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
-        uint32_t s[8][16];
-        float alpha = 1.f;
-        bool grow = false;
-        if (!idle) {
+        // PV of the group's last tile has read P and added to O; the item's
+        // first may start O once the first group has read what it holds
+        auto o_ready = [&]() {
+          if (v > 0) return wait(kBarPvDone + w, units - 1);
+          if (held) {
+            held = false;
+            return wait(kBarXFree, xn - 1);
+          }
+          return true;
+        };
+        // (written before the loads that QK waited for)
+        const uint2 note = lds64(sb + kOffMeta + 8u * ((kt0 + first + (one ? 2 * v : v)) % kMeta));
+        if (idle) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarSFree + w));
+          if (!(ok = o_ready())) break;
+        } else {
+          // the whole row of scores, so that QK may overwrite S at once
+          uint32_t x[4][32];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) tmem_ld16(tS + 16 * q, s[q]);
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, x[q]);
           tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 8; ++q) reg_after_wait(s[q]);
-        }
-        tc_fence_before_sync();
-        // (written before the loads that QK waited for)
-        const uint2 note =
-            lds64(sb + kOffMeta + 8u * ((kt0 + first + (one ? 2 * v : v)) % kMeta));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarSFree + w));
-        if (!idle) {
-          if (note.y != 0u) {
+          for (int q = 0; q < 4; ++q) reg_after_wait32(x[q]);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarSFree + w));
+          if (note.y != 0u) {  // columns that this row does not see
             const uint32_t bad = note.y;
             const int pos = lds_int(item_addr(slot) + 12) + (row >> 2) + (one ? 0 : kHalfTokens * w);
             const int64_t base = static_cast<int64_t>(note.x) * kKvTokens;
@@ -731,69 +763,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
               if ((bad >> (2 * q + 1)) & 1u) vis &= 0x0000FFFFu;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!((vis >> e) & 1u)) s[2 * q + (e >> 4)][e & 15] = 0xFF800000u;  // -inf
+                if (!((vis >> e) & 1u)) x[q][e] = 0xFF800000u;  // -inf
             }
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // The reference maximum is set by the first tile a row sees anything
+          // of, and moves only when a tile's weights sum to 2^kRescale or more
+          // (FP32 sums and bf16 weights keep their relative precision below).
+          bool ready = false, measure = __any_sync(kFull, m_ref == -INFINITY);
+          for (;;) {
+            float alpha = 1.f;
+            if (measure) {
+              float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
+              for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(s[q][e]),
-                                       __uint_as_float(s[q][e + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          grow = top > m_ref + kRescale;
-          if (grow) {
-            alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
-            m_ref = top;
-          }
-        }
-        // PV of the group's last tile has read P and added to O; the item's
-        // first may start O once the first group has read what it holds
-        if (v > 0) {
-          if (!(ok = wait(kBarPvDone + w, units - 1))) break;
-        } else if (held) {
-          if (!(ok = wait(kBarXFree, xn - 1))) break;
-          held = false;
-        }
-        tc_fence_after_sync();
-        if (!idle) {
-          if (v > 0 && __any_sync(kFull, grow)) {
+                for (int e = 0; e < 32; e += 2)
+                  mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[q][e]),
+                                           __uint_as_float(x[q][e + 1]));
+              const float top = fmaxf(mx[0], mx[1]) * c;
+              if (top > m_ref) {
+                alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
+                m_ref = top;
+              }
+              if (!ready) {
+                if (!(ok = o_ready())) break;
+                ready = true;
+                tc_fence_after_sync();
+              }
+              if (v > 0 && __any_sync(kFull, alpha != 1.f)) {
+                l_run *= alpha;
+#pragma unroll 1
+                for (int q = 0; q < kHeadDim / 16; ++q) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * q, o);
+                  tmem_wait_ld();
+                  reg_after_wait(o);
 #pragma unroll
-            for (int q = 0; q < kHeadDim / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld16(tO + 16 * q, o);
-              tmem_wait_ld();
-              reg_after_wait(o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(tO + 16 * q, o);
+                  for (int e = 0; e < 16; ++e)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                  tmem_st16(tO + 16 * q, o);
+                }
+              }
             }
-          }
-          // (a row that has seen no token yet: every weight 2^(-inf) = 0)
-          const float m = m_ref == -INFINITY ? 0.f : m_ref;
-          const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
-          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // 32 columns at a time: the scores of a step enter it at its start,
-          // so that the steps before do not hold its results in registers
+            // (a row that has seen no token yet: every weight 2^(-inf) = 0)
+            const float m = m_ref == -INFINITY ? 0.f : m_ref;
+            const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pw[16];
-            reg_after_wait(s[2 * q]);
-            reg_after_wait(s[2 * q + 1]);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pw[16];
+              reg_after_wait32(x[q]);  // (keeps the steps' results apart)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t* sp = &s[2 * q + (e >> 3)][2 * (e & 7)];
-              float2 x = ffma2(make_float2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), c2, m2);
-              x.x = fast_exp2(x.x);
-              x.y = fast_exp2(x.y);
-              ls[e & 1] = fadd2(ls[e & 1], x);
-              pw[e] = pack_bf16x2(x.x, x.y);
+              for (int e = 0; e < 16; ++e) {
+                float2 y = ffma2(make_float2(__uint_as_float(x[q][2 * e]),
+                                             __uint_as_float(x[q][2 * e + 1])), c2, m2);
+                y.x = fast_exp2(y.x);
+                y.y = fast_exp2(y.y);
+                ls[e & 1] = fadd2(ls[e & 1], y);
+                pw[e] = pack_bf16x2(y.x, y.y);
+              }
+              if (q == 0 && !ready) {
+                if (!(ok = o_ready())) break;
+                ready = true;
+                tc_fence_after_sync();
+              }
+              tmem_st16(tP + 16 * q, pw);
             }
-            tmem_st16(tP + 16 * q, pw);
+            if (!ok) break;
+            const float2 l2 = fadd2(ls[0], ls[1]);
+            const float sum = l2.x + l2.y;
+            // (NaN too; a tile that has just been measured stands as it is)
+            const bool over = !(sum < kRescale);
+            if (measure || !__any_sync(kFull, over)) {
+              l_run += sum;
+              break;
+            }
+            measure = true;
           }
-          const float2 l2 = fadd2(ls[0], ls[1]);
-          l_run = l_run * alpha + (l2.x + l2.y);
+          if (!ok) break;
           tmem_wait_st();
         }
         tc_fence_before_sync();
