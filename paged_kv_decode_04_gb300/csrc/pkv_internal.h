@@ -279,7 +279,7 @@ struct MaskedArgs {
 // Tiles of the chunk kernel: new tokens (all 4 query heads of a kv head) and
 // cached tokens.
 constexpr int kChunkTileTokens = 64;
-constexpr int kChunkKvTokens = 128;
+constexpr int kChunkKvTokens = 64;
 
 // grid persistent CTAs (at most one per SM), then the merge of the ranges.
 // q_map: q as [num_tokens][32][64], boxes of 32 tokens and 4 heads, 128-byte
