@@ -6,41 +6,53 @@
 // t < sinks).  A tile is up to 64 consecutive new tokens of one sequence; for
 // one kv head their 4 query heads each make 256 rows (row = 4 token + head),
 // two MMA row tiles of 128, which share every K/V row that is loaded.  The
-// cached tokens come in tiles of 64 (4 pages).  Per row tile and kv tile
+// cached tokens come in tiles of 128 (8 pages).  Per row tile and kv tile
 //
-//   S = Q K^T   (128 x 64, 4 MMAs of K = 16; Q and K rows in shared memory)
+//   S = Q K^T   (128 x 128, 4 MMAs of K = 16; Q and K rows in shared memory)
 //   P = 2^(c S - m), the FP32 online softmax, one thread per row
-//   O += P V    (128 x 64, 4 MMAs of K = 16; P in TMEM, V rows in shared)
+//   O += P V    (128 x 64, 8 MMAs of K = 16; P in TMEM, V rows in shared)
 //
-// Four softmax warp groups, each with its S, P and O: two for each row tile,
-// taking its even and its odd kv tiles.  A tile of at most 32 tokens has one
-// row tile only; its kv tiles go round the four groups.  The groups that saw
-// the same rows are joined at the end like ranges of a split.
+// A tile of at most 32 tokens has one row tile only; the two softmax warp
+// groups then take the even and the odd kv tiles of the same rows, and their
+// states are joined at the end like two ranges.
 //
-// TMEM (512 columns): S of group g at 64 g with P over it (the scores are in
-// registers by then), O at 256 + 64 g.
+// TMEM (512 columns): S of row tile / group w at 128 w, P at 256 + 64 w, O at
+// 384 + 64 w.  P does not lie over S, so S of the next kv tile is computed
+// while this one's exponentials are taken.
 //
 // Warps, one persistent CTA per SM, each role walking the CTA's items (tile,
 // kv head, range of the kv tiles) and handing over through mbarriers, so the
 // next item's loads and first products run under the last one's epilogue:
-//   0-15    softmax, rescaling of O, epilogue (group = warp / 4)
-//   16, 19  issue QK and PV.  A unit is a (row tile, kv tile) pair; QK of a
-//           group's next unit follows PV of its last
-//   17      loads: Q by one box per row tile, K and V by 2 KiB boxes of one
-//           page and head, two kv tiles to a stage; pages outside every row's
-//           sight (or with a bad id) are read at a page index past the pool,
-//           i.e. as zeros
-//   18      finds the CTA's next items from the offsets and lengths (items
-//           without any kv tile it answers itself), and relays "V has landed":
-//           in the tiles that some row sees in part only it first replaces
-//           non-finite V values by zero (a masked weight is zero, but 0 x NaN
-//           is not); rows that do see such a value get it added in the epilogue
-// Four groups because a unit is a chain (QK, scores to registers, exponentials,
-// P to TMEM, PV) whose steps each take one pass of latency: with two groups of
-// 128 x 128 units the exponentials filled 44 % of the special-function unit's
-// time (2 x 4096 tokens over 8192: 420 us; with four of 128 x 64 TIME us).
-// What the issuing warps execute per unit is kept short: with both products
-// and their look-ahead in one warp, that warp set the pace.
+//   0-3, 4-7  softmax of S_0 and S_1, rescaling of O, epilogue
+//   8, 11     issue QK and PV.  A unit is a (row tile, kv tile) pair; units
+//             alternate between S_0 and S_1, across items too
+//   9         loads: Q by one box per row tile, K and V by 2 KiB boxes of one
+//             page and head; pages outside every row's sight (or with a bad
+//             id) are read at a page index past the pool, i.e. as zeros
+//   10        finds the CTA's next items from the offsets and lengths (items
+//             without any kv tile it answers itself), and relays "V has
+//             landed": in the tiles that some row sees in part only it first
+//             replaces non-finite V values by zero (a masked weight is zero,
+//             but 0 x NaN is not); rows that do see such a value get it added
+//             in the epilogue
+// Measured on 2 x 4096 tokens over 8192 (391 GFLOP): 413 us, 0.95 PFLOP/s, half
+// of the card's cuBLAS bf16 rate.  A unit takes 1230 cycles of an SM, of which
+// its MMAs fill 440 and its exponentials 546 (30 a clock), the rest being the
+// latencies of the chain scores -> registers -> P -> PV; the two groups' chains
+// overlap, but two warps to a scheduler do not hide them all.  What moved it:
+//  * the issue of QK and PV by two warps (680 -> 567 us): the issuing warps'
+//    instruction streams are slow next to the softmax (they share the
+//    schedulers' instruction caches), and one warp for both took 1400 cycles a
+//    unit;
+//  * no register spills in the softmax (567 -> 449 us): the epilogue runs in
+//    16-column steps, and what the loop needs of an item it reads again;
+//  * one elected lane for the copies of a kv tile, and no maximum per tile
+//    (449 -> 415 us);
+//  * not: 16 softmax warps of half a row each (558 us: twice the hand-over
+//    instructions), four groups of 128 x 64 units with P over S (485 us: twice
+//    the units for the issuing warps), scalar instead of packed FP32 (493 us),
+//    skipping 32-column steps that no row sees (463 us: no overlap between
+//    steps).
 // P enters the product with V as bf16 (8 significant bits, an error of at
 // most 2^-8 of sum p |v|, averaged over the tokens, below the output's own
 // bf16 rounding); the row sums take the unrounded FP32 values.  The reference
@@ -63,36 +75,34 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kQTokens = kChunkTileTokens;    // 64 tokens a tile
 constexpr int kHalfTokens = kQTokens / 2;     // 32 tokens: one MMA row tile
-constexpr int kKvTokens = kChunkKvTokens;     // 64 cached tokens a kv tile
+constexpr int kKvTokens = kChunkKvTokens;     // 128 cached tokens a kv tile
 constexpr int kKvPages = kKvTokens / kPageSize;
-constexpr int kStageTiles = 2;                // kv tiles of a stage
-constexpr int kStagePages = kStageTiles * kKvPages;
 constexpr int kRow = kHeadDim * 2;            // 128 B
-constexpr int kRowTileBytes = 128 * kRow;     // 16 KiB: a row tile of Q, a stage of K or V
+constexpr int kRowTileBytes = 128 * kRow;     // 16 KiB: a row tile of Q, a kv tile of K or V
 constexpr int kPageBytes = kPageSize * kRow;  // 2 KiB: one head's K (or V) rows of a page
-constexpr int kKvBytes = kKvPages * kPageBytes;
-constexpr int kStages = 4;                    // stages in flight
+constexpr int kStages = 4;                    // kv tiles in flight
 constexpr int kItems = 8;                     // slots for published items
 constexpr int kAhead = 3;                     // items published before the relay starts one
-constexpr int kGroups = 4;
-constexpr int kSoftmaxWarps = 4 * kGroups;
-constexpr int kQkWarp = 16, kLoadWarp = 17, kSchedWarp = 18;  // and 19 issues PV
-constexpr int kThreads = 32 * 20;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kQkWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11 issues PV
+constexpr int kThreads = 32 * 12;
+// Registers: 168 x 384 threads at launch = 64512 = 256 x 216 + 128 x 72.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads,
+              "the split stays within the registers the block starts with");
 constexpr float kRescale = 65536.f;  // 2^16
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 256;
+constexpr uint32_t kTmemP = 256, kTmemO = 384;
 constexpr uint32_t kIdescQK = tc_idesc_bf16(128, kKvTokens, false);
 constexpr uint32_t kIdescPV = tc_idesc_bf16(128, kHeadDim, true);
-static_assert(kKvTokens * kGroups <= kTmemO && kTmemO + kHeadDim * kGroups <= kTmemCols,
-              "S and O of every group");
 
 // Shared memory, from a 1024-byte aligned base.
 constexpr int kOffQ = 0;                               // [2 items][2 row tiles]
 constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
 constexpr int kOffV = kOffK + kStages * kRowTileBytes;
-constexpr int kOffMl = kOffV + kStages * kRowTileBytes;  // [groups][128] (m, l) handed over
-constexpr int kOffItems = kOffMl + kGroups * 128 * 8;
+constexpr int kOffMl = kOffV + kStages * kRowTileBytes;  // [128] (m, l) handed between groups
+constexpr int kOffItems = kOffMl + 128 * 8;
 constexpr int kItemWords = 16;
 constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
 enum {
@@ -104,24 +114,25 @@ enum {
   kBarQFull = kBarVEmpty + kStages,
   kBarQEmpty = kBarQFull + 2,
   kBarSFull = kBarQEmpty + 2,
-  kBarPFull = kBarSFull + kGroups,
-  kBarPvDone = kBarPFull + kGroups,
-  kBarXFull = kBarPvDone + kGroups,  // a group's rows may be read by the joining one
-  kBarXFree = kBarXFull + kGroups,   // and have been
-  kBarItemFull = kBarXFree + kGroups,
+  kBarSFree = kBarSFull + 2,
+  kBarPFull = kBarSFree + 2,
+  kBarPvDone = kBarPFull + 2,
+  kBarItemFull = kBarPvDone + 2,
   kBarItemEmpty = kBarItemFull + kItems,
-  kBarQkFin = kBarItemEmpty + kItems,
+  kBarXFull = kBarItemEmpty + kItems,
+  kBarXFree,
+  kBarQkFin,
   kBarPvFin,
   kNumBars
 };
-// The loader's notes on the kv tiles of the last stages (place in the
-// sequence; bits of bad pages, and kPartial), then the TMEM address.  Twice
-// the stages: until a softmax group has read the note of its unit n it holds
-// back QK(n + 4), so the loads are two stages and the ring ahead at most.
+// The loader's notes on the last kv tiles (place in the sequence; bits of bad
+// pages, and kPartial), then the TMEM address.  Twice the stages: while a
+// softmax group reads kv tile j's, QK(j + 2) has not been issued, so the loads
+// are at tile j + 1 + kStages at most.
 constexpr int kMeta = 2 * kStages;
 constexpr uint32_t kPartial = 0x100;  // some row does not see some token
 constexpr int kOffMeta = kOffBars + 8 * kNumBars;
-constexpr int kSmem = 1024 + kOffMeta + 8 * kStageTiles * kMeta + 16;
+constexpr int kSmem = 1024 + kOffMeta + 4 * (2 * kMeta + 4);
 static_assert(kSmem <= 227 * 1024, "fits one CTA");
 
 // One item as the roles see it (also its words in shared memory).
@@ -136,18 +147,15 @@ struct Item {
   int w0;       // first kv tile of the window
   int t0, t1;   // range [t0, t1) of the tile's list: sinks, then window
   int lo;       // first token of any row's window
-  int pad;
+  int first_w;  // softmax group of the first unit
   // in shared memory also: whether a live non-finite V value was replaced (the
-  // relay's answer), units(), tiles() and halves() (what the MMA warps read)
+  // relay's answer), units(), tiles() and halves() (what the MMA warp reads)
 
   __device__ __forceinline__ bool halves() const { return nt <= kHalfTokens; }
   __device__ __forceinline__ int tiles() const { return t1 - t0; }
   __device__ __forceinline__ int units() const { return halves() ? tiles() : 2 * tiles(); }
-  // The v-th kv tile of group g is the list's (stride() v + first(g))-th.
-  __device__ __forceinline__ int stride() const { return halves() ? 4 : 2; }
-  __device__ __forceinline__ int first(int g_) const { return halves() ? g_ : g_ & 1; }
-  __device__ __forceinline__ int units_of(int g_) const {
-    return (tiles() - first(g_) + stride() - 1) / stride();
+  __device__ __forceinline__ int units_of(int w) const {
+    return halves() ? (tiles() + (w == first_w ? 1 : 0)) >> 1 : tiles();
   }
   __device__ __forceinline__ int tile(int k) const { return k < ns ? k : w0 + (k - ns); }
   __device__ __forceinline__ int end() const { return pos0 + nt; }  // tokens seen by the last row
@@ -169,7 +177,7 @@ __device__ __forceinline__ Item read_item(uint32_t addr) {
   const uint4 a = lds128(addr), b = lds128(addr + 16), c = lds128(addr + 32);
   it.b = a.x; it.row0 = a.y; it.nt = a.z; it.pos0 = a.w;
   it.g = b.x; it.split = b.y; it.ns = b.z; it.w0 = b.w;
-  it.t0 = c.x; it.t1 = c.y; it.lo = c.z; it.pad = 0;
+  it.t0 = c.x; it.t1 = c.y; it.lo = c.z; it.first_w = c.w;
   return it;
 }
 
@@ -287,12 +295,6 @@ __device__ __forceinline__ int clamp_cols(int64_t v) {
   return v < -1 ? -1 : (v > kKvTokens ? kKvTokens : static_cast<int>(v));
 }
 
-// bf16 pair: mask of the halves that are not finite.
-__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
-  return ((w & 0x00007F80u) == 0x00007F80u ? 0x0000FFFFu : 0u) |
-         ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-}
-
 // Add to dims [d0, d0 + 16) of a row at position pos the non-finite V values
 // that the relay replaced by zero and the row sees (rare: plain loads).
 __device__ __forceinline__ void add_nonfinite(const MaskedArgs& a, const Item& it, int pos, int d0,
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
   int* s_items = reinterpret_cast<int*>(smem + kOffItems);
   auto item_addr = [&](int slot) { return sb + kOffItems + 4u * kItemWords * slot; };
-  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta][2][2], then the TMEM address
+  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta][2], then the TMEM address
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // Barriers and TMEM before a dependent grid may start: its CTAs then never
@@ -341,26 +343,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     tma_prefetch_desc(&page_map);
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
-      if ((i >= kBarPFull && i < kBarPvDone) || (i >= kBarXFull && i < kBarItemFull)) n = 4;
-      if (i >= kBarItemEmpty && i < kBarQkFin) n = kSoftmaxWarps + 4;
+      if (i >= kBarSFree && i < kBarPvDone) n = 4;               // s_free, p_full
+      if (i >= kBarItemEmpty && i < kBarXFull) n = kSoftmaxWarps + 4;
+      if (i == kBarXFull || i == kBarXFree) n = 4;
       mbar_init(bar(i), n);
     }
     fence_barrier_init();
   }
   if (warp == kQkWarp) {
     __syncwarp();
-    tmem_alloc(sb + kOffMeta + 8 * kStageTiles * kMeta, kTmemCols);
+    tmem_alloc(sb + kOffMeta + 8 * kMeta, kTmemCols);
     tmem_relinquish_alloc_permit();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = s_meta[2 * kStageTiles * kMeta];
+  const uint32_t tmem = s_meta[2 * kMeta];
   wait_for_prior_grids();
   allow_dependent_grids();
 
   bool ok = true;
   if (warp >= kQkWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSchedWarp) {
       // --------------------------------------------- scheduler, V's relay
       // Items in order (tile, range, head); the tiles of a sequence from its
@@ -370,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       const int per_tile = a.num_splits * kNumKvHeads;
       int b0 = -32, before = 0, sum = 0;      // 32 sequences from b0: tiles before them, theirs
       int cnt = 0, incl = 0, o0 = 0, o1 = 0;  // this lane's sequence
-      int out_i = 0;                          // items published
-      int round = 0, ks = 0;  // ..., stages relayed
+      int parity = 0, out_i = 0;              // units so far mod 2, items published
+      int round = 0, kt = 0;
       bool more = true;
       // publish the next item (or the end); false: a wait ran out
       auto publish = [&]() {
@@ -391,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             if (o0 < 0 || o1 < o0 || o1 > a.num_tokens) {
               if (blockIdx.x == 0) record_error(a.dev_err, kErrOffsets);
             } else {
-              cnt = (o1 - o0 + kQTokens - 1) / kQTokens;
+              // (shorter chunks are the other kernel's)
+              cnt = o1 - o0 > kShortTokens ? (o1 - o0 + kQTokens - 1) / kQTokens : 0;
             }
           }
           incl = cnt;
@@ -448,6 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             }
             continue;
           }
+          it.first_w = parity;
+          parity = (parity + it.units()) & 1;
         }
         const int slot = out_i % kItems;
         if (out_i >= kItems && !wait(kBarItemEmpty + slot, out_i / kItems - 1)) return false;
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           int4* w = reinterpret_cast<int4*>(s_items + slot * kItemWords);
           w[0] = make_int4(it.b, it.row0, it.nt, it.pos0);
           w[1] = make_int4(it.g, it.split, it.ns, it.w0);
-          w[2] = make_int4(it.t0, it.t1, it.lo, 0);
+          w[2] = make_int4(it.t0, it.t1, it.lo, it.first_w);
           w[3] = make_int4(0, it.b < 0 ? 0 : it.units(), it.tiles(), it.halves() ? 1 : 0);
           mbar_arrive(bar(kBarItemFull + slot));
         }
@@ -475,20 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         const Item it = read_item(item_addr(slot));
         if (it.b < 0) break;
         bool live_bad = false;
-        for (int k = it.t0; k < it.t1; k += kStageTiles, ++ks) {
-          const int st = ks % kStages;
-          if (!wait(kBarVFull + st, ks / kStages)) {
+        for (int k = it.t0; k < it.t1; ++k, ++kt) {
+          const int st = kt % kStages, tile = it.tile(k);
+          if (!wait(kBarVFull + st, kt / kStages)) {
             ok = false;
             break;
           }
-          bool scanned = false;
-          for (int h = 0; h < kStageTiles && k + h < it.t1; ++h) {
-            const int tile = it.tile(k + h);
-            if (!it.partial(tile, a)) continue;
-            scanned = true;
+          if (it.partial(tile, a)) {
             // 4 rows of 8 16-byte chunks at a time (the swizzle permutes
             // chunks within a row only)
-            const uint32_t v0 = sb + kOffV + st * kRowTileBytes + h * kKvBytes + lane * 16;
+            const uint32_t v0 = sb + kOffV + st * kRowTileBytes + lane * 16;
             const int row_end = it.end() - tile * kKvTokens;  // rows that some query sees
 #pragma unroll 1
             for (int r = 0; r < kKvTokens; r += 16) {
@@ -506,11 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
                 }
               }
             }
+            fence_proxy_async_smem();
           }
-          if (scanned) fence_proxy_async_smem();
           const bool any = __any_sync(kFull, live_bad);
           if (lane == 0) {
-            if (k + kStageTiles >= it.t1) s_items[slot * kItemWords + 12] = any ? 1 : 0;
+            if (k == it.t1 - 1) s_items[slot * kItemWords + 12] = any ? 1 : 0;
             mbar_arrive(bar(kBarVReady + st));
           }
           __syncwarp();
@@ -520,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     } else if (warp == kLoadWarp) {
       // ----------------------------------------------------------- loads
       // One elected lane issues the copies (a lane apiece took 76 cycles a
-      // copy, one lane for all 48).  Lane 4 j + p holds the id of page p of
-      // the j-th of the next eight kv tiles, fetched eight tiles ahead, across
+      // copy, one lane for all 48).  Lane 8 j + p holds the id of page p of
+      // the j-th of the next four kv tiles, fetched four tiles ahead, across
       // items too.
       const bool issuer = elect_one();
-      int ks = 0, qn = 0;  // stages and items loaded so far
+      int kt = 0, qn = 0;  // kv tiles and items loaded so far
       int k_issued = 0, v_issued = 0;
       auto fetch = [&](int i, Item& it) {
         if (!wait(kBarItemFull + i % kItems, i / kItems)) return false;
@@ -533,9 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       };
       auto load_ids = [&](const Item& it, int k0) {
         int pid = -2;  // no row sees it
-        const int k = k0 + (lane >> 2);
+        const int k = k0 + (lane >> 3);
         if (k < it.t1) {
-          const int page = it.tile(k) * kKvPages + (lane & 3), t = page * kPageSize;
+          const int page = it.tile(k) * kKvPages + (lane & 7), t = page * kPageSize;
           if (t < it.end() && (t + kPageSize > it.lo || t < a.sinks)) {
             pid = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + page];
             if (pid < 0 || pid >= a.num_pages) {
@@ -563,53 +566,45 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         }
         __syncwarp();
         ++qn;
-        for (int k0 = it.t0; ok && k0 < it.t1; k0 += 8) {
+        for (int k0 = it.t0; ok && k0 < it.t1; k0 += 4) {
           int ids_next = 0;
-          if (k0 + 8 < it.t1) {
-            ids_next = load_ids(it, k0 + 8);
+          if (k0 + 4 < it.t1) {
+            ids_next = load_ids(it, k0 + 4);
           } else {
             if (!(ok = fetch(i + 1, nx))) break;
             if (nx.b >= 0) ids_next = load_ids(nx, nx.t0);
           }
           const unsigned bad = __ballot_sync(kFull, ids == -1);
           const int z = ids < 0 ? static_cast<int>(a.num_pages) : ids;  // past the pool: zeros
-          for (int j = 0; j < 8 && k0 + j < it.t1; j += kStageTiles, ++ks) {
-            const int st = ks % kStages;
-            if (ks >= kStages && !(ok = wait(kBarKEmpty + st, ks / kStages - 1))) break;
-            int zp[kStagePages];
+          for (int j = 0; j < 4 && k0 + j < it.t1; ++j, ++kt) {
+            const int st = kt % kStages;
+            if (kt >= kStages && !(ok = wait(kBarKEmpty + st, kt / kStages - 1))) break;
+            const int tile = it.tile(k0 + j);
+            const bool part = it.partial(tile, a);
+            int zp[kKvPages];
 #pragma unroll
-            for (int p = 0; p < kStagePages; ++p) zp[p] = __shfl_sync(kFull, z, 4 * j + p);
+            for (int p = 0; p < kKvPages; ++p) zp[p] = __shfl_sync(kFull, z, 8 * j + p);
             const int x = it.g * kHeadDim;
-            const bool both = k0 + j + 1 < it.t1;  // else the stage holds one kv tile
-            const uint32_t bytes = both ? kRowTileBytes : kKvBytes;
             if (issuer) {
-#pragma unroll
-              for (int h = 0; h < kStageTiles; ++h) {
-                const int tile = it.tile(k0 + j + h);
-                const uint32_t bits = (bad >> (4 * (j + h))) & 0xFu;
-                *reinterpret_cast<uint2*>(s_meta + 2 * (kStageTiles * (ks % kMeta) + h)) =
-                    make_uint2(tile, bits | (it.partial(tile, a) ? kPartial : 0u));
-              }
+              *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
+                  make_uint2(tile, ((bad >> (8 * j)) & 0xFFu) | (part ? kPartial : 0u));
               const uint32_t full = bar(kBarKFull + st), dst = sb + kOffK + st * kRowTileBytes;
-              mbar_arrive_expect_tx(full, bytes);
+              mbar_arrive_expect_tx(full, kRowTileBytes);
 #pragma unroll
-              for (int p = 0; p < kStagePages; ++p)
-                if (p < kKvPages || both)
-                  tma_load_box(dst + p * kPageBytes, &page_map, full, x, 0, zp[p]);
+              for (int p = 0; p < kKvPages; ++p)
+                tma_load_box(dst + p * kPageBytes, &page_map, full, x, 0, zp[p]);
             }
-            k_issued = ks + 1;
-            __syncwarp();
-            if (ks >= kStages && !(ok = wait(kBarVEmpty + st, ks / kStages - 1))) break;
+            k_issued = kt + 1;
+            if (kt >= kStages && !(ok = wait(kBarVEmpty + st, kt / kStages - 1))) break;
             if (issuer) {
               const uint32_t full = bar(kBarVFull + st), dst = sb + kOffV + st * kRowTileBytes;
-              mbar_arrive_expect_tx(full, bytes);
+              mbar_arrive_expect_tx(full, kRowTileBytes);
 #pragma unroll
-              for (int p = 0; p < kStagePages; ++p)
-                if (p < kKvPages || both)
-                  tma_load_box(dst + p * kPageBytes, &page_map, full, x, kPageSize, zp[p]);
+              for (int p = 0; p < kKvPages; ++p)
+                tma_load_box(dst + p * kPageBytes, &page_map, full, x, kPageSize, zp[p]);
             }
             __syncwarp();
-            v_issued = ks + 1;
+            v_issued = kt + 1;
           }
           ids = ids_next;
         }
@@ -632,40 +627,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       // (the whole warp walks the units, so that what the instructions take
       // is uniform over it; one elected lane issues them)
       const bool issuer = elect_one();
-      int ks = 0;            // stages before
-      uint32_t phase = 0;    // bit g: units of group g so far, mod 2
+      int n = 0, kt = 0;  // units and kv tiles before; unit n is group (n & 1)'s n / 2th
       for (int i = 0; ok; ++i) {
         const int slot = i % kItems, qb = i & 1;
         if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
-        const uint4 x = lds128(item_addr(slot) + 48);
+        const int4 x = *reinterpret_cast<const int4*>(s_items + slot * kItemWords + 12);
         const int U = x.y;
         const bool one = x.w != 0;
         if (U == 0) break;
         if (!(ok = wait(kBarQFull + qb, i >> 1))) break;
         const uint32_t q0 = desc_lo(sb + kOffQ + 2 * qb * kRowTileBytes);
-        const int in_stage = one ? 1 : 3;  // units of a stage less one
-        for (int u = 0; u < U; ++u) {
-          const int g = one ? u & 3 : 2 * (u & 1) + ((u >> 1) & 1);
-          const int h = (one ? u : u >> 1) & 1;  // kv tile of the stage
-          const int st = ks % kStages;
-          const bool last = u == U - 1 || (u & in_stage) == in_stage;
-          if ((u & in_stage) == 0 && !(ok = wait(kBarKFull + st, ks / kStages))) break;
-          // the group's last P has been read: S may take its place (at once
-          // before its first unit)
-          if (!(ok = wait(kBarPvDone + g, static_cast<int>((phase >> g) & 1u) ^ 1))) break;
-          phase ^= 1u << g;
+        for (int u = 0; u < U; ++u, ++n) {
+          const int w = n & 1, st = kt % kStages;
+          const bool last = one || (u & 1);  // use of this kv tile
+          if (!(ok = wait(kBarKFull + st, kt / kStages))) break;
+          if (n >= 2 && !(ok = wait(kBarSFree + w, (n >> 1) - 1))) break;
           tc_fence_after_sync();
-          const uint32_t q = q0 + (one ? 0 : u & 1) * (kRowTileBytes >> 4);
-          const uint32_t kr = desc_lo(sb + kOffK) + st * (kRowTileBytes >> 4) + h * (kKvBytes >> 4);
+          const uint32_t q = q0 + (one ? 0 : w) * (kRowTileBytes >> 4);
+          const uint32_t kr = desc_lo(sb + kOffK) + st * (kRowTileBytes >> 4);
           if (issuer) {
 #pragma unroll
             for (int kk = 0; kk < kHeadDim / 16; ++kk)
-              mma_ss(tmem + kKvTokens * g, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
-            tc_commit(bar(kBarSFull + g));
+              mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
+            tc_commit(bar(kBarSFull + w));
             if (last) tc_commit(bar(kBarKEmpty + st));
             if (u == U - 1) tc_commit(bar(kBarQEmpty + qb));
           }
-          if (last) ++ks;
+          if (last) ++kt;
         }
         if (issuer) mbar_arrive(bar(kBarItemEmpty + slot));
       }
@@ -678,36 +666,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     } else {
       // --------------------------------------------------------- O += P V
       const bool issuer = elect_one();
-      int ks = 0;
-      uint32_t phase = 0;
+      int n = 0, kt = 0;
       for (int i = 0; ok; ++i) {
         const int slot = i % kItems;
         if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
-        const uint4 x = lds128(item_addr(slot) + 48);
+        const int4 x = *reinterpret_cast<const int4*>(s_items + slot * kItemWords + 12);
         const int U = x.y;
         const bool one = x.w != 0;
         if (U == 0) break;
-        const int in_stage = one ? 1 : 3;
-        for (int u = 0; u < U; ++u) {
-          const int g = one ? u & 3 : 2 * (u & 1) + ((u >> 1) & 1);
-          const int h = (one ? u : u >> 1) & 1;
-          const int st = ks % kStages;
-          const bool last = u == U - 1 || (u & in_stage) == in_stage;
-          if ((u & in_stage) == 0 && !(ok = wait(kBarVReady + st, ks / kStages))) break;
-          if (!(ok = wait(kBarPFull + g, (phase >> g) & 1u))) break;
-          phase ^= 1u << g;
+        for (int u = 0; u < U; ++u, ++n) {
+          const int w = n & 1, st = kt % kStages;
+          const bool last = one || (u & 1);
+          if (!(ok = wait(kBarVReady + st, kt / kStages))) break;
+          if (!(ok = wait(kBarPFull + w, n >> 1))) break;
           tc_fence_after_sync();
-          const uint32_t vr = desc_lo(sb + kOffV) + st * (kRowTileBytes >> 4) + h * (kKvBytes >> 4);
+          const uint32_t vr = desc_lo(sb + kOffV) + st * (kRowTileBytes >> 4);
           if (issuer) {
-            const uint32_t d = tmem + kTmemO + kHeadDim * g, pa = tmem + kKvTokens * g;
-            mma_ts(d, pa, vr, kIdescPV, u >= 4);  // a group's first unit of the item starts O
+            const uint32_t d = tmem + kTmemO + kHeadDim * w, pa = tmem + kTmemP + 64 * w;
+            mma_ts(d, pa, vr, kIdescPV, u >= 2);  // a group's first unit of the item starts O
 #pragma unroll
             for (int p = 1; p < kKvPages; ++p)
               mma_ts(d, pa + 8 * p, vr + p * (kPageBytes >> 4), kIdescPV, true);
-            tc_commit(bar(kBarPvDone + g));
+            tc_commit(bar(kBarPvDone + w));
             if (last) tc_commit(bar(kBarVEmpty + st));
           }
-          if (last) ++ks;
+          if (last) ++kt;
         }
         if (issuer) mbar_arrive(bar(kBarItemEmpty + slot));
       }
@@ -718,91 +701,104 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       __syncwarp();
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // --------------------------------------------------- softmax, epilogue
-    const int grp = warp >> 2;
-    const int row = tid & 127;  // MMA row = TMEM lane
+    const int w = warp >> 2;
+    const int row = tid & 127;                 // MMA row = TMEM lane
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t tS = t_lane + kKvTokens * grp, tO = t_lane + kTmemO + kHeadDim * grp;
+    const uint32_t tS = t_lane + 128 * w, tP = t_lane + kTmemP + 64 * w,
+                   tO = t_lane + kTmemO + kHeadDim * w;
     const float c = a.scale_log2;
-    // this group's units, stages of the items before, times its rows were
-    // handed over
-    int units = 0, ks0 = 0, xn = 0;
-    uint32_t xphase = 0;  // bit g: times group g's rows were handed over, to whichever group, mod 2
-    bool held = false;    // this group's O has not been read by the joining one yet
+    // this group's units, kv tiles of the items before, rows handed over
+    int units = 0, kt0 = 0, xn = 0;
+    bool held = false;  // the second group's O has not been read by the first yet
     for (int i = 0; ok; ++i) {
       const int slot = i % kItems;
       if (!(ok = wait(kBarItemFull + slot, i / kItems))) break;
       bool one, idle;  // one row tile; no row of this warp is a token's
-      int nu, k, step; // this group's units, places of its kv tiles in the list
+      int nu, first;   // this group's units, its first place in the list of kv tiles
       {
         const Item it = read_item(item_addr(slot));
         if (it.b < 0) break;
         one = it.halves();
-        idle = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * (grp >> 1)) >= it.nt;
-        nu = it.units_of(grp);
-        k = it.first(grp);
-        step = it.stride();
+        idle = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w) >= it.nt;
+        nu = it.units_of(w);
+        first = one && w != it.first_w ? 1 : 0;
       }
       float m_ref = -INFINITY, l_run = 0.f;
-      for (int v = 0; v < nu; ++v, ++units, k += step) {
-        if (!(ok = wait(kBarSFull + grp, units))) break;
+      for (int v = 0; v < nu; ++v, ++units) {
+        if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
-        if (!idle) {
-          // (written before the loads that QK waited for)
-          const uint2 note =
-              lds64(sb + kOffMeta +
-                    8u * (kStageTiles * ((ks0 + (k >> 1)) % kMeta) + (k & 1)));
-          uint32_t vis[2] = {kFull, kFull};  // columns that this row sees
-          if (note.y != 0u) {
-            const int pos =
-                lds_int(item_addr(slot) + 12) + (row >> 2) + (one ? 0 : kHalfTokens * (grp >> 1));
+        // PV of the group's last tile has read P and added to O; the item's
+        // first may start O once the first group has read what it holds
+        auto o_ready = [&]() {
+          if (v > 0) return wait(kBarPvDone + w, units - 1);
+          if (held) {
+            held = false;
+            return wait(kBarXFree, xn - 1);
+          }
+          return true;
+        };
+        // (written before the loads that QK waited for)
+        const uint2 note = lds64(sb + kOffMeta + 8u * ((kt0 + first + (one ? 2 * v : v)) % kMeta));
+        if (idle) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarSFree + w));
+          if (!(ok = o_ready())) break;
+        } else {
+          // the whole row of scores, so that QK may overwrite S at once
+          uint32_t x[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, x[q]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) reg_after_wait32(x[q]);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarSFree + w));
+          if (note.y != 0u) {  // columns that this row does not see
+            const uint32_t bad = note.y;
+            const int pos = lds_int(item_addr(slot) + 12) + (row >> 2) + (one ? 0 : kHalfTokens * w);
             const int64_t base = static_cast<int64_t>(note.x) * kKvTokens;
             const int ch = clamp_cols(pos - base) + 1;  // columns [0, ch): t <= pos
             // [cl, ..): t > pos - window; [0, cs): t < sinks
             const int cl = clamp_cols(static_cast<int64_t>(pos) - a.window - base) + 1;
             const int cs = clamp_cols(a.sinks - base);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              vis[q] = bits_between(0, ch - 32 * q) &
-                       (bits_between(cl - 32 * q, 32) | bits_between(0, cs - 32 * q));
-              if ((note.y >> (2 * q)) & 1u) vis[q] &= 0xFFFF0000u;
-              if ((note.y >> (2 * q + 1)) & 1u) vis[q] &= 0x0000FFFFu;
-            }
-          }
-          // 32 scores of the row, those it does not see -inf
-          auto scores = [&](int q, uint32_t (&x)[32]) {
-            tmem_ld32(tS + 32 * q, x);
-            tmem_wait_ld();
-            reg_after_wait32(x);
-            if (note.y != 0u) {
+            for (int q = 0; q < 4; ++q) {
+              uint32_t vis = bits_between(0, ch - 32 * q) &
+                             (bits_between(cl - 32 * q, 32) | bits_between(0, cs - 32 * q));
+              if ((bad >> (2 * q)) & 1u) vis &= 0xFFFF0000u;
+              if ((bad >> (2 * q + 1)) & 1u) vis &= 0x0000FFFFu;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!((vis[q] >> e) & 1u)) x[e] = 0xFF800000u;
+                if (!((vis >> e) & 1u)) x[q][e] = 0xFF800000u;  // -inf
             }
-          };
+          }
           // The reference maximum is set by the first tile a row sees anything
-          // of, and moves only when a tile's weights sum to 2^16 or more (FP32
-          // sums and bf16 weights keep their relative precision below).
-          bool measure = __any_sync(kFull, m_ref == -INFINITY);
-          uint32_t pw[2][16];
+          // of, and moves only when a tile's weights sum to 2^kRescale or more
+          // (FP32 sums and bf16 weights keep their relative precision below).
+          bool ready = false, measure = __any_sync(kFull, m_ref == -INFINITY);
           for (;;) {
+            float alpha = 1.f;
             if (measure) {
-              float mx = -INFINITY;
+              float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                uint32_t x[32];
-                scores(q, x);
+              for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2)
-                  mx = fmax3(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              }
-              const float top = mx * c;
-              float alpha = 1.f;
+                  mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[q][e]),
+                                           __uint_as_float(x[q][e + 1]));
+              const float top = fmaxf(mx[0], mx[1]) * c;
               if (top > m_ref) {
                 alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
                 m_ref = top;
               }
-              // (S is there, so PV of the group's last tile is done)
+              if (!ready) {
+                if (!(ok = o_ready())) break;
+                ready = true;
+                tc_fence_after_sync();
+              }
               if (v > 0 && __any_sync(kFull, alpha != 1.f)) {
                 l_run *= alpha;
 #pragma unroll 1
@@ -823,148 +819,133 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t x[32];
-              scores(q, x);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pw[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                float2 y = ffma2(make_float2(__uint_as_float(x[2 * e]),
-                                             __uint_as_float(x[2 * e + 1])), c2, m2);
+                float2 y = ffma2(make_float2(__uint_as_float(x[q][2 * e]),
+                                             __uint_as_float(x[q][2 * e + 1])), c2, m2);
                 y.x = fast_exp2(y.x);
                 y.y = fast_exp2(y.y);
                 ls[e & 1] = fadd2(ls[e & 1], y);
-                pw[q][e] = pack_bf16x2(y.x, y.y);
+                pw[e] = pack_bf16x2(y.x, y.y);
               }
-              reg_after_wait(pw[q]);  // (keeps the steps' results apart)
+              if (q == 0 && !ready) {
+                if (!(ok = o_ready())) break;
+                ready = true;
+                tc_fence_after_sync();
+              }
+              tmem_st16(tP + 16 * q, pw);
             }
+            if (!ok) break;
             const float2 l2 = fadd2(ls[0], ls[1]);
             const float sum = l2.x + l2.y;
             // (NaN too; a tile that has just been measured stands as it is)
-            if (measure || !__any_sync(kFull, !(sum < kRescale))) {
+            const bool over = !(sum < kRescale);
+            if (measure || !__any_sync(kFull, over)) {
               l_run += sum;
               break;
             }
             measure = true;
           }
-          // P over S
-          tmem_st16(tS, pw[0]);
-          tmem_st16(tS + 16, pw[1]);
+          if (!ok) break;
           tmem_wait_st();
         }
-        // the item's first PV starts O anew: not before what it holds was read
-        if (held) {
-          if (!(ok = wait(kBarXFree + grp, xn - 1))) break;
-          held = false;
-        }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull + grp));
+        if (lane == 0) mbar_arrive(bar(kBarPFull + w));
       }
       if (!ok) break;
-
-      // ---- epilogue: the first group of each row tile takes the other groups'
-      // rows from TMEM (the same lanes) and writes them
       const Item it = read_item(item_addr(slot));
-      ks0 += (it.tiles() + kStageTiles - 1) / kStageTiles;
-      const int lead = one ? 0 : grp & 2, followers = one ? 3 : 1;
-      const int tok = (row >> 2) + (one ? 0 : kHalfTokens * (grp >> 1));
+      kt0 += it.tiles();
+      const int tok = (row >> 2) + (one ? 0 : kHalfTokens * w);
       const int pos = it.pos0 + tok;
-      float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + row;
-      if (nu > 0 && !(ok = wait(kBarPvDone + grp, units - 1))) break;
+
+      // ---- epilogue
+      if (nu > 0 && !(ok = wait(kBarPvDone + w, units - 1))) break;
       tc_fence_after_sync();
-      if (grp != lead) {
-        if (nu > 0) {
-          xml[128 * grp] = make_float2(m_ref, l_run);
+      bool writes = tok < it.nt;
+      const bool other = one && it.units_of(1) > 0;  // both groups saw these rows
+      float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + row;
+      if (one && w == 1) {
+        // the first group takes this one's rows from TMEM (the same lanes)
+        writes = false;
+        if (other) {
+          *xml = make_float2(m_ref, l_run);
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarXFull + grp));
+          if (lane == 0) mbar_arrive(bar(kBarXFull));
           held = true;
-          ++xn;
         }
-      } else {
-        // (the first group of a row tile has units whenever another has)
-        float wt[4] = {1.f, 0.f, 0.f, 0.f};
-        int have = 1;  // groups with rows: the first of the row tile and the next ones
-#pragma unroll
-        for (int f = 1; f < kGroups; ++f)
-          if (f <= followers && it.units_of(lead + f) > 0) {
-            if (!(ok = wait(kBarXFull + lead + f, (xphase >> (lead + f)) & 1u))) break;
-            have = f + 1;
-          }
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (have > 1) {
-          float2 ml[4];
-          float M = m_ref;
-#pragma unroll
-          for (int f = 1; f < kGroups; ++f) {
-            ml[f] = f < have ? xml[128 * (lead + f)] : make_float2(-INFINITY, 0.f);
-            M = fmaxf(M, ml[f].x);
-          }
-          // (a group whose tiles the row did not see: zeros)
-          wt[0] = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
-          l_run *= wt[0];
-#pragma unroll
-          for (int f = 1; f < kGroups; ++f) {
-            wt[f] = ml[f].x == -INFINITY ? 1.f : fast_exp2(ml[f].x - M);
-            l_run = fmaf(ml[f].y, wt[f], l_run);
-          }
-          m_ref = M;
-        }
-        // (written before the last kv tile's V was handed to its PV, which the
-        // groups waited for)
-        const int bad_v = lds_int(item_addr(slot) + 48);
-        if (!idle) {
-          const bool writes = tok < it.nt;
-          const int64_t r =
-              static_cast<int64_t>(it.row0 + tok) * kNumQHeads + it.g * kGroup + (row & 3);
-          const int64_t part = r * a.num_splits + it.split;
-          const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
-          if (a.num_splits > 1 && writes)
-            *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_run);
-#pragma unroll 1
-          for (int q = 0; q < kHeadDim / 16; ++q) {
-            float o[16];
-#pragma unroll
-            for (int f = 0; f < kGroups; ++f)
-              if (f < have) {
-                uint32_t x[16];
-                tmem_ld16(tO + kHeadDim * f + 16 * q, x);
-                tmem_wait_ld();
-                reg_after_wait(x);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  o[e] = f == 0 ? __uint_as_float(x[e]) * wt[0]
-                                : fmaf(__uint_as_float(x[e]), wt[f], o[e]);
-              }
-            if (!writes) continue;
-            if (bad_v != 0) add_nonfinite(a, it, pos, 16 * q, o);
-            if (a.num_splits == 1) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim + 16 * q);
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                    pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                    pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                    pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-            } else if (l_run != 0.f) {
-              float4* dst = reinterpret_cast<float4*>(a.part_acc + part * kHeadDim + 16 * q);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-          }
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0)
-          for (int f = 1; f < have; ++f) mbar_arrive(bar(kBarXFree + lead + f));
       }
+      float w0 = 1.f, w1 = 0.f;
+      if (other && w == 0) {
+        if (!(ok = wait(kBarXFull, xn))) break;
+        tc_fence_after_sync();
+        const float2 ml = *xml;
+        const float M = fmaxf(m_ref, ml.x);
+        // (a group whose tiles the row did not see: zeros)
+        w0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
+        w1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+        l_run = l_run * w0 + ml.y * w1;
+        m_ref = M;
+      }
+      // (written before the last kv tile's V was handed to its PV, which this
+      // row's group, or the other one, has waited for)
+      const int bad_v = *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
+      if (!(one && w == 1) && !idle) {
+        const int64_t r =
+            static_cast<int64_t>(it.row0 + tok) * kNumQHeads + it.g * kGroup + (row & 3);
+        const int64_t part = r * a.num_splits + it.split;
+        const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+        if (a.num_splits > 1 && writes)
+          *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_run);
+#pragma unroll 1
+        for (int q = 0; q < kHeadDim / 16; ++q) {
+          uint32_t x[16];
+          float o[16];
+          if (nu > 0) {
+            tmem_ld16(tO + 16 * q, x);
+            tmem_wait_ld();
+            reg_after_wait(x);
+          } else {
 #pragma unroll
-      for (int f = 1; f < kGroups; ++f)
-        if ((one || (f & 1)) && it.units_of(f) > 0) xphase ^= 1u << f;
+            for (int e = 0; e < 16; ++e) x[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]) * w0;
+          if (other) {
+            tmem_ld16(tO + kHeadDim + 16 * q, x);
+            tmem_wait_ld();
+            reg_after_wait(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), w1, o[e]);
+          }
+          if (!writes) continue;
+          if (bad_v != 0) add_nonfinite(a, it, pos, 16 * q, o);
+          if (a.num_splits == 1) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                  pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                  pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          } else if (l_run != 0.f) {
+            float4* dst = reinterpret_cast<float4*>(a.part_acc + part * kHeadDim + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+      }
+      tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+      if (lane == 0) {
+        if (other && w == 0) mbar_arrive(bar(kBarXFree));
+        mbar_arrive(bar(kBarItemEmpty + slot));
+      }
+      if (other) ++xn;
     }
   }
   if (!ok && lane == 0) record_error(a.dev_err, kErrTimeout);
@@ -996,11 +977,13 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_chunk_kernel(const Mask
   }
   const int o0 = a.token_offsets[lo], o1 = a.token_offsets[lo + 1];
   if (o0 < 0 || o1 > a.num_tokens || tok < o0 || tok >= o1) return;
+  if (o1 - o0 <= kShortTokens) return;  // the other kernel's
+  const int splits = a.num_splits;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.num_splits;
   const float2* acc = reinterpret_cast<const float2*>(a.part_acc) +
                       row * a.num_splits * (kHeadDim / 2) + lane;
   float M = -INFINITY;
-  for (int s = lane; s < a.num_splits; s += 32) {
+  for (int s = lane; s < splits; s += 32) {
     const float2 x = __ldcg(ml + s);
     if (x.y != 0.f) M = fmaxf(M, x.x);
   }
@@ -1008,7 +991,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_chunk_kernel(const Mask
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
   float L = 0.f;
   float2 O = make_float2(0.f, 0.f);
-  for (int s = 0; s < a.num_splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     const float2 x = __ldcg(ml + s);
     if (x.y == 0.f) continue;  // saw no token; its accumulator was not written
     const float wt = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M);  // (-inf: a NaN row)
@@ -1025,8 +1008,13 @@ cudaError_t configure(int device) {
   static std::atomic<unsigned long long> done{0};
   const unsigned long long bit = 1ull << (device & 63);
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t err = cudaFuncSetAttribute(
-      paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaFuncAttributes fa;
+  cudaError_t err = cudaFuncGetAttributes(&fa, paged_chunk_kernel);
+  if (err != cudaSuccess) return err;
+  // the register split must stay within what the block starts with
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  err = cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem);
   if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
   return err;
 }
@@ -1039,9 +1027,11 @@ cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& 
   cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
   if ((err = configure(device)) != cudaSuccess) return err;
-  err = launch_pdl(paged_chunk_kernel, dim3(grid), dim3(kThreads), kSmem, stream, q_map, page_map,
-                   args);
-  if (err != cudaSuccess || args.num_splits == 1) return err;
+  return launch_pdl(paged_chunk_kernel, dim3(grid), dim3(kThreads), kSmem, stream, q_map, page_map,
+                    args);
+}
+
+cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream) {
   static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
   return launch_pdl(merge_chunk_kernel, dim3(args.num_tokens * (kNumQHeads / kMergeRows)),
                     dim3(32 * kMergeRows), 0, stream, args);

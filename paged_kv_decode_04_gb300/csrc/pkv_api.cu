@@ -896,39 +896,6 @@ bool chunk_q_map(const void* q, int num_tokens, CUtensorMap* out) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Ranges and CTAs of a chunk call.  A tile holds up to 64 tokens of one
-// sequence, so there are at most min(tokens, batch + tokens / 64) of them.
-struct ChunkPlan {
-  int num_splits, grid;
-  size_t workspace;
-};
-
-bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks, int num_splits,
-                ChunkPlan* plan) {
-  const long long tiles =
-      std::min<long long>(num_tokens, batch + num_tokens / pkv::kChunkTileTokens);
-  const long long items = tiles * kNumKvHeads;
-  constexpr int kKvPages = pkv::kChunkKvTokens / kPageSize;
-  long long kv = (max_blocks + kKvPages - 1) / kKvPages;  // most kv tiles of an item
-  if (window > 0)
-    kv = std::min(kv, (static_cast<long long>(window) + pkv::kChunkTileTokens - 2) /
-                              pkv::kChunkKvTokens + 2 +
-                          (static_cast<long long>(sinks) + pkv::kChunkKvTokens - 1) /
-                              pkv::kChunkKvTokens);
-  long long s = num_splits;
-  const int sms = current_sm_count();
-  if (s == 0) {
-    if (sms <= 0) return false;
-    s = std::max(1LL, std::min(sms / std::max(items, 1LL), kv / 2));
-  }
-  s = std::min(s, std::max(kv, 1LL));
-  plan->num_splits = static_cast<int>(s);
-  plan->grid = static_cast<int>(std::min<long long>(sms > 0 ? sms : 1, items * s));
-  const size_t parts = static_cast<size_t>(num_tokens) * kNumQHeads * plan->num_splits;
-  plan->workspace = s > 1 ? parts * (kHeadDim + 2) * sizeof(float) : 0;
-  return true;
-}
-
 // Ranges of a one-token call whose sequences see at most `pages` pages, as
 // make_plan chooses them: about four CTAs per SM, eight pages a range or more.
 int one_token_splits(int batch, long long pages, int num_splits) {
@@ -944,6 +911,62 @@ long long window_pages(int max_blocks, int window, int sinks) {
   return std::min<long long>(max_blocks, (static_cast<long long>(window) + kPageSize - 2) / kPageSize +
                                              1 + (static_cast<long long>(sinks) + kPageSize - 1) /
                                                      kPageSize);
+}
+
+// Ranges and CTAs of a chunk call.  Chunks of more than kShortTokens tokens
+// are cut into tiles of up to 64, so there are at most tokens / 64 + the
+// number of such chunks of them.
+struct ChunkPlan {
+  int num_splits, short_splits, grid;  // grid 0: no long chunk is possible
+  size_t long_parts, short_parts;      // rows of partials
+  size_t workspace;
+};
+
+bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks, int num_splits,
+                ChunkPlan* plan) {
+  const long long chunks = std::min(batch, num_tokens / (pkv::kShortTokens + 1));
+  const long long items =
+      chunks > 0 ? (num_tokens / pkv::kChunkTileTokens + chunks) * kNumKvHeads : 0;
+  constexpr int kKvPages = pkv::kChunkKvTokens / kPageSize;
+  long long kv = (max_blocks + kKvPages - 1) / kKvPages;  // most kv tiles of an item
+  long long pages = max_blocks;                           // most pages of a short chunk
+  if (window > 0) {
+    kv = std::min(kv, (static_cast<long long>(window) + pkv::kChunkTileTokens - 2) /
+                              pkv::kChunkKvTokens + 2 +
+                          (static_cast<long long>(sinks) + pkv::kChunkKvTokens - 1) /
+                              pkv::kChunkKvTokens);
+    pages = window_pages(max_blocks, static_cast<int>(std::min<long long>(
+                                         static_cast<long long>(window) + pkv::kShortTokens - 1,
+                                         INT32_MAX)), sinks);
+  }
+  const int sms = current_sm_count();
+  long long s = num_splits;
+  if (s == 0) {
+    if (sms <= 0) return false;
+    s = std::max(1LL, std::min(sms / std::max(items, 1LL), kv / 8));
+  }
+  s = std::min(s, std::max(kv, 1LL));
+  plan->num_splits = static_cast<int>(items > 0 ? s : 1);
+  // short chunks: one wave of three CTAs per SM, eight pages a range or more;
+  // more tokens than short chunks of this batch can have mean a long one
+  long long t = num_splits;
+  if (t == 0) {
+    const long long most = num_tokens > pkv::kShortTokens * static_cast<long long>(batch)
+                               ? std::max(batch - 1, 1)
+                               : std::min(batch, num_tokens);
+    t = std::max(1LL, std::min(3LL * sms / (most * kNumKvHeads), (pages + 7) / 8));
+    if (num_tokens > pkv::kShortTokens && batch == 1) t = 1;
+  }
+  plan->short_splits = static_cast<int>(std::min(t, pages));
+  plan->grid = static_cast<int>(std::min<long long>(sms > 0 ? sms : 1, items * s));
+  plan->long_parts = plan->num_splits > 1
+                         ? static_cast<size_t>(num_tokens) * kNumQHeads * plan->num_splits
+                         : 0;
+  plan->short_parts = plan->short_splits > 1 ? static_cast<size_t>(batch) * pkv::kShortTokens *
+                                                   kNumQHeads * plan->short_splits
+                                             : 0;
+  plan->workspace = (plan->long_parts + plan->short_parts) * (kHeadDim + 2) * sizeof(float);
+  return true;
 }
 
 size_t part_bytes(int batch, int splits) {
@@ -1047,18 +1070,25 @@ PKV_API int pkv_paged_chunk_attention(
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
   a.num_splits = plan.num_splits;
-  if (plan.workspace > 0) {
-    a.part_acc = static_cast<float*>(workspace);
-    a.part_ml = a.part_acc + static_cast<size_t>(num_tokens) * kNumQHeads * plan.num_splits * kHeadDim;
-  }
+  a.short_splits = plan.short_splits;
+  // partials: accumulators of the long and of the short chunks, then the
+  // (max, sum) pairs
+  a.part_acc = static_cast<float*>(workspace);
+  a.short_acc = a.part_acc + plan.long_parts * kHeadDim;
+  a.part_ml = a.short_acc + plan.short_parts * kHeadDim;
+  a.short_ml = a.part_ml + plan.long_parts * 2;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  CUtensorMap q_map, page_map;
+  CUtensorMap q_map, page_map, pool_map;
   if (!chunk_q_map(q, num_tokens, &q_map) ||
-      !pool_tensor_map(pool, num_pages, &page_map, kPageSize))
+      !pool_tensor_map(pool, num_pages, &page_map, kPageSize) ||
+      !pool_tensor_map(pool, num_pages, &pool_map))
     return PKV_ECUDA;
-  const cudaError_t err = pkv::launch_chunk_attention(q_map, page_map, a, plan.grid,
-                                                      reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
+  if (plan.grid > 0) err = pkv::launch_chunk_attention(q_map, page_map, a, plan.grid, st);
+  if (err == cudaSuccess) err = pkv::launch_short_chunks(pool_map, a, plan.grid > 0, st);
+  if (err == cudaSuccess && plan.grid > 0 && a.num_splits > 1) err = pkv::launch_chunk_merge(a, st);
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

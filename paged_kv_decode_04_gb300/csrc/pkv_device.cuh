@@ -267,6 +267,12 @@ __device__ __forceinline__ uint16_t float_to_bf16_rne(float f) {
   return static_cast<uint16_t>(u >> 16);
 }
 
+// bf16 pair: mask of the halves that are not finite.
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
+  return ((w & 0x00007F80u) == 0x00007F80u ? 0x0000FFFFu : 0u) |
+         ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
 // Two floats -> packed bf16 pair (lo in the low half), each rounded to
 // nearest even by the conversion instruction.
 __device__ __forceinline__ uint32_t cvt_bf16x2_rn(float lo, float hi) {

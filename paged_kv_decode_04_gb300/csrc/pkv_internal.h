@@ -271,7 +271,10 @@ struct MaskedArgs {
   int num_tokens;
   int window;
   int sinks;
-  int num_splits;
+  int num_splits;                // ranges of a row (chunks: of long chunks)
+  int short_splits;              // chunks: ranges of chunks of at most kShortTokens
+  float* short_acc;              // partials of the short chunks, [batch][kShortTokens * 32 rows]
+  float* short_ml;               // [short_splits]
   float scale_log2;              // softmax scale * log2(e)
   unsigned long long wait_ns;
 };
@@ -279,13 +282,22 @@ struct MaskedArgs {
 // Tiles of the chunk kernel: new tokens (all 4 query heads of a kv head) and
 // cached tokens.
 constexpr int kChunkTileTokens = 64;
-constexpr int kChunkKvTokens = 64;
+constexpr int kChunkKvTokens = 128;
+// Chunks of up to this many tokens go to short_chunk.cu's kernel.
+constexpr int kShortTokens = 4;
 
-// grid persistent CTAs (at most one per SM), then the merge of the ranges.
+// Chunks of more than kShortTokens tokens: grid persistent CTAs (at most one
+// per SM).
 // q_map: q as [num_tokens][32][64], boxes of 32 tokens and 4 heads, 128-byte
 // swizzled; page_map: boxes of one page's K (or V) rows of one head.
 cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& page_map,
                                    const MaskedArgs& args, int grid, cudaStream_t stream);
+// The other chunks, and the merge of their ranges when short_splits > 1;
+// beside: right after launch_chunk_attention, next to whose CTAs these run.
+cudaError_t launch_short_chunks(const CUtensorMap& pool_map, const MaskedArgs& args, bool beside,
+                                cudaStream_t stream);
+// Combine the ranges of the long chunks' rows (num_splits > 1).
+cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream);
 
 // One-token attention under a window, or with the weights added to args.mass
 // (no window then), and the merge of the ranges when args.num_splits > 1.

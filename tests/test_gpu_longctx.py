@@ -46,7 +46,8 @@ def run_chunk(lens, counts, window=0, sinks=0, *, splits=0, seed=1, pad=0, cache
 @pytest.mark.parametrize("lens,counts", [
     ([1], [1]), ([17], [17]), ([16], [1]), ([129], [128]), ([515], [5]), ([300], [300]),
     ([40, 3, 131], [5, 3, 1]), ([33, 7, 64, 5], [0, 7, 0, 1]), ([700, 64, 200], [130, 64, 33]),
-    ([1100], [1]), ([257, 256, 255, 1], [9, 65, 31, 1]),
+    ([1100], [1]), ([257, 256, 255, 1], [9, 65, 31, 1]), ([4], [4]), ([5], [5]),
+    ([500, 499, 17, 1300], [2, 3, 4, 1]),
 ])
 def test_chunk_causal(lens, counts, splits):
     assert run_chunk(lens, counts, splits=splits, pad=2) == 0
@@ -67,15 +68,39 @@ def test_chunk_window(window, sinks, splits):
     ([100] * 70, [2] * 70, 0), ([1 + i for i in range(64)], [1] * 64, 0),
     ([90 + 20 * i for i in range(40)], [1 + (i * 29) % 80 for i in range(40)], 0),
     ([200 + 7 * (i % 5) for i in range(45)], [(0, 1, 33, 64, 70)[i % 5] for i in range(45)], 60),
+    ([8 + (i * 61) % 300 for i in range(90)], [1 + i % 4 if i % 9 else 5 for i in range(90)], 40),
 ])
 def test_chunk_many_items(lens, counts, window, splits):
     assert run_chunk(lens, counts, window, 3 if window else 0, splits=splits) == 0
 
 
-def test_chunk_scales():
+@pytest.mark.parametrize("counts", [[70], [4]])
+def test_chunk_scales(counts):
     # flat weights, and weights that all fall on a few tokens
-    run_chunk([400], [70], scale=2.0 ** -20)
-    run_chunk([400], [70], scale=2.0)
+    run_chunk([400], counts, scale=2.0 ** -20)
+    run_chunk([400], counts, scale=2.0)
+
+
+@pytest.mark.parametrize("counts,splits", [([90], 1), ([90], 2), ([20], 1), ([3], 1), ([3], 3)])
+@pytest.mark.parametrize("shape", ["rising", "falling", "steps"])
+def test_chunk_scores_that_ramp(counts, splits, shape):
+    """Scores that rise or fall by hundreds over the cache: the reference
+    maximum moves in every tile, or never after the first."""
+    lens = [700]
+    pool, bt = make_cache(lens, seed=25)
+    t = np.arange(700)
+    ramp = {"rising": t / 2.0, "falling": -t / 2.0, "steps": (t // 150) * 90.0 % 270}[shape]
+    for tok in range(700):
+        # dim 0 of the keys, against queries of 1 there
+        pool[int(bt[0, tok // P]), 0, tok % P, :, 0] = float(ramp[tok])
+    off = offsets(counts)
+    q = normal((counts[0], HQ, 64), 26)
+    q[..., 0] = 1.0
+    dev, b = cuda_or_skip(), binding()
+    out = b.paged_chunk_attention(q.to(dev), off.to(dev), pool.to(dev), bt.to(dev),
+                                  lens_t(lens).to(dev), scale=0.5, num_splits=splits)
+    want, tol = chunk_reference(q, off, pool, bt, lens, 0, 0, torch.zeros_like(q), 0.5)
+    check(out, want, tol, shape)
 
 
 @pytest.mark.parametrize("splits", [1, 4])
@@ -190,6 +215,34 @@ def test_chunk_repeats_bit_for_bit_and_replays():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, b.paged_chunk_attention(q2, *args, num_splits=3, workspace=ws))
+
+
+def test_waits_that_run_out():
+    """With a wait limit of 0 every kernel gives up at its first look, reports
+    it, and leaves the stream and the next calls as they should be."""
+    dev, b = cuda_or_skip(), binding()
+    lens, counts = [900, 70, 1500, 333], [3, 70, 200, 1]
+    pool, bt = (x.to(dev) for x in make_cache(lens, seed=19))
+    off, ln = offsets(counts).to(dev), lens_t(lens).to(dev)
+    q = normal((sum(counts), HQ, 64), 20).to(dev)
+    mass = torch.zeros((4, HKV, bt.shape[1] * P), device=dev)
+    calls = [lambda e: b.paged_chunk_attention(q, off, pool, bt, ln, dev_err=e),
+             lambda e: b.paged_chunk_attention(q, off, pool, bt, ln, num_splits=3, dev_err=e),
+             lambda e: b.paged_window_attention(q[:4], pool, bt, ln, 500, dev_err=e),
+             lambda e: b.paged_scored_attention(q[:4], pool, bt, ln, mass.zero_(), dev_err=e)]
+    for call in calls:
+        want = call(None)
+        old = b.set_wait_limit_ns(0)
+        err = dev_err(dev)
+        try:
+            call(err)
+        finally:
+            b.set_wait_limit_ns(old)
+        torch.cuda.synchronize()
+        assert int(err.item()) & 8
+        assert not torch.isnan(mass).any()
+        err = dev_err(dev)
+        assert torch.equal(want, call(err)) and int(err.item()) == 0
 
 
 def test_calls_on_another_stream():
