@@ -17,7 +17,9 @@
 // rows) and wants many CTAs, the selection reads 4 bytes a token and is short:
 // so a (sequence, kv head) gets several CTAs, each of which repeats the
 // selection and copies its own part of the kept rows -- one launch, and no
-// CTA waits for another.
+// CTA waits for another.  64 sequences of 4096 tokens down to 1024 (279 MB)
+// took 65 us, 4.3 TB/s, 58 us on the device; about 12 us of it are the
+// selection, in which every CTA of the one wave is at once.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -32,15 +34,23 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;
-constexpr int kWarps = kThreads / 32;
+// Tables of up to kManyTokens tokens: CTAs of 256 threads, four to an SM.
+// Longer ones: CTAs of 1024 threads (the selection is the longer part), one to
+// an SM; up to kSmemTokens the keys stay in shared memory, beyond it every
+// pass reads the weights again (from L2).  One sequence of 32768 tokens took
+// 119 us with small CTAs, 29.5 us with large ones.
+constexpr int kManyTokens = 8192, kSmemTokens = 49152;
+template <bool kMany>
+struct Shape {
+  static constexpr int kThreads = kMany ? 1024 : 256;
+  static constexpr int kCtas = kMany ? 1 : 4;
+};
 constexpr int kBins = 2048;
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// Tables up to this many tokens keep the keys in shared memory; longer ones
-// read the weights again (from L2) in every pass.
-constexpr int kSmemTokens = 8192;
-constexpr int kCopyRows = 4;  // tokens whose rows a group of 8 lanes has in flight
+constexpr int kLoads = 8;  // weights a thread has in flight
+// Tokens whose rows a group of 8 lanes has in flight (two: 65.4 us on the batch
+// above, three 65.0, four spill registers: 71.3; 512 threads and two CTAs 77.7).
+constexpr int kCopyRows = 3;
 
 // Order-preserving key of a weight.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -49,8 +59,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <bool kSmemKeys>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_evict_kernel(const EvictArgs a) {
+template <bool kMany, bool kSmemKeys>
+__global__ void __launch_bounds__(Shape<kMany>::kThreads, Shape<kMany>::kCtas)
+    kv_evict_kernel(const EvictArgs a) {
+  constexpr int kThreads = Shape<kMany>::kThreads, kWarps = kThreads / 32;
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) int s_hist[kBins];
   __shared__ int s_above[kWarps], s_eq[kWarps], s_gt[kWarps];
@@ -88,9 +100,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_evict_kernel(const Ev
   } else {
     // tokens [lo, hi) compete; the others stay
     const int lo = a.sinks, hi = L - a.recent;
-    if (kSmemKeys) {
-      for (int t = lo + tid; t < hi; t += kThreads) s_keys[t] = weight_key(mass[t]);
-    }
+    // this thread's share of the competing tokens' keys
+    auto each_key = [&](auto&& f) {
+      for (int t0 = lo + tid; t0 < hi; t0 += kLoads * kThreads) {
+        float v[kLoads];
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int t = t0 + e * kThreads;
+          v[e] = t < hi ? mass[t] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int t = t0 + e * kThreads;
+          if (t < hi) f(t, weight_key(v[e]));
+        }
+      }
+    };
+    if (kSmemKeys) each_key([&](int t, uint32_t k) { s_keys[t] = k; });
     auto key = [&](int t) { return kSmemKeys ? s_keys[t] : weight_key(mass[t]); };
     uint32_t prefix = 0;
     int need = a.budget - a.sinks - a.recent;
@@ -100,24 +126,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_evict_kernel(const Ev
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
       const uint32_t high = pass == 0 ? 0u : (pass == 1 ? ~0u << 21 : ~0u << 10);
       constexpr int kMine = kBins / kThreads;  // consecutive counters of one thread
-      int4* mine = reinterpret_cast<int4*>(s_hist + tid * kMine);
+      int2* mine = reinterpret_cast<int2*>(s_hist + tid * kMine);
 #pragma unroll
-      for (int e = 0; e < kMine / 4; ++e) mine[e] = make_int4(0, 0, 0, 0);
+      for (int e = 0; e < kMine / 2; ++e) mine[e] = make_int2(0, 0);
       __syncthreads();
-      for (int t = lo + tid; t < hi; t += kThreads) {
-        const uint32_t k = key(t);
+      auto count = [&](int, uint32_t k) {
         if ((k & high) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+      };
+      if (kSmemKeys) {
+        for (int t = lo + tid; t < hi; t += kThreads) count(t, s_keys[t]);
+      } else {
+        each_key(count);
       }
       __syncthreads();
       // from the highest digit down, the first whose running count reaches need
       int h[kMine], sum = 0;
 #pragma unroll
-      for (int e = 0; e < kMine / 4; ++e) {
-        const int4 v = mine[e];
-        h[4 * e] = v.x;
-        h[4 * e + 1] = v.y;
-        h[4 * e + 2] = v.z;
-        h[4 * e + 3] = v.w;
+      for (int e = 0; e < kMine / 2; ++e) {
+        const int2 v = mine[e];
+        h[2 * e] = v.x;
+        h[2 * e + 1] = v.y;
       }
 #pragma unroll
       for (int e = 0; e < kMine; ++e) sum += h[e];
@@ -150,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_evict_kernel(const Ev
     const int span = ((L + kWarps - 1) / kWarps + 31) & ~31;
     const int t0 = min(warp * span, L), t1 = min(t0 + span, L);
     int eq = 0, gt = 0;
+#pragma unroll 4
     for (int t = t0 + lane; t < t1; t += 32) {
       const bool contest = t >= lo && t < hi;
       const uint32_t k = contest ? key(t) : 0xFFFFFFFFu;
@@ -247,19 +276,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_evict_kernel(const Ev
   }
 }
 
+template <bool kMany, bool kSmemKeys>
+cudaError_t launch(const EvictArgs& args, int num_sms, cudaStream_t stream) {
+  using Sh = Shape<kMany>;
+  const int64_t tokens = static_cast<int64_t>(args.max_blocks) * kPageSize;
+  const size_t smem = kSmemKeys ? tokens * sizeof(uint32_t) : 0;
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = 1ull << (device & 63);
+  if (kSmemKeys && !(done.load(std::memory_order_acquire) & bit)) {
+    err = cudaFuncSetAttribute(
+        kv_evict_kernel<kMany, kSmemKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (kMany ? kSmemTokens : kManyTokens) * static_cast<int>(sizeof(uint32_t)));
+    if (err != cudaSuccess) return err;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  // one wave of CTAs, at least 64 kept rows each
+  const long long units = static_cast<long long>(args.batch) * kNumKvHeads;
+  const long long parts = std::max(1LL, std::min(static_cast<long long>(Sh::kCtas) * num_sms / units,
+                                                 (args.budget + 63LL) / 64));
+  return launch_pdl(kv_evict_kernel<kMany, kSmemKeys>,
+                    dim3(static_cast<unsigned>(kNumKvHeads * parts), args.batch),
+                    dim3(Sh::kThreads), smem, stream, args);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& args, int num_sms, cudaStream_t stream) {
-  // one wave of CTAs, at least 64 kept rows each
-  const long long units = static_cast<long long>(args.batch) * kNumKvHeads;
-  const long long parts = std::max(
-      1LL, std::min(static_cast<long long>(kCtasPerSm) * num_sms / units, (args.budget + 63LL) / 64));
-  const dim3 grid(static_cast<unsigned>(kNumKvHeads * parts), args.batch);
   const int64_t tokens = static_cast<int64_t>(args.max_blocks) * kPageSize;
-  return tokens <= kSmemTokens
-             ? launch_pdl(kv_evict_kernel<true>, grid, dim3(kThreads), tokens * sizeof(uint32_t),
-                          stream, args)
-             : launch_pdl(kv_evict_kernel<false>, grid, dim3(kThreads), 0, stream, args);
+  if (tokens <= kManyTokens) return launch<false, true>(args, num_sms, stream);
+  return tokens <= kSmemTokens ? launch<true, true>(args, num_sms, stream)
+                               : launch<true, false>(args, num_sms, stream);
 }
 
 }  // namespace pkv

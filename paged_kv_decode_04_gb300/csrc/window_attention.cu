@@ -32,20 +32,35 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;  // tiles in flight per warp
-constexpr int kRingBytes = kWarps * kStages * kTileBytes;
+// Warps of a CTA, tiles in flight per warp and CTAs per SM of the instances.
+// The scores of 2048 tokens take 32 KiB, so with weights two CTAs share an SM,
+// and eight warps each with rings of two keep as many bytes in flight as four
+// CTAs of four warps do without: 128 sequences of 2048 took 72.7 us (5.8 TB/s),
+// with four warps and rings of four 80.5 us, with one CTA of eight warps and
+// rings of three 85 us, with the scores in the workspace and three CTAs 86 us.
+// Without weights 256 sequences of 1004 visible tokens took 86.5 us (6.1 TB/s,
+// 90 % of the measured copy rate), with three CTAs of rings of four 87.4 us.
+template <bool kScored>
+struct Shape {
+  static constexpr int kWarps = kScored ? 8 : 4;
+  static constexpr int kStages = kScored ? 2 : 3;
+  static constexpr int kCtas = kScored ? 2 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRingBytes = kWarps * kStages * kTileBytes;
+};
+constexpr int kMergeThreads = 32 * kGroup;  // one warp per query row of a kv head
 constexpr int kPageScoreBytes = kPageSize * kGroup * 4;
 constexpr int kMassTokens = 1024;  // tokens of one CTA of merge_scored_kernel
 
-__host__ __device__ constexpr size_t win_smem(int score_pages) {
-  return 1024 /* alignment slack */ + kRingBytes + 8 * kWarps * kStages +
+template <bool kScored>
+constexpr size_t win_smem(int score_pages) {
+  using Sh = Shape<kScored>;
+  static_assert(Sh::kWarps * (2 * kGroup + kGroup * kHeadDim) * 4 <= Sh::kRingBytes,
+                "end-of-CTA merge scratch must fit in the ring");
+  static_assert(Sh::kWarps >= kGroup, "a warp for each query row");
+  return 1024 /* alignment slack */ + Sh::kRingBytes + 8 * Sh::kWarps * Sh::kStages +
          static_cast<size_t>(score_pages) * kPageScoreBytes;
 }
-
-static_assert(kWarps * (2 * kGroup + kGroup * kHeadDim) * 4 <= kRingBytes,
-              "end-of-CTA merge scratch must fit in the ring");
 
 // The list of pages a query at position L - 1 sees.
 struct Visible {
@@ -79,8 +94,10 @@ __device__ __forceinline__ int clamped_len(const MaskedArgs& a, int b, bool repo
 }
 
 template <bool kScored>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(Shape<kScored>::kThreads, Shape<kScored>::kCtas)
     paged_window_kernel(const __grid_constant__ CUtensorMap pool_map, const MaskedArgs a) {
+  constexpr int kWarps = Shape<kScored>::kWarps, kStages = Shape<kScored>::kStages;
+  constexpr int kThreads = Shape<kScored>::kThreads, kRingBytes = Shape<kScored>::kRingBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -231,36 +248,39 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   __syncthreads();
 
-  const int r = warp;  // 4 warps <-> 4 query rows
-  float M = -INFINITY;
+  const int r = warp;  // the first 4 warps <-> 4 query rows
+  float M = -INFINITY, inv = 0.f;
+  if (r < kGroup) {
 #pragma unroll
-  for (int x = 0; x < kWarps; ++x) M = fmaxf(M, sm_m[x * kGroup + r]);
-  float Ls = 0.f;
-  float2 O = make_float2(0.f, 0.f);
+    for (int x = 0; x < kWarps; ++x) M = fmaxf(M, sm_m[x * kGroup + r]);
+    float Ls = 0.f;
+    float2 O = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int x = 0; x < kWarps; ++x) {
-    const float ms = sm_m[x * kGroup + r];
-    const float ls = sm_l[x * kGroup + r];
-    if (ls == 0.f) continue;  // saw no token
-    const float wt = ms == -INFINITY ? 1.f : fast_exp2(ms - M);  // (-inf: a NaN row)
-    Ls += ls * wt;
-    const float2 os =
-        *reinterpret_cast<const float2*>(sm_o + (x * kGroup + r) * kHeadDim + 2 * lane);
-    O.x = fmaf(wt, os.x, O.x);
-    O.y = fmaf(wt, os.y, O.y);
+    for (int x = 0; x < kWarps; ++x) {
+      const float ms = sm_m[x * kGroup + r];
+      const float ls = sm_l[x * kGroup + r];
+      if (ls == 0.f) continue;  // saw no token
+      const float wt = ms == -INFINITY ? 1.f : fast_exp2(ms - M);  // (-inf: a NaN row)
+      Ls += ls * wt;
+      const float2 os =
+          *reinterpret_cast<const float2*>(sm_o + (x * kGroup + r) * kHeadDim + 2 * lane);
+      O.x = fmaf(wt, os.x, O.x);
+      O.y = fmaf(wt, os.y, O.y);
+    }
+    const int64_t row = static_cast<int64_t>(b) * kNumQHeads + g * kGroup + r;
+    if (a.num_splits > 1) {
+      const int64_t part = row * a.num_splits + split;
+      *reinterpret_cast<float2*>(a.part_acc + part * kHeadDim + 2 * lane) = O;
+      if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(M, Ls);
+    } else {
+      inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+      reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
+    }
   }
-  const int64_t row = static_cast<int64_t>(b) * kNumQHeads + g * kGroup + r;
-  if (a.num_splits > 1) {
-    const int64_t part = row * a.num_splits + split;
-    *reinterpret_cast<float2*>(a.part_acc + part * kHeadDim + 2 * lane) = O;
-    if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(M, Ls);
-    return;
-  }
-  const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
+  if (a.num_splits > 1) return;
   if constexpr (kScored) {
     __syncthreads();  // the states have been read
-    if (lane == 0) {
+    if (lane == 0 && r < kGroup) {
       sm_m[r] = M == -INFINITY ? 0.f : M;
       sm_l[r] = inv;
     }
@@ -316,7 +336,7 @@ __device__ __forceinline__ void merge_out(const MaskedArgs& a, int64_t row, floa
 }
 
 // grid (8 kv heads, batch), one warp per query row of the head.
-__global__ void __launch_bounds__(kThreads) merge_window_kernel(const MaskedArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) merge_window_kernel(const MaskedArgs a) {
   allow_dependent_grids();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31;
@@ -328,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) merge_window_kernel(const MaskedArgs
 // grid (8 kv heads x pieces of kMassTokens tokens, batch): every piece works
 // out the rows' statistics, the first writes the output, and each adds its
 // tokens' weights.
-__global__ void __launch_bounds__(kThreads) merge_scored_kernel(const MaskedArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) merge_scored_kernel(const MaskedArgs a) {
   __shared__ float s_m[kGroup], s_inv[kGroup];
   allow_dependent_grids();
   wait_for_prior_grids();
@@ -349,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) merge_scored_kernel(const MaskedArgs
   float* mass = a.mass + bg * a.mass_stride;
   const float c = a.scale_log2;
   const int end = min(L, (piece + 1) * kMassTokens);
-  for (int t = piece * kMassTokens + threadIdx.x; t < end; t += kThreads) {
+  for (int t = piece * kMassTokens + threadIdx.x; t < end; t += kMergeThreads) {
     const float4 x = __ldcg(scores + t);
     mass[t] += (fast_exp2(fmaf(x.x, c, -s_m[0])) * s_inv[0] +
                 fast_exp2(fmaf(x.y, c, -s_m[1])) * s_inv[1]) +
@@ -366,7 +386,7 @@ cudaError_t configure(int device) {
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
   const cudaError_t err = cudaFuncSetAttribute(
       paged_window_kernel<kScored>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(win_smem(kScored ? kScoredSmemPages : 0)));
+      static_cast<int>(win_smem<kScored>(kScored ? kScoredSmemPages : 0)));
   if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
   return err;
 }
@@ -382,17 +402,17 @@ cudaError_t launch_window_attention(const CUtensorMap& pool_map, const MaskedArg
   err = scored ? configure<true>(device) : configure<false>(device);
   if (err != cudaSuccess) return err;
   const dim3 grid(kNumKvHeads * args.num_splits, args.batch);
-  err = scored ? launch_pdl(paged_window_kernel<true>, grid, dim3(kThreads), win_smem(score_pages),
-                            stream, pool_map, args)
-               : launch_pdl(paged_window_kernel<false>, grid, dim3(kThreads), win_smem(0), stream,
-                            pool_map, args);
+  err = scored ? launch_pdl(paged_window_kernel<true>, grid, dim3(Shape<true>::kThreads),
+                            win_smem<true>(score_pages), stream, pool_map, args)
+               : launch_pdl(paged_window_kernel<false>, grid, dim3(Shape<false>::kThreads),
+                            win_smem<false>(0), stream, pool_map, args);
   if (err != cudaSuccess || args.num_splits == 1) return err;
   if (!scored)
-    return launch_pdl(merge_window_kernel, dim3(kNumKvHeads, args.batch), dim3(kThreads), 0, stream,
-                      args);
+    return launch_pdl(merge_window_kernel, dim3(kNumKvHeads, args.batch), dim3(kMergeThreads), 0,
+                      stream, args);
   const int pieces = (args.max_blocks * kPageSize + kMassTokens - 1) / kMassTokens;
-  return launch_pdl(merge_scored_kernel, dim3(kNumKvHeads * pieces, args.batch), dim3(kThreads), 0,
-                    stream, args);
+  return launch_pdl(merge_scored_kernel, dim3(kNumKvHeads * pieces, args.batch), dim3(kMergeThreads),
+                    0, stream, args);
 }
 
 }  // namespace pkv

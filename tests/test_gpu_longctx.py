@@ -376,11 +376,11 @@ def evict_reference(mass, n, budget, sinks, recent):
     return kept
 
 
-def run_evict(lens, budget, sinks, recent, mass=None, seed=41, extra=1):
+def run_evict(lens, budget, sinks, recent, mass=None, seed=41, extra=1, width=None):
     dev, b = cuda_or_skip(), binding()
     B = len(lens)
     wide = -(-budget // P) + extra
-    pool, bt = make_cache(lens, seed=seed, spare=B * wide + 2)
+    pool, bt = make_cache(lens, seed=seed, spare=B * wide + 2, width=width)
     free = sorted(set(range(pool.shape[0])) - set(bt[bt >= 0].tolist()))
     dst = torch.tensor(np.random.default_rng(seed).permutation(free)[:B * wide].reshape(B, wide),
                        dtype=torch.int32)
@@ -420,6 +420,12 @@ def test_evict(budget, sinks, recent):
 
 def test_evict_long():
     run_evict([20011, 5000], 1000, 4, 200)
+
+
+@pytest.mark.parametrize("width", [512, 513, 3100, 4000])
+def test_evict_wide_tables(width):
+    # tables of 8192 and of 49152 tokens and more select with other kernels
+    run_evict([700, 1, 300, 64], 100, 4, 16, width=width)
 
 
 def test_evict_values_at_their_limits():
