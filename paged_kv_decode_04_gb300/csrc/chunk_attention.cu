@@ -101,7 +101,9 @@ constexpr uint32_t kIdescPV = tc_idesc_bf16(128, kHeadDim, true);
 constexpr int kOffQ = 0;                               // [2 items][2 row tiles]
 constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
 constexpr int kOffV = kOffK + kStages * kRowTileBytes;
-constexpr int kOffMl = kOffV + kStages * kRowTileBytes;  // [128] (m, l) handed between groups
+constexpr int kOffOut = kOffV + kStages * kRowTileBytes;  // [warp][32 rows] of 128 B
+constexpr int kOutBytes = 32 * 128;
+constexpr int kOffMl = kOffOut + kSoftmaxWarps * kOutBytes;  // [128] (m, l) handed between groups
 constexpr int kOffItems = kOffMl + 128 * 8;
 constexpr int kItemWords = 16;
 constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
@@ -894,12 +896,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       // row's group, or the other one, has waited for)
       const int bad_v = *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
       if (!(one && w == 1) && !idle) {
-        const int64_t r =
-            static_cast<int64_t>(it.row0 + tok) * kNumQHeads + it.g * kGroup + (row & 3);
-        const int64_t part = r * a.num_splits + it.split;
+        const int tok0 = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w);  // the warp's first
+        const int64_t r0 = static_cast<int64_t>(it.row0 + tok0) * kNumQHeads + it.g * kGroup;
+        const uint32_t stage = sb + kOffOut + warp * kOutBytes + lane * 128;
+        // 128 B of each of the warp's rows, staged in shared memory (16-byte
+        // pieces swizzled by the row), to base + row of the output x stride:
+        // whole rows to a store instruction
+        auto write_rows = [&](void* base, int64_t stride) {
+          __syncwarp();
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const int y = 4 * t + (lane >> 3);
+            const uint4 v = lds128(sb + kOffOut + warp * kOutBytes + y * 128 +
+                                   (((lane ^ y) & 7) << 4));
+            if (tok0 + t < it.nt)
+              *reinterpret_cast<uint4*>(static_cast<char*>(base) +
+                                        (t * kNumQHeads + (lane >> 3)) * stride +
+                                        16 * (lane & 7)) = v;
+          }
+          __syncwarp();
+        };
         const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
         if (a.num_splits > 1 && writes)
-          *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_run);
+          *reinterpret_cast<float2*>(
+              a.part_ml +
+              2 * ((r0 + (tok - tok0) * kNumQHeads + (row & 3)) * a.num_splits + it.split)) =
+              make_float2(m_ref, l_run);
 #pragma unroll 1
         for (int q = 0; q < kHeadDim / 16; ++q) {
           uint32_t x[16];
@@ -921,21 +943,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), w1, o[e]);
           }
-          if (!writes) continue;
-          if (bad_v != 0) add_nonfinite(a, it, pos, 16 * q, o);
+          if (bad_v != 0 && writes) add_nonfinite(a, it, pos, 16 * q, o);
           if (a.num_splits == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim + 16 * q);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                  pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                  pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-          } else if (l_run != 0.f) {
-            float4* dst = reinterpret_cast<float4*>(a.part_acc + part * kHeadDim + 16 * q);
+              sts128(stage + (((2 * q + e) ^ (lane & 7)) << 4),
+                     pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                     pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                     pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                     pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            if (q == 3) write_rows(a.out + r0 * kHeadDim, kHeadDim * 2);
+          } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              sts128(stage + (((4 * (q & 1) + e) ^ (lane & 7)) << 4),
+                     __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                     __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+            if (q & 1)
+              write_rows(a.part_acc + (r0 * a.num_splits + it.split) * kHeadDim + 32 * (q >> 1),
+                         static_cast<int64_t>(a.num_splits) * kHeadDim * 4);
           }
         }
       }
