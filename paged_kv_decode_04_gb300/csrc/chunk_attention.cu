@@ -86,8 +86,8 @@ constexpr int kAhead = 3;                     // items published before the rela
 constexpr int kSoftmaxWarps = 8;
 constexpr int kQkWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11 issues PV
 constexpr int kThreads = 32 * 12;
-// Registers: 168 x 384 threads at launch = 64512 = 256 x 216 + 128 x 72.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+// Registers: 168 x 384 threads at launch = 64512 = 256 x 200 + 128 x 104.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads,
               "the split stays within the registers the block starts with");
 constexpr float kRescale = 65536.f;  // 2^16
@@ -207,6 +207,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       "%28, %29, %30, %31}, [%32];"
       : PKV_R16(r, 0), PKV_R16(r, 16)
       : "r"(taddr)
+      : "memory");
+}
+#define PKV_I16(r, i)                                                                       \
+  "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+      "r"(r[i + 6]), "r"(r[i + 7]), "r"(r[i + 8]), "r"(r[i + 9]), "r"(r[i + 10]),      \
+      "r"(r[i + 11]), "r"(r[i + 12]), "r"(r[i + 13]), "r"(r[i + 14]), "r"(r[i + 15])
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(taddr), PKV_I16(r, 0), PKV_I16(r, 16)
       : "memory");
 }
 #undef PKV_R16
@@ -780,7 +791,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           // The reference maximum is set by the first tile a row sees anything
           // of, and moves only when a tile's weights sum to 2^kRescale or more
           // (FP32 sums and bf16 weights keep their relative precision below).
-          bool ready = false, measure = __any_sync(kFull, m_ref == -INFINITY);
+          bool measure = __any_sync(kFull, m_ref == -INFINITY);
+          if (!(ok = o_ready())) break;
+          tc_fence_after_sync();
           for (;;) {
             float alpha = 1.f;
             if (measure) {
@@ -795,11 +808,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
               if (top > m_ref) {
                 alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
                 m_ref = top;
-              }
-              if (!ready) {
-                if (!(ok = o_ready())) break;
-                ready = true;
-                tc_fence_after_sync();
               }
               if (v > 0 && __any_sync(kFull, alpha != 1.f)) {
                 l_run *= alpha;
@@ -821,25 +829,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t pw[16];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t pw[32];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float2 y = ffma2(make_float2(__uint_as_float(x[q][2 * e]),
-                                             __uint_as_float(x[q][2 * e + 1])), c2, m2);
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t* s2 = &x[2 * q + (e >> 4)][2 * (e & 15)];
+                float2 y = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])),
+                                 c2, m2);
                 y.x = fast_exp2(y.x);
                 y.y = fast_exp2(y.y);
                 ls[e & 1] = fadd2(ls[e & 1], y);
                 pw[e] = pack_bf16x2(y.x, y.y);
               }
-              if (q == 0 && !ready) {
-                if (!(ok = o_ready())) break;
-                ready = true;
-                tc_fence_after_sync();
-              }
-              tmem_st16(tP + 16 * q, pw);
+              tmem_st32(tP + 32 * q, pw);
             }
-            if (!ok) break;
             const float2 l2 = fadd2(ls[0], ls[1]);
             const float sum = l2.x + l2.y;
             // (NaN too; a tile that has just been measured stands as it is)
@@ -850,7 +853,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             }
             measure = true;
           }
-          if (!ok) break;
           tmem_wait_st();
         }
         tc_fence_before_sync();
