@@ -35,8 +35,8 @@
 //             replaces non-finite V values by zero (a masked weight is zero,
 //             but 0 x NaN is not); rows that do see such a value get it added
 //             in the epilogue
-// Measured on 2 x 4096 tokens over 8192 (391 GFLOP): 413 us, 0.95 PFLOP/s, half
-// of the card's cuBLAS bf16 rate.  A unit takes 1230 cycles of an SM, of which
+// Measured on 2 x 4096 tokens over 8192 (391 GFLOP): 356 us, 1.10 PFLOP/s, 0.59
+// of the card's cuBLAS bf16 rate.  A unit takes 1060 cycles of an SM, of which
 // its MMAs fill 440 and its exponentials 546 (30 a clock), the rest being the
 // latencies of the chain scores -> registers -> P -> PV; the two groups' chains
 // overlap, but two warps to a scheduler do not hide them all.  What moved it:
@@ -47,7 +47,12 @@
 //  * no register spills in the softmax (567 -> 449 us): the epilogue runs in
 //    16-column steps, and what the loop needs of an item it reads again;
 //  * one elected lane for the copies of a kv tile, and no maximum per tile
-//    (449 -> 415 us);
+//    (449 -> 413 us);
+//  * the exponentials of a unit as one straight block, its weights stored in
+//    two parts of 64 columns and the wait for the group's last PV before it
+//    (412 -> 356 us; four parts of 32 with the wait after the first part left
+//    the compiler short of registers, and all 64 words stored at the end cost
+//    451 us);
 //  * not: 16 softmax warps of half a row each (558 us: twice the hand-over
 //    instructions), four groups of 128 x 64 units with P over S (485 us: twice
 //    the units for the issuing warps), scalar instead of packed FP32 (493 us),
