@@ -613,7 +613,8 @@ PKV_API size_t pkv_scored_workspace_bytes(int batch, int num_q_heads, int num_kv
  *                    tokens' old places in order, then -1
  *   dev_err          PKV_DEVERR_PAGE (a row whose old or new page is bad is
  *                    not copied) / _SEQLEN
- * 0 <= sinks, 0 <= recent, sinks + recent <= budget, budget >= 1.  The old
+ * 0 <= sinks, 0 <= recent, sinks + recent <= budget, budget >= 1; both tables
+ * hold less than 2^31 - 2^16 tokens a sequence.  The old
  * pages are read only (a shared prefix stays intact); dst slots at or past
  * new_lens[b] are left as they were.
  */

@@ -1224,8 +1224,10 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
   if (!mass || !pool || !block_table || !seq_lens || !dst_block_table || !new_lens ||
       !new_mass || !kept)
     return PKV_EINVAL;
+  // (the kernel steps over tokens by up to 2^16 in 32 bits)
+  constexpr int kMaxBlocks = (INT32_MAX - (1 << 16)) / kPageSize;
   if (bad_cache(batch, num_pages, max_blocks) || bad_cache(batch, num_pages, dst_max_blocks) ||
-      budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks ||
+      max_blocks > kMaxBlocks || dst_max_blocks > kMaxBlocks || budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks ||
       budget > static_cast<int64_t>(dst_max_blocks) * kPageSize ||
       mass_stride < static_cast<int64_t>(max_blocks) * kPageSize || new_mass_stride < budget)
     return PKV_EINVAL;

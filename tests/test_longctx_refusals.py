@@ -72,6 +72,7 @@ def append(B, **kw):
     (evict, dict(stride=2047)), (evict, dict(new_stride=63)), (evict, dict(new_mass=A1)),
     (evict, dict(new_lens=A4)), (evict, dict(kept=A7)), (evict, dict(dst=None)),
     (evict, dict(kept=None)), (evict, dict(recent=2 ** 31 - 1)),
+    (evict, dict(mb=2 ** 27 - 1, stride=2 ** 31)), (evict, dict(dmb=2 ** 27 - 1)),
     (append, dict(slots=None)), (append, dict(theta=0.0)), (append, dict(q_in=A7)),
     (append, dict(q_in=A7, q_out=A7, hq=32)), (append, dict(mb=2 ** 28)),
 ])
