@@ -687,10 +687,15 @@ def _err(dev_err, index):
 
 
 def _new(shape, dtype, index, stream):
-    """A tensor the call makes for itself, kept for the stream it is used on."""
-    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor the call makes for itself.  Its memory is the call's stream's
+    (work of another stream may still be using what that one freed), and is
+    kept for the current stream too, where the caller may use and free it."""
+    device = torch.device("cuda", index)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(index))
     return t
 
 
@@ -754,12 +759,14 @@ def paged_chunk_attention(q, token_offsets, pool, block_table, seq_lens, out=Non
     num_splits = _count(num_splits, "num_splits")
     raw = _on(index, stream)
     if out is None:
+        out = _new(q.shape, _BF16, index, stream)
         if stream is None:
-            out = torch.zeros_like(q)
+            out.zero_()
         else:
             with torch.cuda.stream(stream):
-                out = torch.zeros_like(q)
-    _heads(out, "out", index, rows)
+                out.zero_()
+    else:
+        _heads(out, "out", index, rows)
     if rows == 0 or B == 0:
         return out
     ws, ws_ptr, ws_bytes = _scratch(

@@ -451,9 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           const int p0 = max(it.pos0, 0);
           it.lo = p0 >= a.window ? p0 - a.window + 1 : 0;
           it.w0 = it.lo / kKvTokens;
-          it.ns = min((min(a.sinks, it.lo) + kKvTokens - 1) / kKvTokens, it.w0);
-          const int tiles =
-              it.end() > 0 ? it.ns + (it.end() + kKvTokens - 1) / kKvTokens - it.w0 : 0;
+          auto kv_tiles = [](int n) {  // (n + 127 may pass 2^31)
+            return static_cast<int>((static_cast<uint32_t>(n) + kKvTokens - 1) / kKvTokens);
+          };
+          it.ns = min(kv_tiles(min(a.sinks, it.lo)), it.w0);
+          const int tiles = it.end() > 0 ? it.ns + kv_tiles(it.end()) - it.w0 : 0;
           it.t0 = static_cast<int>(static_cast<int64_t>(tiles) * it.split / a.num_splits);
           it.t1 = static_cast<int>(static_cast<int64_t>(tiles) * (it.split + 1) / a.num_splits);
           if (it.tiles() == 0) {

@@ -263,6 +263,58 @@ def test_calls_on_another_stream():
         assert torch.equal(want, got) and torch.equal(w1, g1)
 
 
+def test_results_of_a_side_stream_keep_clear_of_the_current_one():
+    """A call on another stream makes its result of memory that the current
+    stream's work, still running, is about to write."""
+    dev, b = cuda_or_skip(), binding()
+    lens = [333, 40]
+    pool, bt = (x.to(dev) for x in make_cache(lens, seed=17))
+    ln, q = lens_t(lens).to(dev), normal((2, HQ, 64), 18).to(dev)
+    off = offsets([1, 1]).to(dev)
+    calls = (lambda **kw: b.paged_window_attention(q, pool, bt, ln, 50, num_splits=2, **kw),
+             lambda **kw: b.paged_chunk_attention(q, off, pool, bt, ln, num_splits=2, **kw))
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        freed = torch.empty_like(q)
+        torch.cuda._sleep(20_000_000)
+        freed.fill_(9)
+        del freed
+        got = call(stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("counts", [[5], [3]])
+def test_largest_table(counts):
+    """Positions up to the last one a table can name."""
+    dev, b = cuda_or_skip(), binding()
+    blocks, window, sinks, n = 2 ** 27 - 1, 200, 3, counts[0]
+    L = blocks * 16 - 2
+    last = 16                                   # the table's pages that exist: 0 and the last 16
+    pool = normal((last + 1, 2, 16, HKV, 64), 40)
+    q = normal((n, HQ, 64), 41)
+    bt = torch.full((1, blocks), -1, dtype=torch.int32, device=dev)
+    bt[0, 0] = last
+    bt[0, blocks - last:] = torch.arange(last, dtype=torch.int32, device=dev)
+    near = np.concatenate([[last], np.arange(last)]).astype(np.int32)
+    want, tol = np.zeros((n, HQ, 64)), np.zeros((n, HQ, 64))
+    for i in range(n):
+        p = L - n + i
+        t = np.concatenate([np.arange(sinks), 16 + np.arange(p - window + 1, p + 1) -
+                            16 * (blocks - last)])
+        want[i], tol[i], _, _ = attend(q[i], pool, near, t)
+    args = pool.to(dev), bt, torch.tensor([L], dtype=torch.int32, device=dev)
+    err = dev_err(dev)
+    out = b.paged_chunk_attention(q.to(dev), offsets(counts).to(dev), *args, window=window,
+                                  sinks=sinks, dev_err=err)
+    check(out, want, tol, "chunk")
+    out = b.paged_window_attention(q[-1:].to(dev), *args, window, sinks=sinks, dev_err=err)
+    check(out, want[-1:], tol[-1:], "window")
+    assert int(err.item()) == 0
+
+
 # ------------------------------------------------- one token under a window --
 
 def run_window(lens, window, sinks, *, splits=0, seed=21, cache=None):
