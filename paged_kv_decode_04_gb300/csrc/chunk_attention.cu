@@ -1017,26 +1017,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_chunk_kernel(const Mask
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.num_splits;
   const float2* acc = reinterpret_cast<const float2*>(a.part_acc) +
                       row * a.num_splits * (kHeadDim / 2) + lane;
-  float M = -INFINITY;
-  for (int s = lane; s < splits; s += 32) {
-    const float2 x = __ldcg(ml + s);
-    if (x.y != 0.f) M = fmaxf(M, x.x);
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-  float L = 0.f;
-  float2 O = make_float2(0.f, 0.f);
-  for (int s = 0; s < splits; ++s) {
-    const float2 x = __ldcg(ml + s);
-    if (x.y == 0.f) continue;  // saw no token; its accumulator was not written
-    const float wt = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M);  // (-inf: a NaN row)
-    const float2 v = __ldcg(acc + static_cast<int64_t>(s) * (kHeadDim / 2));
-    L = fmaf(x.y, wt, L);
-    O.x = fmaf(v.x, wt, O.x);
-    O.y = fmaf(v.y, wt, O.y);
-  }
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
+  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = merge_ranges(ml, acc, splits, lane);
 }
 
 cudaError_t configure(int device) {

@@ -617,4 +617,41 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                : "memory");
 }
 
+// One warp combines a row's ranges, added in order: (max in log2 units, sum) of
+// range s at ml[s], this lane's two dims of its accumulator at acc[s * 32]
+// (not read into the result when the range saw no token).  Returns the lane's
+// two dims of the output.
+__device__ __forceinline__ uint32_t merge_ranges(const float2* ml, const float2* acc, int splits,
+                                                 int lane) {
+  float M = -INFINITY;
+  for (int s = lane; s < splits; s += 32) {
+    const float2 x = __ldcg(ml + s);
+    if (x.y != 0.f) M = fmaxf(M, x.x);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+  float L = 0.f;
+  float2 O = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    float2 x[8], v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = s0 + e < splits;
+      x[e] = in ? __ldcg(ml + s0 + e) : make_float2(0.f, 0.f);
+      v[e] = in ? __ldcg(acc + static_cast<int64_t>(s0 + e) * 32) : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (x[e].y == 0.f) continue;  // saw no token
+      const float wt = x[e].x == -INFINITY ? 1.f : fast_exp2(x[e].x - M);  // (-inf: a NaN row)
+      L = fmaf(x[e].y, wt, L);
+      O.x = fmaf(v[e].x, wt, O.x);
+      O.y = fmaf(v[e].y, wt, O.y);
+    }
+  }
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  return pack_bf16x2(O.x * inv, O.y * inv);
+}
+
 }  // namespace pkv

@@ -4,8 +4,9 @@
 //
 // Such a chunk reads its whole cache for 16 query rows of a kv head, so it is
 // bound by memory, and a 128-row MMA tile would be mostly padding: a unit of
-// the tcgen05 kernel costs the same for 16 rows as for 128, and 64 sequences
-// of 4 tokens over 2048 took 60 us there against 45 us here.  This kernel
+// the tcgen05 kernel costs the same for 16 rows as for 128: with cold caches 64
+// sequences of 5 to 16 tokens over 2048 take 65-68 us there, of 4 tokens 53 us
+// here (256 over 512: 102 and 59 us).  This kernel
 // streams pages as the one-token kernels do: one CTA per (sequence, kv head,
 // range of the pages), 4 warps taking every 4th page through private rings of
 // 4 KiB tiles, mma.sync with the tokens of a page as M and the query rows as
@@ -384,42 +385,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kStages))
   if constexpr (kBeside) wait_for_prior_grids();
 }
 
-// grid (kv heads, batch): combine the ranges of a short chunk's rows, added in
-// order; lane l holds dims 2l and 2l + 1.
-__global__ void __launch_bounds__(kThreads) merge_short_kernel(const MaskedArgs a) {
+// grid (kv heads x tokens, batch): combine the ranges of a short chunk's rows,
+// added in order; a warp to a row, lane l holding dims 2l and 2l + 1, with the
+// loads of eight ranges in flight.  (Every step of the sum is an L2 latency:
+// with four warps for all rows of a kv head, 4 tokens over 2048 took 39 us,
+// this way 14 us.)
+__global__ void __launch_bounds__(32 * kGroup) merge_short_kernel(const MaskedArgs a) {
   allow_dependent_grids();
   wait_for_prior_grids();
-  const int lane = threadIdx.x & 31, g = blockIdx.x, b = blockIdx.y;
+  const int lane = threadIdx.x & 31, g = blockIdx.x % kNumKvHeads, b = blockIdx.y;
+  const int r = blockIdx.x / kNumKvHeads * kGroup + (threadIdx.x >> 5);
   const int o0 = a.token_offsets[b], o1 = a.token_offsets[b + 1];
   if (o0 < 0 || o1 > a.num_tokens || o1 <= o0 || o1 - o0 > kShortTokens) return;
-  for (int r = threadIdx.x >> 5; r < (o1 - o0) * kGroup; r += kWarps) {
-    const int64_t first = part_row(b, g, r) * a.short_splits;
-    const float2* ml = reinterpret_cast<const float2*>(a.short_ml) + first;
-    const float2* acc = reinterpret_cast<const float2*>(a.short_acc) + first * (kHeadDim / 2) + lane;
-    float M = -INFINITY;
-    for (int s = lane; s < a.short_splits; s += 32) {
-      const float2 x = __ldcg(ml + s);
-      if (x.y != 0.f) M = fmaxf(M, x.x);
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
-    float L = 0.f;
-    float2 O = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < a.short_splits; ++s) {
-      const float2 x = __ldcg(ml + s);
-      const float2 v = __ldcg(acc + static_cast<int64_t>(s) * (kHeadDim / 2));
-      if (x.y == 0.f) continue;  // saw no token
-      const float wt = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M);  // (-inf: a NaN row)
-      L = fmaf(x.y, wt, L);
-      O.x = fmaf(v.x, wt, O.x);
-      O.y = fmaf(v.y, wt, O.y);
-    }
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    const int64_t row =
-        static_cast<int64_t>(o0 + r / kGroup) * kNumQHeads + g * kGroup + r % kGroup;
-    reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
-  }
+  if (r >= (o1 - o0) * kGroup) return;
+  const int64_t first = part_row(b, g, r) * a.short_splits;
+  const float2* ml = reinterpret_cast<const float2*>(a.short_ml) + first;
+  const float2* acc = reinterpret_cast<const float2*>(a.short_acc) + first * (kHeadDim / 2) + lane;
+  const int64_t row = static_cast<int64_t>(o0 + r / kGroup) * kNumQHeads + g * kGroup + r % kGroup;
+  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] =
+      merge_ranges(ml, acc, a.short_splits, lane);
 }
 
 template <bool kBeside, int kStages>
@@ -452,8 +436,8 @@ cudaError_t launch_short_chunks(const CUtensorMap& pool_map, const MaskedArgs& a
                           : launch<false, kShallow>(pool_map, args, stream))
                 : launch<true, kDeep>(pool_map, args, stream);
   if (err != cudaSuccess || args.short_splits == 1) return err;
-  return launch_pdl(merge_short_kernel, dim3(kNumKvHeads, args.batch), dim3(kThreads), 0, stream,
-                    args);
+  return launch_pdl(merge_short_kernel, dim3(kNumKvHeads * kShortTokens, args.batch),
+                    dim3(32 * kGroup), 0, stream, args);
 }
 
 }  // namespace pkv
