@@ -534,7 +534,9 @@ PKV_API int pkv_paged_decode_attention_static_ws(
  *                  _POSITION (a chunk longer than its sequence: the rows before
  *                  position 0 are zero) / _TIMEOUT
  * Table entries of pages that no query of the chunk sees are not read, so
- * pages that have left every window may be freed.
+ * pages that have left every window may be freed.  After _TIMEOUT rows of out
+ * may be unwritten.  Calls that overlap on the GPU need workspaces of their
+ * own.
  */
 PKV_API int pkv_paged_chunk_attention(
     const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const pkv_bf16* pool,
