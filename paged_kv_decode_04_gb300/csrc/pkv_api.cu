@@ -953,14 +953,16 @@ bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks
   }
   s = std::min(s, std::max(kv, 1LL));
   plan->num_splits = static_cast<int>(items > 0 ? s : 1);
-  // short chunks: one wave of three CTAs per SM, eight pages a range or more;
-  // more tokens than short chunks of this batch can have mean a long one
+  // short chunks: one wave of the CTAs that fit (short_chunk.cu: three per SM
+  // beside a long chunk, else four), eight pages a range or more; more tokens
+  // than short chunks of this batch can have mean a long one.  (32 x 4 tokens
+  // over 4096: 69 us in one range, 58 us in two; 64 x 4 over 2048 53 and 60.)
   long long t = num_splits;
   if (t == 0) {
-    const long long most = num_tokens > pkv::kShortTokens * static_cast<long long>(batch)
-                               ? std::max(batch - 1, 1)
-                               : std::min(batch, num_tokens);
-    t = std::max(1LL, std::min(3LL * sms / (most * kNumKvHeads), (pages + 7) / 8));
+    const bool a_long_one = num_tokens > pkv::kShortTokens * static_cast<long long>(batch);
+    const long long most = a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens);
+    t = std::max(1LL, std::min((a_long_one ? 3LL : 4LL) * sms / (most * kNumKvHeads),
+                               (pages + 7) / 8));
     if (num_tokens > pkv::kShortTokens && batch == 1) t = 1;
   }
   plan->short_splits = static_cast<int>(std::min(t, pages));
