@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       // last (under a causal mask the longest) to its first.  Every second
       // round runs through the CTAs backwards, so that long items pair with
       // short ones.
-      const int per_tile = a.num_splits * kNumKvHeads;
+      const uint32_t per_tile = a.num_splits * kNumKvHeads;
       int b0 = -32, before = 0, sum = 0;      // 32 sequences from b0: tiles before them, theirs
-      int cnt = 0, incl = 0, o0 = 0, o1 = 0;  // this lane's sequence
+      int cnt = 0, incl = 0, o0 = 0, o1 = 0, len = 0;  // this lane's sequence
       int parity = 0, out_i = 0;              // units so far mod 2, items published
       int round = 0, kt = 0;
       bool more = true;
@@ -400,8 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
        for (;; ++round) {
         const int64_t idx = static_cast<int64_t>(round) * gridDim.x +
                             ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const int64_t tile64 = idx / per_tile;
-        const int rest = static_cast<int>(idx % per_tile);
+        // (a 64-bit division takes as long as the rest of this)
+        const int64_t tile64 = idx >> 32 == 0 ? static_cast<uint32_t>(idx) / per_tile
+                                              : idx / per_tile;
+        const int rest = static_cast<int>(idx - tile64 * per_tile);
         while (b0 < a.batch && tile64 >= static_cast<int64_t>(before) + sum) {
           before += sum;
           b0 += 32;
@@ -410,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           if (b < a.batch) {
             o0 = a.token_offsets[b];
             o1 = a.token_offsets[b + 1];
+            len = a.seq_lens[b];
             if (o0 < 0 || o1 < o0 || o1 > a.num_tokens) {
               if (blockIdx.x == 0) record_error(a.dev_err, kErrOffsets);
             } else {
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           it.g = rest % kNumKvHeads;
           it.split = rest / kNumKvHeads;
           const int Lmax = a.max_blocks * kPageSize;
-          int L = a.seq_lens[it.b];
+          int L = __shfl_sync(kFull, len, src);
           if (L < 0 || L > Lmax) {
             if (lane == 0) record_error(a.dev_err, kErrSeqLen);
             L = L < 0 ? 0 : Lmax;
@@ -512,9 +515,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
             // 4 rows of 8 16-byte chunks at a time (the swizzle permutes
             // chunks within a row only)
             const uint32_t v0 = sb + kOffV + st * kRowTileBytes + lane * 16;
-            const int row_end = it.end() - tile * kKvTokens;  // rows that some query sees
+            const int base = tile * kKvTokens;
+            const int row_end = it.end() - base;  // rows that some query sees
+            const int64_t gone = static_cast<int64_t>(it.end()) - 1 - a.window;
+            bool wrote = false;
 #pragma unroll 1
-            for (int r = 0; r < kKvTokens; r += 16) {
+            for (int r = 0; r < kKvTokens && r < row_end; r += kPageSize) {
+              // pages that every query sees stand, those that none does are zeros
+              const int t = base + r;
+              if (t + kPageSize - 1 <= it.pos0 && (t > gone || t + kPageSize <= a.sinks)) continue;
+              if (t + kPageSize <= it.lo && t >= a.sinks) continue;
               uint4 x[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[e] = lds128(v0 + (r + 4 * e) * kRow);
@@ -524,12 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
                                m2 = nonfinite_halves(x[e].z), m3 = nonfinite_halves(x[e].w);
                 if ((m0 | m1 | m2 | m3) != 0u) {
                   if (r + 4 * e + (lane >> 3) < row_end) live_bad = true;
+                  wrote = true;
                   sts128(v0 + (r + 4 * e) * kRow, x[e].x & ~m0, x[e].y & ~m1, x[e].z & ~m2,
                          x[e].w & ~m3);
                 }
               }
             }
-            fence_proxy_async_smem();
+            if (wrote) fence_proxy_async_smem();
           }
           const bool any = __any_sync(kFull, live_bad);
           if (lane == 0) {
