@@ -53,11 +53,14 @@
 //    (412 -> 356 us; four parts of 32 with the wait after the first part left
 //    the compiler short of registers, and all 64 words stored at the end cost
 //    451 us);
+//  * the relay of V scans only the pages that some row does not see (a prompt
+//    of 8192 under a window of 1024: 109 -> 104 us);
 //  * not: 16 softmax warps of half a row each (558 us: twice the hand-over
 //    instructions), four groups of 128 x 64 units with P over S (485 us: twice
-//    the units for the issuing warps), scalar instead of packed FP32 (493 us),
-//    skipping 32-column steps that no row sees (463 us: no overlap between
-//    steps).
+//    the units for the issuing warps), the row in two rolled halves with S given
+//    back at the end (484 us), four more warps for the epilogue (402 us: fewer
+//    registers for every role), scalar instead of packed FP32 (493 us), skipping
+//    32-column steps that no row sees (463 us: no overlap between steps).
 // P enters the product with V as bf16 (8 significant bits, an error of at
 // most 2^-8 of sum p |v|, averaged over the tokens, below the output's own
 // bf16 rounding); the row sums take the unrounded FP32 values.  The reference
@@ -170,7 +173,8 @@ struct Item {
   __device__ __forceinline__ bool partial(int tile, const MaskedArgs& a) const {
     const int base = tile * kKvTokens, last = base + kKvTokens - 1;
     if (last > pos0) return true;
-    const int64_t gone = static_cast<int64_t>(end()) - 1 - a.window;  // last token out of the window
+    // the last token out of the last row's window
+    const int64_t gone = static_cast<int64_t>(end()) - 1 - a.window;
     const int64_t from = base > a.sinks ? base : a.sinks;
     return from <= (gone < last ? gone : last);
   }
@@ -351,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
   int* s_items = reinterpret_cast<int*>(smem + kOffItems);
   auto item_addr = [&](int slot) { return sb + kOffItems + 4u * kItemWords * slot; };
-  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);  // [kMeta][2], then the TMEM address
+  // [kMeta][2], then the TMEM address
+  uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // Barriers and TMEM before a dependent grid may start: its CTAs then never
@@ -789,7 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
           if (lane == 0) mbar_arrive(bar(kBarSFree + w));
           if (note.y != 0u) {  // columns that this row does not see
             const uint32_t bad = note.y;
-            const int pos = lds_int(item_addr(slot) + 12) + (row >> 2) + (one ? 0 : kHalfTokens * w);
+            const int pos =
+                lds_int(item_addr(slot) + 12) + (row >> 2) + (one ? 0 : kHalfTokens * w);
             const int64_t base = static_cast<int64_t>(note.x) * kKvTokens;
             const int ch = clamp_cols(pos - base) + 1;  // columns [0, ch): t <= pos
             // [cl, ..): t > pos - window; [0, cs): t < sinks

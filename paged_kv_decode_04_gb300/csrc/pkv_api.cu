@@ -896,21 +896,28 @@ bool chunk_q_map(const void* q, int num_tokens, CUtensorMap* out) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Ranges of a one-token call whose sequences see at most `pages` pages, as
-// make_plan chooses them: about four CTAs per SM, eight pages a range or more.
-int one_token_splits(int batch, long long pages, int num_splits) {
+// Ranges of a one-token call whose sequences see at most `pages` pages: CTAs for
+// two an SM (scored: one and a half), but 20 pages a range or more (scored: 48,
+// its merge also adds the weights), where a range's streaming is as long as the
+// merge it costs.  One sequence of 4093: 14 us in 8 ranges, 37 in one, 18 in 32;
+// 34 of 403: 12 us in one, 18 in three.  Scored: one of 4093 21 us in 8, 31 in
+// one, 23 in 32; 36 of 1076 23 us in one, 33 in two.
+int one_token_splits(int batch, long long pages, int num_splits, bool scored) {
   if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, pages));
   const int sms = current_sm_count();
   if (sms <= 0) return -1;
   const long long units = static_cast<long long>(batch) * kNumKvHeads;
-  return static_cast<int>(std::max(
-      1LL, std::min((4LL * sms + units - 1) / units, (pages + 7) / 8)));
+  long long s = std::min((scored ? 3LL : 4LL) * sms / (2 * units), pages / (scored ? 48 : 20));
+  // (weights that do not fit shared memory go through the workspace anyway: 45
+  // sequences of 9593 took 154 us in one range, 139 in two)
+  if (scored && pages > pkv::kScoredSmemPages) s = std::max(s, 2LL);
+  return static_cast<int>(std::max(1LL, s));
 }
 
 long long window_pages(int max_blocks, int window, int sinks) {
-  return std::min<long long>(max_blocks, (static_cast<long long>(window) + kPageSize - 2) / kPageSize +
-                                             1 + (static_cast<long long>(sinks) + kPageSize - 1) /
-                                                     kPageSize);
+  const long long seen = (static_cast<long long>(window) + kPageSize - 2) / kPageSize + 1;
+  return std::min<long long>(
+      max_blocks, seen + (static_cast<long long>(sinks) + kPageSize - 1) / kPageSize);
 }
 
 // Ranges and CTAs of a chunk call.  Chunks of more than kShortTokens tokens
@@ -1107,7 +1114,8 @@ PKV_API size_t pkv_window_workspace_bytes(int batch, int num_q_heads, int num_kv
       !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
   if (batch == 0) return 0;
-  const int splits = one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits);
+  const int splits =
+      one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits, false);
   return splits < 1 ? static_cast<size_t>(-1) : part_bytes(batch, splits);
 }
 
@@ -1127,7 +1135,8 @@ PKV_API int pkv_paged_window_attention(
     return PKV_EALIGN;
   if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
-  const int splits = one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits);
+  const int splits =
+      one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits, false);
   if (splits < 1) return PKV_ECUDA;
   const size_t need = part_bytes(batch, splits);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
@@ -1164,7 +1173,7 @@ PKV_API size_t pkv_scored_workspace_bytes(int batch, int num_q_heads, int num_kv
       !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
   if (batch == 0) return 0;
-  const int splits = one_token_splits(batch, max_blocks, num_splits);
+  const int splits = one_token_splits(batch, max_blocks, num_splits, true);
   return splits < 1 ? static_cast<size_t>(-1)
                     : part_bytes(batch, splits) + score_bytes(batch, max_blocks, splits);
 }
@@ -1187,7 +1196,7 @@ PKV_API int pkv_paged_scored_attention(
     return PKV_EALIGN;
   if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
-  const int splits = one_token_splits(batch, max_blocks, num_splits);
+  const int splits = one_token_splits(batch, max_blocks, num_splits, true);
   if (splits < 1) return PKV_ECUDA;
   const size_t parts = part_bytes(batch, splits), keep = score_bytes(batch, max_blocks, splits);
   if (parts + keep > 0 && (workspace == nullptr || workspace_bytes < parts + keep))
@@ -1218,7 +1227,8 @@ PKV_API int pkv_paged_scored_attention(
   CUtensorMap map;
   if (!pool_tensor_map(pool, num_pages, &map)) return PKV_ECUDA;
   const cudaError_t err =
-      pkv::launch_window_attention(map, a, keep > 0 ? 0 : max_blocks, reinterpret_cast<cudaStream_t>(stream));
+      pkv::launch_window_attention(map, a, keep > 0 ? 0 : max_blocks,
+                                   reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -1235,7 +1245,8 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
   // (the kernel steps over tokens by up to 2^16 in 32 bits)
   constexpr int kMaxBlocks = (INT32_MAX - (1 << 16)) / kPageSize;
   if (bad_cache(batch, num_pages, max_blocks) || bad_cache(batch, num_pages, dst_max_blocks) ||
-      max_blocks > kMaxBlocks || dst_max_blocks > kMaxBlocks || budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks ||
+      max_blocks > kMaxBlocks || dst_max_blocks > kMaxBlocks || budget < 1 || sinks < 0 ||
+      recent < 0 || sinks > budget || recent > budget - sinks ||
       budget > static_cast<int64_t>(dst_max_blocks) * kPageSize ||
       mass_stride < static_cast<int64_t>(max_blocks) * kPageSize || new_mass_stride < budget)
     return PKV_EINVAL;

@@ -218,8 +218,10 @@ def test_chunk_repeats_bit_for_bit_and_replays():
 
 
 def test_waits_that_run_out():
-    """With a wait limit of 0 every kernel gives up at its first look, reports
-    it, and leaves the stream and the next calls as they should be."""
+    """With a wait limit of 0 every kernel gives up at its first look at a copy
+    that has not landed, reports it, and leaves the stream and the next calls as
+    they should be.  (The pages come from memory, what a kernel reads before
+    that look from L2, so such a copy is certain.)"""
     dev, b = cuda_or_skip(), binding()
     lens, counts = [900, 70, 1500, 333], [3, 70, 200, 1]
     pool, bt = (x.to(dev) for x in make_cache(lens, seed=19))
@@ -234,6 +236,9 @@ def test_waits_that_run_out():
         want = call(None)
         old = b.set_wait_limit_ns(0)
         err = dev_err(dev)
+        torch.empty(1 << 28, dtype=torch.uint8, device=dev).zero_()
+        for x in (q, off, bt, ln):
+            x.clone()
         try:
             call(err)
         finally:
