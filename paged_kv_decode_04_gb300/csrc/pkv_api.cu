@@ -957,6 +957,12 @@ bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks
     const long long likely =
         chunks * ((each + pkv::kChunkTileTokens - 1) / pkv::kChunkTileTokens) * kNumKvHeads;
     s = std::max(1LL, std::min(sms / std::max(likely, 1LL), kv / 8));
+    // long caches whose last round of items would leave a third of the SMs idle:
+    // three ranges (2 x 700 tokens over 16384, 176 items: 252 -> 202 us; 6 x 128
+    // over 16384, 96 items: 139 -> 107; but 5 x 256 over 6000, 160 items: 68 ->
+    // 83, where the merge costs more)
+    const long long rounds = (likely + sms - 1) / sms;
+    if (s == 1 && kv >= 64 && 2 * rounds * sms >= 3 * likely) s = 3;
   }
   s = std::min(s, std::max(kv, 1LL));
   plan->num_splits = static_cast<int>(items > 0 ? s : 1);
