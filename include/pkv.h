@@ -576,7 +576,8 @@ PKV_API size_t pkv_window_workspace_bytes(int batch, int num_q_heads, int num_kv
  *   j of kv head g of softmax_t(scale * q[b][j] . K_t),   t < seq_lens[b],
  * in FP32, in an order that does not change from run to run.
  *   mass  float, rows of mass_stride >= max_blocks * page_size; entries at or
- *         past seq_lens[b] and those of skipped pages are left as they were
+ *         past seq_lens[b] and those of skipped pages are left as they were.
+ *         Tables hold less than 2^31 - 2^16 tokens a sequence
  * Workspace, num_splits and dev_err as for pkv_paged_decode_attention, sized
  * by pkv_scored_workspace_bytes().
  */

@@ -876,6 +876,10 @@ bool bad_cache(int batch, int64_t num_pages, int max_blocks) {
          max_blocks > (INT32_MAX / kPageSize);
 }
 
+// Widest tables of calls with a mass: their kernels step over tokens by up to
+// 2^16 in 32 bits.
+constexpr int kMaxMassBlocks = (INT32_MAX - (1 << 16)) / kPageSize;
+
 // TMA descriptor of the query rows of a chunk, [num_tokens][32 heads][64] bf16:
 // a box of 4 heads of 32 tokens, 128-byte swizzled.
 bool chunk_q_map(const void* q, int num_tokens, CUtensorMap* out) {
@@ -1175,7 +1179,7 @@ PKV_API int pkv_paged_window_attention(
 
 PKV_API size_t pkv_scored_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
                                           int head_dim, int max_blocks, int num_splits) {
-  if (bad_cache(batch, 1, max_blocks) || num_splits < 0 ||
+  if (bad_cache(batch, 1, max_blocks) || max_blocks > kMaxMassBlocks || num_splits < 0 ||
       !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
   if (batch == 0) return 0;
@@ -1191,7 +1195,7 @@ PKV_API int pkv_paged_scored_attention(
     void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
     pkv_stream_t stream) {
   if (!q || !pool || !block_table || !seq_lens || !out || !mass) return PKV_EINVAL;
-  if (bad_cache(batch, num_pages, max_blocks) || num_splits < 0 ||
+  if (bad_cache(batch, num_pages, max_blocks) || max_blocks > kMaxMassBlocks || num_splits < 0 ||
       mass_stride < static_cast<int64_t>(max_blocks) * kPageSize)
     return PKV_EINVAL;
   if (!(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
@@ -1248,10 +1252,8 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
   if (!mass || !pool || !block_table || !seq_lens || !dst_block_table || !new_lens ||
       !new_mass || !kept)
     return PKV_EINVAL;
-  // (the kernel steps over tokens by up to 2^16 in 32 bits)
-  constexpr int kMaxBlocks = (INT32_MAX - (1 << 16)) / kPageSize;
   if (bad_cache(batch, num_pages, max_blocks) || bad_cache(batch, num_pages, dst_max_blocks) ||
-      max_blocks > kMaxBlocks || dst_max_blocks > kMaxBlocks || budget < 1 || sinks < 0 ||
+      max_blocks > kMaxMassBlocks || dst_max_blocks > kMaxMassBlocks || budget < 1 || sinks < 0 ||
       recent < 0 || sinks > budget || recent > budget - sinks ||
       budget > static_cast<int64_t>(dst_max_blocks) * kPageSize ||
       mass_stride < static_cast<int64_t>(max_blocks) * kPageSize || new_mass_stride < budget)

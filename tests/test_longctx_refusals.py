@@ -67,6 +67,7 @@ def append(B, **kw):
     (window, dict(scale=float("nan"))), (window, dict(out=A1)), (window, dict(mb=2 ** 28)),
     (scored, dict(mass=None)), (scored, dict(stride=2047)), (scored, dict(splits=-2)),
     (scored, dict(out=A1)), (scored, dict(scale=-1.0)),
+    (scored, dict(mb=2 ** 27 - 1, stride=2 ** 31)),
     (evict, dict(budget=0)), (evict, dict(sinks=-1)), (evict, dict(recent=-1)),
     (evict, dict(sinks=40, recent=25)), (evict, dict(sinks=65)), (evict, dict(dmb=3)),
     (evict, dict(stride=2047)), (evict, dict(new_stride=63)), (evict, dict(new_mass=A1)),
