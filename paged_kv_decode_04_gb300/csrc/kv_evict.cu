@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(Shape<kMany>::kThreads, Shape<kMany>::kCtas)
         }
       }
     };
-    if (kSmemKeys) each_key([&](int t, uint32_t k) { s_keys[t] = k; });
     auto key = [&](int t) { return kSmemKeys ? s_keys[t] : weight_key(mass[t]); };
     uint32_t prefix = 0;
     int need = a.budget - a.sinks - a.recent;
@@ -133,7 +132,12 @@ __global__ void __launch_bounds__(Shape<kMany>::kThreads, Shape<kMany>::kCtas)
       auto count = [&](int, uint32_t k) {
         if ((k & high) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
       };
-      if (kSmemKeys) {
+      if (kSmemKeys && pass == 0) {
+        each_key([&](int t, uint32_t k) {
+          s_keys[t] = k;
+          count(t, k);
+        });
+      } else if (kSmemKeys) {
         for (int t = lo + tid; t < hi; t += kThreads) count(t, s_keys[t]);
       } else {
         each_key(count);
