@@ -34,16 +34,21 @@ namespace pkv {
 
 namespace {
 
-// Tables of up to kManyTokens tokens: CTAs of 256 threads, four to an SM.
+// Tables of up to kSmallTokens tokens: CTAs of 256 threads, four to an SM.
 // Longer ones: CTAs of 1024 threads (the selection is the longer part), one to
-// an SM; up to kSmemTokens the keys stay in shared memory, beyond it every
-// pass reads the weights again (from L2).  One sequence of 32768 tokens took
-// 119 us with small CTAs, 29.5 us with large ones.
-constexpr int kManyTokens = 8192, kSmemTokens = 49152;
-template <bool kMany>
+// an SM, or of 512, two to an SM, for tables of up to kPairTokens when there are
+// more (sequence, kv head) pairs than SMs; up to kSmemTokens the keys stay in
+// shared memory, beyond it every pass reads the weights again (from L2).  One
+// sequence of 32768 tokens took 119 us with small CTAs, 29.5 us with large ones;
+// 40 of 12000 43 us with large, 35 with pairs; 10 of 20000 37 and 45.
+enum Kind { kSmall, kPair, kLarge };
+constexpr int kSmallTokens = 8192, kPairTokens = 24576, kSmemTokens = 49152;
+template <Kind kKind>
 struct Shape {
-  static constexpr int kThreads = kMany ? 1024 : 256;
-  static constexpr int kCtas = kMany ? 1 : 4;
+  static constexpr int kThreads = kKind == kSmall ? 256 : kKind == kPair ? 512 : 1024;
+  static constexpr int kCtas = kKind == kSmall ? 4 : kKind == kPair ? 2 : 1;
+  static constexpr int kKeys =
+      kKind == kSmall ? kSmallTokens : kKind == kPair ? kPairTokens : kSmemTokens;
 };
 constexpr int kBins = 2048;
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -59,10 +64,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <bool kMany, bool kSmemKeys>
-__global__ void __launch_bounds__(Shape<kMany>::kThreads, Shape<kMany>::kCtas)
+template <Kind kKind, bool kSmemKeys>
+__global__ void __launch_bounds__(Shape<kKind>::kThreads, Shape<kKind>::kCtas)
     kv_evict_kernel(const EvictArgs a) {
-  constexpr int kThreads = Shape<kMany>::kThreads, kWarps = kThreads / 32;
+  constexpr int kThreads = Shape<kKind>::kThreads, kWarps = kThreads / 32;
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) int s_hist[kBins];
   __shared__ int s_above[kWarps], s_eq[kWarps], s_gt[kWarps];
@@ -280,9 +285,9 @@ __global__ void __launch_bounds__(Shape<kMany>::kThreads, Shape<kMany>::kCtas)
   }
 }
 
-template <bool kMany, bool kSmemKeys>
+template <Kind kKind, bool kSmemKeys>
 cudaError_t launch(const EvictArgs& args, int num_sms, cudaStream_t stream) {
-  using Sh = Shape<kMany>;
+  using Sh = Shape<kKind>;
   const int64_t tokens = static_cast<int64_t>(args.max_blocks) * kPageSize;
   const size_t smem = kSmemKeys ? tokens * sizeof(uint32_t) : 0;
   int device = 0;
@@ -292,8 +297,8 @@ cudaError_t launch(const EvictArgs& args, int num_sms, cudaStream_t stream) {
   const unsigned long long bit = 1ull << (device & 63);
   if (kSmemKeys && !(done.load(std::memory_order_acquire) & bit)) {
     err = cudaFuncSetAttribute(
-        kv_evict_kernel<kMany, kSmemKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        (kMany ? kSmemTokens : kManyTokens) * static_cast<int>(sizeof(uint32_t)));
+        kv_evict_kernel<kKind, kSmemKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        Sh::kKeys * static_cast<int>(sizeof(uint32_t)));
     if (err != cudaSuccess) return err;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -301,7 +306,7 @@ cudaError_t launch(const EvictArgs& args, int num_sms, cudaStream_t stream) {
   const long long units = static_cast<long long>(args.batch) * kNumKvHeads;
   const long long parts = std::max(1LL, std::min(static_cast<long long>(Sh::kCtas) * num_sms / units,
                                                  (args.budget + 63LL) / 64));
-  return launch_pdl(kv_evict_kernel<kMany, kSmemKeys>,
+  return launch_pdl(kv_evict_kernel<kKind, kSmemKeys>,
                     dim3(static_cast<unsigned>(kNumKvHeads * parts), args.batch),
                     dim3(Sh::kThreads), smem, stream, args);
 }
@@ -310,9 +315,11 @@ cudaError_t launch(const EvictArgs& args, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_kv_evict(const EvictArgs& args, int num_sms, cudaStream_t stream) {
   const int64_t tokens = static_cast<int64_t>(args.max_blocks) * kPageSize;
-  if (tokens <= kManyTokens) return launch<false, true>(args, num_sms, stream);
-  return tokens <= kSmemTokens ? launch<true, true>(args, num_sms, stream)
-                               : launch<true, false>(args, num_sms, stream);
+  if (tokens <= kSmallTokens) return launch<kSmall, true>(args, num_sms, stream);
+  if (tokens <= kPairTokens && static_cast<int64_t>(args.batch) * kNumKvHeads > num_sms)
+    return launch<kPair, true>(args, num_sms, stream);
+  return tokens <= kSmemTokens ? launch<kLarge, true>(args, num_sms, stream)
+                               : launch<kLarge, false>(args, num_sms, stream);
 }
 
 }  // namespace pkv

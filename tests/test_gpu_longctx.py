@@ -485,6 +485,11 @@ def test_evict_wide_tables(width):
     run_evict([700, 1, 300, 64], 100, 4, 16, width=width)
 
 
+def test_evict_wide_tables_of_a_large_batch():
+    # more (sequence, head) pairs than SMs, tables of more than 8192 tokens
+    run_evict([700, 1, 300, 9600] + [64, 0, 129, 500] * 4, 100, 4, 16, width=600)
+
+
 def test_evict_values_at_their_limits():
     """NaN, infinities, zeros of both signs, subnormals, negative values."""
     n, B = 300, 1
