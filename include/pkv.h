@@ -504,6 +504,8 @@ PKV_API int pkv_paged_decode_attention_static_ws(
  *   t <= p  and  (t > p - window  or  t < sinks).
  * Tokens that a query does not see never reach its result, whatever their K
  * and V hold (NaN and infinities included), and a row that sees none is zero.
+ * A seen token whose score is -inf has the weight 0; a row whose seen scores
+ * are all -inf is zero.
  */
 
 /*

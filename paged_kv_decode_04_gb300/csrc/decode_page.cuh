@@ -14,7 +14,9 @@
 // ldmatrix.trans.  The softmax keeps a lazily updated reference maximum per
 // row: the accumulators are rescaled only when a score exceeds it by more
 // than kRescaleLog2 (weights stay <= 2^kRescaleLog2); the final division by
-// the running sum makes the result independent of the reference.  P enters
+// the running sum makes the result independent of the reference.  It is -inf
+// until a row has seen a score above that: scores of -inf alone weigh nothing,
+// so what is subtracted from them is finite (-inf - -inf would be NaN).  P enters
 // the second product as two bf16 terms, hi = bf16(P) and lo = bf16(P - hi),
 // so every weight keeps about 16 significant bits.
 #pragma once
@@ -29,6 +31,7 @@ namespace pkv {
 constexpr int kRowBytes = kHeadDim * 2;                // 128 B: one head's row
 constexpr int kTileBytes = 2 * kPageSize * kRowBytes;  // 4 KiB: 16 K rows, 16 V rows
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLowest = -3.402823466e38f;            // the lowest finite float
 constexpr unsigned kFullMask = 0xFFFFFFFFu;
 
 // Per-lane fragment coordinates and swizzled ldmatrix row offsets.
@@ -115,7 +118,8 @@ __device__ __forceinline__ void fold_page(uint32_t kt, const float (&s)[4], floa
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
       const float m_new = fmaxf(S.m_ref[rr], mx[rr]);
-      const float alpha = fast_exp2(S.m_ref[rr] - m_new);  // 0 on the first page
+      // 0 until the row has seen a score above -inf
+      const float alpha = fast_exp2(S.m_ref[rr] - fmaxf(m_new, kLowest));
       S.l_run[rr] *= alpha;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
@@ -125,9 +129,10 @@ __device__ __forceinline__ void fold_page(uint32_t kt, const float (&s)[4], floa
       S.m_ref[rr] = m_new;
     }
   }
+  const float m[2] = {fmaxf(S.m_ref[0], kLowest), fmaxf(S.m_ref[1], kLowest)};
   float p[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(s[e], c, -S.m_ref[e & 1]));
+  for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(s[e], c, -m[e & 1]));
   S.l_run[0] += p[0] + p[2];
   S.l_run[1] += p[1] + p[3];
 

@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
       const float m_new = grow ? fmaxf(m_ref, mx) : m_ref;
       const float alpha = grow ? fast_exp2(m_ref - m_new) : 1.f;  // 0 on the first live page
       m_ref = m_new;
+      const float m_sub = fmaxf(m_ref, kLowest);  // scores of -inf alone weigh nothing
       // P = 2^(s c - m_ref) as hi + lo bf16 terms; word w of page q packs
       // tokens 2w, 2w + 1
       uint32_t hi[16], lo[16];
@@ -456,8 +457,8 @@ __global__ void __launch_bounds__(kTcThreads, kTcCtasPerSm)
         for (int w = 0; w < 8; ++w) {
           float x0 = 0.f, x1 = 0.f;
           if (live[q]) {
-            x0 = fast_exp2(fmaf(__uint_as_float(sr[q][2 * w]), c, -m_ref));
-            x1 = fast_exp2(fmaf(__uint_as_float(sr[q][2 * w + 1]), c, -m_ref));
+            x0 = fast_exp2(fmaf(__uint_as_float(sr[q][2 * w]), c, -m_sub));
+            x1 = fast_exp2(fmaf(__uint_as_float(sr[q][2 * w + 1]), c, -m_sub));
           }
           ls[w & 3] += x0 + x1;
           const uint32_t hw = pack_bf16x2(x0, x1);
