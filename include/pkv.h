@@ -499,8 +499,11 @@ PKV_API int pkv_paged_decode_attention_static_ws(
  * cache, and a cache that does not keep every token.  (The source pages have
  * prefill attention and the decode step only; these calls are this library's
  * own.)  Shapes, pool, tables, scale, dev_err, streams and errors are as
- * above; every call also returns PKV_EINVAL when an output overlaps an input
- * that it must not.  A query at position p sees the cached token t when
+ * above; every call also returns PKV_EINVAL when memory that it writes (out,
+ * q_out, mass, new_lens, new_mass, kept, dev_err and the workspace it needs)
+ * shares a byte with the memory of another argument, the pool's pages included.
+ * Which pages append and eviction write is up to their tables, and not checked
+ * on the host.  A query at position p sees the cached token t when
  *   t <= p  and  (t > p - window  or  t < sinks).
  * Tokens that a query does not see never reach its result, whatever their K
  * and V hold (NaN and infinities included), and a row that sees none is zero.
@@ -635,7 +638,7 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
  * pkv_kv_append_at -- pkv_kv_append with the RoPE position and the cache slot
  * given apart: sequence b's token is rotated for positions[b] (any value >= 0)
  * and stored as cached token slots[b] of its table.  pkv_kv_append is the
- * case slots == positions, bit for bit.  q_in and q_out must not overlap.
+ * case slots == positions, bit for bit.
  */
 PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_bf16* pool,
                              int64_t num_pages, const int32_t* block_table, int max_blocks,

@@ -865,10 +865,45 @@ PKV_API int pkv_kv_write_prefill_layers(int layers, const pkv_bf16* k, const pkv
 
 namespace {
 
-// True when [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p != nullptr && q != nullptr && n > 0 && m > 0 && a < b + m && b < a + n;
+// Bytes [p, p + n) that a call reads or writes.
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+bool overlap(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.p != nullptr && y.p != nullptr && x.n > 0 && y.n > 0 && a < b + y.n && b < a + x.n;
+}
+
+// True when an output shares a byte with an input or another output: outputs
+// are written while inputs are still read, and in no order among themselves.
+template <int kOuts, int kIns>
+bool outputs_overlap(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
+  for (int o = 0; o < kOuts; ++o) {
+    for (const Span& i : ins)
+      if (overlap(outs[o], i)) return true;
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return true;
+  }
+  return false;
+}
+
+template <int kOuts, int kIns>
+bool workspace_overlaps(const Span& ws, const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
+  return outputs_overlap({ws}, outs) || outputs_overlap({ws}, ins);
+}
+
+Span ints(const int32_t* p, size_t n) { return {p, n * sizeof(int32_t)}; }
+
+Span pages_span(const pkv_bf16* pool, int64_t num_pages) {
+  return {pool, static_cast<size_t>(num_pages) * 2 * kPageSize * kNumKvHeads * kHeadDim *
+                    sizeof(pkv_bf16)};
+}
+
+// `rows` rows of `row` floats, `stride` floats apart.
+Span rows_span(const float* p, size_t rows, int64_t stride, int64_t row) {
+  return {p, rows > 0 ? ((rows - 1) * static_cast<size_t>(stride) + row) * sizeof(float) : 0};
 }
 
 bool bad_cache(int batch, int64_t num_pages, int max_blocks) {
@@ -1008,8 +1043,8 @@ size_t score_bytes(int batch, int max_blocks, int splits) {
          sizeof(float);
 }
 
-size_t q_row_bytes(int rows) {
-  return static_cast<size_t>(rows) * kNumQHeads * kHeadDim * sizeof(pkv_bf16);
+Span heads_span(const pkv_bf16* p, int rows, int heads = kNumQHeads) {
+  return {p, static_cast<size_t>(rows) * heads * kHeadDim * sizeof(pkv_bf16)};
 }
 
 }  // namespace
@@ -1033,7 +1068,19 @@ PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_b
       !aligned(q_out, 2) || !aligned(positions, 4) || !aligned(slots, 4) ||
       !aligned(block_table, 4) || !aligned(dev_err, 4))
     return PKV_EALIGN;
-  if (overlap(q_in, q_row_bytes(batch), q_out, q_row_bytes(batch))) return PKV_EINVAL;
+  const size_t rows = static_cast<size_t>(batch);
+  // (the pool is the caller's: a page that is not appended to may hold inputs)
+  const Span ins[] = {heads_span(k_new, batch, kNumKvHeads),
+                      heads_span(v_new, batch, kNumKvHeads),
+                      heads_span(q_in, batch),
+                      ints(block_table, rows * max_blocks),
+                      ints(positions, rows),
+                      ints(slots, rows)};
+  const Span outs[] = {heads_span(q_out, batch), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
+  if (overlap(outs[0], pages_span(pool, num_pages)) ||
+      overlap(outs[1], pages_span(pool, num_pages)))
+    return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   pkv::RopeFreqs freqs;
@@ -1073,13 +1120,19 @@ PKV_API int pkv_paged_chunk_attention(
       !aligned(token_offsets, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
       !aligned(dev_err, 4))
     return PKV_EALIGN;
-  if (overlap(q, q_row_bytes(num_tokens), out, q_row_bytes(num_tokens))) return PKV_EINVAL;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(q, num_tokens), ints(token_offsets, seqs + 1),
+                      pages_span(pool, num_pages), ints(block_table, seqs * max_blocks),
+                      ints(seq_lens, seqs)};
+  const Span outs[] = {heads_span(out, num_tokens), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0 || num_tokens == 0) return PKV_OK;
   ChunkPlan plan;
   if (!chunk_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
     return PKV_ECUDA;
   if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
     return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, plan.workspace}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.pool = pool;
@@ -1143,13 +1196,18 @@ PKV_API int pkv_paged_window_attention(
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 4) || !aligned(workspace, 16) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(dev_err, 4))
     return PKV_EALIGN;
-  if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(q, batch), pages_span(pool, num_pages),
+                      ints(block_table, seqs * max_blocks), ints(seq_lens, seqs)};
+  const Span outs[] = {heads_span(out, batch), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
   const int splits =
       one_token_splits(batch, window_pages(max_blocks, window, sinks), num_splits, false);
   if (splits < 1) return PKV_ECUDA;
   const size_t need = part_bytes(batch, splits);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.pool = pool;
@@ -1204,13 +1262,21 @@ PKV_API int pkv_paged_scored_attention(
       !aligned(mass, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
       !aligned(dev_err, 4))
     return PKV_EALIGN;
-  if (overlap(q, q_row_bytes(batch), out, q_row_bytes(batch))) return PKV_EINVAL;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(q, batch), pages_span(pool, num_pages),
+                      ints(block_table, seqs * max_blocks), ints(seq_lens, seqs)};
+  const Span outs[] = {heads_span(out, batch),
+                       rows_span(mass, seqs * kNumKvHeads, mass_stride,
+                                 static_cast<int64_t>(max_blocks) * kPageSize),
+                       ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
   const int splits = one_token_splits(batch, max_blocks, num_splits, true);
   if (splits < 1) return PKV_ECUDA;
   const size_t parts = part_bytes(batch, splits), keep = score_bytes(batch, max_blocks, splits);
   if (parts + keep > 0 && (workspace == nullptr || workspace_bytes < parts + keep))
     return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, parts + keep}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.pool = pool;
@@ -1264,21 +1330,16 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
       !aligned(seq_lens, 4) || !aligned(dst_block_table, 4) || !aligned(new_lens, 4) ||
       !aligned(new_mass, 4) || !aligned(kept, 4) || !aligned(dev_err, 4))
     return PKV_EALIGN;
-  // the outputs are written while the inputs are still read
-  const size_t rows = static_cast<size_t>(batch) * kNumKvHeads;
-  const struct { const void* p; size_t n; } in[] = {
-      {mass, rows * mass_stride * 4}, {seq_lens, static_cast<size_t>(batch) * 4},
-      {block_table, static_cast<size_t>(batch) * max_blocks * 4},
-      {dst_block_table, static_cast<size_t>(batch) * dst_max_blocks * 4}};
-  const struct { const void* p; size_t n; } outs[] = {
-      {new_lens, static_cast<size_t>(batch) * 4}, {new_mass, rows * new_mass_stride * 4},
-      {kept, rows * budget * 4}};
-  for (int o = 0; o < 3; ++o) {
-    for (const auto& i : in)
-      if (overlap(outs[o].p, outs[o].n, i.p, i.n)) return PKV_EINVAL;
-    for (int p = 0; p < o; ++p)
-      if (overlap(outs[o].p, outs[o].n, outs[p].p, outs[p].n)) return PKV_EINVAL;
-  }
+  const size_t seqs = static_cast<size_t>(batch), rows = seqs * kNumKvHeads;
+  const Span ins[] = {rows_span(mass, rows, mass_stride,
+                                static_cast<int64_t>(max_blocks) * kPageSize),
+                      pages_span(pool, num_pages), ints(seq_lens, seqs),
+                      ints(block_table, seqs * max_blocks),
+                      ints(dst_block_table, seqs * dst_max_blocks)};
+  const Span outs[] = {ints(new_lens, seqs),
+                       rows_span(new_mass, rows, new_mass_stride, new_mass_stride),
+                       ints(kept, rows * budget), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
   pkv::EvictArgs a = {};
   a.mass = mass;
