@@ -1007,15 +1007,17 @@ bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks
   plan->num_splits = static_cast<int>(items > 0 ? s : 1);
   // short chunks: one wave of the CTAs that fit (short_chunk.cu: three per SM
   // beside a long chunk, else four), eight pages a range or more; more tokens
-  // than short chunks of this batch can have mean a long one.  (32 x 4 tokens
-  // over 4096: 69 us in one range, 58 us in two; 64 x 4 over 2048 53 and 60.)
+  // than short chunks of this batch can have mean a long one, or a padded q: one
+  // sequence gets its ranges all the same.  (32 x 4 tokens over 4096: 69 us in
+  // one range, 58 us in two; 64 x 4 over 2048 53 and 60.  One sequence of 4
+  // tokens in a q of 8 rows, over 2048, 16384 and 131072: 17, 28 and 69 us, in
+  // one range 30, 155 and 1350; a long chunk pays the merge, 1 us.)
   long long t = num_splits;
   if (t == 0) {
     const bool a_long_one = num_tokens > pkv::kShortTokens * static_cast<long long>(batch);
     const long long most = a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens);
     t = std::max(1LL, std::min((a_long_one ? 3LL : 4LL) * sms / (most * kNumKvHeads),
                                (pages + 7) / 8));
-    if (num_tokens > pkv::kShortTokens && batch == 1) t = 1;
   }
   plan->short_splits = static_cast<int>(std::min(t, pages));
   plan->grid = static_cast<int>(std::min<long long>(sms > 0 ? sms : 1, items * s));
