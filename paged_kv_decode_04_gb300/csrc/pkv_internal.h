@@ -303,7 +303,10 @@ cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream);
 // (no window then), and the merge of the ranges when args.num_splits > 1.
 // Scores (weights wanted only) are kept in shared memory for score_pages
 // pages, at most kScoredSmemPages, when args.scores is null (one range then).
-constexpr int kScoredSmemPages = 256;
+// That many leave room for two CTAs an SM, which the kernel's rings are made for:
+// 128 sequences of up to 3060 tokens (192 pages) took 141 us with one CTA an SM,
+// 125 with the scores in the workspace and two ranges; of up to 2950 113 and 121.
+constexpr int kScoredSmemPages = 191;
 cudaError_t launch_window_attention(const CUtensorMap& pool_map, const MaskedArgs& args,
                                     int score_pages, cudaStream_t stream);
 

@@ -67,6 +67,11 @@ constexpr size_t win_smem(int score_pages) {
          static_cast<size_t>(score_pages) * kPageScoreBytes;
 }
 
+// Shared memory of an SM, a KiB of it taken by each CTA.
+constexpr size_t kSmemOfSm = 228 * 1024;
+static_assert(Shape<true>::kCtas * (win_smem<true>(kScoredSmemPages) + 1024) <= kSmemOfSm,
+              "the scores kept in shared memory leave room for every CTA of an SM");
+
 // The list of pages a query at position L - 1 sees.
 struct Visible {
   int L, lo, sinks;  // t < L and (t >= lo or t < sinks)
