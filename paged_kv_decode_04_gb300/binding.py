@@ -699,11 +699,19 @@ def _new(shape, dtype, index, stream):
     return t
 
 
+def _there(index, f, *args):
+    """f(*args) with device `index` current."""
+    if torch._C._cuda_getDevice() == index:
+        return f(*args)
+    with torch.cuda.device(index):
+        return f(*args)
+
+
 def _scratch(ws, need, index, stream):
     """(tensor, pointer, bytes) of the caller's workspace, or of a new one of
-    need() bytes."""
+    need() bytes (which depend on the device's number of SMs)."""
     if ws is None:
-        n = need()
+        n = _there(index, need)
         if not n:
             return None, None, 0
         ws = _new(n, torch.uint8, index, stream)
@@ -723,18 +731,15 @@ def _on(index, stream):
 
 def _launch(f, index, *args):
     """Call entry point `f` with the tensors' device current."""
-    if torch._C._cuda_getDevice() == index:
-        rc = f(*args)
-    else:
-        with torch.cuda.device(index):
-            rc = f(*args)
+    rc = _there(index, f, *args)
     if rc != PKV_OK:
         raise PkvError(rc, f.__name__)
 
 
 def chunk_workspace_bytes(num_tokens: int, batch: int, max_blocks: int, num_splits: int = 0, *,
                           window: int = 0, sinks: int = 0) -> int:
-    """Workspace bytes of paged_chunk_attention for these sizes."""
+    """Workspace bytes of paged_chunk_attention for these sizes on the current
+    device."""
     return _bytes(_lib.pkv_chunk_workspace_bytes(
         _count(num_tokens, "num_tokens"), _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS,
         HEAD_DIM, _count(max_blocks, "max_blocks"), _count(window, "window"),
@@ -782,7 +787,8 @@ def paged_chunk_attention(q, token_offsets, pool, block_table, seq_lens, out=Non
 
 def window_workspace_bytes(batch: int, max_blocks: int, window: int, num_splits: int = 0, *,
                            sinks: int = 0) -> int:
-    """Workspace bytes of paged_window_attention for these sizes."""
+    """Workspace bytes of paged_window_attention for these sizes on the current
+    device."""
     return _bytes(_lib.pkv_window_workspace_bytes(
         _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
         _count(max_blocks, "max_blocks"), _count(window, "window", 1), _count(sinks, "sinks"),
@@ -817,7 +823,8 @@ def paged_window_attention(q, pool, block_table, seq_lens, window: int, out=None
 
 
 def scored_workspace_bytes(batch: int, max_blocks: int, num_splits: int = 0) -> int:
-    """Workspace bytes of paged_scored_attention for these sizes."""
+    """Workspace bytes of paged_scored_attention for these sizes on the current
+    device."""
     return _bytes(_lib.pkv_scored_workspace_bytes(
         _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
         _count(max_blocks, "max_blocks"), _count(num_splits, "num_splits")),
