@@ -550,7 +550,10 @@ PKV_API int pkv_paged_chunk_attention(
     int sinks, float scale, pkv_bf16* out, void* workspace, size_t workspace_bytes,
     int num_splits, int32_t* dev_err, pkv_stream_t stream);
 
-/* Bytes of workspace that call needs; (size_t)-1 for invalid sizes. */
+/* Bytes of workspace that call needs on the current device; (size_t)-1 for
+ * invalid sizes.  With automatic ranges the need does not grow with the sizes
+ * (4096 tokens may need none where 64 do): a buffer for calls of several sizes
+ * takes the largest of their needs.  The same holds for the two sizes below. */
 PKV_API size_t pkv_chunk_workspace_bytes(int num_tokens, int batch, int num_q_heads,
                                          int num_kv_heads, int head_dim, int max_blocks,
                                          int window, int sinks, int num_splits);

@@ -739,7 +739,8 @@ def _launch(f, index, *args):
 def chunk_workspace_bytes(num_tokens: int, batch: int, max_blocks: int, num_splits: int = 0, *,
                           window: int = 0, sinks: int = 0) -> int:
     """Workspace bytes of paged_chunk_attention for these sizes on the current
-    device."""
+    device.  More tokens may need less (longer chunks need fewer ranges): a
+    buffer for several sizes takes the largest of their needs."""
     return _bytes(_lib.pkv_chunk_workspace_bytes(
         _count(num_tokens, "num_tokens"), _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS,
         HEAD_DIM, _count(max_blocks, "max_blocks"), _count(window, "window"),
@@ -788,7 +789,7 @@ def paged_chunk_attention(q, token_offsets, pool, block_table, seq_lens, out=Non
 def window_workspace_bytes(batch: int, max_blocks: int, window: int, num_splits: int = 0, *,
                            sinks: int = 0) -> int:
     """Workspace bytes of paged_window_attention for these sizes on the current
-    device."""
+    device; a larger batch may need less."""
     return _bytes(_lib.pkv_window_workspace_bytes(
         _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
         _count(max_blocks, "max_blocks"), _count(window, "window", 1), _count(sinks, "sinks"),
@@ -824,7 +825,7 @@ def paged_window_attention(q, pool, block_table, seq_lens, window: int, out=None
 
 def scored_workspace_bytes(batch: int, max_blocks: int, num_splits: int = 0) -> int:
     """Workspace bytes of paged_scored_attention for these sizes on the current
-    device."""
+    device; a larger batch may need less."""
     return _bytes(_lib.pkv_scored_workspace_bytes(
         _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
         _count(max_blocks, "max_blocks"), _count(num_splits, "num_splits")),
