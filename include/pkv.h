@@ -520,8 +520,9 @@ PKV_API int pkv_paged_decode_attention_static_ws(
  * Sequence b owns rows [token_offsets[b], token_offsets[b+1]) of q and out
  * (none is allowed); its i-th of n tokens stands at position seq_lens[b] - n
  * + i and sees the tokens above.  Scores, softmax and sums are FP32; the
- * weights enter the product with V as bf16 (the row sums take them unrounded)
- * and the output is rounded to bf16 once.
+ * weights enter the product with V as bf16 (two bf16 terms in chunks of up to 4
+ * tokens, as in the one-token calls; the row sums take them unrounded) and the
+ * output is rounded to bf16 once.
  *
  *   q, out         [num_tokens][num_q_heads][head_dim] bf16 (q rotated)
  *   token_offsets  int32 [batch + 1], non-decreasing, in [0, num_tokens];

@@ -17,7 +17,11 @@
 // of the sequence, of the window and of the sinks.  There the scores of unseen
 // tokens become -inf, and non-finite V values become zero in shared memory
 // (0 x NaN is NaN) and are added again at the end for the rows that see them.
-// Weights enter the product with V as bf16, as in the tcgen05 kernel.
+// Weights enter the product with V as two bf16 terms (16 significant bits), as
+// in the one-token kernels, so a single token's result has their precision
+// whichever call makes it.  The second term costs the 64 x 4 tokens over 2048
+// 42.3 -> 43.3 us; moving the terms between the lanes with shuffles instead of
+// movmatrix 44.7.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -54,10 +58,18 @@ struct TileState {
   float oacc[4][4];
 };
 
+// An 8 x 8 matrix of 16-bit values, lane l holding columns 2 (l & 3) and + 1 of
+// row l / 4, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Fold a page's masked scores of one n-tile into S.  va: the page's V^T
 // fragments (4 tiles of 16 dims).
 __device__ __forceinline__ void fold_tile(const float (&s)[4], const uint32_t (&va)[4][4], float c,
-                                          const LaneGeom& G, TileState& S) {
+                                          TileState& S) {
   float mx0 = fmaxf(s[0], s[2]) * c;
   float mx1 = fmaxf(s[1], s[3]) * c;
   const bool grow = mx0 > S.m_ref[0] + kRescaleLog2 || mx1 > S.m_ref[1] + kRescaleLog2;
@@ -90,16 +102,19 @@ __device__ __forceinline__ void fold_tile(const float (&s)[4], const uint32_t (&
   }
   S.l_run[0] += p[0] + p[2];
   S.l_run[1] += p[1] + p[3];
-  const uint32_t even = pack_bf16x2(p[0], p[2]), odd = pack_bf16x2(p[1], p[3]);
-  const uint32_t ea = __shfl_sync(kFullMask, even, G.src_a);
-  const uint32_t oa = __shfl_sync(kFullMask, odd, G.src_a);
-  const uint32_t eb = __shfl_sync(kFullMask, even, G.src_b);
-  const uint32_t ob = __shfl_sync(kFullMask, odd, G.src_b);
-  const uint32_t wa = G.odd_row ? oa : ea;  // tokens 2ft (lo), 2ft+8 (hi)
-  const uint32_t wb = G.odd_row ? ob : eb;  // tokens 2ft+1 (lo), 2ft+9 (hi)
-  const uint32_t b0 = prmt(wa, wb, 0x5410u), b1 = prmt(wa, wb, 0x7632u);
+  // The weights of tokens fg and fg + 8 (rows 2ft, 2ft + 1) as hi + lo bf16
+  // terms, transposed into P^T fragments (tokens 2ft, 2ft + 1 of row fg)
+  const uint32_t h0 = pack_bf16x2(p[0], p[1]), h1 = pack_bf16x2(p[2], p[3]);
+  const uint32_t l0 = pack_bf16x2(p[0] - __uint_as_float(h0 << 16),
+                                  p[1] - __uint_as_float(h0 & 0xFFFF0000u));
+  const uint32_t l1 = pack_bf16x2(p[2] - __uint_as_float(h1 << 16),
+                                  p[3] - __uint_as_float(h1 & 0xFFFF0000u));
+  const uint32_t th0 = transpose8x8(h0), th1 = transpose8x8(h1);
+  const uint32_t tl0 = transpose8x8(l0), tl1 = transpose8x8(l1);
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) mma_16816_bf16(S.oacc[mt], va[mt], b0, b1);
+  for (int mt = 0; mt < 4; ++mt) mma_16816_bf16(S.oacc[mt], va[mt], th0, th1);
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) mma_16816_bf16(S.oacc[mt], va[mt], tl0, tl1);
 }
 
 // Place of query row r of (sequence, kv head) among the partials.
@@ -290,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kStages))
                       va[mt]);
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
-        if (i < tiles) fold_tile(s[i], va, c, G, S[i]);
+        if (i < tiles) fold_tile(s[i], va, c, S[i]);
     }
     __syncwarp();
     // refill the stage with the page kStages ahead
