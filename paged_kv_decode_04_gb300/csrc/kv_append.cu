@@ -87,11 +87,13 @@ __global__ void __launch_bounds__(kAppendThreads)
       pos_ok ? block_table[static_cast<int64_t>(b) * max_blocks + at / kPageSize] : -1;
   // Past the table the FP64 sincos of a pair is taken once and shared by the
   // 8 heads' threads (FP64 runs at a small fraction of FP32's rate here: 2048
-  // sequences far past the table took 36.4 us with one for every thread, 16.2
-  // this way, near ones 11.4).
+  // sequences far past the table took 36.4 us with one for every thread, 15.4
+  // this way).  The choice is the same in every thread without a
+  // vote, which near tokens would pay for (2048 sequences: 12.0 us with one, 11.7
+  // without); a table that is still being built is left to each thread.
   __shared__ double2 s_cs[kHalf];
   RopeCS cs;
-  if (__syncthreads_or(!table_ok || pos < 0 || pos >= kRopeTablePositions)) {
+  if (freqs.table_theta == nullptr || pos < 0 || pos >= kRopeTablePositions) {
     if (h == 0) {
       const RopeCS f = rope_cs(freqs, false, pos, i);
       s_cs[i] = make_double2(f.c64, f.s64);
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     cs.s32 = static_cast<float>(cs.s64);
     cs.have64 = true;
   } else {
-    cs = rope_cs(freqs, true, pos, i);
+    cs = rope_cs(freqs, table_ok, pos, i);
   }
 
   // Optional out-of-place query rotation: 32 heads x 32 pairs, 4 per thread.
