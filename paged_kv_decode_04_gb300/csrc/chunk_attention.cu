@@ -35,7 +35,7 @@
 //             replaces non-finite V values by zero (a masked weight is zero,
 //             but 0 x NaN is not); rows that do see such a value get it added
 //             in the epilogue
-// Measured on 2 x 4096 tokens over 8192 (391 GFLOP): 356 us, 1.10 PFLOP/s, 0.59
+// Measured on 2 x 4096 tokens over 8192 (391 GFLOP): 354 us, 1.10 PFLOP/s, 0.59
 // of the card's cuBLAS bf16 rate.  A unit takes 1060 cycles of an SM, of which
 // its MMAs fill 440 and its exponentials 546 (30 a clock), the rest being the
 // latencies of the chain scores -> registers -> P -> PV; the two groups' chains
@@ -54,7 +54,7 @@
 //    the compiler short of registers, and all 64 words stored at the end cost
 //    451 us);
 //  * the relay of V scans only the pages that some row does not see (a prompt
-//    of 8192 under a window of 1024: 109 -> 104 us);
+//    of 8192 under a window of 1024: 109 -> 104 us then);
 //  * not: 16 softmax warps of half a row each (558 us: twice the hand-over
 //    instructions), four groups of 128 x 64 units with P over S (485 us: twice
 //    the units for the issuing warps), the row in two rolled halves with S given

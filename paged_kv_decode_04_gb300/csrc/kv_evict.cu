@@ -18,7 +18,7 @@
 // so a (sequence, kv head) gets several CTAs, each of which repeats the
 // selection and copies its own part of the kept rows -- one launch, and no
 // CTA waits for another.  64 sequences of 4096 tokens down to 1024 (279 MB)
-// took 65 us, 4.3 TB/s, 58 us on the device; about 12 us of it are the
+// took 63 us, 4.4 TB/s, 57 us on the device; about 12 us of it are the
 // selection, in which every CTA of the one wave is at once.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -53,8 +53,9 @@ struct Shape {
 constexpr int kBins = 2048;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kLoads = 8;  // weights a thread has in flight
-// Tokens whose rows a group of 8 lanes has in flight (two: 65.4 us on the batch
-// above, three 65.0, four spill registers: 71.3; 512 threads and two CTAs 77.7).
+// Tokens whose rows a group of 8 lanes has in flight (when chosen, two: 65.4 us on
+// the batch above, three 65.0, four spill registers: 71.3; 512 threads and two
+// CTAs 77.7).
 constexpr int kCopyRows = 3;
 
 // Order-preserving key of a weight.

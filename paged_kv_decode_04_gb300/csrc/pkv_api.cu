@@ -938,9 +938,9 @@ bool chunk_q_map(const void* q, int num_tokens, CUtensorMap* out) {
 // Ranges of a one-token call whose sequences see at most `pages` pages: CTAs for
 // two an SM (scored: one and a half), but 20 pages a range or more (scored: 48,
 // its merge also adds the weights), where a range's streaming is as long as the
-// merge it costs.  One sequence of 4093: 14 us in 8 ranges, 37 in one, 18 in 32;
-// 34 of 403: 12 us in one, 18 in three.  Scored: one of 4093 21 us in 8, 31 in
-// one, 23 in 32; 36 of 1076 23 us in one, 33 in two.
+// merge it costs.  With cold caches, one sequence of 4093: 14 us in 8 ranges, 37
+// in one, 18 in 32; 34 of 403: 12 us in one, 18 in three.  Scored: one of 4093
+// 21 us in 8, 31 in one, 23 in 32; 36 of 1076 23 us in one, 33 in two.
 int one_token_splits(int batch, long long pages, int num_splits, bool scored) {
   if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, pages));
   const int sms = current_sm_count();
