@@ -188,6 +188,35 @@ __device__ __forceinline__ void attend_page(uint32_t kt, int valid, const uint32
   fold_page(kt, s, c, G, S);
 }
 
+// A row's accumulators of dims 2 lane and 2 lane + 1 where it sees V values that
+// are not finite: their sum, whatever the weights, which are positive.  (The
+// products do not give it: the lo term of a weight may be 0 or negative.)  Rare,
+// so plain loads: page_of(i) is the i-th page of [i0, i1), seen(page) the mask
+// of its tokens that the row sees.
+template <typename PageOf, typename Seen>
+__device__ __forceinline__ void set_nonfinite(float2& O, const uint16_t* pool, int64_t num_pages,
+                                              const int32_t* table, int g, int lane, int i0,
+                                              int i1, const PageOf& page_of, const Seen& seen) {
+  float2 f = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    const int page = page_of(i), pid = table[page];
+    if (pid < 0 || pid >= num_pages) continue;
+    const uint32_t vis = seen(page);
+#pragma unroll 1
+    for (int t = 0; t < kPageSize; ++t) {
+      if (!((vis >> t) & 1u)) continue;
+      const float2 v = bf16x2_to_float2(reinterpret_cast<const uint32_t*>(
+          pool + (((static_cast<int64_t>(pid) * 2 + 1) * kPageSize + t) * kNumKvHeads + g) *
+                     kHeadDim)[lane]);
+      if (!(fabsf(v.x) < INFINITY)) f.x += v.x;
+      if (!(fabsf(v.y) < INFINITY)) f.y += v.y;
+    }
+  }
+  if (f.x != 0.f) O.x = f.x;
+  if (f.y != 0.f) O.y = f.y;
+}
+
 // Sum the lanes' shares of the row sums (lanes with the same ft).
 __device__ __forceinline__ void reduce_row_sums(AttnState& S) {
 #pragma unroll

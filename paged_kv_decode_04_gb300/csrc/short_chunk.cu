@@ -16,7 +16,7 @@
 // t < sinks), so the rows of a page differ in what they see only near the end
 // of the sequence, of the window and of the sinks.  There the scores of unseen
 // tokens become -inf, and non-finite V values become zero in shared memory
-// (0 x NaN is NaN) and are added again at the end for the rows that see them.
+// (0 x NaN is NaN); a row that sees such a value gets it at the end.
 // Weights enter the product with V as two bf16 terms (16 significant bits), as
 // in the one-token kernels, so a single token's result has their precision
 // whichever call makes it.  The second term costs the 64 x 4 tokens over 2048
@@ -370,27 +370,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kStages))
       O.x = fmaf(wt, os.x, O.x);
       O.y = fmaf(wt, os.y, O.y);
     }
-    if (any_nonfinite) {
-      // (rare: plain loads of the pages that some row sees in part)
-      const int pos = pos0 + r / kGroup;
-      for (int i = r0; i < r1; ++i) {
-        const int base = (i < ns ? i : w0 + (i - ns)) * kPageSize;
-        if (base + kPageSize - 1 <= pos0 && (base >= last_lo || base + kPageSize <= a.sinks))
-          continue;
-        const int pid =
-            a.block_table[static_cast<int64_t>(b) * a.max_blocks + base / kPageSize];
-        if (pid < 0 || pid >= a.num_pages) continue;
-        const uint32_t vis = seen_by(base, pos);
-        for (int t = 0; t < kPageSize; ++t) {
-          if (!((vis >> t) & 1u)) continue;
-          const float2 v = bf16x2_to_float2(reinterpret_cast<const uint32_t*>(
-              a.pool + (((static_cast<int64_t>(pid) * 2 + 1) * kPageSize + t) * kNumKvHeads + g) *
-                           kHeadDim)[lane]);
-          if (!(fabsf(v.x) < INFINITY)) O.x += v.x;
-          if (!(fabsf(v.y) < INFINITY)) O.y += v.y;
-        }
-      }
-    }
+    // seen values that are not finite: some were replaced, or a product with
+    // them is NaN (a row whose sum is stays so)
+    if (any_nonfinite || __any_sync(kFullMask, (O.x != O.x || O.y != O.y) && Ls == Ls))
+      set_nonfinite(
+          O, a.pool, a.num_pages, a.block_table + static_cast<int64_t>(b) * a.max_blocks, g, lane,
+          r0, r1, [&](int i) { return i < ns ? i : w0 + (i - ns); },
+          [&](int page) { return seen_by(page * kPageSize, pos0 + r / kGroup); });
     const int64_t row =
         static_cast<int64_t>(o0 + r / kGroup) * kNumQHeads + g * kGroup + r % kGroup;
     if (a.short_splits > 1) {
