@@ -278,6 +278,11 @@ __global__ void __launch_bounds__(Shape<kScored>::kThreads, Shape<kScored>::kCta
       O.x = fmaf(wt, os.x, O.x);
       O.y = fmaf(wt, os.y, O.y);
     }
+    // seen values that are not finite (a row whose sum is NaN stays so)
+    if (__any_sync(kFullMask, (O.x != O.x || O.y != O.y) && Ls == Ls))
+      set_nonfinite(
+          O, a.pool, a.num_pages, a.block_table + static_cast<int64_t>(b) * a.max_blocks, g, lane,
+          r0, r1, [&](int i) { return V.page(i); }, [&](int page) { return V.mask(page); });
     const int64_t row = static_cast<int64_t>(b) * kNumQHeads + g * kGroup + r;
     if (a.num_splits > 1) {
       const int64_t part = row * a.num_splits + split;

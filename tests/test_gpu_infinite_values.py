@@ -47,6 +47,33 @@ def check_row(got, q, clean, bt, s, tokens, what):
 
 
 @pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (300, 4), (60, 20)])
+def test_window(window, sinks, splits):
+    dev, b = cuda_or_skip(), binding()
+    pool, clean, bt = cache(131)
+    q = normal((len(LENS), HQ, 64), 132)
+    out = b.paged_window_attention(q.to(dev), pool.to(dev), bt.to(dev),
+                                   torch.tensor(LENS, dtype=torch.int32, device=dev), window,
+                                   sinks=sinks, num_splits=splits).cpu()
+    for s, n in enumerate(LENS):
+        check_row(out[s], q[s], clean, bt, s, visible(n - 1, window, sinks), f"sequence {s}")
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_scored(splits):
+    dev, b = cuda_or_skip(), binding()
+    pool, clean, bt = cache(133)
+    q = normal((len(LENS), HQ, 64), 134)
+    mass = torch.zeros((len(LENS), 8, bt.shape[1] * P), device=dev)
+    out = b.paged_scored_attention(q.to(dev), pool.to(dev), bt.to(dev),
+                                   torch.tensor(LENS, dtype=torch.int32, device=dev), mass,
+                                   num_splits=splits).cpu()
+    assert torch.isfinite(mass).all()
+    for s, n in enumerate(LENS):
+        check_row(out[s], q[s], clean, bt, s, np.arange(n), f"sequence {s}")
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (300, 4), (60, 20)])
 @pytest.mark.parametrize("counts", [[1, 2, 4], [4, 3, 1], [70, 80, 17], [20, 4, 9]])
 def test_chunk(counts, window, sinks, splits):
