@@ -509,6 +509,8 @@ PKV_API int pkv_paged_decode_attention_static_ws(
  * and V hold (NaN and infinities included), and a row that sees none is zero.
  * A seen token whose score is -inf has the weight 0; a row whose seen scores
  * are all -inf is zero.
+ * A dim of a row that sees V values there that are not finite is their sum:
+ * +inf, -inf or NaN.
  */
 
 /*
