@@ -33,7 +33,7 @@ own = False
 HQ, HKV, G, D, P = 32, 8, 4, 64, 16
 SCALE = D ** -0.5
 THETA = 500000.0
-BIAS, LEAST, MOST = 127, 1, 240          # scale exponents: bias, smallest, largest
+BIAS, LEAST, MOST = 127, 3, 240          # scale exponents: bias, smallest, largest
 TOP = {"e4m3": 448.0, "int8": 127.0}     # largest code of each format
 
 
