@@ -98,6 +98,7 @@ typedef struct CUstream_st* pkv_stream_t; /* same type as cudaStream_t */
 #define PKV_DEVERR_TIMEOUT 8u   /* an in-kernel wait for a page copy gave up */
 #define PKV_DEVERR_OFFSETS 16u  /* a token outside the ranges of token_offsets */
 #define PKV_DEVERR_PLAN 32u     /* seq_lens[b] differs from the length a work plan holds */
+#define PKV_DEVERR_VALUE 64u    /* a K or V value given to the 8-bit cache is not finite */
 
 /* Library ABI version (bumped when a signature changes). */
 PKV_API int pkv_abi_version(void);
@@ -652,6 +653,117 @@ PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_b
                              int num_kv_heads, int head_dim, int page_size, double rope_theta,
                              const pkv_bf16* q_in, pkv_bf16* q_out, int num_q_heads,
                              int32_t* dev_err, pkv_stream_t stream);
+
+/*
+ * The 8-bit cache
+ * ---------------
+ * The paged cache at half the bytes: K and V as 8-bit codes with one scale for
+ * each block, the 16 tokens of a page of K or V of one kv head.  (The source
+ * pages have a bf16 cache only; these calls are this library's own.)  Streams,
+ * tables, errors and the refusal of outputs that overlap other arguments are as
+ * above (the pool and the scales are outputs of the calls that write them).
+ *
+ *   pool    [num_pages][2 (K, V)][num_kv_heads][page_size][head_dim] codes of 8
+ *           bits, 16-byte aligned: e4m3 floats (PKV_KV8_E4M3) or signed integers
+ *           in [-127, 127] (PKV_KV8_INT8)
+ *   scales  uint8 [num_pages][2][num_kv_heads], 16-byte aligned: a block's value
+ *           is code * 2^(scale - 127), scale in [3, 240] (other bytes count as
+ *           the nearest of these)
+ *
+ * A block that is given rows of values x gets the scale max(need, its own scale
+ * if it holds earlier tokens): need is the smallest with max |x| <= T *
+ * 2^(need - 127), T = 448 (e4m3) or 127 (int8), within [3, 240]; the codes are x
+ * / 2^(scale - 127), rounded to nearest even (magnitudes past T * 2^113 become
+ * that).  When the scale grows the earlier tokens' codes are rounded again to
+ * it.  A block holds earlier tokens when the first slot that the call writes of
+ * its page is not slot 0; the slots before it are those tokens.  Keys are
+ * rotated and rounded to bf16 as pkv_kv_append does first.  Values that are not
+ * finite are stored as zero and set PKV_DEVERR_VALUE.  Every cached value is a
+ * bf16 number: products of bf16 values with them, and pkv_kv8_read, are exact.
+ * e4m3's NaN codes (0x7F and 0xFF, never written here) may lie in slots that no
+ * query sees; where one is seen the sequence's results are not specified.
+ */
+#define PKV_KV8_E4M3 0
+#define PKV_KV8_INT8 1
+
+/*
+ * pkv_kv8_append -- pkv_kv_append_at into the 8-bit cache: sequence b's token,
+ * its key rotated for positions[b] >= 0, becomes cached token slots[b] of its
+ * table (slots NULL: positions[b]).  The queries' rotation is the same.
+ *   dev_err  PKV_DEVERR_PAGE / _POSITION / _VALUE
+ * No two sequences may name the same page (a page's tokens share their scales).
+ */
+PKV_API int pkv_kv8_append(const pkv_bf16* k_new, const pkv_bf16* v_new, void* pool,
+                           uint8_t* scales, int format, int64_t num_pages,
+                           const int32_t* block_table, int max_blocks, const int32_t* positions,
+                           const int32_t* slots, int batch, int num_kv_heads, int head_dim,
+                           int page_size, double rope_theta, const pkv_bf16* q_in,
+                           pkv_bf16* q_out, int num_q_heads, int32_t* dev_err,
+                           pkv_stream_t stream);
+
+/*
+ * pkv_kv8_write_prefill -- pkv_kv_write_prefill into the 8-bit cache.  A block's
+ * tokens of one call are rounded together, to one scale.
+ *   dev_err  PKV_DEVERR_PAGE / _POSITION (tokens outside the table are skipped)
+ *            / _OFFSETS (a sequence with bad offsets is skipped) / _VALUE
+ * No two sequences may name the same page.
+ */
+PKV_API int pkv_kv8_write_prefill(const pkv_bf16* k, const pkv_bf16* v, int num_tokens,
+                                  const int32_t* token_offsets, const int32_t* start_positions,
+                                  void* pool, uint8_t* scales, int format, int64_t num_pages,
+                                  const int32_t* block_table, int max_blocks, int batch,
+                                  int num_kv_heads, int head_dim, int page_size,
+                                  double rope_theta, int32_t* dev_err, pkv_stream_t stream);
+
+/*
+ * pkv_kv8_read -- cached tokens as bf16, the way back of pkv_kv8_write_prefill
+ * (keys as they are cached, rotated): rows [token_offsets[b], token_offsets[b +
+ * 1]) of k and v ([num_tokens][num_kv_heads][head_dim], 16-byte aligned) become
+ * the cached tokens start_positions[b] and on of sequence b.  Rows of tokens on
+ * a bad page, outside the table or of no sequence are left as they were.
+ *   dev_err  PKV_DEVERR_PAGE / _POSITION / _OFFSETS
+ */
+PKV_API int pkv_kv8_read(const void* pool, const uint8_t* scales, int format, int64_t num_pages,
+                         const int32_t* block_table, int max_blocks,
+                         const int32_t* token_offsets, const int32_t* start_positions,
+                         int num_tokens, int batch, int num_kv_heads, int head_dim, int page_size,
+                         pkv_bf16* k, pkv_bf16* v, int32_t* dev_err, pkv_stream_t stream);
+
+/*
+ * pkv_paged8_decode_attention -- pkv_paged_decode_attention over the 8-bit
+ * cache, with a sliding window and sink tokens where window > 0 (0: the whole
+ * cache).  Scores and softmax are FP32, weights enter the product with V with 22
+ * significant bits, the output is rounded to bf16 once.  Workspace, num_splits
+ * and dev_err as there, sized by pkv_decode8_workspace_bytes().
+ */
+PKV_API int pkv_paged8_decode_attention(
+    const pkv_bf16* q, const void* pool, const uint8_t* scales, int format, int64_t num_pages,
+    const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
+    int num_q_heads, int num_kv_heads, int head_dim, int page_size, int window, int sinks,
+    float scale, pkv_bf16* out, void* workspace, size_t workspace_bytes, int num_splits,
+    int32_t* dev_err, pkv_stream_t stream);
+
+/* Bytes of workspace that call needs on the current device; (size_t)-1 for
+ * invalid sizes.  A larger batch may need less, here and below. */
+PKV_API size_t pkv_decode8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                           int head_dim, int max_blocks, int window, int sinks,
+                                           int num_splits);
+
+/*
+ * pkv_paged8_chunk_attention -- pkv_paged_chunk_attention over the 8-bit cache,
+ * the same arguments and rules, sized by pkv_chunk8_workspace_bytes().
+ */
+PKV_API int pkv_paged8_chunk_attention(
+    const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const void* pool,
+    const uint8_t* scales, int format, int64_t num_pages, const int32_t* block_table,
+    int max_blocks, const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, int window, int sinks, float scale, pkv_bf16* out,
+    void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
+    pkv_stream_t stream);
+
+PKV_API size_t pkv_chunk8_workspace_bytes(int num_tokens, int batch, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int max_blocks,
+                                          int window, int sinks, int num_splits);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,9 @@ _BINDING_NAMES = {
     "kv_append", "paged_decode_attention", "decode_step", "kv_write_prefill", "workspace_bytes", "plan_splits", "strerror",
     "abi_version", "PkvError", "paged_chunk_attention", "chunk_workspace_bytes",
     "paged_window_attention", "window_workspace_bytes", "paged_scored_attention",
-    "scored_workspace_bytes", "kv_evict", "kv_append_at",
+    "scored_workspace_bytes", "kv_evict", "kv_append_at", "kv8_append", "kv8_write_prefill",
+    "kv8_read", "paged8_decode_attention", "decode8_workspace_bytes", "paged8_chunk_attention",
+    "chunk8_workspace_bytes",
 }
 
 

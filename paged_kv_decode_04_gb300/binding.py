@@ -30,6 +30,9 @@ DEVERR_POSITION = 4
 DEVERR_TIMEOUT = 8
 DEVERR_OFFSETS = 16
 DEVERR_PLAN = 32
+DEVERR_VALUE = 64
+KV8_E4M3 = 0
+KV8_INT8 = 1
 PLAN_MAGIC = 0x32564B50
 PLAN_HEADER_WORDS = 12
 
@@ -118,6 +121,25 @@ def _load():
     L.pkv_kv_evict.argtypes = [vp, i64, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
                                vp, i32, vp, vp, i64, vp, vp, vp]
     L.pkv_kv_evict.restype = i32
+    L.pkv_kv8_append.argtypes = [vp, vp, vp, vp, i32, i64, vp, i32, vp, vp, i32, i32, i32, i32,
+                                 f64, vp, vp, i32, vp, vp]
+    L.pkv_kv8_append.restype = i32
+    L.pkv_kv8_write_prefill.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i64, vp, i32, i32, i32,
+                                        i32, i32, f64, vp, vp]
+    L.pkv_kv8_write_prefill.restype = i32
+    L.pkv_kv8_read.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp,
+                               vp, vp]
+    L.pkv_kv8_read.restype = i32
+    L.pkv_decode8_workspace_bytes.argtypes = [i32] * 8
+    L.pkv_decode8_workspace_bytes.restype = sz
+    L.pkv_paged8_decode_attention.argtypes = [vp, vp, vp, i32, i64, vp, i32, vp, i32, i32, i32,
+                                              i32, i32, i32, i32, f32, vp, vp, sz, i32, vp, vp]
+    L.pkv_paged8_decode_attention.restype = i32
+    L.pkv_chunk8_workspace_bytes.argtypes = [i32] * 9
+    L.pkv_chunk8_workspace_bytes.restype = sz
+    L.pkv_paged8_chunk_attention.argtypes = [vp, i32, vp, vp, vp, i32, i64, vp, i32, vp, i32, i32,
+                                             i32, i32, i32, i32, i32, f32, vp, vp, sz, i32, vp, vp]
+    L.pkv_paged8_chunk_attention.restype = i32
     return L
 
 
@@ -934,3 +956,192 @@ def kv_append_at(k_new, v_new, pool, block_table, positions, slots, *,
                 num_pages, block_table.data_ptr(), max_blocks, positions.data_ptr(),
                 slots.data_ptr(), B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, float(rope_theta), q_ptr,
                 out_ptr, 0 if q_ptr is None else NUM_Q_HEADS, _err(dev_err, index), raw)
+
+
+# ----------------------------------------------------------- the 8-bit cache --
+
+_KV8_ROW = (2, NUM_KV_HEADS, PAGE_SIZE, HEAD_DIM)
+_KV8_SCALES = (2, NUM_KV_HEADS)
+_KV8_FORMATS = {torch.float8_e4m3fn: KV8_E4M3, torch.int8: KV8_INT8}
+
+
+def _pool8(pool, scales):
+    """(device index, pages, format) of an 8-bit pool and its scales."""
+    if not (isinstance(pool, torch.Tensor) and pool.dtype in _KV8_FORMATS):
+        raise TypeError("pool must be a float8_e4m3fn or int8 tensor")
+    if pool.dim() != 5 or pool.shape[1:] != _KV8_ROW:
+        raise ValueError("pool must be [num_pages][2][8][16][64] codes")
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    if not pool.is_cuda:
+        raise ValueError(f"pool must be on a CUDA device, not {pool.device}")
+    index, pages = pool.get_device(), pool.shape[0]
+    _is(scales, "scales", torch.uint8, 3, index)
+    if scales.shape[0] != pages or scales.shape[1:] != _KV8_SCALES:
+        raise ValueError(f"scales must be [{pages}][2][8], got {tuple(scales.shape)}")
+    return index, pages, _KV8_FORMATS[pool.dtype]
+
+
+def kv8_append(k_new, v_new, pool, scales, block_table, positions, slots=None, *,
+               rope_theta: float = 500000.0, q_in=None, q_out=None, dev_err=None,
+               stream=None) -> None:
+    """kv_append_at into an 8-bit cache: pool [num_pages][2][8][16][64] codes
+    (float8_e4m3fn or int8), scales uint8 [num_pages][2][8]; a cached value is
+    code * 2**(scale - 127).  Without slots a token's slot is its position.
+    No two sequences may append to the same page."""
+    index, num_pages, fmt = _pool8(pool, scales)
+    _is(block_table, "block_table", _I32, 2, index)
+    _is(positions, "positions", _I32, 1, index)
+    B, max_blocks = block_table.shape
+    _heads(k_new, "k_new", index, B, NUM_KV_HEADS)
+    _heads(v_new, "v_new", index, B, NUM_KV_HEADS)
+    if positions.shape[0] != B:
+        raise ValueError("positions and block_table disagree on the batch")
+    slots_ptr = q_ptr = out_ptr = None
+    if slots is not None:
+        _is(slots, "slots", _I32, 1, index)
+        if slots.shape[0] != B:
+            raise ValueError("slots and block_table disagree on the batch")
+        slots_ptr = slots.data_ptr()
+    if q_in is not None or q_out is not None:
+        _heads(q_in, "q_in", index, B)
+        _heads(q_out, "q_out", index, B)
+        q_ptr, out_ptr = q_in.data_ptr(), q_out.data_ptr()
+    raw = _on(index, stream)
+    if B > 0:
+        _launch(_lib.pkv_kv8_append, index, k_new.data_ptr(), v_new.data_ptr(), pool.data_ptr(),
+                scales.data_ptr(), fmt, num_pages, block_table.data_ptr(), max_blocks,
+                positions.data_ptr(), slots_ptr, B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE,
+                float(rope_theta), q_ptr, out_ptr, 0 if q_ptr is None else NUM_Q_HEADS,
+                _err(dev_err, index), raw)
+
+
+def _ragged(token_offsets, start_positions, block_table, index):
+    """The batch and table width of a ragged batch of tokens."""
+    _is(token_offsets, "token_offsets", _I32, 1, index)
+    _is(start_positions, "start_positions", _I32, 1, index)
+    _is(block_table, "block_table", _I32, 2, index)
+    B, max_blocks = block_table.shape
+    if start_positions.shape[0] != B or token_offsets.shape[0] != B + 1:
+        raise ValueError("start_positions must have batch entries and token_offsets batch + 1")
+    return B, max_blocks
+
+
+def kv8_write_prefill(k, v, token_offsets, start_positions, pool, scales, block_table, *,
+                      rope_theta: float = 500000.0, dev_err=None, stream=None) -> None:
+    """kv_write_prefill into an 8-bit cache (see kv8_append): rows
+    token_offsets[b] .. token_offsets[b + 1] of k and v become the cached tokens
+    start_positions[b] and on of sequence b.  A block's tokens share a scale, so
+    no two sequences may write to the same page."""
+    index, num_pages, fmt = _pool8(pool, scales)
+    B, max_blocks = _ragged(token_offsets, start_positions, block_table, index)
+    rows = _heads(k, "k", index, None, NUM_KV_HEADS)
+    _heads(v, "v", index, rows, NUM_KV_HEADS)
+    raw = _on(index, stream)
+    if rows > 0 and B > 0:
+        _launch(_lib.pkv_kv8_write_prefill, index, k.data_ptr(), v.data_ptr(), rows,
+                token_offsets.data_ptr(), start_positions.data_ptr(), pool.data_ptr(),
+                scales.data_ptr(), fmt, num_pages, block_table.data_ptr(), max_blocks, B,
+                NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, float(rope_theta), _err(dev_err, index), raw)
+
+
+def kv8_read(token_offsets, start_positions, pool, scales, block_table, k, v, *, dev_err=None,
+             stream=None):
+    """Cached tokens of an 8-bit cache as bf16 (exact): rows token_offsets[b] ..
+    token_offsets[b + 1] of k and v ([num_tokens][8][64], written) become the
+    cached tokens start_positions[b] and on of sequence b.  Returns (k, v)."""
+    index, num_pages, fmt = _pool8(pool, scales)
+    B, max_blocks = _ragged(token_offsets, start_positions, block_table, index)
+    rows = _heads(k, "k", index, None, NUM_KV_HEADS)
+    _heads(v, "v", index, rows, NUM_KV_HEADS)
+    raw = _on(index, stream)
+    if rows > 0 and B > 0:
+        _launch(_lib.pkv_kv8_read, index, pool.data_ptr(), scales.data_ptr(), fmt, num_pages,
+                block_table.data_ptr(), max_blocks, token_offsets.data_ptr(),
+                start_positions.data_ptr(), rows, B, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE,
+                k.data_ptr(), v.data_ptr(), _err(dev_err, index), raw)
+    return k, v
+
+
+def decode8_workspace_bytes(batch: int, max_blocks: int, num_splits: int = 0, *, window: int = 0,
+                            sinks: int = 0) -> int:
+    """Workspace bytes of paged8_decode_attention for these sizes on the current
+    device; a larger batch may need less."""
+    return _bytes(_lib.pkv_decode8_workspace_bytes(
+        _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
+        _count(max_blocks, "max_blocks"), _count(window, "window"), _count(sinks, "sinks"),
+        _count(num_splits, "num_splits")), "pkv_decode8_workspace_bytes")
+
+
+def paged8_decode_attention(q, pool, scales, block_table, seq_lens, out=None, *, window: int = 0,
+                            sinks: int = 0, scale: float = None, workspace=None,
+                            num_splits: int = 0, dev_err=None, stream=None) -> torch.Tensor:
+    """paged_decode_attention over an 8-bit cache (see kv8_append), with window >
+    0 over each sequence's newest `window` tokens and its first `sinks`."""
+    index, num_pages, fmt = _pool8(pool, scales)
+    B, max_blocks = _tables(block_table, seq_lens, index)
+    _heads(q, "q", index, B)
+    window, sinks = _count(window, "window"), _count(sinks, "sinks")
+    num_splits = _count(num_splits, "num_splits")
+    raw = _on(index, stream)
+    if out is None:
+        out = _new(q.shape, _BF16, index, stream)
+    else:
+        _heads(out, "out", index, B)
+    if B == 0:
+        return out
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: decode8_workspace_bytes(B, max_blocks, num_splits, window=window,
+                                                   sinks=sinks), index, stream)
+    _launch(_lib.pkv_paged8_decode_attention, index, q.data_ptr(), pool.data_ptr(),
+            scales.data_ptr(), fmt, num_pages, block_table.data_ptr(), max_blocks,
+            seq_lens.data_ptr(), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, window, sinks,
+            _SCALE if scale is None else float(scale), out.data_ptr(), ws_ptr, ws_bytes,
+            num_splits, _err(dev_err, index), raw)
+    return out
+
+
+def chunk8_workspace_bytes(num_tokens: int, batch: int, max_blocks: int, num_splits: int = 0, *,
+                           window: int = 0, sinks: int = 0) -> int:
+    """Workspace bytes of paged8_chunk_attention for these sizes on the current
+    device; more tokens may need less."""
+    return _bytes(_lib.pkv_chunk8_workspace_bytes(
+        _count(num_tokens, "num_tokens"), _count(batch, "batch"), NUM_Q_HEADS, NUM_KV_HEADS,
+        HEAD_DIM, _count(max_blocks, "max_blocks"), _count(window, "window"),
+        _count(sinks, "sinks"), _count(num_splits, "num_splits")), "pkv_chunk8_workspace_bytes")
+
+
+def paged8_chunk_attention(q, token_offsets, pool, scales, block_table, seq_lens, out=None, *,
+                           window: int = 0, sinks: int = 0, scale: float = None, workspace=None,
+                           num_splits: int = 0, dev_err=None, stream=None) -> torch.Tensor:
+    """paged_chunk_attention over an 8-bit cache (see kv8_append).  Without `out`
+    rows of no sequence are zero."""
+    index, num_pages, fmt = _pool8(pool, scales)
+    rows = _heads(q, "q", index, None)
+    _is(token_offsets, "token_offsets", _I32, 1, index)
+    B, max_blocks = _tables(block_table, seq_lens, index)
+    if token_offsets.shape[0] != B + 1:
+        raise ValueError("token_offsets must have batch + 1 entries")
+    window, sinks = _count(window, "window"), _count(sinks, "sinks")
+    num_splits = _count(num_splits, "num_splits")
+    raw = _on(index, stream)
+    if out is None:
+        out = _new(q.shape, _BF16, index, stream)
+        if stream is None:
+            out.zero_()
+        else:
+            with torch.cuda.stream(stream):
+                out.zero_()
+    else:
+        _heads(out, "out", index, rows)
+    if rows == 0 or B == 0:
+        return out
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: chunk8_workspace_bytes(rows, B, max_blocks, num_splits, window=window,
+                                                  sinks=sinks), index, stream)
+    _launch(_lib.pkv_paged8_chunk_attention, index, q.data_ptr(), rows, token_offsets.data_ptr(),
+            pool.data_ptr(), scales.data_ptr(), fmt, num_pages, block_table.data_ptr(), max_blocks,
+            seq_lens.data_ptr(), B, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE, window, sinks,
+            _SCALE if scale is None else float(scale), out.data_ptr(), ws_ptr, ws_bytes,
+            num_splits, _err(dev_err, index), raw)
+    return out

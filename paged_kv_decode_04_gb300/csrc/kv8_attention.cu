@@ -1,0 +1,676 @@
+// kv8_attention.cu -- attention of one new token, or of chunks of a few, per
+// sequence over the 8-bit paged cache, streaming its pages once.
+//
+// One CTA per (sequence, range of the pages that its queries see): a producer
+// warp brings whole pages (16 KiB, all kv heads, one TMA box, and the 16 bytes of
+// their scales) into a ring in shared memory, and warp g of eight takes kv head
+// g's blocks of every page.  So a page is one copy and one barrier for all heads,
+// and the heads' states never meet.
+//
+// mma.sync m16n8k16 in f16, FP32 accumulators, for a page (16 tokens) and a kv
+// head; codes become f16 exactly (one instruction for two e4m3 codes):
+//   S^T = K Q^T    tokens as M, query rows as N.  A lane reads 16 codes in a row
+//                  of K for its four k-steps; which dims share a k-step does not
+//                  matter, as Q's fragments take the same ones.  Q enters as f16
+//                  times the power of two that takes its row's largest magnitude
+//                  to [2^14, 2^15): exact for values down to 2^-31 of it (bf16
+//                  has 8 significant bits, f16 24 bits below that magnitude).
+//   O^T += V^T P^T dims as M.  V^T comes through ldmatrix on 8-bit elements,
+//                  transposed, four tokens to a lane's word; K's rows are read
+//                  in the order that gives P those tokens.
+// The scales of a block stay out of the products: K's goes into the factor of
+// the scores, V's multiplies the page's own product, added to the accumulators in
+// FP32; so weights and codes of f16 keep their range whatever the scales are.
+// Weights are 2^(s - m + 7), m the running reference of decode_page.cuh (which
+// moves when a score passes it by 8, so they stay below 2^15), and enter the
+// product as two f16 terms (22 significant bits, 2^-32 of the reference's weight
+// at the least); for one token the terms are the columns 0-3 and 4-7 of one MMA.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kv8.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "visible.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kWarps = kNumKvHeads;            // and one that loads
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kStages = 6, kCtas = 2;
+constexpr int kTileTokens = kShortTokens;      // tokens of a row tile of a chunk
+constexpr int kOffScales = kStages * kPage8Bytes;
+constexpr int kOffMeta = kOffScales + kStages * kPageScales;
+constexpr int kOffBars = kOffMeta + kStages * 8;
+constexpr size_t kSmem = 1024 + kOffBars + 2 * 8 * kStages;
+static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM fit");
+
+constexpr float kMoveLog2 = 8.f;   // a score this far above the reference moves it
+constexpr float kLift = 7.f;       // weights are 2^(s - m + kLift) <= 2^15
+constexpr float kLowestFloat = -3.402823466e38f;
+
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two 16 x 16 matrices of bytes, transposed: lane l gives the address of row
+// l & 15 of matrix l >> 4 and gets, of each, columns l / 4 and l / 4 + 8 of rows
+// 4 (l & 3) .. + 3.
+__device__ __forceinline__ void ldsm_b8_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
+  float2 f;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, "
+      "y;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(w));
+  return f;
+}
+
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// A lane's places in the fragments.
+struct Lane {
+  int fg, ft;          // fragment row and column group
+  int tok;             // token of row fg of S^T; row fg + 8 is token tok + 2
+  uint32_t k0, k1;     // this lane's 16 codes of both rows of a K block
+  uint32_t v0, v1;     // this lane's rows of V's matrices of dims 0-31 and 32-63
+  __device__ __forceinline__ explicit Lane(int lane) {
+    fg = lane >> 2;
+    ft = lane & 3;
+    tok = 4 * (fg >> 1) + (fg & 1);
+    // 16-byte chunk c of row r lies at chunk c ^ (r / 2 mod 4) (TMA's 64-byte
+    // swizzle)
+    auto at = [](int r, int c) {
+      return static_cast<uint32_t>(r * kHeadDim + ((c ^ ((r >> 1) & 3)) << 4));
+    };
+    k0 = at(tok, ft);
+    k1 = at(tok + 2, ft);
+    v0 = at(lane & 15, lane >> 4);
+    v1 = at(lane & 15, 2 + (lane >> 4));
+  }
+};
+
+// Online softmax of 8 query rows (columns of S^T) of a warp.
+struct State {
+  float m[2], l[2];    // of columns 2 ft, 2 ft + 1: reference, this lane's share of the sum
+  float2 o[4][2];      // O^T: dims 16 mt + fg (+ 8), columns 2 ft, 2 ft + 1
+  __device__ __forceinline__ void reset() {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) o[mt][0] = o[mt][1] = make_float2(0.f, 0.f);
+  }
+};
+
+// Q^T as B fragments of a row of q: column fg's dims 16 ft + 4 kk + {0, 1} and
+// {2, 3}.  Returns the power of two that undoes the row's own (the same in the
+// row's four lanes).
+__device__ __forceinline__ float load_q(const uint16_t* row, int ft, uint32_t (&qb)[4][2]) {
+  uint32_t w[8];
+  if (row != nullptr) {
+    const uint4 a = reinterpret_cast<const uint4*>(row)[2 * ft];
+    const uint4 b = reinterpret_cast<const uint4*>(row)[2 * ft + 1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0u;
+  }
+  uint32_t top = 0;  // largest finite magnitude
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu & ~nonfinite_halves(w[i]));
+  top = max(top & 0xFFFFu, top >> 16);
+  top = max(top, __shfl_xor_sync(kFull, top, 1));
+  top = max(top, __shfl_xor_sync(kFull, top, 2));
+  // 2^(14 - exponent), within normal numbers
+  const int up = min(max(14 + 127 - static_cast<int>(top >> 7), -126), 126);
+  const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = bf16x2_to_float2(w[i]);
+    qb[i >> 1][i & 1] = pack_f16x2(x.x * f, x.y * f);
+  }
+  return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+}
+
+// A K block's rows as A fragments of the four k-steps.
+template <int kFmt>
+__device__ __forceinline__ void load_k(uint32_t kt, const Lane& P, uint32_t (&ka)[4][4]) {
+  const uint4 x = lds128(kt + P.k0), y = lds128(kt + P.k1);
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    decode_f16<kFmt>(a[kk], ka[kk][0], ka[kk][2]);
+    decode_f16<kFmt>(b[kk], ka[kk][1], ka[kk][3]);
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void load_v(uint32_t vt, const Lane& P, uint32_t (&va)[4][4]) {
+  uint32_t r[8];
+  ldsm_b8_trans(vt + P.v0, *reinterpret_cast<uint32_t(*)[4]>(&r[0]));
+  ldsm_b8_trans(vt + P.v1, *reinterpret_cast<uint32_t(*)[4]>(&r[4]));
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+    decode_f16<kFmt>(r[2 * mt], va[mt][0], va[mt][2]);
+    decode_f16<kFmt>(r[2 * mt + 1], va[mt][1], va[mt][3]);
+  }
+}
+
+// Fold a page's masked scores (in log2 units) into S.  kOne: columns 4-7 stand
+// for the same rows as 0-3 and take the weights' second term.
+template <bool kOne>
+__device__ __forceinline__ void fold(const float (&x)[4], const uint32_t (&va)[4][4], float sv,
+                                     int ft, State& S) {
+  float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+  if (__any_sync(kFull, mx0 > S.m[0] + kMoveLog2 || mx1 > S.m[1] + kMoveLog2)) {
+#pragma unroll
+    for (int i = 4; i <= 16; i <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, i));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, i));
+    }
+    const float m0 = fmaxf(S.m[0], mx0), m1 = fmaxf(S.m[1], mx1);
+    // (0 until the row has seen a score above -inf)
+    const float2 alpha = make_float2(fast_exp2(S.m[0] - fmaxf(m0, kLowestFloat)),
+                                     fast_exp2(S.m[1] - fmaxf(m1, kLowestFloat)));
+    S.l[0] *= alpha.x;
+    S.l[1] *= alpha.y;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      S.o[mt][0] = fmul2(S.o[mt][0], alpha);
+      S.o[mt][1] = fmul2(S.o[mt][1], alpha);
+    }
+    S.m[0] = m0;
+    S.m[1] = m1;
+  }
+  const float d0 = kLift - fmaxf(S.m[0], kLowestFloat), d1 = kLift - fmaxf(S.m[1], kLowestFloat);
+  const float p0 = fast_exp2(x[0] + d0), p1 = fast_exp2(x[1] + d1);
+  const float p2 = fast_exp2(x[2] + d0), p3 = fast_exp2(x[3] + d1);
+  S.l[0] += p0 + p2;
+  S.l[1] += p1 + p3;
+  const uint32_t h0 = pack_f16x2(p0, p1), h1 = pack_f16x2(p2, p3);
+  const float2 f0 = f16x2_to_float2(h0), f1 = f16x2_to_float2(h1);
+  const uint32_t l0 = pack_f16x2(p0 - f0.x, p1 - f0.y), l1 = pack_f16x2(p2 - f1.x, p3 - f1.y);
+  const float2 s2 = make_float2(sv, sv);
+  if constexpr (kOne) {
+    const uint32_t b0 = transpose8x8(ft < 2 ? h0 : l0), b1 = transpose8x8(ft < 2 ? h1 : l1);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_16816_f16(t, va[mt], b0, b1);
+      S.o[mt][0] = ffma2(make_float2(t[0], t[1]), s2, S.o[mt][0]);
+      S.o[mt][1] = ffma2(make_float2(t[2], t[3]), s2, S.o[mt][1]);
+    }
+  } else {
+    const uint32_t th0 = transpose8x8(h0), th1 = transpose8x8(h1);
+    const uint32_t tl0 = transpose8x8(l0), tl1 = transpose8x8(l1);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_16816_f16(t, va[mt], th0, th1);
+      mma_16816_f16(t, va[mt], tl0, tl1);
+      S.o[mt][0] = ffma2(make_float2(t[0], t[1]), s2, S.o[mt][0]);
+      S.o[mt][1] = ffma2(make_float2(t[2], t[3]), s2, S.o[mt][1]);
+    }
+  }
+}
+
+// Zero the V rows of a block whose tokens are not in `vis`: their codes may be
+// NaN, and 0 x NaN is not 0.
+__device__ __forceinline__ void hide_v(uint32_t vt, uint32_t vis, int lane) {
+#pragma unroll
+  for (int i = lane; i < kPageSize * 4; i += 32)
+    if (!((vis >> (i >> 2)) & 1u)) sts128_zero(vt + i * 16);
+  fence_proxy_async_smem();  // the ring's next copy comes after these writes
+  __syncwarp();
+}
+
+// The ring of a CTA.
+struct Ring {
+  uint32_t base;
+  __device__ __forceinline__ uint32_t page(int st) const { return base + st * kPage8Bytes; }
+  __device__ __forceinline__ uint32_t scales(int st) const {
+    return base + kOffScales + st * kPageScales;
+  }
+  __device__ __forceinline__ uint32_t meta(int st) const { return base + kOffMeta + st * 8; }
+  __device__ __forceinline__ uint32_t full(int st) const { return base + kOffBars + st * 8; }
+  __device__ __forceinline__ uint32_t empty(int st) const {
+    return base + kOffBars + (kStages + st) * 8;
+  }
+};
+
+// The producer warp: pages [r0, r1) of the list page_of, ids 32 at a time.
+template <typename PageOf>
+__device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map,
+                                           const MaskedArgs& a, const uint8_t* scales, int b,
+                                           int r0, int r1, int lane, const PageOf& page_of) {
+  const int n = r1 - r0;
+  auto load_ids = [&](int k0) {
+    int pid = -1;
+    if (k0 + lane < n) {
+      pid = a.block_table[static_cast<int64_t>(b) * a.max_blocks + page_of(r0 + k0 + lane)];
+      if (pid < 0 || pid >= a.num_pages) {
+        record_error(a.dev_err, kErrPage);
+        pid = -1;
+      }
+    }
+    return pid;
+  };
+  const uint64_t policy = l2_policy_evict_first();
+  int ids = load_ids(0), ids_next = load_ids(32);
+  int k = 0;
+  for (; k < n; ++k) {
+    const int st = k % kStages;
+    if (k >= kStages) {
+      const bool ok = mbar_wait_bounded(R.empty(st), (k / kStages - 1) & 1, a.wait_ns);
+      if (!__all_sync(kFull, ok)) {
+        if (lane == 0) record_error(a.dev_err, kErrTimeout);
+        break;
+      }
+    }
+    const int pid = __shfl_sync(kFull, ids, k & 31);
+    if (lane == 0) {
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(R.meta(st)), "r"(page_of(r0 + k)),
+                   "r"(pid)
+                   : "memory");
+      if (pid >= 0) {
+        mbar_arrive_expect_tx(R.full(st), kPage8Bytes + kPageScales);
+        tma_load_3d(R.page(st), map, R.full(st), 0, 0, pid, policy);
+        bulk_load(R.scales(st), scales + static_cast<int64_t>(pid) * kPageScales, kPageScales,
+                  R.full(st), policy);
+      } else {
+        mbar_arrive(R.full(st));  // keep the stage's phase sequence in step
+      }
+    }
+    __syncwarp();
+    if ((k & 31) == 31) {
+      ids = ids_next;
+      ids_next = load_ids(k + 33);
+    }
+  }
+  // every copy has landed before the CTA ends (full limit)
+  for (int j = k > kStages ? k - kStages : 0; j < k; ++j)
+    mbar_wait_bounded(R.full(j % kStages), (j / kStages) & 1);
+}
+
+__device__ __forceinline__ Ring make_ring(uint8_t* raw, const CUtensorMap* map) {
+  const Ring R{(smem_addr(raw) + 1023u) & ~1023u};
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(map);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(R.full(s), 1);
+      mbar_init(R.empty(s), kWarps);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  return R;
+}
+
+// Column 2 ft + j of S as a row's output, or as its partial result of a range.
+__device__ __forceinline__ void put_row(const MaskedArgs& a, int64_t row, int split, const State& S,
+                                        int j, int fg) {
+  if (a.num_splits > 1) {
+    const int64_t part = row * a.num_splits + split;
+    float* dst = a.part_acc + part * kHeadDim + fg;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[8 * i] = j == 0 ? S.o[i >> 1][i & 1].x : S.o[i >> 1][i & 1].y;
+    if (fg == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(S.m[j], S.l[j]);
+  } else {
+    const float inv = S.l[j] > 0.f || S.l[j] != S.l[j] ? 1.f / S.l[j] : 0.f;
+    uint16_t* dst = a.out + row * kHeadDim + fg;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      dst[8 * i] = static_cast<uint16_t>(pack_bf16x2(
+          (j == 0 ? S.o[i >> 1][i & 1].x : S.o[i >> 1][i & 1].y) * inv, 0.f));
+  }
+}
+
+// One token a sequence; grid (ranges, batch).
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads, kCtas)
+    paged8_decode_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a,
+                         const uint8_t* __restrict__ scales) {
+  extern __shared__ uint8_t smem_raw[];
+  const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
+  const int split = blockIdx.x, b = blockIdx.y;
+  const Ring R = make_ring(smem_raw, &map);
+  wait_for_prior_grids();
+  allow_dependent_grids();
+  const Visible V(clamped_len(a, b, tid == 0 && split == 0), a.window, a.sinks);
+  const int r0 = static_cast<int>(static_cast<int64_t>(V.n) * split / a.num_splits);
+  const int r1 = static_cast<int>(static_cast<int64_t>(V.n) * (split + 1) / a.num_splits);
+  if (g == kWarps) {
+    load_pages(R, &map, a, scales, b, r0, r1, lane, [&](int i) { return V.page(i); });
+    return;
+  }
+
+  const Lane P(lane);
+  uint32_t qb[4][2];
+  const int64_t row0 = static_cast<int64_t>(b) * kNumQHeads + g * kGroup;
+  const float undo = load_q(a.q + (row0 + (P.fg & 3)) * kHeadDim, P.ft, qb);
+  // factors of the scores of columns 2 ft and 2 ft + 1
+  const int h = (2 * P.ft) & 3;
+  const float c0 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h);
+  const float c1 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h + 4);
+  State S;
+  S.reset();
+  for (int k = 0; k < r1 - r0; ++k) {
+    const int st = k % kStages;
+    const bool ready = mbar_wait_bounded(R.full(st), (k / kStages) & 1, a.wait_ns);
+    if (!__all_sync(kFull, ready)) {
+      if (lane == 0) record_error(a.dev_err, kErrTimeout);
+      break;
+    }
+    const uint2 meta = lds64(R.meta(st));
+    if (static_cast<int>(meta.y) >= 0) {
+      const uint32_t kt = R.page(st) + g * kBlockBytes, vt = kt + kNumKvHeads * kBlockBytes;
+      const float sk = scale_value(stored_scale(lds8(R.scales(st) + g)));
+      const float sv = scale_value(stored_scale(lds8(R.scales(st) + kNumKvHeads + g)));
+      uint32_t ka[4][4], va[4][4];
+      load_k<kFmt>(kt, P, ka);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_16816_f16(s, ka[kk], qb[kk][0], qb[kk][1]);
+      s[0] *= c0 * sk;
+      s[1] *= c1 * sk;
+      s[2] *= c0 * sk;
+      s[3] *= c1 * sk;
+      const uint32_t vis = V.mask(meta.x);
+      if (vis != 0xFFFFu) {
+        if (!((vis >> P.tok) & 1u)) s[0] = s[1] = -INFINITY;
+        if (!((vis >> (P.tok + 2)) & 1u)) s[2] = s[3] = -INFINITY;
+        if constexpr (kFmt == kKv8E4m3) hide_v(vt, vis, lane);
+      }
+      load_v<kFmt>(vt, P, va);
+      fold<true>(s, va, sv, P.ft, S);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(R.empty(st));
+  }
+
+  // the terms' columns meet; lanes ft < 2 hold heads 2 ft and 2 ft + 1
+#pragma unroll
+  for (int i = 4; i <= 16; i <<= 1) {
+    S.l[0] += __shfl_xor_sync(kFull, S.l[0], i);
+    S.l[1] += __shfl_xor_sync(kFull, S.l[1], i);
+  }
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      S.o[mt][e].x += __shfl_xor_sync(kFull, S.o[mt][e].x, 2);
+      S.o[mt][e].y += __shfl_xor_sync(kFull, S.o[mt][e].y, 2);
+    }
+  if (P.ft >= 2) return;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) put_row(a, row0 + 2 * P.ft + j, split, S, j, P.fg);
+}
+
+// A tile of up to four new tokens of a sequence: 16 query rows of a kv head, as
+// two n-tiles of 8 (row = 4 token + head).  Tiles are numbered so that a
+// sequence's first is off[b] / 4 + b (n tokens make at most n / 4 + 1 tiles).
+constexpr int kRowTiles = kTileTokens / 2;
+
+__device__ __forceinline__ int find_tile(int64_t u, const MaskedArgs& a, int lane, int& tile) {
+  auto first = [&](int b) { return static_cast<int64_t>(a.token_offsets[b] / kTileTokens) + b; };
+  int lo = 0, n = a.batch;
+  while (n > 1) {  // 32 places at a time
+    const int step = (n + 31) / 32, at = lane * step;
+    const unsigned below = __ballot_sync(kFull, at < n && first(lo + min(at, n - 1)) <= u);
+    const int cut = max(__popc(below) - 1, 0) * step;
+    lo += cut;
+    n = min(step, n - cut);
+  }
+  const int64_t t = u - first(lo);
+  tile = t < 0 || t > INT32_MAX / kTileTokens ? INT32_MAX / kTileTokens : static_cast<int>(t);
+  return lo;
+}
+
+// grid (tiles, ranges).
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads, kCtas)
+    paged8_chunk_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a,
+                        const uint8_t* __restrict__ scales) {
+  extern __shared__ uint8_t smem_raw[];
+  const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
+  const int split = blockIdx.y;
+  const Ring R = make_ring(smem_raw, &map);
+  wait_for_prior_grids();
+  allow_dependent_grids();
+  int tile;
+  const int b = find_tile(blockIdx.x, a, lane, tile);
+  const int o0 = a.token_offsets[b], o1 = a.token_offsets[b + 1];
+  if (o0 < 0 || o1 < o0 || o1 > a.num_tokens) {
+    if (tid == 0) record_error(a.dev_err, kErrOffsets);
+    return;
+  }
+  const int first = tile * kTileTokens;
+  if (first >= o1 - o0) return;
+  const int nt = min(o1 - o0 - first, kTileTokens), q0 = o0 + first;
+  const int L = clamped_len(a, b, tid == 0 && split == 0);
+  const int pos0 = L - (o1 - o0) + first;
+  if (pos0 < 0 && tid == 0 && split == 0) record_error(a.dev_err, kErrPosition);
+  // pages that some row sees: those of the sinks, then those of the windows
+  const int end = pos0 + nt, p_first = max(pos0, 0);
+  const int lo = p_first >= a.window ? p_first - a.window + 1 : 0;
+  const int w0 = lo / kPageSize;
+  const int ns = min((min(a.sinks, lo) + kPageSize - 1) / kPageSize, w0);
+  const int pages = end > 0 ? ns + (end + kPageSize - 1) / kPageSize - w0 : 0;
+  const int r0 = static_cast<int>(static_cast<int64_t>(pages) * split / a.num_splits);
+  const int r1 = static_cast<int>(static_cast<int64_t>(pages) * (split + 1) / a.num_splits);
+  if (g == kWarps) {
+    load_pages(R, &map, a, scales, b, r0, r1, lane,
+               [&](int i) { return i < ns ? i : w0 + (i - ns); });
+    return;
+  }
+
+  const Lane P(lane);
+  uint32_t qb[kRowTiles][4][2];
+  float c[kRowTiles][2];
+  State S[kRowTiles];
+#pragma unroll
+  for (int i = 0; i < kRowTiles; ++i) {
+    const int tok = 2 * i + (P.fg >> 2);
+    const float undo = load_q(
+        tok < nt ? a.q + (static_cast<int64_t>(q0 + tok) * kNumQHeads + g * kGroup + (P.fg & 3)) *
+                             kHeadDim
+                 : nullptr,
+        P.ft, qb[i]);
+    c[i][0] = a.scale_log2 * __shfl_sync(kFull, undo, 8 * P.ft);
+    c[i][1] = a.scale_log2 * __shfl_sync(kFull, undo, 8 * P.ft + 4);
+    S[i].reset();
+  }
+  const int tiles = (nt + 1) >> 1;
+  // bits of a page's slots below token x (as a distance from the page's first)
+  auto below = [](int64_t x) {
+    return x <= 0 ? 0u : (x >= kPageSize ? 0xFFFFu : (1u << static_cast<int>(x)) - 1u);
+  };
+  // tokens of the page at `base` that positions p0 to p1 see, taken together
+  auto seen_by = [&](int base, int p0, int p1) {
+    return below(static_cast<int64_t>(p1) + 1 - base) &
+           ((0xFFFFu & ~below(static_cast<int64_t>(p0) - a.window + 1 - base)) |
+            below(static_cast<int64_t>(a.sinks) - base));
+  };
+  for (int k = 0; k < r1 - r0; ++k) {
+    const int st = k % kStages;
+    const bool ready = mbar_wait_bounded(R.full(st), (k / kStages) & 1, a.wait_ns);
+    if (!__all_sync(kFull, ready)) {
+      if (lane == 0) record_error(a.dev_err, kErrTimeout);
+      break;
+    }
+    const uint2 meta = lds64(R.meta(st));
+    if (static_cast<int>(meta.y) >= 0) {
+      const uint32_t kt = R.page(st) + g * kBlockBytes, vt = kt + kNumKvHeads * kBlockBytes;
+      const float sk = scale_value(stored_scale(lds8(R.scales(st) + g)));
+      const float sv = scale_value(stored_scale(lds8(R.scales(st) + kNumKvHeads + g)));
+      const int base = static_cast<int>(meta.x) * kPageSize;
+      // does every row see the whole page?
+      const bool whole = base + kPageSize - 1 <= pos0 &&
+                         (static_cast<int64_t>(base) > static_cast<int64_t>(end) - 1 - a.window ||
+                          base + kPageSize <= a.sinks);
+      float s[kRowTiles][4];
+      {
+        uint32_t ka[4][4];
+        load_k<kFmt>(kt, P, ka);
+#pragma unroll
+        for (int i = 0; i < kRowTiles; ++i)
+          if (i < tiles) {
+            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_16816_f16(s[i], ka[kk], qb[i][kk][0], qb[i][kk][1]);
+            s[i][0] *= c[i][0] * sk;
+            s[i][1] *= c[i][1] * sk;
+            s[i][2] *= c[i][0] * sk;
+            s[i][3] *= c[i][1] * sk;
+          }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < kRowTiles; ++i) {
+          // this lane's two rows are of one token
+          const int p = pos0 + 2 * i + (P.ft >> 1);
+          const uint32_t vis = seen_by(base, p, p);
+          if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
+          if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
+        }
+        if constexpr (kFmt == kKv8E4m3) hide_v(vt, seen_by(base, pos0, end - 1), lane);
+      }
+      uint32_t va[4][4];
+      load_v<kFmt>(vt, P, va);
+#pragma unroll
+      for (int i = 0; i < kRowTiles; ++i)
+        if (i < tiles) fold<false>(s[i], va, sv, P.ft, S[i]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(R.empty(st));
+  }
+
+#pragma unroll
+  for (int i = 0; i < kRowTiles; ++i) {
+#pragma unroll
+    for (int x = 4; x <= 16; x <<= 1) {
+      S[i].l[0] += __shfl_xor_sync(kFull, S[i].l[0], x);
+      S[i].l[1] += __shfl_xor_sync(kFull, S[i].l[1], x);
+    }
+    const int tok = 2 * i + (P.ft >> 1);
+    if (tok >= nt) continue;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      put_row(a, static_cast<int64_t>(q0 + tok) * kNumQHeads + g * kGroup + ((2 * P.ft) & 3) + j,
+              split, S[i], j, P.fg);
+  }
+}
+
+// One warp per query row combines its ranges (kChunk: rows of no sequence keep
+// what they hold).
+constexpr int kMergeRows = 4;
+template <bool kChunk>
+__global__ void __launch_bounds__(32 * kMergeRows) merge8_kernel(const MaskedArgs a) {
+  allow_dependent_grids();
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  if constexpr (kChunk) {
+    const int tok = static_cast<int>(row / kNumQHeads);
+    int lo = 0, hi = a.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.token_offsets[mid] <= tok) lo = mid; else hi = mid;
+    }
+    const int o0 = a.token_offsets[lo], o1 = a.token_offsets[lo + 1];
+    if (o0 < 0 || o1 > a.num_tokens || tok < o0 || tok >= o1) return;
+  }
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.num_splits;
+  const float2* acc =
+      reinterpret_cast<const float2*>(a.part_acc) + row * a.num_splits * (kHeadDim / 2) + lane;
+  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] =
+      merge_ranges(ml, acc, a.num_splits, lane);
+}
+
+// Shared memory opt-in, once per device.
+template <typename Kernel>
+cudaError_t configure(Kernel kernel, std::atomic<unsigned long long>& done) {
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem));
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return err;
+}
+
+template <int kFmt>
+cudaError_t launch_stream(const CUtensorMap& map, const MaskedArgs& a, const uint8_t* scales,
+                          cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0}, done_chunk{0};
+  const bool chunk = a.token_offsets != nullptr;
+  const cudaError_t err = chunk ? configure(paged8_chunk_kernel<kFmt>, done_chunk)
+                                : configure(paged8_decode_kernel<kFmt>, done);
+  if (err != cudaSuccess) return err;
+  if (!chunk)
+    return launch_pdl(paged8_decode_kernel<kFmt>, dim3(a.num_splits, a.batch), dim3(kThreads),
+                      kSmem, stream, map, a, scales);
+  return launch_pdl(paged8_chunk_kernel<kFmt>, dim3(a.num_tokens / kTileTokens + a.batch, a.num_splits),
+                    dim3(kThreads), kSmem, stream, map, a, scales);
+}
+
+template <bool kChunk>
+cudaError_t launch_merge(const MaskedArgs& a, cudaStream_t stream) {
+  static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
+  return launch_pdl(merge8_kernel<kChunk>, dim3(a.num_tokens * (kNumQHeads / kMergeRows)),
+                    dim3(32 * kMergeRows), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged8_attention(const CUtensorMap& page_map, const MaskedArgs& args,
+                                    const uint8_t* scales, int format, cudaStream_t stream) {
+  const cudaError_t err = format == kKv8E4m3
+                              ? launch_stream<kKv8E4m3>(page_map, args, scales, stream)
+                              : launch_stream<kKv8Int8>(page_map, args, scales, stream);
+  if (err != cudaSuccess || args.num_splits == 1) return err;
+  return args.token_offsets != nullptr ? launch_merge<true>(args, stream)
+                                       : launch_merge<false>(args, stream);
+}
+
+}  // namespace pkv

@@ -1369,3 +1369,344 @@ PKV_API int pkv_kv_evict(const float* mass, int64_t mass_stride, pkv_bf16* pool,
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The 8-bit cache: writing it, reading it back, attention over it.
+
+namespace {
+
+// What every call on the 8-bit cache checks of it.
+int check_kv8(const void* pool, const uint8_t* scales, int format, int64_t num_pages,
+              const int32_t* block_table, int max_blocks, int batch, int num_kv_heads,
+              int head_dim, int page_size) {
+  if (!pool || !scales || !block_table) return PKV_EINVAL;
+  if (bad_cache(batch, num_pages, max_blocks)) return PKV_EINVAL;
+  if (format != PKV_KV8_E4M3 && format != PKV_KV8_INT8) return PKV_EUNSUPPORTED;
+  if (num_kv_heads != kNumKvHeads || head_dim != kHeadDim || page_size != kPageSize)
+    return PKV_EUNSUPPORTED;
+  return aligned(pool, 16) && aligned(scales, 16) && aligned(block_table, 4) ? PKV_OK : PKV_EALIGN;
+}
+
+Span codes_span(const void* pool, int64_t num_pages) {
+  return {pool, static_cast<size_t>(num_pages) * 2 * kNumKvHeads * kPageSize * kHeadDim};
+}
+
+Span scales_span(const uint8_t* scales, int64_t num_pages) {
+  return {scales, static_cast<size_t>(num_pages) * 2 * kNumKvHeads};
+}
+
+pkv::Kv8 kv8_of(const void* pool, const uint8_t* scales, int format, int64_t num_pages,
+                const int32_t* block_table, int max_blocks, int batch) {
+  pkv::Kv8 c = {};
+  c.pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  c.scales = const_cast<uint8_t*>(scales);
+  c.block_table = block_table;
+  c.num_pages = num_pages;
+  c.max_blocks = max_blocks;
+  c.batch = batch;
+  c.format = format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8;
+  return c;
+}
+
+// TMA descriptor of the 8-bit pool viewed as [num_pages][256 rows (K|V x kv head
+// x slot)][64] bytes, 64-byte swizzled, with boxes of box_rows rows: 256 take a
+// page, 16 a block.  Cached per thread for the last (device, pool, pages).
+bool pool8_map(const void* pool, int64_t num_pages, int box_rows, CUtensorMap* out) {
+  struct Entry {
+    int device = -1;
+    const void* pool = nullptr;
+    int64_t num_pages = 0;
+    CUtensorMap map;
+  };
+  constexpr int kRows = 2 * kNumKvHeads * kPageSize;
+  thread_local Entry cached[2];
+  Entry& c = cached[box_rows == kRows ? 0 : 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (c.device != dev || c.pool != pool || c.num_pages != num_pages) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(kRows),
+                                static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim),
+                                   static_cast<cuuint64_t>(kRows * kHeadDim)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim),
+                               static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUtensorMap m;
+    if (enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+    c.device = dev;
+    c.pool = pool;
+    c.num_pages = num_pages;
+    c.map = m;
+  }
+  *out = c.map;
+  return true;
+}
+
+// Ranges of `units` sequences (or row tiles) of at most `pages` pages, one CTA
+// for all kv heads each: CTAs for two an SM, but four pages a range or more.
+int stream8_splits(long long units, long long pages, int num_splits) {
+  if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, pages));
+  const int sms = current_sm_count();
+  if (sms <= 0) return -1;
+  return static_cast<int>(std::max(1LL, std::min(2LL * sms / std::max(units, 1LL), pages / 4)));
+}
+
+int decode8_splits(int batch, int max_blocks, int window, int sinks, int num_splits) {
+  return stream8_splits(batch, window > 0 ? window_pages(max_blocks, window, sinks) : max_blocks,
+                        num_splits);
+}
+
+int chunk8_splits(int num_tokens, int batch, int max_blocks, int window, int sinks,
+                  int num_splits) {
+  const long long wide = static_cast<long long>(window) + pkv::kShortTokens - 1;
+  const long long pages =
+      window > 0 ? window_pages(max_blocks, static_cast<int>(std::min<long long>(wide, INT32_MAX)),
+                                sinks)
+                 : max_blocks;
+  const long long tiles = num_tokens / pkv::kShortTokens + batch;
+  return stream8_splits(std::min<long long>(tiles, num_tokens), pages, num_splits);
+}
+
+}  // namespace
+
+extern "C" {
+
+PKV_API int pkv_kv8_append(const pkv_bf16* k_new, const pkv_bf16* v_new, void* pool,
+                           uint8_t* scales, int format, int64_t num_pages,
+                           const int32_t* block_table, int max_blocks, const int32_t* positions,
+                           const int32_t* slots, int batch, int num_kv_heads, int head_dim,
+                           int page_size, double rope_theta, const pkv_bf16* q_in,
+                           pkv_bf16* q_out, int num_q_heads, int32_t* dev_err,
+                           pkv_stream_t stream) {
+  if (!k_new || !v_new || !positions) return PKV_EINVAL;
+  const int rc = check_kv8(pool, scales, format, num_pages, block_table, max_blocks, batch,
+                           num_kv_heads, head_dim, page_size);
+  if (rc == PKV_EINVAL) return rc;
+  if ((q_in == nullptr) != (q_out == nullptr)) return PKV_EINVAL;
+  if (!(rope_theta > 0.0) || !isfinite(rope_theta)) return PKV_EINVAL;
+  if (rc == PKV_EUNSUPPORTED || (q_in != nullptr && num_q_heads != kNumQHeads))
+    return PKV_EUNSUPPORTED;
+  if (rc != PKV_OK || !aligned(v_new, 4) || !aligned(k_new, 2) || !aligned(q_in, 2) ||
+      !aligned(q_out, 2) || !aligned(positions, 4) || !aligned(slots, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  const size_t rows = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(k_new, batch, kNumKvHeads),
+                      heads_span(v_new, batch, kNumKvHeads),
+                      heads_span(q_in, batch),
+                      ints(block_table, rows * max_blocks),
+                      ints(positions, rows),
+                      ints(slots, rows)};
+  const Span outs[] = {codes_span(pool, num_pages), scales_span(scales, num_pages),
+                       heads_span(q_out, batch), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  pkv::RopeFreqs freqs;
+  if (pkv::prepare_rope(rope_theta, &freqs, st) != cudaSuccess) return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_kv8_append(
+      k_new, v_new, kv8_of(pool, scales, format, num_pages, block_table, max_blocks, batch),
+      positions, slots, freqs, q_in, q_out, dev_err, st);
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API int pkv_kv8_write_prefill(const pkv_bf16* k, const pkv_bf16* v, int num_tokens,
+                                  const int32_t* token_offsets, const int32_t* start_positions,
+                                  void* pool, uint8_t* scales, int format, int64_t num_pages,
+                                  const int32_t* block_table, int max_blocks, int batch,
+                                  int num_kv_heads, int head_dim, int page_size,
+                                  double rope_theta, int32_t* dev_err, pkv_stream_t stream) {
+  if (!k || !v || !token_offsets || !start_positions || num_tokens < 0) return PKV_EINVAL;
+  const int rc = check_kv8(pool, scales, format, num_pages, block_table, max_blocks, batch,
+                           num_kv_heads, head_dim, page_size);
+  if (rc == PKV_EINVAL) return rc;
+  if (!(rope_theta > 0.0) || !isfinite(rope_theta)) return PKV_EINVAL;
+  if (rc == PKV_EUNSUPPORTED) return rc;
+  if (rc != PKV_OK || !aligned(k, 16) || !aligned(v, 16) || !aligned(token_offsets, 4) ||
+      !aligned(start_positions, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(k, num_tokens, kNumKvHeads),
+                      heads_span(v, num_tokens, kNumKvHeads), ints(token_offsets, seqs + 1),
+                      ints(start_positions, seqs), ints(block_table, seqs * max_blocks)};
+  const Span outs[] = {codes_span(pool, num_pages), scales_span(scales, num_pages),
+                       ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
+  if (batch == 0 || num_tokens == 0) return PKV_OK;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PKV_ECUDA;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  pkv::RopeFreqs freqs;
+  if (pkv::prepare_rope(rope_theta, &freqs, st) != cudaSuccess) return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_kv8_write(
+      k, v, num_tokens, token_offsets, start_positions,
+      kv8_of(pool, scales, format, num_pages, block_table, max_blocks, batch), freqs, sms, dev_err,
+      st);
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API int pkv_kv8_read(const void* pool, const uint8_t* scales, int format, int64_t num_pages,
+                         const int32_t* block_table, int max_blocks,
+                         const int32_t* token_offsets, const int32_t* start_positions,
+                         int num_tokens, int batch, int num_kv_heads, int head_dim, int page_size,
+                         pkv_bf16* k, pkv_bf16* v, int32_t* dev_err, pkv_stream_t stream) {
+  if (!k || !v || !token_offsets || !start_positions || num_tokens < 0) return PKV_EINVAL;
+  const int rc = check_kv8(pool, scales, format, num_pages, block_table, max_blocks, batch,
+                           num_kv_heads, head_dim, page_size);
+  if (rc == PKV_EINVAL || rc == PKV_EUNSUPPORTED) return rc;
+  if (rc != PKV_OK || !aligned(k, 16) || !aligned(v, 16) || !aligned(token_offsets, 4) ||
+      !aligned(start_positions, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {codes_span(pool, num_pages), scales_span(scales, num_pages),
+                      ints(token_offsets, seqs + 1), ints(start_positions, seqs),
+                      ints(block_table, seqs * max_blocks)};
+  const Span outs[] = {heads_span(k, num_tokens, kNumKvHeads),
+                       heads_span(v, num_tokens, kNumKvHeads), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
+  if (batch == 0 || num_tokens == 0) return PKV_OK;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_kv8_read(
+      k, v, num_tokens, token_offsets, start_positions,
+      kv8_of(pool, scales, format, num_pages, block_table, max_blocks, batch), sms, dev_err,
+      reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API size_t pkv_decode8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                           int head_dim, int max_blocks, int window, int sinks,
+                                           int num_splits) {
+  if (bad_cache(batch, 1, max_blocks) || window < 0 || sinks < 0 || num_splits < 0 ||
+      !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
+    return static_cast<size_t>(-1);
+  if (batch == 0) return 0;
+  const int splits = decode8_splits(batch, max_blocks, window, sinks, num_splits);
+  return splits < 1 ? static_cast<size_t>(-1) : part_bytes(batch, splits);
+}
+
+PKV_API size_t pkv_chunk8_workspace_bytes(int num_tokens, int batch, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int max_blocks,
+                                          int window, int sinks, int num_splits) {
+  if (num_tokens < 0 || bad_cache(batch, 1, max_blocks) || window < 0 || sinks < 0 ||
+      num_splits < 0 || !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
+    return static_cast<size_t>(-1);
+  if (num_tokens == 0 || batch == 0) return 0;
+  const int splits = chunk8_splits(num_tokens, batch, max_blocks, window, sinks, num_splits);
+  return splits < 1 ? static_cast<size_t>(-1) : part_bytes(num_tokens, splits);
+}
+
+PKV_API int pkv_paged8_decode_attention(
+    const pkv_bf16* q, const void* pool, const uint8_t* scales, int format, int64_t num_pages,
+    const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
+    int num_q_heads, int num_kv_heads, int head_dim, int page_size, int window, int sinks,
+    float scale, pkv_bf16* out, void* workspace, size_t workspace_bytes, int num_splits,
+    int32_t* dev_err, pkv_stream_t stream) {
+  if (!q || !seq_lens || !out || window < 0 || sinks < 0 || num_splits < 0) return PKV_EINVAL;
+  const int rc = check_kv8(pool, scales, format, num_pages, block_table, max_blocks, batch,
+                           num_kv_heads, head_dim, page_size);
+  if (rc == PKV_EINVAL) return rc;
+  if (!(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+  if (rc == PKV_EUNSUPPORTED || num_q_heads != kNumQHeads) return PKV_EUNSUPPORTED;
+  if (rc != PKV_OK || !aligned(q, 16) || !aligned(out, 4) || !aligned(workspace, 16) ||
+      !aligned(seq_lens, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(q, batch), codes_span(pool, num_pages),
+                      scales_span(scales, num_pages), ints(block_table, seqs * max_blocks),
+                      ints(seq_lens, seqs)};
+  const Span outs[] = {heads_span(out, batch), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  const int splits = decode8_splits(batch, max_blocks, window, sinks, num_splits);
+  if (splits < 1) return PKV_ECUDA;
+  const size_t need = part_bytes(batch, splits);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
+  pkv::MaskedArgs a = {};
+  a.q = q;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.dev_err = dev_err;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.num_tokens = batch;
+  a.window = window > 0 ? window : INT32_MAX;
+  a.sinks = sinks;
+  a.num_splits = splits;
+  a.part_acc = static_cast<float*>(workspace);
+  a.part_ml = a.part_acc + static_cast<size_t>(batch) * kNumQHeads * splits * kHeadDim;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = pkv::wait_limit_ns();
+  CUtensorMap map;
+  if (!pool8_map(pool, num_pages, 2 * kNumKvHeads * kPageSize, &map)) return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_paged8_attention(
+      map, a, scales, format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8,
+      reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+PKV_API int pkv_paged8_chunk_attention(
+    const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const void* pool,
+    const uint8_t* scales, int format, int64_t num_pages, const int32_t* block_table,
+    int max_blocks, const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, int window, int sinks, float scale, pkv_bf16* out,
+    void* workspace, size_t workspace_bytes, int num_splits, int32_t* dev_err,
+    pkv_stream_t stream) {
+  if (!q || !token_offsets || !seq_lens || !out || num_tokens < 0 || window < 0 || sinks < 0 ||
+      num_splits < 0)
+    return PKV_EINVAL;
+  const int rc = check_kv8(pool, scales, format, num_pages, block_table, max_blocks, batch,
+                           num_kv_heads, head_dim, page_size);
+  if (rc == PKV_EINVAL) return rc;
+  if (!(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+  if (rc == PKV_EUNSUPPORTED || num_q_heads != kNumQHeads) return PKV_EUNSUPPORTED;
+  if (rc != PKV_OK || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+      !aligned(token_offsets, 4) || !aligned(seq_lens, 4) || !aligned(dev_err, 4))
+    return PKV_EALIGN;
+  const size_t seqs = static_cast<size_t>(batch);
+  const Span ins[] = {heads_span(q, num_tokens), ints(token_offsets, seqs + 1),
+                      codes_span(pool, num_pages), scales_span(scales, num_pages),
+                      ints(block_table, seqs * max_blocks), ints(seq_lens, seqs)};
+  const Span outs[] = {heads_span(out, num_tokens), ints(dev_err, 1)};
+  if (outputs_overlap(outs, ins)) return PKV_EINVAL;
+  if (batch == 0 || num_tokens == 0) return PKV_OK;
+  const int splits = chunk8_splits(num_tokens, batch, max_blocks, window, sinks, num_splits);
+  if (splits < 1) return PKV_ECUDA;
+  const size_t need = part_bytes(num_tokens, splits);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
+  pkv::MaskedArgs a = {};
+  a.q = q;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.token_offsets = token_offsets;
+  a.out = out;
+  a.dev_err = dev_err;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.num_tokens = num_tokens;
+  a.window = window > 0 ? window : INT32_MAX;
+  a.sinks = sinks;
+  a.num_splits = splits;
+  a.part_acc = static_cast<float*>(workspace);
+  a.part_ml = a.part_acc + static_cast<size_t>(num_tokens) * kNumQHeads * splits * kHeadDim;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = pkv::wait_limit_ns();
+  CUtensorMap map;
+  if (!pool8_map(pool, num_pages, 2 * kNumKvHeads * kPageSize, &map)) return PKV_ECUDA;
+  const cudaError_t err = pkv::launch_paged8_attention(
+      map, a, scales, format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8,
+      reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+}  // extern "C"

@@ -27,6 +27,7 @@ constexpr int kErrPosition = 4;
 constexpr int kErrTimeout = 8;
 constexpr int kErrOffsets = 16;
 constexpr int kErrPlan = 32;
+constexpr int kErrValue = 64;
 
 // Work plans (include/pkv.h): header words, item and merge entry sizes.
 constexpr int kPlanHeaderWords = 12;
@@ -328,6 +329,38 @@ struct EvictArgs {
 };
 
 cudaError_t launch_kv_evict(const EvictArgs& args, int num_sms, cudaStream_t stream);
+
+// The 8-bit cache (kv8.cuh): formats of its codes, and where it lies.
+constexpr int kKv8E4m3 = 0, kKv8Int8 = 1;
+struct Kv8 {
+  uint8_t* pool;    // [pages][K|V][8][16][64] codes
+  uint8_t* scales;  // [pages][K|V][8]
+  const int32_t* block_table;
+  int64_t num_pages;
+  int max_blocks;
+  int batch;
+  int format;
+};
+
+// One token per sequence (slots: its cache slot, or nullptr for its position),
+// ragged prompts, and the way back to bf16 (kv8_write.cu).
+cudaError_t launch_kv8_append(const uint16_t* k_new, const uint16_t* v_new, const Kv8& cache,
+                              const int32_t* positions, const int32_t* slots,
+                              const RopeFreqs& freqs, const uint16_t* q_in, uint16_t* q_out,
+                              int32_t* dev_err, cudaStream_t stream);
+cudaError_t launch_kv8_write(const uint16_t* k, const uint16_t* v, int num_tokens,
+                             const int32_t* token_offsets, const int32_t* start_positions,
+                             const Kv8& cache, const RopeFreqs& freqs, int num_sms,
+                             int32_t* dev_err, cudaStream_t stream);
+cudaError_t launch_kv8_read(uint16_t* k, uint16_t* v, int num_tokens,
+                            const int32_t* token_offsets, const int32_t* start_positions,
+                            const Kv8& cache, int num_sms, int32_t* dev_err, cudaStream_t stream);
+
+// Attention over the 8-bit cache (kv8_attention.cu; args.pool unused), of one
+// token a sequence or, with args.token_offsets, of chunks.
+// page_map: boxes of one page's codes, 64-byte swizzled.
+cudaError_t launch_paged8_attention(const CUtensorMap& page_map, const MaskedArgs& args,
+                                    const uint8_t* scales, int format, cudaStream_t stream);
 
 // Largest logical page range one attention CTA handles.
 int max_pages_per_split();
