@@ -73,6 +73,7 @@
 
 #include <atomic>
 
+#include "kv8.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -93,11 +94,20 @@ constexpr int kItems = 8;                     // slots for published items
 constexpr int kAhead = 3;                     // items published before the relay starts one
 constexpr int kSoftmaxWarps = 8;
 constexpr int kQkWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11 issues PV
-constexpr int kThreads = 32 * 12;
-// Registers: 168 x 384 threads at launch = 64512 = 256 x 200 + 128 x 104.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads,
-              "the split stays within the registers the block starts with");
+constexpr int kConvertWarp = 12, kConvertWarps = 4;         // over an 8-bit cache
+// The cache's format: bf16 pages, or codes (kKv8E4m3, kKv8Int8).
+constexpr int kBf16 = -1;
+// Threads and registers of the roles: 168 x 384 threads at launch = 64512 = 256 x
+// 200 + 128 x 104; with converting warps 128 x 512 = 256 x 184 + 256 x 72.
+template <bool kCodes>
+struct Roles {
+  static constexpr int kThreads = 32 * (kCodes ? kConvertWarp + kConvertWarps : kConvertWarp);
+  static constexpr int kLaunchRegs = kCodes ? 128 : 168;
+  static constexpr int kSoftmaxRegs = kCodes ? 184 : 200;
+  static constexpr int kOtherRegs = kCodes ? 72 : 104;
+  static_assert(kSoftmaxRegs * 256 + kOtherRegs * (kThreads - 256) <= kLaunchRegs * kThreads,
+                "the split stays within the registers the block starts with");
+};
 constexpr float kRescale = 65536.f;  // 2^16
 
 constexpr uint32_t kTmemCols = 512;
@@ -344,9 +354,154 @@ __device__ __forceinline__ void add_nonfinite(const MaskedArgs& a, const Item& i
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
+// Eight codes (two words) as bf16 values times `s` (exact: a power of two), the
+// first in the low half of the first word.
+template <int kFmt>
+__device__ __forceinline__ uint4 codes_to_bf16(uint32_t w0, uint32_t w1, float s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i == 0 ? w0 : w1;
+    const float2 s2 = make_float2(s, s);
+    float2 lo, hi;
+    if constexpr (kFmt == kKv8E4m3) {
+      const float4 v = decode4<kFmt>(w);
+      lo = fmul2(make_float2(v.x, v.y), s2);
+      hi = fmul2(make_float2(v.z, v.w), s2);
+    } else {
+      // (2^23 + u) s - (2^23 + 128) s, u = code + 128: one rounding, of an exact value
+      const uint32_t u = w ^ 0x80808080u;
+      const float2 off = make_float2(-8388736.f * s, -8388736.f * s);
+      auto raw = [u](uint32_t sel) { return __uint_as_float(prmt(u, 0x4B000000u, sel)); };
+      lo = ffma2(make_float2(raw(0x7540u), raw(0x7541u)), s2, off);
+      hi = ffma2(make_float2(raw(0x7542u), raw(0x7543u)), s2, off);
+    }
+    o[2 * i] = pack_bf16x2(lo.x, lo.y);
+    o[2 * i + 1] = pack_bf16x2(hi.x, hi.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One of the converting warps: it takes rows [32 w, 32 w + 32) (two pages) of the
+// K and V of every kv tile of the CTA's items, lane 4 r + c the 16 codes c of rows
+// r, r + 8, r + 16 and r + 24, loads them a tile ahead, straight from the pool
+// into registers, and stores them as bf16 where the TMA boxes would have put them
+// (128-byte swizzled).  False: a wait ran out.
+template <int kFmt>
+__device__ __forceinline__ bool convert_tiles(const MaskedArgs& a, uint32_t sb, uint32_t* s_meta,
+                                              int w, int lane) {
+  auto bar = [&](int i) { return sb + kOffBars + 8u * i; };
+  auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
+  // The tile whose codes are loaded next: page ids in lanes 0-7 (-1: bad, -2: no
+  // row sees it), and what its notes say.
+  Item it = {};
+  int item = 0, k = 0;
+  int tile = -1, g = 0, end = 0, lo = 0, ids = -2;
+  bool part = false;
+  // false: a wait ran out; tile -1: no more
+  auto next = [&]() {
+    while (k >= it.t1) {
+      const int slot = item % kItems;
+      if (!wait(kBarItemFull + slot, item / kItems)) return false;
+      it = read_item(sb + kOffItems + 4u * kItemWords * slot);
+      __syncwarp();
+      if (it.b < 0) {
+        tile = -1;
+        return true;
+      }
+      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+      ++item;
+      k = it.t0;
+    }
+    tile = it.tile(k++);
+    g = it.g;
+    end = it.end();
+    lo = it.lo;
+    part = it.partial(tile, a);
+    const int page = tile * kKvPages + (lane & 7), t = page * kPageSize;
+    ids = -2;
+    if (t < end && (t + kPageSize > lo || t < a.sinks)) {
+      ids = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + page];
+      if (ids < 0 || ids >= a.num_pages) {
+        if (w == 0 && lane < 8) record_error(a.dev_err, kErrPage);
+        ids = -1;
+      }
+    }
+    return true;
+  };
+  const int r = lane >> 2, c = lane & 3;
+  // scales of the warp's two pages: lanes 2 kv + p
+  auto load_scale = [&]() {
+    const int pid = __shfl_sync(kFull, ids, 2 * w + (lane & 1));
+    return pid >= 0 ? stored_scale(a.scales[scale_at(pid, (lane >> 1) & 1, g)]) : kScaleBias;
+  };
+  // row i of this lane: 32 w + 8 i + r, of page 2 w + i / 2
+  auto load = [&](int kv, uint4 (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pid = __shfl_sync(kFull, ids, 2 * w + (i >> 1));
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      // (V of tokens that no row sees: zeros, whatever their codes)
+      const int t = tile * kKvTokens + 32 * w + 8 * i + r;
+      if (pid >= 0 && (kv == 0 || (t < end && (t >= lo || t < a.sinks))))
+        x[i] = __ldcg(reinterpret_cast<const uint4*>(
+            a.codes + block_at(pid, kv, g) + (8 * (i & 1) + r) * kHeadDim + 16 * c));
+    }
+  };
+  auto store = [&](uint32_t dst, const uint4 (&x)[4], float s0, float s1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = i < 2 ? s0 : s1;
+      const uint32_t row = dst + (32 * w + 8 * i + r) * kRow;
+      const uint4 y = codes_to_bf16<kFmt>(x[i].x, x[i].y, s);
+      sts128(row + (((2 * c) ^ r) << 4), y.x, y.y, y.z, y.w);
+      const uint4 z = codes_to_bf16<kFmt>(x[i].z, x[i].w, s);
+      sts128(row + (((2 * c + 1) ^ r) << 4), z.x, z.y, z.z, z.w);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  if (!next()) return false;
+  uint4 xk[4], xv[4];
+  uint32_t scale = kScaleBias;
+  if (tile >= 0) {
+    scale = load_scale();
+    load(0, xk);
+    load(1, xv);
+  }
+  for (int kt = 0; tile >= 0; ++kt) {
+    const int st = kt % kStages;
+    if (kt >= kStages && !wait(kBarKEmpty + st, kt / kStages - 1)) return false;
+    if (w == 0) {
+      const unsigned bad = __ballot_sync(kFull, ids == -1) & 0xFFu;
+      if (lane == 0)
+        *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
+            make_uint2(tile, bad | (part ? kPartial : 0u));
+    }
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = scale_value(__shfl_sync(kFull, scale, i));
+    store(sb + kOffK + st * kRowTileBytes, xk, s[0], s[1]);
+    if (lane == 0) mbar_arrive(bar(kBarKFull + st));
+    if (!next()) return false;
+    if (tile >= 0) {
+      scale = load_scale();
+      load(0, xk);
+    }
+    if (kt >= kStages && !wait(kBarVEmpty + st, kt / kStages - 1)) return false;
+    store(sb + kOffV + st * kRowTileBytes, xv, s[2], s[3]);
+    if (lane == 0) mbar_arrive(bar(kBarVReady + st));
+    if (tile >= 0) load(1, xv);
+  }
+  return true;
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk_kernel(
     const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap page_map,
     const MaskedArgs a) {
+  constexpr bool kCodes = kFmt != kBf16;
+  using R = Roles<kCodes>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -367,7 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
       if (i >= kBarSFree && i < kBarPvDone) n = 4;               // s_free, p_full
-      if (i >= kBarItemEmpty && i < kBarXFull) n = kSoftmaxWarps + 4;
+      if (i >= kBarItemEmpty && i < kBarXFull)
+        n = kSoftmaxWarps + (kCodes ? 3 + kConvertWarps : 4);
+      if (kCodes && ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVReady && i < kBarVEmpty)))
+        n = kConvertWarps;
       if (i == kBarXFull || i == kBarXFree) n = 4;
       mbar_init(bar(i), n);
     }
@@ -386,8 +544,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
   allow_dependent_grids();
 
   bool ok = true;
-  if (warp >= kQkWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (kCodes && warp >= kConvertWarp) {
+    if constexpr (kCodes) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
+      // ---------------------------------------------- K and V from codes
+      ok = convert_tiles<kFmt>(a, sb, s_meta, warp - kConvertWarp, lane);
+    }
+  } else if (warp >= kQkWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
     if (warp == kSchedWarp) {
       // --------------------------------------------- scheduler, V's relay
       // Items in order (tile, range, head); the tiles of a sequence from its
@@ -500,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         return true;
        }
       };
-      for (int i = 0; ok; ++i) {
+      if constexpr (kCodes) {  // (V is whole when the converting warps hand it over)
+        while (ok && more) ok = publish();
+      } else for (int i = 0; ok; ++i) {
         while (ok && more && out_i <= i + kAhead) ok = publish();
         const int slot = i % kItems;
         if (!ok || !wait(kBarItemFull + slot, i / kItems)) {
@@ -587,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       };
       Item it, nx;
       ok = fetch(0, it);
-      int ids = ok && it.b >= 0 ? load_ids(it, it.t0) : 0;
+      int ids = !kCodes && ok && it.b >= 0 ? load_ids(it, it.t0) : 0;
       for (int i = 0; ok && it.b >= 0; ++i) {
         const int qb = qn & 1;
         if (qn >= 2 && !(ok = wait(kBarQEmpty + qb, qn / 2 - 1))) break;
@@ -602,7 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
         }
         __syncwarp();
         ++qn;
-        for (int k0 = it.t0; ok && k0 < it.t1; k0 += 4) {
+        if constexpr (kCodes) {  // K and V are the converting warps'
+          if (!(ok = fetch(i + 1, nx))) break;
+        }
+        for (int k0 = it.t0; !kCodes && ok && k0 < it.t1; k0 += 4) {
           int ids_next = 0;
           if (k0 + 4 < it.t1) {
             ids_next = load_ids(it, k0 + 4);
@@ -737,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
     // --------------------------------------------------- softmax, epilogue
     const int w = warp >> 2;
     const int row = tid & 127;                 // MMA row = TMEM lane
@@ -920,7 +1089,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
       }
       // (written before the last kv tile's V was handed to its PV, which this
       // row's group, or the other one, has waited for)
-      const int bad_v = *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
+      const int bad_v =
+          kCodes ? 0 : *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
       if (!(one && w == 1) && !idle) {
         const int tok0 = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w);  // the warp's first
         const int64_t r0 = static_cast<int64_t>(it.row0 + tok0) * kNumQHeads + it.g * kGroup;
@@ -1037,31 +1207,40 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_chunk_kernel(const Mask
   reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = merge_ranges(ml, acc, splits, lane);
 }
 
-cudaError_t configure(int device) {
+template <int kFmt>
+cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& page_map, const MaskedArgs& args,
+                   int grid, cudaStream_t stream) {
+  using R = Roles<kFmt != kBf16>;
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
   static std::atomic<unsigned long long> done{0};
   const unsigned long long bit = 1ull << (device & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  cudaFuncAttributes fa;
-  cudaError_t err = cudaFuncGetAttributes(&fa, paged_chunk_kernel);
-  if (err != cudaSuccess) return err;
-  // the register split must stay within what the block starts with
-  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  err = cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
-  return err;
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    cudaFuncAttributes fa;
+    if ((err = cudaFuncGetAttributes(&fa, paged_chunk_kernel<kFmt>)) != cudaSuccess) return err;
+    // the register split must stay within what the block starts with
+    if (fa.numRegs != R::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    err = cudaFuncSetAttribute(paged_chunk_kernel<kFmt>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (err != cudaSuccess) return err;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_pdl(paged_chunk_kernel<kFmt>, dim3(grid), dim3(R::kThreads), kSmem, stream, q_map,
+                    page_map, args);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& page_map,
                                    const MaskedArgs& args, int grid, cudaStream_t stream) {
-  int device = 0;
-  cudaError_t err = cudaGetDevice(&device);
-  if (err != cudaSuccess) return err;
-  if ((err = configure(device)) != cudaSuccess) return err;
-  return launch_pdl(paged_chunk_kernel, dim3(grid), dim3(kThreads), kSmem, stream, q_map, page_map,
-                    args);
+  return launch<kBf16>(q_map, page_map, args, grid, stream);
+}
+
+cudaError_t launch_chunk8_attention(const CUtensorMap& q_map, const MaskedArgs& args, int format,
+                                    int grid, cudaStream_t stream) {
+  return format == kKv8E4m3 ? launch<kKv8E4m3>(q_map, q_map, args, grid, stream)
+                            : launch<kKv8Int8>(q_map, q_map, args, grid, stream);
 }
 
 cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream) {

@@ -45,7 +45,6 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kWarps = kNumKvHeads;            // and one that loads
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 6, kCtas = 2;
-constexpr int kTileTokens = kShortTokens;      // tokens of a row tile of a chunk
 constexpr int kOffScales = kStages * kPage8Bytes;
 constexpr int kOffMeta = kOffScales + kStages * kPageScales;
 constexpr int kOffBars = kOffMeta + kStages * 8;
@@ -279,8 +278,8 @@ struct Ring {
 // The producer warp: pages [r0, r1) of the list page_of, ids 32 at a time.
 template <typename PageOf>
 __device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map,
-                                           const MaskedArgs& a, const uint8_t* scales, int b,
-                                           int r0, int r1, int lane, const PageOf& page_of) {
+                                           const MaskedArgs& a, int b, int r0, int r1, int lane,
+                                           const PageOf& page_of) {
   const int n = r1 - r0;
   auto load_ids = [&](int k0) {
     int pid = -1;
@@ -313,7 +312,7 @@ __device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map
       if (pid >= 0) {
         mbar_arrive_expect_tx(R.full(st), kPage8Bytes + kPageScales);
         tma_load_3d(R.page(st), map, R.full(st), 0, 0, pid, policy);
-        bulk_load(R.scales(st), scales + static_cast<int64_t>(pid) * kPageScales, kPageScales,
+        bulk_load(R.scales(st), a.scales + static_cast<int64_t>(pid) * kPageScales, kPageScales,
                   R.full(st), policy);
       } else {
         mbar_arrive(R.full(st));  // keep the stage's phase sequence in step
@@ -344,21 +343,20 @@ __device__ __forceinline__ Ring make_ring(uint8_t* raw, const CUtensorMap* map) 
   return R;
 }
 
-// Column 2 ft + j of S as a row's output, or as its partial result of a range.
-__device__ __forceinline__ void put_row(const MaskedArgs& a, int64_t row, int split, const State& S,
-                                        int j, int fg) {
-  if (a.num_splits > 1) {
-    const int64_t part = row * a.num_splits + split;
-    float* dst = a.part_acc + part * kHeadDim + fg;
+// Column 2 ft + j of S as a row's output or, where the row has several ranges, as
+// its partial result number `part`.
+__device__ __forceinline__ void put_row(const State& S, int j, int fg, uint16_t* out, bool partial,
+                                        float* acc, float* ml, int64_t part) {
+  if (partial) {
+    float* dst = acc + part * kHeadDim + fg;
 #pragma unroll
     for (int i = 0; i < 8; ++i) dst[8 * i] = j == 0 ? S.o[i >> 1][i & 1].x : S.o[i >> 1][i & 1].y;
-    if (fg == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(S.m[j], S.l[j]);
+    if (fg == 0) *reinterpret_cast<float2*>(ml + 2 * part) = make_float2(S.m[j], S.l[j]);
   } else {
     const float inv = S.l[j] > 0.f || S.l[j] != S.l[j] ? 1.f / S.l[j] : 0.f;
-    uint16_t* dst = a.out + row * kHeadDim + fg;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      dst[8 * i] = static_cast<uint16_t>(pack_bf16x2(
+      out[fg + 8 * i] = static_cast<uint16_t>(pack_bf16x2(
           (j == 0 ? S.o[i >> 1][i & 1].x : S.o[i >> 1][i & 1].y) * inv, 0.f));
   }
 }
@@ -366,8 +364,7 @@ __device__ __forceinline__ void put_row(const MaskedArgs& a, int64_t row, int sp
 // One token a sequence; grid (ranges, batch).
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, kCtas)
-    paged8_decode_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a,
-                         const uint8_t* __restrict__ scales) {
+    paged8_decode_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
   const int split = blockIdx.x, b = blockIdx.y;
@@ -378,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int r0 = static_cast<int>(static_cast<int64_t>(V.n) * split / a.num_splits);
   const int r1 = static_cast<int>(static_cast<int64_t>(V.n) * (split + 1) / a.num_splits);
   if (g == kWarps) {
-    load_pages(R, &map, a, scales, b, r0, r1, lane, [&](int i) { return V.page(i); });
+    load_pages(R, &map, a, b, r0, r1, lane, [&](int i) { return V.page(i); });
     return;
   }
 
@@ -441,52 +438,38 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     }
   if (P.ft >= 2) return;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) put_row(a, row0 + 2 * P.ft + j, split, S, j, P.fg);
-}
-
-// A tile of up to four new tokens of a sequence: 16 query rows of a kv head, as
-// two n-tiles of 8 (row = 4 token + head).  Tiles are numbered so that a
-// sequence's first is off[b] / 4 + b (n tokens make at most n / 4 + 1 tiles).
-constexpr int kRowTiles = kTileTokens / 2;
-
-__device__ __forceinline__ int find_tile(int64_t u, const MaskedArgs& a, int lane, int& tile) {
-  auto first = [&](int b) { return static_cast<int64_t>(a.token_offsets[b] / kTileTokens) + b; };
-  int lo = 0, n = a.batch;
-  while (n > 1) {  // 32 places at a time
-    const int step = (n + 31) / 32, at = lane * step;
-    const unsigned below = __ballot_sync(kFull, at < n && first(lo + min(at, n - 1)) <= u);
-    const int cut = max(__popc(below) - 1, 0) * step;
-    lo += cut;
-    n = min(step, n - cut);
+  for (int j = 0; j < 2; ++j) {
+    const int64_t row = row0 + 2 * P.ft + j;
+    put_row(S, j, P.fg, a.out + row * kHeadDim, a.num_splits > 1, a.part_acc, a.part_ml,
+            row * a.num_splits + split);
   }
-  const int64_t t = u - first(lo);
-  tile = t < 0 || t > INT32_MAX / kTileTokens ? INT32_MAX / kTileTokens : static_cast<int>(t);
-  return lo;
 }
 
-// grid (tiles, ranges).
-template <int kFmt>
+// Chunks of at most four tokens: 16 query rows of a kv head, as two n-tiles of 8
+// (row = 4 token + head); grid (ranges, batch).  kBeside: launched right after the
+// tcgen05 kernel of the same call, as short_chunk.cu's kernel is: it starts at
+// once, and its first CTA and those without a short chunk end after that grid.
+constexpr int kRowTiles = kShortTokens / 2;
+
+template <int kFmt, bool kBeside>
 __global__ void __launch_bounds__(kThreads, kCtas)
-    paged8_chunk_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a,
-                        const uint8_t* __restrict__ scales) {
+    paged8_short_chunk_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
-  const int split = blockIdx.y;
+  const int split = blockIdx.x, b = blockIdx.y;
   const Ring R = make_ring(smem_raw, &map);
-  wait_for_prior_grids();
+  if constexpr (!kBeside) wait_for_prior_grids();
   allow_dependent_grids();
-  int tile;
-  const int b = find_tile(blockIdx.x, a, lane, tile);
   const int o0 = a.token_offsets[b], o1 = a.token_offsets[b + 1];
-  if (o0 < 0 || o1 < o0 || o1 > a.num_tokens) {
-    if (tid == 0) record_error(a.dev_err, kErrOffsets);
+  const bool bad_offsets = o0 < 0 || o1 < o0 || o1 > a.num_tokens;
+  if (bad_offsets && !kBeside && tid == 0) record_error(a.dev_err, kErrOffsets);
+  if (bad_offsets || o1 == o0 || o1 - o0 > kShortTokens) {
+    if constexpr (kBeside) wait_for_prior_grids();
     return;
   }
-  const int first = tile * kTileTokens;
-  if (first >= o1 - o0) return;
-  const int nt = min(o1 - o0 - first, kTileTokens), q0 = o0 + first;
+  const int nt = o1 - o0;
   const int L = clamped_len(a, b, tid == 0 && split == 0);
-  const int pos0 = L - (o1 - o0) + first;
+  const int pos0 = L - nt;
   if (pos0 < 0 && tid == 0 && split == 0) record_error(a.dev_err, kErrPosition);
   // pages that some row sees: those of the sinks, then those of the windows
   const int end = pos0 + nt, p_first = max(pos0, 0);
@@ -494,11 +477,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int w0 = lo / kPageSize;
   const int ns = min((min(a.sinks, lo) + kPageSize - 1) / kPageSize, w0);
   const int pages = end > 0 ? ns + (end + kPageSize - 1) / kPageSize - w0 : 0;
-  const int r0 = static_cast<int>(static_cast<int64_t>(pages) * split / a.num_splits);
-  const int r1 = static_cast<int>(static_cast<int64_t>(pages) * (split + 1) / a.num_splits);
+  const int r0 = static_cast<int>(static_cast<int64_t>(pages) * split / a.short_splits);
+  const int r1 = static_cast<int>(static_cast<int64_t>(pages) * (split + 1) / a.short_splits);
   if (g == kWarps) {
-    load_pages(R, &map, a, scales, b, r0, r1, lane,
-               [&](int i) { return i < ns ? i : w0 + (i - ns); });
+    load_pages(R, &map, a, b, r0, r1, lane, [&](int i) { return i < ns ? i : w0 + (i - ns); });
+    if (kBeside && blockIdx.x == 0 && blockIdx.y == 0) wait_for_prior_grids();
     return;
   }
 
@@ -510,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   for (int i = 0; i < kRowTiles; ++i) {
     const int tok = 2 * i + (P.fg >> 2);
     const float undo = load_q(
-        tok < nt ? a.q + (static_cast<int64_t>(q0 + tok) * kNumQHeads + g * kGroup + (P.fg & 3)) *
+        tok < nt ? a.q + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + (P.fg & 3)) *
                              kHeadDim
                  : nullptr,
         P.ft, qb[i]);
@@ -593,31 +576,23 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int tok = 2 * i + (P.ft >> 1);
     if (tok >= nt) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      put_row(a, static_cast<int64_t>(q0 + tok) * kNumQHeads + g * kGroup + ((2 * P.ft) & 3) + j,
-              split, S[i], j, P.fg);
+    for (int j = 0; j < 2; ++j) {
+      const int h = ((2 * P.ft) & 3) + j;
+      put_row(S[i], j, P.fg,
+              a.out + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + h) * kHeadDim,
+              a.short_splits > 1, a.short_acc, a.short_ml,
+              short_part_row(b, g, tok * kGroup + h) * a.short_splits + split);
+    }
   }
 }
 
-// One warp per query row combines its ranges (kChunk: rows of no sequence keep
-// what they hold).
+// One warp per query row combines its ranges.
 constexpr int kMergeRows = 4;
-template <bool kChunk>
 __global__ void __launch_bounds__(32 * kMergeRows) merge8_kernel(const MaskedArgs a) {
   allow_dependent_grids();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
-  if constexpr (kChunk) {
-    const int tok = static_cast<int>(row / kNumQHeads);
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.token_offsets[mid] <= tok) lo = mid; else hi = mid;
-    }
-    const int o0 = a.token_offsets[lo], o1 = a.token_offsets[lo + 1];
-    if (o0 < 0 || o1 > a.num_tokens || tok < o0 || tok >= o1) return;
-  }
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.num_splits;
   const float2* acc =
       reinterpret_cast<const float2*>(a.part_acc) + row * a.num_splits * (kHeadDim / 2) + lane;
@@ -625,52 +600,45 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge8_kernel(const MaskedArg
       merge_ranges(ml, acc, a.num_splits, lane);
 }
 
-// Shared memory opt-in, once per device.
-template <typename Kernel>
-cudaError_t configure(Kernel kernel, std::atomic<unsigned long long>& done) {
+// Launch a streaming kernel, opting in to its shared memory once per device.
+template <auto kKernel>
+cudaError_t launch(const CUtensorMap& map, const MaskedArgs& a, int splits, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
   int device = 0;
   cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
   const unsigned long long bit = 1ull << (device & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmem));
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
-  return err;
-}
-
-template <int kFmt>
-cudaError_t launch_stream(const CUtensorMap& map, const MaskedArgs& a, const uint8_t* scales,
-                          cudaStream_t stream) {
-  static std::atomic<unsigned long long> done{0}, done_chunk{0};
-  const bool chunk = a.token_offsets != nullptr;
-  const cudaError_t err = chunk ? configure(paged8_chunk_kernel<kFmt>, done_chunk)
-                                : configure(paged8_decode_kernel<kFmt>, done);
-  if (err != cudaSuccess) return err;
-  if (!chunk)
-    return launch_pdl(paged8_decode_kernel<kFmt>, dim3(a.num_splits, a.batch), dim3(kThreads),
-                      kSmem, stream, map, a, scales);
-  return launch_pdl(paged8_chunk_kernel<kFmt>, dim3(a.num_tokens / kTileTokens + a.batch, a.num_splits),
-                    dim3(kThreads), kSmem, stream, map, a, scales);
-}
-
-template <bool kChunk>
-cudaError_t launch_merge(const MaskedArgs& a, cudaStream_t stream) {
-  static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
-  return launch_pdl(merge8_kernel<kChunk>, dim3(a.num_tokens * (kNumQHeads / kMergeRows)),
-                    dim3(32 * kMergeRows), 0, stream, a);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_pdl(kKernel, dim3(splits, a.batch), dim3(kThreads), kSmem, stream, map, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged8_attention(const CUtensorMap& page_map, const MaskedArgs& args,
-                                    const uint8_t* scales, int format, cudaStream_t stream) {
-  const cudaError_t err = format == kKv8E4m3
-                              ? launch_stream<kKv8E4m3>(page_map, args, scales, stream)
-                              : launch_stream<kKv8Int8>(page_map, args, scales, stream);
+cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
+                           cudaStream_t stream) {
+  const cudaError_t err =
+      format == kKv8E4m3
+          ? launch<paged8_decode_kernel<kKv8E4m3>>(page_map, args, args.num_splits, stream)
+          : launch<paged8_decode_kernel<kKv8Int8>>(page_map, args, args.num_splits, stream);
   if (err != cudaSuccess || args.num_splits == 1) return err;
-  return args.token_offsets != nullptr ? launch_merge<true>(args, stream)
-                                       : launch_merge<false>(args, stream);
+  static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
+  return launch_pdl(merge8_kernel, dim3(args.batch * (kNumQHeads / kMergeRows)),
+                    dim3(32 * kMergeRows), 0, stream, args);
+}
+
+cudaError_t launch_short_chunks8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
+                                 bool beside, cudaStream_t stream) {
+  const int n = args.short_splits;
+  if (format == kKv8E4m3)
+    return beside ? launch<paged8_short_chunk_kernel<kKv8E4m3, true>>(page_map, args, n, stream)
+                  : launch<paged8_short_chunk_kernel<kKv8E4m3, false>>(page_map, args, n, stream);
+  return beside ? launch<paged8_short_chunk_kernel<kKv8Int8, true>>(page_map, args, n, stream)
+                : launch<paged8_short_chunk_kernel<kKv8Int8, false>>(page_map, args, n, stream);
 }
 
 }  // namespace pkv

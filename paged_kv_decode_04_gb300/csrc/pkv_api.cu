@@ -1031,6 +1031,17 @@ bool chunk_plan(int num_tokens, int batch, int max_blocks, int window, int sinks
   return true;
 }
 
+// The ranges of a chunk call and their partials in its workspace: accumulators of
+// the long and of the short chunks, then the (max, sum) pairs.
+void set_parts(pkv::MaskedArgs& a, const ChunkPlan& plan, void* workspace) {
+  a.num_splits = plan.num_splits;
+  a.short_splits = plan.short_splits;
+  a.part_acc = static_cast<float*>(workspace);
+  a.short_acc = a.part_acc + plan.long_parts * kHeadDim;
+  a.part_ml = a.short_acc + plan.short_parts * kHeadDim;
+  a.short_ml = a.part_ml + plan.long_parts * 2;
+}
+
 size_t part_bytes(int batch, int splits) {
   return splits > 1 ? static_cast<size_t>(batch) * kNumQHeads * splits * (kHeadDim + 2) *
                           sizeof(float)
@@ -1149,14 +1160,7 @@ PKV_API int pkv_paged_chunk_attention(
   a.num_tokens = num_tokens;
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
-  a.num_splits = plan.num_splits;
-  a.short_splits = plan.short_splits;
-  // partials: accumulators of the long and of the short chunks, then the
-  // (max, sum) pairs
-  a.part_acc = static_cast<float*>(workspace);
-  a.short_acc = a.part_acc + plan.long_parts * kHeadDim;
-  a.part_ml = a.short_acc + plan.short_parts * kHeadDim;
-  a.short_ml = a.part_ml + plan.long_parts * 2;
+  set_parts(a, plan, workspace);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
   CUtensorMap q_map, page_map, pool_map;
@@ -1409,9 +1413,9 @@ pkv::Kv8 kv8_of(const void* pool, const uint8_t* scales, int format, int64_t num
 }
 
 // TMA descriptor of the 8-bit pool viewed as [num_pages][256 rows (K|V x kv head
-// x slot)][64] bytes, 64-byte swizzled, with boxes of box_rows rows: 256 take a
-// page, 16 a block.  Cached per thread for the last (device, pool, pages).
-bool pool8_map(const void* pool, int64_t num_pages, int box_rows, CUtensorMap* out) {
+// x slot)][64] bytes, 64-byte swizzled, with boxes of one page.  Cached per thread
+// for the last (device, pool, pages).
+bool pool8_map(const void* pool, int64_t num_pages, CUtensorMap* out) {
   struct Entry {
     int device = -1;
     const void* pool = nullptr;
@@ -1419,8 +1423,7 @@ bool pool8_map(const void* pool, int64_t num_pages, int box_rows, CUtensorMap* o
     CUtensorMap map;
   };
   constexpr int kRows = 2 * kNumKvHeads * kPageSize;
-  thread_local Entry cached[2];
-  Entry& c = cached[box_rows == kRows ? 0 : 1];
+  thread_local Entry c;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (c.device != dev || c.pool != pool || c.num_pages != num_pages) {
@@ -1431,7 +1434,7 @@ bool pool8_map(const void* pool, int64_t num_pages, int box_rows, CUtensorMap* o
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim),
                                    static_cast<cuuint64_t>(kRows * kHeadDim)};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim),
-                               static_cast<cuuint32_t>(box_rows), 1};
+                               static_cast<cuuint32_t>(kRows), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUtensorMap m;
     if (enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
@@ -1448,8 +1451,8 @@ bool pool8_map(const void* pool, int64_t num_pages, int box_rows, CUtensorMap* o
   return true;
 }
 
-// Ranges of `units` sequences (or row tiles) of at most `pages` pages, one CTA
-// for all kv heads each: CTAs for two an SM, but four pages a range or more.
+// Ranges of `units` sequences of at most `pages` pages, one CTA for all kv heads
+// each: CTAs for two an SM, but four pages a range or more.
 int stream8_splits(long long units, long long pages, int num_splits) {
   if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, pages));
   const int sms = current_sm_count();
@@ -1462,15 +1465,25 @@ int decode8_splits(int batch, int max_blocks, int window, int sinks, int num_spl
                         num_splits);
 }
 
-int chunk8_splits(int num_tokens, int batch, int max_blocks, int window, int sinks,
-                  int num_splits) {
+// chunk_plan with short chunks of one CTA for all kv heads.
+bool chunk8_plan(int num_tokens, int batch, int max_blocks, int window, int sinks, int num_splits,
+                 ChunkPlan* plan) {
+  if (!chunk_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, plan)) return false;
   const long long wide = static_cast<long long>(window) + pkv::kShortTokens - 1;
   const long long pages =
       window > 0 ? window_pages(max_blocks, static_cast<int>(std::min<long long>(wide, INT32_MAX)),
                                 sinks)
                  : max_blocks;
-  const long long tiles = num_tokens / pkv::kShortTokens + batch;
-  return stream8_splits(std::min<long long>(tiles, num_tokens), pages, num_splits);
+  // (more tokens than short chunks can have mean a long one, or a padded q)
+  const bool a_long_one = num_tokens > pkv::kShortTokens * static_cast<long long>(batch);
+  const int splits = stream8_splits(a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens),
+                                    pages, num_splits);
+  if (splits < 1) return false;
+  plan->short_splits = splits;
+  plan->short_parts = splits > 1 ? static_cast<size_t>(batch) * pkv::kShortTokens * kNumQHeads * splits
+                                 : 0;
+  plan->workspace = (plan->long_parts + plan->short_parts) * (kHeadDim + 2) * sizeof(float);
+  return true;
 }
 
 }  // namespace
@@ -1597,8 +1610,10 @@ PKV_API size_t pkv_chunk8_workspace_bytes(int num_tokens, int batch, int num_q_h
       num_splits < 0 || !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
   if (num_tokens == 0 || batch == 0) return 0;
-  const int splits = chunk8_splits(num_tokens, batch, max_blocks, window, sinks, num_splits);
-  return splits < 1 ? static_cast<size_t>(-1) : part_bytes(num_tokens, splits);
+  ChunkPlan plan;
+  if (!chunk8_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
+    return static_cast<size_t>(-1);
+  return plan.workspace;
 }
 
 PKV_API int pkv_paged8_decode_attention(
@@ -1630,6 +1645,8 @@ PKV_API int pkv_paged8_decode_attention(
   if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
+  a.codes = static_cast<const uint8_t*>(pool);
+  a.scales = scales;
   a.block_table = block_table;
   a.seq_lens = seq_lens;
   a.out = out;
@@ -1646,10 +1663,10 @@ PKV_API int pkv_paged8_decode_attention(
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
   CUtensorMap map;
-  if (!pool8_map(pool, num_pages, 2 * kNumKvHeads * kPageSize, &map)) return PKV_ECUDA;
-  const cudaError_t err = pkv::launch_paged8_attention(
-      map, a, scales, format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8,
-      reinterpret_cast<cudaStream_t>(stream));
+  if (!pool8_map(pool, num_pages, &map)) return PKV_ECUDA;
+  const cudaError_t err =
+      pkv::launch_decode8(map, a, format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8,
+                          reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -1678,13 +1695,16 @@ PKV_API int pkv_paged8_chunk_attention(
   const Span outs[] = {heads_span(out, num_tokens), ints(dev_err, 1)};
   if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0 || num_tokens == 0) return PKV_OK;
-  const int splits = chunk8_splits(num_tokens, batch, max_blocks, window, sinks, num_splits);
-  if (splits < 1) return PKV_ECUDA;
-  const size_t need = part_bytes(num_tokens, splits);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
-  if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
+  ChunkPlan plan;
+  if (!chunk8_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
+    return PKV_ECUDA;
+  if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
+    return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, plan.workspace}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
+  a.codes = static_cast<const uint8_t*>(pool);
+  a.scales = scales;
   a.block_table = block_table;
   a.seq_lens = seq_lens;
   a.token_offsets = token_offsets;
@@ -1696,16 +1716,19 @@ PKV_API int pkv_paged8_chunk_attention(
   a.num_tokens = num_tokens;
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
-  a.num_splits = splits;
-  a.part_acc = static_cast<float*>(workspace);
-  a.part_ml = a.part_acc + static_cast<size_t>(num_tokens) * kNumQHeads * splits * kHeadDim;
+  set_parts(a, plan, workspace);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  CUtensorMap map;
-  if (!pool8_map(pool, num_pages, 2 * kNumKvHeads * kPageSize, &map)) return PKV_ECUDA;
-  const cudaError_t err = pkv::launch_paged8_attention(
-      map, a, scales, format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8,
-      reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap q_map, page_map;
+  if (!chunk_q_map(q, num_tokens, &q_map) || !pool8_map(pool, num_pages, &page_map))
+    return PKV_ECUDA;
+  const int fmt = format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
+  if (plan.grid > 0) err = pkv::launch_chunk8_attention(q_map, a, fmt, plan.grid, st);
+  if (err == cudaSuccess) err = pkv::launch_short_chunks8(page_map, a, fmt, plan.grid > 0, st);
+  if (err == cudaSuccess) err = pkv::launch_short_merge(a, st);
+  if (err == cudaSuccess && plan.grid > 0 && a.num_splits > 1) err = pkv::launch_chunk_merge(a, st);
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -255,7 +255,9 @@ cudaError_t launch_shared_prefix_attention(const CUtensorMap& pool_map, const At
 // or t < sinks); window is at least 1 (INT32_MAX: no window).
 struct MaskedArgs {
   const uint16_t* q;
-  const uint16_t* pool;
+  const uint16_t* pool;          // a bf16 cache, or
+  const uint8_t* codes;          // an 8-bit one
+  const uint8_t* scales;         // and its scales (16-byte aligned, as the codes)
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* token_offsets;  // chunks only: [batch + 1]
@@ -297,6 +299,8 @@ cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& 
 // beside: right after launch_chunk_attention, next to whose CTAs these run.
 cudaError_t launch_short_chunks(const CUtensorMap& pool_map, const MaskedArgs& args, bool beside,
                                 cudaStream_t stream);
+// That merge by itself (nothing to do for one range).
+cudaError_t launch_short_merge(const MaskedArgs& args, cudaStream_t stream);
 // Combine the ranges of the long chunks' rows (num_splits > 1).
 cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream);
 
@@ -356,11 +360,17 @@ cudaError_t launch_kv8_read(uint16_t* k, uint16_t* v, int num_tokens,
                             const int32_t* token_offsets, const int32_t* start_positions,
                             const Kv8& cache, int num_sms, int32_t* dev_err, cudaStream_t stream);
 
-// Attention over the 8-bit cache (kv8_attention.cu; args.pool unused), of one
-// token a sequence or, with args.token_offsets, of chunks.
+// Attention over the 8-bit cache (args.codes and scales): of one token a
+// sequence, and the merge of its ranges; of chunks of more than kShortTokens
+// tokens (chunk_attention.cu); of the other chunks, with launch_short_merge, where
+// beside: right after launch_chunk8_attention (kv8_attention.cu).
 // page_map: boxes of one page's codes, 64-byte swizzled.
-cudaError_t launch_paged8_attention(const CUtensorMap& page_map, const MaskedArgs& args,
-                                    const uint8_t* scales, int format, cudaStream_t stream);
+cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
+                           cudaStream_t stream);
+cudaError_t launch_chunk8_attention(const CUtensorMap& q_map, const MaskedArgs& args, int format,
+                                    int grid, cudaStream_t stream);
+cudaError_t launch_short_chunks8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
+                                 bool beside, cudaStream_t stream);
 
 // Largest logical page range one attention CTA handles.
 int max_pages_per_split();
