@@ -89,7 +89,7 @@ constexpr int kKvPages = kKvTokens / kPageSize;
 constexpr int kRow = kHeadDim * 2;            // 128 B
 constexpr int kRowTileBytes = 128 * kRow;     // 16 KiB: a row tile of Q, a kv tile of K or V
 constexpr int kPageBytes = kPageSize * kRow;  // 2 KiB: one head's K (or V) rows of a page
-constexpr int kStages = 4;                    // kv tiles in flight
+constexpr int kMaxStages = 4;                 // kv tiles in flight, at most
 constexpr int kItems = 8;                     // slots for published items
 constexpr int kAhead = 3;                     // items published before the relay starts one
 constexpr int kSoftmaxWarps = 8;
@@ -103,37 +103,36 @@ template <bool kCodes>
 struct Roles {
   static constexpr int kThreads = 32 * (kCodes ? kConvertWarp + kConvertWarps : kConvertWarp);
   static constexpr int kLaunchRegs = kCodes ? 128 : 168;
-  static constexpr int kSoftmaxRegs = kCodes ? 184 : 200;
-  static constexpr int kOtherRegs = kCodes ? 72 : 104;
-  static_assert(kSoftmaxRegs * 256 + kOtherRegs * (kThreads - 256) <= kLaunchRegs * kThreads,
+  static constexpr int kSoftmaxRegs = kCodes ? 192 : 200;
+  static constexpr int kOtherRegs = kCodes ? 48 : 104;
+  static constexpr int kConvertRegs = 80;
+  static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 + (kCodes ? kConvertRegs * 128 : 0) <=
+                    kLaunchRegs * kThreads,
                 "the split stays within the registers the block starts with");
 };
-constexpr float kRescale = 65536.f;  // 2^16
+constexpr float kRescale = 65536.f;     // 2^16
+constexpr float kRescaleF16 = 32768.f;  // 2^15: every weight stays a finite f16
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemP = 256, kTmemO = 384;
-constexpr uint32_t kIdescQK = tc_idesc_bf16(128, kKvTokens, false);
-constexpr uint32_t kIdescPV = tc_idesc_bf16(128, kHeadDim, true);
+// (f16 operands: both formats 0)
+constexpr uint32_t kF16 = ~((1u << 7) | (1u << 10));
+template <bool kCodes>
+struct Idesc {
+  static constexpr uint32_t kQK = tc_idesc_bf16(128, kKvTokens, false) & (kCodes ? kF16 : ~0u);
+  static constexpr uint32_t kPV = tc_idesc_bf16(128, kHeadDim, true) & (kCodes ? kF16 : ~0u);
+};
 
-// Shared memory, from a 1024-byte aligned base.
-constexpr int kOffQ = 0;                               // [2 items][2 row tiles]
-constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
-constexpr int kOffV = kOffK + kStages * kRowTileBytes;
-constexpr int kOffOut = kOffV + kStages * kRowTileBytes;  // [warp][32 rows] of 128 B
-constexpr int kOutBytes = 32 * 128;
-constexpr int kOffMl = kOffOut + kSoftmaxWarps * kOutBytes;  // [128] (m, l) handed between groups
-constexpr int kOffItems = kOffMl + 128 * 8;
-constexpr int kItemWords = 16;
-constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
 enum {
   kBarKFull = 0,
-  kBarKEmpty = kBarKFull + kStages,
-  kBarVFull = kBarKEmpty + kStages,
-  kBarVReady = kBarVFull + kStages,
-  kBarVEmpty = kBarVReady + kStages,
-  kBarQFull = kBarVEmpty + kStages,
+  kBarKEmpty = kBarKFull + kMaxStages,
+  kBarVFull = kBarKEmpty + kMaxStages,
+  kBarVReady = kBarVFull + kMaxStages,
+  kBarVEmpty = kBarVReady + kMaxStages,
+  kBarQFull = kBarVEmpty + kMaxStages,
   kBarQEmpty = kBarQFull + 2,
-  kBarSFull = kBarQEmpty + 2,
+  kBarQReady = kBarQEmpty + 2,
+  kBarSFull = kBarQReady + 2,
   kBarSFree = kBarSFull + 2,
   kBarPFull = kBarSFree + 2,
   kBarPvDone = kBarPFull + 2,
@@ -145,15 +144,49 @@ enum {
   kBarPvFin,
   kNumBars
 };
-// The loader's notes on the last kv tiles (place in the sequence; bits of bad
-// pages, and kPartial), then the TMEM address.  Twice the stages: while a
-// softmax group reads kv tile j's, QK(j + 2) has not been issued, so the loads
-// are at tile j + 1 + kStages at most.
-constexpr int kMeta = 2 * kStages;
 constexpr uint32_t kPartial = 0x100;  // some row does not see some token
-constexpr int kOffMeta = kOffBars + 8 * kNumBars;
-constexpr int kSmem = 1024 + kOffMeta + 4 * (2 * kMeta + 4);
-static_assert(kSmem <= 227 * 1024, "fits one CTA");
+constexpr int kOutBytes = 32 * 128;
+constexpr int kItemWords = 16;
+
+// Shared memory, from a 1024-byte aligned base.
+template <bool kCodes>
+struct Layout {
+  static constexpr int kStages = kCodes ? 3 : kMaxStages;  // kv tiles in flight
+  static constexpr int kOffQ = 0;                          // [2 items][2 row tiles]
+  static constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kRowTileBytes;
+  static constexpr int kOffOut = kOffV + kStages * kRowTileBytes;  // [warp][32 rows] of 128 B
+  // [128] (m, l) handed between groups (and the scale of their V)
+  static constexpr int kOffMl = kOffOut + kSoftmaxWarps * kOutBytes;
+  static constexpr int kMlBytes = kCodes ? 16 : 8;
+  static constexpr int kOffItems = kOffMl + 128 * kMlBytes;
+  static constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
+  // Notes on the last kv tiles: place in the sequence; bits of bad pages, and
+  // kPartial; over codes also what Note says.  Then the TMEM address.  Twice the
+  // stages: while a softmax group reads kv tile j's, QK(j + 2) has not been
+  // issued, so the loads are at tile j + 1 + kStages at most.
+  static constexpr int kMeta = 2 * kStages, kMetaBytes = kCodes ? 64 : 8;
+  static constexpr int kOffMeta = kOffBars + 8 * ((kNumBars + 1) / 2 * 2);
+  static constexpr int kOffTmem = kOffMeta + kMeta * kMetaBytes;
+  static constexpr int kOffUndo = kOffTmem + 16;  // codes: [item][256 rows], see convert_q
+  // codes of the next kv tile, [K|V][row][thread] (each thread's are its own)
+  static constexpr int kOffRaw = kOffUndo + (kCodes ? kItems * 256 : 0);
+  static constexpr int kRawBytes = 16 * 32 * kConvertWarps;
+  static constexpr int kSmem = 1024 + kOffRaw + (kCodes ? 8 * kRawBytes : 0);
+  static_assert(kSmem <= 227 * 1024, "fits one CTA");
+};
+
+// Over codes a kv tile's note goes on with
+//   word 2   V's scale exponent that the tile's P V is in units of (0: no page)
+//   word 3   whether some page's weights take a factor (byte 48 + page)
+//   16       the pages' K scales, as floats
+//   48       octaves that a page's weights are to be divided by
+// V enters the product as f16 code * 2^d with d = its scale - word 2 in [-15, 7],
+// exactly; weights take the rest of scales further down.  Word 2 follows the
+// largest scale of an item's tiles so far, and moves when that is more than 2^7
+// above it.
+constexpr int kVDown = 15, kVUp = 7;
+constexpr float kLift = 6.f;  // f16 weights: the reference maximum's is 2^6
 
 // One item as the roles see it (also its words in shared memory).
 struct Item {
@@ -256,6 +289,27 @@ __device__ __forceinline__ int lds_int(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // True in one lane of the (converged) warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -354,144 +408,225 @@ __device__ __forceinline__ void add_nonfinite(const MaskedArgs& a, const Item& i
   }
 }
 
-// Eight codes (two words) as bf16 values times `s` (exact: a power of two), the
-// first in the low half of the first word.
-template <int kFmt>
-__device__ __forceinline__ uint4 codes_to_bf16(uint32_t w0, uint32_t w1, float s) {
-  uint32_t o[4];
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A converting warp turns its rows of an item's Q (32 w + lane, of each row tile
+// at `q`) into f16 times the power of two that takes the row's largest magnitude
+// to [2^14, 2^15), in place: exact for values down to 2^-31 of it.  `undo` gets
+// the biased exponents of the inverses.
+__device__ __forceinline__ void convert_q(uint32_t q, uint8_t* undo, int row_tiles, int w,
+                                          int lane) {
+#pragma unroll 1
+  for (int t = 0; t < row_tiles; ++t) {
+    const uint32_t row = q + t * kRowTileBytes + (32 * w + lane) * kRow;
+    uint32_t top = 0;  // largest finite magnitude
+#pragma unroll 2
+    for (int j = 0; j < 8; ++j) {
+      const uint4 x = lds128(row + ((j ^ (lane & 7)) << 4));
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w = i == 0 ? w0 : w1;
-    const float2 s2 = make_float2(s, s);
-    float2 lo, hi;
-    if constexpr (kFmt == kKv8E4m3) {
-      const float4 v = decode4<kFmt>(w);
-      lo = fmul2(make_float2(v.x, v.y), s2);
-      hi = fmul2(make_float2(v.z, v.w), s2);
-    } else {
-      // (2^23 + u) s - (2^23 + 128) s, u = code + 128: one rounding, of an exact value
-      const uint32_t u = w ^ 0x80808080u;
-      const float2 off = make_float2(-8388736.f * s, -8388736.f * s);
-      auto raw = [u](uint32_t sel) { return __uint_as_float(prmt(u, 0x4B000000u, sel)); };
-      lo = ffma2(make_float2(raw(0x7540u), raw(0x7541u)), s2, off);
-      hi = ffma2(make_float2(raw(0x7542u), raw(0x7543u)), s2, off);
+      for (int i = 0; i < 4; ++i)
+        top = __vmaxu2(top, y[i] & 0x7FFF7FFFu & ~nonfinite_halves(y[i]));
     }
-    o[2 * i] = pack_bf16x2(lo.x, lo.y);
-    o[2 * i + 1] = pack_bf16x2(hi.x, hi.y);
+    top = max(top & 0xFFFFu, top >> 16);
+    const int up = top == 0 ? 0 : min(max(14 + 127 - static_cast<int>(top >> 7), -126), 126);
+    const float2 f = make_float2(__uint_as_float(static_cast<uint32_t>(up + 127) << 23),
+                                 __uint_as_float(static_cast<uint32_t>(up + 127) << 23));
+    undo[128 * t + 32 * w + lane] = static_cast<uint8_t>(127 - up);
+#pragma unroll 2
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t at = row + ((j ^ (lane & 7)) << 4);
+      const uint4 x = lds128(at);
+      uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 z = fmul2(bf16x2_to_float2(y[i]), f);
+        y[i] = pack_f16x2(z.x, z.y);
+      }
+      sts128(at, y[0], y[1], y[2], y[3]);
+    }
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // One of the converting warps: it takes rows [32 w, 32 w + 32) (two pages) of the
 // K and V of every kv tile of the CTA's items, lane 4 r + c the 16 codes c of rows
-// r, r + 8, r + 16 and r + 24, loads them a tile ahead, straight from the pool
-// into registers, and stores them as bf16 where the TMA boxes would have put them
-// (128-byte swizzled).  False: a wait ran out.
+// r, r + 8, r + 16 and r + 24, copies them a tile ahead, straight from the pool
+// into its own places in shared memory, and stores them as f16 where the TMA boxes
+// would have put them (128-byte swizzled); and its rows of Q.  False: a wait ran
+// out.
 template <int kFmt>
-__device__ __forceinline__ bool convert_tiles(const MaskedArgs& a, uint32_t sb, uint32_t* s_meta,
-                                              int w, int lane) {
-  auto bar = [&](int i) { return sb + kOffBars + 8u * i; };
+__device__ __forceinline__ bool convert_tiles(const MaskedArgs& a, uint8_t* smem, int w,
+                                              int lane) {
+  using L = Layout<true>;
+  constexpr int kStages = L::kStages;
+  const uint32_t sb = smem_addr(smem);
+  auto bar = [&](int i) { return sb + L::kOffBars + 8u * i; };
   auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
-  // The tile whose codes are loaded next: page ids in lanes 0-7 (-1: bad, -2: no
-  // row sees it), and what its notes say.
+  // A tile of the walk, its entries of the block table in lanes 8 i + page.
+  struct Tile {
+    int tile, g, end, lo, ids;  // tile -1: no more
+    int row_tiles;              // of an item's first tile: Q's, else 0
+    bool part;
+  };
+  const int r = lane >> 2, c = lane & 3;
   Item it = {};
   int item = 0, k = 0;
-  int tile = -1, g = 0, end = 0, lo = 0, ids = -2;
-  bool part = false;
-  // false: a wait ran out; tile -1: no more
-  auto next = [&]() {
+  // The next tile, its table entries on their way; false: a wait ran out.
+  auto next = [&](Tile& x) {
+    x.row_tiles = 0;
     while (k >= it.t1) {
       const int slot = item % kItems;
       if (!wait(kBarItemFull + slot, item / kItems)) return false;
-      it = read_item(sb + kOffItems + 4u * kItemWords * slot);
+      it = read_item(sb + L::kOffItems + 4u * kItemWords * slot);
       __syncwarp();
       if (it.b < 0) {
-        tile = -1;
+        it.t1 = k;  // (asked again, the same answer)
+        x.tile = -1;
         return true;
       }
       if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
       ++item;
       k = it.t0;
+      x.row_tiles = it.halves() ? 1 : 2;
     }
-    tile = it.tile(k++);
-    g = it.g;
-    end = it.end();
-    lo = it.lo;
-    part = it.partial(tile, a);
-    const int page = tile * kKvPages + (lane & 7), t = page * kPageSize;
-    ids = -2;
-    if (t < end && (t + kPageSize > lo || t < a.sinks)) {
-      ids = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + page];
-      if (ids < 0 || ids >= a.num_pages) {
-        if (w == 0 && lane < 8) record_error(a.dev_err, kErrPage);
-        ids = -1;
-      }
-    }
+    x.tile = it.tile(k++);
+    x.g = it.g;
+    x.end = it.end();
+    x.lo = it.lo;
+    x.part = it.partial(x.tile, a);
+    const int page = x.tile * kKvPages + (lane & 7);
+    x.ids = -1;
+    if (page * kPageSize < x.end)
+      x.ids = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + page];
     return true;
   };
-  const int r = lane >> 2, c = lane & 3;
-  // scales of the warp's two pages: lanes 2 kv + p
-  auto load_scale = [&]() {
-    const int pid = __shfl_sync(kFull, ids, 2 * w + (lane & 1));
-    return pid >= 0 ? stored_scale(a.scales[scale_at(pid, (lane >> 1) & 1, g)]) : kScaleBias;
-  };
-  // row i of this lane: 32 w + 8 i + r, of page 2 w + i / 2
-  auto load = [&](int kv, uint4 (&x)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int pid = __shfl_sync(kFull, ids, 2 * w + (i >> 1));
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      // (V of tokens that no row sees: zeros, whatever their codes)
-      const int t = tile * kKvTokens + 32 * w + 8 * i + r;
-      if (pid >= 0 && (kv == 0 || (t < end && (t >= lo || t < a.sinks))))
-        x[i] = __ldcg(reinterpret_cast<const uint4*>(
-            a.codes + block_at(pid, kv, g) + (8 * (i & 1) + r) * kHeadDim + 16 * c));
+  // Its page ids: -1 where bad, -2 where no row sees the page.
+  auto settle = [&](Tile& x) {
+    const int t = (x.tile * kKvPages + (lane & 7)) * kPageSize;
+    if (!(t < x.end && (t + kPageSize > x.lo || t < a.sinks))) {
+      x.ids = -2;
+    } else if (x.ids < 0 || x.ids >= a.num_pages) {
+      if (w == 0 && lane < 8) record_error(a.dev_err, kErrPage);
+      x.ids = -1;
     }
   };
-  auto store = [&](uint32_t dst, const uint4 (&x)[4], float s0, float s1) {
+  // The pages' scales: lanes 8 kv + page.
+  auto load_scale = [&](const Tile& x) {
+    return lane < 16 && x.ids >= 0
+               ? static_cast<uint32_t>(a.scales[scale_at(x.ids, lane >> 3, x.g)])
+               : 0u;
+  };
+  const uint32_t raw = sb + L::kOffRaw + 16 * (32 * w + lane);
+  // Row i of this lane: 32 w + 8 i + r, of page 2 w + i / 2.  A copy group per
+  // call, empty where there is no tile.
+  auto load = [&](const Tile& x, int kv) {
+    if (x.tile >= 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int pid = __shfl_sync(kFull, x.ids, 2 * w + (i >> 1));
+        // (V of tokens that no row sees: zeros, whatever their codes)
+        const int t = x.tile * kKvTokens + 32 * w + 8 * i + r;
+        const bool in = pid >= 0 && (kv == 0 || (t < x.end && (t >= x.lo || t < a.sinks)));
+        const uint8_t* src =
+            a.codes + (in ? block_at(pid, kv, x.g) + (8 * (i & 1) + r) * kHeadDim + 16 * c : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         raw + (4 * kv + i) * L::kRawBytes),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // (the last group is the other one of K's and V's)
+  auto store = [&](uint32_t dst, int kv, uint32_t f0, uint32_t f1) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float s = i < 2 ? s0 : s1;
+      const uint32_t f = i < 2 ? f0 : f1;
       const uint32_t row = dst + (32 * w + 8 * i + r) * kRow;
-      const uint4 y = codes_to_bf16<kFmt>(x[i].x, x[i].y, s);
-      sts128(row + (((2 * c) ^ r) << 4), y.x, y.y, y.z, y.w);
-      const uint4 z = codes_to_bf16<kFmt>(x[i].z, x[i].w, s);
-      sts128(row + (((2 * c + 1) ^ r) << 4), z.x, z.y, z.z, z.w);
+      const uint4 x = lds128(raw + (4 * kv + i) * L::kRawBytes);
+      uint32_t y[8];
+      decode_f16<kFmt>(x.x, y[0], y[1]);
+      decode_f16<kFmt>(x.y, y[2], y[3]);
+      decode_f16<kFmt>(x.z, y[4], y[5]);
+      decode_f16<kFmt>(x.w, y[6], y[7]);
+      if (f != 0x3C003C00u) {  // 1.0 twice
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = hmul2(y[e], f);
+      }
+      sts128(row + (((2 * c) ^ r) << 4), y[0], y[1], y[2], y[3]);
+      sts128(row + (((2 * c + 1) ^ r) << 4), y[4], y[5], y[6], y[7]);
     }
     fence_proxy_async_smem();
     __syncwarp();
   };
-  if (!next()) return false;
-  uint4 xk[4], xv[4];
-  uint32_t scale = kScaleBias;
-  if (tile >= 0) {
-    scale = load_scale();
-    load(0, xk);
-    load(1, xv);
+  // x: the tile whose codes are being copied; y: the one after it
+  Tile x, y;
+  uint32_t scale = 0, unit = 0;  // this lane's page's; the item's V is in units of
+  int qn = 0;
+  if (!next(x)) return false;
+  y.tile = -1;
+  if (x.tile >= 0) {
+    if (!next(y)) return false;
+    settle(x);
+    scale = load_scale(x);
+    load(x, 0);
+    load(x, 1);
   }
-  for (int kt = 0; tile >= 0; ++kt) {
+  for (int kt = 0; x.tile >= 0; ++kt) {
     const int st = kt % kStages;
+    if (x.row_tiles > 0) {
+      const int qb = qn & 1;
+      if (!wait(kBarQFull + qb, qn >> 1)) return false;
+      // (x's item is the last read, or the one before when y begins another)
+      const int slot = (y.tile >= 0 && y.row_tiles > 0 ? item - 2 : item - 1) % kItems;
+      convert_q(sb + L::kOffQ + 2 * qb * kRowTileBytes, smem + L::kOffUndo + 256 * slot,
+                x.row_tiles, w, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQReady + qb));
+      ++qn;
+      unit = 0;
+    }
     if (kt >= kStages && !wait(kBarKEmpty + st, kt / kStages - 1)) return false;
+    const uint32_t e = x.ids >= 0 && lane < 16 ? stored_scale(scale) : 0u;
+    const uint32_t most = __reduce_max_sync(kFull, lane >= 8 ? e : 0u);
+    if (most > 0 && (unit == 0 || most > unit + kVUp)) unit = most;
+    const int d = static_cast<int>(e) - static_cast<int>(unit);
+    const int dv = max(d, -kVDown);
+    const uint32_t f = dv == -kVDown ? 0x0200u : static_cast<uint32_t>(dv + 15) << 10;
     if (w == 0) {
-      const unsigned bad = __ballot_sync(kFull, ids == -1) & 0xFFu;
+      uint8_t* note = smem + L::kOffMeta + L::kMetaBytes * (kt % L::kMeta);
+      const unsigned bad = __ballot_sync(kFull, x.ids == -1) & 0xFFu;
+      const unsigned ext = __ballot_sync(kFull, lane >= 8 && e > 0 && d < dv);
+      if (lane < 8) {
+        reinterpret_cast<float*>(note + 16)[lane] = e > 0 ? scale_value(e) : 1.f;
+      } else if (lane < 16) {
+        note[40 + lane] = static_cast<uint8_t>(e > 0 ? dv - d : 0);
+      }
       if (lane == 0)
-        *reinterpret_cast<uint2*>(s_meta + 2 * (kt % kMeta)) =
-            make_uint2(tile, bad | (part ? kPartial : 0u));
+        *reinterpret_cast<uint4*>(note) =
+            make_uint4(x.tile, bad | (x.part ? kPartial : 0u), unit, ext);
     }
-    float s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = scale_value(__shfl_sync(kFull, scale, i));
-    store(sb + kOffK + st * kRowTileBytes, xk, s[0], s[1]);
+    const uint32_t f0 = __shfl_sync(kFull, f, 8 + 2 * w) * 0x10001u;
+    const uint32_t f1 = __shfl_sync(kFull, f, 9 + 2 * w) * 0x10001u;
+    store(sb + L::kOffK + st * kRowTileBytes, 0, 0x3C003C00u, 0x3C003C00u);
     if (lane == 0) mbar_arrive(bar(kBarKFull + st));
-    if (!next()) return false;
-    if (tile >= 0) {
-      scale = load_scale();
-      load(0, xk);
+    x = y;
+    if (x.tile >= 0) {
+      settle(x);
+      scale = load_scale(x);
     }
+    load(x, 0);
+    if (x.tile >= 0 && !next(y)) return false;
     if (kt >= kStages && !wait(kBarVEmpty + st, kt / kStages - 1)) return false;
-    store(sb + kOffV + st * kRowTileBytes, xv, s[2], s[3]);
+    store(sb + L::kOffV + st * kRowTileBytes, 1, f0, f1);
     if (lane == 0) mbar_arrive(bar(kBarVReady + st));
-    if (tile >= 0) load(1, xv);
+    load(x, 1);
   }
   return true;
 }
@@ -502,6 +637,11 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
     const MaskedArgs a) {
   constexpr bool kCodes = kFmt != kBf16;
   using R = Roles<kCodes>;
+  using Lay = Layout<kCodes>;
+  constexpr int kStages = Lay::kStages, kMeta = Lay::kMeta;
+  constexpr int kOffQ = Lay::kOffQ, kOffK = Lay::kOffK, kOffV = Lay::kOffV;
+  constexpr int kOffOut = Lay::kOffOut, kOffMl = Lay::kOffMl, kOffItems = Lay::kOffItems;
+  constexpr int kOffBars = Lay::kOffBars, kOffMeta = Lay::kOffMeta;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -510,7 +650,6 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
   auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
   int* s_items = reinterpret_cast<int*>(smem + kOffItems);
   auto item_addr = [&](int slot) { return sb + kOffItems + 4u * kItemWords * slot; };
-  // [kMeta][2], then the TMEM address
   uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -526,6 +665,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         n = kSoftmaxWarps + (kCodes ? 3 + kConvertWarps : 4);
       if (kCodes && ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVReady && i < kBarVEmpty)))
         n = kConvertWarps;
+      if (i >= kBarQReady && i < kBarSFull) n = kConvertWarps;
       if (i == kBarXFull || i == kBarXFree) n = 4;
       mbar_init(bar(i), n);
     }
@@ -533,22 +673,23 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
   }
   if (warp == kQkWarp) {
     __syncwarp();
-    tmem_alloc(sb + kOffMeta + 8 * kMeta, kTmemCols);
+    tmem_alloc(sb + Lay::kOffTmem, kTmemCols);
     tmem_relinquish_alloc_permit();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = s_meta[2 * kMeta];
+  const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + Lay::kOffTmem);
   wait_for_prior_grids();
   allow_dependent_grids();
 
   bool ok = true;
   if (kCodes && warp >= kConvertWarp) {
     if constexpr (kCodes) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kConvertRegs));
       // ---------------------------------------------- K and V from codes
-      ok = convert_tiles<kFmt>(a, sb, s_meta, warp - kConvertWarp, lane);
+      ok = convert_tiles<kFmt>(a, smem, warp - kConvertWarp, lane);
+      asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
     }
   } else if (warp >= kQkWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
@@ -840,7 +981,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         const int U = x.y;
         const bool one = x.w != 0;
         if (U == 0) break;
-        if (!(ok = wait(kBarQFull + qb, i >> 1))) break;
+        if (!(ok = wait((kCodes ? kBarQReady : kBarQFull) + qb, i >> 1))) break;
         const uint32_t q0 = desc_lo(sb + kOffQ + 2 * qb * kRowTileBytes);
         for (int u = 0; u < U; ++u, ++n) {
           const int w = n & 1, st = kt % kStages;
@@ -853,7 +994,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           if (issuer) {
 #pragma unroll
             for (int kk = 0; kk < kHeadDim / 16; ++kk)
-              mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
+              mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, Idesc<kCodes>::kQK, kk > 0);
             tc_commit(bar(kBarSFull + w));
             if (last) tc_commit(bar(kBarKEmpty + st));
             if (u == U - 1) tc_commit(bar(kBarQEmpty + qb));
@@ -888,10 +1029,10 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           const uint32_t vr = desc_lo(sb + kOffV) + st * (kRowTileBytes >> 4);
           if (issuer) {
             const uint32_t d = tmem + kTmemO + kHeadDim * w, pa = tmem + kTmemP + 64 * w;
-            mma_ts(d, pa, vr, kIdescPV, u >= 2);  // a group's first unit of the item starts O
+            mma_ts(d, pa, vr, Idesc<kCodes>::kPV, u >= 2);  // a group's first unit of the item starts O
 #pragma unroll
             for (int p = 1; p < kKvPages; ++p)
-              mma_ts(d, pa + 8 * p, vr + p * (kPageBytes >> 4), kIdescPV, true);
+              mma_ts(d, pa + 8 * p, vr + p * (kPageBytes >> 4), Idesc<kCodes>::kPV, true);
             tc_commit(bar(kBarPvDone + w));
             if (last) tc_commit(bar(kBarVEmpty + st));
           }
@@ -931,6 +1072,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         first = one && w != it.first_w ? 1 : 0;
       }
       float m_ref = -INFINITY, l_run = 0.f;
+      uint32_t unit = 0;  // codes: O is in units of 2^(unit - 127)
       for (int v = 0; v < nu; ++v, ++units) {
         if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
@@ -945,7 +1087,9 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           return true;
         };
         // (written before the loads that QK waited for)
-        const uint2 note = lds64(sb + kOffMeta + 8u * ((kt0 + first + (one ? 2 * v : v)) % kMeta));
+        const uint32_t note_at =
+            sb + kOffMeta + Lay::kMetaBytes * ((kt0 + first + (one ? 2 * v : v)) % kMeta);
+        const uint2 note = lds64(note_at);
         if (idle) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarSFree + w));
@@ -987,34 +1131,64 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           bool measure = __any_sync(kFull, m_ref == -INFINITY);
           if (!(ok = o_ready())) break;
           tc_fence_after_sync();
+          auto scale_o = [&](float f) {
+#pragma unroll 1
+            for (int q = 0; q < kHeadDim / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * q, o);
+              tmem_wait_ld();
+              reg_after_wait(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tO + 16 * q, o);
+            }
+          };
+          float c_row = c;
+          if constexpr (kCodes) {
+            // Q's row was multiplied by a power of two; the tile may be in larger
+            // units of V than O is
+            c_row *= scale_value(lds8(sb + Lay::kOffUndo + 256 * slot + row + (one ? 0 : 128 * w)));
+            const uint32_t u = lds32(note_at + 8);
+            if (u != unit && u != 0u) {
+              if (v > 0 && unit != 0u) {
+                scale_o(u - unit > 126u ? 0.f : scale_value(127 + unit - u));
+                tmem_wait_st();
+              }
+              unit = u;
+            }
+          }
           for (;;) {
             float alpha = 1.f;
             if (measure) {
               float mx[2] = {-INFINITY, -INFINITY};
+              if constexpr (kCodes) {
+                float best = -INFINITY;  // of the pages, each with its scale
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 8; ++q) {
+                  float y = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                  mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[q][e]),
-                                           __uint_as_float(x[q][e + 1]));
-              const float top = fmaxf(mx[0], mx[1]) * c;
+                  for (int e = 0; e < 16; e += 2)
+                    y = fmax3(y, __uint_as_float(x[q >> 1][16 * (q & 1) + e]),
+                              __uint_as_float(x[q >> 1][16 * (q & 1) + e + 1]));
+                  best = fmaxf(best, y * (c_row * __uint_as_float(lds32(note_at + 16 + 4 * q))));
+                }
+                mx[0] = best - kLift;
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                  for (int e = 0; e < 32; e += 2)
+                    mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[q][e]),
+                                             __uint_as_float(x[q][e + 1]));
+              }
+              const float top = kCodes ? fmaxf(mx[0], mx[1]) : fmaxf(mx[0], mx[1]) * c;
               if (top > m_ref) {
                 alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
                 m_ref = top;
               }
               if (v > 0 && __any_sync(kFull, alpha != 1.f)) {
                 l_run *= alpha;
-#pragma unroll 1
-                for (int q = 0; q < kHeadDim / 16; ++q) {
-                  uint32_t o[16];
-                  tmem_ld16(tO + 16 * q, o);
-                  tmem_wait_ld();
-                  reg_after_wait(o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                  tmem_st16(tO + 16 * q, o);
-                }
+                scale_o(alpha);
               }
             }
             // (a row that has seen no token yet: every weight 2^(-inf) = 0)
@@ -1024,22 +1198,32 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t pw[32];
+              uint4 k_scales = make_uint4(0u, 0u, 0u, 0u);  // of the pages of this half
+              if constexpr (kCodes) k_scales = lds128(note_at + 16 + 16 * q);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const uint32_t* s2 = &x[2 * q + (e >> 4)][2 * (e & 15)];
+                float2 cp = c2;
+                if constexpr (kCodes) {
+                  const uint32_t k = e < 8    ? k_scales.x
+                                     : e < 16 ? k_scales.y
+                                     : e < 24 ? k_scales.z
+                                              : k_scales.w;
+                  cp.x = cp.y = fmaxf(c_row * __uint_as_float(k), 0x1p-126f);  // (0 x -inf is NaN)
+                }
                 float2 y = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])),
-                                 c2, m2);
+                                 cp, m2);
                 y.x = fast_exp2(y.x);
                 y.y = fast_exp2(y.y);
                 ls[e & 1] = fadd2(ls[e & 1], y);
-                pw[e] = pack_bf16x2(y.x, y.y);
+                pw[e] = kCodes ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
               }
               tmem_st32(tP + 32 * q, pw);
             }
             const float2 l2 = fadd2(ls[0], ls[1]);
             const float sum = l2.x + l2.y;
             // (NaN too; a tile that has just been measured stands as it is)
-            const bool over = !(sum < kRescale);
+            const bool over = !(sum < (kCodes ? kRescaleF16 : kRescale));
             if (measure || !__any_sync(kFull, over)) {
               l_run += sum;
               break;
@@ -1047,6 +1231,28 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
             measure = true;
           }
           tmem_wait_st();
+          if constexpr (kCodes) {
+            if (lds32(note_at + 12) != 0u) {  // pages whose V scales are far below the unit
+#pragma unroll 1
+              for (int p = 0; p < kKvPages; ++p) {
+                const uint32_t down = lds8(note_at + 48 + p);
+                if (down == 0u) continue;
+                const uint32_t f = down > 24u  ? 0u
+                                   : down > 14u ? 1u << (24u - down)
+                                                : (15u - down) << 10;
+                uint32_t y[8];
+                tmem_ld8(tP + 8 * p, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  asm volatile("" : "+r"(y[e]));  // (after the wait)
+                  y[e] = hmul2(y[e], f * 0x10001u);
+                }
+                tmem_st8(tP + 8 * p, y);
+              }
+              tmem_wait_st();
+            }
+          }
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -1063,12 +1269,15 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       tc_fence_after_sync();
       bool writes = tok < it.nt;
       const bool other = one && it.units_of(1) > 0;  // both groups saw these rows
-      float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + row;
+      float* xml = reinterpret_cast<float*>(smem + kOffMl + Lay::kMlBytes * row);
+      const float v_unit = kCodes && unit != 0u ? scale_value(unit) : 1.f;
       if (one && w == 1) {
         // the first group takes this one's rows from TMEM (the same lanes)
         writes = false;
         if (other) {
-          *xml = make_float2(m_ref, l_run);
+          xml[0] = m_ref;
+          xml[1] = l_run;
+          if constexpr (kCodes) xml[2] = v_unit;
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarXFull));
@@ -1079,14 +1288,16 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       if (other && w == 0) {
         if (!(ok = wait(kBarXFull, xn))) break;
         tc_fence_after_sync();
-        const float2 ml = *xml;
+        const float2 ml = make_float2(xml[0], xml[1]);
         const float M = fmaxf(m_ref, ml.x);
         // (a group whose tiles the row did not see: zeros)
         w0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
         w1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
         l_run = l_run * w0 + ml.y * w1;
         m_ref = M;
+        if constexpr (kCodes) w1 *= xml[2];
       }
+      if constexpr (kCodes) w0 *= v_unit;
       // (written before the last kv tile's V was handed to its PV, which this
       // row's group, or the other one, has waited for)
       const int bad_v =
@@ -1211,6 +1422,7 @@ template <int kFmt>
 cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& page_map, const MaskedArgs& args,
                    int grid, cudaStream_t stream) {
   using R = Roles<kFmt != kBf16>;
+  using L = Layout<kFmt != kBf16>;
   int device = 0;
   cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
@@ -1222,12 +1434,12 @@ cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& page_map, const 
     // the register split must stay within what the block starts with
     if (fa.numRegs != R::kLaunchRegs) return cudaErrorInvalidConfiguration;
     err = cudaFuncSetAttribute(paged_chunk_kernel<kFmt>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (err != cudaSuccess) return err;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch_pdl(paged_chunk_kernel<kFmt>, dim3(grid), dim3(R::kThreads), kSmem, stream, q_map,
-                    page_map, args);
+  return launch_pdl(paged_chunk_kernel<kFmt>, dim3(grid), dim3(R::kThreads), L::kSmem, stream,
+                    q_map, page_map, args);
 }
 
 }  // namespace

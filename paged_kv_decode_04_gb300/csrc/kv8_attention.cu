@@ -79,11 +79,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
   float2 f;
   asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, "
@@ -93,11 +88,6 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
   return f;
 }
 
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -159,7 +149,7 @@ __device__ __forceinline__ float load_q(const uint16_t* row, int ft, uint32_t (&
   top = max(top, __shfl_xor_sync(kFull, top, 1));
   top = max(top, __shfl_xor_sync(kFull, top, 2));
   // 2^(14 - exponent), within normal numbers
-  const int up = min(max(14 + 127 - static_cast<int>(top >> 7), -126), 126);
+  const int up = top == 0 ? 0 : min(max(14 + 127 - static_cast<int>(top >> 7), -126), 126);
   const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
