@@ -433,7 +433,7 @@ __device__ __forceinline__ void convert_q(uint32_t q, uint8_t* undo, int row_til
         top = __vmaxu2(top, y[i] & 0x7FFF7FFFu & ~nonfinite_halves(y[i]));
     }
     top = max(top & 0xFFFFu, top >> 16);
-    const int up = top == 0 ? 0 : min(max(14 + 127 - static_cast<int>(top >> 7), -126), 126);
+    const int up = top == 0 ? 0 : min(14 + 127 - static_cast<int>(top >> 7), 60);
     const float2 f = make_float2(__uint_as_float(static_cast<uint32_t>(up + 127) << 23),
                                  __uint_as_float(static_cast<uint32_t>(up + 127) << 23));
     undo[128 * t + 32 * w + lane] = static_cast<uint8_t>(127 - up);
@@ -449,6 +449,27 @@ __device__ __forceinline__ void convert_q(uint32_t q, uint8_t* undo, int row_til
       }
       sts128(at, y[0], y[1], y[2], y[3]);
     }
+  }
+}
+
+// Divide the weights of a kv tile's pages (16 columns of f16 pairs' halves: 8
+// words each) by 2^n, n the bytes at `down`.
+__device__ __noinline__ void scale_weights(uint32_t tP, uint32_t down) {
+  tmem_wait_st();
+#pragma unroll 1
+  for (int p = 0; p < kKvPages; ++p) {
+    const uint32_t n = lds8(down + p);
+    if (n == 0u) continue;
+    const uint32_t f = n > 24u ? 0u : n > 14u ? 1u << (24u - n) : (15u - n) << 10;
+    uint32_t y[8];
+    tmem_ld8(tP + 8 * p, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      asm volatile("" : "+r"(y[e]));  // (after the wait)
+      y[e] = hmul2(y[e], f * 0x10001u);
+    }
+    tmem_st8(tP + 8 * p, y);
   }
 }
 
@@ -604,7 +625,11 @@ __device__ __forceinline__ bool convert_tiles(const MaskedArgs& a, uint8_t* smem
       const unsigned bad = __ballot_sync(kFull, x.ids == -1) & 0xFFu;
       const unsigned ext = __ballot_sync(kFull, lane >= 8 && e > 0 && d < dv);
       if (lane < 8) {
-        reinterpret_cast<float*>(note + 16)[lane] = e > 0 ? scale_value(e) : 1.f;
+        // (2^-60 or more, as what undoes Q's power of two: times each other and an
+        // unseen token's -inf they stay -inf; what this adds to smaller scales'
+        // scores is far below 1)
+        reinterpret_cast<float*>(note + 16)[lane] =
+            e > 0 ? scale_value(max(e, static_cast<uint32_t>(kScaleBias - 60))) : 1.f;
       } else if (lane < 16) {
         note[40 + lane] = static_cast<uint8_t>(e > 0 ? dv - d : 0);
       }
@@ -1073,6 +1098,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       }
       float m_ref = -INFINITY, l_run = 0.f;
       uint32_t unit = 0;  // codes: O is in units of 2^(unit - 127)
+      float c_row = c;    // codes: undoes the power of two of Q's row
       for (int v = 0; v < nu; ++v, ++units) {
         if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
@@ -1089,7 +1115,16 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         // (written before the loads that QK waited for)
         const uint32_t note_at =
             sb + kOffMeta + Lay::kMetaBytes * ((kt0 + first + (one ? 2 * v : v)) % kMeta);
-        const uint2 note = lds64(note_at);
+        uint4 note = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kCodes) {
+          note = lds128(note_at);
+          if (v == 0)
+            c_row *= scale_value(lds8(sb + Lay::kOffUndo + 256 * slot + row + (one ? 0 : 128 * w)));
+        } else {
+          const uint2 n = lds64(note_at);
+          note.x = n.x;
+          note.y = n.y;
+        }
         if (idle) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarSFree + w));
@@ -1129,37 +1164,21 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           // of, and moves only when a tile's weights sum to 2^kRescale or more
           // (FP32 sums and bf16 weights keep their relative precision below).
           bool measure = __any_sync(kFull, m_ref == -INFINITY);
+          // (what is rare about codes is dealt with on the measuring path too)
+          if constexpr (kCodes) measure |= note.z != unit || note.w != 0u;
           if (!(ok = o_ready())) break;
           tc_fence_after_sync();
-          auto scale_o = [&](float f) {
-#pragma unroll 1
-            for (int q = 0; q < kHeadDim / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld16(tO + 16 * q, o);
-              tmem_wait_ld();
-              reg_after_wait(o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(tO + 16 * q, o);
-            }
-          };
-          float c_row = c;
-          if constexpr (kCodes) {
-            // Q's row was multiplied by a power of two; the tile may be in larger
-            // units of V than O is
-            c_row *= scale_value(lds8(sb + Lay::kOffUndo + 256 * slot + row + (one ? 0 : 128 * w)));
-            const uint32_t u = lds32(note_at + 8);
-            if (u != unit && u != 0u) {
-              if (v > 0 && unit != 0u) {
-                scale_o(u - unit > 126u ? 0.f : scale_value(127 + unit - u));
-                tmem_wait_st();
-              }
-              unit = u;
-            }
-          }
           for (;;) {
             float alpha = 1.f;
             if (measure) {
+              float o_unit = 1.f;  // O in the tile's units of V
+              if constexpr (kCodes) {
+                if (note.z != unit && note.z != 0u) {
+                  if (unit != 0u)
+                    o_unit = note.z - unit > 126u ? 0.f : scale_value(127 + unit - note.z);
+                  unit = note.z;
+                }
+              }
               float mx[2] = {-INFINITY, -INFINITY};
               if constexpr (kCodes) {
                 float best = -INFINITY;  // of the pages, each with its scale
@@ -1186,9 +1205,19 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
                 alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
                 m_ref = top;
               }
-              if (v > 0 && __any_sync(kFull, alpha != 1.f)) {
+              if (v > 0 && __any_sync(kFull, alpha != 1.f || o_unit != 1.f)) {
                 l_run *= alpha;
-                scale_o(alpha);
+#pragma unroll 1
+                for (int q = 0; q < kHeadDim / 16; ++q) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * q, o);
+                  tmem_wait_ld();
+                  reg_after_wait(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha * o_unit));
+                  tmem_st16(tO + 16 * q, o);
+                }
               }
             }
             // (a row that has seen no token yet: every weight 2^(-inf) = 0)
@@ -1209,7 +1238,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
                                      : e < 16 ? k_scales.y
                                      : e < 24 ? k_scales.z
                                               : k_scales.w;
-                  cp.x = cp.y = fmaxf(c_row * __uint_as_float(k), 0x1p-126f);  // (0 x -inf is NaN)
+                  cp.x = cp.y = c_row * __uint_as_float(k);
                 }
                 float2 y = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])),
                                  cp, m2);
@@ -1224,35 +1253,18 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
             const float sum = l2.x + l2.y;
             // (NaN too; a tile that has just been measured stands as it is)
             const bool over = !(sum < (kCodes ? kRescaleF16 : kRescale));
-            if (measure || !__any_sync(kFull, over)) {
-              l_run += sum;
-              break;
+            if (!measure && __any_sync(kFull, over)) {
+              measure = true;
+              continue;
             }
-            measure = true;
+            l_run += sum;
+            if constexpr (kCodes) {
+              // weights of pages whose V scales are far below the unit
+              if (measure && note.w != 0u) scale_weights(tP, note_at + 48);
+            }
+            break;
           }
           tmem_wait_st();
-          if constexpr (kCodes) {
-            if (lds32(note_at + 12) != 0u) {  // pages whose V scales are far below the unit
-#pragma unroll 1
-              for (int p = 0; p < kKvPages; ++p) {
-                const uint32_t down = lds8(note_at + 48 + p);
-                if (down == 0u) continue;
-                const uint32_t f = down > 24u  ? 0u
-                                   : down > 14u ? 1u << (24u - down)
-                                                : (15u - down) << 10;
-                uint32_t y[8];
-                tmem_ld8(tP + 8 * p, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  asm volatile("" : "+r"(y[e]));  // (after the wait)
-                  y[e] = hmul2(y[e], f * 0x10001u);
-                }
-                tmem_st8(tP + 8 * p, y);
-              }
-              tmem_wait_st();
-            }
-          }
         }
         tc_fence_before_sync();
         __syncwarp();
