@@ -73,7 +73,6 @@
 
 #include <atomic>
 
-#include "kv8.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -89,50 +88,42 @@ constexpr int kKvPages = kKvTokens / kPageSize;
 constexpr int kRow = kHeadDim * 2;            // 128 B
 constexpr int kRowTileBytes = 128 * kRow;     // 16 KiB: a row tile of Q, a kv tile of K or V
 constexpr int kPageBytes = kPageSize * kRow;  // 2 KiB: one head's K (or V) rows of a page
-constexpr int kMaxStages = 4;                 // kv tiles in flight, at most
+constexpr int kStages = 4;                    // kv tiles in flight
 constexpr int kItems = 8;                     // slots for published items
 constexpr int kAhead = 3;                     // items published before the relay starts one
 constexpr int kSoftmaxWarps = 8;
 constexpr int kQkWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11 issues PV
-constexpr int kConvertWarp = 12, kConvertWarps = 4;         // over an 8-bit cache
-// The cache's format: bf16 pages, or codes (kKv8E4m3, kKv8Int8).
-constexpr int kBf16 = -1;
-// Threads and registers of the roles: 168 x 384 threads at launch = 64512 = 256 x
-// 200 + 128 x 104; with converting warps 128 x 512 = 256 x 184 + 256 x 72.
-template <bool kCodes>
-struct Roles {
-  static constexpr int kThreads = 32 * (kCodes ? kConvertWarp + kConvertWarps : kConvertWarp);
-  static constexpr int kLaunchRegs = kCodes ? 128 : 168;
-  static constexpr int kSoftmaxRegs = kCodes ? 192 : 200;
-  static constexpr int kOtherRegs = kCodes ? 48 : 104;
-  static constexpr int kConvertRegs = 80;
-  static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 + (kCodes ? kConvertRegs * 128 : 0) <=
-                    kLaunchRegs * kThreads,
-                "the split stays within the registers the block starts with");
-};
-constexpr float kRescale = 65536.f;     // 2^16
-constexpr float kRescaleF16 = 32768.f;  // 2^15: every weight stays a finite f16
+constexpr int kThreads = 32 * 12;
+// Registers: 168 x 384 threads at launch = 64512 = 256 x 200 + 128 x 104.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads,
+              "the split stays within the registers the block starts with");
+constexpr float kRescale = 65536.f;  // 2^16
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemP = 256, kTmemO = 384;
-// (f16 operands: both formats 0)
-constexpr uint32_t kF16 = ~((1u << 7) | (1u << 10));
-template <bool kCodes>
-struct Idesc {
-  static constexpr uint32_t kQK = tc_idesc_bf16(128, kKvTokens, false) & (kCodes ? kF16 : ~0u);
-  static constexpr uint32_t kPV = tc_idesc_bf16(128, kHeadDim, true) & (kCodes ? kF16 : ~0u);
-};
+constexpr uint32_t kIdescQK = tc_idesc_bf16(128, kKvTokens, false);
+constexpr uint32_t kIdescPV = tc_idesc_bf16(128, kHeadDim, true);
 
+// Shared memory, from a 1024-byte aligned base.
+constexpr int kOffQ = 0;                               // [2 items][2 row tiles]
+constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
+constexpr int kOffV = kOffK + kStages * kRowTileBytes;
+constexpr int kOffOut = kOffV + kStages * kRowTileBytes;  // [warp][32 rows] of 128 B
+constexpr int kOutBytes = 32 * 128;
+constexpr int kOffMl = kOffOut + kSoftmaxWarps * kOutBytes;  // [128] (m, l) handed between groups
+constexpr int kOffItems = kOffMl + 128 * 8;
+constexpr int kItemWords = 16;
+constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
 enum {
   kBarKFull = 0,
-  kBarKEmpty = kBarKFull + kMaxStages,
-  kBarVFull = kBarKEmpty + kMaxStages,
-  kBarVReady = kBarVFull + kMaxStages,
-  kBarVEmpty = kBarVReady + kMaxStages,
-  kBarQFull = kBarVEmpty + kMaxStages,
+  kBarKEmpty = kBarKFull + kStages,
+  kBarVFull = kBarKEmpty + kStages,
+  kBarVReady = kBarVFull + kStages,
+  kBarVEmpty = kBarVReady + kStages,
+  kBarQFull = kBarVEmpty + kStages,
   kBarQEmpty = kBarQFull + 2,
-  kBarQReady = kBarQEmpty + 2,
-  kBarSFull = kBarQReady + 2,
+  kBarSFull = kBarQEmpty + 2,
   kBarSFree = kBarSFull + 2,
   kBarPFull = kBarSFree + 2,
   kBarPvDone = kBarPFull + 2,
@@ -144,49 +135,15 @@ enum {
   kBarPvFin,
   kNumBars
 };
+// The loader's notes on the last kv tiles (place in the sequence; bits of bad
+// pages, and kPartial), then the TMEM address.  Twice the stages: while a
+// softmax group reads kv tile j's, QK(j + 2) has not been issued, so the loads
+// are at tile j + 1 + kStages at most.
+constexpr int kMeta = 2 * kStages;
 constexpr uint32_t kPartial = 0x100;  // some row does not see some token
-constexpr int kOutBytes = 32 * 128;
-constexpr int kItemWords = 16;
-
-// Shared memory, from a 1024-byte aligned base.
-template <bool kCodes>
-struct Layout {
-  static constexpr int kStages = kCodes ? 3 : kMaxStages;  // kv tiles in flight
-  static constexpr int kOffQ = 0;                          // [2 items][2 row tiles]
-  static constexpr int kOffK = kOffQ + 4 * kRowTileBytes;
-  static constexpr int kOffV = kOffK + kStages * kRowTileBytes;
-  static constexpr int kOffOut = kOffV + kStages * kRowTileBytes;  // [warp][32 rows] of 128 B
-  // [128] (m, l) handed between groups (and the scale of their V)
-  static constexpr int kOffMl = kOffOut + kSoftmaxWarps * kOutBytes;
-  static constexpr int kMlBytes = kCodes ? 16 : 8;
-  static constexpr int kOffItems = kOffMl + 128 * kMlBytes;
-  static constexpr int kOffBars = kOffItems + kItems * kItemWords * 4;
-  // Notes on the last kv tiles: place in the sequence; bits of bad pages, and
-  // kPartial; over codes also what Note says.  Then the TMEM address.  Twice the
-  // stages: while a softmax group reads kv tile j's, QK(j + 2) has not been
-  // issued, so the loads are at tile j + 1 + kStages at most.
-  static constexpr int kMeta = 2 * kStages, kMetaBytes = kCodes ? 64 : 8;
-  static constexpr int kOffMeta = kOffBars + 8 * ((kNumBars + 1) / 2 * 2);
-  static constexpr int kOffTmem = kOffMeta + kMeta * kMetaBytes;
-  static constexpr int kOffUndo = kOffTmem + 16;  // codes: [item][256 rows], see convert_q
-  // codes of the next kv tile, [K|V][row][thread] (each thread's are its own)
-  static constexpr int kOffRaw = kOffUndo + (kCodes ? kItems * 256 : 0);
-  static constexpr int kRawBytes = 16 * 32 * kConvertWarps;
-  static constexpr int kSmem = 1024 + kOffRaw + (kCodes ? 8 * kRawBytes : 0);
-  static_assert(kSmem <= 227 * 1024, "fits one CTA");
-};
-
-// Over codes a kv tile's note goes on with
-//   word 2   V's scale exponent that the tile's P V is in units of (0: no page)
-//   word 3   whether some page's weights take a factor (byte 48 + page)
-//   16       the pages' K scales, as floats
-//   48       octaves that a page's weights are to be divided by
-// V enters the product as f16 code * 2^d with d = its scale - word 2 in [-15, 7],
-// exactly; weights take the rest of scales further down.  Word 2 follows the
-// largest scale of an item's tiles so far, and moves when that is more than 2^7
-// above it.
-constexpr int kVDown = 15, kVUp = 7;
-constexpr float kLift = 6.f;  // f16 weights: the reference maximum's is 2^6
+constexpr int kOffMeta = kOffBars + 8 * kNumBars;
+constexpr int kSmem = 1024 + kOffMeta + 4 * (2 * kMeta + 4);
+static_assert(kSmem <= 227 * 1024, "fits one CTA");
 
 // One item as the roles see it (also its words in shared memory).
 struct Item {
@@ -289,27 +246,6 @@ __device__ __forceinline__ int lds_int(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-// 8 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-
 // True in one lane of the (converged) warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -408,265 +344,9 @@ __device__ __forceinline__ void add_nonfinite(const MaskedArgs& a, const Item& i
   }
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// A converting warp turns its rows of an item's Q (32 w + lane, of each row tile
-// at `q`) into f16 times the power of two that takes the row's largest magnitude
-// to [2^14, 2^15), in place: exact for values down to 2^-31 of it.  `undo` gets
-// the biased exponents of the inverses.
-__device__ __forceinline__ void convert_q(uint32_t q, uint8_t* undo, int row_tiles, int w,
-                                          int lane) {
-#pragma unroll 1
-  for (int t = 0; t < row_tiles; ++t) {
-    const uint32_t row = q + t * kRowTileBytes + (32 * w + lane) * kRow;
-    uint32_t top = 0;  // largest finite magnitude
-#pragma unroll 2
-    for (int j = 0; j < 8; ++j) {
-      const uint4 x = lds128(row + ((j ^ (lane & 7)) << 4));
-      const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        top = __vmaxu2(top, y[i] & 0x7FFF7FFFu & ~nonfinite_halves(y[i]));
-    }
-    top = max(top & 0xFFFFu, top >> 16);
-    const int up = top == 0 ? 0 : min(14 + 127 - static_cast<int>(top >> 7), 60);
-    const float2 f = make_float2(__uint_as_float(static_cast<uint32_t>(up + 127) << 23),
-                                 __uint_as_float(static_cast<uint32_t>(up + 127) << 23));
-    undo[128 * t + 32 * w + lane] = static_cast<uint8_t>(127 - up);
-#pragma unroll 2
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t at = row + ((j ^ (lane & 7)) << 4);
-      const uint4 x = lds128(at);
-      uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 z = fmul2(bf16x2_to_float2(y[i]), f);
-        y[i] = pack_f16x2(z.x, z.y);
-      }
-      sts128(at, y[0], y[1], y[2], y[3]);
-    }
-  }
-}
-
-// Divide the weights of a kv tile's pages (16 columns of f16 pairs' halves: 8
-// words each) by 2^n, n the bytes at `down`.
-__device__ __noinline__ void scale_weights(uint32_t tP, uint32_t down) {
-  tmem_wait_st();
-#pragma unroll 1
-  for (int p = 0; p < kKvPages; ++p) {
-    const uint32_t n = lds8(down + p);
-    if (n == 0u) continue;
-    const uint32_t f = n > 24u ? 0u : n > 14u ? 1u << (24u - n) : (15u - n) << 10;
-    uint32_t y[8];
-    tmem_ld8(tP + 8 * p, y);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      asm volatile("" : "+r"(y[e]));  // (after the wait)
-      y[e] = hmul2(y[e], f * 0x10001u);
-    }
-    tmem_st8(tP + 8 * p, y);
-  }
-}
-
-// One of the converting warps: it takes rows [32 w, 32 w + 32) (two pages) of the
-// K and V of every kv tile of the CTA's items, lane 4 r + c the 16 codes c of rows
-// r, r + 8, r + 16 and r + 24, copies them a tile ahead, straight from the pool
-// into its own places in shared memory, and stores them as f16 where the TMA boxes
-// would have put them (128-byte swizzled); and its rows of Q.  False: a wait ran
-// out.
-template <int kFmt>
-__device__ __forceinline__ bool convert_tiles(const MaskedArgs& a, uint8_t* smem, int w,
-                                              int lane) {
-  using L = Layout<true>;
-  constexpr int kStages = L::kStages;
-  const uint32_t sb = smem_addr(smem);
-  auto bar = [&](int i) { return sb + L::kOffBars + 8u * i; };
-  auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
-  // A tile of the walk, its entries of the block table in lanes 8 i + page.
-  struct Tile {
-    int tile, g, end, lo, ids;  // tile -1: no more
-    int row_tiles;              // of an item's first tile: Q's, else 0
-    bool part;
-  };
-  const int r = lane >> 2, c = lane & 3;
-  Item it = {};
-  int item = 0, k = 0;
-  // The next tile, its table entries on their way; false: a wait ran out.
-  auto next = [&](Tile& x) {
-    x.row_tiles = 0;
-    while (k >= it.t1) {
-      const int slot = item % kItems;
-      if (!wait(kBarItemFull + slot, item / kItems)) return false;
-      it = read_item(sb + L::kOffItems + 4u * kItemWords * slot);
-      __syncwarp();
-      if (it.b < 0) {
-        it.t1 = k;  // (asked again, the same answer)
-        x.tile = -1;
-        return true;
-      }
-      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
-      ++item;
-      k = it.t0;
-      x.row_tiles = it.halves() ? 1 : 2;
-    }
-    x.tile = it.tile(k++);
-    x.g = it.g;
-    x.end = it.end();
-    x.lo = it.lo;
-    x.part = it.partial(x.tile, a);
-    const int page = x.tile * kKvPages + (lane & 7);
-    x.ids = -1;
-    if (page * kPageSize < x.end)
-      x.ids = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + page];
-    return true;
-  };
-  // Its page ids: -1 where bad, -2 where no row sees the page.
-  auto settle = [&](Tile& x) {
-    const int t = (x.tile * kKvPages + (lane & 7)) * kPageSize;
-    if (!(t < x.end && (t + kPageSize > x.lo || t < a.sinks))) {
-      x.ids = -2;
-    } else if (x.ids < 0 || x.ids >= a.num_pages) {
-      if (w == 0 && lane < 8) record_error(a.dev_err, kErrPage);
-      x.ids = -1;
-    }
-  };
-  // The pages' scales: lanes 8 kv + page.
-  auto load_scale = [&](const Tile& x) {
-    return lane < 16 && x.ids >= 0
-               ? static_cast<uint32_t>(a.scales[scale_at(x.ids, lane >> 3, x.g)])
-               : 0u;
-  };
-  const uint32_t raw = sb + L::kOffRaw + 16 * (32 * w + lane);
-  // Row i of this lane: 32 w + 8 i + r, of page 2 w + i / 2.  A copy group per
-  // call, empty where there is no tile.
-  auto load = [&](const Tile& x, int kv) {
-    if (x.tile >= 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pid = __shfl_sync(kFull, x.ids, 2 * w + (i >> 1));
-        // (V of tokens that no row sees: zeros, whatever their codes)
-        const int t = x.tile * kKvTokens + 32 * w + 8 * i + r;
-        const bool in = pid >= 0 && (kv == 0 || (t < x.end && (t >= x.lo || t < a.sinks)));
-        const uint8_t* src =
-            a.codes + (in ? block_at(pid, kv, x.g) + (8 * (i & 1) + r) * kHeadDim + 16 * c : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         raw + (4 * kv + i) * L::kRawBytes),
-                     "l"(src), "r"(in ? 16 : 0)
-                     : "memory");
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  // (the last group is the other one of K's and V's)
-  auto store = [&](uint32_t dst, int kv, uint32_t f0, uint32_t f1) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t f = i < 2 ? f0 : f1;
-      const uint32_t row = dst + (32 * w + 8 * i + r) * kRow;
-      const uint4 x = lds128(raw + (4 * kv + i) * L::kRawBytes);
-      uint32_t y[8];
-      decode_f16<kFmt>(x.x, y[0], y[1]);
-      decode_f16<kFmt>(x.y, y[2], y[3]);
-      decode_f16<kFmt>(x.z, y[4], y[5]);
-      decode_f16<kFmt>(x.w, y[6], y[7]);
-      if (f != 0x3C003C00u) {  // 1.0 twice
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = hmul2(y[e], f);
-      }
-      sts128(row + (((2 * c) ^ r) << 4), y[0], y[1], y[2], y[3]);
-      sts128(row + (((2 * c + 1) ^ r) << 4), y[4], y[5], y[6], y[7]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-  };
-  // x: the tile whose codes are being copied; y: the one after it
-  Tile x, y;
-  uint32_t scale = 0, unit = 0;  // this lane's page's; the item's V is in units of
-  int qn = 0;
-  if (!next(x)) return false;
-  y.tile = -1;
-  if (x.tile >= 0) {
-    if (!next(y)) return false;
-    settle(x);
-    scale = load_scale(x);
-    load(x, 0);
-    load(x, 1);
-  }
-  for (int kt = 0; x.tile >= 0; ++kt) {
-    const int st = kt % kStages;
-    if (x.row_tiles > 0) {
-      const int qb = qn & 1;
-      if (!wait(kBarQFull + qb, qn >> 1)) return false;
-      // (x's item is the last read, or the one before when y begins another)
-      const int slot = (y.tile >= 0 && y.row_tiles > 0 ? item - 2 : item - 1) % kItems;
-      convert_q(sb + L::kOffQ + 2 * qb * kRowTileBytes, smem + L::kOffUndo + 256 * slot,
-                x.row_tiles, w, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarQReady + qb));
-      ++qn;
-      unit = 0;
-    }
-    if (kt >= kStages && !wait(kBarKEmpty + st, kt / kStages - 1)) return false;
-    const uint32_t e = x.ids >= 0 && lane < 16 ? stored_scale(scale) : 0u;
-    const uint32_t most = __reduce_max_sync(kFull, lane >= 8 ? e : 0u);
-    if (most > 0 && (unit == 0 || most > unit + kVUp)) unit = most;
-    const int d = static_cast<int>(e) - static_cast<int>(unit);
-    const int dv = max(d, -kVDown);
-    const uint32_t f = dv == -kVDown ? 0x0200u : static_cast<uint32_t>(dv + 15) << 10;
-    if (w == 0) {
-      uint8_t* note = smem + L::kOffMeta + L::kMetaBytes * (kt % L::kMeta);
-      const unsigned bad = __ballot_sync(kFull, x.ids == -1) & 0xFFu;
-      const unsigned ext = __ballot_sync(kFull, lane >= 8 && e > 0 && d < dv);
-      if (lane < 8) {
-        // (2^-60 or more, as what undoes Q's power of two: times each other and an
-        // unseen token's -inf they stay -inf; what this adds to smaller scales'
-        // scores is far below 1)
-        reinterpret_cast<float*>(note + 16)[lane] =
-            e > 0 ? scale_value(max(e, static_cast<uint32_t>(kScaleBias - 60))) : 1.f;
-      } else if (lane < 16) {
-        note[40 + lane] = static_cast<uint8_t>(e > 0 ? dv - d : 0);
-      }
-      if (lane == 0)
-        *reinterpret_cast<uint4*>(note) =
-            make_uint4(x.tile, bad | (x.part ? kPartial : 0u), unit, ext);
-    }
-    const uint32_t f0 = __shfl_sync(kFull, f, 8 + 2 * w) * 0x10001u;
-    const uint32_t f1 = __shfl_sync(kFull, f, 9 + 2 * w) * 0x10001u;
-    store(sb + L::kOffK + st * kRowTileBytes, 0, 0x3C003C00u, 0x3C003C00u);
-    if (lane == 0) mbar_arrive(bar(kBarKFull + st));
-    x = y;
-    if (x.tile >= 0) {
-      settle(x);
-      scale = load_scale(x);
-    }
-    load(x, 0);
-    if (x.tile >= 0 && !next(y)) return false;
-    if (kt >= kStages && !wait(kBarVEmpty + st, kt / kStages - 1)) return false;
-    store(sb + L::kOffV + st * kRowTileBytes, 1, f0, f1);
-    if (lane == 0) mbar_arrive(bar(kBarVReady + st));
-    load(x, 1);
-  }
-  return true;
-}
-
-template <int kFmt>
-__global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk_kernel(
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(
     const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap page_map,
     const MaskedArgs a) {
-  constexpr bool kCodes = kFmt != kBf16;
-  using R = Roles<kCodes>;
-  using Lay = Layout<kCodes>;
-  constexpr int kStages = Lay::kStages, kMeta = Lay::kMeta;
-  constexpr int kOffQ = Lay::kOffQ, kOffK = Lay::kOffK, kOffV = Lay::kOffV;
-  constexpr int kOffOut = Lay::kOffOut, kOffMl = Lay::kOffMl, kOffItems = Lay::kOffItems;
-  constexpr int kOffBars = Lay::kOffBars, kOffMeta = Lay::kOffMeta;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -675,6 +355,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
   auto wait = [&](int i, int phase) { return warp_wait(bar(i), phase, a.wait_ns); };
   int* s_items = reinterpret_cast<int*>(smem + kOffItems);
   auto item_addr = [&](int slot) { return sb + kOffItems + 4u * kItemWords * slot; };
+  // [kMeta][2], then the TMEM address
   uint32_t* s_meta = reinterpret_cast<uint32_t*>(smem + kOffMeta);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -686,11 +367,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
       if (i >= kBarSFree && i < kBarPvDone) n = 4;               // s_free, p_full
-      if (i >= kBarItemEmpty && i < kBarXFull)
-        n = kSoftmaxWarps + (kCodes ? 3 + kConvertWarps : 4);
-      if (kCodes && ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVReady && i < kBarVEmpty)))
-        n = kConvertWarps;
-      if (i >= kBarQReady && i < kBarSFull) n = kConvertWarps;
+      if (i >= kBarItemEmpty && i < kBarXFull) n = kSoftmaxWarps + 4;
       if (i == kBarXFull || i == kBarXFree) n = 4;
       mbar_init(bar(i), n);
     }
@@ -698,26 +375,19 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
   }
   if (warp == kQkWarp) {
     __syncwarp();
-    tmem_alloc(sb + Lay::kOffTmem, kTmemCols);
+    tmem_alloc(sb + kOffMeta + 8 * kMeta, kTmemCols);
     tmem_relinquish_alloc_permit();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + Lay::kOffTmem);
+  const uint32_t tmem = s_meta[2 * kMeta];
   wait_for_prior_grids();
   allow_dependent_grids();
 
   bool ok = true;
-  if (kCodes && warp >= kConvertWarp) {
-    if constexpr (kCodes) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kConvertRegs));
-      // ---------------------------------------------- K and V from codes
-      ok = convert_tiles<kFmt>(a, smem, warp - kConvertWarp, lane);
-      asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
-    }
-  } else if (warp >= kQkWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
+  if (warp >= kQkWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSchedWarp) {
       // --------------------------------------------- scheduler, V's relay
       // Items in order (tile, range, head); the tiles of a sequence from its
@@ -753,6 +423,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
             } else {
               // (shorter chunks are the other kernel's)
               cnt = o1 - o0 > kShortTokens ? (o1 - o0 + kQTokens - 1) / kQTokens : 0;
+              if (a.rounds != nullptr && a.rounds[b] != a.round) cnt = 0;
             }
           }
           incl = cnt;
@@ -830,9 +501,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         return true;
        }
       };
-      if constexpr (kCodes) {  // (V is whole when the converting warps hand it over)
-        while (ok && more) ok = publish();
-      } else for (int i = 0; ok; ++i) {
+      for (int i = 0; ok; ++i) {
         while (ok && more && out_i <= i + kAhead) ok = publish();
         const int slot = i % kItems;
         if (!ok || !wait(kBarItemFull + slot, i / kItems)) {
@@ -919,7 +588,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       };
       Item it, nx;
       ok = fetch(0, it);
-      int ids = !kCodes && ok && it.b >= 0 ? load_ids(it, it.t0) : 0;
+      int ids = ok && it.b >= 0 ? load_ids(it, it.t0) : 0;
       for (int i = 0; ok && it.b >= 0; ++i) {
         const int qb = qn & 1;
         if (qn >= 2 && !(ok = wait(kBarQEmpty + qb, qn / 2 - 1))) break;
@@ -934,10 +603,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         }
         __syncwarp();
         ++qn;
-        if constexpr (kCodes) {  // K and V are the converting warps'
-          if (!(ok = fetch(i + 1, nx))) break;
-        }
-        for (int k0 = it.t0; !kCodes && ok && k0 < it.t1; k0 += 4) {
+        for (int k0 = it.t0; ok && k0 < it.t1; k0 += 4) {
           int ids_next = 0;
           if (k0 + 4 < it.t1) {
             ids_next = load_ids(it, k0 + 4);
@@ -1006,7 +672,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         const int U = x.y;
         const bool one = x.w != 0;
         if (U == 0) break;
-        if (!(ok = wait((kCodes ? kBarQReady : kBarQFull) + qb, i >> 1))) break;
+        if (!(ok = wait(kBarQFull + qb, i >> 1))) break;
         const uint32_t q0 = desc_lo(sb + kOffQ + 2 * qb * kRowTileBytes);
         for (int u = 0; u < U; ++u, ++n) {
           const int w = n & 1, st = kt % kStages;
@@ -1019,7 +685,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           if (issuer) {
 #pragma unroll
             for (int kk = 0; kk < kHeadDim / 16; ++kk)
-              mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, Idesc<kCodes>::kQK, kk > 0);
+              mma_ss(tmem + 128 * w, q + 2 * kk, kr + 2 * kk, kIdescQK, kk > 0);
             tc_commit(bar(kBarSFull + w));
             if (last) tc_commit(bar(kBarKEmpty + st));
             if (u == U - 1) tc_commit(bar(kBarQEmpty + qb));
@@ -1054,10 +720,10 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           const uint32_t vr = desc_lo(sb + kOffV) + st * (kRowTileBytes >> 4);
           if (issuer) {
             const uint32_t d = tmem + kTmemO + kHeadDim * w, pa = tmem + kTmemP + 64 * w;
-            mma_ts(d, pa, vr, Idesc<kCodes>::kPV, u >= 2);  // a group's first unit of the item starts O
+            mma_ts(d, pa, vr, kIdescPV, u >= 2);  // a group's first unit of the item starts O
 #pragma unroll
             for (int p = 1; p < kKvPages; ++p)
-              mma_ts(d, pa + 8 * p, vr + p * (kPageBytes >> 4), Idesc<kCodes>::kPV, true);
+              mma_ts(d, pa + 8 * p, vr + p * (kPageBytes >> 4), kIdescPV, true);
             tc_commit(bar(kBarPvDone + w));
             if (last) tc_commit(bar(kBarVEmpty + st));
           }
@@ -1072,7 +738,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // --------------------------------------------------- softmax, epilogue
     const int w = warp >> 2;
     const int row = tid & 127;                 // MMA row = TMEM lane
@@ -1097,8 +763,6 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
         first = one && w != it.first_w ? 1 : 0;
       }
       float m_ref = -INFINITY, l_run = 0.f;
-      uint32_t unit = 0;  // codes: O is in units of 2^(unit - 127)
-      float c_row = c;    // codes: undoes the power of two of Q's row
       for (int v = 0; v < nu; ++v, ++units) {
         if (!(ok = wait(kBarSFull + w, units))) break;
         tc_fence_after_sync();
@@ -1113,18 +777,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           return true;
         };
         // (written before the loads that QK waited for)
-        const uint32_t note_at =
-            sb + kOffMeta + Lay::kMetaBytes * ((kt0 + first + (one ? 2 * v : v)) % kMeta);
-        uint4 note = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (kCodes) {
-          note = lds128(note_at);
-          if (v == 0)
-            c_row *= scale_value(lds8(sb + Lay::kOffUndo + 256 * slot + row + (one ? 0 : 128 * w)));
-        } else {
-          const uint2 n = lds64(note_at);
-          note.x = n.x;
-          note.y = n.y;
-        }
+        const uint2 note = lds64(sb + kOffMeta + 8u * ((kt0 + first + (one ? 2 * v : v)) % kMeta));
         if (idle) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarSFree + w));
@@ -1164,48 +817,24 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
           // of, and moves only when a tile's weights sum to 2^kRescale or more
           // (FP32 sums and bf16 weights keep their relative precision below).
           bool measure = __any_sync(kFull, m_ref == -INFINITY);
-          // (what is rare about codes is dealt with on the measuring path too)
-          if constexpr (kCodes) measure |= note.z != unit || note.w != 0u;
           if (!(ok = o_ready())) break;
           tc_fence_after_sync();
           for (;;) {
             float alpha = 1.f;
             if (measure) {
-              float o_unit = 1.f;  // O in the tile's units of V
-              if constexpr (kCodes) {
-                if (note.z != unit && note.z != 0u) {
-                  if (unit != 0u)
-                    o_unit = note.z - unit > 126u ? 0.f : scale_value(127 + unit - note.z);
-                  unit = note.z;
-                }
-              }
               float mx[2] = {-INFINITY, -INFINITY};
-              if constexpr (kCodes) {
-                float best = -INFINITY;  // of the pages, each with its scale
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  float y = -INFINITY;
+              for (int q = 0; q < 4; ++q)
 #pragma unroll
-                  for (int e = 0; e < 16; e += 2)
-                    y = fmax3(y, __uint_as_float(x[q >> 1][16 * (q & 1) + e]),
-                              __uint_as_float(x[q >> 1][16 * (q & 1) + e + 1]));
-                  best = fmaxf(best, y * (c_row * __uint_as_float(lds32(note_at + 16 + 4 * q))));
-                }
-                mx[0] = best - kLift;
-              } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                  for (int e = 0; e < 32; e += 2)
-                    mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[q][e]),
-                                             __uint_as_float(x[q][e + 1]));
-              }
-              const float top = kCodes ? fmaxf(mx[0], mx[1]) : fmaxf(mx[0], mx[1]) * c;
+                for (int e = 0; e < 32; e += 2)
+                  mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[q][e]),
+                                           __uint_as_float(x[q][e + 1]));
+              const float top = fmaxf(mx[0], mx[1]) * c;
               if (top > m_ref) {
                 alpha = fast_exp2(m_ref - top);  // 0 on the first live tile
                 m_ref = top;
               }
-              if (v > 0 && __any_sync(kFull, alpha != 1.f || o_unit != 1.f)) {
+              if (v > 0 && __any_sync(kFull, alpha != 1.f)) {
                 l_run *= alpha;
 #pragma unroll 1
                 for (int q = 0; q < kHeadDim / 16; ++q) {
@@ -1215,7 +844,7 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
                   reg_after_wait(o);
 #pragma unroll
                   for (int e = 0; e < 16; ++e)
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha * o_unit));
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                   tmem_st16(tO + 16 * q, o);
                 }
               }
@@ -1227,42 +856,27 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t pw[32];
-              uint4 k_scales = make_uint4(0u, 0u, 0u, 0u);  // of the pages of this half
-              if constexpr (kCodes) k_scales = lds128(note_at + 16 + 16 * q);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const uint32_t* s2 = &x[2 * q + (e >> 4)][2 * (e & 15)];
-                float2 cp = c2;
-                if constexpr (kCodes) {
-                  const uint32_t k = e < 8    ? k_scales.x
-                                     : e < 16 ? k_scales.y
-                                     : e < 24 ? k_scales.z
-                                              : k_scales.w;
-                  cp.x = cp.y = c_row * __uint_as_float(k);
-                }
                 float2 y = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])),
-                                 cp, m2);
+                                 c2, m2);
                 y.x = fast_exp2(y.x);
                 y.y = fast_exp2(y.y);
                 ls[e & 1] = fadd2(ls[e & 1], y);
-                pw[e] = kCodes ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
+                pw[e] = pack_bf16x2(y.x, y.y);
               }
               tmem_st32(tP + 32 * q, pw);
             }
             const float2 l2 = fadd2(ls[0], ls[1]);
             const float sum = l2.x + l2.y;
             // (NaN too; a tile that has just been measured stands as it is)
-            const bool over = !(sum < (kCodes ? kRescaleF16 : kRescale));
-            if (!measure && __any_sync(kFull, over)) {
-              measure = true;
-              continue;
+            const bool over = !(sum < kRescale);
+            if (measure || !__any_sync(kFull, over)) {
+              l_run += sum;
+              break;
             }
-            l_run += sum;
-            if constexpr (kCodes) {
-              // weights of pages whose V scales are far below the unit
-              if (measure && note.w != 0u) scale_weights(tP, note_at + 48);
-            }
-            break;
+            measure = true;
           }
           tmem_wait_st();
         }
@@ -1281,15 +895,12 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       tc_fence_after_sync();
       bool writes = tok < it.nt;
       const bool other = one && it.units_of(1) > 0;  // both groups saw these rows
-      float* xml = reinterpret_cast<float*>(smem + kOffMl + Lay::kMlBytes * row);
-      const float v_unit = kCodes && unit != 0u ? scale_value(unit) : 1.f;
+      float2* xml = reinterpret_cast<float2*>(smem + kOffMl) + row;
       if (one && w == 1) {
         // the first group takes this one's rows from TMEM (the same lanes)
         writes = false;
         if (other) {
-          xml[0] = m_ref;
-          xml[1] = l_run;
-          if constexpr (kCodes) xml[2] = v_unit;
+          *xml = make_float2(m_ref, l_run);
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarXFull));
@@ -1300,20 +911,17 @@ __global__ void __launch_bounds__(Roles<kFmt != kBf16>::kThreads, 1) paged_chunk
       if (other && w == 0) {
         if (!(ok = wait(kBarXFull, xn))) break;
         tc_fence_after_sync();
-        const float2 ml = make_float2(xml[0], xml[1]);
+        const float2 ml = *xml;
         const float M = fmaxf(m_ref, ml.x);
         // (a group whose tiles the row did not see: zeros)
         w0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - M);
         w1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
         l_run = l_run * w0 + ml.y * w1;
         m_ref = M;
-        if constexpr (kCodes) w1 *= xml[2];
       }
-      if constexpr (kCodes) w0 *= v_unit;
       // (written before the last kv tile's V was handed to its PV, which this
       // row's group, or the other one, has waited for)
-      const int bad_v =
-          kCodes ? 0 : *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
+      const int bad_v = *reinterpret_cast<volatile int*>(s_items + slot * kItemWords + 12);
       if (!(one && w == 1) && !idle) {
         const int tok0 = ((row & ~31) >> 2) + (one ? 0 : kHalfTokens * w);  // the warp's first
         const int64_t r0 = static_cast<int64_t>(it.row0 + tok0) * kNumQHeads + it.g * kGroup;
@@ -1430,41 +1038,31 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_chunk_kernel(const Mask
   reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = merge_ranges(ml, acc, splits, lane);
 }
 
-template <int kFmt>
-cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& page_map, const MaskedArgs& args,
-                   int grid, cudaStream_t stream) {
-  using R = Roles<kFmt != kBf16>;
-  using L = Layout<kFmt != kBf16>;
-  int device = 0;
-  cudaError_t err = cudaGetDevice(&device);
-  if (err != cudaSuccess) return err;
+cudaError_t configure(int device) {
   static std::atomic<unsigned long long> done{0};
   const unsigned long long bit = 1ull << (device & 63);
-  if (!(done.load(std::memory_order_acquire) & bit)) {
-    cudaFuncAttributes fa;
-    if ((err = cudaFuncGetAttributes(&fa, paged_chunk_kernel<kFmt>)) != cudaSuccess) return err;
-    // the register split must stay within what the block starts with
-    if (fa.numRegs != R::kLaunchRegs) return cudaErrorInvalidConfiguration;
-    err = cudaFuncSetAttribute(paged_chunk_kernel<kFmt>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-    if (err != cudaSuccess) return err;
-    done.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  return launch_pdl(paged_chunk_kernel<kFmt>, dim3(grid), dim3(R::kThreads), L::kSmem, stream,
-                    q_map, page_map, args);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes fa;
+  cudaError_t err = cudaFuncGetAttributes(&fa, paged_chunk_kernel);
+  if (err != cudaSuccess) return err;
+  // the register split must stay within what the block starts with
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  err = cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return err;
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& page_map,
                                    const MaskedArgs& args, int grid, cudaStream_t stream) {
-  return launch<kBf16>(q_map, page_map, args, grid, stream);
-}
-
-cudaError_t launch_chunk8_attention(const CUtensorMap& q_map, const MaskedArgs& args, int format,
-                                    int grid, cudaStream_t stream) {
-  return format == kKv8E4m3 ? launch<kKv8E4m3>(q_map, q_map, args, grid, stream)
-                            : launch<kKv8Int8>(q_map, q_map, args, grid, stream);
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  if ((err = configure(device)) != cudaSuccess) return err;
+  return launch_pdl(paged_chunk_kernel, dim3(grid), dim3(kThreads), kSmem, stream, q_map, page_map,
+                    args);
 }
 
 cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream) {

@@ -422,19 +422,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (!in[s]) continue;
-        const uint32_t x[4] = {w[kv][s].x, w[kv][s].y, w[kv][s].z, w[kv][s].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 y = decode4<kFmt>(x[i]);
-          o[2 * i] = pack_bf16x2(y.x * f, y.y * f);
-          o[2 * i + 1] = pack_bf16x2(y.z * f, y.w * f);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(
-            (kv == 0 ? k : v) + (t.row0 + r + 8 * s) * (kNumKvHeads * kHeadDim) + h * kHeadDim +
-            16 * q);
-        __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-        __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+        widen16<kFmt>(w[kv][s], f,
+                      reinterpret_cast<uint4*>((kv == 0 ? k : v) +
+                                               (t.row0 + r + 8 * s) * (kNumKvHeads * kHeadDim) +
+                                               h * kHeadDim + 16 * q));
       }
     }
   }

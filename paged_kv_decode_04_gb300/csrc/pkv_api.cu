@@ -1412,8 +1412,8 @@ pkv::Kv8 kv8_of(const void* pool, const uint8_t* scales, int format, int64_t num
   return c;
 }
 
-// TMA descriptor of the 8-bit pool viewed as [num_pages][256 rows (K|V x kv head
-// x slot)][64] bytes, 64-byte swizzled, with boxes of one page.  Cached per thread
+// TMA descriptor of the 8-bit pool viewed as [num_pages][256 rows (K|V x kv head x
+// slot)][64] bytes, 64-byte swizzled, with boxes of one page.  Cached per thread
 // for the last (device, pool, pages).
 bool pool8_map(const void* pool, int64_t num_pages, CUtensorMap* out) {
   struct Entry {
@@ -1433,8 +1433,8 @@ bool pool8_map(const void* pool, int64_t num_pages, CUtensorMap* out) {
                                 static_cast<cuuint64_t>(num_pages)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim),
                                    static_cast<cuuint64_t>(kRows * kHeadDim)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim),
-                               static_cast<cuuint32_t>(kRows), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim), static_cast<cuuint32_t>(kRows),
+                               1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUtensorMap m;
     if (enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
@@ -1465,24 +1465,58 @@ int decode8_splits(int batch, int max_blocks, int window, int sinks, int num_spl
                         num_splits);
 }
 
-// chunk_plan with short chunks of one CTA for all kv heads.
+// A chunk call over the 8-bit cache: chunk_plan with short chunks of one CTA for
+// all kv heads, and the bf16 pages of the long ones (kv8_widen.cu).  Their places
+// take the most that the sizes allow (the lengths are on the device), or kPlaces,
+// 2 GiB, or twice the most of one sequence; then the long chunks take several rounds, of
+// `per_round` pages and what the last sequence has above them.
+struct Chunk8Plan {
+  ChunkPlan chunk;
+  int rounds;
+  int64_t places, per_round;
+  size_t table_at, pages_at, workspace;  // bytes; the rounds' array lies before the table
+};
+
 bool chunk8_plan(int num_tokens, int batch, int max_blocks, int window, int sinks, int num_splits,
-                 ChunkPlan* plan) {
-  if (!chunk_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, plan)) return false;
-  const long long wide = static_cast<long long>(window) + pkv::kShortTokens - 1;
-  const long long pages =
-      window > 0 ? window_pages(max_blocks, static_cast<int>(std::min<long long>(wide, INT32_MAX)),
-                                sinks)
-                 : max_blocks;
+                 Chunk8Plan* plan) {
+  ChunkPlan& c = plan->chunk;
+  if (!chunk_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &c)) return false;
+  auto pages_of = [&](int tokens) -> long long {
+    if (window == 0) return max_blocks;
+    const long long wide = static_cast<long long>(window) + tokens - 1;
+    return window_pages(max_blocks, static_cast<int>(std::min<long long>(wide, INT32_MAX)), sinks);
+  };
   // (more tokens than short chunks can have mean a long one, or a padded q)
   const bool a_long_one = num_tokens > pkv::kShortTokens * static_cast<long long>(batch);
-  const int splits = stream8_splits(a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens),
-                                    pages, num_splits);
+  const int splits =
+      stream8_splits(a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens),
+                     pages_of(pkv::kShortTokens), num_splits);
   if (splits < 1) return false;
-  plan->short_splits = splits;
-  plan->short_parts = splits > 1 ? static_cast<size_t>(batch) * pkv::kShortTokens * kNumQHeads * splits
-                                 : 0;
-  plan->workspace = (plan->long_parts + plan->short_parts) * (kHeadDim + 2) * sizeof(float);
+  c.short_splits = splits;
+  c.short_parts = splits > 1 ? static_cast<size_t>(batch) * pkv::kShortTokens * kNumQHeads * splits
+                             : 0;
+  c.workspace = (c.long_parts + c.short_parts) * (kHeadDim + 2) * sizeof(float);
+  plan->rounds = 0;
+  plan->places = plan->per_round = 0;
+  plan->table_at = plan->pages_at = plan->workspace = c.workspace;
+  if (c.grid == 0) return true;
+  constexpr long long kPlaces = 65536;
+  const long long chunks = std::min(batch, num_tokens / (pkv::kShortTokens + 1));
+  const long long most = pages_of(num_tokens);
+  plan->places = chunks * most;
+  plan->per_round = INT64_MAX;
+  plan->rounds = 1;
+  if (plan->places > std::max(kPlaces, 2 * most)) {
+    plan->places = std::max(kPlaces, 2 * most);
+    plan->per_round = plan->places - most;
+    plan->rounds = static_cast<int>((chunks * most + plan->per_round - 1) / plan->per_round);
+  }
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  plan->table_at = up(c.workspace) + up(static_cast<size_t>(batch) * sizeof(int32_t));
+  plan->pages_at =
+      plan->table_at + up(static_cast<size_t>(batch) * max_blocks * sizeof(int32_t));
+  plan->workspace = plan->pages_at + static_cast<size_t>(plan->places) * 2 * kPageSize *
+                                         kNumKvHeads * kHeadDim * sizeof(pkv_bf16);
   return true;
 }
 
@@ -1610,7 +1644,7 @@ PKV_API size_t pkv_chunk8_workspace_bytes(int num_tokens, int batch, int num_q_h
       num_splits < 0 || !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
   if (num_tokens == 0 || batch == 0) return 0;
-  ChunkPlan plan;
+  Chunk8Plan plan;
   if (!chunk8_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
     return static_cast<size_t>(-1);
   return plan.workspace;
@@ -1645,7 +1679,6 @@ PKV_API int pkv_paged8_decode_attention(
   if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
-  a.codes = static_cast<const uint8_t*>(pool);
   a.scales = scales;
   a.block_table = block_table;
   a.seq_lens = seq_lens;
@@ -1695,7 +1728,7 @@ PKV_API int pkv_paged8_chunk_attention(
   const Span outs[] = {heads_span(out, num_tokens), ints(dev_err, 1)};
   if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0 || num_tokens == 0) return PKV_OK;
-  ChunkPlan plan;
+  Chunk8Plan plan;
   if (!chunk8_plan(num_tokens, batch, max_blocks, window, sinks, num_splits, &plan))
     return PKV_ECUDA;
   if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
@@ -1703,7 +1736,6 @@ PKV_API int pkv_paged8_chunk_attention(
   if (workspace_overlaps({workspace, plan.workspace}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
-  a.codes = static_cast<const uint8_t*>(pool);
   a.scales = scales;
   a.block_table = block_table;
   a.seq_lens = seq_lens;
@@ -1716,19 +1748,53 @@ PKV_API int pkv_paged8_chunk_attention(
   a.num_tokens = num_tokens;
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
-  set_parts(a, plan, workspace);
+  set_parts(a, plan.chunk, workspace);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
-  CUtensorMap q_map, page_map;
-  if (!chunk_q_map(q, num_tokens, &q_map) || !pool8_map(pool, num_pages, &page_map))
-    return PKV_ECUDA;
-  const int fmt = format == PKV_KV8_E4M3 ? pkv::kKv8E4m3 : pkv::kKv8Int8;
+  CUtensorMap codes_map;
+  if (!pool8_map(pool, num_pages, &codes_map)) return PKV_ECUDA;
+  const pkv::Kv8 cache = kv8_of(pool, scales, format, num_pages, block_table, max_blocks, batch);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;
-  if (plan.grid > 0) err = pkv::launch_chunk8_attention(q_map, a, fmt, plan.grid, st);
-  if (err == cudaSuccess) err = pkv::launch_short_chunks8(page_map, a, fmt, plan.grid > 0, st);
+  if (plan.rounds > 0) {
+    char* ws = static_cast<char*>(workspace);
+    pkv::WidenArgs w = {};
+    w.cache = cache;
+    w.seq_lens = seq_lens;
+    w.token_offsets = token_offsets;
+    w.num_tokens = num_tokens;
+    w.window = a.window;
+    w.sinks = sinks;
+    w.table = reinterpret_cast<int32_t*>(ws + plan.table_at);
+    if (plan.rounds > 1)
+      w.rounds = w.table - (static_cast<size_t>(batch) * sizeof(int32_t) + 255) / 256 * 64;
+    w.pages = reinterpret_cast<pkv_bf16*>(ws + plan.pages_at);
+    w.dev_err = dev_err;
+    w.places = plan.places;
+    w.per_round = plan.per_round;
+    w.num_rounds = plan.rounds;
+    pkv::MaskedArgs l = a;
+    l.pool = w.pages;
+    l.num_pages = plan.places;
+    l.block_table = w.table;
+    l.rounds = w.rounds;
+    CUtensorMap q_map, page_map;
+    const int sms = current_sm_count();
+    if (sms <= 0 || !chunk_q_map(q, num_tokens, &q_map) ||
+        !pool_tensor_map(w.pages, plan.places, &page_map, kPageSize))
+      return PKV_ECUDA;
+    for (int r = 0; err == cudaSuccess && r < plan.rounds; ++r) {
+      w.round = l.round = r;
+      err = pkv::launch_widen(w, sms, st);
+      if (err == cudaSuccess)
+        err = pkv::launch_chunk_attention(q_map, page_map, l, plan.chunk.grid, st);
+    }
+  }
+  if (err == cudaSuccess)
+    err = pkv::launch_short_chunks8(codes_map, a, cache.format, plan.rounds > 0, st);
   if (err == cudaSuccess) err = pkv::launch_short_merge(a, st);
-  if (err == cudaSuccess && plan.grid > 0 && a.num_splits > 1) err = pkv::launch_chunk_merge(a, st);
+  if (err == cudaSuccess && plan.rounds > 0 && a.num_splits > 1)
+    err = pkv::launch_chunk_merge(a, st);
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -255,9 +255,8 @@ cudaError_t launch_shared_prefix_attention(const CUtensorMap& pool_map, const At
 // or t < sinks); window is at least 1 (INT32_MAX: no window).
 struct MaskedArgs {
   const uint16_t* q;
-  const uint16_t* pool;          // a bf16 cache, or
-  const uint8_t* codes;          // an 8-bit one
-  const uint8_t* scales;         // and its scales (16-byte aligned, as the codes)
+  const uint16_t* pool;          // a bf16 cache
+  const uint8_t* scales;         // of an 8-bit cache, 16-byte aligned
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* token_offsets;  // chunks only: [batch + 1]
@@ -278,6 +277,8 @@ struct MaskedArgs {
   int short_splits;              // chunks: ranges of chunks of at most kShortTokens
   float* short_acc;              // partials of the short chunks, [batch][kShortTokens * 32 rows]
   float* short_ml;               // [short_splits]
+  const int32_t* rounds;         // long chunks: only sequences of this round, or nullptr
+  int round;
   float scale_log2;              // softmax scale * log2(e)
   unsigned long long wait_ns;
 };
@@ -360,15 +361,30 @@ cudaError_t launch_kv8_read(uint16_t* k, uint16_t* v, int num_tokens,
                             const int32_t* token_offsets, const int32_t* start_positions,
                             const Kv8& cache, int num_sms, int32_t* dev_err, cudaStream_t stream);
 
-// Attention over the 8-bit cache (args.codes and scales): of one token a
-// sequence, and the merge of its ranges; of chunks of more than kShortTokens
-// tokens (chunk_attention.cu); of the other chunks, with launch_short_merge, where
-// beside: right after launch_chunk8_attention (kv8_attention.cu).
-// page_map: boxes of one page's codes, 64-byte swizzled.
+// The pages that the chunks of more than kShortTokens tokens see, as bf16 pages in
+// a workspace (kv8_widen.cu), for launch_chunk_attention: round r takes the
+// sequences whose pages, counted on through the batch, begin in [r per_round, (r +
+// 1) per_round).
+struct WidenArgs {
+  Kv8 cache;
+  const int32_t* seq_lens;
+  const int32_t* token_offsets;
+  int num_tokens, window, sinks;
+  int32_t* rounds;      // [batch] written, the round of each sequence; nullptr: one round
+  int32_t* table;       // [batch][max_blocks] written: a seen page's place, or -1
+  uint16_t* pages;      // [places][K|V][16][8][64] written
+  int32_t* dev_err;
+  int64_t places, per_round;
+  int round, num_rounds;
+};
+cudaError_t launch_widen(const WidenArgs& args, int num_sms, cudaStream_t stream);
+
+// Attention over the 8-bit cache (args.scales): of one token a sequence, and the
+// merge of its ranges; of chunks of at most kShortTokens tokens, with
+// launch_short_merge, where beside: right after launch_chunk_attention
+// (kv8_attention.cu).  page_map: boxes of one page's codes, 64-byte swizzled.
 cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
                            cudaStream_t stream);
-cudaError_t launch_chunk8_attention(const CUtensorMap& q_map, const MaskedArgs& args, int format,
-                                    int grid, cudaStream_t stream);
 cudaError_t launch_short_chunks8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
                                  bool beside, cudaStream_t stream);
 
