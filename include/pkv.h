@@ -25,7 +25,7 @@
  *    also across streams.  State kept between calls: a per-thread cache of
  *    TMA descriptors and of the wait limit (pkv_set_wait_limit_ns), the
  *    device's SM count, and per device up to four RoPE cos/sin tables for
- *    positions below 2048 (6 MiB of static device memory).  The first call
+ *    positions below 2048 (8 MiB of static device memory).  The first call
  *    with a rope_theta not seen before on a device builds a table for it in
  *    a free slot, on the calling stream, and tags the slot afterwards; a
  *    tagged slot is never rewritten.  Kernels read a table only once they

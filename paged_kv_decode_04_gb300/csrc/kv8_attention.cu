@@ -55,13 +55,21 @@ constexpr float kMoveLog2 = 8.f;   // a score this far above the reference moves
 constexpr float kLift = 7.f;       // weights are 2^(s - m + kLift) <= 2^15
 constexpr float kLowestFloat = -3.402823466e38f;
 
-__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+// D = A B (+ D), FP32 accumulators.  (Not volatile: the compiler may interleave the
+// chains of two pages.)
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Two 16 x 16 matrices of bytes, transposed: lane l gives the address of row
@@ -183,61 +191,63 @@ __device__ __forceinline__ void load_v(uint32_t vt, const Lane& P, uint32_t (&va
   }
 }
 
-// Fold a page's masked scores (in log2 units) into S.  kOne: columns 4-7 stand
-// for the same rows as 0-3 and take the weights' second term.
-template <bool kOne>
-__device__ __forceinline__ void fold(const float (&x)[4], const uint32_t (&va)[4][4], float sv,
-                                     int ft, State& S) {
-  float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-  if (__any_sync(kFull, mx0 > S.m[0] + kMoveLog2 || mx1 > S.m[1] + kMoveLog2)) {
+// Move the references of S's rows to what the masked scores x of two pages ask for;
+// f: the factors of the pages' scores, of columns 2 ft and 2 ft + 1.
+__device__ __forceinline__ void move_reference(const float (&x)[2][4], const float (&f)[2][2],
+                                               State& S) {
+  float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]) * f[0][0], fmaxf(x[1][0], x[1][2]) * f[1][0]);
+  float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]) * f[0][1], fmaxf(x[1][1], x[1][3]) * f[1][1]);
+  if (!__any_sync(kFull, mx0 > S.m[0] + kMoveLog2 || mx1 > S.m[1] + kMoveLog2)) return;
 #pragma unroll
-    for (int i = 4; i <= 16; i <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, i));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, i));
-    }
-    const float m0 = fmaxf(S.m[0], mx0), m1 = fmaxf(S.m[1], mx1);
-    // (0 until the row has seen a score above -inf)
-    const float2 alpha = make_float2(fast_exp2(S.m[0] - fmaxf(m0, kLowestFloat)),
-                                     fast_exp2(S.m[1] - fmaxf(m1, kLowestFloat)));
-    S.l[0] *= alpha.x;
-    S.l[1] *= alpha.y;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      S.o[mt][0] = fmul2(S.o[mt][0], alpha);
-      S.o[mt][1] = fmul2(S.o[mt][1], alpha);
-    }
-    S.m[0] = m0;
-    S.m[1] = m1;
+  for (int i = 4; i <= 16; i <<= 1) {
+    mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, i));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, i));
   }
+  const float m0 = fmaxf(S.m[0], mx0), m1 = fmaxf(S.m[1], mx1);
+  // (0 until the row has seen a score above -inf)
+  const float2 alpha = make_float2(fast_exp2(S.m[0] - fmaxf(m0, kLowestFloat)),
+                                   fast_exp2(S.m[1] - fmaxf(m1, kLowestFloat)));
+  S.l[0] *= alpha.x;
+  S.l[1] *= alpha.y;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+    S.o[mt][0] = fmul2(S.o[mt][0], alpha);
+    S.o[mt][1] = fmul2(S.o[mt][1], alpha);
+  }
+  S.m[0] = m0;
+  S.m[1] = m1;
+}
+
+// A page's weights as the B fragment of the second product: columns 0-3 the first
+// terms of the four rows, columns 4-7 (lanes ft >= 2, which hold the same scores)
+// their second ones.
+__device__ __forceinline__ void page_weights(const float (&x)[4], const float (&f)[2], int ft,
+                                             State& S, uint32_t& b0, uint32_t& b1) {
   const float d0 = kLift - fmaxf(S.m[0], kLowestFloat), d1 = kLift - fmaxf(S.m[1], kLowestFloat);
-  const float p0 = fast_exp2(x[0] + d0), p1 = fast_exp2(x[1] + d1);
-  const float p2 = fast_exp2(x[2] + d0), p3 = fast_exp2(x[3] + d1);
+  const float p0 = fast_exp2(fmaf(x[0], f[0], d0)), p1 = fast_exp2(fmaf(x[1], f[1], d1));
+  const float p2 = fast_exp2(fmaf(x[2], f[0], d0)), p3 = fast_exp2(fmaf(x[3], f[1], d1));
   S.l[0] += p0 + p2;
   S.l[1] += p1 + p3;
   const uint32_t h0 = pack_f16x2(p0, p1), h1 = pack_f16x2(p2, p3);
   const float2 f0 = f16x2_to_float2(h0), f1 = f16x2_to_float2(h1);
   const uint32_t l0 = pack_f16x2(p0 - f0.x, p1 - f0.y), l1 = pack_f16x2(p2 - f1.x, p3 - f1.y);
+  b0 = transpose8x8(ft < 2 ? h0 : l0);
+  b1 = transpose8x8(ft < 2 ? h1 : l1);
+}
+
+// O += sv * V^T P^T of a page.
+template <int kFmt>
+__device__ __forceinline__ void add_values(uint32_t vt, const Lane& P, float sv, uint32_t b0,
+                                           uint32_t b1, State& S) {
+  uint32_t va[4][4];
+  load_v<kFmt>(vt, P, va);
   const float2 s2 = make_float2(sv, sv);
-  if constexpr (kOne) {
-    const uint32_t b0 = transpose8x8(ft < 2 ? h0 : l0), b1 = transpose8x8(ft < 2 ? h1 : l1);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_16816_f16(t, va[mt], b0, b1);
-      S.o[mt][0] = ffma2(make_float2(t[0], t[1]), s2, S.o[mt][0]);
-      S.o[mt][1] = ffma2(make_float2(t[2], t[3]), s2, S.o[mt][1]);
-    }
-  } else {
-    const uint32_t th0 = transpose8x8(h0), th1 = transpose8x8(h1);
-    const uint32_t tl0 = transpose8x8(l0), tl1 = transpose8x8(l1);
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_16816_f16(t, va[mt], th0, th1);
-      mma_16816_f16(t, va[mt], tl0, tl1);
-      S.o[mt][0] = ffma2(make_float2(t[0], t[1]), s2, S.o[mt][0]);
-      S.o[mt][1] = ffma2(make_float2(t[2], t[3]), s2, S.o[mt][1]);
-    }
+  for (int mt = 0; mt < 4; ++mt) {
+    float t[4];
+    mma_new(t, va[mt], b0, b1);
+    S.o[mt][0] = ffma2(make_float2(t[0], t[1]), s2, S.o[mt][0]);
+    S.o[mt][1] = ffma2(make_float2(t[2], t[3]), s2, S.o[mt][1]);
   }
 }
 
@@ -265,6 +275,17 @@ struct Ring {
   }
 };
 
+// The ring's stages in turn, and the parity of their barriers' phases.
+struct Turn {
+  int stage = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // The producer warp: pages [r0, r1) of the list page_of, ids 32 at a time.
 template <typename PageOf>
 __device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map,
@@ -285,10 +306,11 @@ __device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map
   const uint64_t policy = l2_policy_evict_first();
   int ids = load_ids(0), ids_next = load_ids(32);
   int k = 0;
-  for (; k < n; ++k) {
-    const int st = k % kStages;
+  Turn T;
+  for (; k < n; ++k, T.next()) {
+    const int st = T.stage;
     if (k >= kStages) {
-      const bool ok = mbar_wait_bounded(R.empty(st), (k / kStages - 1) & 1, a.wait_ns);
+      const bool ok = mbar_wait_bounded(R.empty(st), T.phase ^ 1, a.wait_ns);
       if (!__all_sync(kFull, ok)) {
         if (lane == 0) record_error(a.dev_err, kErrTimeout);
         break;
@@ -379,38 +401,81 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const float c1 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h + 4);
   State S;
   S.reset();
-  for (int k = 0; k < r1 - r0; ++k) {
-    const int st = k % kStages;
-    const bool ready = mbar_wait_bounded(R.full(st), (k / kStages) & 1, a.wait_ns);
+  // Two pages at a time: one alone is a chain of latencies (copy, products, weights,
+  // products), and what is checked is checked once for both.
+  const int n = r1 - r0;
+  Turn T;
+  for (int k = 0; k < n; k += 2) {
+    const int st0 = T.stage, phase0 = T.phase;
+    T.next();
+    const int st1 = T.stage, phase1 = T.phase;
+    T.next();
+    bool ready = mbar_wait_bounded(R.full(st0), phase0, a.wait_ns);
+    if (k + 1 < n) ready &= mbar_wait_bounded(R.full(st1), phase1, a.wait_ns);
     if (!__all_sync(kFull, ready)) {
       if (lane == 0) record_error(a.dev_err, kErrTimeout);
       break;
     }
-    const uint2 meta = lds64(R.meta(st));
-    if (static_cast<int>(meta.y) >= 0) {
-      const uint32_t kt = R.page(st) + g * kBlockBytes, vt = kt + kNumKvHeads * kBlockBytes;
-      const float sk = scale_value(stored_scale(lds8(R.scales(st) + g)));
-      const float sv = scale_value(stored_scale(lds8(R.scales(st) + kNumKvHeads + g)));
-      uint32_t ka[4][4], va[4][4];
+    // seen tokens of the pages (none where there is none, or it was not read)
+    auto seen = [&](int st, bool there) {
+      const uint2 meta = lds64(R.meta(st));
+      if (!there || static_cast<int>(meta.y) < 0) return 0u;
+      return V.whole(meta.x) ? 0xFFFFu : V.mask(meta.x);
+    };
+    const uint32_t vis0 = seen(st0, true), vis1 = seen(st1, k + 1 < n);
+    const uint32_t kt0 = R.page(st0) + g * kBlockBytes, kt1 = R.page(st1) + g * kBlockBytes;
+    constexpr uint32_t kV = kNumKvHeads * kBlockBytes;
+    const float sk0 = scale_value(lds8(R.scales(st0) + g));
+    const float sk1 = scale_value(lds8(R.scales(st1) + g));
+    const float sv0 = scale_value(lds8(R.scales(st0) + kNumKvHeads + g));
+    const float sv1 = scale_value(lds8(R.scales(st1) + kNumKvHeads + g));
+    // (a factor of 0 would make NaN of a masked score)
+    const float f[2][2] = {{fmaxf(c0 * sk0, 0x1p-126f), fmaxf(c1 * sk0, 0x1p-126f)},
+                           {fmaxf(c0 * sk1, 0x1p-126f), fmaxf(c1 * sk1, 0x1p-126f)}};
+    float s[2][4];
+    uint32_t b[2][2];
+    auto scores = [&](uint32_t kt, float (&x)[4]) {
+      uint32_t ka[4][4];
       load_k<kFmt>(kt, P, ka);
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_new(x, ka[0], qb[0][0], qb[0][1]);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_16816_f16(s, ka[kk], qb[kk][0], qb[kk][1]);
-      s[0] *= c0 * sk;
-      s[1] *= c1 * sk;
-      s[2] *= c0 * sk;
-      s[3] *= c1 * sk;
-      const uint32_t vis = V.mask(meta.x);
-      if (vis != 0xFFFFu) {
-        if (!((vis >> P.tok) & 1u)) s[0] = s[1] = -INFINITY;
-        if (!((vis >> (P.tok + 2)) & 1u)) s[2] = s[3] = -INFINITY;
-        if constexpr (kFmt == kKv8E4m3) hide_v(vt, vis, lane);
+      for (int kk = 1; kk < 4; ++kk) mma_add(x, ka[kk], qb[kk][0], qb[kk][1]);
+    };
+    if ((vis0 & vis1) == 0xFFFFu) {
+      scores(kt0, s[0]);
+      scores(kt1, s[1]);
+      move_reference(s, f, S);
+      page_weights(s[0], f[0], P.ft, S, b[0][0], b[0][1]);
+      page_weights(s[1], f[1], P.ft, S, b[1][0], b[1][1]);
+      add_values<kFmt>(kt0 + kV, P, sv0, b[0][0], b[0][1], S);
+      add_values<kFmt>(kt1 + kV, P, sv1, b[1][0], b[1][1], S);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t vis = i == 0 ? vis0 : vis1, kt = i == 0 ? kt0 : kt1;
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
+        if (vis == 0u) continue;
+        scores(kt, s[i]);
+        if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
+        if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
+        if constexpr (kFmt == kKv8E4m3) hide_v(kt + kV, vis, lane);
       }
-      load_v<kFmt>(vt, P, va);
-      fold<true>(s, va, sv, P.ft, S);
+      // (the scales of a page that was not read may be anything)
+      const float g2[2][2] = {{vis0 ? f[0][0] : 1.f, vis0 ? f[0][1] : 1.f},
+                              {vis1 ? f[1][0] : 1.f, vis1 ? f[1][1] : 1.f}};
+      move_reference(s, g2, S);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        page_weights(s[i], g2[i], P.ft, S, b[i][0], b[i][1]);
+        if ((i == 0 ? vis0 : vis1) != 0u)
+          add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, i == 0 ? sv0 : sv1, b[i][0], b[i][1], S);
+      }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(R.empty(st));
+    if (lane == 0) {
+      mbar_arrive(R.empty(st0));
+      if (k + 1 < n) mbar_arrive(R.empty(st1));
+    }
   }
 
   // the terms' columns meet; lanes ft < 2 hold heads 2 ft and 2 ft + 1
@@ -435,12 +500,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
 }
 
-// Chunks of at most four tokens: 16 query rows of a kv head, as two n-tiles of 8
-// (row = 4 token + head); grid (ranges, batch).  kBeside: launched right after the
-// tcgen05 kernel of the same call, as short_chunk.cu's kernel is: it starts at
-// once, and its first CTA and those without a short chunk end after that grid.
-constexpr int kRowTiles = kShortTokens / 2;
-
+// Chunks of at most four tokens: the 16 query rows of a kv head (row = 4 token +
+// head) as M of both products, tokens and then dims as N.  Rows fg and fg + 8 of a
+// lane are of tokens fg / 4 and 2 + fg / 4.  The scores' fragment of a page is the
+// weights' of the second product as it stands.  grid (ranges, batch).  kBeside:
+// launched right after the tcgen05 kernel of the same call, as short_chunk.cu's
+// kernel is: it starts at once, and its first CTA and those without a short chunk
+// end after that grid.
 template <int kFmt, bool kBeside>
 __global__ void __launch_bounds__(kThreads, kCtas)
     paged8_short_chunk_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a) {
@@ -476,22 +542,26 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
 
   const Lane P(lane);
-  uint32_t qb[kRowTiles][4][2];
-  float c[kRowTiles][2];
-  State S[kRowTiles];
+  uint32_t qa[4][4];  // A fragments: [k-step][row fg, fg + 8 of dims {0, 1}, then {2, 3}]
+  float c[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < kRowTiles; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int tok = 2 * i + (P.fg >> 2);
-    const float undo = load_q(
-        tok < nt ? a.q + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + (P.fg & 3)) *
-                             kHeadDim
-                 : nullptr,
-        P.ft, qb[i]);
-    c[i][0] = a.scale_log2 * __shfl_sync(kFull, undo, 8 * P.ft);
-    c[i][1] = a.scale_log2 * __shfl_sync(kFull, undo, 8 * P.ft + 4);
-    S[i].reset();
+    uint32_t qb[4][2];
+    c[i] = a.scale_log2 *
+           load_q(tok < nt ? a.q + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup +
+                                    (P.fg & 3)) * kHeadDim
+                           : nullptr,
+                  P.ft, qb);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      qa[kk][i] = qb[kk][0];
+      qa[kk][2 + i] = qb[kk][1];
+    }
   }
-  const int tiles = (nt + 1) >> 1;
+  float2 o[8][2];  // dims 8 nt + 2 ft, + 1 of rows fg and fg + 8
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
   // bits of a page's slots below token x (as a distance from the page's first)
   auto below = [](int64_t x) {
     return x <= 0 ? 0u : (x >= kPageSize ? 0xFFFFu : (1u << static_cast<int>(x)) - 1u);
@@ -502,9 +572,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
            ((0xFFFFu & ~below(static_cast<int64_t>(p0) - a.window + 1 - base)) |
             below(static_cast<int64_t>(a.sinks) - base));
   };
-  for (int k = 0; k < r1 - r0; ++k) {
-    const int st = k % kStages;
-    const bool ready = mbar_wait_bounded(R.full(st), (k / kStages) & 1, a.wait_ns);
+  Turn T;
+  for (int k = 0; k < r1 - r0; ++k, T.next()) {
+    const int st = T.stage;
+    const bool ready = mbar_wait_bounded(R.full(st), T.phase, a.wait_ns);
     if (!__all_sync(kFull, ready)) {
       if (lane == 0) record_error(a.dev_err, kErrTimeout);
       break;
@@ -512,73 +583,131 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const uint2 meta = lds64(R.meta(st));
     if (static_cast<int>(meta.y) >= 0) {
       const uint32_t kt = R.page(st) + g * kBlockBytes, vt = kt + kNumKvHeads * kBlockBytes;
-      const float sk = scale_value(stored_scale(lds8(R.scales(st) + g)));
-      const float sv = scale_value(stored_scale(lds8(R.scales(st) + kNumKvHeads + g)));
+      const float sk = scale_value(lds8(R.scales(st) + g));
+      const float sv = scale_value(lds8(R.scales(st) + kNumKvHeads + g));
       const int base = static_cast<int>(meta.x) * kPageSize;
       // does every row see the whole page?
       const bool whole = base + kPageSize - 1 <= pos0 &&
                          (static_cast<int64_t>(base) > static_cast<int64_t>(end) - 1 - a.window ||
                           base + kPageSize <= a.sinks);
-      float s[kRowTiles][4];
+      // s[j][2 i + e]: row fg + 8 i, token 4 ft + 2 j + e
+      float s[2][4];
       {
-        uint32_t ka[4][4];
-        load_k<kFmt>(kt, P, ka);
+        const uint4 x = lds128(kt + P.k0), y = lds128(kt + P.k1);
+        const uint32_t k0[4] = {x.x, x.y, x.z, x.w}, k1[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < kRowTiles; ++i)
-          if (i < tiles) {
-            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_16816_f16(s[i], ka[kk], qb[i][kk][0], qb[i][kk][1]);
-            s[i][0] *= c[i][0] * sk;
-            s[i][1] *= c[i][1] * sk;
-            s[i][2] *= c[i][0] * sk;
-            s[i][3] *= c[i][1] * sk;
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t b0, b1, d0, d1;
+          decode_f16<kFmt>(k0[kk], b0, b1);
+          decode_f16<kFmt>(k1[kk], d0, d1);
+          if (kk == 0) {
+            mma_new(s[0], qa[kk], b0, b1);
+            mma_new(s[1], qa[kk], d0, d1);
+          } else {
+            mma_add(s[0], qa[kk], b0, b1);
+            mma_add(s[1], qa[kk], d0, d1);
           }
+        }
       }
+      const float f[2] = {c[0] * sk, c[1] * sk};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] *= f[e >> 1];
       if (!whole) {
 #pragma unroll
-        for (int i = 0; i < kRowTiles; ++i) {
-          // this lane's two rows are of one token
-          const int p = pos0 + 2 * i + (P.ft >> 1);
-          const uint32_t vis = seen_by(base, p, p);
-          if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
-          if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
+        for (int i = 0; i < 2; ++i) {
+          const int p = pos0 + 2 * i + (P.fg >> 2);
+          const uint32_t vis = seen_by(base, p, p) >> (4 * P.ft);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((vis >> (2 * j + e)) & 1u)) s[j][2 * i + e] = -INFINITY;
         }
         if constexpr (kFmt == kKv8E4m3) hide_v(vt, seen_by(base, pos0, end - 1), lane);
       }
-      uint32_t va[4][4];
-      load_v<kFmt>(vt, P, va);
+      // the running reference of both rows
+      float mx[2];
 #pragma unroll
-      for (int i = 0; i < kRowTiles; ++i)
-        if (i < tiles) fold<false>(s[i], va, sv, P.ft, S[i]);
+      for (int i = 0; i < 2; ++i)
+        mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+      if (__any_sync(kFull, mx[0] > m[0] + kMoveLog2 || mx[1] > m[1] + kMoveLog2)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
+          const float top = fmaxf(m[i], mx[i]);
+          const float alpha = fast_exp2(m[i] - fmaxf(top, kLowestFloat));
+          l[i] *= alpha;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[d][i] = fmul2(o[d][i], make_float2(alpha, alpha));
+          m[i] = top;
+        }
+      }
+      // weights as two f16 terms
+      uint32_t hi[4], lo2[4];  // A fragments: row fg of tokens {0, 1}, row fg + 8, then {2, 3}
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float d = kLift - fmaxf(m[i], kLowestFloat);
+          const float p0 = fast_exp2(s[j][2 * i] + d), p1 = fast_exp2(s[j][2 * i + 1] + d);
+          l[i] += p0 + p1;
+          const uint32_t w = pack_f16x2(p0, p1);
+          const float2 r = f16x2_to_float2(w);
+          hi[2 * j + i] = w;
+          lo2[2 * j + i] = pack_f16x2(p0 - r.x, p1 - r.y);
+        }
+      uint32_t vb[8];
+      ldsm_b8_trans(vt + P.v0, *reinterpret_cast<uint32_t(*)[4]>(&vb[0]));
+      ldsm_b8_trans(vt + P.v1, *reinterpret_cast<uint32_t(*)[4]>(&vb[4]));
+      const float2 s2 = make_float2(sv, sv);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t b0, b1;
+        decode_f16<kFmt>(vb[d], b0, b1);
+        float t[4];
+        mma_new(t, hi, b0, b1);
+        mma_add(t, lo2, b0, b1);
+        o[d][0] = ffma2(make_float2(t[0], t[1]), s2, o[d][0]);
+        o[d][1] = ffma2(make_float2(t[2], t[3]), s2, o[d][1]);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(R.empty(st));
   }
 
 #pragma unroll
-  for (int i = 0; i < kRowTiles; ++i) {
-#pragma unroll
-    for (int x = 4; x <= 16; x <<= 1) {
-      S[i].l[0] += __shfl_xor_sync(kFull, S[i].l[0], x);
-      S[i].l[1] += __shfl_xor_sync(kFull, S[i].l[1], x);
-    }
-    const int tok = 2 * i + (P.ft >> 1);
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(kFull, l[i], 1);
+    l[i] += __shfl_xor_sync(kFull, l[i], 2);
+    const int tok = 2 * i + (P.fg >> 2), h = P.fg & 3;
     if (tok >= nt) continue;
+    if (a.short_splits > 1) {
+      const int64_t part = short_part_row(b, g, tok * kGroup + h) * a.short_splits + split;
+      float2* dst = reinterpret_cast<float2*>(a.short_acc + part * kHeadDim) + P.ft;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int h = ((2 * P.ft) & 3) + j;
-      put_row(S[i], j, P.fg,
-              a.out + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + h) * kHeadDim,
-              a.short_splits > 1, a.short_acc, a.short_ml,
-              short_part_row(b, g, tok * kGroup + h) * a.short_splits + split);
+      for (int d = 0; d < 8; ++d) dst[4 * d] = o[d][i];
+      if (P.ft == 0) *reinterpret_cast<float2*>(a.short_ml + 2 * part) = make_float2(m[i], l[i]);
+    } else {
+      const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+                          a.out + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + h) *
+                                      kHeadDim) + P.ft;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) dst[4 * d] = pack_bf16x2(o[d][i].x * inv, o[d][i].y * inv);
     }
   }
 }
 
-// One warp per query row combines its ranges.
-constexpr int kMergeRows = 4;
-__global__ void __launch_bounds__(32 * kMergeRows) merge8_kernel(const MaskedArgs a) {
+// Combine a row's ranges, added in an order that does not change.  Up to kFewRanges
+// of them a warp to a row; more take a CTA to a row, warp w the ranges w, w +
+// kMergeWarps, ... (each step of a sum is an L2 latency: the 304 ranges of one
+// sequence of 30011 tokens took 33 us with one warp, 9 with eight and a maximum over
+// all ranges first).
+constexpr int kMergeRows = 4, kMergeWarps = 16, kFewRanges = 16;
+__global__ void __launch_bounds__(32 * kMergeRows) merge8_few_kernel(const MaskedArgs a) {
   allow_dependent_grids();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31;
@@ -588,6 +717,78 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge8_kernel(const MaskedArg
       reinterpret_cast<const float2*>(a.part_acc) + row * a.num_splits * (kHeadDim / 2) + lane;
   reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] =
       merge_ranges(ml, acc, a.num_splits, lane);
+}
+
+__global__ void __launch_bounds__(32 * kMergeWarps) merge8_many_kernel(const MaskedArgs a) {
+  __shared__ float2 s_ml[kMergeWarps];
+  __shared__ float2 s_o[kMergeWarps][kHeadDim / 2];
+  allow_dependent_grids();
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, splits = a.num_splits;
+  const int64_t row = blockIdx.x;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * splits;
+  const float2* acc =
+      reinterpret_cast<const float2*>(a.part_acc) + row * splits * (kHeadDim / 2) + lane;
+  // this warp's state; a range that saw no token has a sum of 0
+  float M = -INFINITY, L = 0.f;
+  float2 O = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int s0 = w; s0 < splits; s0 += 32 * kMergeWarps) {
+    // lane i: (max, sum) of range s0 + i kMergeWarps
+    const int mine = s0 + lane * kMergeWarps;
+    const float2 x = mine < splits ? __ldcg(ml + mine) : make_float2(-INFINITY, 0.f);
+    float top = x.y != 0.f ? x.x : -INFINITY;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+    top = fmaxf(top, M);
+    const float old = M == -INFINITY ? 1.f : fast_exp2(M - top);
+    // (-inf: a NaN row)
+    const float wt = x.y == 0.f ? 0.f : x.x == -INFINITY ? 1.f : fast_exp2(x.x - top);
+    float sum = x.y == 0.f ? 0.f : x.y * wt;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
+    L = L * old + sum;
+    O.x *= old;
+    O.y *= old;
+    M = top;
+#pragma unroll 1
+    for (int e0 = 0; e0 < 32 && s0 + e0 * kMergeWarps < splits; e0 += 16) {
+      float2 v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int s = s0 + (e0 + e) * kMergeWarps;
+        v[e] = s < splits ? __ldcg(acc + static_cast<int64_t>(s) * (kHeadDim / 2))
+                          : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float f = __shfl_sync(kFull, wt, e0 + e);
+        if (f != 0.f) {  // (what a range without tokens left is not read)
+          O.x = fmaf(v[e].x, f, O.x);
+          O.y = fmaf(v[e].y, f, O.y);
+        }
+      }
+    }
+  }
+  s_o[w][lane] = O;
+  if (lane == 0) s_ml[w] = make_float2(M, L);
+  __syncthreads();
+  if (w > 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) top = fmaxf(top, s_ml[i].x);
+  L = 0.f;
+  O = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) {
+    if (s_ml[i].y == 0.f) continue;
+    const float f = s_ml[i].x == -INFINITY ? 1.f : fast_exp2(s_ml[i].x - top);
+    L = fmaf(s_ml[i].y, f, L);
+    O.x = fmaf(s_o[i][lane].x, f, O.x);
+    O.y = fmaf(s_o[i][lane].y, f, O.y);
+  }
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
 }
 
 // Launch a streaming kernel, opting in to its shared memory once per device.
@@ -617,7 +818,10 @@ cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, 
           : launch<paged8_decode_kernel<kKv8Int8>>(page_map, args, args.num_splits, stream);
   if (err != cudaSuccess || args.num_splits == 1) return err;
   static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
-  return launch_pdl(merge8_kernel, dim3(args.batch * (kNumQHeads / kMergeRows)),
+  if (args.num_splits > kFewRanges)
+    return launch_pdl(merge8_many_kernel, dim3(args.batch * kNumQHeads), dim3(32 * kMergeWarps), 0,
+                      stream, args);
+  return launch_pdl(merge8_few_kernel, dim3(args.batch * (kNumQHeads / kMergeRows)),
                     dim3(32 * kMergeRows), 0, stream, args);
 }
 

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kv8.cuh"
 #include "pkv_device.cuh"
@@ -24,7 +25,110 @@ constexpr int kHalf = kHeadDim / 2;
 constexpr int kThreads = 32 * kNumKvHeads;  // a warp to a kv head
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long ra, rb, rd;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
+}
+
+// (cos, sin) of a rotation, as floats and what they leave.
+struct Angle {
+  float c, s, c_lo, s_lo;
+};
+__device__ __forceinline__ Angle make_angle(double c, double s) {
+  Angle t;
+  t.c = static_cast<float>(c);
+  t.s = static_cast<float>(s);
+  t.c_lo = static_cast<float>(__dsub_rn(c, static_cast<double>(t.c)));
+  t.s_lo = static_cast<float>(__dsub_rn(s, static_cast<double>(t.s)));
+  return t;
+}
+
+// a c + b s rounded once to bf16, where FP32 with the rounding errors carried along
+// decides it: off by at most 2^-43 (|a| + |b|) (2^-24 of terms of 2^-23 of that, and
+// what is left of cos and sin), it rounds as the exact value, and as FP64, unless it
+// is that close to a midpoint or so small that half its FP32 spacing is below that.
+// a, b: bf16 values, not too far from 1.
+__device__ __forceinline__ bool turn_exactly(float a, float b, const Angle& t, uint16_t* out) {
+  const float p = a * t.c, q = b * t.s;
+  const float pe = fmaf(a, t.c, -p), qe = fmaf(b, t.s, -q);  // exactly what they left
+  auto two_sum = [](float x, float y, float& e) {
+    const float h = __fadd_rn(x, y), z = __fsub_rn(h, x);
+    e = __fadd_rn(__fsub_rn(x, __fsub_rn(h, z)), __fsub_rn(y, z));
+    return h;
+  };
+  float e, lo;
+  const float h = two_sum(p, q, e);
+  const float hi = two_sum(h, __fadd_rn(e, __fadd_rn(__fadd_rn(pe, qe),
+                                                     fmaf(a, t.c_lo, b * t.s_lo))), lo);
+  // hi + lo is on hi's side of a bf16 midpoint, half a spacing from it, unless hi is
+  // one
+  const uint32_t bits = __float_as_uint(hi);
+  const float s0 = fabsf(a) + fabsf(b);
+  const bool large = fabsf(hi) > 0x1p-18f * s0;
+  if ((bits & 0xFFFFu) != 0x8000u) {
+    *out = float_to_bf16_rne(hi);
+    return large;
+  }
+  const float away = hi < 0.f ? -lo : lo;  // beyond the midpoint, as a magnitude
+  *out = static_cast<uint16_t>((bits >> 16) + (away > 0.f ? 1u : 0u));
+  return large && fabsf(lo) > 0x1p-43f * s0;
+}
+
+// Both values of a rotated pair, rotate_pair's bits.
+__device__ __noinline__ uint2 rotate_in_fp64(uint32_t h1, uint32_t h2, double angle) {
+  double c, s;
+  sincos(angle, &s, &c);
+  uint16_t y1, y2;
+  rotate_pair(static_cast<uint16_t>(h1), static_cast<uint16_t>(h2), c, s, &y1, &y2);
+  return make_uint2(y1, y2);
+}
+__device__ __forceinline__ void rotate_carefully(uint32_t h1, uint32_t h2, const Angle& t,
+                                                 double angle, uint16_t* y1, uint16_t* y2) {
+  const float u = __uint_as_float(h1 << 16), v = __uint_as_float(h2 << 16);
+  const float s0 = fabsf(u) + fabsf(v);
+  // (tiny, huge, not finite: FP32 would lose them)
+  const bool fine = s0 >= 0x1p-70f && s0 <= 0x1p+100f;
+  Angle n = t;
+  n.s = -t.s;
+  n.s_lo = -t.s_lo;
+  const bool ok1 = turn_exactly(u, v, n, y1), ok2 = turn_exactly(v, u, t, y2);
+  if (!(fine && ok1 && ok2)) {
+    const uint2 y = rotate_in_fp64(h1 & 0xFFFFu, h2 & 0xFFFFu, angle);
+    *y1 = static_cast<uint16_t>(y.x);
+    *y2 = static_cast<uint16_t>(y.y);
+  }
+}
+
+// FP32 rotation of a pair with a bound on its error: bf16 pairs (y1 in the low half)
+// at and below, and at and above, rotate_pair's.  y is off by at most 3 x 2^-24 (|x1|
+// + |x2|): 2^-24 of both factors for cos and sin, of one product, and of y, |y| <= |x1|
+// + |x2|; y - A and y + A, A = 1.125 x 2^-22 (|x1| + |x2|), are off by another 2^-24 of
+// that, so they enclose the FP64 value.  `odd`: too small, too large or not finite for
+// that.
+__device__ __forceinline__ uint2 rotate_fast(float u, float v, float c, float s, bool& odd) {
+  const float2 t = fmul2(make_float2(v, u), make_float2(-s, s));
+  const float2 y = ffma2(make_float2(u, v), make_float2(c, c), t);
+  const float s0 = fabsf(u) + fabsf(v), A = s0 * 0x1.2p-22f;
+  // (zeros keep their sign: y itself both times)
+  const float2 l = fadd2(y, make_float2(-A, -A)), r = fadd2(y, make_float2(A, A));
+  const uint32_t lo = cvt_bf16x2_rn(l.x, l.y);
+  // 2^-70 <= s0 <= 2^100, or zeros
+  odd = __float_as_uint(s0) - 0x1C800000u > 0x71800000u - 0x1C800000u && s0 != 0.f;
+  return make_uint2(lo, s0 == 0.f ? lo : cvt_bf16x2_rn(r.x, r.y));
+}
 
 // A warp stores the largest magnitude's scale of a block that holds `earlier`
 // tokens already, whose codes follow it, and returns the scale.
@@ -79,23 +183,34 @@ __global__ void __launch_bounds__(kThreads)
     old_v = stored_scale(c.scales[scale_at(page, 1, h)]);
   }
   // Past the table a pair's FP64 sincos is taken once and shared by the 8 heads'
-  // threads (as in kv_append_kernel).
-  __shared__ double2 s_cs[kHalf];
-  RopeCS cs;
+  // threads (as in kv_append_kernel); a table that is still being built is left to
+  // each thread.
+  __shared__ Angle s_angle[kHalf];
+  Angle t;
+  const double angle = __dmul_rn(static_cast<double>(pos), freqs.inv_freq[i]);
   if (freqs.table_theta == nullptr || pos < 0 || pos >= kRopeTablePositions) {
     if (h == 0) {
-      const RopeCS f = rope_cs(freqs, false, pos, i);
-      s_cs[i] = make_double2(f.c64, f.s64);
+      double s64, c64;
+      sincos(angle, &s64, &c64);
+      s_angle[i] = make_angle(c64, s64);
     }
     __syncthreads();
-    cs.c64 = s_cs[i].x;
-    cs.s64 = s_cs[i].y;
-    cs.c32 = static_cast<float>(cs.c64);
-    cs.s32 = static_cast<float>(cs.s64);
-    cs.have64 = true;
+    t = s_angle[i];
+  } else if (table_ok) {
+    const float2 hi = freqs.table32[pos * kHalf + i], lo = freqs.table_lo[pos * kHalf + i];
+    t = {hi.x, hi.y, lo.x, lo.y};
   } else {
-    cs = rope_cs(freqs, table_ok, pos, i);
+    double s64, c64;
+    sincos(angle, &s64, &c64);
+    t = make_angle(c64, s64);
   }
+  auto rotate = [&](uint16_t x1, uint16_t x2, uint16_t* y1, uint16_t* y2) {
+    bool odd;
+    const uint2 y = rotate_fast(bf16_to_float(x1), bf16_to_float(x2), t.c, t.s, odd);
+    *y1 = static_cast<uint16_t>(y.x);
+    *y2 = static_cast<uint16_t>(y.x >> 16);
+    if (odd || y.x != y.y) rotate_carefully(x1, x2, t, angle, y1, y2);
+  };
 
   if (q_in != nullptr) {
     const int64_t qbase = static_cast<int64_t>(b) * kNumQHeads * kHeadDim;
@@ -110,7 +225,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = 0; k < 4; ++k) {
       const int64_t o = qbase + (h + 8 * k) * kHeadDim + i;
       uint16_t y1, y2;
-      rotate_pair_rope(freqs, table_ok, pos, i, cs, x1[k], x2[k], &y1, &y2);
+      rotate(x1[k], x2[k], &y1, &y2);
       q_out[o] = y1;
       q_out[o + kHalf] = y2;
     }
@@ -121,7 +236,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 
   uint16_t y1, y2;
-  rotate_pair_rope(freqs, table_ok, pos, i, cs, k1, k2, &y1, &y2);
+  rotate(k1, k2, &y1, &y2);
   uint32_t v1 = vw & 0xFFFFu, v2 = vw >> 16;
   if (!finite_bf16(y1) || !finite_bf16(y2) || !finite_bf16(v1) || !finite_bf16(v2)) {
     record_error(dev_err, kErrValue);
@@ -147,63 +262,78 @@ __global__ void __launch_bounds__(kThreads)
 // A unit is one page of one sequence.  Units are numbered so that a sequence's
 // first is off[b] / 16 + 2 b: n tokens touch at most n / 16 + 2 pages, so the
 // ranges of numbers do not meet (some numbers name no page), and the sequence of
-// a unit is found by search, without a prefix sum.
+// a unit is found by search, without a prefix sum.  A CTA takes consecutive
+// numbers, 32 at a time: each lane finds one unit, so the searches and the loads
+// behind them (lengths, places, table entries) cost their latency once for 32.
 struct Unit {
-  int b, page;          // sequence, page of it; b < 0: none
   int64_t row0;         // row of k and v of the token in slot 0 of the page
+  int pool_page;        // -1: no unit
+  int page;             // page of the sequence
   int s0, s1;           // slots [s0, s1) are the call's
-  int64_t pool_page;
 };
 
 __host__ __device__ inline int64_t unit_count(int num_tokens, int batch) {
   return num_tokens / kPageSize + 2 * static_cast<int64_t>(batch);
 }
 
-// Found by a whole warp (the same in every lane); `report`: one warp of the unit
+// The unit of number u, by each lane for itself; `report`: one warp of a CTA
 // reports what is wrong with it.
-__device__ __forceinline__ Unit find_unit(int64_t u, const Kv8& c,
+__device__ __forceinline__ Unit find_unit(int64_t u, int64_t end, const Kv8& c,
                                           const int32_t* __restrict__ off,
                                           const int32_t* __restrict__ starts, int num_tokens,
-                                          int32_t* dev_err, bool report, int lane) {
+                                          int32_t* dev_err, bool report) {
+  Unit r = {0, -1, 0, 0, 0};
+  if (u >= end) return r;
   auto first = [&](int b) { return static_cast<int64_t>(off[b] / kPageSize) + 2ll * b; };
-  int lo = 0, n = c.batch;
-  while (n > 1) {  // 32 places at a time
-    const int step = (n + 31) / 32, at = lane * step;
-    const unsigned below = __ballot_sync(kFull, at < n && first(lo + min(at, n - 1)) <= u);
-    const int cut = max(__popc(below) - 1, 0) * step;
-    lo += cut;
-    n = min(step, n - cut);
+  int lo = 0, hi = c.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first(mid) <= u) lo = mid; else hi = mid;
   }
-  Unit r;
-  r.b = -1;
-  r.page = 0;
-  r.row0 = 0;
-  r.s0 = r.s1 = 0;
-  r.pool_page = -1;
   const int o0 = off[lo], o1 = off[lo + 1];
   if (o0 < 0 || o1 < o0 || o1 > num_tokens) {
-    if (report && lane == 0) record_error(dev_err, kErrOffsets);
+    if (report) record_error(dev_err, kErrOffsets);
     return r;
   }
-  const int64_t start = starts[lo], end = start + (o1 - o0);
+  const int64_t start = starts[lo], past = start + (o1 - o0);
   const int64_t limit = static_cast<int64_t>(c.max_blocks) * kPageSize;
-  const int64_t p0 = start > 0 ? start : 0, p1 = end < limit ? end : limit;
-  if (o1 > o0 && (p0 != start || p1 != end) && report && lane == 0)
-    record_error(dev_err, kErrPosition);
+  const int64_t p0 = start > 0 ? start : 0, p1 = past < limit ? past : limit;
+  if (o1 > o0 && (p0 != start || p1 != past) && report) record_error(dev_err, kErrPosition);
   const int64_t page = p0 / kPageSize + (u - first(lo));
   if (u < first(lo) || p1 <= p0 || page * kPageSize >= p1) return r;
+  const int pid = c.block_table[static_cast<int64_t>(lo) * c.max_blocks + page];
+  if (pid < 0 || pid >= c.num_pages) {
+    if (report) record_error(dev_err, kErrPage);
+    return r;
+  }
+  r.pool_page = pid;
   r.page = static_cast<int>(page);
   r.s0 = max(static_cast<int>(p0 - page * kPageSize), 0);
   r.s1 = p1 - page * kPageSize < kPageSize ? static_cast<int>(p1 - page * kPageSize) : kPageSize;
   r.row0 = o0 + page * kPageSize - start;
-  r.pool_page = c.block_table[static_cast<int64_t>(lo) * c.max_blocks + page];
-  if (r.pool_page < 0 || r.pool_page >= c.num_pages) {
-    if (report && lane == 0) record_error(dev_err, kErrPage);
-    return r;
-  }
-  r.b = lo;
   return r;
 }
+
+// Lane `src`'s unit.
+__device__ __forceinline__ Unit unit_of(const Unit& t, int src) {
+  Unit r;
+  r.row0 = __shfl_sync(kFull, t.row0, src);
+  r.pool_page = __shfl_sync(kFull, t.pool_page, src);
+  r.page = __shfl_sync(kFull, t.page, src);
+  const int s = __shfl_sync(kFull, t.s0 | (t.s1 << 8), src);
+  r.s0 = s & 0xFF;
+  r.s1 = s >> 8;
+  return r;
+}
+
+// The numbers [u0, u1) of a CTA.
+struct Share {
+  int64_t u0, u1;
+  __device__ __forceinline__ explicit Share(int64_t units) {
+    u0 = units * blockIdx.x / gridDim.x;
+    u1 = units * (blockIdx.x + 1) / gridDim.x;
+  }
+};
 
 // Offsets that do not begin at 0 and end at the number of tokens.
 __device__ __forceinline__ void check_ends(const Kv8& c, const int32_t* off, int num_tokens,
@@ -212,99 +342,85 @@ __device__ __forceinline__ void check_ends(const Kv8& c, const int32_t* off, int
     record_error(dev_err, kErrOffsets);
 }
 
-// RoPE of the 8 pairs (x1, x2) = dims (8 q + p, 32 + 8 q + p) of a row, in place:
-// FP32 with both ends of its error bound rounded to bf16, the pairs where these
-// differ (or that are outside FP32's comfort) again in FP64 (rotate_pair).
-__device__ __forceinline__ void rotate8(const RopeFreqs& f, bool table_ok, int pos, int q,
-                                        uint4& x1, uint4& x2) {
-  uint32_t* a = &x1.x;
-  uint32_t* b = &x2.x;
-  const int i0 = 8 * q;
-  float c[8], sn[8];
-  if (table_ok) {
-    const float4* t = reinterpret_cast<const float4*>(f.table32 + pos * kHalf + i0);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 cs = t[e];
-      c[2 * e] = cs.x;
-      sn[2 * e] = cs.y;
-      c[2 * e + 1] = cs.z;
-      sn[2 * e + 1] = cs.w;
-    }
-  } else {
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-      double s64, c64;
-      sincos(__dmul_rn(static_cast<double>(pos), f.inv_freq[i0 + e]), &s64, &c64);
-#pragma unroll
-      for (int p = 0; p < 8; ++p)
-        if (p == e) {
-          c[p] = static_cast<float>(c64);
-          sn[p] = static_cast<float>(s64);
-        }
-    }
-  }
-  uint32_t bad = 0, o1[4], o2[4];
+// RoPE of the 8 pairs (x1, x2) = dims (8 q + p, 32 + 8 q + p) of a row: x1, x2 become
+// bf16 values at or below the rotated ones, y1, y2 at or above them (mostly the same:
+// one pair in 500 differs, where its values cancel or one is much larger).  Returns
+// bits of the pairs that have to be done again.  turn: their (cos, sin) in shared
+// memory.
+__device__ __forceinline__ uint32_t rotate8(uint32_t turn, uint4& x1, uint4& x2, uint4& y1,
+                                            uint4& y2) {
+  const uint32_t a[4] = {x1.x, x1.y, x1.z, x1.w}, b[4] = {x2.x, x2.y, x2.z, x2.w};
+  uint32_t again = 0, l1[4], l2[4], h1[4], h2[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float y1[2], y2[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int p = 2 * e + h;
-      const float u = __uint_as_float(h ? (a[e] & 0xFFFF0000u) : (a[e] << 16));
-      const float v = __uint_as_float(h ? (b[e] & 0xFFFF0000u) : (b[e] << 16));
-      y1[h] = fmaf(u, c[p], -(v * sn[p]));
-      y2[h] = fmaf(v, c[p], u * sn[p]);
-      const float s0 = fabsf(u) + fabsf(v);
-      const float m1 = s0 + fabsf(y1[h]), m2 = s0 + fabsf(y2[h]);
-      const uint32_t lo = cvt_bf16x2_rn(fmaf(m1, -0x1p-22f, y1[h]), fmaf(m2, -0x1p-22f, y2[h]));
-      const uint32_t hi = cvt_bf16x2_rn(fmaf(m1, 0x1p-22f, y1[h]), fmaf(m2, 0x1p-22f, y2[h]));
-      // 2^-100 <= s0 <= 2^100
-      const bool in_range = __float_as_uint(s0) - 0x0D800000u <= 0x71800000u - 0x0D800000u;
-      if (lo != hi || !in_range) bad |= 1u << p;
-    }
-    o1[e] = cvt_bf16x2_rn(y1[0], y1[1]);
-    o2[e] = cvt_bf16x2_rn(y2[0], y2[1]);
+    const uint4 w = lds128(turn + 16 * e);
+    bool odd[2];
+    const float2 u = bf16x2_to_float2(a[e]), v = bf16x2_to_float2(b[e]);
+    const uint2 y0 = rotate_fast(u.x, v.x, __uint_as_float(w.x), __uint_as_float(w.y), odd[0]);
+    const uint2 z0 = rotate_fast(u.y, v.y, __uint_as_float(w.z), __uint_as_float(w.w), odd[1]);
+    if (odd[0]) again |= 1u << (2 * e);
+    if (odd[1]) again |= 2u << (2 * e);
+    l1[e] = prmt(y0.x, z0.x, 0x5410u);
+    l2[e] = prmt(y0.x, z0.x, 0x7632u);
+    h1[e] = prmt(y0.y, z0.y, 0x5410u);
+    h2[e] = prmt(y0.y, z0.y, 0x7632u);
   }
-  while (bad != 0) {
-    const int p = __ffs(bad) - 1;
-    bad &= bad - 1;
-    uint32_t wa = 0, wb = 0;
+  x1 = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+  x2 = make_uint4(l2[0], l2[1], l2[2], l2[3]);
+  y1 = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+  y2 = make_uint4(h2[0], h2[1], h2[2], h2[3]);
+  return again;
+}
+
+// Bits of the pairs whose bounds differ.
+__device__ __forceinline__ uint32_t pairs_apart(const uint4& x1, const uint4& x2, const uint4& y1,
+                                                const uint4& y2) {
+  const uint32_t d[4] = {(x1.x ^ y1.x) | (x2.x ^ y2.x), (x1.y ^ y1.y) | (x2.y ^ y2.y),
+                         (x1.z ^ y1.z) | (x2.z ^ y2.z), (x1.w ^ y1.w) | (x2.w ^ y2.w)};
+  uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e == p >> 1) {
-        wa = a[e];
-        wb = b[e];
-      }
-    const int sh = 16 * (p & 1);
-    double c64, s64;
-    if (table_ok) {
-      const double2 t = f.table64[pos * kHalf + i0 + p];
-      c64 = t.x;
-      s64 = t.y;
-    } else {
-      sincos(__dmul_rn(static_cast<double>(pos), f.inv_freq[i0 + p]), &s64, &c64);
-    }
+  for (int e = 0; e < 4; ++e) {
+    if ((d[e] & 0xFFFFu) != 0u) m |= 1u << (2 * e);
+    if ((d[e] >> 16) != 0u) m |= 2u << (2 * e);
+  }
+  return m;
+}
+
+// The pairs `bad` of a row again, exactly, from shared memory (the row's x1 at `row`,
+// x2 64 bytes on; what the angles' floats leave `left` bytes behind them) and through
+// it, by an index that is each lane's own: words picked so would go to memory.
+__device__ __forceinline__ void rotate_again(uint32_t bad, const double* inv_freq, uint32_t row,
+                                             uint32_t turn, uint32_t left, int pos, uint4& x1,
+                                             uint4& x2) {
+  for (uint32_t rest = bad; rest != 0; rest &= rest - 1) {
+    const int p = __ffs(rest) - 1;
+    const uint2 hi = lds64(turn + 8 * p), lo = lds64(turn + left + 8 * p);
+    const Angle t = {__uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(lo.x),
+                     __uint_as_float(lo.y)};
     uint16_t y1, y2;
-    rotate_pair(static_cast<uint16_t>(wa >> sh), static_cast<uint16_t>(wb >> sh), c64, s64, &y1,
-                &y2);
+    rotate_carefully(lds16(row + 2 * p), lds16(row + 64 + 2 * p), t,
+                     __dmul_rn(static_cast<double>(pos), inv_freq[p]), &y1, &y2);
+    sts16(row + 2 * p, y1);
+    sts16(row + 64 + 2 * p, y2);
+  }
+  const uint4 c1 = lds128(row), c2 = lds128(row + 64);
+  const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w}, w2[4] = {c2.x, c2.y, c2.z, c2.w};
+  uint32_t o1[4] = {x1.x, x1.y, x1.z, x1.w}, o2[4] = {x2.x, x2.y, x2.z, x2.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e == p >> 1) {
-        o1[e] = (o1[e] & ~(0xFFFFu << sh)) | (static_cast<uint32_t>(y1) << sh);
-        o2[e] = (o2[e] & ~(0xFFFFu << sh)) | (static_cast<uint32_t>(y2) << sh);
-      }
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t m = ((bad >> (2 * e)) & 1u ? 0xFFFFu : 0u) |
+                       ((bad >> (2 * e)) & 2u ? 0xFFFF0000u : 0u);
+    o1[e] = (o1[e] & ~m) | (w1[e] & m);
+    o2[e] = (o2[e] & ~m) | (w2[e] & m);
   }
   x1 = make_uint4(o1[0], o1[1], o1[2], o1[3]);
   x2 = make_uint4(o2[0], o2[1], o2[2], o2[3]);
 }
 
-// Zero the values of 8 that are not finite; true when there were some.
-__device__ __forceinline__ bool drop_nonfinite(uint4& x) {
-  const uint32_t m0 = nonfinite_halves(x.x), m1 = nonfinite_halves(x.y),
-                 m2 = nonfinite_halves(x.z), m3 = nonfinite_halves(x.w);
-  x = make_uint4(x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
-  return (m0 | m1 | m2 | m3) != 0u;
+// Zero the values of 8 that are not finite.
+__device__ __forceinline__ void drop_nonfinite(uint4& x) {
+  x = make_uint4(x.x & ~nonfinite_halves(x.x), x.y & ~nonfinite_halves(x.y),
+                 x.z & ~nonfinite_halves(x.z), x.w & ~nonfinite_halves(x.w));
 }
 
 // The larger magnitude of each half, over the words.
@@ -315,84 +431,252 @@ __device__ __forceinline__ uint32_t top_halves(uint32_t top, const uint4& x) {
 
 template <int kFmt>
 __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
-  const float2 a = bf16x2_to_float2(x.x), b = bf16x2_to_float2(x.y), c = bf16x2_to_float2(x.z),
-               d = bf16x2_to_float2(x.w);
-  return make_uint2(encode4<kFmt>(a.x * f, a.y * f, b.x * f, b.y * f),
-                    encode4<kFmt>(c.x * f, c.y * f, d.x * f, d.y * f));
+  const float2 f2 = make_float2(f, f);
+  const float2 a = fmul2(bf16x2_to_float2(x.x), f2), b = fmul2(bf16x2_to_float2(x.y), f2),
+               c = fmul2(bf16x2_to_float2(x.z), f2), d = fmul2(bf16x2_to_float2(x.w), f2);
+  return make_uint2(encode4<kFmt>(a.x, a.y, b.x, b.y), encode4<kFmt>(c.x, c.y, d.x, d.y));
 }
 
-// Warp h of a CTA takes the K and the V block of kv head h of a unit: lane 4 r +
-// q holds dims [8 q, 8 q + 8) and [32 + 8 q, 32 + 8 q + 8) of slots r and r + 8.
+// Ragged prompts: a CTA brings its units' rows of k and v (16 KiB each, in a row)
+// into a ring of two stages in shared memory, so the next unit's are on their way
+// while one is rotated and rounded; the angles of its 16 positions are a 4 KiB row of
+// the tables each, or evaluated once for all heads.  Warp h takes the K and the V block of kv head h:
+// lane 4 r + q holds dims [8 q, 8 q + 8) and [32 + 8 q, 32 + 8 q + 8) of slots r and r +
+// 8 (odd r their other half first: a phase of 8 lanes then covers all banks).
+constexpr int kWriteStages = 2, kWriteCtas = 3;
+constexpr int kTokenBytes = kNumKvHeads * kHeadDim * 2;        // a row of k or v
+constexpr int kHalfStage = kPageSize * kTokenBytes;            // 16 KiB
+constexpr int kTurnRow = kHalf + 4;  // (cos, sin) of a position, and padding: two positions a phase
+constexpr int kTurnBytes = kPageSize * kTurnRow * 8;
+constexpr int kOffTurn = kWriteStages * 2 * kHalfStage;  // [16] (cos, sin), then what they leave
+constexpr int kOffWriteBars = kOffTurn + 2 * kTurnBytes;  // the stages', the angles'
+constexpr size_t kWriteSmem = kOffWriteBars + 8 * (kWriteStages + 1);
+static_assert(kWriteCtas * (kWriteSmem + 1024) <= 228 * 1024, "the CTAs of an SM fit");
+
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kWriteCtas)
     kv8_write_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                      int num_tokens, const int32_t* __restrict__ off,
-                     const int32_t* __restrict__ starts, const Kv8 c, RopeFreqs freqs,
-                     int32_t* dev_err) {
-  const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
+                     const int32_t* __restrict__ starts, const Kv8 c,
+                     const __grid_constant__ RopeFreqs freqs, int32_t* dev_err,
+                     unsigned long long wait_ns) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
   const int r = lane >> 2, q = lane & 3;
+  const uint32_t sb = smem_addr(smem);
+  float2* turn = reinterpret_cast<float2*>(smem + kOffTurn);
+  if (tid == 0) {
+    for (int s = 0; s <= kWriteStages; ++s) mbar_init(sb + kOffWriteBars + 8 * s, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
   wait_for_prior_grids();
   allow_dependent_grids();
   check_ends(c, off, num_tokens, dev_err);
   const bool tag_ok = rope_table_ready(freqs);
-  const int64_t units = unit_count(num_tokens, c.batch);
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit t = find_unit(u, c, off, starts, num_tokens, dev_err, h == 0, lane);
-    if (t.b < 0) continue;
-    uint4 x[2][2][2];  // [K|V][slot r, r + 8][dims 8 q, 32 + 8 q]
-    bool in[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int slot = r + 8 * s;
-      in[s] = slot >= t.s0 && slot < t.s1;
-      const int64_t at = (t.row0 + slot) * (kNumKvHeads * kHeadDim) + h * kHeadDim + 8 * q;
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        x[0][s][d] = x[1][s][d] = make_uint4(0u, 0u, 0u, 0u);
-        if (in[s]) {
-          x[0][s][d] = __ldcs(reinterpret_cast<const uint4*>(k + at + kHalf * d));
-          x[1][s][d] = __ldcs(reinterpret_cast<const uint4*>(v + at + kHalf * d));
+  const Share share(unit_count(num_tokens, c.batch));
+  const uint64_t policy = l2_policy_evict_first();
+  const uint32_t turn_bar = sb + kOffWriteBars + 8 * kWriteStages;
+  int issued = 0, done = 0;  // units whose rows were asked for, units written
+  int turns = 0;             // copies of angles asked for
+  auto is_near = [&](const Unit& t) {
+    return tag_ok && (t.page + 1) * kPageSize <= kRopeTablePositions;
+  };
+  bool ok = true;
+  for (int64_t u0 = share.u0; ok && u0 < share.u1; u0 += 32) {
+    const Unit mine =
+        find_unit(u0 + lane, share.u1, c, off, starts, num_tokens, dev_err, h == 0);
+    // the units there are, in order; the same in every warp
+    unsigned todo = __ballot_sync(kFull, mine.pool_page >= 0), ahead = todo;
+    auto ask = [&]() {  // the next unit's rows into the next stage
+      if (ahead == 0) return;
+      const Unit t = unit_of(mine, __ffs(ahead) - 1);
+      ahead &= ahead - 1;
+      if (tid == 0) {
+        const int st = issued % kWriteStages;
+        const uint32_t bar = sb + kOffWriteBars + 8 * st, dst = sb + st * 2 * kHalfStage;
+        const uint32_t bytes = (t.s1 - t.s0) * kTokenBytes;
+        const int64_t at = (t.row0 + t.s0) * (kTokenBytes / 2);
+        mbar_arrive_expect_tx(bar, 2 * bytes);
+        bulk_load(dst + t.s0 * kTokenBytes, k + at, bytes, bar, policy);
+        bulk_load(dst + kHalfStage + t.s0 * kTokenBytes, v + at, bytes, bar, policy);
+      }
+      ++issued;
+    };
+    auto ask_turn = [&]() {  // the angles of the next unit to be written
+      if (todo == 0) return;
+      const Unit t = unit_of(mine, __ffs(todo) - 1);
+      if (!is_near(t)) return;
+      if (h == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(turn_bar, 2 * kPageSize * kHalf * 8);
+        __syncwarp();
+        const int row = lane % kPageSize;
+        bulk_load(sb + kOffTurn + lane * kTurnRow * 8,
+                  (lane < kPageSize ? freqs.table32 : freqs.table_lo) +
+                      (static_cast<int64_t>(t.page) * kPageSize + row) * kHalf,
+                  kHalf * 8, turn_bar, policy);
+      }
+      ++turns;
+    };
+    for (int s = 0; s < kWriteStages; ++s) ask();
+    ask_turn();
+    while (todo != 0) {
+      const Unit t = unit_of(mine, __ffs(todo) - 1);
+      todo &= todo - 1;
+      const int st = done % kWriteStages;
+      const int pos0 = t.page * kPageSize;
+      const bool near = is_near(t);
+      if (!near) {
+        for (int i = tid; i < kPageSize * kHalf; i += kThreads) {
+          const int pos = pos0 + i / kHalf, p = i % kHalf;
+          double s64, c64;
+          sincos(__dmul_rn(static_cast<double>(pos), freqs.inv_freq[p]), &s64, &c64);
+          const Angle t2 = make_angle(c64, s64);
+          const int at = i / kHalf * kTurnRow + p;
+          turn[at] = make_float2(t2.c, t2.s);
+          turn[kPageSize * kTurnRow + at] = make_float2(t2.c_lo, t2.s_lo);
         }
       }
-    }
+      const uint32_t old_k = t.s0 > 0 ? c.scales[scale_at(t.pool_page, 0, h)] : 0u;
+      const uint32_t old_v = t.s0 > 0 ? c.scales[scale_at(t.pool_page, 1, h)] : 0u;
+      const bool ready = mbar_wait_bounded(sb + kOffWriteBars + 8 * st,
+                                           (done / kWriteStages) & 1, wait_ns);
+      ok = __syncthreads_and(ready) != 0;  // (the same in every thread)
+      if (!ok) break;
+      ++done;
+      const uint32_t rows = sb + st * 2 * kHalfStage + h * (kHeadDim * 2) + 16 * q;
+      uint4 x[2][2];  // [slot r, r + 8][dims 8 q, 32 + 8 q]
+      auto load = [&](uint32_t at) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int pos = t.page * kPageSize + r + 8 * s;
-      if (in[s]) rotate8(freqs, tag_ok && pos < kRopeTablePositions, pos, q, x[0][s][0], x[0][s][1]);
-    }
-    bool dropped = false;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          dropped |= drop_nonfinite(x[kv][s][d]);
-          top = top_halves(top, x[kv][s][d]);
+        for (int s = 0; s < 2; ++s) {
+          const bool in = r + 8 * s >= t.s0 && r + 8 * s < t.s1;
+          const uint32_t row = at + (r + 8 * s) * kTokenBytes;
+          const uint4 y = lds128(row + 64 * (r & 1)), z = lds128(row + 64 * (~r & 1));
+          const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+          x[s][0] = !in ? none : r & 1 ? z : y;
+          x[s][1] = !in ? none : r & 1 ? y : z;
         }
-      top = __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16));
-      const uint32_t old =
-          t.s0 > 0 ? stored_scale(c.scales[scale_at(t.pool_page, kv, h)]) : 0u;
-      const uint32_t e = settle_scale<kFmt>(c, t.pool_page, kv, h, top, t.s0, old, lane);
-      const float f = scale_inverse(e);
-      uint8_t* block = c.pool + block_at(t.pool_page, kv, h);
+      };
+      // the largest magnitude, values that are not finite left out
+      auto largest = [&](uint4 (&y)[2][2]) {
+        auto top_of = [&]() {
+          uint32_t top = 0;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (in[s])
+          for (int s = 0; s < 2; ++s) top = top_halves(top_halves(top, y[s][0]), y[s][1]);
+          return __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16));
+        };
+        const uint32_t top = top_of();
+        if (top < 0x7F80u) return top;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          drop_nonfinite(y[s][0]);
+          drop_nonfinite(y[s][1]);
+        }
+        if (lane == 0) record_error(dev_err, kErrValue);
+        return top_of();
+      };
+      auto put = [&](int kv, uint32_t top, uint32_t old, const uint2 (&codes)[2][2]) {
+        settle_scale<kFmt>(c, t.pool_page, kv, h, top, t.s0, old, lane);
+        uint8_t* block = c.pool + block_at(t.pool_page, kv, h) + 8 * q;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int slot = r + 8 * s;
+          if (slot < t.s0 || slot >= t.s1) continue;
 #pragma unroll
           for (int d = 0; d < 2; ++d)
-            *reinterpret_cast<uint2*>(block + (r + 8 * s) * kHeadDim + kHalf * d + 8 * q) =
-                encode8<kFmt>(x[kv][s][d], f);
+            *reinterpret_cast<uint2*>(block + slot * kHeadDim + kHalf * d) = codes[s][d];
+        }
+      };
+      // the block's scale, once `top` has come to it
+      auto scale_for = [&](uint32_t top, uint32_t old) {
+        const uint32_t e = needed_scale<kFmt>(top);
+        return t.s0 > 0 ? max(e, old) : e;
+      };
+      auto encode = [&](const uint4 (&y)[2][2], float f, uint2 (&codes)[2][2]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int d = 0; d < 2; ++d) codes[s][d] = encode8<kFmt>(y[s][d], f);
+      };
+      uint2 codes[2][2];
+      {
+        load(rows + kHalfStage);
+        const uint32_t top = largest(x), old = stored_scale(old_v);
+        encode(x, scale_inverse(scale_for(top, old)), codes);
+        put(1, top, old, codes);
+      }
+      load(rows);
+      const bool turned = !near || mbar_wait_bounded(turn_bar, (turns - 1) & 1, wait_ns);
+      ok = __syncthreads_and(turned) != 0;  // (and the angles evaluated above are there)
+      if (!ok) break;
+      // Bounds x, y of the rotated keys, which give the same codes but for a key in a
+      // few ten thousand.  (Deciding each of them exactly took 84 us for 64 prompts of
+      // up to 2047 tokens, with FP64, whose rate here is a small fraction of FP32's,
+      // 119; not at all 64.)
+      uint4 y[2][2];
+      auto again = [&](int s, uint32_t bad) {
+        const int slot = r + 8 * s;
+        rotate_again(bad, freqs.inv_freq + 8 * q, rows + slot * kTokenBytes,
+                     sb + kOffTurn + (slot * kTurnRow + 8 * q) * 8, kTurnBytes, pos0 + slot,
+                     x[s][0], x[s][1]);
+        y[s][0] = x[s][0];
+        y[s][1] = x[s][1];
+      };
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t odd = rotate8(sb + kOffTurn + ((r + 8 * s) * kTurnRow + 8 * q) * 8, x[s][0],
+                                     x[s][1], y[s][0], y[s][1]);
+        if (odd != 0) again(s, odd);
+      }
+      uint32_t top = largest(x);
+      const uint32_t old = stored_scale(old_k);
+      uint32_t apart[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) apart[s] = pairs_apart(x[s][0], x[s][1], y[s][0], y[s][1]);
+      if (__any_sync(kFull, (apart[0] | apart[1]) != 0)) {
+        bool differ = needed_scale<kFmt>(largest(y)) != needed_scale<kFmt>(top);  // (all lanes)
+        if (!differ) {
+          uint2 z[2][2];
+          const float f = scale_inverse(scale_for(top, old));
+          encode(x, f, codes);
+          encode(y, f, z);
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              differ |= ((codes[s][d].x ^ z[s][d].x) | (codes[s][d].y ^ z[s][d].y)) != 0u;
+        }
+        if (differ) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (apart[s] != 0) again(s, apart[s]);
+        }
+        __syncwarp();
+        top = largest(x);
+      }
+      encode(x, scale_inverse(scale_for(top, old)), codes);
+      put(0, top, old, codes);
+      fence_proxy_async_smem();
+      __syncthreads();  // the stage can be filled again, the angles replaced
+      ask();
+      ask_turn();
     }
-    if (dropped) record_error(dev_err, kErrValue);
+  }
+  if (!ok && tid == 0) record_error(dev_err, kErrTimeout);
+  // every copy asked for has landed before the CTA ends (full limit)
+  if (tid == 0) {
+    for (int j = issued > kWriteStages ? issued - kWriteStages : 0; j < issued; ++j)
+      mbar_wait_bounded(sb + kOffWriteBars + 8 * (j % kWriteStages), (j / kWriteStages) & 1);
+    if (turns > 0) mbar_wait_bounded(turn_bar, (turns - 1) & 1);
   }
 }
 
-// Warp h of a CTA reads the K and the V block of kv head h of a unit: lane 4 r +
-// q holds dims [16 q, 16 q + 16) of slots r and r + 8.
+// Warp h of a CTA reads the K and the V block of kv head h of its units, the next
+// one's codes on their way: lane 4 r + q holds dims [16 q, 16 q + 16) of slots r and
+// r + 8.
+constexpr int kReadCtas = 4;
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kReadCtas)
     kv8_read_kernel(uint16_t* __restrict__ k, uint16_t* __restrict__ v, int num_tokens,
                     const int32_t* __restrict__ off, const int32_t* __restrict__ starts,
                     const Kv8 c, int32_t* dev_err) {
@@ -401,31 +685,38 @@ __global__ void __launch_bounds__(kThreads)
   wait_for_prior_grids();
   allow_dependent_grids();
   check_ends(c, off, num_tokens, dev_err);
-  const int64_t units = unit_count(num_tokens, c.batch);
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit t = find_unit(u, c, off, starts, num_tokens, dev_err, h == 0, lane);
-    if (t.b < 0) continue;
-    uint4 w[2][2];
-    bool in[2];
+  const Share share(unit_count(num_tokens, c.batch));
+  for (int64_t u0 = share.u0; u0 < share.u1; u0 += 32) {
+    const Unit mine =
+        find_unit(u0 + lane, share.u1, c, off, starts, num_tokens, dev_err, h == 0);
+    unsigned todo = __ballot_sync(kFull, mine.pool_page >= 0);
+    uint4 w[2][2];  // [K|V][slot r, r + 8]
+    uint32_t e[2];
+    auto load = [&](int src) {
+      const int64_t page = __shfl_sync(kFull, mine.pool_page, src);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      in[s] = r + 8 * s >= t.s0 && r + 8 * s < t.s1;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
-        if (in[s])
-          w[kv][s] = __ldcs(reinterpret_cast<const uint4*>(c.pool + block_at(t.pool_page, kv, h)) +
-                            lane + 32 * s);
-    }
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const float f = scale_value(stored_scale(c.scales[scale_at(t.pool_page, kv, h)]));
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint4* at = reinterpret_cast<const uint4*>(c.pool + block_at(page, kv, h)) + lane;
+        w[kv][0] = __ldcs(at);
+        w[kv][1] = __ldcs(at + 32);
+        e[kv] = c.scales[scale_at(page, kv, h)];
+      }
+    };
+    if (todo != 0) load(__ffs(todo) - 1);
+    while (todo != 0) {
+      const Unit t = unit_of(mine, __ffs(todo) - 1);
+      todo &= todo - 1;
+      const uint4 x[2][2] = {{w[0][0], w[0][1]}, {w[1][0], w[1][1]}};
+      const float f[2] = {scale_value(stored_scale(e[0])), scale_value(stored_scale(e[1]))};
+      if (todo != 0) load(__ffs(todo) - 1);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        if (!in[s]) continue;
-        widen16<kFmt>(w[kv][s], f,
-                      reinterpret_cast<uint4*>((kv == 0 ? k : v) +
-                                               (t.row0 + r + 8 * s) * (kNumKvHeads * kHeadDim) +
-                                               h * kHeadDim + 16 * q));
+        const int slot = r + 8 * s;
+        if (slot < t.s0 || slot >= t.s1) continue;
+        const int64_t at =
+            (t.row0 + slot) * (kNumKvHeads * kHeadDim) + h * kHeadDim + 16 * q;
+        widen16<kFmt>(x[0][s], f[0], reinterpret_cast<uint4*>(k + at));
+        widen16<kFmt>(x[1][s], f[1], reinterpret_cast<uint4*>(v + at));
       }
     }
   }
@@ -434,6 +725,28 @@ __global__ void __launch_bounds__(kThreads)
 int unit_grid(int num_tokens, int batch, int num_sms, int per_sm) {
   return static_cast<int>(std::min<int64_t>(unit_count(num_tokens, batch),
                                             static_cast<int64_t>(num_sms) * per_sm));
+}
+
+template <int kFmt>
+cudaError_t launch_write(const uint16_t* k, const uint16_t* v, int num_tokens,
+                         const int32_t* token_offsets, const int32_t* start_positions,
+                         const Kv8& cache, const RopeFreqs& freqs, int num_sms, int32_t* dev_err,
+                         cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    err = cudaFuncSetAttribute(kv8_write_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kWriteSmem));
+    if (err != cudaSuccess) return err;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_pdl(kv8_write_kernel<kFmt>,
+                    dim3(unit_grid(num_tokens, cache.batch, num_sms, kWriteCtas)), dim3(kThreads),
+                    kWriteSmem, stream, k, v, num_tokens, token_offsets, start_positions, cache,
+                    freqs, dev_err, wait_limit_ns());
 }
 
 }  // namespace
@@ -452,10 +765,11 @@ cudaError_t launch_kv8_write(const uint16_t* k, const uint16_t* v, int num_token
                              const int32_t* token_offsets, const int32_t* start_positions,
                              const Kv8& cache, const RopeFreqs& freqs, int num_sms,
                              int32_t* dev_err, cudaStream_t stream) {
-  return launch_pdl(
-      cache.format == kKv8E4m3 ? kv8_write_kernel<kKv8E4m3> : kv8_write_kernel<kKv8Int8>,
-      dim3(unit_grid(num_tokens, cache.batch, num_sms, 8)), dim3(kThreads), 0, stream, k, v,
-      num_tokens, token_offsets, start_positions, cache, freqs, dev_err);
+  return cache.format == kKv8E4m3
+             ? launch_write<kKv8E4m3>(k, v, num_tokens, token_offsets, start_positions, cache,
+                                      freqs, num_sms, dev_err, stream)
+             : launch_write<kKv8Int8>(k, v, num_tokens, token_offsets, start_positions, cache,
+                                      freqs, num_sms, dev_err, stream);
 }
 
 cudaError_t launch_kv8_read(uint16_t* k, uint16_t* v, int num_tokens,
@@ -463,8 +777,8 @@ cudaError_t launch_kv8_read(uint16_t* k, uint16_t* v, int num_tokens,
                             const Kv8& cache, int num_sms, int32_t* dev_err, cudaStream_t stream) {
   return launch_pdl(
       cache.format == kKv8E4m3 ? kv8_read_kernel<kKv8E4m3> : kv8_read_kernel<kKv8Int8>,
-      dim3(unit_grid(num_tokens, cache.batch, num_sms, 8)), dim3(kThreads), 0, stream, k, v,
-      num_tokens, token_offsets, start_positions, cache, dev_err);
+      dim3(unit_grid(num_tokens, cache.batch, num_sms, kReadCtas)), dim3(kThreads), 0, stream, k,
+      v, num_tokens, token_offsets, start_positions, cache, dev_err);
 }
 
 }  // namespace pkv

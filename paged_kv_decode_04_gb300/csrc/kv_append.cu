@@ -40,6 +40,7 @@ constexpr int kRopeEntries = kRopeTablePositions * kHalf;
 // theta evaluate sincos in the kernels (the same values).
 constexpr int kRopeSlots = 4;
 __device__ __align__(16) float2 g_rope32[kRopeSlots][kRopeEntries];
+__device__ __align__(16) float2 g_rope_lo[kRopeSlots][kRopeEntries];
 __device__ __align__(16) double2 g_rope64[kRopeSlots][kRopeEntries];
 __device__ double g_rope_theta[kRopeSlots];
 
@@ -52,7 +53,10 @@ __global__ void __launch_bounds__(256) rope_table_kernel(RopeFreqs f, int slot) 
   double sn, cs;
   sincos(__dmul_rn(static_cast<double>(pos), f.inv_freq[i]), &sn, &cs);
   g_rope64[slot][e] = make_double2(cs, sn);
-  g_rope32[slot][e] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
+  const float2 hi = make_float2(static_cast<float>(cs), static_cast<float>(sn));
+  g_rope32[slot][e] = hi;
+  g_rope_lo[slot][e] = make_float2(static_cast<float>(__dsub_rn(cs, static_cast<double>(hi.x))),
+                                   static_cast<float>(__dsub_rn(sn, static_cast<double>(hi.y))));
 }
 
 // One CTA per sequence, thread (h, i) rotates pair i of kv head h (and of
@@ -443,6 +447,7 @@ __global__ void __launch_bounds__(kPfThreads)
 // and the theta each slot was given (NaN: free).
 struct RopeTableAddrs {
   float2* t32 = nullptr;
+  float2* tlo = nullptr;
   double2* t64 = nullptr;
   double* theta = nullptr;
   double slot_theta[kRopeSlots] = {NAN, NAN, NAN, NAN};
@@ -458,6 +463,7 @@ cudaError_t prepare_rope(double theta, RopeFreqs* f, cudaStream_t stream) {
     f->inv_freq[i] = pow(theta, -(2.0 * i) / static_cast<double>(kHeadDim));
   f->theta = theta;
   f->table32 = nullptr;
+  f->table_lo = nullptr;
   f->table64 = nullptr;
   f->table_theta = nullptr;
   int dev = 0;
@@ -467,13 +473,15 @@ cudaError_t prepare_rope(double theta, RopeFreqs* f, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_rope_mutex);
   RopeTableAddrs& a = g_rope_addrs[dev];
   if (a.t32 == nullptr) {
-    void *p32 = nullptr, *p64 = nullptr, *pt = nullptr;
+    void *p32 = nullptr, *plo = nullptr, *p64 = nullptr, *pt = nullptr;
     if ((err = cudaGetSymbolAddress(&p32, g_rope32)) != cudaSuccess) return err;
+    if ((err = cudaGetSymbolAddress(&plo, g_rope_lo)) != cudaSuccess) return err;
     if ((err = cudaGetSymbolAddress(&p64, g_rope64)) != cudaSuccess) return err;
     if ((err = cudaGetSymbolAddress(&pt, g_rope_theta)) != cudaSuccess) return err;
-    a.t32 = static_cast<float2*>(p32);
+    a.tlo = static_cast<float2*>(plo);
     a.t64 = static_cast<double2*>(p64);
     a.theta = static_cast<double*>(pt);
+    a.t32 = static_cast<float2*>(p32);
   }
   int slot = -1;
   for (int s = 0; s < kRopeSlots && slot < 0; ++s)
@@ -490,6 +498,7 @@ cudaError_t prepare_rope(double theta, RopeFreqs* f, cudaStream_t stream) {
     a.slot_theta[slot] = theta;
   }
   f->table32 = a.t32 + static_cast<size_t>(slot) * kRopeEntries;
+  f->table_lo = a.tlo + static_cast<size_t>(slot) * kRopeEntries;
   f->table64 = a.t64 + static_cast<size_t>(slot) * kRopeEntries;
   f->table_theta = a.theta + slot;
   return cudaSuccess;

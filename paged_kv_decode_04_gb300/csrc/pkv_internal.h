@@ -99,6 +99,7 @@ struct RopeFreqs {
   double inv_freq[32];
   double theta;
   const float2* table32;     // [pos][i] (cos, sin) rounded to float
+  const float2* table_lo;    // [pos][i] what that rounding left, rounded to float
   const double2* table64;    // [pos][i] (cos, sin)
   const double* table_theta; // theta the table holds
 };

@@ -21,6 +21,11 @@ struct Visible {
     n = L > 0 ? ns + (L + kPageSize - 1) / kPageSize - w0 : 0;
   }
   __device__ __forceinline__ int page(int k) const { return k < ns ? k : w0 + (k - ns); }
+  // Is every slot of the page seen?
+  __device__ __forceinline__ bool whole(int page) const {
+    const int base = page * kPageSize;
+    return base + kPageSize <= L && (base >= lo || base + kPageSize <= sinks);
+  }
   // Bits of the page's slots that are seen.
   __device__ __forceinline__ uint32_t mask(int page) const {
     auto below = [](int x) { return x <= 0 ? 0u : (x >= kPageSize ? 0xFFFFu : (1u << x) - 1u); };
