@@ -52,19 +52,21 @@ __device__ __forceinline__ uint32_t needed_scale(uint32_t bits) {
   return static_cast<uint32_t>(min(max(s, kLeastScale), kMostScale));
 }
 
-// Four values (already divided by the scale) as codes, the first in the low
-// byte; past the largest code (scales end at 240) they saturate.
-template <int kFmt>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+// Four values times f (the scale's inverse; exact products) as codes, the first in
+// the low byte.  Past the largest code (scales end at 240) e4m3 codes saturate;
+// integers do where kClamp.
+template <int kFmt, bool kClamp>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float f) {
   if constexpr (kFmt == kKv8E4m3) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * f), "f"(a * f));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * f), "f"(c * f));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   } else {
-    // 1.5 x 2^23 + y holds y, rounded to nearest even, in its low bits
-    auto code = [](float y) {
-      return __float_as_uint(fminf(fmaxf(y, -127.f), 127.f) + 12582912.f);
+    // 1.5 x 2^23 + y holds y, rounded once to nearest even, in its low bits
+    auto code = [f](float y) {
+      return __float_as_uint(kClamp ? fminf(fmaxf(y * f, -127.f), 127.f) + 12582912.f
+                                    : fmaf(y, f, 12582912.f));
     };
     return prmt(prmt(code(a), code(b), 0x0040u), prmt(code(c), code(d), 0x0040u), 0x5410u);
   }
@@ -154,7 +156,7 @@ __device__ __forceinline__ void rescale_rows(uint8_t* block, int rows, uint32_t 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = decode4<kFmt>(x[i]);
-      x[i] = encode4<kFmt>(v.x * f, v.y * f, v.z * f, v.w * f);
+      x[i] = encode4<kFmt, false>(v.x, v.y, v.z, v.w, f);
     }
     *at = w;
   }

@@ -33,16 +33,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
 
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  unsigned long long ra, rb, rd;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
-  return d;
-}
-
 // (cos, sin) of a rotation, as floats and what they leave.
 struct Angle {
   float c, s, c_lo, s_lo;
@@ -112,23 +102,13 @@ __device__ __forceinline__ void rotate_carefully(uint32_t h1, uint32_t h2, const
   }
 }
 
-// FP32 rotation of a pair with a bound on its error: bf16 pairs (y1 in the low half)
-// at and below, and at and above, rotate_pair's.  y is off by at most 3 x 2^-24 (|x1|
-// + |x2|): 2^-24 of both factors for cos and sin, of one product, and of y, |y| <= |x1|
-// + |x2|; y - A and y + A, A = 1.125 x 2^-22 (|x1| + |x2|), are off by another 2^-24 of
-// that, so they enclose the FP64 value.  `odd`: too small, too large or not finite for
-// that.
-__device__ __forceinline__ uint2 rotate_fast(float u, float v, float c, float s, bool& odd) {
-  const float2 t = fmul2(make_float2(v, u), make_float2(-s, s));
-  const float2 y = ffma2(make_float2(u, v), make_float2(c, c), t);
-  const float s0 = fabsf(u) + fabsf(v), A = s0 * 0x1.2p-22f;
-  // (zeros keep their sign: y itself both times)
-  const float2 l = fadd2(y, make_float2(-A, -A)), r = fadd2(y, make_float2(A, A));
-  const uint32_t lo = cvt_bf16x2_rn(l.x, l.y);
-  // 2^-70 <= s0 <= 2^100, or zeros
-  odd = __float_as_uint(s0) - 0x1C800000u > 0x71800000u - 0x1C800000u && s0 != 0.f;
-  return make_uint2(lo, s0 == 0.f ? lo : cvt_bf16x2_rn(r.x, r.y));
-}
+// FP32 rotation (a c + b s) with a bound on its error: values at and below, and at
+// and above, the FP64 one.  y is off by at most 3 x 2^-24 (|a| + |b|): 2^-24 of both
+// factors for cos and sin, of one product, and of y, |y| <= |a| + |b|; y - A and y + A,
+// A = 1.125 x 2^-22 (|a| + |b|), are off by another 2^-24 of that.  For |a| + |b| in
+// [2^-70, 2^100].
+constexpr float kTurnBound = 0x1.2p-22f;
+constexpr uint32_t kTiny = (127u - 60u) << 7, kHuge = (127u + 99u) << 7;  // bf16 2^-60, 2^99
 
 // A warp stores the largest magnitude's scale of a block that holds `earlier`
 // tokens already, whose codes follow it, and returns the scale.
@@ -205,11 +185,13 @@ __global__ void __launch_bounds__(kThreads)
     t = make_angle(c64, s64);
   }
   auto rotate = [&](uint16_t x1, uint16_t x2, uint16_t* y1, uint16_t* y2) {
-    bool odd;
-    const uint2 y = rotate_fast(bf16_to_float(x1), bf16_to_float(x2), t.c, t.s, odd);
-    *y1 = static_cast<uint16_t>(y.x);
-    *y2 = static_cast<uint16_t>(y.x >> 16);
-    if (odd || y.x != y.y) rotate_carefully(x1, x2, t, angle, y1, y2);
+    const float u = bf16_to_float(x1), v = bf16_to_float(x2), s0 = fabsf(u) + fabsf(v);
+    const float a = fmaf(u, t.c, -(v * t.s)), b = fmaf(v, t.c, u * t.s), A = s0 * kTurnBound;
+    const uint32_t lo = cvt_bf16x2_rn(a - A, b - A);
+    *y1 = static_cast<uint16_t>(lo);
+    *y2 = static_cast<uint16_t>(lo >> 16);
+    if (lo != cvt_bf16x2_rn(a + A, b + A) || !(s0 >= 0x1p-70f && s0 <= 0x1p+100f))
+      rotate_carefully(x1, x2, t, angle, y1, y2);
   };
 
   if (q_in != nullptr) {
@@ -250,13 +232,14 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t ek = settle_scale<kFmt>(c, page, 0, h, top_k, slot, old_k, i);
   const uint32_t ev = settle_scale<kFmt>(c, page, 1, h, top_v, slot, old_v, i);
   const float fk = scale_inverse(ek), fv = scale_inverse(ev);
-  const uint32_t w = encode4<kFmt>(bf16_to_float(y1) * fk, bf16_to_float(y2) * fk,
-                                   __uint_as_float(v1 << 16) * fv, __uint_as_float(v2 << 16) * fv);
+  const uint32_t wk = encode4<kFmt, true>(bf16_to_float(y1), bf16_to_float(y2), 0.f, 0.f, fk);
+  const uint32_t wv =
+      encode4<kFmt, true>(__uint_as_float(v1 << 16), __uint_as_float(v2 << 16), 0.f, 0.f, fv);
   uint8_t* kd = c.pool + block_at(page, 0, h) + slot * kHeadDim;
   uint8_t* vd = c.pool + block_at(page, 1, h) + slot * kHeadDim;
-  kd[i] = static_cast<uint8_t>(w);
-  kd[i + kHalf] = static_cast<uint8_t>(w >> 8);
-  reinterpret_cast<uint16_t*>(vd)[i] = static_cast<uint16_t>(w >> 16);
+  kd[i] = static_cast<uint8_t>(wk);
+  kd[i + kHalf] = static_cast<uint8_t>(wk >> 8);
+  reinterpret_cast<uint16_t*>(vd)[i] = static_cast<uint16_t>(wv);
 }
 
 // A unit is one page of one sequence.  Units are numbered so that a sequence's
@@ -344,32 +327,31 @@ __device__ __forceinline__ void check_ends(const Kv8& c, const int32_t* off, int
 
 // RoPE of the 8 pairs (x1, x2) = dims (8 q + p, 32 + 8 q + p) of a row: x1, x2 become
 // bf16 values at or below the rotated ones, y1, y2 at or above them (mostly the same:
-// one pair in 500 differs, where its values cancel or one is much larger).  Returns
-// bits of the pairs that have to be done again.  turn: their (cos, sin) in shared
-// memory.
-__device__ __forceinline__ uint32_t rotate8(uint32_t turn, uint4& x1, uint4& x2, uint4& y1,
-                                            uint4& y2) {
+// one pair in 500 differs, where its values cancel or one is much larger).  turn: the
+// pairs' (cos, sin) in shared memory.
+__device__ __forceinline__ void rotate8(uint32_t turn, uint4& x1, uint4& x2, uint4& y1,
+                                        uint4& y2) {
   const uint32_t a[4] = {x1.x, x1.y, x1.z, x1.w}, b[4] = {x2.x, x2.y, x2.z, x2.w};
-  uint32_t again = 0, l1[4], l2[4], h1[4], h2[4];
+  uint32_t l1[4], l2[4], h1[4], h2[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint4 w = lds128(turn + 16 * e);
-    bool odd[2];
     const float2 u = bf16x2_to_float2(a[e]), v = bf16x2_to_float2(b[e]);
-    const uint2 y0 = rotate_fast(u.x, v.x, __uint_as_float(w.x), __uint_as_float(w.y), odd[0]);
-    const uint2 z0 = rotate_fast(u.y, v.y, __uint_as_float(w.z), __uint_as_float(w.w), odd[1]);
-    if (odd[0]) again |= 1u << (2 * e);
-    if (odd[1]) again |= 2u << (2 * e);
-    l1[e] = prmt(y0.x, z0.x, 0x5410u);
-    l2[e] = prmt(y0.x, z0.x, 0x7632u);
-    h1[e] = prmt(y0.y, z0.y, 0x5410u);
-    h2[e] = prmt(y0.y, z0.y, 0x7632u);
+    const float c0 = __uint_as_float(w.x), s0 = __uint_as_float(w.y);
+    const float c1 = __uint_as_float(w.z), s1 = __uint_as_float(w.w);
+    const float p0 = fmaf(u.x, c0, -(v.x * s0)), q0 = fmaf(v.x, c0, u.x * s0);
+    const float p1 = fmaf(u.y, c1, -(v.y * s1)), q1 = fmaf(v.y, c1, u.y * s1);
+    const float A0 = (fabsf(u.x) + fabsf(v.x)) * kTurnBound;
+    const float A1 = (fabsf(u.y) + fabsf(v.y)) * kTurnBound;
+    l1[e] = cvt_bf16x2_rn(p0 - A0, p1 - A1);
+    l2[e] = cvt_bf16x2_rn(q0 - A0, q1 - A1);
+    h1[e] = cvt_bf16x2_rn(p0 + A0, p1 + A1);
+    h2[e] = cvt_bf16x2_rn(q0 + A0, q1 + A1);
   }
   x1 = make_uint4(l1[0], l1[1], l1[2], l1[3]);
   x2 = make_uint4(l2[0], l2[1], l2[2], l2[3]);
   y1 = make_uint4(h1[0], h1[1], h1[2], h1[3]);
   y2 = make_uint4(h2[0], h2[1], h2[2], h2[3]);
-  return again;
 }
 
 // Bits of the pairs whose bounds differ.
@@ -423,18 +405,31 @@ __device__ __forceinline__ void drop_nonfinite(uint4& x) {
                  x.z & ~nonfinite_halves(x.z), x.w & ~nonfinite_halves(x.w));
 }
 
-// The larger magnitude of each half, over the words.
-__device__ __forceinline__ uint32_t top_halves(uint32_t top, const uint4& x) {
-  top = __vmaxu2(top, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu));
-  return __vmaxu2(top, __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+// The larger magnitude of each half (NaN where there is one), under a sign of no
+// meaning.
+__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t top8(const uint4& x) {
+  return top2(top2(x.x, x.y), top2(x.z, x.w));
+}
+
+// Magnitudes past 127 x 2^113, the largest that scales reach, become that.
+__device__ __forceinline__ void saturate8(uint4& x) {
+  uint32_t* w = &x.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = (w[i] & 0x80008000u) | __vminu2(w[i] & 0x7FFF7FFFu, 0x7B7E7B7Eu);
 }
 
 template <int kFmt>
 __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
-  const float2 f2 = make_float2(f, f);
-  const float2 a = fmul2(bf16x2_to_float2(x.x), f2), b = fmul2(bf16x2_to_float2(x.y), f2),
-               c = fmul2(bf16x2_to_float2(x.z), f2), d = fmul2(bf16x2_to_float2(x.w), f2);
-  return make_uint2(encode4<kFmt>(a.x, a.y, b.x, b.y), encode4<kFmt>(c.x, c.y, d.x, d.y));
+  const float2 a = bf16x2_to_float2(x.x), b = bf16x2_to_float2(x.y), c = bf16x2_to_float2(x.z),
+               d = bf16x2_to_float2(x.w);
+  return make_uint2(encode4<kFmt, false>(a.x, a.y, b.x, b.y, f),
+                    encode4<kFmt, false>(c.x, c.y, d.x, d.y, f));
 }
 
 // Ragged prompts: a CTA brings its units' rows of k and v (16 KiB each, in a row)
@@ -560,10 +555,9 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       // the largest magnitude, values that are not finite left out
       auto largest = [&](uint4 (&y)[2][2]) {
         auto top_of = [&]() {
-          uint32_t top = 0;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) top = top_halves(top_halves(top, y[s][0]), y[s][1]);
-          return __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16));
+          const uint32_t m = top2(top2(top8(y[0][0]), top8(y[0][1])),
+                                  top2(top8(y[1][0]), top8(y[1][1])));
+          return __reduce_max_sync(kFull, max(m & 0x7FFFu, (m >> 16) & 0x7FFFu));
         };
         const uint32_t top = top_of();
         if (top < 0x7F80u) return top;
@@ -587,22 +581,24 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
             *reinterpret_cast<uint2*>(block + slot * kHeadDim + kHalf * d) = codes[s][d];
         }
       };
-      // the block's scale, once `top` has come to it
-      auto scale_for = [&](uint32_t top, uint32_t old) {
-        const uint32_t e = needed_scale<kFmt>(top);
-        return t.s0 > 0 ? max(e, old) : e;
-      };
-      auto encode = [&](const uint4 (&y)[2][2], float f, uint2 (&codes)[2][2]) {
+      // codes of values whose largest is `top`
+      auto encode = [&](uint4 (&y)[2][2], uint32_t top, uint32_t old, uint2 (&codes)[2][2]) {
+        uint32_t e = needed_scale<kFmt>(top);
+        if (t.s0 > 0) e = max(e, old);
+        const float f = scale_inverse(e);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int d = 0; d < 2; ++d) codes[s][d] = encode8<kFmt>(y[s][d], f);
+          for (int d = 0; d < 2; ++d) {
+            if (kFmt == kKv8Int8 && e == kMostScale) saturate8(y[s][d]);
+            codes[s][d] = encode8<kFmt>(y[s][d], f);
+          }
       };
       uint2 codes[2][2];
       {
         load(rows + kHalfStage);
         const uint32_t top = largest(x), old = stored_scale(old_v);
-        encode(x, scale_inverse(scale_for(top, old)), codes);
+        encode(x, top, old, codes);
         put(1, top, old, codes);
       }
       load(rows);
@@ -614,47 +610,55 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       // up to 2047 tokens, with FP64, whose rate here is a small fraction of FP32's,
       // 119; not at all 64.)
       uint4 y[2][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        rotate8(sb + kOffTurn + ((r + 8 * s) * kTurnRow + 8 * q) * 8, x[s][0], x[s][1], y[s][0],
+                y[s][1]);
+        if (r + 8 * s < t.s0 || r + 8 * s >= t.s1)  // (zeros: their signs do not matter)
+          y[s][0] = y[s][1] = x[s][0] = x[s][1] = make_uint4(0u, 0u, 0u, 0u);
+      }
       auto again = [&](int s, uint32_t bad) {
         const int slot = r + 8 * s;
         rotate_again(bad, freqs.inv_freq + 8 * q, rows + slot * kTokenBytes,
                      sb + kOffTurn + (slot * kTurnRow + 8 * q) * 8, kTurnBytes, pos0 + slot,
                      x[s][0], x[s][1]);
-        y[s][0] = x[s][0];
-        y[s][1] = x[s][1];
       };
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t odd = rotate8(sb + kOffTurn + ((r + 8 * s) * kTurnRow + 8 * q) * 8, x[s][0],
-                                     x[s][1], y[s][0], y[s][1]);
-        if (odd != 0) again(s, odd);
-      }
       uint32_t top = largest(x);
       const uint32_t old = stored_scale(old_k);
-      uint32_t apart[2];
+      // (pairs of less than 2^-70 matter only where the block's largest is tiny)
+      const bool odd = (top > 0 && top < kTiny) || top >= kHuge;
+      encode(x, top, old, codes);
+      uint32_t apart = 0;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) apart[s] = pairs_apart(x[s][0], x[s][1], y[s][0], y[s][1]);
-      if (__any_sync(kFull, (apart[0] | apart[1]) != 0)) {
-        bool differ = needed_scale<kFmt>(largest(y)) != needed_scale<kFmt>(top);  // (all lanes)
-        if (!differ) {
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+          apart |= (x[s][d].x ^ y[s][d].x) | (x[s][d].y ^ y[s][d].y) | (x[s][d].z ^ y[s][d].z) |
+                   (x[s][d].w ^ y[s][d].w);
+      if (odd || __any_sync(kFull, apart != 0)) {
+        bool differ = odd || needed_scale<kFmt>(largest(y)) != needed_scale<kFmt>(top);
+        if (!differ) {  // (the same in all lanes so far)
           uint2 z[2][2];
-          const float f = scale_inverse(scale_for(top, old));
-          encode(x, f, codes);
-          encode(y, f, z);
+          encode(y, top, old, z);
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int d = 0; d < 2; ++d)
               differ |= ((codes[s][d].x ^ z[s][d].x) | (codes[s][d].y ^ z[s][d].y)) != 0u;
         }
-        if (differ) {
+        if (__any_sync(kFull, differ)) {
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
-            if (apart[s] != 0) again(s, apart[s]);
+          for (int s = 0; s < 2; ++s) {
+            const bool in = r + 8 * s >= t.s0 && r + 8 * s < t.s1;
+            const uint32_t bad =
+                !in ? 0u : odd ? 0xFFu : pairs_apart(x[s][0], x[s][1], y[s][0], y[s][1]);
+            if (differ && bad != 0) again(s, bad);
+          }
+          __syncwarp();
+          top = largest(x);
+          encode(x, top, old, codes);
         }
-        __syncwarp();
-        top = largest(x);
       }
-      encode(x, scale_inverse(scale_for(top, old)), codes);
       put(0, top, old, codes);
       fence_proxy_async_smem();
       __syncthreads();  // the stage can be filled again, the angles replaced
