@@ -681,6 +681,13 @@ def _bytes(n, what):
 
 def _heads(t, name, index, rows, heads=NUM_Q_HEADS):
     """t is a bf16 tensor [rows][heads][64] (rows None: any number of rows)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == index
+            and t.is_contiguous()):
+        shape = t.shape
+        if rows is None and len(shape) == 3:
+            rows = shape[0]
+        if shape == (rows, heads, HEAD_DIM):
+            return rows
     _is(t, name, _BF16, 3, index)
     n, h, d = t.shape
     if h != heads or d != HEAD_DIM or (rows is not None and n != rows):
@@ -967,6 +974,14 @@ _KV8_FORMATS = {torch.float8_e4m3fn: KV8_E4M3, torch.int8: KV8_INT8}
 
 def _pool8(pool, scales):
     """(device index, pages, format) of an 8-bit pool and its scales."""
+    if isinstance(pool, torch.Tensor) and isinstance(scales, torch.Tensor) and pool.dim() == 5:
+        index, pages, fmt = pool.get_device(), pool.shape[0], _KV8_FORMATS.get(pool.dtype)
+        if (fmt is not None and index >= 0 and pool.shape == (pages, *_KV8_ROW)
+                and scales.shape == (pages, *_KV8_SCALES) and scales.dtype is torch.uint8
+                and scales.get_device() == index and pool.is_contiguous()
+                and scales.is_contiguous()):
+            return index, pages, fmt
+    # what is wrong, in words
     if not (isinstance(pool, torch.Tensor) and pool.dtype in _KV8_FORMATS):
         raise TypeError("pool must be a float8_e4m3fn or int8 tensor")
     if pool.dim() != 5 or pool.shape[1:] != _KV8_ROW:
@@ -975,11 +990,8 @@ def _pool8(pool, scales):
         raise ValueError("pool must be contiguous")
     if not pool.is_cuda:
         raise ValueError(f"pool must be on a CUDA device, not {pool.device}")
-    index, pages = pool.get_device(), pool.shape[0]
-    _is(scales, "scales", torch.uint8, 3, index)
-    if scales.shape[0] != pages or scales.shape[1:] != _KV8_SCALES:
-        raise ValueError(f"scales must be [{pages}][2][8], got {tuple(scales.shape)}")
-    return index, pages, _KV8_FORMATS[pool.dtype]
+    _is(scales, "scales", torch.uint8, 3, pool.get_device())
+    raise ValueError(f"scales must be [{pool.shape[0]}][2][8], got {tuple(scales.shape)}")
 
 
 def kv8_append(k_new, v_new, pool, scales, block_table, positions, slots=None, *,
@@ -991,16 +1003,14 @@ def kv8_append(k_new, v_new, pool, scales, block_table, positions, slots=None, *
     No two sequences may append to the same page."""
     index, num_pages, fmt = _pool8(pool, scales)
     _is(block_table, "block_table", _I32, 2, index)
-    _is(positions, "positions", _I32, 1, index)
     B, max_blocks = block_table.shape
     _heads(k_new, "k_new", index, B, NUM_KV_HEADS)
     _heads(v_new, "v_new", index, B, NUM_KV_HEADS)
-    if positions.shape[0] != B:
+    if not _ints(positions, "positions", index, B):
         raise ValueError("positions and block_table disagree on the batch")
     slots_ptr = q_ptr = out_ptr = None
     if slots is not None:
-        _is(slots, "slots", _I32, 1, index)
-        if slots.shape[0] != B:
+        if not _ints(slots, "slots", index, B):
             raise ValueError("slots and block_table disagree on the batch")
         slots_ptr = slots.data_ptr()
     if q_in is not None or q_out is not None:
@@ -1016,13 +1026,21 @@ def kv8_append(k_new, v_new, pool, scales, block_table, positions, slots=None, *
                 _err(dev_err, index), raw)
 
 
+def _ints(t, name, index, size):
+    """t is an int32 tensor [size]."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.shape == (size,)
+            and t.get_device() == index and t.is_contiguous()):
+        _is(t, name, _I32, 1, index)
+        return False
+    return True
+
+
 def _ragged(token_offsets, start_positions, block_table, index):
     """The batch and table width of a ragged batch of tokens."""
-    _is(token_offsets, "token_offsets", _I32, 1, index)
-    _is(start_positions, "start_positions", _I32, 1, index)
     _is(block_table, "block_table", _I32, 2, index)
     B, max_blocks = block_table.shape
-    if start_positions.shape[0] != B or token_offsets.shape[0] != B + 1:
+    if not (_ints(token_offsets, "token_offsets", index, B + 1)
+            and _ints(start_positions, "start_positions", index, B)):
         raise ValueError("start_positions must have batch entries and token_offsets batch + 1")
     return B, max_blocks
 

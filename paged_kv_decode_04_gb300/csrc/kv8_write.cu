@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t lo = cvt_bf16x2_rn(a - A, b - A);
     *y1 = static_cast<uint16_t>(lo);
     *y2 = static_cast<uint16_t>(lo >> 16);
-    if (lo != cvt_bf16x2_rn(a + A, b + A) || !(s0 >= 0x1p-70f && s0 <= 0x1p+100f))
+    // (zeros keep their signs in FP32)
+    if (s0 != 0.f &&
+        (lo != cvt_bf16x2_rn(a + A, b + A) || !(s0 >= 0x1p-70f && s0 <= 0x1p+100f)))
       rotate_carefully(x1, x2, t, angle, y1, y2);
   };
 

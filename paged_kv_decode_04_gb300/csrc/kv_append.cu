@@ -459,6 +459,16 @@ RopeTableAddrs g_rope_addrs[64];
 }  // namespace
 
 cudaError_t prepare_rope(double theta, RopeFreqs* f, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  // The thread's last answer with a table: the slot it names is never rewritten.
+  // (Working the frequencies out takes longer than a launch.)
+  thread_local RopeFreqs last;
+  thread_local int last_dev = -1;
+  if (err == cudaSuccess && dev == last_dev && last.theta == theta) {
+    *f = last;
+    return cudaSuccess;
+  }
   for (int i = 0; i < kHalf; ++i)
     f->inv_freq[i] = pow(theta, -(2.0 * i) / static_cast<double>(kHeadDim));
   f->theta = theta;
@@ -466,8 +476,6 @@ cudaError_t prepare_rope(double theta, RopeFreqs* f, cudaStream_t stream) {
   f->table_lo = nullptr;
   f->table64 = nullptr;
   f->table_theta = nullptr;
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaSuccess;  // no table: kernels evaluate sincos
   std::lock_guard<std::mutex> lock(g_rope_mutex);
@@ -501,6 +509,8 @@ cudaError_t prepare_rope(double theta, RopeFreqs* f, cudaStream_t stream) {
   f->table_lo = a.tlo + static_cast<size_t>(slot) * kRopeEntries;
   f->table64 = a.t64 + static_cast<size_t>(slot) * kRopeEntries;
   f->table_theta = a.theta + slot;
+  last = *f;
+  last_dev = dev;
   return cudaSuccess;
 }
 
