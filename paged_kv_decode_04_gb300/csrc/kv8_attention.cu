@@ -1,11 +1,22 @@
 // kv8_attention.cu -- attention of one new token, or of chunks of a few, per
 // sequence over the 8-bit paged cache, streaming its pages once.
 //
-// One CTA per (sequence, range of the pages that its queries see): a producer
-// warp brings whole pages (16 KiB, all kv heads, one TMA box, and the 16 bytes of
-// their scales) into a ring in shared memory, and warp g of eight takes kv head
-// g's blocks of every page.  So a page is one copy and one barrier for all heads,
-// and the heads' states never meet.
+// In a CTA a producer warp brings
+// whole pages (16 KiB, all kv heads, one TMA box, and the 16 bytes of their scales)
+// into a ring in shared memory, and warp g of eight takes kv head g's blocks of every
+// page.  So a page is one copy and one barrier for all heads, and the heads' states
+// never meet.
+//
+// A CTA takes a range of one sequence's pages (grid (ranges, sequences)) or, kShared,
+// an even share of the batch's: the pages that the queries see, counted on from sequence
+// to sequence, are dealt out to two CTAs an SM, CTA c of N the pages [c T / N,
+// (c + 1) T / N) of T, which it works out from the lengths (a sum and a scan of them in
+// every CTA).  A sequence that lies in one CTA is answered there; of the others each CTA
+// leaves a partial result (two at most), which the merge kernel combines.
+//
+// Bound by memory, in the middle by latencies: one token for 256 sequences of 1024 to
+// 2048 tokens (409 MB) 76 us, 5.4 TB/s, where the copies alone take 74; 64 x 4 new
+// tokens over 1024 to 2048 (104 MB) 34 us without the launches around, the copies 22.
 //
 // mma.sync m16n8k16 in f16, FP32 accumulators, for a page (16 tokens) and a kv
 // head; codes become f16 exactly (one instruction for two e4m3 codes):
@@ -44,7 +55,7 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kWarps = kNumKvHeads;            // and one that loads
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kStages = 6, kCtas = 2;
+constexpr int kStages = 6, kCtas = kStream8Ctas;
 constexpr int kOffScales = kStages * kPage8Bytes;
 constexpr int kOffMeta = kOffScales + kStages * kPageScales;
 constexpr int kOffBars = kOffMeta + kStages * 8;
@@ -286,16 +297,17 @@ struct Turn {
   }
 };
 
-// The producer warp: pages [r0, r1) of the list page_of, ids 32 at a time.
-template <typename PageOf>
-__device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map,
-                                           const MaskedArgs& a, int b, int r0, int r1, int lane,
-                                           const PageOf& page_of) {
+// The producer warp: pages [r0, r1) of a sequence's list, ids 32 at a time.  k counts
+// the pages of all segments.  False: a wait ran out.
+template <typename Seq>
+__device__ __forceinline__ bool load_pages(const Ring& R, const CUtensorMap* map,
+                                           const MaskedArgs& a, int b, const Seq& seq, int r0,
+                                           int r1, int lane, Turn& T, int& k) {
   const int n = r1 - r0;
   auto load_ids = [&](int k0) {
     int pid = -1;
     if (k0 + lane < n) {
-      pid = a.block_table[static_cast<int64_t>(b) * a.max_blocks + page_of(r0 + k0 + lane)];
+      pid = a.block_table[static_cast<int64_t>(b) * a.max_blocks + seq.page(r0 + k0 + lane)];
       if (pid < 0 || pid >= a.num_pages) {
         record_error(a.dev_err, kErrPage);
         pid = -1;
@@ -305,20 +317,15 @@ __device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map
   };
   const uint64_t policy = l2_policy_evict_first();
   int ids = load_ids(0), ids_next = load_ids(32);
-  int k = 0;
-  Turn T;
-  for (; k < n; ++k, T.next()) {
+  for (int i = 0; i < n; ++i, ++k, T.next()) {
     const int st = T.stage;
     if (k >= kStages) {
       const bool ok = mbar_wait_bounded(R.empty(st), T.phase ^ 1, a.wait_ns);
-      if (!__all_sync(kFull, ok)) {
-        if (lane == 0) record_error(a.dev_err, kErrTimeout);
-        break;
-      }
+      if (!__all_sync(kFull, ok)) return false;
     }
-    const int pid = __shfl_sync(kFull, ids, k & 31);
+    const int pid = __shfl_sync(kFull, ids, i & 31);
     if (lane == 0) {
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(R.meta(st)), "r"(page_of(r0 + k)),
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(R.meta(st)), "r"(seq.page(r0 + i)),
                    "r"(pid)
                    : "memory");
       if (pid >= 0) {
@@ -331,14 +338,127 @@ __device__ __forceinline__ void load_pages(const Ring& R, const CUtensorMap* map
       }
     }
     __syncwarp();
-    if ((k & 31) == 31) {
+    if ((i & 31) == 31) {
       ids = ids_next;
-      ids_next = load_ids(k + 33);
+      ids_next = load_ids(i + 33);
     }
   }
-  // every copy has landed before the CTA ends (full limit)
+  return true;
+}
+
+// Every copy has landed before the CTA ends (full limit): the last ones of k.
+__device__ __forceinline__ void drain(const Ring& R, int k) {
   for (int j = k > kStages ? k - kStages : 0; j < k; ++j)
     mbar_wait_bounded(R.full(j % kStages), (j / kStages) & 1);
+}
+
+// The CTA's part of the work, dealt out as above, or with num_splits one range of one
+// sequence.
+struct Part {
+  int64_t u0, u1;  // pages [u0, u1) of all
+  int64_t base;    // pages before sequence b, the first of them
+  int b;
+};
+constexpr int kLeastPages = 4;  // of a CTA, while there are fewer than all of them need
+
+// CTAs that share `total` pages, and the first page of one.
+__device__ __forceinline__ int64_t parts_of(int64_t total, int ctas) {
+  return max(1ll, min(static_cast<long long>(ctas), static_cast<long long>(total / kLeastPages)));
+}
+__device__ __forceinline__ int64_t part_start(int64_t total, int64_t parts, int64_t c) {
+  return total * c / parts;
+}
+
+// make(b): sequence b's list.  By all threads of the CTA.  The first CTA writes the
+// sequences' bases, and the total behind them, for the merge.
+template <typename Make>
+__device__ __forceinline__ Part share_out(const MaskedArgs& a, const Make& make) {
+  __shared__ int64_t s_warp[kThreads / 32];
+  __shared__ int64_t s_base;
+  __shared__ int s_first;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  int64_t sum = 0;
+  int mine = 0;  // of sequence tid
+  for (int b = tid; b < a.batch; b += kThreads) {
+    const int n = make(b).n;
+    if (b == tid) mine = n;
+    sum += n;
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+  if (lane == 0) s_warp[w] = sum;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) total += s_warp[i];
+  const int64_t parts = parts_of(total, gridDim.x);
+  Part p = {0, 0, 0, 0};
+  if (blockIdx.x < parts) {
+    p.u0 = part_start(total, parts, blockIdx.x);
+    p.u1 = part_start(total, parts, blockIdx.x + 1);
+  }
+  const bool report = blockIdx.x == 0;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.batch && (report || before <= p.u0); b0 += kThreads) {
+    const int b = b0 + tid;
+    const int n = b0 == 0 ? mine : b < a.batch ? make(b).n : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, incl, x);
+      if (lane >= x) incl += y;
+    }
+    __syncthreads();  // s_warp has been read
+    if (lane == 31) s_warp[w] = incl;
+    __syncthreads();
+    int64_t base = before + incl - n, all = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < w) base += s_warp[i];
+      all += s_warp[i];
+    }
+    if (base <= p.u0 && p.u0 < base + n) {
+      s_first = b;
+      s_base = base;
+    }
+    if (report && b < a.batch) a.part_bases[b] = base;
+    before += all;
+  }
+  if (report && tid == 0) a.part_bases[a.batch] = total;
+  __syncthreads();
+  if (p.u0 < p.u1) {
+    p.b = s_first;
+    p.base = s_base;
+  }
+  return p;
+}
+
+// Call f(b, list, r0, r1, slot) for the CTA's segments: pages [r0, r1) of sequence b,
+// slot -1 where these are all of them, else the place of the partial result.  Ends
+// when f returns false.
+template <bool kShared, typename Make, typename F>
+__device__ __forceinline__ void each_segment(int num_splits, const Part& p, const Make& make,
+                                             const F& f) {
+  if constexpr (!kShared) {
+    const int b = blockIdx.y;
+    const auto seq = make(b);
+    const int r0 = static_cast<int>(static_cast<int64_t>(seq.n) * blockIdx.x / num_splits);
+    const int r1 = static_cast<int>(static_cast<int64_t>(seq.n) * (blockIdx.x + 1) / num_splits);
+    f(b, seq, r0, r1, num_splits > 1 ? b * num_splits + static_cast<int>(blockIdx.x) : -1);
+  } else {
+    int64_t base = p.base;
+    for (int b = p.b; base < p.u1 && p.u0 < p.u1; ++b) {
+      const auto seq = make(b);
+      if (seq.n == 0) continue;
+      const int r0 = p.u0 > base ? static_cast<int>(p.u0 - base) : 0;
+      const int r1 = p.u1 - base < seq.n ? static_cast<int>(p.u1 - base) : seq.n;
+      const bool all = r0 == 0 && r1 == seq.n;
+      // (a part's first segment, or its last)
+      if (!f(b, seq, r0, r1, all ? -1 : 2 * static_cast<int>(blockIdx.x) + (p.u0 < base ? 1 : 0)))
+        return;
+      base += seq.n;
+    }
+  }
 }
 
 __device__ __forceinline__ Ring make_ring(uint8_t* raw, const CUtensorMap* map) {
@@ -357,9 +477,9 @@ __device__ __forceinline__ Ring make_ring(uint8_t* raw, const CUtensorMap* map) 
 
 // Column 2 ft + j of S as a row's output or, where the row has several ranges, as
 // its partial result number `part`.
-__device__ __forceinline__ void put_row(const State& S, int j, int fg, uint16_t* out, bool partial,
-                                        float* acc, float* ml, int64_t part) {
-  if (partial) {
+__device__ __forceinline__ void put_row(const State& S, int j, int fg, uint16_t* out, float* acc,
+                                        float* ml, int64_t part) {
+  if (part >= 0) {
     float* dst = acc + part * kHeadDim + fg;
 #pragma unroll
     for (int i = 0; i < 8; ++i) dst[8 * i] = j == 0 ? S.o[i >> 1][i & 1].x : S.o[i >> 1][i & 1].y;
@@ -373,370 +493,485 @@ __device__ __forceinline__ void put_row(const State& S, int j, int fg, uint16_t*
   }
 }
 
-// One token a sequence; grid (ranges, batch).
-template <int kFmt>
+// Zero rows of a kv head's group for a token that sees nothing.
+__device__ __forceinline__ void put_zeros(uint16_t* out, int lane) {
+#pragma unroll
+  for (int h = 0; h < kGroup; ++h) reinterpret_cast<uint32_t*>(out + h * kHeadDim)[lane] = 0u;
+}
+
+// One token a sequence.  Grid: the CTAs that share the work, or (num_splits, batch).
+template <int kFmt, bool kShared>
 __global__ void __launch_bounds__(kThreads, kCtas)
     paged8_decode_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
-  const int split = blockIdx.x, b = blockIdx.y;
   const Ring R = make_ring(smem_raw, &map);
   wait_for_prior_grids();
   allow_dependent_grids();
-  const Visible V(clamped_len(a, b, tid == 0 && split == 0), a.window, a.sinks);
-  const int r0 = static_cast<int>(static_cast<int64_t>(V.n) * split / a.num_splits);
-  const int r1 = static_cast<int>(static_cast<int64_t>(V.n) * (split + 1) / a.num_splits);
+  const bool report = blockIdx.x == 0 && (kShared || tid == 0);
+  auto make = [&](int b) { return Visible(clamped_len(a, b, report), a.window, a.sinks); };
+  Part part = {0, 0, 0, 0};
+  if constexpr (kShared) part = share_out(a, make);
+  Turn T;
   if (g == kWarps) {
-    load_pages(R, &map, a, b, r0, r1, lane, [&](int i) { return V.page(i); });
+    int k = 0;
+    each_segment<kShared>(a.num_splits, part, make,
+                 [&](int b, const Visible& V, int r0, int r1, int) {
+                   const bool ok = load_pages(R, &map, a, b, V, r0, r1, lane, T, k);
+                   if (!ok && lane == 0) record_error(a.dev_err, kErrTimeout);
+                   return ok;
+                 });
+    drain(R, k);
     return;
   }
 
+  // (while the first copies are on their way)
+  if constexpr (kShared)
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x)
+      if (make(b).n == 0)
+        put_zeros(a.out + (static_cast<int64_t>(b) * kNumQHeads + g * kGroup) * kHeadDim, lane);
   const Lane P(lane);
-  uint32_t qb[4][2];
-  const int64_t row0 = static_cast<int64_t>(b) * kNumQHeads + g * kGroup;
-  const float undo = load_q(a.q + (row0 + (P.fg & 3)) * kHeadDim, P.ft, qb);
-  // factors of the scores of columns 2 ft and 2 ft + 1
-  const int h = (2 * P.ft) & 3;
-  const float c0 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h);
-  const float c1 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h + 4);
-  State S;
-  S.reset();
-  // Two pages at a time: one alone is a chain of latencies (copy, products, weights,
-  // products), and what is checked is checked once for both.
-  const int n = r1 - r0;
-  Turn T;
-  for (int k = 0; k < n; k += 2) {
-    const int st0 = T.stage, phase0 = T.phase;
-    T.next();
-    const int st1 = T.stage, phase1 = T.phase;
-    T.next();
-    bool ready = mbar_wait_bounded(R.full(st0), phase0, a.wait_ns);
-    if (k + 1 < n) ready &= mbar_wait_bounded(R.full(st1), phase1, a.wait_ns);
-    if (!__all_sync(kFull, ready)) {
-      if (lane == 0) record_error(a.dev_err, kErrTimeout);
-      break;
-    }
-    // seen tokens of the pages (none where there is none, or it was not read)
-    auto seen = [&](int st, bool there) {
-      const uint2 meta = lds64(R.meta(st));
-      if (!there || static_cast<int>(meta.y) < 0) return 0u;
-      return V.whole(meta.x) ? 0xFFFFu : V.mask(meta.x);
-    };
-    const uint32_t vis0 = seen(st0, true), vis1 = seen(st1, k + 1 < n);
-    const uint32_t kt0 = R.page(st0) + g * kBlockBytes, kt1 = R.page(st1) + g * kBlockBytes;
-    constexpr uint32_t kV = kNumKvHeads * kBlockBytes;
-    const float sk0 = scale_value(lds8(R.scales(st0) + g));
-    const float sk1 = scale_value(lds8(R.scales(st1) + g));
-    const float sv0 = scale_value(lds8(R.scales(st0) + kNumKvHeads + g));
-    const float sv1 = scale_value(lds8(R.scales(st1) + kNumKvHeads + g));
-    // (a factor of 0 would make NaN of a masked score)
-    const float f[2][2] = {{fmaxf(c0 * sk0, 0x1p-126f), fmaxf(c1 * sk0, 0x1p-126f)},
-                           {fmaxf(c0 * sk1, 0x1p-126f), fmaxf(c1 * sk1, 0x1p-126f)}};
-    float s[2][4];
-    uint32_t b[2][2];
-    auto scores = [&](uint32_t kt, float (&x)[4]) {
-      uint32_t ka[4][4];
-      load_k<kFmt>(kt, P, ka);
-      mma_new(x, ka[0], qb[0][0], qb[0][1]);
-#pragma unroll
-      for (int kk = 1; kk < 4; ++kk) mma_add(x, ka[kk], qb[kk][0], qb[kk][1]);
-    };
-    if ((vis0 & vis1) == 0xFFFFu) {
-      scores(kt0, s[0]);
-      scores(kt1, s[1]);
-      move_reference(s, f, S);
-      page_weights(s[0], f[0], P.ft, S, b[0][0], b[0][1]);
-      page_weights(s[1], f[1], P.ft, S, b[1][0], b[1][1]);
-      add_values<kFmt>(kt0 + kV, P, sv0, b[0][0], b[0][1], S);
-      add_values<kFmt>(kt1 + kV, P, sv1, b[1][0], b[1][1], S);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t vis = i == 0 ? vis0 : vis1, kt = i == 0 ? kt0 : kt1;
-        s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
-        if (vis == 0u) continue;
-        scores(kt, s[i]);
-        if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
-        if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
-        if constexpr (kFmt == kKv8E4m3) hide_v(kt + kV, vis, lane);
+  each_segment<kShared>(a.num_splits, part, make, [&](int b, const Visible& V, int r0, int r1,
+                                                int slot) {
+    uint32_t qb[4][2];
+    const int64_t row0 = static_cast<int64_t>(b) * kNumQHeads + g * kGroup;
+    const float undo = load_q(a.q + (row0 + (P.fg & 3)) * kHeadDim, P.ft, qb);
+    // factors of the scores of columns 2 ft and 2 ft + 1
+    const int h = (2 * P.ft) & 3;
+    const float c0 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h);
+    const float c1 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h + 4);
+    State S;
+    S.reset();
+    bool ok = true;
+    // Two pages at a time: one alone is a chain of latencies (copy, products, weights,
+    // products), and what is checked is checked once for both.
+    const int n = r1 - r0;
+    for (int k = 0; k < n; k += 2) {
+      const int st0 = T.stage, phase0 = T.phase;
+      T.next();
+      const int st1 = T.stage, phase1 = T.phase;
+      if (k + 1 < n) T.next();
+      bool ready = mbar_wait_bounded(R.full(st0), phase0, a.wait_ns);
+      if (k + 1 < n) ready &= mbar_wait_bounded(R.full(st1), phase1, a.wait_ns);
+      if (!__all_sync(kFull, ready)) {
+        if (lane == 0) record_error(a.dev_err, kErrTimeout);
+        ok = false;
+        break;
       }
-      // (the scales of a page that was not read may be anything)
-      const float g2[2][2] = {{vis0 ? f[0][0] : 1.f, vis0 ? f[0][1] : 1.f},
-                              {vis1 ? f[1][0] : 1.f, vis1 ? f[1][1] : 1.f}};
-      move_reference(s, g2, S);
+      // seen tokens of the pages (none where there is none, or it was not read)
+      auto seen = [&](int st, bool there) {
+        const uint2 meta = lds64(R.meta(st));
+        if (!there || static_cast<int>(meta.y) < 0) return 0u;
+        return V.whole(meta.x) ? 0xFFFFu : V.mask(meta.x);
+      };
+      const uint32_t vis0 = seen(st0, true), vis1 = seen(st1, k + 1 < n);
+      const uint32_t kt0 = R.page(st0) + g * kBlockBytes, kt1 = R.page(st1) + g * kBlockBytes;
+      constexpr uint32_t kV = kNumKvHeads * kBlockBytes;
+      const float sk0 = scale_value(lds8(R.scales(st0) + g));
+      const float sk1 = scale_value(lds8(R.scales(st1) + g));
+      const float sv0 = scale_value(lds8(R.scales(st0) + kNumKvHeads + g));
+      const float sv1 = scale_value(lds8(R.scales(st1) + kNumKvHeads + g));
+      // (a factor of 0 would make NaN of a masked score)
+      const float f[2][2] = {{fmaxf(c0 * sk0, 0x1p-126f), fmaxf(c1 * sk0, 0x1p-126f)},
+                             {fmaxf(c0 * sk1, 0x1p-126f), fmaxf(c1 * sk1, 0x1p-126f)}};
+      float s[2][4];
+      uint32_t b[2][2];
+      auto scores = [&](uint32_t kt, float (&x)[4]) {
+        uint32_t ka[4][4];
+        load_k<kFmt>(kt, P, ka);
+        mma_new(x, ka[0], qb[0][0], qb[0][1]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        page_weights(s[i], g2[i], P.ft, S, b[i][0], b[i][1]);
-        if ((i == 0 ? vis0 : vis1) != 0u)
-          add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, i == 0 ? sv0 : sv1, b[i][0], b[i][1], S);
+        for (int kk = 1; kk < 4; ++kk) mma_add(x, ka[kk], qb[kk][0], qb[kk][1]);
+      };
+      if ((vis0 & vis1) == 0xFFFFu) {
+        scores(kt0, s[0]);
+        scores(kt1, s[1]);
+        move_reference(s, f, S);
+        page_weights(s[0], f[0], P.ft, S, b[0][0], b[0][1]);
+        page_weights(s[1], f[1], P.ft, S, b[1][0], b[1][1]);
+        add_values<kFmt>(kt0 + kV, P, sv0, b[0][0], b[0][1], S);
+        add_values<kFmt>(kt1 + kV, P, sv1, b[1][0], b[1][1], S);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t vis = i == 0 ? vis0 : vis1, kt = i == 0 ? kt0 : kt1;
+          s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
+          if (vis == 0u) continue;
+          scores(kt, s[i]);
+          if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
+          if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
+          if constexpr (kFmt == kKv8E4m3) hide_v(kt + kV, vis, lane);
+        }
+        // (the scales of a page that was not read may be anything)
+        const float g2[2][2] = {{vis0 ? f[0][0] : 1.f, vis0 ? f[0][1] : 1.f},
+                                {vis1 ? f[1][0] : 1.f, vis1 ? f[1][1] : 1.f}};
+        move_reference(s, g2, S);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          page_weights(s[i], g2[i], P.ft, S, b[i][0], b[i][1]);
+          if ((i == 0 ? vis0 : vis1) != 0u)
+            add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, i == 0 ? sv0 : sv1, b[i][0], b[i][1], S);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(R.empty(st0));
+        if (k + 1 < n) mbar_arrive(R.empty(st1));
       }
     }
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(R.empty(st0));
-      if (k + 1 < n) mbar_arrive(R.empty(st1));
-    }
-  }
 
-  // the terms' columns meet; lanes ft < 2 hold heads 2 ft and 2 ft + 1
+    // the terms' columns meet; lanes ft < 2 hold heads 2 ft and 2 ft + 1
 #pragma unroll
-  for (int i = 4; i <= 16; i <<= 1) {
-    S.l[0] += __shfl_xor_sync(kFull, S.l[0], i);
-    S.l[1] += __shfl_xor_sync(kFull, S.l[1], i);
-  }
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      S.o[mt][e].x += __shfl_xor_sync(kFull, S.o[mt][e].x, 2);
-      S.o[mt][e].y += __shfl_xor_sync(kFull, S.o[mt][e].y, 2);
+    for (int i = 4; i <= 16; i <<= 1) {
+      S.l[0] += __shfl_xor_sync(kFull, S.l[0], i);
+      S.l[1] += __shfl_xor_sync(kFull, S.l[1], i);
     }
-  if (P.ft >= 2) return;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t row = row0 + 2 * P.ft + j;
-    put_row(S, j, P.fg, a.out + row * kHeadDim, a.num_splits > 1, a.part_acc, a.part_ml,
-            row * a.num_splits + split);
-  }
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        S.o[mt][e].x += __shfl_xor_sync(kFull, S.o[mt][e].x, 2);
+        S.o[mt][e].y += __shfl_xor_sync(kFull, S.o[mt][e].y, 2);
+      }
+    if (P.ft < 2) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        put_row(S, j, P.fg, a.out + (row0 + 2 * P.ft + j) * kHeadDim, a.part_acc, a.part_ml,
+                slot < 0 ? -1
+                         : static_cast<int64_t>(slot) * kNumQHeads + g * kGroup + 2 * P.ft + j);
+    }
+    return ok;
+  });
 }
 
 // Chunks of at most four tokens: the 16 query rows of a kv head (row = 4 token +
 // head) as M of both products, tokens and then dims as N.  Rows fg and fg + 8 of a
 // lane are of tokens fg / 4 and 2 + fg / 4.  The scores' fragment of a page is the
-// weights' of the second product as it stands.  grid (ranges, batch).  kBeside:
-// launched right after the tcgen05 kernel of the same call, as short_chunk.cu's
-// kernel is: it starts at once, and its first CTA and those without a short chunk
-// end after that grid.
-template <int kFmt, bool kBeside>
+// weights' of the second product as it stands.  Grid: the CTAs that share the work, or
+// (short_splits, batch).  kBeside: launched right after the tcgen05 kernel of the same
+// call, as short_chunk.cu's kernel is: it starts at once, and its first CTA and those
+// without pages end after that grid.
+constexpr int kShortRows = kShortTokens * kGroup;
+
+// A short chunk and the pages that some row of it sees: those of the sinks, then those
+// of the windows (no pages, and no tokens, of a sequence without a short chunk).
+struct ShortList {
+  int o0, nt, pos0, ns, w0, n;
+  __device__ __forceinline__ int page(int i) const { return i < ns ? i : w0 + (i - ns); }
+  __device__ __forceinline__ ShortList(const MaskedArgs& a, int b, bool report,
+                                       bool report_offsets) {
+    o0 = a.token_offsets[b];
+    const int o1 = a.token_offsets[b + 1];
+    const bool bad = o0 < 0 || o1 < o0 || o1 > a.num_tokens;
+    if (bad && report_offsets) record_error(a.dev_err, kErrOffsets);
+    nt = bad || o1 - o0 > kShortTokens ? 0 : o1 - o0;
+    pos0 = ns = w0 = n = 0;
+    if (nt == 0) return;
+    const int L = clamped_len(a, b, report);
+    pos0 = L - nt;
+    if (pos0 < 0 && report) record_error(a.dev_err, kErrPosition);
+    const int first = max(pos0, 0), lo = first >= a.window ? first - a.window + 1 : 0;
+    w0 = lo / kPageSize;
+    ns = min((min(a.sinks, lo) + kPageSize - 1) / kPageSize, w0);
+    n = L > 0 ? ns + (L + kPageSize - 1) / kPageSize - w0 : 0;
+  }
+};
+
+template <int kFmt, bool kBeside, bool kShared>
 __global__ void __launch_bounds__(kThreads, kCtas)
     paged8_short_chunk_kernel(const __grid_constant__ CUtensorMap map, const MaskedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, g = tid >> 5;
-  const int split = blockIdx.x, b = blockIdx.y;
   const Ring R = make_ring(smem_raw, &map);
   if constexpr (!kBeside) wait_for_prior_grids();
   allow_dependent_grids();
-  const int o0 = a.token_offsets[b], o1 = a.token_offsets[b + 1];
-  const bool bad_offsets = o0 < 0 || o1 < o0 || o1 > a.num_tokens;
-  if (bad_offsets && !kBeside && tid == 0) record_error(a.dev_err, kErrOffsets);
-  if (bad_offsets || o1 == o0 || o1 - o0 > kShortTokens) {
-    if constexpr (kBeside) wait_for_prior_grids();
-    return;
-  }
-  const int nt = o1 - o0;
-  const int L = clamped_len(a, b, tid == 0 && split == 0);
-  const int pos0 = L - nt;
-  if (pos0 < 0 && tid == 0 && split == 0) record_error(a.dev_err, kErrPosition);
-  // pages that some row sees: those of the sinks, then those of the windows
-  const int end = pos0 + nt, p_first = max(pos0, 0);
-  const int lo = p_first >= a.window ? p_first - a.window + 1 : 0;
-  const int w0 = lo / kPageSize;
-  const int ns = min((min(a.sinks, lo) + kPageSize - 1) / kPageSize, w0);
-  const int pages = end > 0 ? ns + (end + kPageSize - 1) / kPageSize - w0 : 0;
-  const int r0 = static_cast<int>(static_cast<int64_t>(pages) * split / a.short_splits);
-  const int r1 = static_cast<int>(static_cast<int64_t>(pages) * (split + 1) / a.short_splits);
+  const bool report = blockIdx.x == 0 && (kShared || tid == 0);
+  auto make = [&](int b) { return ShortList(a, b, report, !kBeside && report); };
+  Part part = {0, 0, 0, 0};
+  if constexpr (kShared) part = share_out(a, make);
+  Turn T;
   if (g == kWarps) {
-    load_pages(R, &map, a, b, r0, r1, lane, [&](int i) { return i < ns ? i : w0 + (i - ns); });
-    if (kBeside && blockIdx.x == 0 && blockIdx.y == 0) wait_for_prior_grids();
+    int k = 0;
+    each_segment<kShared>(a.short_splits, part, make,
+                 [&](int b, const ShortList& V, int r0, int r1, int) {
+                   const bool ok = load_pages(R, &map, a, b, V, r0, r1, lane, T, k);
+                   if (!ok && lane == 0) record_error(a.dev_err, kErrTimeout);
+                   return ok;
+                 });
+    drain(R, k);
+    if (kBeside && ((blockIdx.x == 0 && blockIdx.y == 0) || k == 0)) wait_for_prior_grids();
     return;
   }
 
+  // (while the first copies are on their way)
+  if constexpr (kShared)
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+      const ShortList V = make(b);
+      for (int t = 0; t < V.nt && V.n == 0; ++t)
+        put_zeros(a.out + (static_cast<int64_t>(V.o0 + t) * kNumQHeads + g * kGroup) * kHeadDim,
+                  lane);
+    }
   const Lane P(lane);
-  uint32_t qa[4][4];  // A fragments: [k-step][row fg, fg + 8 of dims {0, 1}, then {2, 3}]
-  float c[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  each_segment<kShared>(a.short_splits, part, make, [&](int b, const ShortList& V, int r0, int r1,
+                                                  int slot) {
+    const int nt = V.nt, o0 = V.o0, pos0 = V.pos0, end = V.pos0 + V.nt;
+    if (nt == 0) return true;
+    uint32_t qa[4][4];  // A fragments: [k-step][row fg, fg + 8 of dims {0, 1}, then {2, 3}]
+    float c[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int tok = 2 * i + (P.fg >> 2);
-    uint32_t qb[4][2];
-    c[i] = a.scale_log2 *
-           load_q(tok < nt ? a.q + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup +
-                                    (P.fg & 3)) * kHeadDim
-                           : nullptr,
-                  P.ft, qb);
+    for (int i = 0; i < 2; ++i) {
+      const int tok = 2 * i + (P.fg >> 2);
+      uint32_t qb[4][2];
+      c[i] = a.scale_log2 *
+             load_q(tok < nt ? a.q + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup +
+                                      (P.fg & 3)) * kHeadDim
+                             : nullptr,
+                    P.ft, qb);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      qa[kk][i] = qb[kk][0];
-      qa[kk][2 + i] = qb[kk][1];
+      for (int kk = 0; kk < 4; ++kk) {
+        qa[kk][i] = qb[kk][0];
+        qa[kk][2 + i] = qb[kk][1];
+      }
     }
-  }
-  float2 o[8][2];  // dims 8 nt + 2 ft, + 1 of rows fg and fg + 8
+    bool ok = true;
+    float2 o[8][2];  // dims 8 nt + 2 ft, + 1 of rows fg and fg + 8
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
-  // bits of a page's slots below token x (as a distance from the page's first)
-  auto below = [](int64_t x) {
-    return x <= 0 ? 0u : (x >= kPageSize ? 0xFFFFu : (1u << static_cast<int>(x)) - 1u);
-  };
-  // tokens of the page at `base` that positions p0 to p1 see, taken together
-  auto seen_by = [&](int base, int p0, int p1) {
-    return below(static_cast<int64_t>(p1) + 1 - base) &
-           ((0xFFFFu & ~below(static_cast<int64_t>(p0) - a.window + 1 - base)) |
-            below(static_cast<int64_t>(a.sinks) - base));
-  };
-  Turn T;
-  for (int k = 0; k < r1 - r0; ++k, T.next()) {
-    const int st = T.stage;
-    const bool ready = mbar_wait_bounded(R.full(st), T.phase, a.wait_ns);
-    if (!__all_sync(kFull, ready)) {
-      if (lane == 0) record_error(a.dev_err, kErrTimeout);
-      break;
-    }
-    const uint2 meta = lds64(R.meta(st));
-    if (static_cast<int>(meta.y) >= 0) {
-      const uint32_t kt = R.page(st) + g * kBlockBytes, vt = kt + kNumKvHeads * kBlockBytes;
-      const float sk = scale_value(lds8(R.scales(st) + g));
-      const float sv = scale_value(lds8(R.scales(st) + kNumKvHeads + g));
-      const int base = static_cast<int>(meta.x) * kPageSize;
-      // does every row see the whole page?
-      const bool whole = base + kPageSize - 1 <= pos0 &&
-                         (static_cast<int64_t>(base) > static_cast<int64_t>(end) - 1 - a.window ||
-                          base + kPageSize <= a.sinks);
-      // s[j][2 i + e]: row fg + 8 i, token 4 ft + 2 j + e
-      float s[2][4];
-      {
-        const uint4 x = lds128(kt + P.k0), y = lds128(kt + P.k1);
-        const uint32_t k0[4] = {x.x, x.y, x.z, x.w}, k1[4] = {y.x, y.y, y.z, y.w};
+    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
+    // bits of a page's slots below token x (as a distance from the page's first)
+    auto below = [](int64_t x) {
+      return x <= 0 ? 0u : (x >= kPageSize ? 0xFFFFu : (1u << static_cast<int>(x)) - 1u);
+    };
+    // tokens of the page at `base` that positions p0 to p1 see, taken together
+    auto seen_by = [&](int base, int p0, int p1) {
+      return below(static_cast<int64_t>(p1) + 1 - base) &
+             ((0xFFFFu & ~below(static_cast<int64_t>(p0) - a.window + 1 - base)) |
+              below(static_cast<int64_t>(a.sinks) - base));
+    };
+    for (int k = 0; k < r1 - r0; ++k, T.next()) {
+      const int st = T.stage;
+      const bool ready = mbar_wait_bounded(R.full(st), T.phase, a.wait_ns);
+      if (!__all_sync(kFull, ready)) {
+        if (lane == 0) record_error(a.dev_err, kErrTimeout);
+        ok = false;
+        break;
+      }
+      const uint2 meta = lds64(R.meta(st));
+      if (static_cast<int>(meta.y) >= 0) {
+        const uint32_t kt = R.page(st) + g * kBlockBytes, vt = kt + kNumKvHeads * kBlockBytes;
+        const float sk = scale_value(lds8(R.scales(st) + g));
+        const float sv = scale_value(lds8(R.scales(st) + kNumKvHeads + g));
+        const int base = static_cast<int>(meta.x) * kPageSize;
+        // does every row see the whole page?
+        const bool whole = base + kPageSize - 1 <= pos0 &&
+                           (static_cast<int64_t>(base) > static_cast<int64_t>(end) - 1 - a.window ||
+                            base + kPageSize <= a.sinks);
+        // s[j][2 i + e]: row fg + 8 i, token 4 ft + 2 j + e
+        float s[2][4];
+        {
+          const uint4 x = lds128(kt + P.k0), y = lds128(kt + P.k1);
+          const uint32_t k0[4] = {x.x, x.y, x.z, x.w}, k1[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          uint32_t b0, b1, d0, d1;
-          decode_f16<kFmt>(k0[kk], b0, b1);
-          decode_f16<kFmt>(k1[kk], d0, d1);
-          if (kk == 0) {
-            mma_new(s[0], qa[kk], b0, b1);
-            mma_new(s[1], qa[kk], d0, d1);
-          } else {
-            mma_add(s[0], qa[kk], b0, b1);
-            mma_add(s[1], qa[kk], d0, d1);
+          for (int kk = 0; kk < 4; ++kk) {
+            uint32_t b0, b1, d0, d1;
+            decode_f16<kFmt>(k0[kk], b0, b1);
+            decode_f16<kFmt>(k1[kk], d0, d1);
+            if (kk == 0) {
+              mma_new(s[0], qa[kk], b0, b1);
+              mma_new(s[1], qa[kk], d0, d1);
+            } else {
+              mma_add(s[0], qa[kk], b0, b1);
+              mma_add(s[1], qa[kk], d0, d1);
+            }
           }
         }
-      }
-      const float f[2] = {c[0] * sk, c[1] * sk};
+        const float f[2] = {c[0] * sk, c[1] * sk};
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] *= f[e >> 1];
-      if (!whole) {
+          for (int e = 0; e < 4; ++e) s[j][e] *= f[e >> 1];
+        if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int p = pos0 + 2 * i + (P.fg >> 2);
-          const uint32_t vis = seen_by(base, p, p) >> (4 * P.ft);
+          for (int i = 0; i < 2; ++i) {
+            const int p = pos0 + 2 * i + (P.fg >> 2);
+            const uint32_t vis = seen_by(base, p, p) >> (4 * P.ft);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!((vis >> (2 * j + e)) & 1u)) s[j][2 * i + e] = -INFINITY;
+              for (int e = 0; e < 2; ++e)
+                if (!((vis >> (2 * j + e)) & 1u)) s[j][2 * i + e] = -INFINITY;
+          }
+          if constexpr (kFmt == kKv8E4m3) hide_v(vt, seen_by(base, pos0, end - 1), lane);
         }
-        if constexpr (kFmt == kKv8E4m3) hide_v(vt, seen_by(base, pos0, end - 1), lane);
-      }
-      // the running reference of both rows
-      float mx[2];
+        // the running reference of both rows
+        float mx[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-      if (__any_sync(kFull, mx[0] > m[0] + kMoveLog2 || mx[1] > m[1] + kMoveLog2)) {
+        for (int i = 0; i < 2; ++i)
+          mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        if (__any_sync(kFull, mx[0] > m[0] + kMoveLog2 || mx[1] > m[1] + kMoveLog2)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
-          const float top = fmaxf(m[i], mx[i]);
-          const float alpha = fast_exp2(m[i] - fmaxf(top, kLowestFloat));
-          l[i] *= alpha;
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
+            const float top = fmaxf(m[i], mx[i]);
+            const float alpha = fast_exp2(m[i] - fmaxf(top, kLowestFloat));
+            l[i] *= alpha;
 #pragma unroll
-          for (int d = 0; d < 8; ++d) o[d][i] = fmul2(o[d][i], make_float2(alpha, alpha));
-          m[i] = top;
+            for (int d = 0; d < 8; ++d) o[d][i] = fmul2(o[d][i], make_float2(alpha, alpha));
+            m[i] = top;
+          }
+        }
+        // weights as two f16 terms
+        uint32_t hi[4], lo2[4];  // A fragments: row fg of tokens {0, 1}, row fg + 8, then {2, 3}
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float d = kLift - fmaxf(m[i], kLowestFloat);
+            const float p0 = fast_exp2(s[j][2 * i] + d), p1 = fast_exp2(s[j][2 * i + 1] + d);
+            l[i] += p0 + p1;
+            const uint32_t w = pack_f16x2(p0, p1);
+            const float2 r = f16x2_to_float2(w);
+            hi[2 * j + i] = w;
+            lo2[2 * j + i] = pack_f16x2(p0 - r.x, p1 - r.y);
+          }
+        uint32_t vb[8];
+        ldsm_b8_trans(vt + P.v0, *reinterpret_cast<uint32_t(*)[4]>(&vb[0]));
+        ldsm_b8_trans(vt + P.v1, *reinterpret_cast<uint32_t(*)[4]>(&vb[4]));
+        const float2 s2 = make_float2(sv, sv);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          uint32_t b0, b1;
+          decode_f16<kFmt>(vb[d], b0, b1);
+          float t[4];
+          mma_new(t, hi, b0, b1);
+          mma_add(t, lo2, b0, b1);
+          o[d][0] = ffma2(make_float2(t[0], t[1]), s2, o[d][0]);
+          o[d][1] = ffma2(make_float2(t[2], t[3]), s2, o[d][1]);
         }
       }
-      // weights as two f16 terms
-      uint32_t hi[4], lo2[4];  // A fragments: row fg of tokens {0, 1}, row fg + 8, then {2, 3}
+      __syncwarp();
+      if (lane == 0) mbar_arrive(R.empty(st));
+    }
+
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(kFull, l[i], 1);
+      l[i] += __shfl_xor_sync(kFull, l[i], 2);
+      const int tok = 2 * i + (P.fg >> 2), h = P.fg & 3;
+      if (tok >= nt) continue;
+      if (slot >= 0) {
+        const int64_t row =
+            (static_cast<int64_t>(slot) * kNumKvHeads + g) * kShortRows + tok * kGroup + h;
+        float2* dst = reinterpret_cast<float2*>(a.short_acc + row * kHeadDim) + P.ft;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float d = kLift - fmaxf(m[i], kLowestFloat);
-          const float p0 = fast_exp2(s[j][2 * i] + d), p1 = fast_exp2(s[j][2 * i + 1] + d);
-          l[i] += p0 + p1;
-          const uint32_t w = pack_f16x2(p0, p1);
-          const float2 r = f16x2_to_float2(w);
-          hi[2 * j + i] = w;
-          lo2[2 * j + i] = pack_f16x2(p0 - r.x, p1 - r.y);
-        }
-      uint32_t vb[8];
-      ldsm_b8_trans(vt + P.v0, *reinterpret_cast<uint32_t(*)[4]>(&vb[0]));
-      ldsm_b8_trans(vt + P.v1, *reinterpret_cast<uint32_t(*)[4]>(&vb[4]));
-      const float2 s2 = make_float2(sv, sv);
+        for (int d = 0; d < 8; ++d) dst[4 * d] = o[d][i];
+        if (P.ft == 0) *reinterpret_cast<float2*>(a.short_ml + 2 * row) = make_float2(m[i], l[i]);
+      } else {
+        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+                            a.out + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + h) *
+                                        kHeadDim) + P.ft;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        uint32_t b0, b1;
-        decode_f16<kFmt>(vb[d], b0, b1);
-        float t[4];
-        mma_new(t, hi, b0, b1);
-        mma_add(t, lo2, b0, b1);
-        o[d][0] = ffma2(make_float2(t[0], t[1]), s2, o[d][0]);
-        o[d][1] = ffma2(make_float2(t[2], t[3]), s2, o[d][1]);
+        for (int d = 0; d < 8; ++d) dst[4 * d] = pack_bf16x2(o[d][i].x * inv, o[d][i].y * inv);
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(R.empty(st));
-  }
+    return ok;
+  });
+}
 
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(kFull, l[i], 1);
-    l[i] += __shfl_xor_sync(kFull, l[i], 2);
-    const int tok = 2 * i + (P.fg >> 2), h = P.fg & 3;
-    if (tok >= nt) continue;
-    if (a.short_splits > 1) {
-      const int64_t part = short_part_row(b, g, tok * kGroup + h) * a.short_splits + split;
-      float2* dst = reinterpret_cast<float2*>(a.short_acc + part * kHeadDim) + P.ft;
-#pragma unroll
-      for (int d = 0; d < 8; ++d) dst[4 * d] = o[d][i];
-      if (P.ft == 0) *reinterpret_cast<float2*>(a.short_ml + 2 * part) = make_float2(m[i], l[i]);
-    } else {
-      const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(
-                          a.out + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + h) *
-                                      kHeadDim) + P.ft;
-#pragma unroll
-      for (int d = 0; d < 8; ++d) dst[4 * d] = pack_bf16x2(o[d][i].x * inv, o[d][i].y * inv);
+// The partial results of a sequence's rows: how many, and the place of each.
+template <bool kShared>
+struct Pieces {
+  int n;                       // 1 where the sequence has none: it was answered at once
+  int64_t first, base, total, parts;
+  __device__ __forceinline__ Pieces(const MaskedArgs& a, int num_splits, int b) {
+    n = num_splits;
+    first = static_cast<int64_t>(b) * num_splits;
+    if constexpr (kShared) {
+      base = a.part_bases[b];
+      total = a.part_bases[a.batch];
+      const int64_t past = a.part_bases[b + 1];
+      n = 1;
+      if (past == base) return;
+      parts = parts_of(total, a.part_ctas);
+      // the part that holds page u is the last one that starts at or before it
+      first = ((base + 1) * parts - 1) / total;
+      n = static_cast<int>((past * parts - 1) / total - first) + 1;
     }
   }
+  __device__ __forceinline__ int slot(int i) const {
+    const int64_t c = first + i;
+    if constexpr (kShared)
+      return static_cast<int>(2 * c + (part_start(total, parts, c) < base ? 1 : 0));
+    return static_cast<int>(c);
+  }
+};
+
+// Row r of sequence b (decode: query head; chunks: kv head, token, head of the group)
+// in the partial results and in the output; false: there is no such row.
+template <bool kChunk>
+__device__ __forceinline__ bool merged_row(const MaskedArgs& a, int b, int r, uint16_t*& out) {
+  if constexpr (kChunk) {
+    const int o0 = a.token_offsets[b], o1 = a.token_offsets[b + 1];
+    const int g = r / kShortRows, tok = r % kShortRows / kGroup, h = r % kGroup;
+    if (o0 < 0 || o1 > a.num_tokens || o1 <= o0 || o1 - o0 > kShortTokens || tok >= o1 - o0)
+      return false;
+    out = a.out + (static_cast<int64_t>(o0 + tok) * kNumQHeads + g * kGroup + h) * kHeadDim;
+  } else {
+    out = a.out + (static_cast<int64_t>(b) * kNumQHeads + r) * kHeadDim;
+  }
+  return true;
 }
 
-// Combine a row's ranges, added in an order that does not change.  Up to kFewRanges
-// of them a warp to a row; more take a CTA to a row, warp w the ranges w, w +
-// kMergeWarps, ... (each step of a sum is an L2 latency: the 304 ranges of one
-// sequence of 30011 tokens took 33 us with one warp, 9 with eight and a maximum over
-// all ranges first).
-constexpr int kMergeRows = 4, kMergeWarps = 16, kFewRanges = 16;
-__global__ void __launch_bounds__(32 * kMergeRows) merge8_few_kernel(const MaskedArgs a) {
+// Combine a row's partial results, added in an order that does not change.  Where few
+// are expected a warp takes a row; else a CTA does, warp w the results w, w +
+// kMergeWarps, ... (each step of a sum is an L2 latency: 304 of one sequence of 30011
+// tokens took 33 us with one warp).  grid (rows / 4 or rows, batch).
+constexpr int kMergeRows = 4, kMergeWarps = 16, kFewPieces = 16;
+template <bool kChunk, bool kShared, int kWarpsOfRow>
+__global__ void __launch_bounds__(32 * (kWarpsOfRow == 1 ? kMergeRows : kWarpsOfRow))
+    merge8_kernel(const MaskedArgs a) {
+  constexpr bool kMany = kWarpsOfRow > 1;
+  constexpr int kRows = kChunk ? kNumKvHeads * kShortRows : kNumQHeads;
+  __shared__ float2 s_ml[kWarpsOfRow];
+  __shared__ float2 s_o[kWarpsOfRow][kHeadDim / 2];
   allow_dependent_grids();
   wait_for_prior_grids();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.num_splits;
-  const float2* acc =
-      reinterpret_cast<const float2*>(a.part_acc) + row * a.num_splits * (kHeadDim / 2) + lane;
-  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] =
-      merge_ranges(ml, acc, a.num_splits, lane);
-}
-
-__global__ void __launch_bounds__(32 * kMergeWarps) merge8_many_kernel(const MaskedArgs a) {
-  __shared__ float2 s_ml[kMergeWarps];
-  __shared__ float2 s_o[kMergeWarps][kHeadDim / 2];
-  allow_dependent_grids();
-  wait_for_prior_grids();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, splits = a.num_splits;
-  const int64_t row = blockIdx.x;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * splits;
-  const float2* acc =
-      reinterpret_cast<const float2*>(a.part_acc) + row * splits * (kHeadDim / 2) + lane;
-  // this warp's state; a range that saw no token has a sum of 0
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
+  const int r = kMany ? blockIdx.x : blockIdx.x * kMergeRows + warp, w = kMany ? warp : 0;
+  const int num_splits = kChunk ? a.short_splits : a.num_splits;
+  // (a row that is not there is left when the loads are on their way)
+  uint16_t* out;
+  const bool there = merged_row<kChunk>(a, b, r, out);
+  const Pieces<kShared> P(a, num_splits, b);
+  if (P.n == 1) return;
+  const float2* all_ml = reinterpret_cast<const float2*>(kChunk ? a.short_ml : a.part_ml) + r;
+  const float2* all_acc = reinterpret_cast<const float2*>(kChunk ? a.short_acc : a.part_acc) +
+                          static_cast<int64_t>(r) * (kHeadDim / 2) + lane;
+  // this warp's state; a result that saw no token has a sum of 0
   float M = -INFINITY, L = 0.f;
   float2 O = make_float2(0.f, 0.f);
 #pragma unroll 1
-  for (int s0 = w; s0 < splits; s0 += 32 * kMergeWarps) {
-    // lane i: (max, sum) of range s0 + i kMergeWarps
-    const int mine = s0 + lane * kMergeWarps;
-    const float2 x = mine < splits ? __ldcg(ml + mine) : make_float2(-INFINITY, 0.f);
+  for (int s0 = w; s0 < P.n; s0 += 32 * kWarpsOfRow) {
+    // lane i: the place, and (max, sum), of result s0 + i kWarpsOfRow
+    const int mine = s0 + lane * kWarpsOfRow;
+    const int at = mine < P.n ? P.slot(mine) : 0;
+    const float2 x = mine < P.n ? __ldcg(all_ml + static_cast<int64_t>(at) * kRows)
+                                : make_float2(-INFINITY, 0.f);
+    // (of 16 results at most, half at a time leaves registers for more warps)
+    constexpr int kAhead = kMany || kShared ? 16 : 8;
+    float2 v[kAhead];
+    auto load = [&](int e0) {
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const int64_t place = __shfl_sync(kFull, at, e0 + e);
+        v[e] = s0 + (e0 + e) * kWarpsOfRow < P.n
+                   ? __ldcg(all_acc + place * (kRows * kHeadDim / 2))
+                   : make_float2(0.f, 0.f);
+      }
+    };
+    load(0);
+    if (!there) return;  // (the same for a row's warps)
     float top = x.y != 0.f ? x.x : -INFINITY;
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
@@ -752,43 +987,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge8_many_kernel(const Mas
     O.y *= old;
     M = top;
 #pragma unroll 1
-    for (int e0 = 0; e0 < 32 && s0 + e0 * kMergeWarps < splits; e0 += 16) {
-      float2 v[16];
+    for (int e0 = 0;;) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int s = s0 + (e0 + e) * kMergeWarps;
-        v[e] = s < splits ? __ldcg(acc + static_cast<int64_t>(s) * (kHeadDim / 2))
-                          : make_float2(0.f, 0.f);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < kAhead; ++e) {
         const float f = __shfl_sync(kFull, wt, e0 + e);
         if (f != 0.f) {  // (what a range without tokens left is not read)
           O.x = fmaf(v[e].x, f, O.x);
           O.y = fmaf(v[e].y, f, O.y);
         }
       }
+      e0 += kAhead;
+      if (e0 == 32 || s0 + e0 * kWarpsOfRow >= P.n) break;
+      load(e0);
     }
   }
-  s_o[w][lane] = O;
-  if (lane == 0) s_ml[w] = make_float2(M, L);
-  __syncthreads();
-  if (w > 0) return;
-  float top = -INFINITY;
+  if constexpr (kMany) {
+    s_o[w][lane] = O;
+    if (lane == 0) s_ml[w] = make_float2(M, L);
+    __syncthreads();
+    if (w > 0) return;
+    float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) top = fmaxf(top, s_ml[i].x);
-  L = 0.f;
-  O = make_float2(0.f, 0.f);
+    for (int i = 0; i < kWarpsOfRow; ++i) top = fmaxf(top, s_ml[i].x);
+    L = 0.f;
+    O = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) {
-    if (s_ml[i].y == 0.f) continue;
-    const float f = s_ml[i].x == -INFINITY ? 1.f : fast_exp2(s_ml[i].x - top);
-    L = fmaf(s_ml[i].y, f, L);
-    O.x = fmaf(s_o[i][lane].x, f, O.x);
-    O.y = fmaf(s_o[i][lane].y, f, O.y);
+    for (int i = 0; i < kWarpsOfRow; ++i) {
+      if (s_ml[i].y == 0.f) continue;
+      const float f = s_ml[i].x == -INFINITY ? 1.f : fast_exp2(s_ml[i].x - top);
+      L = fmaf(s_ml[i].y, f, L);
+      O.x = fmaf(s_o[i][lane].x, f, O.x);
+      O.y = fmaf(s_o[i][lane].y, f, O.y);
+    }
   }
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  reinterpret_cast<uint32_t*>(a.out + row * kHeadDim)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
+  reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16x2(O.x * inv, O.y * inv);
+}
+
+template <bool kChunk, bool kShared>
+cudaError_t launch_merge(const MaskedArgs& a, int pieces, cudaStream_t stream) {
+  constexpr int kRows = kChunk ? kNumKvHeads * kShortRows : kNumQHeads;
+  if (pieces > kFewPieces)
+    return launch_pdl(merge8_kernel<kChunk, kShared, kMergeWarps>, dim3(kRows, a.batch),
+                      dim3(32 * kMergeWarps), 0, stream, a);
+  return launch_pdl(merge8_kernel<kChunk, kShared, 1>, dim3(kRows / kMergeRows, a.batch),
+                    dim3(32 * kMergeRows), 0, stream, a);
 }
 
 // Launch a streaming kernel, opting in to its shared memory once per device.
@@ -805,34 +1048,47 @@ cudaError_t launch(const CUtensorMap& map, const MaskedArgs& a, int splits, cuda
     if (err != cudaSuccess) return err;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch_pdl(kKernel, dim3(splits, a.batch), dim3(kThreads), kSmem, stream, map, a);
+  return launch_pdl(kKernel, splits > 0 ? dim3(splits, a.batch) : dim3(a.part_ctas), dim3(kThreads),
+                    kSmem, stream, map, a);
+}
+
+// (shared: the pieces of a sequence where all are of a length)
+template <int kFmt>
+cudaError_t launch_decode(const CUtensorMap& map, const MaskedArgs& a, cudaStream_t stream) {
+  const int n = a.num_splits;
+  const cudaError_t err = n > 0 ? launch<paged8_decode_kernel<kFmt, false>>(map, a, n, stream)
+                                : launch<paged8_decode_kernel<kFmt, true>>(map, a, n, stream);
+  if (err != cudaSuccess || n == 1) return err;
+  return n > 0 ? launch_merge<false, false>(a, n, stream)
+               : launch_merge<false, true>(a, a.part_ctas / a.batch, stream);
+}
+
+template <int kFmt, bool kBeside>
+cudaError_t launch_short(const CUtensorMap& map, const MaskedArgs& a, cudaStream_t stream) {
+  const int n = a.short_splits;
+  const cudaError_t err =
+      n > 0 ? launch<paged8_short_chunk_kernel<kFmt, kBeside, false>>(map, a, n, stream)
+            : launch<paged8_short_chunk_kernel<kFmt, kBeside, true>>(map, a, n, stream);
+  if (err != cudaSuccess || n == 1) return err;
+  return n > 0 ? launch_merge<true, false>(a, n, stream)
+               : launch_merge<true, true>(a, a.part_ctas / a.batch, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
                            cudaStream_t stream) {
-  const cudaError_t err =
-      format == kKv8E4m3
-          ? launch<paged8_decode_kernel<kKv8E4m3>>(page_map, args, args.num_splits, stream)
-          : launch<paged8_decode_kernel<kKv8Int8>>(page_map, args, args.num_splits, stream);
-  if (err != cudaSuccess || args.num_splits == 1) return err;
-  static_assert(kNumQHeads % kMergeRows == 0, "whole CTAs of rows");
-  if (args.num_splits > kFewRanges)
-    return launch_pdl(merge8_many_kernel, dim3(args.batch * kNumQHeads), dim3(32 * kMergeWarps), 0,
-                      stream, args);
-  return launch_pdl(merge8_few_kernel, dim3(args.batch * (kNumQHeads / kMergeRows)),
-                    dim3(32 * kMergeRows), 0, stream, args);
+  return format == kKv8E4m3 ? launch_decode<kKv8E4m3>(page_map, args, stream)
+                            : launch_decode<kKv8Int8>(page_map, args, stream);
 }
 
 cudaError_t launch_short_chunks8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
                                  bool beside, cudaStream_t stream) {
-  const int n = args.short_splits;
   if (format == kKv8E4m3)
-    return beside ? launch<paged8_short_chunk_kernel<kKv8E4m3, true>>(page_map, args, n, stream)
-                  : launch<paged8_short_chunk_kernel<kKv8E4m3, false>>(page_map, args, n, stream);
-  return beside ? launch<paged8_short_chunk_kernel<kKv8Int8, true>>(page_map, args, n, stream)
-                : launch<paged8_short_chunk_kernel<kKv8Int8, false>>(page_map, args, n, stream);
+    return beside ? launch_short<kKv8E4m3, true>(page_map, args, stream)
+                  : launch_short<kKv8E4m3, false>(page_map, args, stream);
+  return beside ? launch_short<kKv8Int8, true>(page_map, args, stream)
+                : launch_short<kKv8Int8, false>(page_map, args, stream);
 }
 
 }  // namespace pkv

@@ -1451,18 +1451,50 @@ bool pool8_map(const void* pool, int64_t num_pages, CUtensorMap* out) {
   return true;
 }
 
-// Ranges of `units` sequences of at most `pages` pages, one CTA for all kv heads
-// each: CTAs for two an SM, but four pages a range or more.
-int stream8_splits(long long units, long long pages, int num_splits) {
-  if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, pages));
+// How the streaming kernels over the 8-bit cache divide the work: ranges of each
+// sequence, or (splits 0) the CTAs share the batch's pages; the partial results, `rows`
+// rows each, and the bytes of these and of the sequences' bases.
+struct Stream8Plan {
+  int splits, ctas;
+  size_t parts, bytes;
+};
+
+// `units` sequences of at most `pages` pages, `batch` places of them.
+bool stream8_plan(int batch, long long units, long long pages, int num_splits, int rows,
+                  Stream8Plan* plan) {
   const int sms = current_sm_count();
-  if (sms <= 0) return -1;
-  return static_cast<int>(std::max(1LL, std::min(2LL * sms / std::max(units, 1LL), pages / 4)));
+  if (sms <= 0) return false;
+  plan->ctas = pkv::kStream8Ctas * sms;
+  // Shared where the table has room for that many pages a CTA: lengths are the kernel's
+  // to read, and may be far from the table's width.  128 sequences, one of 16000 tokens
+  // and the rest of 500: 33 us shared, 404 with a CTA each, 68 with the best number of
+  // ranges (16); 64 of 50 to 6350: 51 and 53 (8 ranges); 256 of 1024 to 2048: 76 and 81
+  // (a CTA each).  Sharing costs 3 to 4 us (a sum of the lengths before, a merge after),
+  // more than it saves below: 128 windows of 1000 tokens 34 us, 31 in two ranges each,
+  // 64 x 4 new tokens over 1024 to 2048 45 and 41.  Many short sequences lose a little
+  // (1000 of 250 to 500: 90 and 80).
+  constexpr long long kSharedPages = 64;
+  if (num_splits > 0)
+    plan->splits = static_cast<int>(std::min<long long>(num_splits, pages));
+  else if (units > 1 && units * pages >= kSharedPages * plan->ctas)
+    plan->splits = 0;
+  else  // a CTA each, but four pages a range or more
+    plan->splits = static_cast<int>(
+        std::max(1LL, std::min(plan->ctas / std::max(units, 1LL), pages / 4)));
+  const size_t slots = plan->splits == 0 ? 2 * static_cast<size_t>(plan->ctas)
+                       : plan->splits > 1 ? static_cast<size_t>(batch) * plan->splits
+                                          : 0;
+  plan->parts = slots * rows;
+  plan->bytes = plan->parts * (kHeadDim + 2) * sizeof(float) +
+                (plan->splits == 0 ? (static_cast<size_t>(batch) + 1) * sizeof(int64_t) : 0);
+  return true;
 }
 
-int decode8_splits(int batch, int max_blocks, int window, int sinks, int num_splits) {
-  return stream8_splits(batch, window > 0 ? window_pages(max_blocks, window, sinks) : max_blocks,
-                        num_splits);
+bool decode8_plan(int batch, int max_blocks, int window, int sinks, int num_splits,
+                  Stream8Plan* plan) {
+  return stream8_plan(batch, batch,
+                      window > 0 ? window_pages(max_blocks, window, sinks) : max_blocks,
+                      num_splits, kNumQHeads, plan);
 }
 
 // A chunk call over the 8-bit cache: chunk_plan with short chunks of one CTA for
@@ -1472,6 +1504,7 @@ int decode8_splits(int batch, int max_blocks, int window, int sinks, int num_spl
 // `per_round` pages and what the last sequence has above them.
 struct Chunk8Plan {
   ChunkPlan chunk;
+  Stream8Plan shorts;
   int rounds;
   int64_t places, per_round;
   size_t table_at, pages_at, workspace;  // bytes; the rounds' array lies before the table
@@ -1486,16 +1519,16 @@ bool chunk8_plan(int num_tokens, int batch, int max_blocks, int window, int sink
     const long long wide = static_cast<long long>(window) + tokens - 1;
     return window_pages(max_blocks, static_cast<int>(std::min<long long>(wide, INT32_MAX)), sinks);
   };
+  // the partials: the long chunks', then the short ones' and the bases
   // (more tokens than short chunks can have mean a long one, or a padded q)
   const bool a_long_one = num_tokens > pkv::kShortTokens * static_cast<long long>(batch);
-  const int splits =
-      stream8_splits(a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens),
-                     pages_of(pkv::kShortTokens), num_splits);
-  if (splits < 1) return false;
-  c.short_splits = splits;
-  c.short_parts = splits > 1 ? static_cast<size_t>(batch) * pkv::kShortTokens * kNumQHeads * splits
-                             : 0;
-  c.workspace = (c.long_parts + c.short_parts) * (kHeadDim + 2) * sizeof(float);
+  if (!stream8_plan(batch, a_long_one ? std::max(batch - 1, 1) : std::min(batch, num_tokens),
+                    pages_of(pkv::kShortTokens), num_splits,
+                    kNumKvHeads * pkv::kShortTokens * pkv::kGroup, &plan->shorts))
+    return false;
+  c.short_splits = plan->shorts.splits;
+  c.short_parts = plan->shorts.parts;
+  c.workspace = c.long_parts * (kHeadDim + 2) * sizeof(float) + plan->shorts.bytes;
   plan->rounds = 0;
   plan->places = plan->per_round = 0;
   plan->table_at = plan->pages_at = plan->workspace = c.workspace;
@@ -1633,8 +1666,10 @@ PKV_API size_t pkv_decode8_workspace_bytes(int batch, int num_q_heads, int num_k
       !supported_dims(num_q_heads, num_kv_heads, head_dim, kPageSize))
     return static_cast<size_t>(-1);
   if (batch == 0) return 0;
-  const int splits = decode8_splits(batch, max_blocks, window, sinks, num_splits);
-  return splits < 1 ? static_cast<size_t>(-1) : part_bytes(batch, splits);
+  Stream8Plan plan;
+  return decode8_plan(batch, max_blocks, window, sinks, num_splits, &plan)
+             ? plan.bytes
+             : static_cast<size_t>(-1);
 }
 
 PKV_API size_t pkv_chunk8_workspace_bytes(int num_tokens, int batch, int num_q_heads,
@@ -1672,11 +1707,11 @@ PKV_API int pkv_paged8_decode_attention(
   const Span outs[] = {heads_span(out, batch), ints(dev_err, 1)};
   if (outputs_overlap(outs, ins)) return PKV_EINVAL;
   if (batch == 0) return PKV_OK;
-  const int splits = decode8_splits(batch, max_blocks, window, sinks, num_splits);
-  if (splits < 1) return PKV_ECUDA;
-  const size_t need = part_bytes(batch, splits);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PKV_EWORKSPACE;
-  if (workspace_overlaps({workspace, need}, outs, ins)) return PKV_EINVAL;
+  Stream8Plan plan;
+  if (!decode8_plan(batch, max_blocks, window, sinks, num_splits, &plan)) return PKV_ECUDA;
+  if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes))
+    return PKV_EWORKSPACE;
+  if (workspace_overlaps({workspace, plan.bytes}, outs, ins)) return PKV_EINVAL;
   pkv::MaskedArgs a = {};
   a.q = q;
   a.scales = scales;
@@ -1690,9 +1725,11 @@ PKV_API int pkv_paged8_decode_attention(
   a.num_tokens = batch;
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
-  a.num_splits = splits;
+  a.num_splits = plan.splits;
+  a.part_ctas = plan.ctas;
   a.part_acc = static_cast<float*>(workspace);
-  a.part_ml = a.part_acc + static_cast<size_t>(batch) * kNumQHeads * splits * kHeadDim;
+  a.part_ml = a.part_acc + plan.parts * kHeadDim;
+  a.part_bases = reinterpret_cast<int64_t*>(a.part_ml + plan.parts * 2);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
   CUtensorMap map;
@@ -1749,6 +1786,8 @@ PKV_API int pkv_paged8_chunk_attention(
   a.window = window > 0 ? window : INT32_MAX;
   a.sinks = sinks;
   set_parts(a, plan.chunk, workspace);
+  a.part_ctas = plan.shorts.ctas;
+  a.part_bases = reinterpret_cast<int64_t*>(a.short_ml + plan.shorts.parts * 2);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = pkv::wait_limit_ns();
   CUtensorMap codes_map;
@@ -1792,7 +1831,6 @@ PKV_API int pkv_paged8_chunk_attention(
   }
   if (err == cudaSuccess)
     err = pkv::launch_short_chunks8(codes_map, a, cache.format, plan.rounds > 0, st);
-  if (err == cudaSuccess) err = pkv::launch_short_merge(a, st);
   if (err == cudaSuccess && plan.rounds > 0 && a.num_splits > 1)
     err = pkv::launch_chunk_merge(a, st);
   return err == cudaSuccess ? PKV_OK : PKV_ECUDA;

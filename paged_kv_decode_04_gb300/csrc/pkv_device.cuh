@@ -617,11 +617,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                : "memory");
 }
 
-// Place of query row r of (sequence, kv head) among the partials of short chunks.
-__device__ __forceinline__ int64_t short_part_row(int b, int g, int r) {
-  return (static_cast<int64_t>(b) * kNumKvHeads + g) * (kShortTokens * kGroup) + r;
-}
-
 // One warp combines a row's ranges, added in order: (max in log2 units, sum) of
 // range s at ml[s], this lane's two dims of its accumulator at acc[s * 32]
 // (not read into the result when the range saw no token).  Returns the lane's

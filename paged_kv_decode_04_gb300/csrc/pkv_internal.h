@@ -278,6 +278,8 @@ struct MaskedArgs {
   int short_splits;              // chunks: ranges of chunks of at most kShortTokens
   float* short_acc;              // partials of the short chunks, [batch][kShortTokens * 32 rows]
   float* short_ml;               // [short_splits]
+  int64_t* part_bases;           // 8-bit cache: [batch + 1] pages before each sequence
+  int part_ctas;                 // and the CTAs that share them (splits 0)
   const int32_t* rounds;         // long chunks: only sequences of this round, or nullptr
   int round;
   float scale_log2;              // softmax scale * log2(e)
@@ -301,8 +303,6 @@ cudaError_t launch_chunk_attention(const CUtensorMap& q_map, const CUtensorMap& 
 // beside: right after launch_chunk_attention, next to whose CTAs these run.
 cudaError_t launch_short_chunks(const CUtensorMap& pool_map, const MaskedArgs& args, bool beside,
                                 cudaStream_t stream);
-// That merge by itself (nothing to do for one range).
-cudaError_t launch_short_merge(const MaskedArgs& args, cudaStream_t stream);
 // Combine the ranges of the long chunks' rows (num_splits > 1).
 cudaError_t launch_chunk_merge(const MaskedArgs& args, cudaStream_t stream);
 
@@ -380,10 +380,12 @@ struct WidenArgs {
 };
 cudaError_t launch_widen(const WidenArgs& args, int num_sms, cudaStream_t stream);
 
-// Attention over the 8-bit cache (args.scales): of one token a sequence, and the
-// merge of its ranges; of chunks of at most kShortTokens tokens, with
-// launch_short_merge, where beside: right after launch_chunk_attention
-// (kv8_attention.cu).  page_map: boxes of one page's codes, 64-byte swizzled.
+// Attention over the 8-bit cache (args.scales), with the merge of partial results: of
+// one token a sequence; of chunks of at most kShortTokens tokens, where beside: right
+// after launch_chunk_attention (kv8_attention.cu).  num_splits, short_splits: ranges
+// of a sequence, or 0: args.part_ctas CTAs share the batch's pages, with two partial
+// results each.  page_map: boxes of one page's codes, 64-byte swizzled.
+constexpr int kStream8Ctas = 2;  // per SM
 cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
                            cudaStream_t stream);
 cudaError_t launch_short_chunks8(const CUtensorMap& page_map, const MaskedArgs& args, int format,

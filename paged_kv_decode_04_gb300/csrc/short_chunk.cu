@@ -117,6 +117,11 @@ __device__ __forceinline__ void fold_tile(const float (&s)[4], const uint32_t (&
   for (int mt = 0; mt < 4; ++mt) mma_16816_bf16(S.oacc[mt], va[mt], tl0, tl1);
 }
 
+// Place of query row r of (sequence, kv head) among the partials.
+__device__ __forceinline__ int64_t part_row(int b, int g, int r) {
+  return (static_cast<int64_t>(b) * kNumKvHeads + g) * kRows + r;
+}
+
 // kBeside: launched right after the tcgen05 kernel of the same call, whose
 // CTAs let this grid start only after their own wait for the prior grids and
 // write other rows: this grid starts at once.  Its first CTA waits for that one
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kStages))
     const int64_t row =
         static_cast<int64_t>(o0 + r / kGroup) * kNumQHeads + g * kGroup + r % kGroup;
     if (a.short_splits > 1) {
-      const int64_t part = short_part_row(b, g, r) * a.short_splits + split;
+      const int64_t part = part_row(b, g, r) * a.short_splits + split;
       *reinterpret_cast<float2*>(a.short_acc + part * kHeadDim + 2 * lane) = O;
       if (lane == 0) *reinterpret_cast<float2*>(a.short_ml + 2 * part) = make_float2(M, Ls);
     } else {
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(32 * kGroup) merge_short_kernel(const MaskedAr
   const int o0 = a.token_offsets[b], o1 = a.token_offsets[b + 1];
   if (o0 < 0 || o1 > a.num_tokens || o1 <= o0 || o1 - o0 > kShortTokens) return;
   if (r >= (o1 - o0) * kGroup) return;
-  const int64_t first = short_part_row(b, g, r) * a.short_splits;
+  const int64_t first = part_row(b, g, r) * a.short_splits;
   const float2* ml = reinterpret_cast<const float2*>(a.short_ml) + first;
   const float2* acc = reinterpret_cast<const float2*>(a.short_acc) + first * (kHeadDim / 2) + lane;
   const int64_t row = static_cast<int64_t>(o0 + r / kGroup) * kNumQHeads + g * kGroup + r % kGroup;
@@ -437,11 +442,7 @@ cudaError_t launch_short_chunks(const CUtensorMap& pool_map, const MaskedArgs& a
       all_short ? (beside ? launch<true, kShallow>(pool_map, args, stream)
                           : launch<false, kShallow>(pool_map, args, stream))
                 : launch<true, kDeep>(pool_map, args, stream);
-  return err != cudaSuccess ? err : launch_short_merge(args, stream);
-}
-
-cudaError_t launch_short_merge(const MaskedArgs& args, cudaStream_t stream) {
-  if (args.short_splits == 1) return cudaSuccess;
+  if (err != cudaSuccess || args.short_splits == 1) return err;
   return launch_pdl(merge_short_kernel, dim3(kNumKvHeads * kShortTokens, args.batch),
                     dim3(32 * kGroup), 0, stream, args);
 }
