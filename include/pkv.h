@@ -667,8 +667,7 @@ PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_b
  *           bits, 16-byte aligned: e4m3 floats (PKV_KV8_E4M3) or signed integers
  *           in [-127, 127] (PKV_KV8_INT8)
  *   scales  uint8 [num_pages][2][num_kv_heads], 16-byte aligned: a block's value
- *           is code * 2^(scale - 127), scale in [3, 240] (other bytes count as
- *           the nearest of these)
+ *           is code * 2^(scale - 127), scale in [3, 240]
  *
  * A block that is given rows of values x gets the scale max(need, its own scale
  * if it holds earlier tokens): need is the smallest with max |x| <= T *
@@ -681,7 +680,8 @@ PKV_API int pkv_kv_append_at(const pkv_bf16* k_new, const pkv_bf16* v_new, pkv_b
  * finite are stored as zero and set PKV_DEVERR_VALUE.  Every cached value is a
  * bf16 number: products of bf16 values with them, and pkv_kv8_read, are exact.
  * e4m3's NaN codes (0x7F and 0xFF, never written here) may lie in slots that no
- * query sees; where one is seen the sequence's results are not specified.
+ * query sees, and other scales in blocks of which none is seen; where one is seen
+ * the sequence's results are not specified.
  */
 #define PKV_KV8_E4M3 0
 #define PKV_KV8_INT8 1
@@ -734,7 +734,11 @@ PKV_API int pkv_kv8_read(const void* pool, const uint8_t* scales, int format, in
  * cache, with a sliding window and sink tokens where window > 0 (0: the whole
  * cache).  Scores and softmax are FP32, weights enter the product with V with 22
  * significant bits, the output is rounded to bf16 once.  Workspace, num_splits
- * and dev_err as there, sized by pkv_decode8_workspace_bytes().
+ * and dev_err as there, sized by pkv_decode8_workspace_bytes().  With num_splits 0
+ * and a large table the batch's pages, as seq_lens has them, are shared out evenly,
+ * whatever the sequences' lengths are; the same inputs give the same bits, but a
+ * sequence's last bits may then depend on the others' lengths (num_splits > 0: they
+ * do not).
  */
 PKV_API int pkv_paged8_decode_attention(
     const pkv_bf16* q, const void* pool, const uint8_t* scales, int format, int64_t num_pages,
@@ -751,7 +755,11 @@ PKV_API size_t pkv_decode8_workspace_bytes(int batch, int num_q_heads, int num_k
 
 /*
  * pkv_paged8_chunk_attention -- pkv_paged_chunk_attention over the 8-bit cache,
- * the same arguments and rules, sized by pkv_chunk8_workspace_bytes().
+ * the same arguments and rules, sized by pkv_chunk8_workspace_bytes().  Chunks of
+ * more than four tokens see their pages as bf16, which the workspace has room for
+ * (32 KiB a page): for all that num_tokens and the table allow, or for 2 GiB at a
+ * time, or two whole rows of the table where that is more.  num_splits 0: shorter
+ * ones share pages as in pkv_paged8_decode_attention.
  */
 PKV_API int pkv_paged8_chunk_attention(
     const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const void* pool,

@@ -1462,8 +1462,8 @@ struct Stream8Plan {
 // `units` sequences of at most `pages` pages, `batch` places of them.
 bool stream8_plan(int batch, long long units, long long pages, int num_splits, int rows,
                   Stream8Plan* plan) {
-  const int sms = current_sm_count();
-  if (sms <= 0) return false;
+  const int sms = num_splits > 0 ? 0 : current_sm_count();
+  if (num_splits == 0 && sms <= 0) return false;
   plan->ctas = pkv::kStream8Ctas * sms;
   // Shared where the table has room for that many pages a CTA: lengths are the kernel's
   // to read, and may be far from the table's width.  128 sequences, one of 16000 tokens
