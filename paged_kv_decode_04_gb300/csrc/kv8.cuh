@@ -127,19 +127,12 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
   }
 }
 
-// 16 codes times a scale's value as bf16 (exact), to `dst`.
+// 8 codes times a scale's value as bf16 (exact).
 template <int kFmt>
-__device__ __forceinline__ void widen16(const uint4& codes, float scale, uint4* dst) {
-  const uint32_t x[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 y = decode4<kFmt>(x[i]);
-    o[2 * i] = pack_bf16x2(y.x * scale, y.y * scale);
-    o[2 * i + 1] = pack_bf16x2(y.z * scale, y.w * scale);
-  }
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+__device__ __forceinline__ uint4 widen8(const uint2& codes, float scale) {
+  const float4 a = decode4<kFmt>(codes.x), b = decode4<kFmt>(codes.y);
+  return make_uint4(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(a.z * scale, a.w * scale),
+                    pack_bf16x2(b.x * scale, b.y * scale), pack_bf16x2(b.z * scale, b.w * scale));
 }
 
 // A warp rounds the first `rows` tokens of a block again, under a scale larger

@@ -10,8 +10,8 @@
 // the softmax for issue slots and shared memory; 64 x 16 tokens over 2048, bound by
 // memory, took 106 us there.
 //
-// One CTA to a page, warp h of it for kv head h, lane 4 r + q the codes [16 q, 16 q
-// + 16) of slots r and r + 8.  The pages are counted on through the batch (a scan
+// One CTA to a page, warp h of it for kv head h, lane 8 r + q the codes [8 q, 8 q + 8)
+// of slots r, r + 4, r + 8 and r + 12.  The pages are counted on through the batch (a scan
 // of the lengths in every CTA), so their places follow from the sizes alone.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -109,19 +109,20 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const WidenArgs a) {
       const bool good = pid >= 0 && pid < c.num_pages;
       if (tid == 0) a.table[at] = good ? static_cast<int32_t>(place) : -1;
       if (!good) continue;  // (reported where it is read)
-      const int r = lane >> 2, q = lane & 3;
+      const int r = lane >> 3, q = lane & 7;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint4* src = reinterpret_cast<const uint4*>(c.pool + block_at(pid, kv, h)) + lane;
-        const uint4 w[2] = {__ldcs(src), __ldcs(src + 32)};
+        const uint2* src = reinterpret_cast<const uint2*>(c.pool + block_at(pid, kv, h)) + lane;
+        uint2 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldcs(src + 32 * i);
         const float f = scale_value(stored_scale(c.scales[scale_at(pid, kv, h)]));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint4* dst = reinterpret_cast<uint4*>(
-              a.pages + (((place * 2 + kv) * kPageSize + r + 8 * i) * kNumKvHeads + h) * kHeadDim +
-              16 * q);
-          widen16<kFmt>(w[i], f, dst);
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(
+              a.pages +
+              (((place * 2 + kv) * kPageSize + r + 4 * i) * kNumKvHeads + h) * kHeadDim + 8 * q) =
+              widen8<kFmt>(w[i], f);
       }
     }
     before = total;
