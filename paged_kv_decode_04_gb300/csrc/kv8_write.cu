@@ -46,6 +46,13 @@ __device__ __forceinline__ Angle make_angle(double c, double s) {
   return t;
 }
 
+// x + y and what rounding it left.
+__device__ __forceinline__ float two_sum(float x, float y, float& e) {
+  const float h = __fadd_rn(x, y), z = __fsub_rn(h, x);
+  e = __fadd_rn(__fsub_rn(x, __fsub_rn(h, z)), __fsub_rn(y, z));
+  return h;
+}
+
 // a c + b s rounded once to bf16, where FP32 with the rounding errors carried along
 // decides it: off by at most 2^-43 (|a| + |b|) (2^-24 of terms of 2^-23 of that, and
 // what is left of cos and sin), it rounds as the exact value, and as FP64, unless it
@@ -54,11 +61,6 @@ __device__ __forceinline__ Angle make_angle(double c, double s) {
 __device__ __forceinline__ bool turn_exactly(float a, float b, const Angle& t, uint16_t* out) {
   const float p = a * t.c, q = b * t.s;
   const float pe = fmaf(a, t.c, -p), qe = fmaf(b, t.s, -q);  // exactly what they left
-  auto two_sum = [](float x, float y, float& e) {
-    const float h = __fadd_rn(x, y), z = __fsub_rn(h, x);
-    e = __fadd_rn(__fsub_rn(x, __fsub_rn(h, z)), __fsub_rn(y, z));
-    return h;
-  };
   float e, lo;
   const float h = two_sum(p, q, e);
   const float hi = two_sum(h, __fadd_rn(e, __fadd_rn(__fadd_rn(pe, qe),
@@ -356,6 +358,16 @@ __device__ __forceinline__ void rotate8(uint32_t turn, uint4& x1, uint4& x2, uin
   y2 = make_uint4(h2[0], h2[1], h2[2], h2[3]);
 }
 
+// a x + b y of factors given as float pairs, rounded to float: off by 2^-25 where it is
+// at most 1.
+__device__ __forceinline__ float dot2(float a, float a_lo, float x, float x_lo, float b,
+                                      float b_lo, float y, float y_lo) {
+  const float p = __fmul_rn(a, x), pe = fmaf(a, x, -p), q = __fmul_rn(b, y), qe = fmaf(b, y, -q);
+  float e;
+  const float h = two_sum(p, q, e);
+  return h + (e + (pe + qe) + fmaf(a, x_lo, b * y_lo) + fmaf(a_lo, x, b_lo * y));
+}
+
 // Bits of the pairs whose bounds differ.
 __device__ __forceinline__ uint32_t pairs_apart(const uint4& x1, const uint4& x2, const uint4& y1,
                                                 const uint4& y2) {
@@ -371,19 +383,26 @@ __device__ __forceinline__ uint32_t pairs_apart(const uint4& x1, const uint4& x2
 }
 
 // The pairs `bad` of a row again, exactly, from shared memory (the row's x1 at `row`,
-// x2 64 bytes on; what the angles' floats leave `left` bytes behind them) and through
-// it, by an index that is each lane's own: words picked so would go to memory.
+// x2 64 bytes on; what the angles' floats leave `left` bytes behind them, 0: not known)
+// and through it, by an index that is each lane's own: words picked so would go to
+// memory.
 __device__ __forceinline__ void rotate_again(uint32_t bad, const double* inv_freq, uint32_t row,
                                              uint32_t turn, uint32_t left, int pos, uint4& x1,
                                              uint4& x2) {
   for (uint32_t rest = bad; rest != 0; rest &= rest - 1) {
     const int p = __ffs(rest) - 1;
-    const uint2 hi = lds64(turn + 8 * p), lo = lds64(turn + left + 8 * p);
-    const Angle t = {__uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(lo.x),
-                     __uint_as_float(lo.y)};
+    const double angle = __dmul_rn(static_cast<double>(pos), inv_freq[p]);
     uint16_t y1, y2;
-    rotate_carefully(lds16(row + 2 * p), lds16(row + 64 + 2 * p), t,
-                     __dmul_rn(static_cast<double>(pos), inv_freq[p]), &y1, &y2);
+    if (left == 0) {
+      const uint2 y = rotate_in_fp64(lds16(row + 2 * p), lds16(row + 64 + 2 * p), angle);
+      y1 = static_cast<uint16_t>(y.x);
+      y2 = static_cast<uint16_t>(y.y);
+    } else {
+      const uint2 hi = lds64(turn + 8 * p), lo = lds64(turn + left + 8 * p);
+      const Angle t = {__uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(lo.x),
+                       __uint_as_float(lo.y)};
+      rotate_carefully(lds16(row + 2 * p), lds16(row + 64 + 2 * p), t, angle, &y1, &y2);
+    }
     sts16(row + 2 * p, y1);
     sts16(row + 64 + 2 * p, y2);
   }
@@ -437,9 +456,10 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
 // Ragged prompts: a CTA brings its units' rows of k and v (16 KiB each, in a row)
 // into a ring of two stages in shared memory, so the next unit's are on their way
 // while one is rotated and rounded; the angles of its 16 positions are a 4 KiB row of
-// the tables each, or evaluated once for all heads.  Warp h takes the K and the V block of kv head h:
-// lane 4 r + q holds dims [8 q, 8 q + 8) and [32 + 8 q, 32 + 8 q + 8) of slots r and r +
-// 8 (odd r their other half first: a phase of 8 lanes then covers all banks).
+// the tables each, or evaluated once for all heads.  Warp h takes the K and the V block
+// of kv head h: lane 4 r + q holds dims [8 q, 8 q + 8) and [32 + 8 q, 32 + 8 q + 8) of
+// slots r and r + 8 (odd r their other half first: a phase of 8 lanes then covers all
+// banks).
 constexpr int kWriteStages = 2, kWriteCtas = 3;
 constexpr int kTokenBytes = kNumKvHeads * kHeadDim * 2;        // a row of k or v
 constexpr int kHalfStage = kPageSize * kTokenBytes;            // 16 KiB
@@ -478,6 +498,15 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
   int turns = 0;             // copies of angles asked for
   auto is_near = [&](const Unit& t) {
     return tag_ok && (t.page + 1) * kPageSize <= kRopeTablePositions;
+  };
+  // Past the tables a page's angles are those of its first position turned by those of
+  // positions 0 to 15: one FP64 sincos for a pair and page, not 16 (64 x 1536 tokens
+  // from 4096 on took 240 us with those, 102 with this).  The angle itself, position x
+  // frequency rounded to FP64, is then off by 2^-52 of it: below 2^24 by 2^-28, which
+  // rotate8's bounds hold.
+  const float top_freq = static_cast<float>(fmax(freqs.inv_freq[0], freqs.inv_freq[kHalf - 1]));
+  auto is_far = [&](const Unit& t) {
+    return tag_ok && static_cast<float>(t.page + 1) * kPageSize * top_freq <= 0x1p24f;
   };
   bool ok = true;
   for (int64_t u0 = share.u0; ok && u0 < share.u1; u0 += 32) {
@@ -522,8 +551,16 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       todo &= todo - 1;
       const int st = done % kWriteStages;
       const int pos0 = t.page * kPageSize;
-      const bool near = is_near(t);
-      if (!near) {
+      const bool near = is_near(t), far = !near && is_far(t);
+      float4* first = reinterpret_cast<float4*>(turn + kPageSize * kTurnRow);
+      if (far) {  // (a warp in turn: the others wait for its sincos)
+        if (h == done % kNumKvHeads) {
+          double s64, c64;
+          sincos(__dmul_rn(static_cast<double>(pos0), freqs.inv_freq[lane]), &s64, &c64);
+          const Angle f = make_angle(c64, s64);
+          first[lane] = make_float4(f.c, f.s, f.c_lo, f.s_lo);
+        }
+      } else if (!near) {
         for (int i = tid; i < kPageSize * kHalf; i += kThreads) {
           const int pos = pos0 + i / kHalf, p = i % kHalf;
           double s64, c64;
@@ -603,6 +640,16 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
         encode(x, top, old, codes);
         put(1, top, old, codes);
       }
+      if (far) {
+#pragma unroll
+        for (int j = h; j < kPageSize; j += kNumKvHeads) {
+          const float4 f = first[lane];
+          const float2 x = freqs.table32[j * kHalf + lane], x_lo = freqs.table_lo[j * kHalf + lane];
+          turn[j * kTurnRow + lane] =
+              make_float2(dot2(f.x, f.z, x.x, x_lo.x, -f.y, -f.w, x.y, x_lo.y),
+                          dot2(f.y, f.w, x.x, x_lo.x, f.x, f.z, x.y, x_lo.y));
+        }
+      }
       load(rows);
       const bool turned = !near || mbar_wait_bounded(turn_bar, (turns - 1) & 1, wait_ns);
       ok = __syncthreads_and(turned) != 0;  // (and the angles evaluated above are there)
@@ -622,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       auto again = [&](int s, uint32_t bad) {
         const int slot = r + 8 * s;
         rotate_again(bad, freqs.inv_freq + 8 * q, rows + slot * kTokenBytes,
-                     sb + kOffTurn + (slot * kTurnRow + 8 * q) * 8, kTurnBytes, pos0 + slot,
+                     sb + kOffTurn + (slot * kTurnRow + 8 * q) * 8, far ? 0 : kTurnBytes,
+                     pos0 + slot,
                      x[s][0], x[s][1]);
       };
       uint32_t top = largest(x);
