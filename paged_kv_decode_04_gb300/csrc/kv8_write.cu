@@ -383,24 +383,23 @@ __device__ __forceinline__ uint32_t pairs_apart(const uint4& x1, const uint4& x2
 }
 
 // The pairs `bad` of a row again, exactly, from shared memory (the row's x1 at `row`,
-// x2 64 bytes on; what the angles' floats leave `left` bytes behind them, 0: not known)
-// and through it, by an index that is each lane's own: words picked so would go to
-// memory.
+// x2 64 bytes on; `left`: what the angles' floats leave, if it is known) and through it,
+// by an index that is each lane's own: words picked so would go to memory.
 __device__ __forceinline__ void rotate_again(uint32_t bad, const double* inv_freq, uint32_t row,
-                                             uint32_t turn, uint32_t left, int pos, uint4& x1,
-                                             uint4& x2) {
+                                             uint32_t turn, const float2* left, int pos,
+                                             uint4& x1, uint4& x2) {
   for (uint32_t rest = bad; rest != 0; rest &= rest - 1) {
     const int p = __ffs(rest) - 1;
     const double angle = __dmul_rn(static_cast<double>(pos), inv_freq[p]);
     uint16_t y1, y2;
-    if (left == 0) {
+    if (left == nullptr) {
       const uint2 y = rotate_in_fp64(lds16(row + 2 * p), lds16(row + 64 + 2 * p), angle);
       y1 = static_cast<uint16_t>(y.x);
       y2 = static_cast<uint16_t>(y.y);
     } else {
-      const uint2 hi = lds64(turn + 8 * p), lo = lds64(turn + left + 8 * p);
-      const Angle t = {__uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(lo.x),
-                       __uint_as_float(lo.y)};
+      const uint2 hi = lds64(turn + 8 * p);
+      const float2 lo = left[p];
+      const Angle t = {__uint_as_float(hi.x), __uint_as_float(hi.y), lo.x, lo.y};
       rotate_carefully(lds16(row + 2 * p), lds16(row + 64 + 2 * p), t, angle, &y1, &y2);
     }
     sts16(row + 2 * p, y1);
@@ -465,9 +464,10 @@ constexpr int kTokenBytes = kNumKvHeads * kHeadDim * 2;        // a row of k or 
 constexpr int kHalfStage = kPageSize * kTokenBytes;            // 16 KiB
 constexpr int kTurnRow = kHalf + 4;  // (cos, sin) of a position, and padding: two positions a phase
 constexpr int kTurnBytes = kPageSize * kTurnRow * 8;
-constexpr int kOffTurn = kWriteStages * 2 * kHalfStage;  // [16] (cos, sin), then what they leave
-constexpr int kOffWriteBars = kOffTurn + 2 * kTurnBytes;  // the stages', the angles'
-constexpr size_t kWriteSmem = kOffWriteBars + 8 * (kWriteStages + 1);
+constexpr int kOffTurn = kWriteStages * 2 * kHalfStage;       // a stage's (cos, sin)
+constexpr int kOffFirst = kOffTurn + kWriteStages * kTurnBytes;  // its first position's Angles
+constexpr int kOffWriteBars = kOffFirst + kWriteStages * kHalf * 16;  // full, empty
+constexpr size_t kWriteSmem = kOffWriteBars + 2 * 8 * kWriteStages;
 static_assert(kWriteCtas * (kWriteSmem + 1024) <= 228 * 1024, "the CTAs of an SM fit");
 
 template <int kFmt>
@@ -481,9 +481,13 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
   const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
   const int r = lane >> 2, q = lane & 3;
   const uint32_t sb = smem_addr(smem);
-  float2* turn = reinterpret_cast<float2*>(smem + kOffTurn);
+  auto full = [&](int st) { return sb + kOffWriteBars + 8 * st; };
+  auto empty = [&](int st) { return sb + kOffWriteBars + 8 * (kWriteStages + st); };
   if (tid == 0) {
-    for (int s = 0; s <= kWriteStages; ++s) mbar_init(sb + kOffWriteBars + 8 * s, 1);
+    for (int s = 0; s < kWriteStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kNumKvHeads);
+    }
     fence_barrier_init();
   }
   __syncthreads();
@@ -493,15 +497,13 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
   const bool tag_ok = rope_table_ready(freqs);
   const Share share(unit_count(num_tokens, c.batch));
   const uint64_t policy = l2_policy_evict_first();
-  const uint32_t turn_bar = sb + kOffWriteBars + 8 * kWriteStages;
   int issued = 0, done = 0;  // units whose rows were asked for, units written
-  int turns = 0;             // copies of angles asked for
   auto is_near = [&](const Unit& t) {
     return tag_ok && (t.page + 1) * kPageSize <= kRopeTablePositions;
   };
   // Past the tables a page's angles are those of its first position turned by those of
   // positions 0 to 15: one FP64 sincos for a pair and page, not 16 (64 x 1536 tokens
-  // from 4096 on took 240 us with those, 102 with this).  The angle itself, position x
+  // from 4096 on took 240 us with those, 94 with this).  The angle itself, position x
   // frequency rounded to FP64, is then off by 2^-52 of it: below 2^24 by 2^-28, which
   // rotate8's bounds hold.
   const float top_freq = static_cast<float>(fmax(freqs.inv_freq[0], freqs.inv_freq[kHalf - 1]));
@@ -514,45 +516,47 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
         find_unit(u0 + lane, share.u1, c, off, starts, num_tokens, dev_err, h == 0);
     // the units there are, in order; the same in every warp
     unsigned todo = __ballot_sync(kFull, mine.pool_page >= 0), ahead = todo;
-    auto ask = [&]() {  // the next unit's rows into the next stage
+    auto ask = [&]() {  // warp 0: the next unit's rows and angles into the next stage
       if (ahead == 0) return;
       const Unit t = unit_of(mine, __ffs(ahead) - 1);
       ahead &= ahead - 1;
-      if (tid == 0) {
-        const int st = issued % kWriteStages;
-        const uint32_t bar = sb + kOffWriteBars + 8 * st, dst = sb + st * 2 * kHalfStage;
+      const int st = issued % kWriteStages;
+      if (issued >= kWriteStages &&
+          !__all_sync(kFull, mbar_wait_bounded(empty(st), (issued / kWriteStages - 1) & 1,
+                                               wait_ns))) {
+        ok = false;
+        return;
+      }
+      const bool near = is_near(t);
+      if (lane == 0) {
+        const uint32_t dst = sb + st * 2 * kHalfStage;
         const uint32_t bytes = (t.s1 - t.s0) * kTokenBytes;
         const int64_t at = (t.row0 + t.s0) * (kTokenBytes / 2);
-        mbar_arrive_expect_tx(bar, 2 * bytes);
-        bulk_load(dst + t.s0 * kTokenBytes, k + at, bytes, bar, policy);
-        bulk_load(dst + kHalfStage + t.s0 * kTokenBytes, v + at, bytes, bar, policy);
+        mbar_arrive_expect_tx(full(st), 2 * bytes + (near ? kPageSize * kHalf * 8 : 0));
+        bulk_load(dst + t.s0 * kTokenBytes, k + at, bytes, full(st), policy);
+        bulk_load(dst + kHalfStage + t.s0 * kTokenBytes, v + at, bytes, full(st), policy);
       }
+      __syncwarp();
+      if (near && lane < kPageSize)
+        bulk_load(sb + kOffTurn + st * kTurnBytes + lane * kTurnRow * 8,
+                  freqs.table32 + (static_cast<int64_t>(t.page) * kPageSize + lane) * kHalf,
+                  kHalf * 8, full(st), policy);
       ++issued;
     };
-    auto ask_turn = [&]() {  // the angles of the next unit to be written
-      if (todo == 0) return;
-      const Unit t = unit_of(mine, __ffs(todo) - 1);
-      if (!is_near(t)) return;
-      if (h == 0) {
-        if (lane == 0) mbar_arrive_expect_tx(turn_bar, 2 * kPageSize * kHalf * 8);
-        __syncwarp();
-        const int row = lane % kPageSize;
-        bulk_load(sb + kOffTurn + lane * kTurnRow * 8,
-                  (lane < kPageSize ? freqs.table32 : freqs.table_lo) +
-                      (static_cast<int64_t>(t.page) * kPageSize + row) * kHalf,
-                  kHalf * 8, turn_bar, policy);
-      }
-      ++turns;
-    };
-    for (int s = 0; s < kWriteStages; ++s) ask();
-    ask_turn();
-    while (todo != 0) {
+    if (h == 0)
+      for (int s = 0; s < kWriteStages && ok; ++s) ask();
+    while (ok && todo != 0) {
       const Unit t = unit_of(mine, __ffs(todo) - 1);
       todo &= todo - 1;
       const int st = done % kWriteStages;
       const int pos0 = t.page * kPageSize;
+      const uint32_t old_k = t.s0 > 0 ? c.scales[scale_at(t.pool_page, 0, h)] : 0u;
+      const uint32_t old_v = t.s0 > 0 ? c.scales[scale_at(t.pool_page, 1, h)] : 0u;
+      ok = __all_sync(kFull, mbar_wait_bounded(full(st), (done / kWriteStages) & 1, wait_ns));
+      if (!ok) break;
       const bool near = is_near(t), far = !near && is_far(t);
-      float4* first = reinterpret_cast<float4*>(turn + kPageSize * kTurnRow);
+      float2* turn = reinterpret_cast<float2*>(smem + kOffTurn + st * kTurnBytes);
+      float4* first = reinterpret_cast<float4*>(smem + kOffFirst) + st * kHalf;
       if (far) {  // (a warp in turn: the others wait for its sincos)
         if (h == done % kNumKvHeads) {
           double s64, c64;
@@ -562,21 +566,13 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
         }
       } else if (!near) {
         for (int i = tid; i < kPageSize * kHalf; i += kThreads) {
-          const int pos = pos0 + i / kHalf, p = i % kHalf;
           double s64, c64;
-          sincos(__dmul_rn(static_cast<double>(pos), freqs.inv_freq[p]), &s64, &c64);
-          const Angle t2 = make_angle(c64, s64);
-          const int at = i / kHalf * kTurnRow + p;
-          turn[at] = make_float2(t2.c, t2.s);
-          turn[kPageSize * kTurnRow + at] = make_float2(t2.c_lo, t2.s_lo);
+          sincos(__dmul_rn(static_cast<double>(pos0 + i / kHalf), freqs.inv_freq[i % kHalf]), &s64,
+                 &c64);
+          turn[i / kHalf * kTurnRow + i % kHalf] =
+              make_float2(static_cast<float>(c64), static_cast<float>(s64));
         }
       }
-      const uint32_t old_k = t.s0 > 0 ? c.scales[scale_at(t.pool_page, 0, h)] : 0u;
-      const uint32_t old_v = t.s0 > 0 ? c.scales[scale_at(t.pool_page, 1, h)] : 0u;
-      const bool ready = mbar_wait_bounded(sb + kOffWriteBars + 8 * st,
-                                           (done / kWriteStages) & 1, wait_ns);
-      ok = __syncthreads_and(ready) != 0;  // (the same in every thread)
-      if (!ok) break;
       ++done;
       const uint32_t rows = sb + st * 2 * kHalfStage + h * (kHeadDim * 2) + 16 * q;
       uint4 x[2][2];  // [slot r, r + 8][dims 8 q, 32 + 8 q]
@@ -641,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
         put(1, top, old, codes);
       }
       if (far) {
+        __syncthreads();
 #pragma unroll
         for (int j = h; j < kPageSize; j += kNumKvHeads) {
           const float4 f = first[lane];
@@ -650,10 +647,8 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
                           dot2(f.y, f.w, x.x, x_lo.x, f.x, f.z, x.y, x_lo.y));
         }
       }
+      if (!near) __syncthreads();  // (warps that gave up have left)
       load(rows);
-      const bool turned = !near || mbar_wait_bounded(turn_bar, (turns - 1) & 1, wait_ns);
-      ok = __syncthreads_and(turned) != 0;  // (and the angles evaluated above are there)
-      if (!ok) break;
       // Bounds x, y of the rotated keys, which give the same codes but for a key in a
       // few ten thousand.  (Deciding each of them exactly took 84 us for 64 prompts of
       // up to 2047 tokens, with FP64, whose rate here is a small fraction of FP32's,
@@ -661,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       uint4 y[2][2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        rotate8(sb + kOffTurn + ((r + 8 * s) * kTurnRow + 8 * q) * 8, x[s][0], x[s][1], y[s][0],
+        rotate8(smem_addr(turn) + ((r + 8 * s) * kTurnRow + 8 * q) * 8, x[s][0], x[s][1], y[s][0],
                 y[s][1]);
         if (r + 8 * s < t.s0 || r + 8 * s >= t.s1)  // (zeros: their signs do not matter)
           y[s][0] = y[s][1] = x[s][0] = x[s][1] = make_uint4(0u, 0u, 0u, 0u);
@@ -669,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       auto again = [&](int s, uint32_t bad) {
         const int slot = r + 8 * s;
         rotate_again(bad, freqs.inv_freq + 8 * q, rows + slot * kTokenBytes,
-                     sb + kOffTurn + (slot * kTurnRow + 8 * q) * 8, far ? 0 : kTurnBytes,
+                     smem_addr(turn) + (slot * kTurnRow + 8 * q) * 8,
+                     near ? freqs.table_lo + static_cast<int64_t>(pos0 + slot) * kHalf + 8 * q
+                          : nullptr,
                      pos0 + slot,
                      x[s][0], x[s][1]);
       };
@@ -710,19 +707,17 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
         }
       }
       put(0, top, old, codes);
-      fence_proxy_async_smem();
-      __syncthreads();  // the stage can be filled again, the angles replaced
-      ask();
-      ask_turn();
+      fence_proxy_async_smem();  // the stage's next copies come after what was written here
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+      if (h == 0) ask();
     }
   }
-  if (!ok && tid == 0) record_error(dev_err, kErrTimeout);
+  if (!ok && lane == 0) record_error(dev_err, kErrTimeout);
   // every copy asked for has landed before the CTA ends (full limit)
-  if (tid == 0) {
+  if (tid == 0)
     for (int j = issued > kWriteStages ? issued - kWriteStages : 0; j < issued; ++j)
-      mbar_wait_bounded(sb + kOffWriteBars + 8 * (j % kWriteStages), (j / kWriteStages) & 1);
-    if (turns > 0) mbar_wait_bounded(turn_bar, (turns - 1) & 1);
-  }
+      mbar_wait_bounded(full(j % kWriteStages), (j / kWriteStages) & 1);
 }
 
 // Warp h of a CTA reads the K and the V block of kv head h of its units, the next
