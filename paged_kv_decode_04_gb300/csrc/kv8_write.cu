@@ -80,15 +80,16 @@ __device__ __forceinline__ bool turn_exactly(float a, float b, const Angle& t, u
 }
 
 // Both values of a rotated pair, rotate_pair's bits.
-__device__ __noinline__ uint2 rotate_in_fp64(uint32_t h1, uint32_t h2, double angle) {
+__device__ __noinline__ uint2 rotate_in_fp64(uint32_t h1, uint32_t h2, int pos, double freq) {
   double c, s;
-  sincos(angle, &s, &c);
+  sincos(__dmul_rn(static_cast<double>(pos), freq), &s, &c);
   uint16_t y1, y2;
   rotate_pair(static_cast<uint16_t>(h1), static_cast<uint16_t>(h2), c, s, &y1, &y2);
   return make_uint2(y1, y2);
 }
 __device__ __forceinline__ void rotate_carefully(uint32_t h1, uint32_t h2, const Angle& t,
-                                                 double angle, uint16_t* y1, uint16_t* y2) {
+                                                 int pos, const double* freq, uint16_t* y1,
+                                                 uint16_t* y2) {
   const float u = __uint_as_float(h1 << 16), v = __uint_as_float(h2 << 16);
   const float s0 = fabsf(u) + fabsf(v);
   // (tiny, huge, not finite: FP32 would lose them)
@@ -98,7 +99,7 @@ __device__ __forceinline__ void rotate_carefully(uint32_t h1, uint32_t h2, const
   n.s_lo = -t.s_lo;
   const bool ok1 = turn_exactly(u, v, n, y1), ok2 = turn_exactly(v, u, t, y2);
   if (!(fine && ok1 && ok2)) {
-    const uint2 y = rotate_in_fp64(h1 & 0xFFFFu, h2 & 0xFFFFu, angle);
+    const uint2 y = rotate_in_fp64(h1 & 0xFFFFu, h2 & 0xFFFFu, pos, *freq);
     *y1 = static_cast<uint16_t>(y.x);
     *y2 = static_cast<uint16_t>(y.y);
   }
@@ -137,7 +138,8 @@ template <int kFmt>
 __global__ void __launch_bounds__(kThreads)
     kv8_append_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
                       const Kv8 c, const int32_t* __restrict__ positions,
-                      const int32_t* __restrict__ slots, RopeFreqs freqs,
+                      const int32_t* __restrict__ slots,
+                      const __grid_constant__ RopeFreqs freqs,
                       const uint16_t* __restrict__ q_in, uint16_t* __restrict__ q_out,
                       int32_t* dev_err) {
   const int b = blockIdx.x;
@@ -169,11 +171,11 @@ __global__ void __launch_bounds__(kThreads)
   // each thread.
   __shared__ Angle s_angle[kHalf];
   Angle t;
-  const double angle = __dmul_rn(static_cast<double>(pos), freqs.inv_freq[i]);
+  auto angle = [&]() { return __dmul_rn(static_cast<double>(pos), freqs.inv_freq[i]); };
   if (freqs.table_theta == nullptr || pos < 0 || pos >= kRopeTablePositions) {
     if (h == 0) {
       double s64, c64;
-      sincos(angle, &s64, &c64);
+      sincos(angle(), &s64, &c64);
       s_angle[i] = make_angle(c64, s64);
     }
     __syncthreads();
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kThreads)
     t = {hi.x, hi.y, lo.x, lo.y};
   } else {
     double s64, c64;
-    sincos(angle, &s64, &c64);
+    sincos(angle(), &s64, &c64);
     t = make_angle(c64, s64);
   }
   auto rotate = [&](uint16_t x1, uint16_t x2, uint16_t* y1, uint16_t* y2) {
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kThreads)
     // (zeros keep their signs in FP32)
     if (s0 != 0.f &&
         (lo != cvt_bf16x2_rn(a + A, b + A) || !(s0 >= 0x1p-70f && s0 <= 0x1p+100f)))
-      rotate_carefully(x1, x2, t, angle, y1, y2);
+      rotate_carefully(x1, x2, t, pos, freqs.inv_freq + i, y1, y2);
   };
 
   if (q_in != nullptr) {
@@ -390,17 +392,18 @@ __device__ __forceinline__ void rotate_again(uint32_t bad, const double* inv_fre
                                              uint4& x1, uint4& x2) {
   for (uint32_t rest = bad; rest != 0; rest &= rest - 1) {
     const int p = __ffs(rest) - 1;
-    const double angle = __dmul_rn(static_cast<double>(pos), inv_freq[p]);
     uint16_t y1, y2;
     if (left == nullptr) {
-      const uint2 y = rotate_in_fp64(lds16(row + 2 * p), lds16(row + 64 + 2 * p), angle);
+      const uint2 y = rotate_in_fp64(lds16(row + 2 * p), lds16(row + 64 + 2 * p), pos,
+                                      inv_freq[p]);
       y1 = static_cast<uint16_t>(y.x);
       y2 = static_cast<uint16_t>(y.y);
     } else {
       const uint2 hi = lds64(turn + 8 * p);
       const float2 lo = left[p];
       const Angle t = {__uint_as_float(hi.x), __uint_as_float(hi.y), lo.x, lo.y};
-      rotate_carefully(lds16(row + 2 * p), lds16(row + 64 + 2 * p), t, angle, &y1, &y2);
+      rotate_carefully(lds16(row + 2 * p), lds16(row + 64 + 2 * p), t, pos, inv_freq + p, &y1,
+                       &y2);
     }
     sts16(row + 2 * p, y1);
     sts16(row + 64 + 2 * p, y2);
