@@ -15,8 +15,10 @@
 // leaves a partial result (two at most), which the merge kernel combines.
 //
 // Bound by memory, in the middle by latencies: one token for 256 sequences of 1024 to
-// 2048 tokens (409 MB) 76 us, 5.4 TB/s, where the copies alone take 74; 64 x 4 new
-// tokens over 1024 to 2048 (104 MB) 34 us without the launches around, the copies 22.
+// 2048 tokens (409 MB) 71 us, 5.7 TB/s; 64 x 4 new tokens over 1024 to 2048 (104 MB) 34
+// us without the launches around (22 without the arithmetic: four warps a scheduler of
+// dependent instructions, 46% of the issue slots while they run.  Two pages at a time,
+// as for one token, spill there: 42).
 //
 // mma.sync m16n8k16 in f16, FP32 accumulators, for a page (16 tokens) and a kv
 // head; codes become f16 exactly (one instruction for two e4m3 codes):
@@ -123,10 +125,12 @@ struct Lane {
     fg = lane >> 2;
     ft = lane & 3;
     tok = 4 * (fg >> 1) + (fg & 1);
-    // 16-byte chunk c of row r lies at chunk c ^ (r / 2 mod 4) (TMA's 64-byte
-    // swizzle)
-    auto at = [](int r, int c) {
-      return static_cast<uint32_t>(r * kHeadDim + ((c ^ ((r >> 1) & 3)) << 4));
+    // two tokens to a row of eight 16-byte chunks, chunk c of row r at chunk c ^ (r mod
+    // 8) (TMA's 128-byte swizzle; boxes with rows of 64 bytes took 76 us for the 256
+    // sequences above, these 71)
+    auto at = [](int t, int c) {
+      const int r = t >> 1;
+      return static_cast<uint32_t>(r * 128 + (((4 * (t & 1) + c) ^ r) << 4));
     };
     k0 = at(tok, ft);
     k1 = at(tok + 2, ft);
@@ -266,8 +270,10 @@ __device__ __forceinline__ void add_values(uint32_t vt, const Lane& P, float sv,
 // NaN, and 0 x NaN is not 0.
 __device__ __forceinline__ void hide_v(uint32_t vt, uint32_t vis, int lane) {
 #pragma unroll
-  for (int i = lane; i < kPageSize * 4; i += 32)
-    if (!((vis >> (i >> 2)) & 1u)) sts128_zero(vt + i * 16);
+  for (int i = lane; i < kPageSize * 4; i += 32) {
+    const int r = i >> 3, c = (i & 7) ^ r;
+    if (!((vis >> (2 * r + (c >> 2))) & 1u)) sts128_zero(vt + i * 16);
+  }
   fence_proxy_async_smem();  // the ring's next copy comes after these writes
   __syncwarp();
 }

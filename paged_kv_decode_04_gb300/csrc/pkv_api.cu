@@ -1413,7 +1413,7 @@ pkv::Kv8 kv8_of(const void* pool, const uint8_t* scales, int format, int64_t num
 }
 
 // TMA descriptor of the 8-bit pool viewed as [num_pages][256 rows (K|V x kv head x
-// slot)][64] bytes, 64-byte swizzled, with boxes of one page.  Cached per thread
+// slot pair)][128] bytes, 128-byte swizzled, with boxes of one page.  Cached per thread
 // for the last (device, pool, pages).
 bool pool8_map(const void* pool, int64_t num_pages, CUtensorMap* out) {
   struct Entry {
@@ -1422,23 +1422,20 @@ bool pool8_map(const void* pool, int64_t num_pages, CUtensorMap* out) {
     int64_t num_pages = 0;
     CUtensorMap map;
   };
-  constexpr int kRows = 2 * kNumKvHeads * kPageSize;
+  constexpr int kRow = 128, kRows = 2 * kNumKvHeads * kPageSize * kHeadDim / kRow;
   thread_local Entry c;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (c.device != dev || c.pool != pool || c.num_pages != num_pages) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(kRows),
-                                static_cast<cuuint64_t>(num_pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim),
-                                   static_cast<cuuint64_t>(kRows * kHeadDim)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim), static_cast<cuuint32_t>(kRows),
-                               1};
+    const cuuint64_t dims[3] = {kRow, kRows, static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[2] = {kRow, kRows * kRow};
+    const cuuint32_t box[3] = {kRow, kRows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUtensorMap m;
     if (enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
@@ -1468,7 +1465,7 @@ bool stream8_plan(int batch, long long units, long long pages, int num_splits, i
   // Shared where the table has room for that many pages a CTA: lengths are the kernel's
   // to read, and may be far from the table's width.  128 sequences, one of 16000 tokens
   // and the rest of 500: 33 us shared, 404 with a CTA each, 68 with the best number of
-  // ranges (16); 64 of 50 to 6350: 51 and 53 (8 ranges); 256 of 1024 to 2048: 76 and 81
+  // ranges (16); 64 of 50 to 6350: 51 and 53 (8 ranges); 256 of 1024 to 2048: 71 and 76
   // (a CTA each).  Sharing costs 3 to 4 us (a sum of the lengths before, a merge after),
   // more than it saves below: 128 windows of 1000 tokens 34 us, 31 in two ranges each,
   // 64 x 4 new tokens over 1024 to 2048 45 and 41.  Many short sequences lose a little

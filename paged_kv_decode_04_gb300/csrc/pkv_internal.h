@@ -384,7 +384,7 @@ cudaError_t launch_widen(const WidenArgs& args, int num_sms, cudaStream_t stream
 // one token a sequence; of chunks of at most kShortTokens tokens, where beside: right
 // after launch_chunk_attention (kv8_attention.cu).  num_splits, short_splits: ranges
 // of a sequence, or 0: args.part_ctas CTAs share the batch's pages, with two partial
-// results each.  page_map: boxes of one page's codes, 64-byte swizzled.
+// results each.  page_map: boxes of one page's codes, 128-byte swizzled.
 constexpr int kStream8Ctas = 2;  // per SM
 cudaError_t launch_decode8(const CUtensorMap& page_map, const MaskedArgs& args, int format,
                            cudaStream_t stream);
