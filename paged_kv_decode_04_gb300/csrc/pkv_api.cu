@@ -1465,7 +1465,7 @@ bool stream8_plan(int batch, long long units, long long pages, int num_splits, i
   // Shared where the table has room for that many pages a CTA: lengths are the kernel's
   // to read, and may be far from the table's width.  128 sequences, one of 16000 tokens
   // and the rest of 500: 33 us shared, 404 with a CTA each, 68 with the best number of
-  // ranges (16); 64 of 50 to 6350: 51 and 53 (8 ranges); 256 of 1024 to 2048: 71 and 76
+  // ranges (16); 64 of 50 to 6350: 47 and 53 (8 ranges); 256 of 1024 to 2048: 71 and 81
   // (a CTA each).  Sharing costs 3 to 4 us (a sum of the lengths before, a merge after),
   // more than it saves below: 128 windows of 1000 tokens 34 us, 31 in two ranges each,
   // 64 x 4 new tokens over 1024 to 2048 45 and 41.  Many short sequences lose a little
