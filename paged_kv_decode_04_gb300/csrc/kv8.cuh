@@ -1,8 +1,8 @@
 // kv8.cuh -- the 8-bit cache: codes, scales and where a block stands.
 //
 // Pool [pages][K|V][8 kv heads][16 tokens][64] of 8-bit codes: a block, the 16
-// tokens of one page, K or V and one kv head, is 1 KiB in a row, so that it is
-// one TMA box and its scale (uint8 [pages][K|V][8]) serves all of it.  A value
+// tokens of one page, K or V and one kv head, is 1 KiB in a row, which its scale
+// (uint8 [pages][K|V][8]) serves, and a page is one TMA box of 16 KiB.  A value
 // is code * 2^(scale - 127), the code an e4m3 float or a signed integer.
 // Powers of two make the products with the scales exact: a bf16 value has 8
 // significant bits and a code at most 7, so dividing by a scale loses nothing

@@ -505,6 +505,121 @@ __device__ __forceinline__ void put_zeros(uint16_t* out, int lane) {
   for (int h = 0; h < kGroup; ++h) reinterpret_cast<uint32_t*>(out + h * kHeadDim)[lane] = 0u;
 }
 
+// One token of a kv head's group over n pages of the ring, V saying what it sees: q and
+// out its four rows, part their place in the partial results or -1.  False: a wait ran
+// out.
+template <int kFmt>
+__device__ __forceinline__ bool attend_one(const MaskedArgs& a, const Ring& R, const Lane& P,
+                                           Turn& T, int g, int lane, const Visible& V, int n,
+                                           const uint16_t* q, uint16_t* out, float* acc, float* ml,
+                                           int64_t part) {
+  uint32_t qb[4][2];
+  const float undo = load_q(q + (P.fg & 3) * kHeadDim, P.ft, qb);
+  // factors of the scores of columns 2 ft and 2 ft + 1
+  const int h = (2 * P.ft) & 3;
+  const float c0 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h);
+  const float c1 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h + 4);
+  State S;
+  S.reset();
+  bool ok = true;
+  // Two pages at a time: one alone is a chain of latencies (copy, products, weights,
+  // products), and what is checked is checked once for both.
+  for (int k = 0; k < n; k += 2) {
+    const int st0 = T.stage, phase0 = T.phase;
+    T.next();
+    const int st1 = T.stage, phase1 = T.phase;
+    if (k + 1 < n) T.next();
+    bool ready = mbar_wait_bounded(R.full(st0), phase0, a.wait_ns);
+    if (k + 1 < n) ready &= mbar_wait_bounded(R.full(st1), phase1, a.wait_ns);
+    if (!__all_sync(kFull, ready)) {
+      if (lane == 0) record_error(a.dev_err, kErrTimeout);
+      ok = false;
+      break;
+    }
+    // seen tokens of the pages (none where there is none, or it was not read)
+    auto seen = [&](int st, bool there) {
+      const uint2 meta = lds64(R.meta(st));
+      if (!there || static_cast<int>(meta.y) < 0) return 0u;
+      return V.whole(meta.x) ? 0xFFFFu : V.mask(meta.x);
+    };
+    const uint32_t vis0 = seen(st0, true), vis1 = seen(st1, k + 1 < n);
+    const uint32_t kt0 = R.page(st0) + g * kBlockBytes, kt1 = R.page(st1) + g * kBlockBytes;
+    constexpr uint32_t kV = kNumKvHeads * kBlockBytes;
+    const float sk0 = scale_value(lds8(R.scales(st0) + g));
+    const float sk1 = scale_value(lds8(R.scales(st1) + g));
+    const float sv0 = scale_value(lds8(R.scales(st0) + kNumKvHeads + g));
+    const float sv1 = scale_value(lds8(R.scales(st1) + kNumKvHeads + g));
+    // (a factor of 0 would make NaN of a masked score)
+    const float f[2][2] = {{fmaxf(c0 * sk0, 0x1p-126f), fmaxf(c1 * sk0, 0x1p-126f)},
+                           {fmaxf(c0 * sk1, 0x1p-126f), fmaxf(c1 * sk1, 0x1p-126f)}};
+    float s[2][4];
+    uint32_t b[2][2];
+    auto scores = [&](uint32_t kt, float (&x)[4]) {
+      uint32_t ka[4][4];
+      load_k<kFmt>(kt, P, ka);
+      mma_new(x, ka[0], qb[0][0], qb[0][1]);
+#pragma unroll
+      for (int kk = 1; kk < 4; ++kk) mma_add(x, ka[kk], qb[kk][0], qb[kk][1]);
+    };
+    if ((vis0 & vis1) == 0xFFFFu) {
+      scores(kt0, s[0]);
+      scores(kt1, s[1]);
+      move_reference(s, f, S);
+      page_weights(s[0], f[0], P.ft, S, b[0][0], b[0][1]);
+      page_weights(s[1], f[1], P.ft, S, b[1][0], b[1][1]);
+      add_values<kFmt>(kt0 + kV, P, sv0, b[0][0], b[0][1], S);
+      add_values<kFmt>(kt1 + kV, P, sv1, b[1][0], b[1][1], S);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t vis = i == 0 ? vis0 : vis1, kt = i == 0 ? kt0 : kt1;
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
+        if (vis == 0u) continue;
+        scores(kt, s[i]);
+        if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
+        if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
+        if constexpr (kFmt == kKv8E4m3) hide_v(kt + kV, vis, lane);
+      }
+      // (the scales of a page that was not read may be anything)
+      const float g2[2][2] = {{vis0 ? f[0][0] : 1.f, vis0 ? f[0][1] : 1.f},
+                              {vis1 ? f[1][0] : 1.f, vis1 ? f[1][1] : 1.f}};
+      move_reference(s, g2, S);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        page_weights(s[i], g2[i], P.ft, S, b[i][0], b[i][1]);
+        if ((i == 0 ? vis0 : vis1) != 0u)
+          add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, i == 0 ? sv0 : sv1, b[i][0], b[i][1], S);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(R.empty(st0));
+      if (k + 1 < n) mbar_arrive(R.empty(st1));
+    }
+  }
+
+  // the terms' columns meet; lanes ft < 2 hold heads 2 ft and 2 ft + 1
+#pragma unroll
+  for (int i = 4; i <= 16; i <<= 1) {
+    S.l[0] += __shfl_xor_sync(kFull, S.l[0], i);
+    S.l[1] += __shfl_xor_sync(kFull, S.l[1], i);
+  }
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      S.o[mt][e].x += __shfl_xor_sync(kFull, S.o[mt][e].x, 2);
+      S.o[mt][e].y += __shfl_xor_sync(kFull, S.o[mt][e].y, 2);
+    }
+  if (P.ft < 2) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      put_row(S, j, P.fg, out + (2 * P.ft + j) * kHeadDim, acc, ml,
+              part < 0 ? -1 : part + 2 * P.ft + j);
+  }
+  return ok;
+}
+
 // One token a sequence.  Grid: the CTAs that share the work, or (num_splits, batch).
 template <int kFmt, bool kShared>
 __global__ void __launch_bounds__(kThreads, kCtas)
@@ -538,115 +653,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         put_zeros(a.out + (static_cast<int64_t>(b) * kNumQHeads + g * kGroup) * kHeadDim, lane);
   const Lane P(lane);
   each_segment<kShared>(a.num_splits, part, make, [&](int b, const Visible& V, int r0, int r1,
-                                                int slot) {
-    uint32_t qb[4][2];
-    const int64_t row0 = static_cast<int64_t>(b) * kNumQHeads + g * kGroup;
-    const float undo = load_q(a.q + (row0 + (P.fg & 3)) * kHeadDim, P.ft, qb);
-    // factors of the scores of columns 2 ft and 2 ft + 1
-    const int h = (2 * P.ft) & 3;
-    const float c0 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h);
-    const float c1 = a.scale_log2 * __shfl_sync(kFull, undo, 4 * h + 4);
-    State S;
-    S.reset();
-    bool ok = true;
-    // Two pages at a time: one alone is a chain of latencies (copy, products, weights,
-    // products), and what is checked is checked once for both.
-    const int n = r1 - r0;
-    for (int k = 0; k < n; k += 2) {
-      const int st0 = T.stage, phase0 = T.phase;
-      T.next();
-      const int st1 = T.stage, phase1 = T.phase;
-      if (k + 1 < n) T.next();
-      bool ready = mbar_wait_bounded(R.full(st0), phase0, a.wait_ns);
-      if (k + 1 < n) ready &= mbar_wait_bounded(R.full(st1), phase1, a.wait_ns);
-      if (!__all_sync(kFull, ready)) {
-        if (lane == 0) record_error(a.dev_err, kErrTimeout);
-        ok = false;
-        break;
-      }
-      // seen tokens of the pages (none where there is none, or it was not read)
-      auto seen = [&](int st, bool there) {
-        const uint2 meta = lds64(R.meta(st));
-        if (!there || static_cast<int>(meta.y) < 0) return 0u;
-        return V.whole(meta.x) ? 0xFFFFu : V.mask(meta.x);
-      };
-      const uint32_t vis0 = seen(st0, true), vis1 = seen(st1, k + 1 < n);
-      const uint32_t kt0 = R.page(st0) + g * kBlockBytes, kt1 = R.page(st1) + g * kBlockBytes;
-      constexpr uint32_t kV = kNumKvHeads * kBlockBytes;
-      const float sk0 = scale_value(lds8(R.scales(st0) + g));
-      const float sk1 = scale_value(lds8(R.scales(st1) + g));
-      const float sv0 = scale_value(lds8(R.scales(st0) + kNumKvHeads + g));
-      const float sv1 = scale_value(lds8(R.scales(st1) + kNumKvHeads + g));
-      // (a factor of 0 would make NaN of a masked score)
-      const float f[2][2] = {{fmaxf(c0 * sk0, 0x1p-126f), fmaxf(c1 * sk0, 0x1p-126f)},
-                             {fmaxf(c0 * sk1, 0x1p-126f), fmaxf(c1 * sk1, 0x1p-126f)}};
-      float s[2][4];
-      uint32_t b[2][2];
-      auto scores = [&](uint32_t kt, float (&x)[4]) {
-        uint32_t ka[4][4];
-        load_k<kFmt>(kt, P, ka);
-        mma_new(x, ka[0], qb[0][0], qb[0][1]);
-#pragma unroll
-        for (int kk = 1; kk < 4; ++kk) mma_add(x, ka[kk], qb[kk][0], qb[kk][1]);
-      };
-      if ((vis0 & vis1) == 0xFFFFu) {
-        scores(kt0, s[0]);
-        scores(kt1, s[1]);
-        move_reference(s, f, S);
-        page_weights(s[0], f[0], P.ft, S, b[0][0], b[0][1]);
-        page_weights(s[1], f[1], P.ft, S, b[1][0], b[1][1]);
-        add_values<kFmt>(kt0 + kV, P, sv0, b[0][0], b[0][1], S);
-        add_values<kFmt>(kt1 + kV, P, sv1, b[1][0], b[1][1], S);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t vis = i == 0 ? vis0 : vis1, kt = i == 0 ? kt0 : kt1;
-          s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
-          if (vis == 0u) continue;
-          scores(kt, s[i]);
-          if (!((vis >> P.tok) & 1u)) s[i][0] = s[i][1] = -INFINITY;
-          if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
-          if constexpr (kFmt == kKv8E4m3) hide_v(kt + kV, vis, lane);
-        }
-        // (the scales of a page that was not read may be anything)
-        const float g2[2][2] = {{vis0 ? f[0][0] : 1.f, vis0 ? f[0][1] : 1.f},
-                                {vis1 ? f[1][0] : 1.f, vis1 ? f[1][1] : 1.f}};
-        move_reference(s, g2, S);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          page_weights(s[i], g2[i], P.ft, S, b[i][0], b[i][1]);
-          if ((i == 0 ? vis0 : vis1) != 0u)
-            add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, i == 0 ? sv0 : sv1, b[i][0], b[i][1], S);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(R.empty(st0));
-        if (k + 1 < n) mbar_arrive(R.empty(st1));
-      }
-    }
-
-    // the terms' columns meet; lanes ft < 2 hold heads 2 ft and 2 ft + 1
-#pragma unroll
-    for (int i = 4; i <= 16; i <<= 1) {
-      S.l[0] += __shfl_xor_sync(kFull, S.l[0], i);
-      S.l[1] += __shfl_xor_sync(kFull, S.l[1], i);
-    }
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        S.o[mt][e].x += __shfl_xor_sync(kFull, S.o[mt][e].x, 2);
-        S.o[mt][e].y += __shfl_xor_sync(kFull, S.o[mt][e].y, 2);
-      }
-    if (P.ft < 2) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        put_row(S, j, P.fg, a.out + (row0 + 2 * P.ft + j) * kHeadDim, a.part_acc, a.part_ml,
-                slot < 0 ? -1
-                         : static_cast<int64_t>(slot) * kNumQHeads + g * kGroup + 2 * P.ft + j);
-    }
-    return ok;
+                                                      int slot) {
+    const int64_t row = (static_cast<int64_t>(b) * kNumQHeads + g * kGroup) * kHeadDim;
+    return attend_one<kFmt>(a, R, P, T, g, lane, V, r1 - r0, a.q + row, a.out + row, a.part_acc,
+                            a.part_ml,
+                            slot < 0 ? -1 : static_cast<int64_t>(slot) * kNumQHeads + g * kGroup);
   });
 }
 
@@ -722,6 +733,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                                                   int slot) {
     const int nt = V.nt, o0 = V.o0, pos0 = V.pos0, end = V.pos0 + V.nt;
     if (nt == 0) return true;
+    // A token by itself would leave three quarters of the MMAs empty: a chunk of 509
+    // tokens beside 63 single ones over 1024 to 2047 took 62 us so, 51 with this.
+    if (nt == 1) {
+      const int64_t row = (static_cast<int64_t>(o0) * kNumQHeads + g * kGroup) * kHeadDim;
+      return attend_one<kFmt>(
+          a, R, P, T, g, lane, Visible(end, a.window, a.sinks), r1 - r0, a.q + row, a.out + row,
+          a.short_acc, a.short_ml,
+          slot < 0 ? -1 : (static_cast<int64_t>(slot) * kNumKvHeads + g) * kShortRows);
+    }
     uint32_t qa[4][4];  // A fragments: [k-step][row fg, fg + 8 of dims {0, 1}, then {2, 3}]
     float c[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
