@@ -705,7 +705,9 @@ PKV_API int pkv_kv8_append(const pkv_bf16* k_new, const pkv_bf16* v_new, void* p
  * pkv_kv8_write_prefill -- pkv_kv_write_prefill into the 8-bit cache.  A block's
  * tokens of one call are rounded together, to one scale.
  *   dev_err  PKV_DEVERR_PAGE / _POSITION (tokens outside the table are skipped)
- *            / _OFFSETS (a sequence with bad offsets is skipped) / _VALUE
+ *            / _OFFSETS (where they do not begin at 0 and end at num_tokens; a
+ *            sequence with bad offsets is skipped, and others may be where
+ *            offsets fall) / _VALUE
  * No two sequences may name the same page.
  */
 PKV_API int pkv_kv8_write_prefill(const pkv_bf16* k, const pkv_bf16* v, int num_tokens,
@@ -721,7 +723,7 @@ PKV_API int pkv_kv8_write_prefill(const pkv_bf16* k, const pkv_bf16* v, int num_
  * 1]) of k and v ([num_tokens][num_kv_heads][head_dim], 16-byte aligned) become
  * the cached tokens start_positions[b] and on of sequence b.  Rows of tokens on
  * a bad page, outside the table or of no sequence are left as they were.
- *   dev_err  PKV_DEVERR_PAGE / _POSITION / _OFFSETS
+ *   dev_err  PKV_DEVERR_PAGE / _POSITION / _OFFSETS, as there
  */
 PKV_API int pkv_kv8_read(const void* pool, const uint8_t* scales, int format, int64_t num_pages,
                          const int32_t* block_table, int max_blocks,

@@ -265,7 +265,12 @@ __host__ __device__ inline int64_t unit_count(int num_tokens, int batch) {
   return num_tokens / kPageSize + 2 * static_cast<int64_t>(batch);
 }
 
-// The unit of number u, by each lane for itself; `report`: one warp of a CTA
+__device__ __forceinline__ bool bad_offsets(int o0, int o1, int num_tokens) {
+  return o0 < 0 || o1 < o0 || o1 > num_tokens;
+}
+
+// The unit of number u, by each lane for itself (found where offsets do not fall);
+// `report`: one warp of a CTA
 // reports what is wrong with it.
 __device__ __forceinline__ Unit find_unit(int64_t u, int64_t end, const Kv8& c,
                                           const int32_t* __restrict__ off,
@@ -280,10 +285,7 @@ __device__ __forceinline__ Unit find_unit(int64_t u, int64_t end, const Kv8& c,
     if (first(mid) <= u) lo = mid; else hi = mid;
   }
   const int o0 = off[lo], o1 = off[lo + 1];
-  if (o0 < 0 || o1 < o0 || o1 > num_tokens) {
-    if (report) record_error(dev_err, kErrOffsets);
-    return r;
-  }
+  if (bad_offsets(o0, o1, num_tokens)) return r;  // (reported by check_offsets)
   const int64_t start = starts[lo], past = start + (o1 - o0);
   const int64_t limit = static_cast<int64_t>(c.max_blocks) * kPageSize;
   const int64_t p0 = start > 0 ? start : 0, p1 = past < limit ? past : limit;
@@ -324,11 +326,15 @@ struct Share {
   }
 };
 
-// Offsets that do not begin at 0 and end at the number of tokens.
-__device__ __forceinline__ void check_ends(const Kv8& c, const int32_t* off, int num_tokens,
-                                           int32_t* dev_err) {
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (off[0] != 0 || off[c.batch] != num_tokens))
-    record_error(dev_err, kErrOffsets);
+// Offsets that do not begin at 0 and end at the number of tokens, or are bad between;
+// by the first CTA, as units of sequences with bad ones may not be found.
+__device__ __forceinline__ void check_offsets(const Kv8& c, const int32_t* off, int num_tokens,
+                                              int32_t* dev_err) {
+  if (blockIdx.x != 0) return;
+  bool bad = threadIdx.x == 0 && (off[0] != 0 || off[c.batch] != num_tokens);
+  for (int b = threadIdx.x; b < c.batch; b += kThreads)
+    bad |= bad_offsets(off[b], off[b + 1], num_tokens);
+  if (bad) record_error(dev_err, kErrOffsets);
 }
 
 // RoPE of the 8 pairs (x1, x2) = dims (8 q + p, 32 + 8 q + p) of a row: x1, x2 become
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
   __syncthreads();
   wait_for_prior_grids();
   allow_dependent_grids();
-  check_ends(c, off, num_tokens, dev_err);
+  check_offsets(c, off, num_tokens, dev_err);
   const bool tag_ok = rope_table_ready(freqs);
   const Share share(unit_count(num_tokens, c.batch));
   const uint64_t policy = l2_policy_evict_first();
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, kReadCtas)
   const int r = lane >> 3, q = lane & 7;
   wait_for_prior_grids();
   allow_dependent_grids();
-  check_ends(c, off, num_tokens, dev_err);
+  check_offsets(c, off, num_tokens, dev_err);
   const Share share(unit_count(num_tokens, c.batch));
   for (int64_t u0 = share.u0; u0 < share.u1; u0 += 32) {
     const Unit mine =

@@ -244,6 +244,45 @@ def test_write_far_positions(fmt, theta, start):
     same(decode(bits(pool), fmt), decode(codes, fmt), "values")
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_write_and_read_with_offsets_that_fall(fmt):
+    """Sequences are written as the definition says or not at all, reported either way,
+    and no page of another one changes."""
+    dev, b = cuda_or_skip(), binding()
+    rng = np.random.default_rng(9)
+    k, v = (oracle_bits(rng.standard_normal((100, HKV, D)).astype(np.float32)) for _ in range(2))
+    bt = np.arange(28, dtype=np.int32).reshape(4, 7)
+    codes, scales, _ = make_cache8([28 * P], fmt, spare=0)
+    for off in ([0, 90, 5, 40, 100], [0, 100, 100, 0, 100], [0, 5, 100, 40, 50],
+                [0, -7, 60, 80, 100], [0, 2 ** 31 - 1, -2 ** 31, 50, 100]):
+        pool, sc, err = as_pool(codes, fmt).to(dev), torch.from_numpy(scales).to(dev), err_of(dev)
+        b.kv8_write_prefill(bf16(k, dev), bf16(v, dev), i32(off, dev), i32([0] * 4, dev), pool, sc,
+                            i32(bt, dev), rope_theta=1e4, dev_err=err)
+        assert int(err.item()) == OFFSETS, off
+        got, got_sc = bits(pool), bits(sc)
+        for i in range(4):
+            pages = bt[i]
+            want, want_sc = codes.copy(), scales.copy()
+            n = off[i + 1] - off[i]
+            if off[i] >= 0 and 0 < n and off[i + 1] <= 100:
+                key = rotated(k[off[i]:off[i + 1]], range(n), 1e4)
+                for a in range(0, n, P):
+                    for kv, x in enumerate((key, oracle.bf16_to_f64(v[off[i]:off[i + 1]]))):
+                        for h in range(HKV):
+                            page = pages[a // P]
+                            want[page, kv, h], want_sc[page, kv, h] = put_block(
+                                want[page, kv, h], want_sc[page, kv, h], 0, x[a:a + P, h], fmt)
+            for p in pages:
+                new = np.array_equal(got_sc[p], want_sc[p]) and np.array_equal(
+                    decode(got[p], fmt), decode(want[p], fmt), equal_nan=True)
+                old = np.array_equal(got_sc[p], scales[p]) and np.array_equal(got[p], codes[p])
+                assert new or old, (off, i, p)
+        out = torch.full((100, HKV, D), 9.0, dtype=torch.bfloat16, device=dev)
+        out2, err = out.clone(), err_of(dev)
+        b.kv8_read(i32(off, dev), i32([0] * 4, dev), pool, sc, i32(bt, dev), out, out2, dev_err=err)
+        assert int(err.item()) == OFFSETS
+
+
 # --------------------------------------------------- streams, graphs, waits --
 
 def batch_of(fmt, lens, counts, seed=1, width=None):
