@@ -15,10 +15,12 @@
 // leaves a partial result (two at most), which the merge kernel combines.
 //
 // Bound by memory, in the middle by latencies: one token for 256 sequences of 1024 to
-// 2048 tokens (409 MB) 71 us, 5.7 TB/s; 64 x 4 new tokens over 1024 to 2048 (104 MB) 34
-// us without the launches around (22 without the arithmetic: four warps a scheduler of
-// dependent instructions, 46% of the issue slots while they run.  Two pages at a time,
-// as for one token, spill there: 42).
+// 2048 tokens (409 MB) 71 us, 5.7 TB/s; 64 x 4 new tokens over 1024 to 2048 (104 MB) 35
+// us without the launches around (22 without the arithmetic).  There a scheduler's time
+// counts: an MMA takes 8.3 cycles of it in which nothing else is issued (with 8 FMAs
+// 17.7), so a page and head take 24 x 8.3 + 245, and an SM with two of the longest CTAs
+// 29 us.  Two pages at a time, as for one token, or the next page's loads during this
+// one's products hide latencies that are hidden already: 42 and 40.
 //
 // mma.sync m16n8k16 in f16, FP32 accumulators, for a page (16 tokens) and a kv
 // head; codes become f16 exactly (one instruction for two e4m3 codes):
