@@ -953,9 +953,12 @@ __device__ __forceinline__ bool merged_row(const MaskedArgs& a, int b, int r, ui
 
 // Combine a row's partial results, added in an order that does not change.  Where few
 // are expected a warp takes a row; else a CTA does, warp w the results w, w +
-// kMergeWarps, ... (each step of a sum is an L2 latency: 304 of one sequence of 30011
-// tokens took 33 us with one warp).  grid (rows / 4 or rows, batch).
-constexpr int kMergeRows = 4, kMergeWarps = 16, kFewPieces = 16;
+// kWarpsOfRow, ... (each step of a sum is an L2 latency: 304 of one sequence of 30011
+// tokens took 33 us with one warp), of sixteen warps while the rows are few, of four
+// where these would take several waves (cold, 4 tokens of 8 sequences of 2048: 30 us
+// with sixteen, 23.5 with four; of 2 of 30000: 35 and 39).  grid (rows / 4 or rows,
+// batch).
+constexpr int kMergeRows = 4, kFewPieces = 16, kFewRows = 256;
 template <bool kChunk, bool kShared, int kWarpsOfRow>
 __global__ void __launch_bounds__(32 * (kWarpsOfRow == 1 ? kMergeRows : kWarpsOfRow))
     merge8_kernel(const MaskedArgs a) {
@@ -1055,9 +1058,12 @@ __global__ void __launch_bounds__(32 * (kWarpsOfRow == 1 ? kMergeRows : kWarpsOf
 template <bool kChunk, bool kShared>
 cudaError_t launch_merge(const MaskedArgs& a, int pieces, cudaStream_t stream) {
   constexpr int kRows = kChunk ? kNumKvHeads * kShortRows : kNumQHeads;
+  if (pieces > kFewPieces && kRows * a.batch <= kFewRows)
+    return launch_pdl(merge8_kernel<kChunk, kShared, 16>, dim3(kRows, a.batch), dim3(32 * 16), 0,
+                      stream, a);
   if (pieces > kFewPieces)
-    return launch_pdl(merge8_kernel<kChunk, kShared, kMergeWarps>, dim3(kRows, a.batch),
-                      dim3(32 * kMergeWarps), 0, stream, a);
+    return launch_pdl(merge8_kernel<kChunk, kShared, 4>, dim3(kRows, a.batch), dim3(32 * 4), 0,
+                      stream, a);
   return launch_pdl(merge8_kernel<kChunk, kShared, 1>, dim3(kRows / kMergeRows, a.batch),
                     dim3(32 * kMergeRows), 0, stream, a);
 }

@@ -105,6 +105,17 @@ def test_short_chunks_with_bad_offsets(splits):
         check(out, want, tol, f"offsets {off}")
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("batch", [1, 2, 3, 8, 9, 20])
+def test_many_ranges(fmt, batch):
+    """Merges of more results than a warp's, by CTAs of each size."""
+    lens = [(1100, 0, 1, 700, 33, 512)[i % 6] + i for i in range(batch)]
+    for splits in (17, 40, 100):
+        assert run_decode(fmt, lens, splits=splits) == 0
+        assert run_chunk(fmt, lens, [min(n, 1 + i % 4) for i, n in enumerate(lens)], splits=splits,
+                         pad=0) == 0
+
+
 # ----------------------------------------------------------- long and large --
 
 def test_widening_in_rounds():
