@@ -133,7 +133,8 @@ __device__ __forceinline__ uint32_t settle_scale(const Kv8& c, int64_t page, int
 
 // One CTA per sequence, warp h of it for kv head h: lane i rotates pair i of K
 // (and of query heads h, h + 8, h + 16, h + 24 when asked) and takes dims 2i and
-// 2i + 1 of V.
+// 2i + 1 of V.  Bound by its chain of loads (position, page, scale, codes to round
+// again): 13 us for 2048 sequences, two waves of CTAs, 6 for one.
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads)
     kv8_append_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
@@ -463,11 +464,15 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float f) {
 
 // Ragged prompts: a CTA brings its units' rows of k and v (16 KiB each, in a row)
 // into a ring of two stages in shared memory, so the next unit's are on their way
-// while one is rotated and rounded; the angles of its 16 positions are a 4 KiB row of
-// the tables each, or evaluated once for all heads.  Warp h takes the K and the V block
-// of kv head h: lane 4 r + q holds dims [8 q, 8 q + 8) and [32 + 8 q, 32 + 8 q + 8) of
-// slots r and r + 8 (odd r their other half first: a phase of 8 lanes then covers all
-// banks).
+// while one is rotated and rounded, with the angles of its 16 positions, 4 KiB of the
+// table; past the table they are worked out once for all heads.  Warp h takes the K and
+// the V block of kv head h: lane 4 r + q holds dims [8 q, 8 q + 8) and [32 + 8 q, 32 +
+// 8 q + 8) of slots r and r + 8 (odd r their other half first: a phase of 8 lanes then
+// covers all banks).  Warp 0 fills the ring; the warps run apart by up to two units
+// (barriers of the whole CTA instead: 79 us).
+//
+// Bound by its instructions, 960 a warp and unit at 61% of the issue slots: 64 prompts of
+// 1024 to 2047 tokens (306 MB) 70 us, 4.4 TB/s.
 constexpr int kWriteStages = 2, kWriteCtas = 3;
 constexpr int kTokenBytes = kNumKvHeads * kHeadDim * 2;        // a row of k or v
 constexpr int kHalfStage = kPageSize * kTokenBytes;            // 16 KiB
@@ -659,9 +664,9 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
       if (!near) __syncthreads();  // (warps that gave up have left)
       load(rows);
       // Bounds x, y of the rotated keys, which give the same codes but for a key in a
-      // few ten thousand.  (Deciding each of them exactly took 84 us for 64 prompts of
-      // up to 2047 tokens, with FP64, whose rate here is a small fraction of FP32's,
-      // 119; not at all 64.)
+      // few ten thousand.  (With barriers of the whole CTA, where this took 79 us,
+      // deciding each of them exactly took 84; with FP64, whose rate here is a small
+      // fraction of FP32's, 119; not at all 64.)
       uint4 y[2][2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
