@@ -967,13 +967,15 @@ __global__ void __launch_bounds__(32 * (kWarpsOfRow == 1 ? kMergeRows : kWarpsOf
   __shared__ float2 s_ml[kWarpsOfRow];
   __shared__ float2 s_o[kWarpsOfRow][kHeadDim / 2];
   allow_dependent_grids();
-  wait_for_prior_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
   const int r = kMany ? blockIdx.x : blockIdx.x * kMergeRows + warp, w = kMany ? warp : 0;
   const int num_splits = kChunk ? a.short_splits : a.num_splits;
-  // (a row that is not there is left when the loads are on their way)
+  // The offsets are the call's input: grids before the call's own were waited for by its
+  // first one, before this one could start.
   uint16_t* out;
   const bool there = merged_row<kChunk>(a, b, r, out);
+  wait_for_prior_grids();
+  if (!there) return;  // (the same for a row's warps)
   const Pieces<kShared> P(a, num_splits, b);
   if (P.n == 1) return;
   const float2* all_ml = reinterpret_cast<const float2*>(kChunk ? a.short_ml : a.part_ml) + r;
@@ -1002,7 +1004,6 @@ __global__ void __launch_bounds__(32 * (kWarpsOfRow == 1 ? kMergeRows : kWarpsOf
       }
     };
     load(0);
-    if (!there) return;  // (the same for a row's warps)
     float top = x.y != 0.f ? x.x : -INFINITY;
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
