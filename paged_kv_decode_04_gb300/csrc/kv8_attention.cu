@@ -377,62 +377,50 @@ __device__ __forceinline__ int64_t part_start(int64_t total, int64_t parts, int6
   return total * c / parts;
 }
 
-// make(b): sequence b's list.  By all threads of the CTA.  The first CTA writes the
-// sequences' bases, and the total behind them, for the merge.
+// make(b): sequence b's list.  By all threads of the CTA, some sequences in a row each.
+// The first CTA writes the sequences' bases, and the total behind them, for the merge.
 template <typename Make>
 __device__ __forceinline__ Part share_out(const MaskedArgs& a, const Make& make) {
   __shared__ int64_t s_warp[kThreads / 32];
   __shared__ int64_t s_base;
   __shared__ int s_first;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
   int64_t sum = 0;
-  int mine = 0;  // of sequence tid
-  for (int b = tid; b < a.batch; b += kThreads) {
-    const int n = make(b).n;
-    if (b == tid) mine = n;
-    sum += n;
+  for (int b = b0; b < b1; ++b) sum += make(b).n;
+  int64_t incl = sum;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int64_t y = __shfl_up_sync(kFull, incl, x);
+    if (lane >= x) incl += y;
   }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-  if (lane == 0) s_warp[w] = sum;
+  if (lane == 31) s_warp[w] = incl;
   __syncthreads();
-  int64_t total = 0;
+  int64_t base = incl - sum, total = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) total += s_warp[i];
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < w) base += s_warp[i];
+    total += s_warp[i];
+  }
   const int64_t parts = parts_of(total, gridDim.x);
   Part p = {0, 0, 0, 0};
   if (blockIdx.x < parts) {
     p.u0 = part_start(total, parts, blockIdx.x);
     p.u1 = part_start(total, parts, blockIdx.x + 1);
   }
-  const bool report = blockIdx.x == 0;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.batch && (report || before <= p.u0); b0 += kThreads) {
-    const int b = b0 + tid;
-    const int n = b0 == 0 ? mine : b < a.batch ? make(b).n : 0;
-    int64_t incl = n;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int64_t y = __shfl_up_sync(kFull, incl, x);
-      if (lane >= x) incl += y;
+  const bool mine = base <= p.u0 && p.u0 < base + sum;
+  if (mine || blockIdx.x == 0)
+    for (int b = b0; b < b1; ++b) {
+      const int n = make(b).n;
+      if (base <= p.u0 && p.u0 < base + n) {
+        s_first = b;
+        s_base = base;
+      }
+      if (blockIdx.x == 0) a.part_bases[b] = base;
+      base += n;
     }
-    __syncthreads();  // s_warp has been read
-    if (lane == 31) s_warp[w] = incl;
-    __syncthreads();
-    int64_t base = before + incl - n, all = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < w) base += s_warp[i];
-      all += s_warp[i];
-    }
-    if (base <= p.u0 && p.u0 < base + n) {
-      s_first = b;
-      s_base = base;
-    }
-    if (report && b < a.batch) a.part_bases[b] = base;
-    before += all;
-  }
-  if (report && tid == 0) a.part_bases[a.batch] = total;
+  if (blockIdx.x == 0 && tid == 0) a.part_bases[a.batch] = total;
   __syncthreads();
   if (p.u0 < p.u1) {
     p.b = s_first;

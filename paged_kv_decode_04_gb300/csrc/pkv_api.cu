@@ -1468,8 +1468,8 @@ bool stream8_plan(int batch, long long units, long long pages, int num_splits, i
   // ranges (16); 64 of 50 to 6350: 47 and 53 (8 ranges); 256 of 1024 to 2048: 71 and 81
   // (a CTA each).  Sharing costs 3 to 4 us (a sum of the lengths before, a merge after),
   // more than it saves below: 128 windows of 1000 tokens 34 us, 31 in two ranges each,
-  // 64 x 4 new tokens over 1024 to 2048 45 and 41.  Many short sequences lose a little
-  // (1000 of 250 to 500: 90 and 80).
+  // 64 x 4 new tokens over 1024 to 2048 42 and 41.  Many sequences for each CTA lose too
+  // (4096 of 500: 328 and 291), but no length among them can make a wave wait.
   constexpr long long kSharedPages = 64;
   if (num_splits > 0)
     plan->splits = static_cast<int>(std::min<long long>(num_splits, pages));

@@ -69,6 +69,32 @@ def test_shared_chunks(fmt, lens):
         assert run_chunk(fmt, lens, counts, pad=5, cache=shared_cache(lens, fmt)) == 0
 
 
+@pytest.mark.parametrize("batch", [289, 1500, 65535])
+def test_shared_large_batches(batch):
+    """Up to the largest batch, of a few lengths in turn: each sequence as in a batch of its
+    own kind."""
+    dev, b = cuda_or_skip(), binding()
+    kinds, width = 70, max(wide(batch), 2)
+    lens = [i % 33 for i in range(kinds - 1)] + [500]
+    codes, sc, few = make_cache8(lens, "e4m3", width=max(width, 32))
+    pool, s = as_pool(codes, "e4m3").to(dev), torch.from_numpy(sc).to(dev)
+    pick = torch.from_numpy(np.random.default_rng(batch).integers(0, kinds, batch)).to(dev)
+    ln, bt = i32(lens, dev), i32(few, dev)
+    q, err = normal((kinds, HQ, D), 3).to(dev), err_of(dev)
+    want = b.paged8_decode_attention(q, pool, s, bt, ln, num_splits=1)
+    got = b.paged8_decode_attention(q[pick], pool, s, bt[pick], ln[pick], dev_err=err)
+    # (sequences that two CTAs share are summed in another order)
+    short = ln[pick] <= 16
+    assert torch.equal(got[short], want[pick][short])
+    assert (got.float() - want[pick].float()).abs().max() <= 2 ** -7 * want.float().abs().max()
+    off = torch.arange(batch + 1, dtype=torch.int32, device=dev)
+    got = b.paged8_chunk_attention(q[pick], off, pool, s, bt[pick], ln[pick], dev_err=err)
+    assert torch.equal(got[short], want[pick][short])
+    assert (got.float() - want[pick].float()).abs().max() <= 2 ** -7 * want.float().abs().max()
+    # (an empty sequence has no place for its chunk's token)
+    assert int(err.item()) == POSITION
+
+
 def test_shared_bad_inputs():
     lens = [300, 40, 17, 2000]
     assert run_decode("e4m3", lens, cache=shared_cache(lens, "e4m3"),
