@@ -280,7 +280,7 @@ struct MaskedArgs {
   float* short_ml;               // [short_splits]
   int64_t* part_bases;           // 8-bit cache: [batch + 1] pages before each sequence
   int part_ctas;                 // and the CTAs that share them (splits 0)
-  const int32_t* rounds;         // long chunks: only sequences of this round, or nullptr
+  const int32_t* rounds;         // long chunks: [batch], those of `round` are taken (nullptr: all)
   int round;
   float scale_log2;              // softmax scale * log2(e)
   unsigned long long wait_ns;
