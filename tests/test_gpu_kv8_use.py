@@ -48,6 +48,17 @@ def test_shared_decode(fmt, lens):
     assert run_decode(fmt, lens, cache=cache) == 0
 
 
+@pytest.mark.parametrize("lens", [
+    [250 + i % 14 for i in range(120)], [256, 257] * 60, [17, 3000, 256, 0, 256, 16] * 12,
+    [300] * 2 + [256] * 80, [256] * 80 + [2000, 1],
+], ids=lambda x: f"{len(x)}x{max(x)}")
+def test_shared_around_what_stays_whole(lens):
+    """Sequences of 16 pages are not cut, those of 17 are."""
+    assert run_decode("int8", lens, cache=shared_cache(lens, "int8")) == 0
+    counts = [min(n, 1 + i % 4) for i, n in enumerate(lens)]
+    assert run_chunk("e4m3", lens, counts, pad=0, cache=shared_cache(lens, "e4m3")) == 0
+
+
 @pytest.mark.parametrize("window,sinks", [(5000, 0), (5000, 70), (6000, 3)])
 def test_shared_windows(window, sinks):
     lens = [6100, 30, 5200, 0, 5001] + [40] * 60
