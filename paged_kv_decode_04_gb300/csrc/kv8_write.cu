@@ -508,7 +508,10 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
   wait_for_prior_grids();
   allow_dependent_grids();
   check_offsets(c, off, num_tokens, dev_err);
-  const bool tag_ok = rope_table_ready(freqs);
+  // The tag may be set meanwhile, by the call that builds the table on another stream,
+  // and the warps' barriers, the copies and who works out the angles follow it: one
+  // answer for the CTA.
+  const bool tag_ok = __syncthreads_and(rope_table_ready(freqs));
   const Share share(unit_count(num_tokens, c.batch));
   const uint64_t policy = l2_policy_evict_first();
   int issued = 0, done = 0;  // units whose rows were asked for, units written
