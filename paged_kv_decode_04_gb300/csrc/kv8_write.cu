@@ -604,14 +604,14 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
           x[s][1] = !in ? none : r & 1 ? y : z;
         }
       };
+      auto top_of = [&](const uint4 (&y)[2][2]) {
+        const uint32_t m =
+            top2(top2(top8(y[0][0]), top8(y[0][1])), top2(top8(y[1][0]), top8(y[1][1])));
+        return __reduce_max_sync(kFull, max(m & 0x7FFFu, (m >> 16) & 0x7FFFu));
+      };
       // the largest magnitude, values that are not finite left out
       auto largest = [&](uint4 (&y)[2][2]) {
-        auto top_of = [&]() {
-          const uint32_t m = top2(top2(top8(y[0][0]), top8(y[0][1])),
-                                  top2(top8(y[1][0]), top8(y[1][1])));
-          return __reduce_max_sync(kFull, max(m & 0x7FFFu, (m >> 16) & 0x7FFFu));
-        };
-        const uint32_t top = top_of();
+        const uint32_t top = top_of(y);
         if (top < 0x7F80u) return top;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
           drop_nonfinite(y[s][1]);
         }
         if (lane == 0) record_error(dev_err, kErrValue);
-        return top_of();
+        return top_of(y);
       };
       auto put = [&](int kv, uint32_t top, uint32_t old, const uint2 (&codes)[2][2]) {
         settle_scale<kFmt>(c, t.pool_page, kv, h, top, t.s0, old, lane);
@@ -687,9 +687,11 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
                      pos0 + slot,
                      x[s][0], x[s][1]);
       };
-      uint32_t top = largest(x);
+      uint32_t top = top_of(x);
       const uint32_t old = stored_scale(old_k);
-      // (pairs of less than 2^-70 matter only where the block's largest is tiny)
+      // Pairs of less than 2^-70 matter only where the block's largest is tiny; where the
+      // bounds of a pair overflow (|u| + |v| may, though the pair's length fits), or a key
+      // is not finite, so is the largest.
       const bool odd = (top > 0 && top < kTiny) || top >= kHuge;
       encode(x, top, old, codes);
       uint32_t apart = 0;
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, kWriteCtas)
           apart |= (x[s][d].x ^ y[s][d].x) | (x[s][d].y ^ y[s][d].y) | (x[s][d].z ^ y[s][d].z) |
                    (x[s][d].w ^ y[s][d].w);
       if (odd || __any_sync(kFull, apart != 0)) {
-        bool differ = odd || needed_scale<kFmt>(largest(y)) != needed_scale<kFmt>(top);
+        bool differ = odd || needed_scale<kFmt>(top_of(y)) != needed_scale<kFmt>(top);
         if (!differ) {  // (the same in all lanes so far)
           uint2 z[2][2];
           encode(y, top, old, z);
