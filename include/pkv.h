@@ -734,8 +734,10 @@ PKV_API int pkv_kv8_read(const void* pool, const uint8_t* scales, int format, in
 /*
  * pkv_paged8_decode_attention -- pkv_paged_decode_attention over the 8-bit
  * cache, with a sliding window and sink tokens where window > 0 (0: the whole
- * cache).  Scores and softmax are FP32, weights enter the product with V with 22
- * significant bits, the output is rounded to bf16 once.  Workspace, num_splits
+ * cache).  Scores and softmax are FP32 (scale * |q| * |K| summed over a head's dims
+ * has to stay below 2^126), weights enter the product with V with 22 significant
+ * bits, V of every magnitude that the cache holds is summed without overflow, the
+ * output is rounded to bf16 once.  Workspace, num_splits
  * and dev_err as there, sized by pkv_decode8_workspace_bytes().  With num_splits 0
  * and a large table the batch's pages, as seq_lens has them, are shared out evenly,
  * whatever the sequences' lengths are; the same inputs give the same bits, but a
@@ -760,8 +762,11 @@ PKV_API size_t pkv_decode8_workspace_bytes(int batch, int num_q_heads, int num_k
  * the same arguments and rules, sized by pkv_chunk8_workspace_bytes().  Chunks of
  * more than four tokens see their pages as bf16, which the workspace has room for
  * (32 KiB a page): for all that num_tokens and the table allow, or for 2 GiB at a
- * time, or two whole rows of the table where that is more.  num_splits 0: shorter
- * ones share pages as in pkv_paged8_decode_attention.
+ * time, or two whole rows of the table where that is more.  They weigh V with
+ * bf16 numbers, as there, and sum it in FP32 under weights that reach 2^16 for 128
+ * tokens together: V has to stay below 2^118 / seq_lens[b].  Chunks of up to four
+ * tokens are summed, and with num_splits 0 share pages, as in
+ * pkv_paged8_decode_attention.
  */
 PKV_API int pkv_paged8_chunk_attention(
     const pkv_bf16* q, int num_tokens, const int32_t* token_offsets, const void* pool,

@@ -40,6 +40,9 @@
 // moves when a score passes it by 8, so they stay below 2^15), and enter the
 // product as two f16 terms (22 significant bits, 2^-32 of the reference's weight
 // at the least); for one token the terms are the columns 0-3 and 4-7 of one MMA.
+// V's factors stay at 2^72 or below, as 2^31 tokens' codes times weights of 2^15 then
+// sum to less than 2^127: where a block seen has a larger scale the accumulators, and
+// the factors after it, are in larger units, and the row's sum is told at the end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -69,6 +72,7 @@ static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM fit");
 constexpr float kMoveLog2 = 8.f;   // a score this far above the reference moves it
 constexpr float kLift = 7.f;       // weights are 2^(s - m + kLift) <= 2^15
 constexpr float kLowestFloat = -3.402823466e38f;
+constexpr float kTopFactor = 0x1p72f;  // the largest factor of V
 
 // D = A B (+ D), FP32 accumulators.  (Not volatile: the compiler may interleave the
 // chains of two pages.)
@@ -141,11 +145,33 @@ struct Lane {
   }
 };
 
+// Accumulators of n pairs in units of 1 / down become such that a block of V whose
+// scale's value is sv, a power of two, can be added: with the factor sv * down.
+template <int n>
+__device__ __forceinline__ void raise_units(float sv, float& down, float2 (&o)[n][2]) {
+  const float factor = sv * down;
+  if (factor <= kTopFactor) return;
+  // kTopFactor / factor
+  const float f = __uint_as_float(((127u + 127u + 72u) - (__float_as_uint(factor) >> 23)) << 23);
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) o[i][j] = fmul2(o[i][j], make_float2(f, f));
+  down *= f;
+}
+// A row's reference and sum beside accumulators in units of 1 / down: l 2^m is the same.
+__device__ __forceinline__ void tell_units(float down, float& m, float& l) {
+  m += static_cast<float>(127 - static_cast<int>(__float_as_uint(down) >> 23));
+  l *= down;
+}
+
 // Online softmax of 8 query rows (columns of S^T) of a warp.
 struct State {
   float m[2], l[2];    // of columns 2 ft, 2 ft + 1: reference, this lane's share of the sum
   float2 o[4][2];      // O^T: dims 16 mt + fg (+ 8), columns 2 ft, 2 ft + 1
+  float down;          // ... in units of 1 / down
   __device__ __forceinline__ void reset() {
+    down = 1.f;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
 #pragma unroll
@@ -208,13 +234,17 @@ __device__ __forceinline__ void load_v(uint32_t vt, const Lane& P, uint32_t (&va
   }
 }
 
-// Move the references of S's rows to what the masked scores x of two pages ask for;
-// f: the factors of the pages' scores, of columns 2 ft and 2 ft + 1.
+// Move the references of S's rows to what the masked scores x of two pages ask for, and
+// the accumulators' units to what sv does, the larger of their V scales' values; f: the
+// factors of the pages' scores, of columns 2 ft and 2 ft + 1.
 __device__ __forceinline__ void move_reference(const float (&x)[2][4], const float (&f)[2][2],
-                                               State& S) {
+                                               float sv, State& S) {
   float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]) * f[0][0], fmaxf(x[1][0], x[1][2]) * f[1][0]);
   float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]) * f[0][1], fmaxf(x[1][1], x[1][3]) * f[1][1]);
-  if (!__any_sync(kFull, mx0 > S.m[0] + kMoveLog2 || mx1 > S.m[1] + kMoveLog2)) return;
+  if (!__any_sync(kFull, mx0 > S.m[0] + kMoveLog2 || mx1 > S.m[1] + kMoveLog2 ||
+                             sv * S.down > kTopFactor))
+    return;
+  raise_units(sv, S.down, S.o);
 #pragma unroll
   for (int i = 4; i <= 16; i <<= 1) {
     mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, i));
@@ -562,11 +592,11 @@ __device__ __forceinline__ bool attend_one(const MaskedArgs& a, const Ring& R, c
     if ((vis0 & vis1) == 0xFFFFu) {
       scores(kt0, s[0]);
       scores(kt1, s[1]);
-      move_reference(s, f, S);
+      move_reference(s, f, fmaxf(sv0, sv1), S);
       page_weights(s[0], f[0], P.ft, S, b[0][0], b[0][1]);
       page_weights(s[1], f[1], P.ft, S, b[1][0], b[1][1]);
-      add_values<kFmt>(kt0 + kV, P, sv0, b[0][0], b[0][1], S);
-      add_values<kFmt>(kt1 + kV, P, sv1, b[1][0], b[1][1], S);
+      add_values<kFmt>(kt0 + kV, P, sv0 * S.down, b[0][0], b[0][1], S);
+      add_values<kFmt>(kt1 + kV, P, sv1 * S.down, b[1][0], b[1][1], S);
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -578,15 +608,16 @@ __device__ __forceinline__ bool attend_one(const MaskedArgs& a, const Ring& R, c
         if (!((vis >> (P.tok + 2)) & 1u)) s[i][2] = s[i][3] = -INFINITY;
         if constexpr (kFmt == kKv8E4m3) hide_v(kt + kV, vis, lane);
       }
-      // (the scales of a page that was not read may be anything)
+      // (the scales of a page that was not read, or is not seen, may be anything)
       const float g2[2][2] = {{vis0 ? f[0][0] : 1.f, vis0 ? f[0][1] : 1.f},
                               {vis1 ? f[1][0] : 1.f, vis1 ? f[1][1] : 1.f}};
-      move_reference(s, g2, S);
+      move_reference(s, g2, fmaxf(vis0 ? sv0 : 0.f, vis1 ? sv1 : 0.f), S);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         page_weights(s[i], g2[i], P.ft, S, b[i][0], b[i][1]);
-        if ((i == 0 ? vis0 : vis1) != 0u)
-          add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, i == 0 ? sv0 : sv1, b[i][0], b[i][1], S);
+        if ((i == 0 ? vis0 : vis1) == 0u) continue;
+        const float sv = i == 0 ? sv0 : sv1;
+        add_values<kFmt>((i == 0 ? kt0 : kt1) + kV, P, sv * S.down, b[i][0], b[i][1], S);
       }
     }
     __syncwarp();
@@ -602,6 +633,8 @@ __device__ __forceinline__ bool attend_one(const MaskedArgs& a, const Ring& R, c
     S.l[0] += __shfl_xor_sync(kFull, S.l[0], i);
     S.l[1] += __shfl_xor_sync(kFull, S.l[1], i);
   }
+  tell_units(S.down, S.m[0], S.l[0]);
+  tell_units(S.down, S.m[1], S.l[1]);
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -758,7 +791,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
     }
     bool ok = true;
-    float2 o[8][2];  // dims 8 nt + 2 ft, + 1 of rows fg and fg + 8
+    float down = 1.f;
+    float2 o[8][2];  // dims 8 nt + 2 ft, + 1 of rows fg and fg + 8, in units of 1 / down
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
     // bits of a page's slots below token x (as a distance from the page's first)
@@ -861,7 +895,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         uint32_t vb[8];
         ldsm_b8_trans(vt + P.v0, *reinterpret_cast<uint32_t(*)[4]>(&vb[0]));
         ldsm_b8_trans(vt + P.v1, *reinterpret_cast<uint32_t(*)[4]>(&vb[4]));
-        const float2 s2 = make_float2(sv, sv);
+        raise_units(sv, down, o);
+        const float2 s2 = make_float2(sv * down, sv * down);
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
           uint32_t b0, b1;
@@ -881,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(kFull, l[i], 1);
       l[i] += __shfl_xor_sync(kFull, l[i], 2);
+      tell_units(down, m[i], l[i]);
       const int tok = 2 * i + (P.fg >> 2), h = P.fg & 3;
       if (tok >= nt) continue;
       if (slot >= 0) {

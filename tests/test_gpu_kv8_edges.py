@@ -1,14 +1,17 @@
 """The 8-bit cache at the ends of its range: keys whose rotation overflows FP32 on the
-way (GPU)."""
+way, values near the largest that it holds (GPU)."""
 import numpy as np
 import pytest
 import torch
 
 import oracle
 from _gpu_util import binding, cuda_or_skip
-from _kv8_util import D, FORMATS, as_pool, bits, decode, put_block, rotated
+from _kv8_util import (D, FORMATS, as_pool, bits, decode, make_cache8, put_block, random_codes,
+                       rotated)
 from _longctx_util import HKV, P
-from test_gpu_kv8 import VALUE, bf16, err_of, i32, oracle_bits, random_cache, run_write, same
+from test_gpu_kv8 import (VALUE, bf16, err_of, i32, oracle_bits, random_cache, run_chunk,
+                          run_decode, run_write, same)
+from test_gpu_kv8_use import wide
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +75,63 @@ def test_write_of_a_pair_that_overflows(fmt):
     assert np.isinf(key).sum() == 1
     codes, scales = random_cache(np.random.default_rng(2), 3, fmt)
     assert run_write(fmt, [n], [0], codes, scales, np.array([[1]], np.int32), k, v) == VALUE
+
+
+# --------------------------------------------------------------- huge values --
+
+SCALES = {                                   # of V's blocks, page by page of a sequence
+    "largest": lambda rng, n: np.full((n, HKV), 240),
+    "rising": lambda rng, n: np.linspace(60, 240, n).astype(int)[:, None].repeat(HKV, 1),
+    "falling": lambda rng, n: np.linspace(240, 3, n).astype(int)[:, None].repeat(HKV, 1),
+    "any": lambda rng, n: rng.integers(3, 241, (n, HKV)),
+}
+
+
+def huge_cache(lens, fmt, kind, width=None):
+    """A cache whose V reaches the largest magnitudes that the format and scales do."""
+    rng = np.random.default_rng(len(lens))
+    codes, sc, bt = make_cache8(lens, fmt, seed=len(lens), width=width)
+    for b, n in enumerate(lens):
+        pages = bt[b, :-(-n // P)]
+        sc[pages, 1] = SCALES[kind](rng, len(pages))
+        v = random_codes(rng, (len(pages), HKV, P, D), fmt, spread=200.0)
+        hidden = np.arange(len(pages) * P).reshape(-1, P) >= n
+        codes[pages, 1] = np.where(hidden[:, None, :, None], codes[pages, 1], v)
+    return codes, sc, bt
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", list(SCALES))
+@pytest.mark.parametrize("splits", [0, 1, 3, 20])
+@pytest.mark.parametrize("lens", [[1], [2, 700, 0, 33], [300, 1300]], ids=str)
+def test_values_of_any_magnitude(fmt, kind, splits, lens):
+    assert run_decode(fmt, lens, splits=splits, cache=huge_cache(lens, fmt, kind)) == 0
+    assert run_decode(fmt, lens, 150, 20, splits, cache=huge_cache(lens, fmt, kind)) == 0
+    for n in (1, 2, 4):
+        counts = [min(x, n) for x in lens]
+        assert run_chunk(fmt, lens, counts, splits=splits, pad=0,
+                         cache=huge_cache(lens, fmt, kind)) == 0
+        assert run_chunk(fmt, lens, counts, 150, 20, splits=splits, pad=0,
+                         cache=huge_cache(lens, fmt, kind)) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", list(SCALES))
+def test_shared_values_of_any_magnitude(fmt, kind):
+    cuda_or_skip()
+    lens = [3000, 17, 0, 256, 900] * 3
+    cache = huge_cache(lens, fmt, kind, width=wide(len(lens)))
+    assert run_decode(fmt, lens, cache=cache) == 0
+    counts = [min(n, 1 + i % 4) for i, n in enumerate(lens)]
+    assert run_chunk(fmt, lens, counts, pad=0, cache=cache) == 0
+
+
+@pytest.mark.parametrize("fmt,scale", [("e4m3", 225), ("int8", 227)])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_longer_chunks_up_to_their_largest_values(fmt, scale, splits):
+    """2^118 / 1300 is 2^107.7: codes of 448 with the scale 2^98, of 127 with 2^100."""
+    lens = [1300, 90]
+    codes, sc, bt = huge_cache(lens, fmt, "largest")
+    sc[:, 1] = np.minimum(sc[:, 1], scale)
+    for counts in ([40, 5], [300, 90], [5, 4]):
+        assert run_chunk(fmt, lens, counts, splits=splits, cache=(codes, sc, bt)) == 0
