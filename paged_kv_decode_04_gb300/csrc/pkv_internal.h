@@ -257,7 +257,6 @@ cudaError_t launch_shared_prefix_attention(const CUtensorMap& pool_map, const At
 struct MaskedArgs {
   const uint16_t* q;
   const uint16_t* pool;          // a bf16 cache
-  const uint8_t* scales;         // of an 8-bit cache, 16-byte aligned
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* token_offsets;  // chunks only: [batch + 1]
@@ -278,12 +277,15 @@ struct MaskedArgs {
   int short_splits;              // chunks: ranges of chunks of at most kShortTokens
   float* short_acc;              // partials of the short chunks, [batch][kShortTokens * 32 rows]
   float* short_ml;               // [short_splits]
-  int64_t* part_bases;           // 8-bit cache: [batch + 1] pages before each sequence
-  int part_ctas;                 // and the CTAs that share them (splits 0)
-  const int32_t* rounds;         // long chunks: [batch], those of `round` are taken (nullptr: all)
-  int round;
   float scale_log2;              // softmax scale * log2(e)
   unsigned long long wait_ns;
+  // 8-bit cache (behind the rest, whose places the code generated for the bf16 kernels
+  // depends on: in between they cost the chunk kernel 0.7 %)
+  const uint8_t* scales;         // 16-byte aligned
+  int64_t* part_bases;           // [batch + 1] pages before each sequence
+  int part_ctas;                 // and the CTAs that share them (splits 0)
+  int round;
+  const int32_t* rounds;         // long chunks: [batch], those of `round` are taken (nullptr: all)
 };
 
 // Tiles of the chunk kernel: new tokens (all 4 query heads of a kv head) and
