@@ -761,8 +761,14 @@ PKV_API size_t pkv_decode8_workspace_bytes(int batch, int num_q_heads, int num_k
  * pkv_paged8_chunk_attention -- pkv_paged_chunk_attention over the 8-bit cache,
  * the same arguments and rules, sized by pkv_chunk8_workspace_bytes().  Chunks of
  * more than four tokens see their pages as bf16, which the workspace has room for
- * (32 KiB a page): for all that num_tokens and the table allow, or for 2 GiB at a
- * time, or two whole rows of the table where that is more.  They weigh V with
+ * (32 KiB a page): for all that num_tokens and the table allow (max_blocks pages,
+ * or the window's, of min(batch, num_tokens / 5) sequences: 212 MiB for 64 x 4
+ * tokens and tables of 128 blocks), or for 2 GiB at a time, or two whole rows of the
+ * table where that is more.  What passes that is taken in rounds, whose number
+ * follows from these sizes and not from the lengths, and which take 7 to 13 us each
+ * even where no chunk is that long: 256 x 4 tokens over 2048 126 us with tables of
+ * 128 blocks, 442 with 8192.  So tables should be no wider than the batch needs.
+ * They weigh V with
  * bf16 numbers, as there, and sum it in FP32 under weights that reach 2^16 for 128
  * tokens together: V has to stay below 2^118 / seq_lens[b].  Chunks of up to four
  * tokens are summed, and with num_splits 0 share pages, as in

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["kv_append.cu", "decode_attention.cu", "decode_pagebox.cu", "decode_shared.cu",
            "decode_segments.cu", "chunk_attention.cu", "short_chunk.cu",
            "window_attention.cu", "kv_evict.cu", "kv8_write.cu", "kv8_widen.cu",
-           "kv8_attention.cu",           "pkv_api.cu", "scheduler.cpp", "planner.cpp"]
+           "kv8_attention.cu", "pkv_api.cu", "scheduler.cpp", "planner.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

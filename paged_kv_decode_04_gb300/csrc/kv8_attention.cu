@@ -1,11 +1,10 @@
 // kv8_attention.cu -- attention of one new token, or of chunks of a few, per
 // sequence over the 8-bit paged cache, streaming its pages once.
 //
-// In a CTA a producer warp brings
-// whole pages (16 KiB, all kv heads, one TMA box, and the 16 bytes of their scales)
-// into a ring in shared memory, and warp g of eight takes kv head g's blocks of every
-// page.  So a page is one copy and one barrier for all heads, and the heads' states
-// never meet.
+// In a CTA a producer warp brings whole pages (16 KiB, all kv heads, one TMA box, and the
+// 16 bytes of their scales) into a ring in shared memory, and warp g of eight takes kv
+// head g's blocks of every page.  So a page is one copy and one barrier for all heads,
+// and the heads' states never meet.
 //
 // A CTA takes a range of one sequence's pages (grid (ranges, sequences)) or, kShared,
 // an even share of the batch's: the pages that the queries see, counted on from sequence
@@ -15,10 +14,10 @@
 // leaves a partial result (two at most), which the merge kernel combines.
 //
 // Bound by memory, in the middle by latencies: one token for 256 sequences of 1024 to
-// 2048 tokens (409 MB) 71 us, 5.7 TB/s; 64 x 4 new tokens over 1024 to 2048 (104 MB) 35
+// 2048 tokens (409 MB) 72 us, 5.7 TB/s; 64 x 4 new tokens over 1024 to 2048 (104 MB) 35
 // us without the launches around (22 without the arithmetic).  There a scheduler's time
 // counts: an MMA takes 8.3 cycles of it in which nothing else is issued (with 8 FMAs
-// 17.7), so a page and head take 24 x 8.3 + 245, and an SM with two of the longest CTAs
+// 17.7), so a page and head take 24 x 8.3 + 250, and an SM with two of the longest CTAs
 // 29 us.  Two pages at a time, as for one token, or the next page's loads during this
 // one's products hide latencies that are hidden already: 42 and 40.
 //

@@ -134,7 +134,7 @@ __device__ __forceinline__ uint32_t settle_scale(const Kv8& c, int64_t page, int
 // One CTA per sequence, warp h of it for kv head h: lane i rotates pair i of K
 // (and of query heads h, h + 8, h + 16, h + 24 when asked) and takes dims 2i and
 // 2i + 1 of V.  Bound by its chain of loads (position, page, scale, codes to round
-// again): 13 us for 2048 sequences, two waves of CTAs, 6 for one.
+// again): 13 us for 2048 sequences, three waves of five CTAs an SM, 6 for one wave.
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads)
     kv8_append_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
@@ -271,8 +271,7 @@ __device__ __forceinline__ bool bad_offsets(int o0, int o1, int num_tokens) {
 }
 
 // The unit of number u, by each lane for itself (found where offsets do not fall);
-// `report`: one warp of a CTA
-// reports what is wrong with it.
+// `report`: one warp of a CTA reports what is wrong with it.
 __device__ __forceinline__ Unit find_unit(int64_t u, int64_t end, const Kv8& c,
                                           const int32_t* __restrict__ off,
                                           const int32_t* __restrict__ starts, int num_tokens,

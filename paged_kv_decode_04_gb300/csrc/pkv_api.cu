@@ -1469,7 +1469,9 @@ bool stream8_plan(int batch, long long units, long long pages, int num_splits, i
   // (a CTA each).  Sharing costs 3 to 4 us (a sum of the lengths before, a merge after),
   // more than it saves below: 128 windows of 1000 tokens 34 us, 31 in two ranges each,
   // 64 x 4 new tokens over 1024 to 2048 42 and 41.  Many sequences for each CTA lose too
-  // (4096 of 500: 328 and 291), but no length among them can make a wave wait.
+  // (4096 of 500: 387 and 343; 20000 of 17: 442 and 298), but no length among them can
+  // make a wave wait (one of 32768 behind 4095 of 500: 393 and 1377; behind 19999 of 17:
+  // 460 and 1339).
   constexpr long long kSharedPages = 64;
   if (num_splits > 0)
     plan->splits = static_cast<int>(std::min<long long>(num_splits, pages));
